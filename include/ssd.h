@@ -270,6 +270,141 @@ ssd_status_t ssd_forward_noalloc(const ssd_problem_t* prob, const void* x, const
  * synchronises `stream` first.  Returns SSD_ERR_CUDA if that failed. */
 ssd_status_t ssd_forward_noalloc_status(void* stream, int32_t* device_status);
 
+/* ---------------------------------------------------------------- around the scan
+ *
+ * The operators next to the scan in a layer of a language model: the short causal
+ * convolution that makes x, B and C from the in-projection, the one-token step that
+ * carries the convolution's window beside the scan's state, the norm in front of the layer
+ * and the gated norm behind the scan.  Here pointers need the alignment of their element
+ * type only (workspaces: 256 bytes; the scan state: 16); tensors whose rows all start on
+ * 16 bytes (8 in the convolution's backward on bf16) move in vectors of that size.  Strides
+ * are counted in elements, from one token or row to the next.  Weights, biases and their
+ * gradients are float32 or bf16 (wdtype), whatever the activations are.  An output must not
+ * overlap another output or, unless the call's comment says so, an input
+ * (SSD_ERR_INVALID_ARG); a tensor counts as everything from its first to its last element. */
+
+/* Causal depthwise convolution over the tokens of a sequence, then SiLU:
+ *     pre[i] = bias + sum_{j < width} weight[c][width - 1 - j] u[i - j],
+ *     out[i] = pre[i] / (1 + exp(-pre[i])).
+ * Tokens before the sequence's first come from its carried state, or are zero.  A
+ * sequence's state is `width` rows of channels in the type of u, row p mod width holding the
+ * token at position p; a call reads the width - 1 positions before its first token
+ * (positions[seq], or 0) and leaves the last `width` positions.  cu_seqlens is read with
+ * every entry clamped to 0 .. T (a malformed array gives wrong values, no access out of
+ * range); tokens from cu_seqlens[nseq] on belong to no sequence: their outputs and
+ * gradients are zero. */
+typedef struct {
+    int64_t batch;       /* rows of a dense batch; 1 with cu_seqlens */
+    int64_t seqlen;      /* tokens per row; with cu_seqlens: all tokens T (<= 2^31 - 1) */
+    int64_t u_stride;    /* elements from one token of u to the next (>= channels) */
+    int64_t du_stride;   /* the same of du (0 in a forward) */
+    int32_t split[3];    /* channels of the up to three contiguous outputs (unused ones 0) */
+    int32_t width;       /* taps: 2, 3 or 4 */
+    int32_t nseq;        /* 0: dense batch; > 0: number of packed sequences */
+    int32_t dtype;       /* ssd_dtype_t of u, the outputs and the states */
+    int32_t wdtype;      /* ssd_dtype_t of weight, bias and their gradients */
+    int32_t activation;  /* 1: SiLU, 0: none */
+} ssd_conv_t;
+
+/* Writes out0 .. out2 ([T][split[i]], contiguous) and, when final_state is not NULL, the
+ * states after the last tokens.  weight [channels][width]; bias [channels] or NULL;
+ * positions int32 [nseq or batch] or NULL (0); initial_state, final_state
+ * [nseq or batch][width][channels] or NULL. */
+ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void* weight,
+                              const void* bias, const int32_t* cu_seqlens,
+                              const int32_t* positions, const void* initial_state, void* out0,
+                              void* out1, void* out2, void* final_state, void* stream);
+
+/* Bytes of workspace ssd_conv_backward needs (it follows the current device's SM count). */
+ssd_status_t ssd_conv_workspace_size(const ssd_conv_t* conv, size_t* bytes);
+
+/* Gradients of u, weight, bias (d_bias may be NULL) and, when d_initial_state is not NULL,
+ * of the carried states, from those of the outputs and (d_final_state, or NULL: zero) of the
+ * final states.  The same inputs give the same bits in every call. */
+ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void* weight,
+                               const void* bias, const int32_t* cu_seqlens,
+                               const int32_t* positions, const void* initial_state,
+                               const void* dout0, const void* dout1, const void* dout2,
+                               const void* d_final_state, void* du, void* d_weight, void* d_bias,
+                               void* d_initial_state, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* One token for each of prob->batch rows (prob->seqlen = 1): the convolution with SiLU over
+ * the row of u (channels x [H][P], B [G][N], C [G][N]), then the scan's step.  Row i uses
+ * cache slot slots[i] (NULL: i) of state [nslots][H][P][N] float32 and conv_state
+ * [nslots][width][channels], both updated in place; a slot outside 0 .. nslots - 1 marks a
+ * padding row, whose y is zero and which touches no state.  The live rows' slots must
+ * differ.  positions int32 [batch]: the position of the new token.  y [batch][H][P]. */
+ssd_status_t ssd_conv_decode_step(const ssd_problem_t* prob, int32_t width, int32_t wdtype,
+                                  int32_t nslots, int64_t u_stride, float* state,
+                                  void* conv_state, const void* u, const float* raw_dt,
+                                  const void* weight, const void* bias, const int32_t* positions,
+                                  const int32_t* slots, void* y, void* stream);
+
+/* Norm over the columns of each row, after the residual add:
+ *     v = x + residual;  y = (v - mu) rstd weight + bias,
+ *     rstd = (mean((v - mu)^2) + eps)^-1/2,  mu = mean(v) (SSD_NORM_RMS: 0).
+ * Rows of up to 16384 columns, 8192 where a row does not start on 16 bytes. */
+typedef enum { SSD_NORM_LAYER = 0, SSD_NORM_RMS = 1 } ssd_norm_kind_t;
+typedef struct {
+    int64_t rows;
+    int64_t x_stride;    /* x; dx in the backward */
+    int64_t r_stride;    /* residual; dh in the backward */
+    int64_t h_stride;    /* h */
+    int64_t y_stride;    /* y; dy in the backward */
+    int32_t dim;
+    int32_t kind;        /* ssd_norm_kind_t */
+    int32_t dtype;       /* ssd_dtype_t of x, y and their gradients */
+    int32_t rdtype;      /* of residual, h and their gradients: dtype, or float32 */
+    int32_t wdtype;      /* of weight, bias and their gradients */
+    float eps;
+} ssd_norm_t;
+
+/* Writes y, h = v (with a residual only; both NULL or neither) and stats [rows][2] float32
+ * (mu, rstd; may be NULL).  bias may be NULL.  y may be x and h may be residual. */
+ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void* residual,
+                              const void* weight, const void* bias, void* y, void* h,
+                              float* stats, void* stream);
+
+ssd_status_t ssd_norm_workspace_size(const ssd_norm_t* norm, size_t* bytes);
+
+/* Gradients from dy and (dh, or NULL) the gradient of h that arrives by the residual stream:
+ * dx = the gradient of v in dtype; d_residual [rows][dim] the same in rdtype (may be NULL);
+ * d_weight, d_bias (may be NULL).  h is what the norm was taken of: the forward's h, or its
+ * x without a residual.  dx may be dy or dh, d_residual may be dh.  The same inputs give the
+ * same bits in every call. */
+ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const void* h,
+                               const void* dh, const void* weight, const float* stats, void* dx,
+                               void* d_residual, void* d_weight, void* d_bias, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The scan's output y under its gate z, normed in each of `groups` equal groups of columns:
+ *     v = y z / (1 + exp(-z));  out = v rstd weight,  rstd = (mean over the group of v^2 + eps)^-1/2.
+ * Groups of up to 16384 columns, 8192 where a row does not start on 16 bytes. */
+typedef struct {
+    int64_t rows;
+    int64_t y_stride, z_stride, out_stride;  /* out_stride: out; dout in the backward */
+    int64_t dy_stride, dz_stride;            /* backward (any value >= dim in a forward) */
+    int32_t dim;
+    int32_t groups;
+    int32_t dtype;       /* ssd_dtype_t of y, z, out and their gradients */
+    int32_t wdtype;      /* of weight and its gradient */
+    float eps;
+} ssd_gated_norm_t;
+
+/* Writes out and rstd [rows][groups] float32 (may be NULL).  out may be y or z. */
+ssd_status_t ssd_gated_norm_forward(const ssd_gated_norm_t* norm, const void* y, const void* z,
+                                    const void* weight, void* out, float* rstd, void* stream);
+
+ssd_status_t ssd_gated_norm_workspace_size(const ssd_gated_norm_t* norm, size_t* bytes);
+
+/* dy, dz, d_weight from dout and the forward's rstd.  dy and dz may each be one of the
+ * inputs.  The same inputs give the same bits in every call. */
+ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* dout, const void* y,
+                                     const void* z, const void* weight, const float* rstd,
+                                     void* dy, void* dz, void* d_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and returns in *device_status the status word that
  * the last call using `workspace` left (SSD_OK, SSD_ERR_DEVICE, SSD_ERR_TIMEOUT).
  * Returns SSD_ERR_CUDA if the synchronisation itself failed. */

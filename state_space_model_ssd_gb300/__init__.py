@@ -11,6 +11,9 @@ missing library or a non-CUDA tensor raises.
 Layouts: x, y, dy, dx ``[batch, L, H, P]``; raw_dt ``[batch, L, H]`` float32;
 B, C ``[batch, L, G, N]``; with ``cu_seqlens`` (int32, ``[nseq + 1]``) the batch
 is 1 and the tokens are packed sequences.
+
+The operators that stand around the scan in a layer (``conv_forward``, ``conv_decode_step``,
+``norm_forward``, ``gated_norm_forward`` and their backward passes) are in ``layer``.
 """
 
 from __future__ import annotations
@@ -22,7 +25,20 @@ from . import _lib
 from ._lib import SSDError, check
 
 __all__ = ["forward", "backward", "bidirectional_forward", "bidirectional_backward", "decode_step", "step_host", "step_host_size", "workspace_size",
-           "dispatch_path", "make_problem", "last_launch_count", "profiler", "SSDError"]
+           "dispatch_path", "make_problem", "last_launch_count", "profiler", "SSDError",
+           "conv_forward", "conv_backward", "conv_decode_step", "norm_forward", "norm_backward",
+           "gated_norm_forward", "gated_norm_backward"]
+
+_LAYER = frozenset(__all__[-7:])
+
+
+def __getattr__(name):
+    # the operators around the scan live in .layer, which imports torch: loaded on first use
+    if name in _LAYER:
+        from . import layer
+        globals()[name] = f = getattr(layer, name)
+        return f
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def _torch():

@@ -36,6 +36,56 @@ class Problem(ctypes.Structure):
     ]
 
 
+class ConvProblem(ctypes.Structure):
+    """Mirror of ssd_conv_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("u_stride", ctypes.c_int64),
+        ("du_stride", ctypes.c_int64),
+        ("split", ctypes.c_int32 * 3),
+        ("width", ctypes.c_int32),
+        ("nseq", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("wdtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+    ]
+
+
+class NormProblem(ctypes.Structure):
+    """Mirror of ssd_norm_t."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("r_stride", ctypes.c_int64),
+        ("h_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("dim", ctypes.c_int32),
+        ("kind", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("rdtype", ctypes.c_int32),
+        ("wdtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class GatedNormProblem(ctypes.Structure):
+    """Mirror of ssd_gated_norm_t."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64),
+        ("dz_stride", ctypes.c_int64),
+        ("dim", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("wdtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class SSDError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -46,7 +96,11 @@ _lib = None
 
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(Problem)
+_PC = ctypes.POINTER(ConvProblem)
+_PN = ctypes.POINTER(NormProblem)
+_PG = ctypes.POINTER(GatedNormProblem)
 _SZ = ctypes.c_size_t
+_I32 = ctypes.c_int32
 _SIGS = {
     "ssd_workspace_size": (ctypes.c_int, [_PP, ctypes.c_int, ctypes.POINTER(_SZ)]),
     "ssd_forward": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
@@ -69,6 +123,16 @@ _SIGS = {
     "ssd_step_host_size": (ctypes.c_int, [_PP, ctypes.POINTER(_SZ)]),
     "ssd_step_host": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                      _VP, _VP, _VP, _SZ, _VP]),
+    "ssd_conv_forward": (ctypes.c_int, [_PC] + [_VP] * 11),
+    "ssd_conv_workspace_size": (ctypes.c_int, [_PC, ctypes.POINTER(_SZ)]),
+    "ssd_conv_backward": (ctypes.c_int, [_PC] + [_VP] * 15 + [_SZ, _VP]),
+    "ssd_conv_decode_step": (ctypes.c_int, [_PP, _I32, _I32, _I32, ctypes.c_int64] + [_VP] * 10),
+    "ssd_norm_forward": (ctypes.c_int, [_PN] + [_VP] * 8),
+    "ssd_norm_workspace_size": (ctypes.c_int, [_PN, ctypes.POINTER(_SZ)]),
+    "ssd_norm_backward": (ctypes.c_int, [_PN] + [_VP] * 10 + [_SZ, _VP]),
+    "ssd_gated_norm_forward": (ctypes.c_int, [_PG] + [_VP] * 6),
+    "ssd_gated_norm_workspace_size": (ctypes.c_int, [_PG, ctypes.POINTER(_SZ)]),
+    "ssd_gated_norm_backward": (ctypes.c_int, [_PG] + [_VP] * 9 + [_SZ, _VP]),
     "ssd_device_status": (ctypes.c_int, [_VP, _VP, ctypes.POINTER(ctypes.c_int32)]),
     "ssd_dispatch_path": (ctypes.c_char_p, [_PP, ctypes.c_int]),
     "ssd_last_launch_count": (ctypes.c_int, []),

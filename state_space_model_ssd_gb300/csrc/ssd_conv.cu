@@ -1,0 +1,714 @@
+// Short causal depthwise convolution over the tokens of packed or dense sequences, with its
+// carried window, and its backward pass.  Channel c, K taps, sequence tokens i = 0, 1, ...
+// at positions p0 + i:
+//
+//   pre[i] = b + sum_{j < K} w[c][K-1-j] u[i-j],   u[-m]: the carried state's token at p0 - m
+//   out[i] = pre[i] sigmoid(pre[i])                (or pre[i])
+//
+//   g[i]   = dout[i] s (1 + pre (1 - s)),  s = sigmoid(pre[i])
+//   du[i]  = sum_{j < K} w[K-1-j] g[i+j]   (tokens of the same sequence)
+//   dw[k]  = sum_i g[i] u[i-(K-1-k)],  db = sum_i g[i]
+//
+// The state of a sequence is K rows of channels; row p mod K holds the token at position p.
+// A step at position p reads the rows of p-1 .. p-K+1 and writes only row p mod K, which no
+// reader of that step needs: the one-token kernel needs no second buffer and no barrier
+// between blocks.
+//
+// Both passes are bound by HBM (forward: u in, out out; backward: u, dout in, du out; about
+// 6 and 12 multiply-adds an element).  A thread owns VEC neighbouring channels and walks a
+// run of tokens with the window in registers, so every element is loaded once, plus K-1
+// tokens at the run's start (forward) or 2 (K-1) around it (backward, which recomputes g
+// there) that its neighbours have brought into L2.
+#include <limits.h>
+
+#include "layer_device.cuh"
+#include "layer_host.cuh"
+
+namespace ssd {
+namespace layer {
+
+namespace {
+
+constexpr int kLanes = 32;   // channel vectors a block covers
+constexpr int kRuns = 8;     // runs of tokens a block covers
+
+struct ConvArgs {
+    const void* u;
+    const void* w;
+    const void* b;
+    const int* cu;
+    const int* pos;
+    const void* init;
+    void* out[3];         // forward outputs, or the backward's dout (read only)
+    const void* dfinal;
+    void* final_state;
+    void* du;
+    void* dinit;
+    float* partial;
+    long long T, L;       // all tokens, tokens per dense row
+    long long us, dus;    // token strides of u and du, elements
+    long long C;
+    int off1, off2;       // first channel of pieces 1 and 2
+    int width[3];
+    int nseq;             // sequences (dense rows or packed)
+    int run;              // tokens a thread walks
+    int nrunblk;          // blocks along the tokens
+    int nchblk;           // blocks along the channels
+    int wbf16;
+};
+
+struct Seq {
+    int s;
+    long long start, end;
+    bool live;            // false: tokens after the last packed sequence
+};
+
+__device__ __forceinline__ long long clampll(long long v, long long lo, long long hi) {
+    return v < lo ? lo : v > hi ? hi : v;
+}
+
+// The sequence of token t.  Packed: the first s whose end lies beyond t; start and end are
+// clamped around t, so that a malformed cu_seqlens gives wrong values, never an access out
+// of range.  Tokens from cu[nseq] on belong to no sequence.
+__device__ __forceinline__ Seq seq_of(const ConvArgs& a, long long t) {
+    Seq q;
+    q.live = true;
+    if (!a.cu) {
+        q.s = (int)(t / a.L);
+        q.start = q.s * a.L;
+        q.end = q.start + a.L;
+        return q;
+    }
+    int lo = 0, hi = a.nseq;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid + 1] > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    q.s = lo;
+    q.start = lo == 0 ? 0 : clampll(a.cu[lo], 0, t);
+    q.live = lo < a.nseq;
+    q.end = q.live ? clampll(a.cu[lo + 1], t + 1, a.T) : a.T;
+    return q;
+}
+// Sequence s as a whole (possibly empty).
+__device__ __forceinline__ Seq seq_at(const ConvArgs& a, int s) {
+    Seq q;
+    q.s = s;
+    q.live = true;
+    if (!a.cu) {
+        q.start = s * a.L;
+        q.end = q.start + a.L;
+    } else {
+        q.start = s == 0 ? 0 : clampll(a.cu[s], 0, a.T);
+        q.end = clampll(a.cu[s + 1], q.start, a.T);
+    }
+    return q;
+}
+
+template <int K>
+__device__ __forceinline__ int state_row(long long p) {
+    const int r = (int)(p % K);
+    return r < 0 ? r + K : r;
+}
+
+// Token i of the sequence that starts at q.start (i < 0: from the carried state), channels
+// c .. c + VEC.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void token(const ConvArgs& a, const Seq& q, long long i, long long c,
+                                      float* f) {
+    Pack<T, VEC> v;
+    if (i >= 0) {
+        v.load(static_cast<const T*>(a.u) + (q.start + i) * a.us + c);
+    } else if (a.init && q.live) {
+        const long long p0 = a.pos ? a.pos[q.s] : 0;
+        v.load(static_cast<const T*>(a.init) + ((long long)q.s * K + state_row<K>(p0 + i)) * a.C + c);
+    } else {
+        v.zero();
+    }
+    v.get(f);
+}
+
+// Weights and bias of a block's channels, transposed to [K + 1][channels] in shared memory
+// (row K is the bias): a thread's VEC channels are then neighbours in every row.
+template <int VEC, int K>
+__device__ __forceinline__ void stage_weights(const ConvArgs& a, long long c0,
+                                              float (*ws)[kLanes * VEC]) {
+    const int tid = threadIdx.y * kLanes + threadIdx.x;
+    const long long n = a.C - c0 < kLanes * VEC ? a.C - c0 : kLanes * VEC;
+    for (int i = tid; i < n * K; i += kLanes * kRuns)
+        ws[i % K][i / K] = param(a.w, c0 * K + i, a.wbf16);
+    for (int i = tid; i < n; i += kLanes * kRuns) ws[K][i] = a.b ? param(a.b, c0 + i, a.wbf16) : 0.f;
+    __syncthreads();
+}
+
+// The piece of the split output that holds channels c .. c + VEC (the split respects VEC).
+template <typename T>
+__device__ __forceinline__ T* piece(const ConvArgs& a, long long c, int* stride) {
+    const int k = c >= a.off2 ? 2 : c >= a.off1 ? 1 : 0;
+    *stride = k == 2 ? a.width[2] : k == 1 ? a.width[1] : a.width[0];
+    T* p = static_cast<T*>(k == 2 ? a.out[2] : k == 1 ? a.out[1] : a.out[0]);
+    return p + (c - (k == 2 ? a.off2 : k == 1 ? a.off1 : 0));
+}
+
+// ------------------------------------------------------------------ forward
+template <typename T, int VEC, int K>
+__global__ void __launch_bounds__(kLanes* kRuns) conv_fwd_kernel(const ConvArgs a, bool silu) {
+    __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
+    const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
+    const long long c0 = (long long)cb * kLanes * VEC;
+    const long long c = c0 + threadIdx.x * VEC;
+    const T* __restrict__ u = static_cast<const T*>(a.u);
+
+    if (rb >= a.nrunblk) {  // the states: one (sequence, row) per thread row
+        const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
+        if (c >= a.C || item >= (long long)a.nseq * K) return;
+        const Seq q = seq_at(a, (int)(item / K));
+        const int r = (int)(item % K);
+        const long long p0 = a.pos ? a.pos[q.s] : 0;
+        const long long last = p0 + (q.end - q.start) - 1;
+        const long long i = last - state_row<K>(last - r) - p0;  // token on row r: last such position
+        float f[VEC];
+        token<T, VEC, K>(a, q, i, c, f);
+        store_vec<VEC>(static_cast<T*>(a.final_state) + item * a.C + c, f);
+        return;
+    }
+
+    stage_weights<VEC, K>(a, c0, ws);
+    const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
+    const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
+    if (c >= a.C || t0 >= t1) return;
+    float w[K][VEC], b[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        b[e] = ws[K][threadIdx.x * VEC + e];
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k][e] = ws[k][threadIdx.x * VEC + e];
+    }
+    int ostride;
+    T* out = piece<T>(a, c, &ostride);
+
+    Seq q = seq_of(a, t0);
+    float win[K - 1][VEC];  // win[j]: token t - 1 - j
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
+
+    constexpr int U = VEC == 1 ? 8 : 4;  // tokens in flight
+    for (long long t = t0; t < t1; t += U) {
+        Pack<T, VEC> raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i < t1) raw[i].load(u + (t + i) * a.us + c);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (t + i >= t1) break;
+            if (t + i == q.end) {
+                q = seq_of(a, t + i);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, -1 - j, c, win[j]);
+            }
+            float cur[VEC], o[VEC];
+            raw[i].get(cur);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float v = fmaf(w[K - 1][e], cur[e], b[e]);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) v = fmaf(w[K - 2 - j][e], win[j][e], v);
+                o[e] = silu ? v * sigmoid_of<T>(v) : v;
+                if (!q.live) o[e] = 0.f;
+#pragma unroll
+                for (int j = K - 2; j > 0; --j) win[j][e] = win[j - 1][e];
+                win[0][e] = cur[e];
+            }
+            store_vec<VEC>(out + (t + i) * ostride, o);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// g and its ingredients at one token: pre from the current token and its window.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void grad_pre(const float (*w)[VEC], const float* b, const float* cur,
+                                         const float (*win)[VEC], const float* dy, bool silu,
+                                         float* g) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        if (!silu) {
+            g[e] = dy[e];
+            continue;
+        }
+        float v = fmaf(w[K - 1][e], cur[e], b[e]);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) v = fmaf(w[K - 2 - j][e], win[j][e], v);
+        const float s = sigmoid_of<T>(v);
+        g[e] = dy[e] * (s * fmaf(v, 1.f - s, 1.f));
+    }
+}
+
+// The carried state's gradient, row r of sequence q: from the first tokens that read the
+// row's position p0 - m, and passed through where the row is still in the final state.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, long long c,
+                                           const float (*w)[VEC], const float* b, bool silu) {
+    const long long p0 = a.pos ? a.pos[q.s] : 0;
+    const long long n = q.end - q.start;
+    int m = state_row<K>(p0 - r);
+    if (m == 0) m = K;
+    const long long at = ((long long)q.s * K + r) * a.C + c;
+    float d[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+    if (a.dfinal && m + n <= K) {
+        Pack<T, VEC> v;
+        v.load(static_cast<const T*>(a.dfinal) + at);
+        v.get(d);
+    }
+    int dstride;
+    const T* dout = piece<T>(a, c, &dstride);
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        if (i >= n || i + m >= K) break;
+        float cur[VEC], win[K - 1][VEC], dy[VEC], g[VEC];
+        token<T, VEC, K>(a, q, i, c, cur);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, i - 1 - j, c, win[j]);
+        Pack<T, VEC> v;
+        v.load(dout + (q.start + i) * dstride);
+        v.get(dy);
+        grad_pre<T, VEC, K>(w, b, cur, win, dy, silu, g);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k == K - 1 - (i + m))
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) d[e] = fmaf(w[k][e], g[e], d[e]);
+    }
+    store_vec<VEC>(static_cast<T*>(a.dinit) + at, d);
+}
+
+template <typename T, int VEC, int K>
+__global__ void __launch_bounds__(kLanes* kRuns) conv_bwd_kernel(const ConvArgs a, bool silu) {
+    __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
+    __shared__ float red[kRuns][K + 1][kLanes * VEC];
+    const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
+    const long long c0 = (long long)cb * kLanes * VEC;
+    const long long c = c0 + threadIdx.x * VEC;
+    const T* __restrict__ u = static_cast<const T*>(a.u);
+
+    stage_weights<VEC, K>(a, c0, ws);
+    float w[K][VEC], b[VEC];
+    if (c < a.C) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            b[e] = ws[K][threadIdx.x * VEC + e];
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][e] = ws[k][threadIdx.x * VEC + e];
+        }
+    }
+    if (rb >= a.nrunblk) {  // the carried states' gradients
+        const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
+        if (c < a.C && item < (long long)a.nseq * K)
+            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, w, b, silu);
+        return;
+    }
+
+    const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
+    const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
+    float dw[K + 1][VEC];
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
+
+    if (c < a.C && t0 < t1) {
+        int dstride;
+        const T* __restrict__ dout = piece<T>(a, c, &dstride);
+        T* du = static_cast<T*>(a.du);
+        // g of the K-1 tokens after the run reaches back into it
+        const long long t2 = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;
+        Seq q = seq_of(a, t0);
+        float win[K - 1][VEC];  // win[j]: token t - 1 - j
+        float acc[K][VEC];      // acc[j]: du of token t - j so far
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+
+        constexpr int U = VEC == 1 ? 4 : 2;  // tokens in flight
+        for (long long t = t0; t < t2; t += U) {
+            Pack<T, VEC> ru[U], rd[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (t + i < t2) {
+                    ru[i].load(u + (t + i) * a.us + c);
+                    rd[i].load(dout + (t + i) * dstride);
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const long long tt = t + i;
+                if (tt >= t2) break;
+                if (tt == q.end) {
+                    q = seq_of(a, tt);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, -1 - j, c, win[j]);
+                }
+                float cur[VEC], dy[VEC], g[VEC];
+                ru[i].get(cur);
+                rd[i].get(dy);
+                grad_pre<T, VEC, K>(w, b, cur, win, dy, silu, g);
+                if (!q.live)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) g[e] = 0.f;
+                if (tt < t1 && q.live) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        dw[K][e] += g[e];
+                        dw[K - 1][e] = fmaf(g[e], cur[e], dw[K - 1][e]);
+#pragma unroll
+                        for (int j = 0; j < K - 1; ++j)
+                            dw[K - 2 - j][e] = fmaf(g[e], win[j][e], dw[K - 2 - j][e]);
+                    }
+                }
+                // shift: acc[j] becomes token tt - j; token tt starts from the final state's
+                // gradient where it is still in the window there
+#pragma unroll
+                for (int j = K - 1; j > 0; --j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[j][e] = acc[j - 1][e];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[0][e] = 0.f;
+                if (a.dfinal && q.live && q.end - tt <= K) {
+                    const long long p = (a.pos ? a.pos[q.s] : 0) + (tt - q.start);
+                    Pack<T, VEC> v;
+                    v.load(static_cast<const T*>(a.dfinal) +
+                           ((long long)q.s * K + state_row<K>(p)) * a.C + c);
+                    v.get(acc[0]);
+                }
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (tt - j >= q.start)  // a token of an earlier sequence gets nothing
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            acc[j][e] = fmaf(w[K - 1 - j][e], g[e], acc[j][e]);
+                if (tt - (K - 1) >= t0) store_vec<VEC>(du + (tt - (K - 1)) * a.dus + c, acc[K - 1]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+                    for (int j = K - 2; j > 0; --j) win[j][e] = win[j - 1][e];
+                    win[0][e] = cur[e];
+                }
+            }
+        }
+        // the last tokens of the run that nothing later reads
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const long long tok = t2 - 1 - j;
+            if (tok >= t0 && tok < t1) store_vec<VEC>(du + tok * a.dus + c, acc[j]);
+        }
+    }
+
+    // one partial per block, weight and channel: the runs are added in order
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) red[threadIdx.y][k][e * kLanes + threadIdx.x] = dw[k][e];
+    __syncthreads();
+    const int tid = threadIdx.y * kLanes + threadIdx.x;
+    for (int i = tid; i < (K + 1) * kLanes * VEC; i += kLanes * kRuns) {
+        const int k = i / (kLanes * VEC), x = i - k * kLanes * VEC;
+        const long long ch = c0 + x;
+        if (ch >= a.C) continue;
+        const int at = (x % VEC) * kLanes + x / VEC;
+        float s = 0.f;
+#pragma unroll
+        for (int y = 0; y < kRuns; ++y) s += red[y][k][at];
+        a.partial[((long long)rb * (K + 1) + k) * a.C + ch] = s;
+    }
+}
+
+// ------------------------------------------------------------------ host
+struct Conv {
+    long long T, C;
+    int nseq;
+    size_t e;
+};
+
+ssd_status_t check_conv(const ssd_conv_t* p, Conv* c) {
+    if (!p) return SSD_ERR_INVALID_ARG;
+    if (p->batch < 1 || p->seqlen < 0 || p->nseq < 0) return SSD_ERR_INVALID_ARG;
+    if (p->nseq > 0 && p->batch != 1) return SSD_ERR_INVALID_ARG;
+    if (!dtype_ok(p->dtype) || !dtype_ok(p->wdtype)) return SSD_ERR_INVALID_ARG;
+    if (p->activation != 0 && p->activation != 1) return SSD_ERR_INVALID_ARG;
+    long long C = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (p->split[i] < 0 || (i > 0 && p->split[i] > 0 && p->split[i - 1] == 0))
+            return SSD_ERR_INVALID_ARG;
+        C += p->split[i];
+    }
+    if (C < 1) return SSD_ERR_INVALID_ARG;
+    if (p->u_stride < C || (p->du_stride != 0 && p->du_stride < C)) return SSD_ERR_INVALID_ARG;
+    if (p->width < 1) return SSD_ERR_INVALID_ARG;
+    if (p->width < 2 || p->width > 4 || C > (1 << 24)) return SSD_ERR_UNSUPPORTED;
+    if (p->seqlen > INT_MAX || p->batch > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    c->T = p->batch * p->seqlen;
+    if (c->T > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    c->C = C;
+    c->nseq = p->nseq > 0 ? p->nseq : (int)p->batch;
+    c->e = dtype_size(p->dtype);
+    return SSD_OK;
+}
+
+// Whether every row of every tensor starts on a vector of n elements (n * e bytes).
+bool fits(const ssd_conv_t* p, const Conv& c, int n, const void* const* ptrs, int np) {
+    for (int i = 0; i < 3; ++i)
+        if (p->split[i] % n) return false;
+    if (p->u_stride % n || p->du_stride % n) return false;
+    for (int i = 0; i < np; ++i)
+        if (!aligned_to(ptrs[i], n * c.e)) return false;
+    return true;
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// Tokens a thread walks.  Long runs re-read less (K-1 tokens a run) but leave fewer threads:
+// the longest power of two up to `most` that still gives every SM `want` threads.
+int choose_run(long long T, long long nvec, int most, int want) {
+    const long long need = (long long)sm_count() * want;
+    int run = most;
+    while (run > 1 && (T + run - 1) / run * nvec < need) run >>= 1;
+    return run;
+}
+
+// Blocks along the tokens of the backward: the partial sums' count, and with it the
+// workspace, follows it; at most kMaxRunBlocks.
+constexpr int kMaxRunBlocks = 1024;
+int bwd_run(long long T, long long C, int vec) {
+    int run = choose_run(T, (C + vec - 1) / vec, 64, 1024);
+    while ((T + (long long)run * kRuns - 1) / ((long long)run * kRuns) > kMaxRunBlocks) run <<= 1;
+    return run;
+}
+
+void fill_args(const ssd_conv_t* p, const Conv& c, ConvArgs* a) {
+    a->T = c.T;
+    a->L = p->seqlen;
+    a->C = c.C;
+    a->us = p->u_stride;
+    a->dus = p->du_stride;
+    // an absent piece starts at the channel count, where no channel falls into it
+    a->off1 = p->split[1] ? p->split[0] : (int)c.C;
+    a->off2 = p->split[2] ? p->split[0] + p->split[1] : (int)c.C;
+    for (int i = 0; i < 3; ++i) a->width[i] = p->split[i];
+    a->nseq = c.nseq;
+    a->wbf16 = p->wdtype == SSD_DTYPE_BF16;
+}
+
+template <typename T, int VEC>
+void launch_fwd(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+    const dim3 blk(kLanes, kRuns);
+    if (K == 2)
+        conv_fwd_kernel<T, VEC, 2><<<grid, blk, 0, s>>>(a, silu);
+    else if (K == 3)
+        conv_fwd_kernel<T, VEC, 3><<<grid, blk, 0, s>>>(a, silu);
+    else
+        conv_fwd_kernel<T, VEC, 4><<<grid, blk, 0, s>>>(a, silu);
+}
+template <typename T, int VEC>
+void launch_bwd(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+    const dim3 blk(kLanes, kRuns);
+    if (K == 2)
+        conv_bwd_kernel<T, VEC, 2><<<grid, blk, 0, s>>>(a, silu);
+    else if (K == 3)
+        conv_bwd_kernel<T, VEC, 3><<<grid, blk, 0, s>>>(a, silu);
+    else
+        conv_bwd_kernel<T, VEC, 4><<<grid, blk, 0, s>>>(a, silu);
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace ssd
+
+using namespace ssd;
+using namespace ssd::layer;
+
+extern "C" {
+
+ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void* weight,
+                              const void* bias, const int32_t* cu_seqlens,
+                              const int32_t* positions, const void* initial_state, void* out0,
+                              void* out1, void* out2, void* final_state, void* stream) {
+    set_last_launches(0);
+    Conv c;
+    ssd_status_t st = check_conv(conv, &c);
+    if (st != SSD_OK) return st;
+    if ((conv->nseq > 0) != (cu_seqlens != nullptr)) return SSD_ERR_INVALID_ARG;
+    void* outs[3] = {out0, out1, out2};
+    if (!weight) return SSD_ERR_INVALID_ARG;
+    if (c.T > 0) {
+        if (!u) return SSD_ERR_INVALID_ARG;
+        for (int i = 0; i < 3; ++i)
+            if (conv->split[i] && !outs[i]) return SSD_ERR_INVALID_ARG;
+    }
+    const void* ptrs[6] = {u, out0, out1, out2, initial_state, final_state};
+    for (const void* p : ptrs)
+        if (!aligned_to(p, c.e)) return SSD_ERR_ALIGNMENT;
+    if (!aligned_to(weight, dtype_size(conv->wdtype)) ||
+        !aligned_to(bias, dtype_size(conv->wdtype)) || !aligned_to(cu_seqlens, 4) ||
+        !aligned_to(positions, 4))
+        return SSD_ERR_ALIGNMENT;
+    // a run reads tokens and states that other blocks may already have written over
+    const Span in(u, c.T, conv->u_stride, c.C, c.e);
+    const long long srows = (long long)c.nseq * conv->width;
+    const Span si(initial_state, srows, c.C, c.C, c.e), so(final_state, srows, c.C, c.C, c.e);
+    if (so.overlaps(si) || so.overlaps(in)) return SSD_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        const Span o(outs[i], c.T, conv->split[i], conv->split[i], c.e);
+        if (conv->split[i] && (o.overlaps(in) || o.overlaps(si) || o.overlaps(so)))
+            return SSD_ERR_INVALID_ARG;
+    }
+    if (c.T == 0 && !final_state) return SSD_OK;
+
+    ConvArgs a = {};
+    fill_args(conv, c, &a);
+    a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
+    a.init = initial_state, a.final_state = final_state;
+    for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
+    const int vec = conv->dtype == SSD_DTYPE_BF16 ? 8 : 4;
+    const bool wide = fits(conv, c, vec, ptrs, 6);
+    const long long nvec = wide ? c.C / vec : c.C;
+    a.run = choose_run(c.T, nvec, 32, 1024);
+    a.nchblk = ceil_div(nvec, kLanes);
+    a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
+    const int nstate = final_state ? ceil_div(srows, kRuns) : 0;
+    const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);
+    if (grid > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    Launch L;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.begin("conv_fwd");
+    const bool silu = conv->activation == 1;
+    if (conv->dtype == SSD_DTYPE_BF16) {
+        if (wide)
+            launch_fwd<__nv_bfloat16, 8>(conv->width, (unsigned)grid, a, silu, L.stream);
+        else
+            launch_fwd<__nv_bfloat16, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
+    } else {
+        if (wide)
+            launch_fwd<float, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
+        else
+            launch_fwd<float, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
+    }
+    const cudaError_t e = L.end();
+    set_last_launches(L.count);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_conv_workspace_size(const ssd_conv_t* conv, size_t* bytes) {
+    if (!bytes) return SSD_ERR_INVALID_ARG;
+    Conv c;
+    ssd_status_t st = check_conv(conv, &c);
+    if (st != SSD_OK) return st;
+    size_t most = 0;
+    const int vecs[2] = {4, 1};  // either path may run, by the pointers' alignment
+    for (int vec : vecs) {
+        const int nb = ceil_div(c.T, (long long)bwd_run(c.T, c.C, vec) * kRuns);
+        const size_t n = sizeof(float) * (size_t)nb * (conv->width + 1) * c.C;
+        if (n > most) most = n;
+    }
+    *bytes = most > 256 ? (most + 255) / 256 * 256 : 256;
+    return SSD_OK;
+}
+
+ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void* weight,
+                               const void* bias, const int32_t* cu_seqlens,
+                               const int32_t* positions, const void* initial_state,
+                               const void* dout0, const void* dout1, const void* dout2,
+                               const void* d_final_state, void* du, void* d_weight, void* d_bias,
+                               void* d_initial_state, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    set_last_launches(0);
+    Conv c;
+    ssd_status_t st = check_conv(conv, &c);
+    if (st != SSD_OK) return st;
+    if ((conv->nseq > 0) != (cu_seqlens != nullptr)) return SSD_ERR_INVALID_ARG;
+    const void* douts[3] = {dout0, dout1, dout2};
+    if (!weight || !d_weight || (d_bias && !bias)) return SSD_ERR_INVALID_ARG;
+    if (conv->du_stride == 0) return SSD_ERR_INVALID_ARG;
+    if (c.T > 0) {
+        if (!u || !du) return SSD_ERR_INVALID_ARG;
+        for (int i = 0; i < 3; ++i)
+            if (conv->split[i] && !douts[i]) return SSD_ERR_INVALID_ARG;
+    }
+    const void* ptrs[8] = {u, dout0, dout1, dout2, initial_state, d_final_state, du, d_initial_state};
+    for (const void* p : ptrs)
+        if (!aligned_to(p, c.e)) return SSD_ERR_ALIGNMENT;
+    const size_t we = dtype_size(conv->wdtype);
+    if (!aligned_to(weight, we) || !aligned_to(bias, we) || !aligned_to(d_weight, we) ||
+        !aligned_to(d_bias, we) || !aligned_to(cu_seqlens, 4) || !aligned_to(positions, 4))
+        return SSD_ERR_ALIGNMENT;
+    const long long srows = (long long)c.nseq * conv->width;
+    const Span in(u, c.T, conv->u_stride, c.C, c.e), o(du, c.T, conv->du_stride, c.C, c.e);
+    const Span si(initial_state, srows, c.C, c.C, c.e), df(d_final_state, srows, c.C, c.C, c.e);
+    const Span di(d_initial_state, srows, c.C, c.C, c.e);
+    if (o.overlaps(in) || o.overlaps(si) || o.overlaps(df) || o.overlaps(di) || di.overlaps(si) ||
+        di.overlaps(in) || di.overlaps(df))
+        return SSD_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        const Span d(douts[i], c.T, conv->split[i], conv->split[i], c.e);
+        if (conv->split[i] && (o.overlaps(d) || di.overlaps(d))) return SSD_ERR_INVALID_ARG;
+    }
+    size_t need = 0;
+    st = ssd_conv_workspace_size(conv, &need);
+    if (st != SSD_OK) return st;
+    if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
+
+    ConvArgs a = {};
+    fill_args(conv, c, &a);
+    a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
+    a.init = initial_state, a.dfinal = d_final_state, a.du = du, a.dinit = d_initial_state;
+    for (int i = 0; i < 3; ++i) a.out[i] = const_cast<void*>(douts[i]);
+    a.partial = static_cast<float*>(workspace);
+    const bool wide = fits(conv, c, 4, ptrs, 8);
+    const long long nvec = wide ? c.C / 4 : c.C;
+    a.run = bwd_run(c.T, c.C, wide ? 4 : 1);
+    a.nchblk = ceil_div(nvec, kLanes);
+    a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
+    const int nstate = d_initial_state ? ceil_div(srows, kRuns) : 0;
+    const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);
+    if (grid > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    Launch L;
+    L.stream = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (grid > 0) {
+        L.begin("conv_bwd");
+        const bool silu = conv->activation == 1;
+        if (conv->dtype == SSD_DTYPE_BF16) {
+            if (wide)
+                launch_bwd<__nv_bfloat16, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
+            else
+                launch_bwd<__nv_bfloat16, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
+        } else {
+            if (wide)
+                launch_bwd<float, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
+            else
+                launch_bwd<float, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
+        }
+        e = L.end();
+    }
+    if (e == cudaSuccess) {
+        ReduceDst d = {};
+        for (int k = 0; k < conv->width; ++k) {
+            d.dst[k] = static_cast<char*>(d_weight) + k * we;
+            d.step[k] = conv->width;
+        }
+        d.dst[conv->width] = d_bias;
+        d.step[conv->width] = 1;
+        e = launch_partial_sum(a.partial, a.nrunblk, conv->width + 1, c.C, d, conv->wdtype, L);
+    }
+    set_last_launches(L.count);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"

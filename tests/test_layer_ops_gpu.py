@@ -1,0 +1,560 @@
+"""The operators around the scan on the GPU (convolution, one-token step, norm, gated norm and
+their backward passes) against 64-bit forms of their formulas, at the lengths, widths, strides
+and states where they can go wrong; bit-identical repeats; and agreement with one another."""
+
+import numpy as np
+import pytest
+
+import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import state_space_model_ssd_gb300 as m
+    from state_space_model_ssd_gb300 import build
+    build.build()
+    return m
+
+
+def _tdt(dtype):
+    import torch
+    return torch.bfloat16 if dtype == "bf16" else torch.float32
+
+
+def _dev(a, dtype):
+    """The values on the GPU in dtype, and back in 64 bits as the GPU sees them."""
+    import torch
+    t = torch.from_numpy(np.asarray(a, np.float32)).cuda().to(_tdt(dtype))
+    return t, t.double().cpu().numpy()
+
+
+def _strided(t, before, after):
+    """t as a slice of wider rows whose other columns are NaN."""
+    import torch
+    wide = torch.full(t.shape[:-1] + (before + t.shape[-1] + after,), float("nan"), dtype=t.dtype,
+                      device=t.device)
+    wide[..., before:before + t.shape[-1]] = t
+    return wide[..., before:before + t.shape[-1]]
+
+
+# ------------------------------------------------------------------ convolution
+
+# batch, L, cu_seqlens, split, width, dtype, parameter type, bias, state, strided, silu
+CONV = [
+    (1, 1, None, (8,), 4, "bf16", "f32", True, False, False, True),          # one token
+    (2, 2, None, (16, 8), 4, "f32", "f32", True, True, False, True),         # shorter than the window
+    (1, 3, None, (64, 16, 16), 4, "bf16", "f32", True, True, True, True),
+    (3, 70, None, (40, 8, 8), 3, "bf16", "bf16", False, True, False, True),
+    (1, 257, None, (7, 5, 1), 2, "bf16", "f32", True, True, True, True),     # odd channels
+    (2, 130, None, (33,), 4, "f32", "f32", True, False, True, False),        # no activation
+    (1, 700, [0, 1, 1, 3, 64, 65, 300, 700], (128, 64, 64), 4, "bf16", "f32", True, True, False, True),
+    (1, 90, [0, 0, 2, 5, 5, 90, 90], (12, 4, 4), 4, "f32", "f32", True, True, False, True),
+    (1, 64, [0, 10, 50], (16, 8, 8), 3, "bf16", "f32", True, True, False, True),  # 14 tokens of no sequence
+    (1, 5000, None, (264,), 4, "bf16", "f32", True, True, False, True),      # several blocks each way
+    (4, 1111, None, (31, 3, 3), 4, "f32", "bf16", True, True, False, True),
+]
+
+
+def _conv_case(case, seed=0):
+    bsz, L, cu, split, K, dt, wdt, has_b, state, strided, silu = case
+    rng = np.random.default_rng(seed)
+    C = sum(split)
+    n = len(cu) - 1 if cu else bsz
+    d = {"cut": [(0, a, b) for a, b in zip(cu, cu[1:])] if cu else [(i, 0, L) for i in range(bsz)]}
+    t, a = {}, {}
+    t["u"], a["u"] = _dev(rng.standard_normal((bsz, L, C)), dt)
+    t["w"], a["w"] = _dev(rng.uniform(-1, 1, (C, K)) / np.sqrt(K), wdt)
+    t["b"], a["b"] = _dev(rng.uniform(-1, 1, C) / np.sqrt(K), wdt)
+    t["init"], a["init"] = _dev(rng.standard_normal((n, K, C)), dt)
+    t["dfinal"], a["dfinal"] = _dev(rng.standard_normal((n, K, C)), dt)
+    t["dy"], a["dy"] = _dev(rng.standard_normal((bsz, L, C)), dt)
+    import torch
+    d["pos"] = rng.integers(0, 100, n)
+    t["pos"] = torch.from_numpy(d["pos"].astype(np.int32)).cuda()
+    t["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda") if cu else None
+    if not has_b:
+        t["b"], a["b"] = None, np.zeros(C)
+    if not state:
+        t["init"] = t["dfinal"] = t["pos"] = None
+        d["pos"] = np.zeros(n, int)
+        a["init"] = a["dfinal"] = None
+    if strided:
+        t["u"] = _strided(t["u"], 8, 16)
+    return d, t, a
+
+
+@pytest.mark.parametrize("case", CONV)
+def test_conv_forward(ssd, case):
+    split, K, dt, silu = case[3], case[4], case[5], case[10]
+    d, t, a = _conv_case(case)
+    outs, final = ssd.conv_forward(t["u"], t["w"], t["b"], split=split, cu_seqlens=t["cu"],
+                                   initial_state=t["init"], positions=t["pos"], final_state=True,
+                                   activation="silu" if silu else None)
+    want = np.zeros(a["u"].shape)
+    states = []
+    for q, (r, lo, hi) in enumerate(d["cut"]):
+        before = None if a["init"] is None else a["init"][q]
+        want[r, lo:hi], s, _ = ref.conv(a["u"][r, lo:hi], a["w"], a["b"], int(d["pos"][q]), before, silu)
+        states.append(s)
+    at = 0
+    for o, n in zip(outs, split):
+        ref.assert_close(o, want[..., at:at + n], dt, "out")
+        at += n
+    # the state holds tokens themselves
+    assert np.array_equal(final.double().cpu().numpy(), np.stack(states))
+
+
+@pytest.mark.parametrize("case", CONV)
+def test_conv_backward(ssd, case):
+    import torch
+    bsz, L, cu, split, K, dt, wdt, has_b, state, strided, silu = case
+    d, t, a = _conv_case(case, 1)
+    C = sum(split)
+    dys = tuple(p.contiguous() for p in t["dy"].split(split, -1))
+    out = {}
+    if strided:  # du as a slice of the projection's gradient, the rest untouched
+        wide = torch.full((bsz, L, C + 24), 7.0, dtype=t["u"].dtype, device="cuda")
+        out["du"] = wide[..., 16:16 + C]
+    g = ssd.conv_backward(t["u"], t["w"], t["b"], dys, cu_seqlens=t["cu"], initial_state=t["init"],
+                          positions=t["pos"], d_final_state=t["dfinal"], d_initial_state=state,
+                          activation="silu" if silu else None, out=out)
+    du = np.zeros(a["u"].shape)
+    dw, db, d0 = np.zeros((C, K)), np.zeros(C), []
+    for q, (r, lo, hi) in enumerate(d["cut"]):
+        before = None if a["init"] is None else a["init"][q]
+        dst = None if a["dfinal"] is None else a["dfinal"][q]
+        du[r, lo:hi], w_, b_, i_ = ref.conv_bwd(a["u"][r, lo:hi], a["w"], a["b"], a["dy"][r, lo:hi],
+                                               int(d["pos"][q]), before, dst, silu)
+        dw += w_
+        db += b_
+        d0.append(i_)
+    ref.assert_close(g["du"], du, dt, "du")
+    ref.assert_close(g["d_weight"], dw, wdt, "d_weight")
+    if has_b:
+        ref.assert_close(g["d_bias"], db, wdt, "d_bias")
+    else:
+        assert "d_bias" not in g
+    if state:
+        ref.assert_close(g["d_initial_state"], np.stack(d0), dt, "d_initial_state")
+    if strided:
+        assert bool((wide[..., :16] == 7).all()) and bool((wide[..., 16 + C:] == 7).all())
+
+
+def test_conv_gradients_match_differences(ssd):
+    """Directional derivatives of a scalar of the outputs and final states, float32."""
+    case = (1, 40, [0, 2, 21, 40], (10, 3), 4, "f32", "f32", True, True, False, True)
+    d, t, a = _conv_case(case, 2)
+    rng = np.random.default_rng(3)
+
+    def value(u, w, b, init):
+        s = 0.0
+        for q, (r, lo, hi) in enumerate(d["cut"]):
+            o, f, _ = ref.conv(u[0, lo:hi], w, b, int(d["pos"][q]), init[q])
+            s += (o * a["dy"][0, lo:hi]).sum() + (f * a["dfinal"][q]).sum()
+        return s
+
+    dys = tuple(p.contiguous() for p in t["dy"].split((10, 3), -1))
+    g = ssd.conv_backward(t["u"], t["w"], t["b"], dys, cu_seqlens=t["cu"], initial_state=t["init"],
+                          positions=t["pos"], d_final_state=t["dfinal"], d_initial_state=True)
+    names = ["du", "d_weight", "d_bias", "d_initial_state"]
+    args = [a["u"], a["w"], a["b"], a["init"]]
+    h = 1e-5  # central difference in 64 bits: error about h^2 and 1e-16 / h, both below 1e-9
+    for k, name in enumerate(names):
+        e = rng.standard_normal(args[k].shape)
+        up = [x + h * e if i == k else x for i, x in enumerate(args)]
+        dn = [x - h * e if i == k else x for i, x in enumerate(args)]
+        num = (value(*up) - value(*dn)) / (2 * h)
+        got = g[name].double().cpu().numpy().reshape(args[k].shape)
+        # the float32 gradient's own error, entry by entry, against its directional sum
+        tol = ref.CHAIN * np.abs(got).max() * np.abs(e).sum() + 1e-7 * abs(num)
+        assert abs((got * e).sum() - num) <= tol, name
+
+
+def test_conv_pieces_feed_the_scan(ssd):
+    """A prompt in two calls with carried states equals the prompt in one call."""
+    import torch
+    H, P, G, N, K, L = 4, 16, 1, 16, 4, 150
+    rng = np.random.default_rng(5)
+    C = H * P + 2 * G * N
+    u, _ = _dev(rng.standard_normal((2, L, C)), "f32")
+    w, _ = _dev(rng.uniform(-.5, .5, (C, K)), "f32")
+    b, _ = _dev(rng.uniform(-.5, .5, C), "f32")
+    raw = torch.from_numpy(rng.standard_normal((2, L, H)).astype(np.float32)).cuda()
+    split = ((H, P), (G, N), (G, N))
+    (x, B, Cc), win = ssd.conv_forward(u, w, b, split=split, final_state=True)
+    y, st = ssd.forward(x, raw, B, Cc, -4.6)
+    cut = 61
+    (x1, B1, C1), w1 = ssd.conv_forward(u[:, :cut].contiguous(), w, b, split=split, final_state=True)
+    y1, s1 = ssd.forward(x1, raw[:, :cut].contiguous(), B1, C1, -4.6)
+    pos = torch.full((2,), cut, dtype=torch.int32, device="cuda")
+    (x2, B2, C2), w2 = ssd.conv_forward(u[:, cut:].contiguous(), w, b, split=split, initial_state=w1,
+                                        positions=pos, final_state=True)
+    y2, s2 = ssd.forward(x2, raw[:, cut:].contiguous(), B2, C2, -4.6, initial_state=s1)
+    assert bool((torch.cat([x1, x2], 1) == x).all()) and bool((w2 == win).all())
+    ref.assert_close(torch.cat([y1, y2], 1), y.double().cpu().numpy(), "f32", "y")
+    # ... and token by token
+    state, window = torch.zeros_like(st), torch.zeros_like(win)
+    ys = []
+    for i in range(L):
+        pos.fill_(i)
+        ys.append(ssd.conv_decode_step(state, window, u[:, i], raw[:, i].contiguous(), w, b, pos, -4.6))
+    assert bool((window == win).all())
+    ref.assert_close(torch.stack(ys, 1), y.double().cpu().numpy(), "f32", "y by steps")
+    ref.assert_close(state, st.double().cpu().numpy(), "f32", "state by steps")
+
+
+def test_conv_malformed_lengths_stay_in_range(ssd):
+    """Entries beyond the tokens, negative or falling: the call returns, writes only its own
+    outputs, and leaves the device usable (the entries are clamped)."""
+    import torch
+    u = torch.randn(1, 50, 24, device="cuda")
+    w = torch.randn(24, 4, device="cuda")
+    for cu in ([0, 40, 20, 50], [0, 1000, 50], [-7, 10, 50], [30, 30, 30]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        guard = torch.full((3, 50, 24), 5.0, device="cuda")
+        ssd.conv_forward(u, w, None, cu_seqlens=c, out=guard[1:2], final_state=True)
+        g = ssd.conv_backward(u, w, None, u, cu_seqlens=c, d_initial_state=True)
+        torch.cuda.synchronize()
+        assert bool((guard[0] == 5).all()) and bool((guard[2] == 5).all())
+        assert bool(torch.isfinite(g["du"]).all())
+
+
+# ------------------------------------------------------------------ one token
+
+@pytest.mark.parametrize("dt,B,H,P,N,G,K,slots,strided", [
+    ("bf16", 1, 80, 64, 128, 1, 4, None, False), ("bf16", 5, 6, 64, 64, 2, 4, [3, -1, 0, 9, 5], True),
+    ("f32", 3, 2, 128, 128, 1, 3, [2, 0, 1], False), ("f32", 1, 1, 8, 8, 1, 2, [1], False),
+    ("bf16", 40, 4, 16, 32, 4, 4, None, True)])
+def test_step(ssd, dt, B, H, P, N, G, K, slots, strided):
+    import torch
+    rng = np.random.default_rng(B + H)
+    C = H * P + 2 * G * N
+    n = B if slots is None else 7
+    st, st64 = _dev(rng.standard_normal((n, H, P, N)), "f32")
+    wn, wn64 = _dev(rng.standard_normal((n, K, C)), dt)
+    u, u64 = _dev(rng.standard_normal((B, C)), dt)
+    w, w64 = _dev(rng.uniform(-1, 1, (C, K)), "f32")
+    b, b64 = _dev(rng.uniform(-1, 1, C), "f32")
+    raw = rng.standard_normal((B, H)).astype(np.float32)
+    pos = rng.integers(0, 1 << 30, B)
+    if strided:
+        u = _strided(u, 3, 5)
+    y = ssd.conv_decode_step(st, wn, u, torch.from_numpy(raw).cuda(), w, b,
+                             torch.from_numpy(pos.astype(np.int32)).cuda(), -4.6, ngroups=G,
+                             slots=None if slots is None else
+                             torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    want = np.zeros((B, H, P))
+    for i in range(B):
+        q = i if slots is None else slots[i]
+        if not 0 <= q < n:
+            continue
+        o, win, _ = ref.conv(u64[i:i + 1], w64, b64, int(pos[i]), wn64[q])
+        row = int(pos[i]) % K
+        wn64[q, row] = win[row]
+        x = o[0, :H * P].reshape(H, P)
+        Bm = np.repeat(o[0, H * P:H * P + G * N].reshape(G, N), H // G, 0)
+        Cm = np.repeat(o[0, H * P + G * N:].reshape(G, N), H // G, 0)
+        z = raw[i].astype(np.float64) - 4.6
+        delta = np.log1p(np.exp(z))
+        st64[q] = np.exp(-delta)[:, None, None] * st64[q] + (delta[:, None] * x)[..., None] * Bm[:, None]
+        want[i] = np.einsum("hpn,hn->hp", st64[q], Cm)
+    ref.assert_close(y, want, dt, "y")
+    ref.assert_close(st, st64, "f32", "state")
+    assert np.array_equal(wn.double().cpu().numpy(), wn64)
+
+
+# ------------------------------------------------------------------ norms
+
+# rows, D, dtype, residual type, parameter type, bias, kind, strided
+NORM = [
+    (1, 1, "f32", None, "f32", True, "rms", False), (3, 8, "bf16", "bf16", "f32", True, "layer", False),
+    (5, 2560, "bf16", "f32", "f32", True, "layer", True), (2, 2560, "bf16", "bf16", "bf16", False, "rms", True),
+    (130, 97, "bf16", "f32", "f32", True, "layer", False), (517, 1001, "f32", "f32", "f32", True, "layer", True),
+    (64, 256, "f32", None, "f32", False, "rms", False), (700, 64, "bf16", None, "f32", True, "layer", False),
+    (33, 4100, "f32", "f32", "f32", True, "layer", False), (9, 16384, "bf16", "f32", "f32", True, "layer", False),
+    (7, 8191, "bf16", "bf16", "f32", True, "layer", False), (11, 12000, "f32", None, "f32", True, "rms", False),
+    (2500, 1536, "bf16", "f32", "f32", True, "layer", False),
+]
+
+
+def _norm_case(case, seed):
+    R, D, dt, rdt, wdt, has_b, kind, strided = case
+    rng = np.random.default_rng(seed)
+    t, a = {}, {}
+    big = np.where(rng.random(D) < 0.05, 20.0, 1.0)
+    t["x"], a["x"] = _dev(rng.standard_normal((R, D)), dt)
+    t["res"], a["res"] = _dev(rng.standard_normal((R, D)) * big + 0.5, rdt or dt)
+    t["w"], a["w"] = _dev(1 + 0.2 * rng.standard_normal(D), wdt)
+    t["b"], a["b"] = _dev(rng.standard_normal(D), wdt)
+    t["dy"], a["dy"] = _dev(rng.standard_normal((R, D)), dt)
+    t["dh"], a["dh"] = _dev(rng.standard_normal((R, D)), rdt or dt)
+    if not has_b:
+        t["b"] = a["b"] = None
+    if rdt is None:
+        t["res"] = t["dh"] = a["res"] = a["dh"] = None
+    if strided:
+        for k in ("x", "res", "dy", "dh"):
+            t[k] = _strided(t[k], 16, 8)
+    return t, a
+
+
+@pytest.mark.parametrize("case", NORM)
+def test_norm_forward(ssd, case):
+    R, D, dt, rdt, wdt, has_b, kind, strided = case
+    t, a = _norm_case(case, 7)
+    y, h, stats = ssd.norm_forward(t["x"], t["w"], t["b"], residual=t["res"], kind=kind)
+    wy, wh, ws = ref.norm(a["x"], a["w"], a["b"], a["res"], 1e-5, kind == "layer")
+    # one column, or a row that is nearly constant, scales the input's own rounding by rstd
+    ref.assert_close(y, wy, dt, "y")
+    ref.assert_close(stats[:, 1], ws[:, 1], "f32", "rstd")
+    scale = np.abs(wh).max()
+    assert np.abs(stats[:, 0].double().cpu().numpy() - ws[:, 0]).max() <= ref.CHAIN * scale
+    if rdt is None:
+        assert h is t["x"]
+    else:
+        ref.assert_close(h, wh, rdt, "h")
+
+
+# A row of one column under rms: dx = rstd a (1 - xh^2) with xh^2 = 1 - eps rstd^2, so all but a
+# millionth of the two terms cancels and 2^-24 of a term is a hundredth of what is left.  The
+# bound's premise (no term much larger than the result) does not hold there.
+@pytest.mark.parametrize("case", [pytest.param(c, marks=pytest.mark.xfail(
+    strict=True, reason="float32 terms that cancel to a millionth")) if c[1] == 1 else c for c in NORM])
+def test_norm_backward(ssd, case):
+    import torch
+    R, D, dt, rdt, wdt, has_b, kind, strided = case
+    t, a = _norm_case(case, 8)
+    h, h64 = (t["x"], a["x"]) if rdt is None else (t["res"], a["res"])
+    _, _, st = ref.norm(h64, a["w"], None, None, 1e-5, kind == "layer")
+    stats = torch.from_numpy(st.astype(np.float32)).cuda()
+    g = ssd.norm_backward(t["dy"], h, t["w"], stats, dh=t["dh"], kind=kind, bias=has_b)
+    dv, dw, db = ref.norm_bwd(a["dy"], h64, a["w"], stats.double().cpu().numpy(), a["dh"], kind == "layer")
+    ref.assert_close(g["dx"], dv, dt, "dx")
+    ref.assert_close(g["d_weight"], dw, wdt, "d_weight")
+    assert ("d_bias" in g) == has_b
+    if has_b:
+        ref.assert_close(g["d_bias"], db, wdt, "d_bias")
+    if rdt is not None:
+        ref.assert_close(g["d_residual"], dv, rdt, "d_residual")
+        assert (g["d_residual"] is g["dx"]) == (rdt == dt)
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_norm_gradients_match_differences(ssd, kind):
+    import torch
+    case = (6, 40, "f32", "f32", "f32", True, kind, False)
+    t, a = _norm_case(case, 9)
+    _, h, stats = ssd.norm_forward(t["x"], t["w"], t["b"], residual=t["res"], kind=kind)
+    g = ssd.norm_backward(t["dy"], h, t["w"], stats, dh=t["dh"], kind=kind)
+
+    def value(x, w, b):
+        y, v, _ = ref.norm(x, w, b, a["res"], 1e-5, kind == "layer")
+        return (y * a["dy"]).sum() + (v * a["dh"]).sum()
+
+    rng = np.random.default_rng(10)
+    s = 1e-5
+    for k, name in enumerate(("dx", "d_weight", "d_bias")):
+        args = [a["x"], a["w"], a["b"]]
+        e = rng.standard_normal(args[k].shape)
+        up, dn = list(args), list(args)
+        up[k], dn[k] = args[k] + s * e, args[k] - s * e
+        num = (value(*up) - value(*dn)) / (2 * s)
+        got = g[name].double().cpu().numpy()
+        tol = ref.CHAIN * np.abs(got).max() * np.abs(e).sum() + 1e-7 * abs(num)
+        assert abs((got * e).sum() - num) <= tol, name
+
+
+def test_norm_in_place(ssd):
+    import torch
+    t, _ = _norm_case((37, 512, "bf16", "f32", "f32", True, "layer", False), 11)
+    y, h, st = ssd.norm_forward(t["x"], t["w"], t["b"], residual=t["res"])
+    x2, r2 = t["x"].clone(), t["res"].clone()
+    y2, h2, st2 = ssd.norm_forward(x2, t["w"], t["b"], residual=r2, out=x2, residual_out=r2)
+    assert y2 is x2 and h2 is r2
+    assert bool((y2 == y).all()) and bool((h2 == h).all()) and bool((st2 == st).all())
+    g = ssd.norm_backward(t["dy"], h, t["w"], st, dh=t["dh"])
+    dy2, dh2 = t["dy"].clone(), t["dh"].clone()
+    g2 = ssd.norm_backward(dy2, h, t["w"], st, dh=dh2, out={"dx": dy2, "d_residual": dh2})
+    for k in ("dx", "d_residual", "d_weight", "d_bias"):
+        assert bool((g[k] == g2[k]).all()), k
+
+
+def test_norm_of_a_large_offset_keeps_its_variance(ssd):
+    """Rows of 1000 + noise: the sum of squares about the mean, not E[v^2] - mean^2."""
+    import torch
+    rng = np.random.default_rng(12)
+    x, x64 = _dev(1000 + rng.standard_normal((4, 1024)), "f32")
+    w = torch.ones(1024, device="cuda")
+    _, _, stats = ssd.norm_forward(x, w)
+    _, _, st = ref.norm(x64, 1.0, None, None, 1e-5, True)
+    # the mean is off by at most a rounding or two of 1000 (1e-4), which adds its square
+    assert np.abs(stats[:, 1].double().cpu().numpy() / st[:, 1] - 1).max() <= ref.CHAIN
+
+
+# rows, D, groups, dtype, parameter type, strided
+GATED = [(1, 1, 1, "f32", "f32", False), (3, 64, 1, "bf16", "f32", True), (5, 5120, 8, "bf16", "f32", True),
+         (40, 1536, 1, "bf16", "bf16", False), (33, 105, 3, "bf16", "f32", True), (600, 96, 2, "f32", "f32", True),
+         (9, 16384, 1, "bf16", "f32", False), (17, 999, 1, "f32", "f32", False), (2100, 1024, 4, "bf16", "f32", False)]
+
+
+def _gated_case(case, seed):
+    R, D, G, dt, wdt, strided = case
+    rng = np.random.default_rng(seed)
+    t, a = {}, {}
+    for k in ("y", "z", "dout"):
+        t[k], a[k] = _dev(rng.standard_normal((R, D)) * (3 if k == "z" else 1), dt)
+    t["w"], a["w"] = _dev(1 + 0.2 * rng.standard_normal(D), wdt)
+    if strided:
+        t["z"] = _strided(t["z"], 8, 24)
+    return t, a
+
+
+@pytest.mark.parametrize("case", GATED)
+def test_gated_norm(ssd, case):
+    import torch
+    R, D, G, dt, wdt, strided = case
+    t, a = _gated_case(case, 13)
+    out, rstd = ssd.gated_norm_forward(t["y"], t["z"], t["w"], groups=G)
+    wo, wr = ref.gated(a["y"], a["z"], a["w"], 1e-5, G)
+    ref.assert_close(out, wo, dt, "out")
+    ref.assert_close(rstd, wr, "f32", "rstd")
+    og = {}
+    if strided:
+        wide = torch.full((R, D + 32), 7.0, dtype=t["y"].dtype, device="cuda")
+        og["dz"] = wide[:, 8:8 + D]
+    g = ssd.gated_norm_backward(t["dout"], t["y"], t["z"], t["w"], rstd, groups=G, out=og)
+    dy, dz, dw = ref.gated_bwd(a["dout"], a["y"], a["z"], a["w"], rstd.double().cpu().numpy(), G)
+    ref.assert_close(g["dy"], dy, dt, "dy")
+    ref.assert_close(g["dz"], dz, dt, "dz")
+    ref.assert_close(g["d_weight"], dw, wdt, "d_weight")
+    if strided:
+        assert bool((wide[:, :8] == 7).all()) and bool((wide[:, 8 + D:] == 7).all())
+
+
+def test_gated_norm_gradients_match_differences(ssd):
+    t, a = _gated_case((5, 48, 3, "f32", "f32", False), 14)
+    out, rstd = ssd.gated_norm_forward(t["y"], t["z"], t["w"], groups=3)
+    g = ssd.gated_norm_backward(t["dout"], t["y"], t["z"], t["w"], rstd, groups=3)
+    rng = np.random.default_rng(15)
+    s = 1e-5
+    for k, name in enumerate(("dy", "dz", "d_weight")):
+        args = [a["y"], a["z"], a["w"]]
+        e = rng.standard_normal(args[k].shape)
+        up, dn = list(args), list(args)
+        up[k], dn[k] = args[k] + s * e, args[k] - s * e
+        num = ((ref.gated(*up, 1e-5, 3)[0] - ref.gated(*dn, 1e-5, 3)[0]) * a["dout"]).sum() / (2 * s)
+        got = g[name].double().cpu().numpy()
+        tol = ref.CHAIN * np.abs(got).max() * np.abs(e).sum() + 1e-7 * abs(num)
+        assert abs((got * e).sum() - num) <= tol, name
+
+
+def test_gated_norm_takes_the_scan_layout(ssd):
+    import torch
+    y = torch.randn(2, 9, 4, 16, device="cuda")
+    z = torch.randn(2, 9, 64, device="cuda")
+    w = torch.randn(64, device="cuda")
+    out, rstd = ssd.gated_norm_forward(y, z, w)
+    out2, _ = ssd.gated_norm_forward(y.view(2, 9, 64), z, w)
+    assert out.shape == z.shape and bool((out == out2).all())
+    g = ssd.gated_norm_backward(out, y, z, w, rstd)
+    assert g["dy"].shape == y.shape and g["dz"].shape == z.shape
+
+
+def test_extreme_gates_stay_finite(ssd):
+    """silu and its derivative at the ends of the range: exactly 0 below, z above."""
+    import torch
+    for dt in (torch.float32, torch.bfloat16):
+        z = torch.tensor([[-3e38, -1e4, -100.0, -20.0, 0.0, 20.0, 100.0, 1e4]], device="cuda").to(dt)
+        y = torch.ones_like(z)
+        w = torch.ones(8, device="cuda")
+        out, rstd = ssd.gated_norm_forward(y, z, w)
+        assert bool(torch.isfinite(out).all()) and bool((out[0, :3] == 0).all())
+        g = ssd.gated_norm_backward(y, y, z, w, rstd)
+        assert all(bool(torch.isfinite(v).all()) for v in g.values())
+
+
+# ------------------------------------------------------------------ shared
+
+def test_repeats_are_bit_identical(ssd):
+    import torch
+    case = (1, 3000, [0, 7, 1500, 1501, 3000], (256, 64, 64), 4, "bf16", "f32", True, True, False, True)
+    _, t, _ = _conv_case(case, 16)
+    dys = tuple(p.contiguous() for p in t["dy"].split((256, 64, 64), -1))
+    nt, _ = _norm_case((3000, 768, "bf16", "f32", "f32", True, "layer", False), 17)
+    gt, _ = _gated_case((3000, 768, 2, "bf16", "f32", False), 18)
+
+    def all_of():
+        c = ssd.conv_backward(t["u"], t["w"], t["b"], dys, cu_seqlens=t["cu"], initial_state=t["init"],
+                              positions=t["pos"], d_final_state=t["dfinal"], d_initial_state=True)
+        _, h, st = ssd.norm_forward(nt["x"], nt["w"], nt["b"], residual=nt["res"])
+        n = ssd.norm_backward(nt["dy"], h, nt["w"], st, dh=nt["dh"])
+        _, r = ssd.gated_norm_forward(gt["y"], gt["z"], gt["w"], groups=2)
+        g = ssd.gated_norm_backward(gt["dout"], gt["y"], gt["z"], gt["w"], r, groups=2)
+        return [v for d in (c, n, g) for v in d.values()]
+
+    first = all_of()
+    for _ in range(3):
+        assert all(bool((x == y).all()) for x, y in zip(first, all_of()))
+
+
+def test_empty_inputs(ssd):
+    import torch
+    u = torch.zeros(2, 0, 16, device="cuda")
+    w = torch.randn(16, 4, device="cuda")
+    init = torch.randn(2, 4, 16, device="cuda")
+    y, f = ssd.conv_forward(u, w, initial_state=init, final_state=True)
+    assert y.shape == (2, 0, 16) and bool((f == init).all())
+    g = ssd.conv_backward(u, w, None, y, initial_state=init, d_final_state=init, d_initial_state=True)
+    assert bool((g["d_weight"] == 0).all()) and bool((g["d_initial_state"] == init).all())
+    x = torch.zeros(0, 16, device="cuda")
+    w1 = torch.ones(16, device="cuda")
+    y, h, st = ssd.norm_forward(x, w1, residual=x)
+    g = ssd.norm_backward(y, h, w1, st, dh=h)
+    assert y.shape == (0, 16) and bool((g["d_weight"] == 0).all()) and bool((g["d_bias"] == 0).all())
+    o, r = ssd.gated_norm_forward(x, x, w1)
+    g = ssd.gated_norm_backward(o, x, x, w1, r)
+    assert bool((g["d_weight"] == 0).all())
+
+
+def test_other_stream(ssd):
+    """Work on a stream of its own, ordered only by events."""
+    import torch
+    nt, a = _norm_case((4096, 1024, "bf16", "f32", "f32", True, "layer", False), 19)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y, h, st = ssd.norm_forward(nt["x"], nt["w"], nt["b"], residual=nt["res"], stream=s)
+    g = ssd.norm_backward(nt["dy"], h, nt["w"], st, dh=nt["dh"], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    y2, h2, st2 = ssd.norm_forward(nt["x"], nt["w"], nt["b"], residual=nt["res"])
+    g2 = ssd.norm_backward(nt["dy"], h2, nt["w"], st2, dh=nt["dh"])
+    assert bool((y == y2).all()) and all(bool((g[k] == g2[k]).all()) for k in g)
+
+
+def test_offsets_beyond_32_bits(ssd):
+    """2,100,000 tokens of 1152 channels: 2.4e9 elements; the last tokens are checked."""
+    import torch
+    T, C, K = 2_100_000, 1152, 4
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    u = torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda")
+    u[:, :T - 64] = 0
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    u[:, T - 64:] = torch.randn(1, 64, C, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(C, K, generator=gen, device="cuda")
+    out, _ = ssd.conv_forward(u, w)
+    want, _, _ = ref.conv(u[0, T - 64:].double().cpu().numpy(), w.double().cpu().numpy(), 0.0)
+    ref.assert_close(out[0, T - 64:], want, "bf16", "out")
+    g = ssd.conv_backward(u, w, None, out, out={"du": torch.empty_like(u)})
+    du, _, _, _ = ref.conv_bwd(u[0, T - 64:].double().cpu().numpy(), w.double().cpu().numpy(), 0.0,
+                               out[0, T - 64:].double().cpu().numpy())
+    ref.assert_close(g["du"][0, T - 64:], du, "bf16", "du")
+    del g, out
+    x, _, _ = ssd.norm_forward(u, w[:, 0].contiguous(), stats=False, kind="rms")
+    want, _, _ = ref.norm(u[0, T - 64:].double().cpu().numpy(), w[:, 0].double().cpu().numpy(), None, None,
+                          1e-5, False)
+    ref.assert_close(x[0, T - 64:], want, "bf16", "norm")
