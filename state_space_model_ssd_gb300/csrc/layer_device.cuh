@@ -75,6 +75,8 @@ template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float* f) {
     if constexpr (VEC == 1) {
         *p = f[0];
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; i += 4)
@@ -89,6 +91,8 @@ template <int VEC>
 __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* f) {
     if constexpr (VEC == 1) {
         *p = __float2bfloat16_rn(f[0]);
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<uint32_t*>(p) = pack2(f[0], f[1]);
     } else if constexpr (VEC == 4) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
     } else {
@@ -97,10 +101,85 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* f) {
     }
 }
 
+template <>
+struct Pack<float, 2> {
+    float2 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ void get(float* f) const { f[0] = v.x, f[1] = v.y; }
+};
+template <>
+struct Pack<__nv_bfloat16, 2> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        v = *reinterpret_cast<const uint32_t*>(p);
+    }
+    __device__ __forceinline__ void zero() { v = 0u; }
+    __device__ __forceinline__ void get(float* f) const { unpack2(v, f); }
+};
+
+// Copies of a thread's own vectors into its own places of a ring in shared memory: they are
+// in flight without holding registers, and since no other thread reads them, waiting for
+// the thread's own copies is enough (no barrier).  A vector of B bytes lies in pieces of 16
+// (or B) bytes, each piece `nthr` threads wide, so that a warp's accesses have no conflicts.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+                     : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T, int VEC>
+struct Slot {
+    static constexpr int bytes = VEC * (int)sizeof(T);
+    static constexpr int piece = bytes < 16 ? bytes : 16;
+    static __device__ __forceinline__ void copy(char* base, int thr, int nthr, const T* src) {
+#pragma unroll
+        for (int i = 0; i < bytes / piece; ++i)
+            cp_async<piece>(base + (i * nthr + thr) * piece,
+                            reinterpret_cast<const char*>(src) + i * piece);
+    }
+    static __device__ __forceinline__ void read(const char* base, int thr, int nthr, float* f) {
+        constexpr int n = piece / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < bytes / piece; ++i) {
+            Pack<T, n> v;
+            v.load(reinterpret_cast<const T*>(base + (i * nthr + thr) * piece));
+            v.get(f + i * n);
+        }
+    }
+};
+
 // Parameters (weight, bias) are float32 or bfloat16, whatever the activations' type.
 __device__ __forceinline__ float param(const void* p, long long i, int bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
                 : static_cast<const float*>(p)[i];
+}
+// Parameters i .. i + VEC; p + i need not be aligned for a vector, which is looked at here.
+template <int VEC>
+__device__ __forceinline__ void params(const void* p, long long i, int bf16, float* f) {
+    if constexpr (VEC >= 4) {
+        if (!bf16 && ((reinterpret_cast<uintptr_t>(p) + 4 * i) & 15) == 0) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4) {
+                Pack<float, 4> v;
+                v.load(static_cast<const float*>(p) + i + e);
+                v.get(f + e);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = param(p, i + e, bf16);
 }
 __device__ __forceinline__ void set_param(void* p, long long i, float v, int bf16) {
     if (bf16)
@@ -109,16 +188,96 @@ __device__ __forceinline__ void set_param(void* p, long long i, float v, int bf1
         static_cast<float*>(p)[i] = v;
 }
 
-// sigmoid(v).  float32 tensors take expf and a correctly rounded quotient.  bfloat16
-// tensors take the hardware's approximations: their relative error (about 1e-6 at
-// |v| = 10) is far below the 2^-9 of the result's rounding, and the two MUFU operations
-// an element then costs fit under the memory time.
+// 1 / (1 + 2^(-v log2 e)).  float32 tensors take expf and a correctly rounded quotient.
+// bfloat16 tensors take the hardware's base-2 exponential and reciprocal, denormals flushed
+// (the sum with 1 drops them in any case): their relative error (about 1e-6 at |v| = 10) is far
+// below the 2^-9 of the result's rounding, and an element then costs two operations of the
+// special function unit and three of the others.  Both ends come out right: 2^inf = inf,
+// 1 / inf = 0.
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float v) {
-    if constexpr (sizeof(T) == 4)
+    if constexpr (sizeof(T) == 4) {
         return 1.f / (1.f + expf(-v));
+    } else {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return r;
+    }
+}
+
+// Two channels in one 64-bit register pair: one instruction does both, which halves the issue
+// slots of the multiply-adds.  A single channel is a plain float.
+struct F2 {
+    unsigned long long v;
+};
+template <int VEC>
+struct Lanes {
+    using V = F2;
+    static constexpr int N = VEC / 2;
+};
+template <>
+struct Lanes<1> {
+    using V = float;
+    static constexpr int N = 1;
+};
+__device__ __forceinline__ F2 join(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float* f) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f[0]), "=f"(f[1]) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma_(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul_(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add_(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ float add_(float a, float b) { return a + b; }
+template <typename V>
+__device__ __forceinline__ V both(float x);
+template <>
+__device__ __forceinline__ F2 both<F2>(float x) { return join(x, x); }
+template <>
+__device__ __forceinline__ float both<float>(float x) { return x; }
+template <int VEC>
+__device__ __forceinline__ void to_lanes(const float* f, typename Lanes<VEC>::V* v) {
+    if constexpr (VEC == 1)
+        v[0] = f[0];
     else
-        return __fdividef(1.f, 1.f + __expf(-v));
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) v[i] = join(f[2 * i], f[2 * i + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ void from_lanes(const typename Lanes<VEC>::V* v, float* f) {
+    if constexpr (VEC == 1)
+        f[0] = v[0];
+    else
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) split(v[i], f + 2 * i);
+}
+template <typename T>
+__device__ __forceinline__ F2 sigmoid_lanes(F2 v) {
+    float f[2];
+    split(v, f);
+    return join(sigmoid_of<T>(f[0]), sigmoid_of<T>(f[1]));
+}
+template <typename T>
+__device__ __forceinline__ float sigmoid_lanes(float v) {
+    return sigmoid_of<T>(v);
 }
 
 }  // namespace layer

@@ -2,9 +2,10 @@
 // float32 partial sum per weight, and this kernel adds them in a fixed order, so the
 // gradients are bit-identical from run to run (no atomics).
 //
-// A block owns 32 columns; its 32 warps take the partials in turn, then one warp adds the
-// 32 warp sums.  Bound by the latency of the loads (each warp nb / 32 of them, four in
-// flight); the bytes (nb * nk * C * 4) come from L2, where the kernel before left them.
+// A block owns 32 columns; its warps take the partials in turn, eight loads in flight each,
+// then the warp sums are added.  Bound by the latency of the loads; the bytes (nb * nk * C *
+// 4) come from L2, where the kernel before left them.  The launch itself overlaps the end of
+// that kernel; griddepcontrol.wait holds the loads back until it has finished.
 #include "layer_device.cuh"
 #include "layer_host.cuh"
 
@@ -13,40 +14,60 @@ namespace layer {
 
 namespace {
 
-constexpr int kSumWarps = 32;
-
-__global__ void __launch_bounds__(32 * kSumWarps)
-    partial_sum_kernel(const float* __restrict__ partial, int nb, int nk, long long C, ReduceDst d,
-                       int bf16) {
-    __shared__ float part[kSumWarps][33];
+template <int W>
+__global__ void __launch_bounds__(32 * W)
+    partial_sum_kernel(const float* partial, int nb, int nk, long long C, ReduceDst d, int bf16) {
+    __shared__ float part[W][32];
     const long long M = C * nk;
     const long long m = (long long)blockIdx.x * 32 + threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.f;
     if (m < M) {
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-        int y = threadIdx.y;
-        for (; y + 3 * kSumWarps < nb; y += 4 * kSumWarps)
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int y = threadIdx.y; y < nb; y += 8 * W)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] += partial[(y + i * kSumWarps) * M + m];
-        for (; y < nb; y += kSumWarps) t[0] += partial[y * M + m];
-        s = (t[0] + t[1]) + (t[2] + t[3]);
+            for (int i = 0; i < 8; ++i)
+                if (y + i * W < nb) t[i] += partial[(y + i * W) * M + m];
+        s = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
     }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y != 0 || m >= M) return;
-    for (int i = 1; i < kSumWarps; ++i) s += part[i][threadIdx.x];
-    const int k = (int)(m / C);
-    if (d.dst[k]) set_param(d.dst[k], (m - k * C) * d.step[k], s, bf16);
+#pragma unroll
+    for (int i = 1; i < W; ++i) s += part[i][threadIdx.x];
+    int k = 0;
+    long long c = m;
+    while (c >= C) c -= C, ++k;
+    if (d.dst[k]) set_param(d.dst[k], c * d.step[k], s, bf16);
+}
+
+template <int W>
+cudaError_t launch(const float* partial, int nb, int nk, long long C, const ReduceDst& d, int bf16,
+                   cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((C * nk + 31) / 32));
+    cfg.blockDim = dim3(32, W);
+    cfg.stream = stream;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, partial_sum_kernel<W>, partial, nb, nk, C, d, bf16);
 }
 
 }  // namespace
 
 cudaError_t launch_partial_sum(const float* partial, int nb, int nk, long long C,
                                const ReduceDst& d, int wdtype, Launch& L) {
+    const int bf16 = wdtype == SSD_DTYPE_BF16;
     L.begin("partial_sum");
-    partial_sum_kernel<<<(unsigned)((C * nk + 31) / 32), dim3(32, kSumWarps), 0, L.stream>>>(
-        partial, nb, nk, C, d, wdtype == SSD_DTYPE_BF16);
-    return L.end();
+    // few partials take few warps, so that a thread has its eight loads to make
+    cudaError_t e = nb <= 64    ? launch<8>(partial, nb, nk, C, d, bf16, L.stream)
+                    : nb <= 256 ? launch<16>(partial, nb, nk, C, d, bf16, L.stream)
+                                : launch<32>(partial, nb, nk, C, d, bf16, L.stream);
+    const cudaError_t last = L.end();
+    return e != cudaSuccess ? e : last;
 }
 
 }  // namespace layer

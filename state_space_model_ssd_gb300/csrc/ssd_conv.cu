@@ -23,6 +23,7 @@
 
 #include "layer_device.cuh"
 #include "layer_host.cuh"
+#include "layer_team.cuh"
 
 namespace ssd {
 namespace layer {
@@ -153,14 +154,67 @@ __device__ __forceinline__ T* piece(const ConvArgs& a, long long c, int* stride)
     return p + (c - (k == 2 ? a.off2 : k == 1 ? a.off1 : 0));
 }
 
+// The tokens of a run on their way to its thread, in groups of kGroup: through a ring in
+// shared memory (S groups, N tensors), or, in single channels (S = 0), through registers one
+// group ahead.
+constexpr int kGroup = 4;
+constexpr int ring_groups(int vec) { return vec == 1 ? 0 : 3; }
+
+template <typename T, int VEC, int S, int N>
+struct Run {
+    Pack<T, VEC> next[S ? 1 : kGroup][N];
+    const T* src[N];  // token 0 of this thread's channels
+    long long stride[N];
+    char* ring;
+    int tid;
+    static constexpr int bytes = VEC * (int)sizeof(T);
+    static constexpr int threads = kLanes * kRuns;
+    __device__ __forceinline__ char* at(int stage, int i, int k) const {
+        return ring + ((stage * kGroup + i) * N + k) * threads * bytes;
+    }
+    // tokens t .. t + kGroup, those before `end`
+    __device__ __forceinline__ void load(long long t, long long end, int stage) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            if (t + i < end)
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const T* p = src[k] + (t + i) * stride[k];
+                    if constexpr (S > 0)
+                        Slot<T, VEC>::copy(at(stage, i, k), tid, threads, p);
+                    else
+                        next[i][k].load(p);
+                }
+        if constexpr (S > 0) cp_async_commit();
+    }
+    __device__ __forceinline__ void get(int stage, int i, int k, typename Lanes<VEC>::V* v) const {
+        float f[VEC];
+        if constexpr (S > 0)
+            Slot<T, VEC>::read(at(stage, i, k), tid, threads, f);
+        else
+            next[i][k].get(f);
+        to_lanes<VEC>(f, v);
+    }
+};
+
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void token_lanes(const ConvArgs& a, const Seq& q, long long i, long long c,
+                                            typename Lanes<VEC>::V* v) {
+    float f[VEC];
+    token<T, VEC, K>(a, q, i, c, f);
+    to_lanes<VEC>(f, v);
+}
+
 // ------------------------------------------------------------------ forward
 template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(kLanes* kRuns) conv_fwd_kernel(const ConvArgs a, bool silu) {
+__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvArgs a, bool silu) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N, S = ring_groups(VEC);
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
+    extern __shared__ __align__(16) char ring[];
     const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
     const long long c0 = (long long)cb * kLanes * VEC;
     const long long c = c0 + threadIdx.x * VEC;
-    const T* __restrict__ u = static_cast<const T*>(a.u);
 
     if (rb >= a.nrunblk) {  // the states: one (sequence, row) per thread row
         const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
@@ -176,255 +230,352 @@ __global__ void __launch_bounds__(kLanes* kRuns) conv_fwd_kernel(const ConvArgs 
         return;
     }
 
-    stage_weights<VEC, K>(a, c0, ws);
     const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
     const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
-    if (c >= a.C || t0 >= t1) return;
-    float w[K][VEC], b[VEC];
+    const bool on = c < a.C && t0 < t1;
+    Run<T, VEC, S, 1> in;
+    in.src[0] = static_cast<const T*>(a.u) + c, in.stride[0] = a.us;
+    in.ring = ring, in.tid = threadIdx.y * kLanes + threadIdx.x;
+    if (on)  // on their way before the weights are looked at
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        b[e] = ws[K][threadIdx.x * VEC + e];
+        for (int s = 0; s < (S ? S : 1); ++s) in.load(t0 + s * kGroup, t1, s);
+    stage_weights<VEC, K>(a, c0, ws);
+    if (!on) return;
+    V w[K][N], b[N];
+    to_lanes<VEC>(&ws[K][threadIdx.x * VEC], b);
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][e] = ws[k][threadIdx.x * VEC + e];
-    }
+    for (int k = 0; k < K; ++k) to_lanes<VEC>(&ws[k][threadIdx.x * VEC], w[k]);
     int ostride;
     T* out = piece<T>(a, c, &ostride);
 
     Seq q = seq_of(a, t0);
-    float win[K - 1][VEC];  // win[j]: token t - 1 - j
+    V win[K - 1][N];  // win[j]: token t - 1 - j
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
+    for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
 
-    constexpr int U = VEC == 1 ? 8 : 4;  // tokens in flight
-    for (long long t = t0; t < t1; t += U) {
-        Pack<T, VEC> raw[U];
+    int stage = 0;
+    for (long long t = t0; t < t1; t += kGroup) {
+        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+        V cur[kGroup][N];
+        auto work = [&](int i) {
+            V o[N];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (t + i < t1) raw[i].load(u + (t + i) * a.us + c);
+            for (int e = 0; e < N; ++e) {
+                V v = fma_(w[K - 1][e], cur[i][e], b[e]);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (t + i >= t1) break;
-            if (t + i == q.end) {
-                q = seq_of(a, t + i);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, -1 - j, c, win[j]);
-            }
-            float cur[VEC], o[VEC];
-            raw[i].get(cur);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float v = fmaf(w[K - 1][e], cur[e], b[e]);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) v = fmaf(w[K - 2 - j][e], win[j][e], v);
-                o[e] = silu ? v * sigmoid_of<T>(v) : v;
-                if (!q.live) o[e] = 0.f;
+                for (int j = 0; j < K - 1; ++j) v = fma_(w[K - 2 - j][e], win[j][e], v);
+                o[e] = silu ? mul_(v, sigmoid_lanes<T>(v)) : v;
 #pragma unroll
                 for (int j = K - 2; j > 0; --j) win[j][e] = win[j - 1][e];
-                win[0][e] = cur[e];
+                win[0][e] = cur[i][e];
             }
-            store_vec<VEC>(out + (t + i) * ostride, o);
+            float f[VEC];
+            from_lanes<VEC>(o, f);
+            if (!q.live)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+            store_vec<VEC>(out + (t + i) * ostride, f);
+        };
+        const bool whole = t + kGroup <= t1 && t + kGroup <= q.end;  // the same for the warp
+        if constexpr (S == 0) {  // the registers are read: the next group takes them
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+                if (whole || t + i < t1) in.get(stage, i, 0, cur[i]);
+            in.load(t + kGroup, t1, stage);
         }
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                if constexpr (S > 0) in.get(stage, i, 0, cur[i]);
+                work(i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                if (t + i >= t1) break;
+                if (t + i == q.end) {
+                    q = seq_of(a, t + i);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
+                }
+                if constexpr (S > 0) in.get(stage, i, 0, cur[i]);
+                work(i);
+            }
+        }
+        // this thread's places of the stage are read: the group S rounds on takes them
+        if constexpr (S > 0) in.load(t + S * kGroup, t1, stage);
+        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
     }
 }
 
 // ------------------------------------------------------------------ backward
-// g and its ingredients at one token: pre from the current token and its window.
+// g at one token: pre from the current token and its window.
 template <typename T, int VEC, int K>
-__device__ __forceinline__ void grad_pre(const float (*w)[VEC], const float* b, const float* cur,
-                                         const float (*win)[VEC], const float* dy, bool silu,
-                                         float* g) {
+__device__ __forceinline__ void grad_pre(const typename Lanes<VEC>::V (*w)[Lanes<VEC>::N],
+                                         const typename Lanes<VEC>::V* b,
+                                         const typename Lanes<VEC>::V* cur,
+                                         const typename Lanes<VEC>::V (*win)[Lanes<VEC>::N],
+                                         const typename Lanes<VEC>::V* dy, bool silu,
+                                         typename Lanes<VEC>::V* g) {
+    using V = typename Lanes<VEC>::V;
+    const V one = both<V>(1.f), minus = both<V>(-1.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int e = 0; e < Lanes<VEC>::N; ++e) {
         if (!silu) {
             g[e] = dy[e];
             continue;
         }
-        float v = fmaf(w[K - 1][e], cur[e], b[e]);
+        V v = fma_(w[K - 1][e], cur[e], b[e]);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) v = fmaf(w[K - 2 - j][e], win[j][e], v);
-        const float s = sigmoid_of<T>(v);
-        g[e] = dy[e] * (s * fmaf(v, 1.f - s, 1.f));
+        for (int j = 0; j < K - 1; ++j) v = fma_(w[K - 2 - j][e], win[j][e], v);
+        const V s = sigmoid_lanes<T>(v);
+        g[e] = mul_(mul_(dy[e], s), fma_(v, fma_(s, minus, one), one));
     }
 }
 
 // The carried state's gradient, row r of sequence q: from the first tokens that read the
 // row's position p0 - m, and passed through where the row is still in the final state.
 template <typename T, int VEC, int K>
-__device__ __forceinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, long long c,
-                                           const float (*w)[VEC], const float* b, bool silu) {
+__device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, long long c,
+                                        const float (*ws)[kLanes * VEC], bool silu) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
+    V w[K][N], b[N];
+    to_lanes<VEC>(&ws[K][threadIdx.x * VEC], b);
+#pragma unroll
+    for (int k = 0; k < K; ++k) to_lanes<VEC>(&ws[k][threadIdx.x * VEC], w[k]);
     const long long p0 = a.pos ? a.pos[q.s] : 0;
     const long long n = q.end - q.start;
     int m = state_row<K>(p0 - r);
     if (m == 0) m = K;
     const long long at = ((long long)q.s * K + r) * a.C + c;
-    float d[VEC];
+    float f[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+    for (int e = 0; e < VEC; ++e) f[e] = 0.f;
     if (a.dfinal && m + n <= K) {
         Pack<T, VEC> v;
         v.load(static_cast<const T*>(a.dfinal) + at);
-        v.get(d);
+        v.get(f);
     }
+    V d[N];
+    to_lanes<VEC>(f, d);
     int dstride;
     const T* dout = piece<T>(a, c, &dstride);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         if (i >= n || i + m >= K) break;
-        float cur[VEC], win[K - 1][VEC], dy[VEC], g[VEC];
-        token<T, VEC, K>(a, q, i, c, cur);
+        V cur[N], win[K - 1][N], dy[N], g[N];
+        token_lanes<T, VEC, K>(a, q, i, c, cur);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, i - 1 - j, c, win[j]);
+        for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, i - 1 - j, c, win[j]);
         Pack<T, VEC> v;
         v.load(dout + (q.start + i) * dstride);
-        v.get(dy);
+        v.get(f);
+        to_lanes<VEC>(f, dy);
         grad_pre<T, VEC, K>(w, b, cur, win, dy, silu, g);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (k == K - 1 - (i + m))
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) d[e] = fmaf(w[k][e], g[e], d[e]);
+                for (int e = 0; e < N; ++e) d[e] = fma_(w[k][e], g[e], d[e]);
     }
-    store_vec<VEC>(static_cast<T*>(a.dinit) + at, d);
+    from_lanes<VEC>(d, f);
+    store_vec<VEC>(static_cast<T*>(a.dinit) + at, f);
 }
 
 template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(kLanes* kRuns) conv_bwd_kernel(const ConvArgs a, bool silu) {
+__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvArgs a, bool silu) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N, S = ring_groups(VEC);
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
-    __shared__ float red[kRuns][K + 1][kLanes * VEC];
+    extern __shared__ __align__(16) char ring[];
     const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
     const long long c0 = (long long)cb * kLanes * VEC;
     const long long c = c0 + threadIdx.x * VEC;
-    const T* __restrict__ u = static_cast<const T*>(a.u);
 
-    stage_weights<VEC, K>(a, c0, ws);
-    float w[K][VEC], b[VEC];
-    if (c < a.C) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            b[e] = ws[K][threadIdx.x * VEC + e];
-#pragma unroll
-            for (int k = 0; k < K; ++k) w[k][e] = ws[k][threadIdx.x * VEC + e];
-        }
-    }
     if (rb >= a.nrunblk) {  // the carried states' gradients
+        stage_weights<VEC, K>(a, c0, ws);
         const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
         if (c < a.C && item < (long long)a.nseq * K)
-            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, w, b, silu);
+            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, ws, silu);
         return;
     }
 
     const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
     const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
-    float dw[K + 1][VEC];
+    // g of the K-1 tokens after the run reaches back into it
+    const long long t2 = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;
+    const bool on = c < a.C && t0 < t1;
+    Run<T, VEC, S, 2> in;
+    in.ring = ring, in.tid = threadIdx.y * kLanes + threadIdx.x;
+    if (on) {
+        int dstride;
+        in.src[0] = static_cast<const T*>(a.u) + c, in.stride[0] = a.us;
+        in.src[1] = piece<T>(a, c, &dstride), in.stride[1] = dstride;
+#pragma unroll
+        for (int s = 0; s < (S ? S : 1); ++s) in.load(t0 + s * kGroup, t2, s);
+    }
+    stage_weights<VEC, K>(a, c0, ws);
+    V dw[K + 1][N];
 #pragma unroll
     for (int k = 0; k <= K; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
+        for (int e = 0; e < N; ++e) dw[k][e] = both<V>(0.f);
 
-    if (c < a.C && t0 < t1) {
-        int dstride;
-        const T* __restrict__ dout = piece<T>(a, c, &dstride);
-        T* du = static_cast<T*>(a.du);
-        // g of the K-1 tokens after the run reaches back into it
-        const long long t2 = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;
-        Seq q = seq_of(a, t0);
-        float win[K - 1][VEC];  // win[j]: token t - 1 - j
-        float acc[K][VEC];      // acc[j]: du of token t - j so far
+    if (on) {
+        V w[K][N], b[N];
+        to_lanes<VEC>(&ws[K][threadIdx.x * VEC], b);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
+        for (int k = 0; k < K; ++k) to_lanes<VEC>(&ws[k][threadIdx.x * VEC], w[k]);
+        T* du = static_cast<T*>(a.du) + c;
+        Seq q = seq_of(a, t0);
+        V win[K - 1][N];  // win[j]: token t - 1 - j
+        V acc[K][N];      // acc[j]: du of token t - j so far
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+            for (int e = 0; e < N; ++e) acc[j][e] = both<V>(0.f);
 
-        constexpr int U = VEC == 1 ? 4 : 2;  // tokens in flight
-        for (long long t = t0; t < t2; t += U) {
-            Pack<T, VEC> ru[U], rd[U];
+        int stage = 0;
+        for (long long t = t0; t < t2; t += kGroup) {
+            if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+            V cur[kGroup][N], dy[kGroup][N], g[N];
+            auto sums = [&](int i) {
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (t + i < t2) {
-                    ru[i].load(u + (t + i) * a.us + c);
-                    rd[i].load(dout + (t + i) * dstride);
+                for (int e = 0; e < N; ++e) {
+                    dw[K][e] = add_(dw[K][e], g[e]);
+                    dw[K - 1][e] = fma_(g[e], cur[i][e], dw[K - 1][e]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j)
+                        dw[K - 2 - j][e] = fma_(g[e], win[j][e], dw[K - 2 - j][e]);
                 }
+            };
+            auto shift = [&](int i) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const long long tt = t + i;
-                if (tt >= t2) break;
-                if (tt == q.end) {
-                    q = seq_of(a, tt);
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) token<T, VEC, K>(a, q, -1 - j, c, win[j]);
-                }
-                float cur[VEC], dy[VEC], g[VEC];
-                ru[i].get(cur);
-                rd[i].get(dy);
-                grad_pre<T, VEC, K>(w, b, cur, win, dy, silu, g);
-                if (!q.live)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[e] = 0.f;
-                if (tt < t1 && q.live) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        dw[K][e] += g[e];
-                        dw[K - 1][e] = fmaf(g[e], cur[e], dw[K - 1][e]);
-#pragma unroll
-                        for (int j = 0; j < K - 1; ++j)
-                            dw[K - 2 - j][e] = fmaf(g[e], win[j][e], dw[K - 2 - j][e]);
-                    }
-                }
-                // shift: acc[j] becomes token tt - j; token tt starts from the final state's
-                // gradient where it is still in the window there
-#pragma unroll
-                for (int j = K - 1; j > 0; --j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[j][e] = acc[j - 1][e];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[0][e] = 0.f;
-                if (a.dfinal && q.live && q.end - tt <= K) {
-                    const long long p = (a.pos ? a.pos[q.s] : 0) + (tt - q.start);
-                    Pack<T, VEC> v;
-                    v.load(static_cast<const T*>(a.dfinal) +
-                           ((long long)q.s * K + state_row<K>(p)) * a.C + c);
-                    v.get(acc[0]);
-                }
-#pragma unroll
-                for (int j = 0; j < K; ++j)
-                    if (tt - j >= q.start)  // a token of an earlier sequence gets nothing
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            acc[j][e] = fmaf(w[K - 1 - j][e], g[e], acc[j][e]);
-                if (tt - (K - 1) >= t0) store_vec<VEC>(du + (tt - (K - 1)) * a.dus + c, acc[K - 1]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
+                for (int e = 0; e < N; ++e) {
 #pragma unroll
                     for (int j = K - 2; j > 0; --j) win[j][e] = win[j - 1][e];
-                    win[0][e] = cur[e];
+                    win[0][e] = cur[i][e];
+                }
+            };
+            auto emit = [&](long long tok, const V* v) {
+                float f[VEC];
+                from_lanes<VEC>(v, f);
+                store_vec<VEC>(du + tok * a.dus, f);
+            };
+            // a whole group inside the run, and no end or beginning of a sequence in reach;
+            // the same for the warp
+            const bool whole = t >= t0 + K - 1 && t + kGroup <= t1 && q.live &&
+                               t >= q.start + K - 1 && t + kGroup + K <= q.end;
+            auto read = [&](int i) {
+                in.get(stage, i, 0, cur[i]);
+                in.get(stage, i, 1, dy[i]);
+            };
+            if constexpr (S == 0) {  // the registers are read: the next group takes them
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i)
+                    if (whole || t + i < t2) read(i);
+                in.load(t + kGroup, t2, stage);
+            }
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    if constexpr (S > 0) read(i);
+                    grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
+                    sums(i);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+#pragma unroll
+                        for (int j = K - 1; j > 0; --j)
+                            acc[j][e] = fma_(w[K - 1 - j][e], g[e], acc[j - 1][e]);
+                        acc[0][e] = mul_(w[K - 1][e], g[e]);
+                    }
+                    emit(t + i - (K - 1), acc[K - 1]);
+                    shift(i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    const long long tt = t + i;
+                    if (tt >= t2) break;
+                    if (tt == q.end) {
+                        q = seq_of(a, tt);
+#pragma unroll
+                        for (int j = 0; j < K - 1; ++j)
+                            token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
+                    }
+                    if constexpr (S > 0) read(i);
+                    grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
+                    if (!q.live)
+#pragma unroll
+                        for (int e = 0; e < N; ++e) g[e] = both<V>(0.f);
+                    if (tt < t1 && q.live) sums(i);
+                    // acc[j] becomes token tt - j; token tt starts from the final state's
+                    // gradient where it is still in the window there
+                    float f[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+                    if (a.dfinal && q.live && q.end - tt <= K) {
+                        const long long p = (a.pos ? a.pos[q.s] : 0) + (tt - q.start);
+                        Pack<T, VEC> v;
+                        v.load(static_cast<const T*>(a.dfinal) +
+                               ((long long)q.s * K + state_row<K>(p)) * a.C + c);
+                        v.get(f);
+                    }
+#pragma unroll
+                    for (int j = K - 1; j > 0; --j)
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[j][e] = acc[j - 1][e];
+                    to_lanes<VEC>(f, acc[0]);
+#pragma unroll
+                    for (int j = 0; j < K; ++j)
+                        if (tt - j >= q.start)  // a token of an earlier sequence gets nothing
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                acc[j][e] = fma_(w[K - 1 - j][e], g[e], acc[j][e]);
+                    if (tt - (K - 1) >= t0) emit(tt - (K - 1), acc[K - 1]);
+                    shift(i);
                 }
             }
+            // this thread's places of the stage are read: the group S rounds on takes them
+            if constexpr (S > 0) in.load(t + S * kGroup, t2, stage);
+            if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
         }
         // the last tokens of the run that nothing later reads
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             const long long tok = t2 - 1 - j;
-            if (tok >= t0 && tok < t1) store_vec<VEC>(du + tok * a.dus + c, acc[j]);
+            if (tok >= t0 && tok < t1) {
+                float f[VEC];
+                from_lanes<VEC>(acc[j], f);
+                store_vec<VEC>(du + tok * a.dus, f);
+            }
         }
     }
 
-    // one partial per block, weight and channel: the runs are added in order
-#pragma unroll
-    for (int k = 0; k <= K; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) red[threadIdx.y][k][e * kLanes + threadIdx.x] = dw[k][e];
+    // one partial per block, weight and channel: the runs are added in order, in the ring's place
+    if constexpr (S > 0) cp_async_wait<0>();
+    float* red = reinterpret_cast<float*>(ring);
     __syncthreads();
-    const int tid = threadIdx.y * kLanes + threadIdx.x;
-    for (int i = tid; i < (K + 1) * kLanes * VEC; i += kLanes * kRuns) {
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+        float f[VEC];
+        from_lanes<VEC>(dw[k], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            red[((threadIdx.y * (K + 1) + k) * VEC + e) * kLanes + threadIdx.x] = f[e];
+    }
+    __syncthreads();
+    for (int i = in.tid; i < (K + 1) * kLanes * VEC; i += kLanes * kRuns) {
         const int k = i / (kLanes * VEC), x = i - k * kLanes * VEC;
         const long long ch = c0 + x;
         if (ch >= a.C) continue;
-        const int at = (x % VEC) * kLanes + x / VEC;
+        const int at = (k * VEC + x % VEC) * kLanes + x / VEC;
         float s = 0.f;
 #pragma unroll
-        for (int y = 0; y < kRuns; ++y) s += red[y][k][at];
+        for (int y = 0; y < kRuns; ++y) s += red[y * (K + 1) * VEC * kLanes + at];
         a.partial[((long long)rb * (K + 1) + k) * a.C + ch] = s;
     }
 }
@@ -461,15 +612,21 @@ ssd_status_t check_conv(const ssd_conv_t* p, Conv* c) {
     return SSD_OK;
 }
 
-// Whether every row of every tensor starts on a vector of n elements (n * e bytes).
-bool fits(const ssd_conv_t* p, const Conv& c, int n, const void* const* ptrs, int np) {
-    for (int i = 0; i < 3; ++i)
-        if (p->split[i] % n) return false;
-    if (p->u_stride % n || p->du_stride % n) return false;
-    for (int i = 0; i < np; ++i)
-        if (!aligned_to(ptrs[i], n * c.e)) return false;
-    return true;
+// Channels of a vector: 16 bytes (8 in a bf16 backward, whose sums take the registers) where
+// every row of every tensor and every piece starts on such a boundary, else a half of it, a
+// quarter, ... down to one channel.
+int conv_vec(const ssd_conv_t* p, const Conv& c, int most, const void* const* ptrs, int np) {
+    const long long strides[5] = {p->split[0], p->split[1], p->split[2], p->u_stride, p->du_stride};
+    for (int vec = most; vec > 1; vec >>= 1) {
+        bool ok = true;
+        for (long long s : strides) ok = ok && s % vec == 0;
+        for (int i = 0; i < np; ++i) ok = ok && aligned_to(ptrs[i], vec * c.e);
+        if (ok) return vec;
+    }
+    return 1;
 }
+int most_fwd(const Conv& c) { return c.e == 2 ? 8 : 4; }
+constexpr int kMostBwd = 4;
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -505,25 +662,40 @@ void fill_args(const ssd_conv_t* p, const Conv& c, ConvArgs* a) {
     a->wbf16 = p->wdtype == SSD_DTYPE_BF16;
 }
 
-template <typename T, int VEC>
-void launch_fwd(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
-    const dim3 blk(kLanes, kRuns);
-    if (K == 2)
-        conv_fwd_kernel<T, VEC, 2><<<grid, blk, 0, s>>>(a, silu);
-    else if (K == 3)
-        conv_fwd_kernel<T, VEC, 3><<<grid, blk, 0, s>>>(a, silu);
-    else
-        conv_fwd_kernel<T, VEC, 4><<<grid, blk, 0, s>>>(a, silu);
+// Shared memory of a block: the ring, or in the backward the runs' sums at the end.
+template <typename T, int VEC, int K>
+constexpr size_t conv_smem(bool bwd) {
+    const size_t ring = (size_t)ring_groups(VEC) * kGroup * kLanes * kRuns * VEC * sizeof(T) * (bwd ? 2 : 1);
+    const size_t sums = bwd ? sizeof(float) * kRuns * (K + 1) * VEC * kLanes : 0;
+    return ring > sums ? ring : sums;
 }
-template <typename T, int VEC>
-void launch_bwd(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
-    const dim3 blk(kLanes, kRuns);
-    if (K == 2)
-        conv_bwd_kernel<T, VEC, 2><<<grid, blk, 0, s>>>(a, silu);
-    else if (K == 3)
-        conv_bwd_kernel<T, VEC, 3><<<grid, blk, 0, s>>>(a, silu);
-    else
-        conv_bwd_kernel<T, VEC, 4><<<grid, blk, 0, s>>>(a, silu);
+template <bool BWD, typename T, int VEC, int K>
+cudaError_t launch_k(unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+    constexpr auto kernel = BWD ? &conv_bwd_kernel<T, BWD ? VEC : 1, K> : &conv_fwd_kernel<T, BWD ? 1 : VEC, K>;
+    constexpr size_t smem = conv_smem<T, VEC, K>(BWD);
+    const cudaError_t e = allow_smem<kernel>(smem);
+    if (e == cudaSuccess) kernel<<<grid, dim3(kLanes, kRuns), smem, s>>>(a, silu);
+    return e;
+}
+template <bool BWD, typename T, int VEC>
+cudaError_t launch_vec(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+    if (K == 2) return launch_k<BWD, T, VEC, 2>(grid, a, silu, s);
+    if (K == 3) return launch_k<BWD, T, VEC, 3>(grid, a, silu, s);
+    return launch_k<BWD, T, VEC, 4>(grid, a, silu, s);
+}
+template <bool BWD, typename T>
+cudaError_t launch_type(int vec, int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2 && !BWD)
+        if (vec == 8) return launch_vec<BWD, T, 8>(K, grid, a, silu, s);
+    if (vec == 4) return launch_vec<BWD, T, 4>(K, grid, a, silu, s);
+    if (vec == 2) return launch_vec<BWD, T, 2>(K, grid, a, silu, s);
+    return launch_vec<BWD, T, 1>(K, grid, a, silu, s);
+}
+template <bool BWD>
+cudaError_t launch_conv(const ssd_conv_t* p, int vec, unsigned grid, const ConvArgs& a, cudaStream_t s) {
+    const bool silu = p->activation == 1;
+    return p->dtype == SSD_DTYPE_BF16 ? launch_type<BWD, __nv_bfloat16>(vec, p->width, grid, a, silu, s)
+                                      : launch_type<BWD, float>(vec, p->width, grid, a, silu, s);
 }
 
 }  // namespace
@@ -575,9 +747,8 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
     a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
     a.init = initial_state, a.final_state = final_state;
     for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
-    const int vec = conv->dtype == SSD_DTYPE_BF16 ? 8 : 4;
-    const bool wide = fits(conv, c, vec, ptrs, 6);
-    const long long nvec = wide ? c.C / vec : c.C;
+    const int vec = conv_vec(conv, c, most_fwd(c), ptrs, 6);
+    const long long nvec = c.C / vec;
     a.run = choose_run(c.T, nvec, 32, 1024);
     a.nchblk = ceil_div(nvec, kLanes);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
@@ -587,19 +758,9 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("conv_fwd");
-    const bool silu = conv->activation == 1;
-    if (conv->dtype == SSD_DTYPE_BF16) {
-        if (wide)
-            launch_fwd<__nv_bfloat16, 8>(conv->width, (unsigned)grid, a, silu, L.stream);
-        else
-            launch_fwd<__nv_bfloat16, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
-    } else {
-        if (wide)
-            launch_fwd<float, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
-        else
-            launch_fwd<float, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
-    }
-    const cudaError_t e = L.end();
+    cudaError_t e = launch_conv<false>(conv, vec, (unsigned)grid, a, L.stream);
+    const cudaError_t last = L.end();
+    if (e == cudaSuccess) e = last;
     set_last_launches(L.count);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -610,8 +771,7 @@ ssd_status_t ssd_conv_workspace_size(const ssd_conv_t* conv, size_t* bytes) {
     ssd_status_t st = check_conv(conv, &c);
     if (st != SSD_OK) return st;
     size_t most = 0;
-    const int vecs[2] = {4, 1};  // either path may run, by the pointers' alignment
-    for (int vec : vecs) {
+    for (int vec = kMostBwd; vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
         const int nb = ceil_div(c.T, (long long)bwd_run(c.T, c.C, vec) * kRuns);
         const size_t n = sizeof(float) * (size_t)nb * (conv->width + 1) * c.C;
         if (n > most) most = n;
@@ -670,9 +830,9 @@ ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void
     a.init = initial_state, a.dfinal = d_final_state, a.du = du, a.dinit = d_initial_state;
     for (int i = 0; i < 3; ++i) a.out[i] = const_cast<void*>(douts[i]);
     a.partial = static_cast<float*>(workspace);
-    const bool wide = fits(conv, c, 4, ptrs, 8);
-    const long long nvec = wide ? c.C / 4 : c.C;
-    a.run = bwd_run(c.T, c.C, wide ? 4 : 1);
+    const int vec = conv_vec(conv, c, kMostBwd, ptrs, 8);
+    const long long nvec = c.C / vec;
+    a.run = bwd_run(c.T, c.C, vec);
     a.nchblk = ceil_div(nvec, kLanes);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = d_initial_state ? ceil_div(srows, kRuns) : 0;
@@ -683,19 +843,9 @@ ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void
     cudaError_t e = cudaSuccess;
     if (grid > 0) {
         L.begin("conv_bwd");
-        const bool silu = conv->activation == 1;
-        if (conv->dtype == SSD_DTYPE_BF16) {
-            if (wide)
-                launch_bwd<__nv_bfloat16, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
-            else
-                launch_bwd<__nv_bfloat16, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
-        } else {
-            if (wide)
-                launch_bwd<float, 4>(conv->width, (unsigned)grid, a, silu, L.stream);
-            else
-                launch_bwd<float, 1>(conv->width, (unsigned)grid, a, silu, L.stream);
-        }
-        e = L.end();
+        e = launch_conv<true>(conv, vec, (unsigned)grid, a, L.stream);
+        const cudaError_t last = L.end();
+        if (e == cudaSuccess) e = last;
     }
     if (e == cudaSuccess) {
         ReduceDst d = {};

@@ -44,8 +44,23 @@ struct StepArgs {
     float delta_init;
 };
 
+// The taps of channel c.
+template <int K>
+__device__ __forceinline__ void taps(const StepArgs& a, long long c, float* w) {
+    if constexpr (K == 4) {
+        if (!a.wbf16 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {
+            Pack<float, 4> v;
+            v.load(static_cast<const float*>(a.w) + c * K);
+            v.get(w);
+            return;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = param(a.w, c * K + k, a.wbf16);
+}
+
 template <typename T, int K>
-__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepArgs a) {
     __shared__ float xs[128], bs[128], cs[128];
     const int row = blockIdx.y;
     const int h = blockIdx.x / a.split, part = blockIdx.x - h * a.split;
@@ -85,11 +100,13 @@ __global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const StepArgs 
                             : j < a.N    ? (long long)a.H * a.P + g * a.N + j
                                          : (long long)a.H * a.P + (a.G + g) * a.N + (j - a.N);
         const T tok = u[c];
-        float v = param(a.w, c * K + K - 1, a.wbf16) * static_cast<float>(tok);
+        float w[K];
+        taps<K>(a, c, w);
+        float v = w[K - 1] * static_cast<float>(tok);
         if (a.b) v += param(a.b, c, a.wbf16);
 #pragma unroll
         for (int k = 1; k < K; ++k)
-            v = fmaf(param(a.w, c * K + K - 1 - k, a.wbf16), static_cast<float>(win[at[k] * a.C + c]), v);
+            v = fmaf(w[K - 1 - k], static_cast<float>(win[at[k] * a.C + c]), v);
         if (j < 0 || owns_bc) win[at[0] * a.C + c] = tok;
         v *= sigmoid_of<float>(v);
         if (j < 0)

@@ -39,74 +39,113 @@ struct GatedArgs {
     float eps;
 };
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) gated_fwd_kernel(const GatedArgs a) {
-    __shared__ float buf[32];
-    const Team t = team_of(a.nw);
-    const int g = blockIdx.x % a.G;
-    const long long row = (long long)(blockIdx.x / a.G) * a.teams + t.id;
-    const bool in = row < a.rows;
-    const int g0 = g * a.n;
-    float v[NV][VEC];
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-        if (in && c < a.n) {
-            Pack<T, VEC> py, pz;
-            py.load(static_cast<const T*>(a.y) + row * a.ys + g0 + c);
-            pz.load(static_cast<const T*>(a.z) + row * a.zs + g0 + c);
-            float z[VEC];
-            py.get(v[i]);
-            pz.get(z);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] *= z[e] * sigmoid_of<T>(z[e]);
-                q = fmaf(v[i][e], v[i][e], q);
-            }
-        }
+// The N tensors of one row, thread by thread, on their way: through the ring (S stages) or, in
+// single elements (S = 0), through registers one row ahead.
+template <typename T, int VEC, int NV, int S, int N>
+struct Rows {
+    Pack<T, VEC> next[S ? 1 : NV][N];
+    const T* src[N];         // this thread's first element of row 0
+    long long stride[N];
+    char* ring;
+    int thr, nthr;
+    static constexpr int bytes = VEC * (int)sizeof(T);
+    __device__ __forceinline__ char* at(int stage, int i, int k) const {
+        return ring + ((size_t)(stage * NV + i) * N + k) * nthr * bytes;
     }
-    team_sum<1>(t, &q, buf);
-    const float rstd = 1.f / sqrtf(q / a.n + a.eps);
-    if (!in) return;
-    if (t.thread == 0 && a.rstd) a.rstd[row * a.G + g] = rstd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c >= a.n) continue;
-        float o[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = v[i][e] * rstd * param(a.w, g0 + c + e, a.wbf16);
-        store_vec<VEC>(static_cast<T*>(a.out) + row * a.os + g0 + c, o);
-    }
-}
-
-template <typename T, int VEC, int NV>
-struct GatedRow {
-    Pack<T, VEC> d[NV], y[NV], z[NV];
-    float rstd;
-    __device__ __forceinline__ void load(const GatedArgs& a, const Team& t, int g, long long row) {
-        rstd = row < a.rows ? a.rstd_in[row * a.G + g] : 0.f;
+    __device__ __forceinline__ void load(const GatedArgs& a, const Team& t, long long row, int stage) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (row < a.rows && c < a.n) {
-                d[i].load(static_cast<const T*>(a.dout) + row * a.os + g * a.n + c);
-                y[i].load(static_cast<const T*>(a.y) + row * a.ys + g * a.n + c);
-                z[i].load(static_cast<const T*>(a.z) + row * a.zs + g * a.n + c);
-            } else {
-                d[i].zero(), y[i].zero(), z[i].zero();
-            }
+            if (row < a.rows && c < a.n)
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const T* p = src[k] + row * stride[k] + c;
+                    if constexpr (S > 0)
+                        Slot<T, VEC>::copy(at(stage, i, k), thr, nthr, p);
+                    else
+                        next[i][k].load(p);
+                }
         }
+        if constexpr (S > 0) cp_async_commit();
+    }
+    __device__ __forceinline__ void get(int stage, int i, int k, float* f) const {
+        if constexpr (S > 0)
+            Slot<T, VEC>::read(at(stage, i, k), thr, nthr, f);
+        else
+            next[i][k].get(f);
     }
 };
 
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) gated_bwd_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(team_threads(VEC)) gated_fwd_kernel(const GatedArgs a) {
+    constexpr int S = ring_stages(VEC, NV);
     __shared__ float buf[2][32];
-    extern __shared__ float acc[];  // several teams: their sums, joined at the end
+    extern __shared__ __align__(16) char ring[];
+    const Team t = team_of(a.nw);
+    const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
+    const int g0 = g * a.n;
+    float w[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t.thread + i * a.nw * 32) * VEC;
+        if (c < a.n) params<VEC>(a.w, g0 + c, a.wbf16, w[i]);
+    }
+    const long long step = (long long)a.nrb * a.teams;
+    long long row = (long long)rb * a.teams + t.id;
+    Rows<T, VEC, NV, S, 2> in;
+    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
+    in.src[0] = static_cast<const T*>(a.y) + g0, in.stride[0] = a.ys;
+    in.src[1] = static_cast<const T*>(a.z) + g0, in.stride[1] = a.zs;
+#pragma unroll
+    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
+    int stage = 0, flip = 0;
+    // every team of the block takes the same number of rows (some of them beyond the last)
+    for (long long first = (long long)rb * a.teams; first < a.rows; first += step) {
+        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+        const bool on = row < a.rows;
+        float v[NV][VEC];
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (on && c < a.n) {
+                float z[VEC];
+                in.get(stage, i, 0, v[i]);
+                in.get(stage, i, 1, z);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    v[i][e] *= z[e] * sigmoid_of<T>(z[e]);
+                    q = fmaf(v[i][e], v[i][e], q);
+                }
+            }
+        }
+        // this thread's places of the stage are read: the row S rounds on takes them
+        in.load(a, t, row + (S ? S : 1) * step, stage);
+        team_sum<1>(t, &q, buf[flip]);
+        flip ^= 1;
+        const float rstd = 1.f / sqrtf(q / a.n + a.eps);
+        if (on) {
+            if (t.thread == 0 && a.rstd) a.rstd[row * a.G + g] = rstd;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t.thread + i * a.nw * 32) * VEC;
+                if (c >= a.n) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = v[i][e] * rstd * w[i][e];
+                store_vec<VEC>(static_cast<T*>(a.out) + row * a.os + g0 + c, o);
+            }
+        }
+        row += step;
+        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+    }
+}
+
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(team_threads(VEC)) gated_bwd_kernel(const GatedArgs a) {
+    constexpr int S = ring_stages(VEC, NV);
+    __shared__ float buf[2][32];
+    extern __shared__ __align__(16) char ring[];
     const Team t = team_of(a.nw);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
@@ -114,62 +153,79 @@ __global__ void __launch_bounds__(team_threads(VEC)) gated_bwd_kernel(const Gate
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t.thread + i * a.nw * 32) * VEC;
+        if (c < a.n) params<VEC>(a.w, g0 + c, a.wbf16, w[i]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[i][e] = c < a.n ? param(a.w, g0 + c + e, a.wbf16) : 0.f;
-            dw[i][e] = 0.f;
-        }
+        for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
     }
     const long long step = (long long)a.nrb * a.teams;
-    GatedRow<T, VEC, NV> cur, next;
     long long row = (long long)rb * a.teams + t.id;
-    next.load(a, t, g, row);
-    int flip = 0;
+    Rows<T, VEC, NV, S, 3> in;
+    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
+    in.src[0] = static_cast<const T*>(a.dout) + g0, in.stride[0] = a.os;
+    in.src[1] = static_cast<const T*>(a.y) + g0, in.stride[1] = a.ys;
+    in.src[2] = static_cast<const T*>(a.z) + g0, in.stride[2] = a.zs;
+#pragma unroll
+    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
+    float next = row < a.rows ? a.rstd_in[row * a.G + g] : 0.f;
+    int stage = 0, flip = 0;
+    // every team of the block takes the same number of rows (some of them beyond the last)
     for (long long first = (long long)rb * a.teams; first < a.rows; first += step) {
-        cur = next;
-        next.load(a, t, g, row + step);
-        float d[NV][VEC], xh[NV][VEC];
+        const float rstd = next;
+        next = row + step < a.rows ? a.rstd_in[(row + step) * a.G + g] : 0.f;
+        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+        const bool on = row < a.rows;
+        // d = w dout, gate = silu(z), gy = y silu'(z)
+        float d[NV][VEC], xh[NV][VEC], gate[NV][VEC], gy[NV][VEC];
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float y[VEC], z[VEC];
-            cur.d[i].get(d[i]);
-            cur.y[i].get(y);
-            cur.z[i].get(z);
+            const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (on && c < a.n) {
+                float y[VEC], z[VEC];
+                in.get(stage, i, 0, d[i]);
+                in.get(stage, i, 1, y);
+                in.get(stage, i, 2, z);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                xh[i][e] = y[e] * (z[e] * sigmoid_of<T>(z[e])) * cur.rstd;
-                dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
-                d[i][e] *= w[i][e];
-                sum = fmaf(d[i][e], xh[i][e], sum);
+                for (int e = 0; e < VEC; ++e) {
+                    const float s = sigmoid_of<T>(z[e]);
+                    gate[i][e] = z[e] * s;
+                    gy[i][e] = y[e] * fmaf(gate[i][e], 1.f - s, s);
+                    xh[i][e] = y[e] * gate[i][e] * rstd;
+                    dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
+                    d[i][e] *= w[i][e];
+                    sum = fmaf(d[i][e], xh[i][e], sum);
+                }
             }
         }
+        // this thread's places of the stage are read: the row S rounds on takes them
+        in.load(a, t, row + (S ? S : 1) * step, stage);
         team_sum<1>(t, &sum, buf[flip]);
         flip ^= 1;
         const float c2 = sum / a.n;
-        if (row < a.rows) {
+        if (on) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (t.thread + i * a.nw * 32) * VEC;
                 if (c >= a.n) continue;
-                float y[VEC], z[VEC], oy[VEC], oz[VEC];
-                cur.y[i].get(y);
-                cur.z[i].get(z);
+                float oy[VEC], oz[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float s = sigmoid_of<T>(z[e]);
-                    const float dv = (d[i][e] - xh[i][e] * c2) * cur.rstd;
-                    oy[e] = dv * (z[e] * s);
-                    oz[e] = dv * y[e] * (s * fmaf(z[e], 1.f - s, 1.f));
+                    const float dv = (d[i][e] - xh[i][e] * c2) * rstd;
+                    oy[e] = dv * gate[i][e];
+                    oz[e] = dv * gy[i][e];
                 }
                 store_vec<VEC>(static_cast<T*>(a.dy) + row * a.dys + g0 + c, oy);
                 store_vec<VEC>(static_cast<T*>(a.dz) + row * a.dzs + g0 + c, oz);
             }
         }
         row += step;
+        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
     }
     float* part = a.partial + (long long)rb * a.D + g0;
-    if (a.teams > 1) {
+    if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
+        if constexpr (S > 0) cp_async_wait<0>();
+        float* acc = reinterpret_cast<float*>(ring);
+        __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
             if (t.id == k)
 #pragma unroll
@@ -205,48 +261,57 @@ ssd_status_t check_gated(const ssd_gated_norm_t* p) {
     return SSD_OK;
 }
 
-int gated_vec(const ssd_gated_norm_t* p, const void* const* ptrs, int np) {
-    const int vec = p->dtype == SSD_DTYPE_BF16 ? 8 : 4;
-    if ((p->dim / p->groups) % vec || p->y_stride % vec || p->z_stride % vec ||
-        p->out_stride % vec || p->dy_stride % vec || p->dz_stride % vec)
-        return 1;
-    for (int i = 0; i < np; ++i)
-        if (!aligned_to(ptrs[i], 16)) return 1;
-    return vec;
-}
+constexpr int kFwdRegs[2] = {32, 4}, kBwdRegs[2] = {40, 7};
+int most_vec(const ssd_gated_norm_t* p) { return p->dtype == SSD_DTYPE_BF16 ? 8 : 4; }
 
-// Blocks of one group in the backward.
+// Blocks of one group.
 int gated_blocks(long long rows, int groups, const RowPlan& p) {
-    const int per_sm = 1024 / (p.nw * p.teams * 32);
-    long long most = ((long long)sm_count() * (per_sm < 1 ? 1 : per_sm) + groups - 1) / groups;
+    const long long most = ((long long)sm_count() * p.per_sm + groups - 1) / groups;
     const long long want = (rows + p.teams - 1) / p.teams;
     return (int)(want < most ? want : most);
 }
 
-template <typename T, int VEC>
-void launch_fwd(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
-    const int threads = p.nw * p.teams * 32;
-    if (p.nv == 1)
-        gated_fwd_kernel<T, VEC, 1><<<grid, threads, 0, s>>>(a);
-    else if (p.nv == 2)
-        gated_fwd_kernel<T, VEC, 2><<<grid, threads, 0, s>>>(a);
-    else if (p.nv == 4)
-        gated_fwd_kernel<T, VEC, 4><<<grid, threads, 0, s>>>(a);
-    else if constexpr (VEC < 8)
-        gated_fwd_kernel<T, VEC, 8><<<grid, threads, 0, s>>>(a);
+// Shared memory of a backward's block: the ring, or the sums of several teams at the end.
+size_t bwd_smem(const RowPlan& p, int n) {
+    const size_t sums = p.teams > 1 ? sizeof(float) * n : 0;
+    return p.ring > sums ? p.ring : sums;
+}
+
+template <typename T, int VEC, int NV>
+cudaError_t launch_nv(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
+                      cudaStream_t s) {
+    const size_t smem = bwd ? bwd_smem(p, a.n) : p.ring;
+    const cudaError_t e = bwd ? allow_smem<&gated_bwd_kernel<T, VEC, NV>>(smem)
+                              : allow_smem<&gated_fwd_kernel<T, VEC, NV>>(smem);
+    if (e != cudaSuccess) return e;
+    if (bwd)
+        gated_bwd_kernel<T, VEC, NV><<<grid, p.threads(), smem, s>>>(a);
+    else
+        gated_fwd_kernel<T, VEC, NV><<<grid, p.threads(), smem, s>>>(a);
+    return cudaSuccess;
 }
 template <typename T, int VEC>
-void launch_bwd(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
-    const int threads = p.nw * p.teams * 32;
-    const size_t smem = p.teams > 1 ? sizeof(float) * a.n : 0;
-    if (p.nv == 1)
-        gated_bwd_kernel<T, VEC, 1><<<grid, threads, smem, s>>>(a);
-    else if (p.nv == 2)
-        gated_bwd_kernel<T, VEC, 2><<<grid, threads, smem, s>>>(a);
-    else if (p.nv == 4)
-        gated_bwd_kernel<T, VEC, 4><<<grid, threads, smem, s>>>(a);
-    else if constexpr (VEC < 8)
-        gated_bwd_kernel<T, VEC, 8><<<grid, threads, smem, s>>>(a);
+cudaError_t launch_vec(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
+                       cudaStream_t s) {
+    if (p.nv == 1) return launch_nv<T, VEC, 1>(bwd, p, grid, a, s);
+    if (p.nv == 2) return launch_nv<T, VEC, 2>(bwd, p, grid, a, s);
+    if (p.nv == 4) return launch_nv<T, VEC, 4>(bwd, p, grid, a, s);
+    if constexpr (most_vectors(VEC, sizeof(T)) == 8) return launch_nv<T, VEC, 8>(bwd, p, grid, a, s);
+    return cudaErrorInvalidValue;
+}
+template <typename T>
+cudaError_t launch_type(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
+                        cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (p.vec == 8) return launch_vec<T, 8>(bwd, p, grid, a, s);
+    if (p.vec == 4) return launch_vec<T, 4>(bwd, p, grid, a, s);
+    if (p.vec == 2) return launch_vec<T, 2>(bwd, p, grid, a, s);
+    return launch_vec<T, 1>(bwd, p, grid, a, s);
+}
+cudaError_t launch_gated(const ssd_gated_norm_t* n, bool bwd, const RowPlan& p, unsigned grid,
+                         const GatedArgs& a, cudaStream_t s) {
+    return n->dtype == SSD_DTYPE_F32 ? launch_type<float>(bwd, p, grid, a, s)
+                                     : launch_type<__nv_bfloat16>(bwd, p, grid, a, s);
 }
 
 void fill_args(const ssd_gated_norm_t* g, const RowPlan& p, GatedArgs* a) {
@@ -288,23 +353,23 @@ ssd_status_t ssd_gated_norm_forward(const ssd_gated_norm_t* norm, const void* y,
         (so.overlaps(sz) && !(out == z && norm->out_stride == norm->z_stride)))
         return SSD_ERR_INVALID_ARG;
     const void* ptrs[3] = {y, z, out};
+    const size_t sizes[3] = {e, e, e};
+    const long long strides[4] = {norm->dim / norm->groups, norm->y_stride, norm->z_stride,
+                                  norm->out_stride};
     RowPlan p;
-    if (!plan_row(norm->dim / norm->groups, gated_vec(norm, ptrs, 3), &p))
+    if (!plan_row(norm->dim / norm->groups, common_vec(most_vec(norm), strides, 4, ptrs, sizes, 3),
+                  most_vec(norm), 2 * (int)e, kFwdRegs, &p))
         return SSD_ERR_UNSUPPORTED;
     GatedArgs a = {};
     fill_args(norm, p, &a);
     a.y = y, a.z = z, a.w = weight, a.out = out, a.rstd = rstd;
-    const unsigned grid = (unsigned)((n + p.teams - 1) / p.teams * norm->groups);
+    a.nrb = gated_blocks(n, norm->groups, p);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("gated_norm_fwd");
-    if (norm->dtype == SSD_DTYPE_F32)
-        p.vec > 1 ? launch_fwd<float, 4>(p, grid, a, L.stream)
-                  : launch_fwd<float, 1>(p, grid, a, L.stream);
-    else
-        p.vec > 1 ? launch_fwd<__nv_bfloat16, 8>(p, grid, a, L.stream)
-                  : launch_fwd<__nv_bfloat16, 1>(p, grid, a, L.stream);
-    const cudaError_t err = L.end();
+    cudaError_t err = launch_gated(norm, false, p, (unsigned)a.nrb * norm->groups, a, L.stream);
+    const cudaError_t last = L.end();
+    if (err == cudaSuccess) err = last;
     set_last_launches(L.count);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -315,11 +380,11 @@ ssd_status_t ssd_gated_norm_workspace_size(const ssd_gated_norm_t* norm, size_t*
     if (st != SSD_OK) return st;
     const int n = norm->dim / norm->groups;
     size_t most = 256;
-    const int vecs[2] = {norm->dtype == SSD_DTYPE_BF16 ? 8 : 4, 1};
     bool any = false;
-    for (int vec : vecs) {
+    for (int vec = most_vec(norm); vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
         RowPlan p;
-        if ((vec > 1 && n % vec) || !plan_row(n, vec, &p)) continue;
+        if (n % vec || !plan_row(n, vec, most_vec(norm), 3 * (int)dtype_size(norm->dtype), kBwdRegs, &p))
+            continue;
         any = true;
         const size_t b = sizeof(float) * (size_t)gated_blocks(norm->rows, norm->groups, p) * norm->dim;
         if (b > most) most = b;
@@ -367,8 +432,12 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
     const void* ptrs[5] = {dout, y, z, dy, dz};
+    const size_t sizes[5] = {e, e, e, e, e};
+    const long long strides[6] = {norm->dim / norm->groups, norm->y_stride, norm->z_stride,
+                                  norm->out_stride, norm->dy_stride, norm->dz_stride};
     RowPlan p;
-    if (!plan_row(norm->dim / norm->groups, gated_vec(norm, ptrs, 5), &p))
+    if (!plan_row(norm->dim / norm->groups, common_vec(most_vec(norm), strides, 6, ptrs, sizes, 5),
+                  most_vec(norm), 3 * (int)e, kBwdRegs, &p))
         return SSD_ERR_UNSUPPORTED;
     GatedArgs a = {};
     fill_args(norm, p, &a);
@@ -381,13 +450,9 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
     cudaError_t err = cudaSuccess;
     if (grid > 0) {
         L.begin("gated_norm_bwd");
-        if (norm->dtype == SSD_DTYPE_F32)
-            p.vec > 1 ? launch_bwd<float, 4>(p, grid, a, L.stream)
-                      : launch_bwd<float, 1>(p, grid, a, L.stream);
-        else
-            p.vec > 1 ? launch_bwd<__nv_bfloat16, 8>(p, grid, a, L.stream)
-                      : launch_bwd<__nv_bfloat16, 1>(p, grid, a, L.stream);
-        err = L.end();
+        err = launch_gated(norm, true, p, grid, a, L.stream);
+        const cudaError_t last = L.end();
+        if (err == cudaSuccess) err = last;
     }
     if (err == cudaSuccess) {
         ReduceDst d = {};

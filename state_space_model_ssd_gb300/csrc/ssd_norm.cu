@@ -48,159 +48,264 @@ struct NormArgs {
     float eps;
 };
 
-template <typename T, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) norm_fwd_kernel(const NormArgs a) {
-    __shared__ float buf[2][32];
-    const Team t = team_of(a.nw);
-    const long long row = (long long)blockIdx.x * a.teams + t.id;
-    const bool in = row < a.rows;
-    float v[NV][VEC];
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (in && c < a.D) {
-            Pack<T, VEC> px;
-            px.load(static_cast<const T*>(a.x) + row * a.xs + c);
-            if (a.res) {
-                Pack<TR, VEC> pr;
-                pr.load(static_cast<const TR*>(a.res) + row * a.rs + c);
-                float r[VEC];
-                pr.get(r);
-                px.get(v[i]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
-                store_vec<VEC>(static_cast<TR*>(a.h) + row * a.hs + c, v[i]);
-            } else {
-                px.get(v[i]);
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += v[i][e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-        }
+// The inputs of one row, thread by thread, on their way: through the ring (S stages) or, in
+// single elements (S = 0), through registers one row ahead.
+template <typename T, typename TR, int VEC, int NV, int S>
+struct FwdRow {
+    Pack<T, VEC> nx[S ? 1 : NV];
+    Pack<TR, VEC> nr[S ? 1 : NV];
+    char* ring;
+    int thr, nthr;
+    static constexpr int xb = VEC * (int)sizeof(T), rb = VEC * (int)sizeof(TR);
+    __device__ __forceinline__ char* at(int stage, int i) const {
+        return ring + (size_t)(stage * NV + i) * nthr * (xb + rb);
     }
-    float mean = 0.f;
-    if (a.layer) {
-        team_sum<1>(t, &s, buf[0]);
-        mean = s / a.D;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.D)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float d = v[i][e] - mean;
-                q = fmaf(d, d, q);
-            }
-    }
-    team_sum<1>(t, &q, buf[1]);
-    const float rstd = 1.f / sqrtf(q / a.D + a.eps);
-    if (!in) return;
-    if (t.thread == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c >= a.D) continue;
-        float o[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            o[e] = (v[i][e] - mean) * rstd * param(a.w, c + e, a.wbf16);
-            if (a.b) o[e] += param(a.b, c + e, a.wbf16);
-        }
-        store_vec<VEC>(static_cast<T*>(a.y) + row * a.ys + c, o);
-    }
-}
-
-// One row's inputs as loaded, so that the next row's loads run under this row's sums.
-template <typename T, typename TR, int VEC, int NV>
-struct NormRow {
-    Pack<T, VEC> dy[NV];
-    Pack<TR, VEC> h[NV], dh[NV];
-    float2 st;
-    __device__ __forceinline__ void load(const NormArgs& a, const Team& t, long long row) {
-        st = make_float2(0.f, 0.f);
-        if (row < a.rows) st = a.stats_in[row];
+    __device__ __forceinline__ void load(const NormArgs& a, const Team& t, long long row, int stage) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t.thread + i * a.nw * 32) * VEC;
             if (row < a.rows && c < a.D) {
-                dy[i].load(static_cast<const T*>(a.dy) + row * a.ys + c);
-                h[i].load(static_cast<const TR*>(a.hin) + row * a.hs + c);
-                if (a.dh) dh[i].load(static_cast<const TR*>(a.dh) + row * a.rs + c);
-            } else {
-                dy[i].zero(), h[i].zero();
+                const T* x = static_cast<const T*>(a.x) + row * a.xs + c;
+                const TR* r = static_cast<const TR*>(a.res) + row * a.rs + c;
+                if constexpr (S > 0) {
+                    char* p = at(stage, i);
+                    Slot<T, VEC>::copy(p, thr, nthr, x);
+                    if (a.res) Slot<TR, VEC>::copy(p + nthr * xb, thr, nthr, r);
+                } else {
+                    nx[i].load(x);
+                    if (a.res) nr[i].load(r);
+                }
             }
+        }
+        if constexpr (S > 0) cp_async_commit();
+    }
+    // vector i of x and (res) of the residual
+    __device__ __forceinline__ void get(int stage, int i, bool res, float* x, float* r) const {
+        if constexpr (S > 0) {
+            const char* p = at(stage, i);
+            Slot<T, VEC>::read(p, thr, nthr, x);
+            if (res) Slot<TR, VEC>::read(p + nthr * xb, thr, nthr, r);
+        } else {
+            nx[i].get(x);
+            if (res) nr[i].get(r);
         }
     }
 };
 
 template <typename T, typename TR, int VEC, int NV>
+__global__ void __launch_bounds__(team_threads(VEC)) norm_fwd_kernel(const NormArgs a) {
+    constexpr int S = ring_stages(VEC, NV);
+    __shared__ float buf[2][32];
+    extern __shared__ __align__(16) char ring[];
+    const Team t = team_of(a.nw);
+    float w[NV][VEC], b[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t.thread + i * a.nw * 32) * VEC;
+        if (c < a.D) {
+            params<VEC>(a.w, c, a.wbf16, w[i]);
+            if (a.b) params<VEC>(a.b, c, a.wbf16, b[i]);
+        }
+        if (c >= a.D || !a.b)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) b[i][e] = 0.f;
+    }
+    const long long step = (long long)gridDim.x * a.teams;
+    long long row = (long long)blockIdx.x * a.teams + t.id;
+    FwdRow<T, TR, VEC, NV, S> in;
+    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
+#pragma unroll
+    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
+    int stage = 0, flip = 0;
+    // every team of the block takes the same number of rows (some of them beyond the last)
+    for (long long first = (long long)blockIdx.x * a.teams; first < a.rows; first += step) {
+        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+        const bool on = row < a.rows;
+        float v[NV][VEC];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (on && c < a.D) {
+                float r[VEC];
+                in.get(stage, i, a.res != nullptr, v[i], r);
+                if (a.res) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
+                    store_vec<VEC>(static_cast<TR*>(a.h) + row * a.hs + c, v[i]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s += v[i][e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+            }
+        }
+        // this thread's places of the stage are read: the row S rounds on takes them
+        in.load(a, t, row + (S ? S : 1) * step, stage);
+        float mean = 0.f;
+        if (a.layer) {
+            team_sum<1>(t, &s, buf[0]);
+            mean = s / a.D;
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (c < a.D)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float d = v[i][e] - mean;
+                    q = fmaf(d, d, q);
+                }
+        }
+        // rms rows take the two buffers in turn
+        team_sum<1>(t, &q, buf[a.layer ? 1 : flip]);
+        const float rstd = 1.f / sqrtf(q / a.D + a.eps);
+        if (on) {
+            if (t.thread == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t.thread + i * a.nw * 32) * VEC;
+                if (c >= a.D) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    o[e] = fmaf((v[i][e] - mean) * rstd, w[i][e], b[i][e]);
+                store_vec<VEC>(static_cast<T*>(a.y) + row * a.ys + c, o);
+            }
+        }
+        flip ^= 1;
+        row += step;
+        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+    }
+}
+
+// The same for the backward: dy, h and (dh) the residual stream's gradient.
+template <typename T, typename TR, int VEC, int NV, int S>
+struct BwdRow {
+    Pack<T, VEC> ndy[S ? 1 : NV];
+    Pack<TR, VEC> nh[S ? 1 : NV], ndh[S ? 1 : NV];
+    char* ring;
+    int thr, nthr;
+    static constexpr int db = VEC * (int)sizeof(T), hb = VEC * (int)sizeof(TR);
+    __device__ __forceinline__ char* at(int stage, int i) const {
+        return ring + (size_t)(stage * NV + i) * nthr * (db + 2 * hb);
+    }
+    __device__ __forceinline__ void load(const NormArgs& a, const Team& t, long long row, int stage) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (row < a.rows && c < a.D) {
+                const T* dy = static_cast<const T*>(a.dy) + row * a.ys + c;
+                const TR* h = static_cast<const TR*>(a.hin) + row * a.hs + c;
+                const TR* dh = static_cast<const TR*>(a.dh) + row * a.rs + c;
+                if constexpr (S > 0) {
+                    char* p = at(stage, i);
+                    Slot<T, VEC>::copy(p, thr, nthr, dy);
+                    Slot<TR, VEC>::copy(p + nthr * db, thr, nthr, h);
+                    if (a.dh) Slot<TR, VEC>::copy(p + nthr * (db + hb), thr, nthr, dh);
+                } else {
+                    ndy[i].load(dy);
+                    nh[i].load(h);
+                    if (a.dh) ndh[i].load(dh);
+                }
+            }
+        }
+        if constexpr (S > 0) cp_async_commit();
+    }
+    __device__ __forceinline__ void get(int stage, int i, float* dy, float* h) const {
+        if constexpr (S > 0) {
+            Slot<T, VEC>::read(at(stage, i), thr, nthr, dy);
+            Slot<TR, VEC>::read(at(stage, i) + nthr * db, thr, nthr, h);
+        } else {
+            ndy[i].get(dy);
+            nh[i].get(h);
+        }
+    }
+    __device__ __forceinline__ void get_dh(int stage, int i, float* dh) const {
+        if constexpr (S > 0)
+            Slot<TR, VEC>::read(at(stage, i) + nthr * (db + hb), thr, nthr, dh);
+        else
+            ndh[i].get(dh);
+    }
+};
+
+template <typename T, typename TR, int VEC, int NV>
 __global__ void __launch_bounds__(team_threads(VEC)) norm_bwd_kernel(const NormArgs a) {
+    constexpr int S = ring_stages(VEC, NV);
     __shared__ float buf[2][64];
-    extern __shared__ float acc[];  // several teams: their sums, joined at the end
+    extern __shared__ __align__(16) char ring[];
     const Team t = team_of(a.nw);
     float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t.thread + i * a.nw * 32) * VEC;
+        if (c < a.D) params<VEC>(a.w, c, a.wbf16, w[i]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[i][e] = c < a.D ? param(a.w, c + e, a.wbf16) : 0.f;
-            dw[i][e] = db[i][e] = 0.f;
-        }
+        for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
     }
     const long long step = (long long)gridDim.x * a.teams;
-    NormRow<T, TR, VEC, NV> cur, next;
     long long row = (long long)blockIdx.x * a.teams + t.id;
-    next.load(a, t, row);
-    int flip = 0;
+    BwdRow<T, TR, VEC, NV, S> in;
+    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
+#pragma unroll
+    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
+    float2 next = row < a.rows ? a.stats_in[row] : make_float2(0.f, 0.f);
+    int stage = 0, flip = 0;
     // every team of the block takes the same number of rows (some of them beyond the last)
     for (long long first = (long long)blockIdx.x * a.teams; first < a.rows; first += step) {
-        cur = next;
-        next.load(a, t, row + step);
-        float xh[NV][VEC], d[NV][VEC];
+        const float2 st = next;
+        next = row + step < a.rows ? a.stats_in[row + step] : make_float2(0.f, 0.f);
+        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+        const bool on = row < a.rows;
+        float xh[NV][VEC], d[NV][VEC], g[NV][VEC];
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            cur.h[i].get(xh[i]);
-            cur.dy[i].get(d[i]);
             const int c = (t.thread + i * a.nw * 32) * VEC;
+            if (on && c < a.D) {
+                in.get(stage, i, d[i], xh[i]);
+                if (a.dh) in.get_dh(stage, i, g[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                xh[i][e] = c < a.D ? (xh[i][e] - cur.st.x) * cur.st.y : 0.f;
-                dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
-                db[i][e] += d[i][e];
-                d[i][e] *= w[i][e];
-                sum[0] += d[i][e];
-                sum[1] = fmaf(d[i][e], xh[i][e], sum[1]);
+                for (int e = 0; e < VEC; ++e) {
+                    xh[i][e] = (xh[i][e] - st.x) * st.y;
+                    dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
+                    db[i][e] += d[i][e];
+                    d[i][e] *= w[i][e];
+                    sum[0] += d[i][e];
+                    sum[1] = fmaf(d[i][e], xh[i][e], sum[1]);
+                }
             }
         }
+        // this thread's places of the stage are read: the row S rounds on takes them
+        in.load(a, t, row + (S ? S : 1) * step, stage);
         team_sum<2>(t, sum, buf[flip]);
         flip ^= 1;
         const float c1 = a.layer ? sum[0] / a.D : 0.f, c2 = sum[1] / a.D;
-        if (row < a.rows) {
+        if (on) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (t.thread + i * a.nw * 32) * VEC;
                 if (c >= a.D) continue;
-                float o[VEC], g[VEC];
-                if (a.dh) cur.dh[i].get(g);
+                float o[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    o[e] = (d[i][e] - c1 - xh[i][e] * c2) * cur.st.y;
-                    if (a.dh) o[e] += g[e];
+                    o[e] = (d[i][e] - c1 - xh[i][e] * c2) * st.y;
+                    if (a.dh) o[e] += g[i][e];
                 }
                 store_vec<VEC>(static_cast<T*>(a.dx) + row * a.xs + c, o);
                 if (a.dres) store_vec<VEC>(static_cast<TR*>(a.dres) + row * a.D + c, o);
             }
         }
         row += step;
+        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
     }
-    if (a.teams > 1) {
+    float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
+    if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
+        if constexpr (S > 0) cp_async_wait<0>();
+        float* acc = reinterpret_cast<float*>(ring);
+        __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
             if (t.id == k)
 #pragma unroll
@@ -215,11 +320,9 @@ __global__ void __launch_bounds__(team_threads(VEC)) norm_bwd_kernel(const NormA
                 }
             __syncthreads();
         }
-        for (int i = threadIdx.x; i < a.nk * a.D; i += blockDim.x)
-            a.partial[(long long)blockIdx.x * a.nk * a.D + i] = acc[i];
+        for (int i = threadIdx.x; i < a.nk * a.D; i += blockDim.x) part[i] = acc[i];
         return;
     }
-    float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t.thread + i * a.nw * 32) * VEC;
@@ -246,49 +349,69 @@ ssd_status_t check_norm(const ssd_norm_t* p) {
     return SSD_OK;
 }
 
-// Vector length of the rows: 16 bytes of the activations, or single elements.
-int row_vec(const ssd_norm_t* p, const void* const* ptrs, int np) {
-    const int vec = p->dtype == SSD_DTYPE_BF16 ? 8 : 4;
-    if (p->dim % vec || p->x_stride % vec || p->r_stride % vec || p->h_stride % vec ||
-        p->y_stride % vec)
-        return 1;
-    for (int i = 0; i < np; ++i)
-        if (!aligned_to(ptrs[i], 16)) return 1;
-    return vec;
+// Bytes of a column that a forward (x, residual) and a backward (dy, h, dh) read.
+int fwd_col(const ssd_norm_t* p) { return (int)(dtype_size(p->dtype) + dtype_size(p->rdtype)); }
+int bwd_col(const ssd_norm_t* p) { return (int)(dtype_size(p->dtype) + 2 * dtype_size(p->rdtype)); }
+constexpr int kFwdRegs[2] = {28, 4}, kBwdRegs[2] = {40, 6};
+int most_vec(const ssd_norm_t* p) { return p->dtype == SSD_DTYPE_BF16 ? 8 : 4; }
+
+int row_vec(const ssd_norm_t* p, const void* const* ptrs, const size_t* sizes, int np) {
+    const long long strides[5] = {p->dim, p->x_stride, p->r_stride, p->h_stride, p->y_stride};
+    return common_vec(most_vec(p), strides, 5, ptrs, sizes, np);
 }
 
-// Blocks of the backward, each with a share of the rows and one partial sum per column.
-int bwd_blocks(long long rows, const RowPlan& p) {
-    const int per_sm = 1024 / (p.nw * p.teams * 32);
-    const long long most = (long long)sm_count() * (per_sm < 1 ? 1 : per_sm);
-    const long long want = (rows + p.teams - 1) / p.teams;
-    return (int)(want < most ? want : most);
+// Shared memory of a block: the ring, or the sums of several teams at the end.
+size_t fwd_smem(const RowPlan& p) { return p.ring; }
+size_t bwd_smem(const RowPlan& p, int dim) {
+    const size_t sums = p.teams > 1 ? sizeof(float) * 2 * dim : 0;
+    return p.ring > sums ? p.ring : sums;
 }
 
-template <typename T, typename TR, int VEC>
-void launch_fwd(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
-    const int threads = p.nw * p.teams * 32;
-    if (p.nv == 1)
-        norm_fwd_kernel<T, TR, VEC, 1><<<grid, threads, 0, s>>>(a);
-    else if (p.nv == 2)
-        norm_fwd_kernel<T, TR, VEC, 2><<<grid, threads, 0, s>>>(a);
-    else if (p.nv == 4)
-        norm_fwd_kernel<T, TR, VEC, 4><<<grid, threads, 0, s>>>(a);
-    else if constexpr (VEC < 8)
-        norm_fwd_kernel<T, TR, VEC, 8><<<grid, threads, 0, s>>>(a);
+template <typename T, typename TR, int VEC, int NV>
+cudaError_t launch_fwd_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    const cudaError_t e = allow_smem<&norm_fwd_kernel<T, TR, VEC, NV>>(fwd_smem(p));
+    if (e == cudaSuccess)
+        norm_fwd_kernel<T, TR, VEC, NV><<<grid, p.threads(), fwd_smem(p), s>>>(a);
+    return e;
+}
+template <typename T, typename TR, int VEC, int NV>
+cudaError_t launch_bwd_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    const cudaError_t e = allow_smem<&norm_bwd_kernel<T, TR, VEC, NV>>(bwd_smem(p, a.D));
+    if (e == cudaSuccess)
+        norm_bwd_kernel<T, TR, VEC, NV><<<grid, p.threads(), bwd_smem(p, a.D), s>>>(a);
+    return e;
 }
 template <typename T, typename TR, int VEC>
-void launch_bwd(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
-    const int threads = p.nw * p.teams * 32;
-    const size_t smem = p.teams > 1 ? sizeof(float) * 2 * a.D : 0;
+cudaError_t launch_vec(bool bwd, const RowPlan& p, unsigned grid, const NormArgs& a,
+                       cudaStream_t s) {
     if (p.nv == 1)
-        norm_bwd_kernel<T, TR, VEC, 1><<<grid, threads, smem, s>>>(a);
-    else if (p.nv == 2)
-        norm_bwd_kernel<T, TR, VEC, 2><<<grid, threads, smem, s>>>(a);
-    else if (p.nv == 4)
-        norm_bwd_kernel<T, TR, VEC, 4><<<grid, threads, smem, s>>>(a);
-    else if constexpr (VEC < 8)
-        norm_bwd_kernel<T, TR, VEC, 8><<<grid, threads, smem, s>>>(a);
+        return bwd ? launch_bwd_nv<T, TR, VEC, 1>(p, grid, a, s)
+                   : launch_fwd_nv<T, TR, VEC, 1>(p, grid, a, s);
+    if (p.nv == 2)
+        return bwd ? launch_bwd_nv<T, TR, VEC, 2>(p, grid, a, s)
+                   : launch_fwd_nv<T, TR, VEC, 2>(p, grid, a, s);
+    if (p.nv == 4)
+        return bwd ? launch_bwd_nv<T, TR, VEC, 4>(p, grid, a, s)
+                   : launch_fwd_nv<T, TR, VEC, 4>(p, grid, a, s);
+    if constexpr (most_vectors(VEC, sizeof(T)) == 8)
+        return bwd ? launch_bwd_nv<T, TR, VEC, 8>(p, grid, a, s)
+                   : launch_fwd_nv<T, TR, VEC, 8>(p, grid, a, s);
+    return cudaErrorInvalidValue;
+}
+template <typename T, typename TR>
+cudaError_t launch_types(bool bwd, const RowPlan& p, unsigned grid, const NormArgs& a,
+                         cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (p.vec == 8) return launch_vec<T, TR, 8>(bwd, p, grid, a, s);
+    if (p.vec == 4) return launch_vec<T, TR, 4>(bwd, p, grid, a, s);
+    if (p.vec == 2) return launch_vec<T, TR, 2>(bwd, p, grid, a, s);
+    return launch_vec<T, TR, 1>(bwd, p, grid, a, s);
+}
+cudaError_t launch_norm(const ssd_norm_t* n, bool bwd, const RowPlan& p, unsigned grid,
+                        const NormArgs& a, cudaStream_t s) {
+    if (n->dtype == SSD_DTYPE_F32) return launch_types<float, float>(bwd, p, grid, a, s);
+    if (n->rdtype == SSD_DTYPE_F32) return launch_types<__nv_bfloat16, float>(bwd, p, grid, a, s);
+    return launch_types<__nv_bfloat16, __nv_bfloat16>(bwd, p, grid, a, s);
 }
 
 }  // namespace
@@ -324,9 +447,11 @@ ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void*
     if ((sy.overlaps(sx) && !same_y) || (sh.overlaps(sr) && !same_h) || sy.overlaps(sr) ||
         sh.overlaps(sx) || sy.overlaps(sh))
         return SSD_ERR_INVALID_ARG;
-    const void* ptrs[4] = {x, residual, y, h};
+    const void* ptrs[4] = {x, y, residual, h};
+    const size_t sizes[4] = {e, e, re, re};
     RowPlan p;
-    if (!plan_row(D, row_vec(norm, ptrs, 4), &p)) return SSD_ERR_UNSUPPORTED;
+    if (!plan_row(D, row_vec(norm, ptrs, sizes, 4), most_vec(norm), fwd_col(norm), kFwdRegs, &p))
+        return SSD_ERR_UNSUPPORTED;
     NormArgs a = {};
     a.x = x, a.res = residual, a.w = weight, a.b = bias, a.y = y, a.h = h;
     a.stats = reinterpret_cast<float2*>(stats);
@@ -335,22 +460,12 @@ ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void*
     a.D = D, a.nw = p.nw, a.teams = p.teams;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;
     a.eps = norm->eps;
-    const unsigned grid = (unsigned)((n + p.teams - 1) / p.teams);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("norm_fwd");
-    using B16 = __nv_bfloat16;
-    const bool rf32 = norm->rdtype == SSD_DTYPE_F32;
-    if (norm->dtype == SSD_DTYPE_F32)
-        p.vec > 1 ? launch_fwd<float, float, 4>(p, grid, a, L.stream)
-                  : launch_fwd<float, float, 1>(p, grid, a, L.stream);
-    else if (rf32)
-        p.vec > 1 ? launch_fwd<B16, float, 8>(p, grid, a, L.stream)
-                  : launch_fwd<B16, float, 1>(p, grid, a, L.stream);
-    else
-        p.vec > 1 ? launch_fwd<B16, B16, 8>(p, grid, a, L.stream)
-                  : launch_fwd<B16, B16, 1>(p, grid, a, L.stream);
-    const cudaError_t err = L.end();
+    cudaError_t err = launch_norm(norm, false, p, (unsigned)team_blocks(n, p), a, L.stream);
+    const cudaError_t last = L.end();
+    if (err == cudaSuccess) err = last;
     set_last_launches(L.count);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -360,14 +475,12 @@ ssd_status_t ssd_norm_workspace_size(const ssd_norm_t* norm, size_t* bytes) {
     ssd_status_t st = check_norm(norm);
     if (st != SSD_OK) return st;
     size_t most = 256;
-    const int wide = norm->dtype == SSD_DTYPE_BF16 ? 8 : 4;
-    const int vecs[2] = {wide, 1};  // either may run, by the pointers' alignment
     bool any = false;
-    for (int vec : vecs) {
+    for (int vec = most_vec(norm); vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
         RowPlan p;
-        if ((vec > 1 && norm->dim % vec) || !plan_row(norm->dim, vec, &p)) continue;
+        if (norm->dim % vec || !plan_row(norm->dim, vec, most_vec(norm), bwd_col(norm), kBwdRegs, &p)) continue;
         any = true;
-        const size_t n = sizeof(float) * (size_t)bwd_blocks(norm->rows, p) * 2 * norm->dim;
+        const size_t n = sizeof(float) * (size_t)team_blocks(norm->rows, p) * 2 * norm->dim;
         if (n > most) most = n;
     }
     if (!any) return SSD_ERR_UNSUPPORTED;
@@ -407,9 +520,11 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     if (st != SSD_OK) return st;
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
-    const void* ptrs[5] = {dy, h, dh, dx, d_residual};
+    const void* ptrs[5] = {dy, dx, h, dh, d_residual};
+    const size_t sizes[5] = {e, e, re, re, re};
     RowPlan p;
-    if (!plan_row(D, row_vec(norm, ptrs, 5), &p)) return SSD_ERR_UNSUPPORTED;
+    if (!plan_row(D, row_vec(norm, ptrs, sizes, 5), most_vec(norm), bwd_col(norm), kBwdRegs, &p))
+        return SSD_ERR_UNSUPPORTED;
     NormArgs a = {};
     a.dy = dy, a.hin = h, a.dh = dh, a.w = weight, a.dx = dx, a.dres = d_residual;
     a.stats_in = reinterpret_cast<const float2*>(stats);
@@ -419,23 +534,15 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     a.D = D, a.nw = p.nw, a.teams = p.teams;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;
     a.nk = d_bias ? 2 : 1;
-    const int blocks = bwd_blocks(n, p);
+    const int blocks = team_blocks(n, p);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
     if (blocks > 0) {
         L.begin("norm_bwd");
-        using B16 = __nv_bfloat16;
-        if (norm->dtype == SSD_DTYPE_F32)
-            p.vec > 1 ? launch_bwd<float, float, 4>(p, blocks, a, L.stream)
-                      : launch_bwd<float, float, 1>(p, blocks, a, L.stream);
-        else if (norm->rdtype == SSD_DTYPE_F32)
-            p.vec > 1 ? launch_bwd<B16, float, 8>(p, blocks, a, L.stream)
-                      : launch_bwd<B16, float, 1>(p, blocks, a, L.stream);
-        else
-            p.vec > 1 ? launch_bwd<B16, B16, 8>(p, blocks, a, L.stream)
-                      : launch_bwd<B16, B16, 1>(p, blocks, a, L.stream);
-        err = L.end();
+        err = launch_norm(norm, true, p, (unsigned)blocks, a, L.stream);
+        const cudaError_t last = L.end();
+        if (err == cudaSuccess) err = last;
     }
     if (err == cudaSuccess) {
         ReduceDst d = {};
