@@ -1,7 +1,9 @@
-"""Builds libssd.so (the CUDA kernels and the C ABI) in-tree for sm_103a.
+"""Builds libssd.so (the CUDA kernels and the C ABI) in-tree for sm_103a, and the binding
+of the operators around the scan to torch tensors.
 
 Each .cu file is compiled by nvcc in parallel, then linked into
-``state_space_model_ssd_gb300/libssd.so``.  No CMake, no torch extension.
+``state_space_model_ssd_gb300/libssd.so``; ``csrc/layer_ext.cpp`` is compiled beside them and
+linked against it and torch's libraries into ``_layer_ext.so``.  No CMake.
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+EXT = os.path.join(PKG, "_layer_ext.so")
+EXT_SRC = os.path.join(CSRC, "layer_ext.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,6 +41,24 @@ def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return hs
+
+
+def _ext_commands(cuda_home):
+    """The compile command of the binding's object (which is of one torch version), the
+    object, and its link command."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    lib = os.path.join(root, "lib")
+    obj = os.path.join(OBJDIR, "layer_ext-torch%s.o" % torch.__version__)
+    cxx = shutil.which("g++") or "g++"
+    compile_ = [cxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+                "-I", os.path.join(root, "include"),
+                "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda_home, "include"),
+                "-c", EXT_SRC, "-o", obj]
+    link = [cxx, "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch", "-ltorch_python", "-L", PKG, "-l:libssd.so", "-Wl,-rpath,$ORIGIN"]
+    return compile_, obj, link
 
 
 def _stale(target, deps) -> bool:
@@ -60,20 +83,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + hdrs):
             jobs.append(common + ["-c", src, "-o", obj])
+    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    ext_compile, ext_obj, ext_link = _ext_commands(cuda_home)
+    if force or _stale(ext_obj, [EXT_SRC] + hdrs):
+        jobs.insert(0, ext_compile)
     if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(jobs))) as ex:
             futs = [ex.submit(subprocess.run, j, capture_output=True, text=True) for j in jobs]
             for j, f in zip(jobs, futs):
                 r = f.result()
                 if verbose or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError("nvcc failed on " + j[-3])
-    if force or jobs or _stale(LIB, objs):
+                    raise RuntimeError("%s failed on %s" % (os.path.basename(j[0]), j[-3]))
+    if force or any(j is not ext_compile for j in jobs) or _stale(LIB, objs):
         tmp = LIB + ".%d.tmp" % os.getpid()
         subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        check=True)
         os.replace(tmp, LIB)
+    if force or _stale(EXT, [ext_obj]):
+        tmp = EXT + ".%d.tmp" % os.getpid()
+        subprocess.run(ext_link + ["-o", tmp], check=True)
+        os.replace(tmp, EXT)
     return LIB
 
 
