@@ -276,12 +276,19 @@ ssd_status_t ssd_forward_noalloc_status(void* stream, int32_t* device_status);
  * convolution that makes x, B and C from the in-projection, the one-token step that
  * carries the convolution's window beside the scan's state, the norm in front of the layer
  * and the gated norm behind the scan.  Here pointers need the alignment of their element
- * type only (workspaces: 256 bytes; the scan state: 16); tensors whose rows all start on
- * 16 bytes (8 in the convolution's backward on bf16) move in vectors of that size.  Strides
+ * type only (workspaces: 256 bytes; the scan state: 16); tensors whose rows all start
+ * on 16 bytes move in bulk copies and vectors of that size, others in vectors of two elements
+ * or one.  Strides
  * are counted in elements, from one token or row to the next.  Weights, biases and their
  * gradients are float32 or bf16 (wdtype), whatever the activations are.  An output must not
  * overlap another output or, unless the call's comment says so, an input
  * (SSD_ERR_INVALID_ARG); a tensor counts as everything from its first to its last element. */
+
+/* Synchronises `stream` and returns in *device_status what the calls of this section have
+ * recorded on the current device since the last query: SSD_OK, or SSD_ERR_TIMEOUT if a
+ * kernel's bounded wait for one of its copies ran out (its outputs are then not valid).
+ * Returns SSD_ERR_CUDA if the synchronisation itself failed. */
+ssd_status_t ssd_layer_status(void* stream, int32_t* device_status);
 
 /* Causal depthwise convolution over the tokens of a sequence, then SiLU:
  *     pre[i] = bias + sum_{j < width} weight[c][width - 1 - j] u[i - j],

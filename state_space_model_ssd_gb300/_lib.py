@@ -123,6 +123,7 @@ _SIGS = {
     "ssd_step_host_size": (ctypes.c_int, [_PP, ctypes.POINTER(_SZ)]),
     "ssd_step_host": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                      _VP, _VP, _VP, _SZ, _VP]),
+    "ssd_layer_status": (ctypes.c_int, [_VP, ctypes.POINTER(_I32)]),
     "ssd_conv_forward": (ctypes.c_int, [_PC] + [_VP] * 11),
     "ssd_conv_workspace_size": (ctypes.c_int, [_PC, ctypes.POINTER(_SZ)]),
     "ssd_conv_backward": (ctypes.c_int, [_PC] + [_VP] * 15 + [_SZ, _VP]),

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "ssd_device.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace layer {
@@ -118,44 +119,20 @@ struct Pack<__nv_bfloat16, 2> {
     __device__ __forceinline__ void get(float* f) const { unpack2(v, f); }
 };
 
-// Copies of a thread's own vectors into its own places of a ring in shared memory: they are
-// in flight without holding registers, and since no other thread reads them, waiting for
-// the thread's own copies is enough (no barrier).  A vector of B bytes lies in pieces of 16
-// (or B) bytes, each piece `nthr` threads wide, so that a warp's accesses have no conflicts.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
-                     : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-template <typename T, int VEC>
-struct Slot {
-    static constexpr int bytes = VEC * (int)sizeof(T);
-    static constexpr int piece = bytes < 16 ? bytes : 16;
-    static __device__ __forceinline__ void copy(char* base, int thr, int nthr, const T* src) {
-#pragma unroll
-        for (int i = 0; i < bytes / piece; ++i)
-            cp_async<piece>(base + (i * nthr + thr) * piece,
-                            reinterpret_cast<const char*>(src) + i * piece);
+// Waits for phase `parity` of a copy's barrier.  The wait is bounded (2 s); one that runs out
+// records SSD_ERR_TIMEOUT and lets every later wait of the thread pass at once, so that a lost
+// copy ends in a status and wrong values, not in a hang.
+struct Waiter {
+    int* status;
+    bool gone = false;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+        if (tc::mbar_try_wait(bar, parity)) return;
+        slow(bar, parity);
     }
-    static __device__ __forceinline__ void read(const char* base, int thr, int nthr, float* f) {
-        constexpr int n = piece / (int)sizeof(T);
-#pragma unroll
-        for (int i = 0; i < bytes / piece; ++i) {
-            Pack<T, n> v;
-            v.load(reinterpret_cast<const T*>(base + (i * nthr + thr) * piece));
-            v.get(f + i * n);
-        }
+    __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) {
+        if (gone || tc::mbar_wait(bar, parity)) return;
+        gone = true;
+        atomicCAS(status, 0, (int)SSD_ERR_TIMEOUT);
     }
 };
 
@@ -272,8 +249,18 @@ __device__ __forceinline__ void from_lanes(const typename Lanes<VEC>::V* v, floa
 template <typename T>
 __device__ __forceinline__ F2 sigmoid_lanes(F2 v) {
     float f[2];
-    split(v, f);
-    return join(sigmoid_of<T>(f[0]), sigmoid_of<T>(f[1]));
+    if constexpr (sizeof(T) == 4) {
+        split(v, f);
+        return join(sigmoid_of<T>(f[0]), sigmoid_of<T>(f[1]));
+    } else {  // sigmoid_of<T> on both, the multiply and the add paired
+        split(mul_(v, both<F2>(-1.44269504f)), f);
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f[0]));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f[1]));
+        split(add_(join(f[0], f[1]), both<F2>(1.f)), f);
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f[0]));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f[1]));
+        return join(f[0], f[1]);
+    }
 }
 template <typename T>
 __device__ __forceinline__ float sigmoid_lanes(float v) {

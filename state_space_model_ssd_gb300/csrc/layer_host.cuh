@@ -16,6 +16,10 @@ inline bool dtype_ok(int d) { return d == SSD_DTYPE_F32 || d == SSD_DTYPE_BF16; 
 inline size_t dtype_size(int d) { return d == SSD_DTYPE_BF16 ? 2 : 4; }
 inline bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Where the kernels of the operators around the scan record a wait that ran out, on the current
+// device (nullptr: no such device).
+int* status_word();
+
 // A tensor as the address range it spans: `rows` rows of `width` elements, `stride`
 // elements apart.
 struct Span {

@@ -1,4 +1,5 @@
-// The second pass of the weight gradients: the blocks of a backward kernel each leave one
+// The status word of the operators around the scan, and the second pass of the weight
+// gradients: the blocks of a backward kernel each leave one
 // float32 partial sum per weight, and this kernel adds them in a fixed order, so the
 // gradients are bit-identical from run to run (no atomics).
 //
@@ -6,6 +7,8 @@
 // then the warp sums are added.  Bound by the latency of the loads; the bytes (nb * nk * C *
 // 4) come from L2, where the kernel before left them.  The launch itself overlaps the end of
 // that kernel; griddepcontrol.wait holds the loads back until it has finished.
+#include <atomic>
+
 #include "layer_device.cuh"
 #include "layer_host.cuh"
 
@@ -56,7 +59,23 @@ cudaError_t launch(const float* partial, int nb, int nk, long long C, const Redu
     return cudaLaunchKernelEx(&cfg, partial_sum_kernel<W>, partial, nb, nk, C, d, bf16);
 }
 
+__device__ int g_status;
+
 }  // namespace
+
+int* status_word() {
+    static std::atomic<int*> word[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    int* p = word[dev].load();
+    if (!p) {
+        void* q = nullptr;
+        if (cudaGetSymbolAddress(&q, g_status) != cudaSuccess) return nullptr;
+        p = static_cast<int*>(q);
+        word[dev].store(p);
+    }
+    return p;
+}
 
 cudaError_t launch_partial_sum(const float* partial, int nb, int nk, long long C,
                                const ReduceDst& d, int wdtype, Launch& L) {
@@ -72,3 +91,18 @@ cudaError_t launch_partial_sum(const float* partial, int nb, int nk, long long C
 
 }  // namespace layer
 }  // namespace ssd
+
+using namespace ssd;
+
+extern "C" ssd_status_t ssd_layer_status(void* stream, int32_t* device_status) {
+    if (!device_status) return SSD_ERR_INVALID_ARG;
+    int* word = layer::status_word();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int v = 0;
+    if (!word || cudaMemcpyAsync(&v, word, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemsetAsync(word, 0, sizeof(int), s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    *device_status = v;
+    return SSD_OK;
+}

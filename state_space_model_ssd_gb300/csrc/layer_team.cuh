@@ -1,6 +1,7 @@
-// Rows of a norm are worked on by teams: `nw` warps that hold one row in registers, thread
-// by thread VEC neighbouring columns NV times over.  A block holds one team, or several
-// one-warp teams.
+// Rows of a norm are worked on by teams: `nw` warps that hold one row in registers.  A warp
+// owns NV * 32 * VEC neighbouring columns, a lane VEC of them NV times over, 32 * VEC apart, so
+// that all of a thread's places in a row are offsets known when compiling.  A block holds one
+// team, or several one-warp teams.
 #pragma once
 
 #include <atomic>
@@ -15,7 +16,7 @@ struct Team {
     int nw;      // warps in the team
     int warp;    // this warp in its team
     int lane;
-    int thread;  // this thread in its team
+    int rank;    // this thread in its team
     int id;      // the team in its block
 };
 __device__ __forceinline__ Team team_of(int nw) {
@@ -25,90 +26,300 @@ __device__ __forceinline__ Team team_of(int nw) {
     t.id = w / nw;
     t.warp = w - t.id * nw;
     t.lane = threadIdx.x & 31;
-    t.thread = t.warp * 32 + t.lane;
+    t.rank = t.warp * 32 + t.lane;
     return t;
 }
 
-// Sums N values over the team, the same bits in every thread.  Every thread of the block
-// calls it (one-warp teams need no barrier).  `buf` holds 32 N floats per call in flight;
-// two calls in a row take different buffers, and a third comes after the barrier of the
-// second, when every thread has read the first.
+// Where the warps of a team meet: N floats per warp.  Zeroed once, so that the places of
+// warps a team does not have add nothing.
 template <int N>
-__device__ __forceinline__ void team_sum(const Team& t, float* v, float* buf) {
+struct TeamBuf {
+    float4 v[2][N][8];
+    __device__ __forceinline__ void clear() {
+        float* f = reinterpret_cast<float*>(v);
+        for (int i = threadIdx.x; i < 2 * N * 32; i += blockDim.x) f[i] = 0.f;
+        __syncthreads();
+    }
+};
+// Sums N values over the team, the same bits in every thread.  Every thread of the block
+// calls it (one-warp teams need no barrier).  Two calls in a row take different halves of the
+// buffer (`flip`); a third comes after the barrier of the second, when every thread has read
+// the first.
+template <int N>
+__device__ __forceinline__ void team_sum(const Team& t, float* x, TeamBuf<N>& buf, int flip) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
     if (t.nw == 1) return;
     if (t.lane == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) buf[i * 32 + t.warp] = v[i];
+        for (int i = 0; i < N; ++i) reinterpret_cast<float*>(buf.v[flip][i])[t.warp] = x[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = t.lane < t.nw ? buf[i * 32 + t.lane] : 0.f;
+    for (int i = 0; i < N; ++i) x[i] = 0.f;
+    for (int k = 0; k < t.nw; k += 4)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    }
+        for (int i = 0; i < N; ++i) {
+            const float4 w = buf.v[flip][i][k >> 2];
+            x[i] += (w.x + w.y) + (w.z + w.w);
+        }
 }
 
-// A row's vectors: 16 bytes of the activations where every row starts on 16 bytes, else 8,
-// 4 or one element, whichever divides the row's length, the strides and the addresses.
+// A row's vectors: `most` elements (16 bytes of the widest tensor) where every row of every
+// tensor starts on 16 bytes, else two elements or one, whichever divides the row's length, the
+// strides and the addresses.
 inline int common_vec(int most, const long long* strides, int ns, const void* const* ptrs,
                       const size_t* sizes, int np) {
-    for (int vec = most; vec > 1; vec >>= 1) {
-        bool ok = true;
-        for (int i = 0; i < ns; ++i) ok = ok && strides[i] % vec == 0;
-        for (int i = 0; i < np; ++i)
-            ok = ok && aligned_to(ptrs[i], vec * sizes[i] < 16 ? vec * sizes[i] : 16);
-        if (ok) return vec;
+    bool wide = true, pairs = true;
+    for (int i = 0; i < ns; ++i) pairs = pairs && strides[i] % 2 == 0;
+    for (int i = 0; i < np; ++i) {
+        const long long n = 16 / (long long)sizes[i];
+        for (int k = 0; k < ns; ++k) wide = wide && strides[k] % n == 0;
+        wide = wide && aligned_to(ptrs[i], 16);
+        pairs = pairs && aligned_to(ptrs[i], 2 * sizes[i]);
     }
-    return 1;
+    return wide ? most : pairs ? 2 : 1;
 }
 
 // How a row of `dim` columns is laid over threads.
 struct RowPlan {
     int vec;     // elements of a vector
-    int nv;      // vectors a thread holds
+    int nv;      // vectors a thread holds: 1, 2, 3, 4 or 8
     int nw;      // warps in a team
     int teams;   // teams in a block
     int per_sm;  // blocks an SM holds at once
-    size_t ring; // bytes of the rows in flight
+    int stages;  // rows in flight by bulk copies (0: through registers)
+    size_t ring; // bytes of shared memory they take
     int threads() const { return nw * teams * 32; }
 };
-constexpr int team_threads(int vec) { return vec == 1 ? 1024 : 512; }
-// (rows of up to 16384 columns in vectors of 16 bytes, 8192 otherwise)
-constexpr int most_vectors(int vec, int esize) { return esize == 2 && vec >= 4 ? 4 : 8; }
-// Rows in flight.  Four cover the latency of HBM where a thread holds one vector; wider rows
-// have enough bytes in flight with two, and the widest do not fit twice.  Rows in single
-// elements are loaded to registers one row ahead (0): a copy moves 4 bytes at least.
-constexpr int ring_stages(int vec, int nv) {
-    return vec == 1 ? 0 : nv == 1 ? 4 : nv * vec <= 16 ? 2 : 1;
+// Longest rows.
+constexpr int most_columns(int vec) { return vec >= 4 ? 16384 : 8192; }
+constexpr int most_vectors(int vec) { return vec == 8 ? 4 : 8; }
+// Registers of a thread that holds e elements of a row: what the kernels need without spilling
+// (beyond 16 elements a backward spills, on rows of more than 8192 columns), and no more, since
+// they decide how many rows an SM works on.
+constexpr int row_regs(int vec, int nv, bool bwd) {
+    const int e = vec * nv;
+    const int r = bwd ? (e <= 2 ? 56 : e <= 4 ? 64 : e <= 8 ? 96 : 128)
+                      : (e <= 2 ? 40 : e <= 4 ? 48 : e <= 8 ? 64 : e <= 16 ? 96 : 128);
+    return vec == 1 && r > 64 ? 64 : r;
 }
-// `col_bytes`: bytes of a column in all tensors that are read; `regs`: registers of a thread
-// that holds e elements of a row are about regs[0] + regs[1] e, 128 at most.  Longest rows:
-// 16384 columns in vectors of 16 bytes, 8192 otherwise.
-inline bool plan_row(int dim, int vec, int most, int col_bytes, const int (&regs)[2], RowPlan* p) {
-    if (dim > (vec == most ? 16384 : 8192)) return false;
+// What a row's plan goes by: the tensors read, na of `ab` bytes an element and nb of `bb`.
+struct RowCost {
+    bool bwd;
+    int na, ab, nb, bb;
+};
+inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
+    if (dim > most_columns(vec)) return false;
     p->vec = vec;
     const int nvec = (dim + vec - 1) / vec;
-    if (vec == 1)  // single elements: up to four a thread for loads in flight, then more threads
-        p->nv = nvec <= 256 ? 1 : nvec <= 512 ? 2 : nvec <= 4096 ? 4 : 8;
-    else
-        for (p->nv = 1; (nvec + p->nv - 1) / p->nv > 512;) p->nv <<= 1;
-    p->nw = ((nvec + p->nv - 1) / p->nv + 31) / 32;
-    if (p->nv > most_vectors(vec, most == 8 ? 2 : 4) || p->nw * 32 > team_threads(vec)) return false;
+    // elements a thread holds at most, as long as a block then has threads enough for the row
+    const int hold = vec == 1 ? 4 : cost.bwd ? 8 : 16;
+    // A warp spends about as long on a row's sums and addresses as on ten elements a lane, so
+    // the cheapest plan has few warps with many elements each, none of them idle.
+    long long best = -1;
+    const int sizes[5] = {1, 2, 3, 4, 8};
+    for (int nv : sizes) {
+        if (nv > most_vectors(vec)) break;
+        const int nw = ((nvec + nv - 1) / nv + 31) / 32;
+        if (nw > 32 || nw * 32 * row_regs(vec, nv, cost.bwd) > 65536) continue;
+        if (nv * vec > hold && best >= 0) break;
+        const long long c = (long long)nw * (10 + nv * vec);
+        if (best >= 0 && c >= best) continue;
+        best = c;
+        p->nv = nv;
+        p->nw = nw;
+    }
+    if (best < 0) return false;
     p->teams = p->nw == 1 ? 4 : 1;
-    p->ring = (size_t)ring_stages(vec, p->nv) * p->threads() * p->nv * vec * col_bytes;
-    int r = regs[0] + regs[1] * p->nv * vec;
-    if (r > (vec == 1 ? 64 : 128)) r = vec == 1 ? 64 : 128;
-    p->per_sm = 65536 / ((r + 7) / 8 * 8) / p->threads();
-    const int fit = (int)((size_t)(220 << 10) / (p->ring + 2048));
-    if (fit < p->per_sm) p->per_sm = fit;
+    p->per_sm = 65536 / row_regs(vec, p->nv, cost.bwd) / p->threads();
     if (p->per_sm > 16) p->per_sm = 16;
-    if (p->per_sm < 1) p->per_sm = 1;
+    p->stages = 0;
+    p->ring = 0;
+    if (vec >= 4) {
+        // two to eight rows in flight a team, within what the blocks of an SM can share
+        const size_t row = (size_t)dim * (cost.na * cost.ab + cost.nb * cost.bb) * p->teams;
+        const size_t all = 210 << 10;
+        while (p->per_sm > 1 && 2 * row + 4096 > all / p->per_sm) --p->per_sm;
+        size_t s = (all / p->per_sm - 4096) / row;
+        p->stages = s > 8 ? 8 : s < 1 ? 1 : (int)s;
+        p->ring = p->stages * row;
+    }
     return true;
 }
+// The tensors of a team's rows on their way to its threads: by bulk copies into a ring of
+// `stages` rows in shared memory, which one thread of the team issues, or, in vectors of less
+// than 16 bytes, through registers one row ahead.  The first NA tensors have elements of type A,
+// the NB others of type B.
+constexpr int kMostStages = 8;
+struct RowBars {
+    uint64_t full[4][kMostStages];  // by team of the block
+};
+template <typename A, typename B, int NA, int NB, int VEC, int NV>
+struct Rows {
+    static constexpr bool BULK = VEC >= 4;
+    Pack<A, VEC> ra[BULK ? 1 : NV][NA];
+    Pack<B, VEC> rb[BULK ? 1 : NV][NB ? NB : 1];
+    const A* pa[NA];           // the next row to load: its start, or this thread's part of it
+    const B* pb[NB ? NB : 1];
+    long long sa[NA], sb[NB ? NB : 1];  // elements from a row to the team's next
+    int left;                  // rows still to load
+    bool in[NV];               // whether vector i lies in the row
+    char* ring;                // this team's
+    uint64_t* full;
+    int cols, stages, fill, stage;
+    uint32_t parity;
+    bool issues;               // this thread issues the copies
+    Waiter waiter;
+
+    static __device__ __forceinline__ int column(const Team& t, int i) {
+        return ((t.warp * NV + i) * 32 + t.lane) * VEC;
+    }
+    // `count` rows for this team, of `n` columns.  A barrier of the block has to come between
+    // this and start().
+    __device__ __forceinline__ void begin(const Team& t, int count, int n, int nstages, char* all,
+                                          RowBars* bars, int* status) {
+        left = count;
+        cols = n;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) in[i] = column(t, i) < n;
+        if constexpr (BULK) {
+            stages = nstages;
+            fill = stage = 0;
+            parity = 0;
+            issues = t.rank == 0;
+            waiter.status = status;
+            full = bars->full[t.id];
+            ring = all + (size_t)t.id * stages * row_bytes();
+            if (issues) {
+                for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
+                tc::fence_mbar_init();
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t row_bytes() const {
+        return (uint32_t)cols * (NA * (int)sizeof(A) + NB * (int)sizeof(B));
+    }
+    template <int K>
+    __device__ __forceinline__ void a(const Team& t, const void* p, long long row, long long by,
+                                      long long stride, int col) {
+        pa[K] = static_cast<const A*>(p) + row * stride + col + (BULK ? 0 : column(t, 0));
+        sa[K] = by * stride;
+    }
+    template <int K>
+    __device__ __forceinline__ void b(const Team& t, const void* p, long long row, long long by,
+                                      long long stride) {
+        pb[K] = static_cast<const B*>(p) + row * stride + (BULK ? 0 : column(t, 0));
+        sb[K] = by * stride;
+    }
+    __device__ __forceinline__ void start() {
+        if constexpr (BULK) {
+            for (int s = 0; s < stages; ++s) issue();
+        } else {
+            fetch();
+        }
+    }
+    __device__ __forceinline__ void advance() {
+#pragma unroll
+        for (int k = 0; k < NA; ++k) pa[k] += sa[k];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) pb[k] += sb[k];
+        --left;
+    }
+    __device__ __forceinline__ void issue() {
+        if (issues && left > 0) {
+            uint64_t* bar = &full[fill];
+            char* at = ring + fill * row_bytes();
+            tc::mbar_expect_tx(bar, row_bytes());
+#pragma unroll
+            for (int k = 0; k < NA; ++k)
+                tc::bulk_load(at + k * cols * (int)sizeof(A), pa[k], cols * (int)sizeof(A), bar);
+            at += NA * cols * (int)sizeof(A);
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+                tc::bulk_load(at + k * cols * (int)sizeof(B), pb[k], cols * (int)sizeof(B), bar);
+            advance();
+            fill = fill + 1 == stages ? 0 : fill + 1;
+        }
+    }
+    __device__ __forceinline__ void fetch() {
+        if (left <= 0) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+#pragma unroll
+                for (int k = 0; k < NA; ++k) ra[i][k].load(pa[k] + i * 32 * VEC);
+#pragma unroll
+                for (int k = 0; k < NB; ++k) rb[i][k].load(pb[k] + i * 32 * VEC);
+            }
+        advance();
+    }
+    // Before the first get of a row that this team has.
+    __device__ __forceinline__ void arrived() {
+        if constexpr (BULK) waiter.wait(&full[stage], parity);
+    }
+    // After the last get of a row: registers take the next row.
+    __device__ __forceinline__ void done() {
+        if constexpr (!BULK) fetch();
+    }
+    // Once the whole team has done its gets (a team of one warp waits for itself here): the
+    // row's place takes another.
+    __device__ __forceinline__ void reuse(const Team& t) {
+        if constexpr (BULK) {
+            if (t.nw == 1) __syncwarp();
+            issue();
+            if (++stage == stages) stage = 0, parity ^= 1;
+        }
+    }
+    // Before the block ends or its ring is used for something else: nothing is on its way any
+    // more unless a wait ran out; then it is waited for once more.
+    __device__ __forceinline__ void drain() {
+        if constexpr (BULK)
+            if (waiter.gone && issues)
+                for (int s = 0; s < stages; ++s) tc::mbar_wait(&full[s], parity);
+    }
+    __device__ __forceinline__ void get_a(const Team& t, int i, int k, typename Lanes<VEC>::V* v) const {
+        float f[VEC];
+        if constexpr (BULK) {
+            Pack<A, VEC> p;
+            p.load(reinterpret_cast<const A*>(ring + stage * row_bytes()) + k * cols + column(t, i));
+            p.get(f);
+        } else {
+            ra[i][k].get(f);
+        }
+        to_lanes<VEC>(f, v);
+    }
+    __device__ __forceinline__ void get_b(const Team& t, int i, int k, typename Lanes<VEC>::V* v) const {
+        float f[VEC];
+        if constexpr (BULK) {
+            Pack<B, VEC> p;
+            p.load(reinterpret_cast<const B*>(ring + stage * row_bytes() + NA * cols * (int)sizeof(A)) +
+                   k * cols + column(t, i));
+            p.get(f);
+        } else {
+            rb[i][k].get(f);
+        }
+        to_lanes<VEC>(f, v);
+    }
+};
+// Rows first, first + by, ... below `rows`.
+__device__ __forceinline__ int rows_of(long long first, long long by, long long rows) {
+    return first < rows ? (int)((rows - first + by - 1) / by) : 0;
+}
+__device__ __forceinline__ float lane_sum(F2 v) {
+    float f[2];
+    split(v, f);
+    return f[0] + f[1];
+}
+__device__ __forceinline__ float lane_sum(float v) { return v; }
+template <int VEC, typename T>
+__device__ __forceinline__ void store_lanes(T* p, const typename Lanes<VEC>::V* v) {
+    float f[VEC];
+    from_lanes<VEC>(v, f);
+    store_vec<VEC>(p, f);
+}
+
 // Blocks that share `rows` rows: as many as the GPU holds at once.
 inline int team_blocks(long long rows, const RowPlan& p) {
     const long long most = (long long)sm_count() * p.per_sm;

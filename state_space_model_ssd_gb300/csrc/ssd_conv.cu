@@ -50,12 +50,14 @@ struct ConvArgs {
     long long us, dus;    // token strides of u and du, elements
     long long C;
     int off1, off2;       // first channel of pieces 1 and 2
+    int blk1, blk2;       // and their first blocks of channels
     int width[3];
     int nseq;             // sequences (dense rows or packed)
     int run;              // tokens a thread walks
     int nrunblk;          // blocks along the tokens
     int nchblk;           // blocks along the channels
     int wbf16;
+    int* status;
 };
 
 struct Seq {
@@ -135,67 +137,158 @@ __device__ __forceinline__ void token(const ConvArgs& a, const Seq& q, long long
 // Weights and bias of a block's channels, transposed to [K + 1][channels] in shared memory
 // (row K is the bias): a thread's VEC channels are then neighbours in every row.
 template <int VEC, int K>
-__device__ __forceinline__ void stage_weights(const ConvArgs& a, long long c0,
+__device__ __forceinline__ void stage_weights(const ConvArgs& a, long long c0, int n,
                                               float (*ws)[kLanes * VEC]) {
     const int tid = threadIdx.y * kLanes + threadIdx.x;
-    const long long n = a.C - c0 < kLanes * VEC ? a.C - c0 : kLanes * VEC;
     for (int i = tid; i < n * K; i += kLanes * kRuns)
         ws[i % K][i / K] = param(a.w, c0 * K + i, a.wbf16);
     for (int i = tid; i < n; i += kLanes * kRuns) ws[K][i] = a.b ? param(a.b, c0 + i, a.wbf16) : 0.f;
     __syncthreads();
 }
 
-// The piece of the split output that holds channels c .. c + VEC (the split respects VEC).
-template <typename T>
-__device__ __forceinline__ T* piece(const ConvArgs& a, long long c, int* stride) {
-    const int k = c >= a.off2 ? 2 : c >= a.off1 ? 1 : 0;
-    *stride = k == 2 ? a.width[2] : k == 1 ? a.width[1] : a.width[0];
-    T* p = static_cast<T*>(k == 2 ? a.out[2] : k == 1 ? a.out[1] : a.out[0]);
-    return p + (c - (k == 2 ? a.off2 : k == 1 ? a.off1 : 0));
-}
-
-// The tokens of a run on their way to its thread, in groups of kGroup: through a ring in
-// shared memory (S groups, N tensors), or, in single channels (S = 0), through registers one
-// group ahead.
+// The tokens of a warp's run on their way to it, in groups of kGroup: by bulk copies into a
+// ring of kGroups groups in shared memory, a lane a token, or, in vectors of less than 16 bytes,
+// through registers one group ahead.  N tensors, of the block's channels.
 constexpr int kGroup = 4;
-constexpr int ring_groups(int vec) { return vec == 1 ? 0 : 3; }
-
-template <typename T, int VEC, int S, int N>
+constexpr int kGroups = 3;
+struct RunBars {
+    uint64_t full[kRuns][kGroups];
+};
+template <typename T, int VEC, int N>
 struct Run {
-    Pack<T, VEC> next[S ? 1 : kGroup][N];
-    const T* src[N];  // token 0 of this thread's channels
+    static constexpr bool BULK = VEC >= 4;
+    static constexpr int line = kLanes * VEC * (int)sizeof(T);  // a token of a tensor in the ring
+    Pack<T, VEC> next[BULK ? 1 : kGroup][N];
+    const T* src[N];  // the next token to load: this lane's of the group, or its channels
     long long stride[N];
-    char* ring;
-    int tid;
-    static constexpr int bytes = VEC * (int)sizeof(T);
-    static constexpr int threads = kLanes * kRuns;
-    __device__ __forceinline__ char* at(int stage, int i, int k) const {
-        return ring + ((stage * kGroup + i) * N + k) * threads * bytes;
+    int left;         // tokens still to load
+    uint32_t bytes;   // of a token
+    char* ring;       // this warp's
+    uint64_t* full;
+    int fill, stage;
+    uint32_t parity;
+    Waiter waiter;
+
+    // `tokens` (perhaps none) from t0 on, `channels` of them; every lane of the warp calls it.
+    __device__ __forceinline__ void begin(int tokens, int channels, char* all, RunBars* bars,
+                                          int* status) {
+        left = tokens;
+        if constexpr (BULK) {
+            bytes = channels * (int)sizeof(T);
+            ring = all + threadIdx.y * (kGroups * kGroup * N * line);
+            full = bars->full[threadIdx.y];
+            fill = stage = 0;
+            parity = 0;
+            waiter.status = status;
+            if (threadIdx.x == 0) {
+                for (int s = 0; s < kGroups; ++s) tc::mbar_init(&full[s], 1);
+                tc::fence_mbar_init();
+            }
+            __syncwarp();
+        }
     }
-    // tokens t .. t + kGroup, those before `end`
-    __device__ __forceinline__ void load(long long t, long long end, int stage) {
+    // tensor k: its token t0, the block's first channel
+    template <int K>
+    __device__ __forceinline__ void tensor(const T* p, long long by) {
+        src[K] = p + (BULK ? threadIdx.x * by : threadIdx.x * VEC);
+        stride[K] = by;
+    }
+    __device__ __forceinline__ void start() {
+        if constexpr (BULK) {
+#pragma unroll
+            for (int s = 0; s < kGroups; ++s) issue();
+        } else {
+            fetch();
+        }
+    }
+    __device__ __forceinline__ void issue() {
+        if (left > 0) {
+            const int n = left < kGroup ? left : kGroup;
+            uint64_t* bar = &full[fill];
+            if (threadIdx.x == 0) tc::mbar_expect_tx(bar, n * N * bytes);
+            __syncwarp();
+            if ((int)threadIdx.x < n) {
+                char* at = ring + (fill * kGroup + threadIdx.x) * (N * line);
+#pragma unroll
+                for (int k = 0; k < N; ++k) tc::bulk_load(at + k * line, src[k], bytes, bar);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) src[k] += kGroup * stride[k];
+            left -= kGroup;
+            fill = fill + 1 == kGroups ? 0 : fill + 1;
+        }
+    }
+    __device__ __forceinline__ void fetch() {
 #pragma unroll
         for (int i = 0; i < kGroup; ++i)
-            if (t + i < end)
+            if (i < left)
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const T* p = src[k] + (t + i) * stride[k];
-                    if constexpr (S > 0)
-                        Slot<T, VEC>::copy(at(stage, i, k), tid, threads, p);
-                    else
-                        next[i][k].load(p);
-                }
-        if constexpr (S > 0) cp_async_commit();
+                for (int k = 0; k < N; ++k) next[i][k].load(src[k] + i * stride[k]);
+        left -= kGroup;
+#pragma unroll
+        for (int k = 0; k < N; ++k) src[k] += kGroup * stride[k];
     }
-    __device__ __forceinline__ void get(int stage, int i, int k, typename Lanes<VEC>::V* v) const {
+    __device__ __forceinline__ void arrived() {
+        if constexpr (BULK) waiter.wait(&full[stage], parity);
+    }
+    // After the last get of a group: its place takes another.
+    __device__ __forceinline__ void reuse() {
+        if constexpr (BULK) {
+            __syncwarp();
+            issue();
+            if (++stage == kGroups) stage = 0, parity ^= 1;
+        }
+    }
+    // Before the block ends or its ring is used for something else: nothing is on its way any
+    // more unless a wait ran out; then it is waited for once more.
+    __device__ __forceinline__ void drain() {
+        if constexpr (BULK)
+            if (waiter.gone)
+                for (int s = 0; s < kGroups; ++s) tc::mbar_wait(&full[s], parity);
+    }
+    __device__ __forceinline__ void get(int i, int k, typename Lanes<VEC>::V* v) const {
         float f[VEC];
-        if constexpr (S > 0)
-            Slot<T, VEC>::read(at(stage, i, k), tid, threads, f);
-        else
+        if constexpr (BULK) {
+            Pack<T, VEC> p;
+            p.load(reinterpret_cast<const T*>(ring + ((stage * kGroup + i) * N + k) * line) +
+                   threadIdx.x * VEC);
+            p.get(f);
+        } else {
             next[i][k].get(f);
+        }
         to_lanes<VEC>(f, v);
     }
 };
+
+// The channels of a block: of one piece of the split only.
+struct Channels {
+    long long c0;   // first
+    int n;          // how many
+    int piece;
+    long long c;    // this lane's first, or the block's where the lane has none
+    bool on;        // this lane has channels
+};
+template <int VEC>
+__device__ __forceinline__ Channels channels_of(const ConvArgs& a, int cb) {
+    Channels r;
+    r.piece = cb >= a.blk2 ? 2 : cb >= a.blk1 ? 1 : 0;
+    const int first = r.piece == 2 ? a.blk2 : r.piece == 1 ? a.blk1 : 0;
+    const int width = r.piece == 2 ? a.width[2] : r.piece == 1 ? a.width[1] : a.width[0];
+    const int off = (cb - first) * (kLanes * VEC);
+    r.c0 = (r.piece == 2 ? a.off2 : r.piece == 1 ? a.off1 : 0) + off;
+    r.n = width - off < kLanes * VEC ? width - off : kLanes * VEC;
+    r.on = (int)threadIdx.x * VEC < r.n;
+    r.c = r.c0 + (r.on ? threadIdx.x * VEC : 0);
+    return r;
+}
+// Token 0 of a piece's tensor at channel c of it.
+template <typename T>
+__device__ __forceinline__ T* piece_at(const ConvArgs& a, const Channels& ch, long long c, int* stride) {
+    const int k = ch.piece;
+    *stride = k == 2 ? a.width[2] : k == 1 ? a.width[1] : a.width[0];
+    return static_cast<T*>(k == 2 ? a.out[2] : k == 1 ? a.out[1] : a.out[0]) +
+           (c - (k == 2 ? a.off2 : k == 1 ? a.off1 : 0));
+}
 
 template <typename T, int VEC, int K>
 __device__ __forceinline__ void token_lanes(const ConvArgs& a, const Seq& q, long long i, long long c,
@@ -209,16 +302,18 @@ __device__ __forceinline__ void token_lanes(const ConvArgs& a, const Seq& q, lon
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvArgs a, bool silu) {
     using V = typename Lanes<VEC>::V;
-    constexpr int N = Lanes<VEC>::N, S = ring_groups(VEC);
+    constexpr int N = Lanes<VEC>::N;
+    using In = Run<T, VEC, 1>;
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
-    extern __shared__ __align__(16) char ring[];
+    __shared__ RunBars bars;
+    extern __shared__ __align__(128) char ring[];
     const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
-    const long long c0 = (long long)cb * kLanes * VEC;
-    const long long c = c0 + threadIdx.x * VEC;
+    const Channels ch = channels_of<VEC>(a, cb);
+    const long long c = ch.c;
 
     if (rb >= a.nrunblk) {  // the states: one (sequence, row) per thread row
         const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
-        if (c >= a.C || item >= (long long)a.nseq * K) return;
+        if (!ch.on || item >= (long long)a.nseq * K) return;
         const Seq q = seq_at(a, (int)(item / K));
         const int r = (int)(item % K);
         const long long p0 = a.pos ? a.pos[q.s] : 0;
@@ -232,30 +327,28 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
 
     const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
     const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
-    const bool on = c < a.C && t0 < t1;
-    Run<T, VEC, S, 1> in;
-    in.src[0] = static_cast<const T*>(a.u) + c, in.stride[0] = a.us;
-    in.ring = ring, in.tid = threadIdx.y * kLanes + threadIdx.x;
-    if (on)  // on their way before the weights are looked at
-#pragma unroll
-        for (int s = 0; s < (S ? S : 1); ++s) in.load(t0 + s * kGroup, t1, s);
-    stage_weights<VEC, K>(a, c0, ws);
-    if (!on) return;
+    In in;
+    in.begin(t0 < t1 ? (int)(t1 - t0) : 0, ch.n, ring, &bars, a.status);
+    if (t0 < t1 && (In::BULK || ch.on)) {  // on their way before the weights are looked at
+        in.template tensor<0>(static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
+        in.start();
+    }
+    stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
+    if (t0 >= t1 || (!In::BULK && !ch.on)) return;
     V w[K][N], b[N];
     to_lanes<VEC>(&ws[K][threadIdx.x * VEC], b);
 #pragma unroll
     for (int k = 0; k < K; ++k) to_lanes<VEC>(&ws[k][threadIdx.x * VEC], w[k]);
     int ostride;
-    T* out = piece<T>(a, c, &ostride);
+    T* out = piece_at<T>(a, ch, c, &ostride) + t0 * a.width[ch.piece];
 
     Seq q = seq_of(a, t0);
     V win[K - 1][N];  // win[j]: token t - 1 - j
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
 
-    int stage = 0;
-    for (long long t = t0; t < t1; t += kGroup) {
-        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+    for (long long t = t0; t < t1; t += kGroup, out += kGroup * ostride) {
+        in.arrived();
         V cur[kGroup][N];
         auto work = [&](int i) {
             V o[N];
@@ -274,19 +367,19 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
             if (!q.live)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) f[e] = 0.f;
-            store_vec<VEC>(out + (t + i) * ostride, f);
+            if (ch.on) store_vec<VEC>(out + i * ostride, f);
         };
         const bool whole = t + kGroup <= t1 && t + kGroup <= q.end;  // the same for the warp
-        if constexpr (S == 0) {  // the registers are read: the next group takes them
+        if constexpr (!In::BULK) {  // the registers are read: the next group takes them
 #pragma unroll
             for (int i = 0; i < kGroup; ++i)
-                if (whole || t + i < t1) in.get(stage, i, 0, cur[i]);
-            in.load(t + kGroup, t1, stage);
+                if (whole || t + i < t1) in.get(i, 0, cur[i]);
+            in.fetch();
         }
         if (whole) {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-                if constexpr (S > 0) in.get(stage, i, 0, cur[i]);
+                if constexpr (In::BULK) in.get(i, 0, cur[i]);
                 work(i);
             }
         } else {
@@ -298,14 +391,13 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
                 }
-                if constexpr (S > 0) in.get(stage, i, 0, cur[i]);
+                if constexpr (In::BULK) in.get(i, 0, cur[i]);
                 work(i);
             }
         }
-        // this thread's places of the stage are read: the group S rounds on takes them
-        if constexpr (S > 0) in.load(t + S * kGroup, t1, stage);
-        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+        in.reuse();
     }
+    in.drain();
 }
 
 // ------------------------------------------------------------------ backward
@@ -337,7 +429,8 @@ __device__ __forceinline__ void grad_pre(const typename Lanes<VEC>::V (*w)[Lanes
 // row's position p0 - m, and passed through where the row is still in the final state.
 template <typename T, int VEC, int K>
 __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, long long c,
-                                        const float (*ws)[kLanes * VEC], bool silu) {
+                                        const Channels& ch, const float (*ws)[kLanes * VEC],
+                                        bool silu) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     V w[K][N], b[N];
@@ -360,7 +453,7 @@ __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, 
     V d[N];
     to_lanes<VEC>(f, d);
     int dstride;
-    const T* dout = piece<T>(a, c, &dstride);
+    const T* dout = piece_at<T>(a, ch, c, &dstride);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         if (i >= n || i + m >= K) break;
@@ -386,18 +479,20 @@ __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, 
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvArgs a, bool silu) {
     using V = typename Lanes<VEC>::V;
-    constexpr int N = Lanes<VEC>::N, S = ring_groups(VEC);
+    constexpr int N = Lanes<VEC>::N;
+    using In = Run<T, VEC, 2>;
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
-    extern __shared__ __align__(16) char ring[];
+    __shared__ RunBars bars;
+    extern __shared__ __align__(128) char ring[];
     const int cb = blockIdx.x % a.nchblk, rb = blockIdx.x / a.nchblk;
-    const long long c0 = (long long)cb * kLanes * VEC;
-    const long long c = c0 + threadIdx.x * VEC;
+    const Channels ch = channels_of<VEC>(a, cb);
+    const long long c = ch.c;
 
     if (rb >= a.nrunblk) {  // the carried states' gradients
-        stage_weights<VEC, K>(a, c0, ws);
+        stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
         const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
-        if (c < a.C && item < (long long)a.nseq * K)
-            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, ws, silu);
+        if (ch.on && item < (long long)a.nseq * K)
+            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, ch, ws, silu);
         return;
     }
 
@@ -405,17 +500,17 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
     const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
     // g of the K-1 tokens after the run reaches back into it
     const long long t2 = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;
-    const bool on = c < a.C && t0 < t1;
-    Run<T, VEC, S, 2> in;
-    in.ring = ring, in.tid = threadIdx.y * kLanes + threadIdx.x;
+    const bool on = t0 < t1 && (In::BULK || ch.on);
+    In in;
+    in.begin(t0 < t1 ? (int)(t2 - t0) : 0, ch.n, ring, &bars, a.status);
     if (on) {
         int dstride;
-        in.src[0] = static_cast<const T*>(a.u) + c, in.stride[0] = a.us;
-        in.src[1] = piece<T>(a, c, &dstride), in.stride[1] = dstride;
-#pragma unroll
-        for (int s = 0; s < (S ? S : 1); ++s) in.load(t0 + s * kGroup, t2, s);
+        const T* dout = piece_at<T>(a, ch, ch.c0, &dstride);
+        in.template tensor<0>(static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
+        in.template tensor<1>(dout + t0 * dstride, dstride);
+        in.start();
     }
-    stage_weights<VEC, K>(a, c0, ws);
+    stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
     V dw[K + 1][N];
 #pragma unroll
     for (int k = 0; k <= K; ++k)
@@ -438,9 +533,8 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[j][e] = both<V>(0.f);
 
-        int stage = 0;
         for (long long t = t0; t < t2; t += kGroup) {
-            if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
+            in.arrived();
             V cur[kGroup][N], dy[kGroup][N], g[N];
             auto sums = [&](int i) {
 #pragma unroll
@@ -463,26 +557,26 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
             auto emit = [&](long long tok, const V* v) {
                 float f[VEC];
                 from_lanes<VEC>(v, f);
-                store_vec<VEC>(du + tok * a.dus, f);
+                if (ch.on) store_vec<VEC>(du + tok * a.dus, f);
             };
             // a whole group inside the run, and no end or beginning of a sequence in reach;
             // the same for the warp
             const bool whole = t >= t0 + K - 1 && t + kGroup <= t1 && q.live &&
                                t >= q.start + K - 1 && t + kGroup + K <= q.end;
             auto read = [&](int i) {
-                in.get(stage, i, 0, cur[i]);
-                in.get(stage, i, 1, dy[i]);
+                in.get(i, 0, cur[i]);
+                in.get(i, 1, dy[i]);
             };
-            if constexpr (S == 0) {  // the registers are read: the next group takes them
+            if constexpr (!In::BULK) {  // the registers are read: the next group takes them
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i)
                     if (whole || t + i < t2) read(i);
-                in.load(t + kGroup, t2, stage);
+                in.fetch();
             }
             if (whole) {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    if constexpr (S > 0) read(i);
+                    if constexpr (In::BULK) read(i);
                     grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
                     sums(i);
 #pragma unroll
@@ -506,7 +600,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
                         for (int j = 0; j < K - 1; ++j)
                             token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
                     }
-                    if constexpr (S > 0) read(i);
+                    if constexpr (In::BULK) read(i);
                     grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
                     if (!q.live)
 #pragma unroll
@@ -539,15 +633,13 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
                     shift(i);
                 }
             }
-            // this thread's places of the stage are read: the group S rounds on takes them
-            if constexpr (S > 0) in.load(t + S * kGroup, t2, stage);
-            if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+            in.reuse();
         }
         // the last tokens of the run that nothing later reads
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             const long long tok = t2 - 1 - j;
-            if (tok >= t0 && tok < t1) {
+            if (ch.on && tok >= t0 && tok < t1) {
                 float f[VEC];
                 from_lanes<VEC>(acc[j], f);
                 store_vec<VEC>(du + tok * a.dus, f);
@@ -556,7 +648,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
     }
 
     // one partial per block, weight and channel: the runs are added in order, in the ring's place
-    if constexpr (S > 0) cp_async_wait<0>();
+    in.drain();
     float* red = reinterpret_cast<float*>(ring);
     __syncthreads();
 #pragma unroll
@@ -568,15 +660,14 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
             red[((threadIdx.y * (K + 1) + k) * VEC + e) * kLanes + threadIdx.x] = f[e];
     }
     __syncthreads();
-    for (int i = in.tid; i < (K + 1) * kLanes * VEC; i += kLanes * kRuns) {
+    for (int i = threadIdx.y * kLanes + threadIdx.x; i < (K + 1) * kLanes * VEC; i += kLanes * kRuns) {
         const int k = i / (kLanes * VEC), x = i - k * kLanes * VEC;
-        const long long ch = c0 + x;
-        if (ch >= a.C) continue;
+        if (x >= ch.n) continue;
         const int at = (k * VEC + x % VEC) * kLanes + x / VEC;
         float s = 0.f;
 #pragma unroll
         for (int y = 0; y < kRuns; ++y) s += red[y * (K + 1) * VEC * kLanes + at];
-        a.partial[((long long)rb * (K + 1) + k) * a.C + ch] = s;
+        a.partial[((long long)rb * (K + 1) + k) * a.C + ch.c0 + x] = s;
     }
 }
 
@@ -612,21 +703,19 @@ ssd_status_t check_conv(const ssd_conv_t* p, Conv* c) {
     return SSD_OK;
 }
 
-// Channels of a vector: 16 bytes (8 in a bf16 backward, whose sums take the registers) where
-// every row of every tensor and every piece starts on such a boundary, else a half of it, a
-// quarter, ... down to one channel.
+// Channels of a vector: `most` where every row of every tensor and every piece starts on 16
+// bytes (and tokens move in bulk copies), else two or one.
 int conv_vec(const ssd_conv_t* p, const Conv& c, int most, const void* const* ptrs, int np) {
     const long long strides[5] = {p->split[0], p->split[1], p->split[2], p->u_stride, p->du_stride};
-    for (int vec = most; vec > 1; vec >>= 1) {
-        bool ok = true;
-        for (long long s : strides) ok = ok && s % vec == 0;
-        for (int i = 0; i < np; ++i) ok = ok && aligned_to(ptrs[i], vec * c.e);
-        if (ok) return vec;
-    }
-    return 1;
+    const int n = (int)(16 / c.e);
+    bool wide = true, pairs = true;
+    for (long long s : strides) wide = wide && s % n == 0, pairs = pairs && s % 2 == 0;
+    for (int i = 0; i < np; ++i)
+        wide = wide && aligned_to(ptrs[i], 16), pairs = pairs && aligned_to(ptrs[i], 2 * c.e);
+    return wide ? most : pairs ? 2 : 1;
 }
 int most_fwd(const Conv& c) { return c.e == 2 ? 8 : 4; }
-constexpr int kMostBwd = 4;
+constexpr int kMostBwd = 4;  // 8 bytes of bf16: the sums take the registers of a wider vector
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -648,16 +737,19 @@ int bwd_run(long long T, long long C, int vec) {
     return run;
 }
 
-void fill_args(const ssd_conv_t* p, const Conv& c, ConvArgs* a) {
+void fill_args(const ssd_conv_t* p, const Conv& c, int vec, ConvArgs* a) {
     a->T = c.T;
     a->L = p->seqlen;
     a->C = c.C;
     a->us = p->u_stride;
     a->dus = p->du_stride;
-    // an absent piece starts at the channel count, where no channel falls into it
-    a->off1 = p->split[1] ? p->split[0] : (int)c.C;
-    a->off2 = p->split[2] ? p->split[0] + p->split[1] : (int)c.C;
+    a->off1 = p->split[0];
+    a->off2 = p->split[0] + p->split[1];
     for (int i = 0; i < 3; ++i) a->width[i] = p->split[i];
+    const int wide = kLanes * vec;
+    a->blk1 = ceil_div(p->split[0], wide);
+    a->blk2 = a->blk1 + ceil_div(p->split[1], wide);
+    a->nchblk = a->blk2 + ceil_div(p->split[2], wide);
     a->nseq = c.nseq;
     a->wbf16 = p->wdtype == SSD_DTYPE_BF16;
 }
@@ -665,7 +757,7 @@ void fill_args(const ssd_conv_t* p, const Conv& c, ConvArgs* a) {
 // Shared memory of a block: the ring, or in the backward the runs' sums at the end.
 template <typename T, int VEC, int K>
 constexpr size_t conv_smem(bool bwd) {
-    const size_t ring = (size_t)ring_groups(VEC) * kGroup * kLanes * kRuns * VEC * sizeof(T) * (bwd ? 2 : 1);
+    const size_t ring = VEC >= 4 ? (size_t)kRuns * kGroups * kGroup * (bwd ? 2 : 1) * kLanes * VEC * sizeof(T) : 0;
     const size_t sums = bwd ? sizeof(float) * kRuns * (K + 1) * VEC * kLanes : 0;
     return ring > sums ? ring : sums;
 }
@@ -685,9 +777,8 @@ cudaError_t launch_vec(int K, unsigned grid, const ConvArgs& a, bool silu, cudaS
 }
 template <bool BWD, typename T>
 cudaError_t launch_type(int vec, int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
-    if constexpr (sizeof(T) == 2 && !BWD)
-        if (vec == 8) return launch_vec<BWD, T, 8>(K, grid, a, silu, s);
-    if (vec == 4) return launch_vec<BWD, T, 4>(K, grid, a, silu, s);
+    constexpr int wide = sizeof(T) == 2 && !BWD ? 8 : 4;
+    if (vec == wide) return launch_vec<BWD, T, wide>(K, grid, a, silu, s);
     if (vec == 2) return launch_vec<BWD, T, 2>(K, grid, a, silu, s);
     return launch_vec<BWD, T, 1>(K, grid, a, silu, s);
 }
@@ -742,15 +833,15 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
     }
     if (c.T == 0 && !final_state) return SSD_OK;
 
+    const int vec = conv_vec(conv, c, most_fwd(c), ptrs, 6);
     ConvArgs a = {};
-    fill_args(conv, c, &a);
+    fill_args(conv, c, vec, &a);
+    if (!(a.status = status_word())) return SSD_ERR_CUDA;
     a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
     a.init = initial_state, a.final_state = final_state;
     for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
-    const int vec = conv_vec(conv, c, most_fwd(c), ptrs, 6);
     const long long nvec = c.C / vec;
     a.run = choose_run(c.T, nvec, 32, 1024);
-    a.nchblk = ceil_div(nvec, kLanes);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = final_state ? ceil_div(srows, kRuns) : 0;
     const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);
@@ -771,7 +862,7 @@ ssd_status_t ssd_conv_workspace_size(const ssd_conv_t* conv, size_t* bytes) {
     ssd_status_t st = check_conv(conv, &c);
     if (st != SSD_OK) return st;
     size_t most = 0;
-    for (int vec = kMostBwd; vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
+    for (int vec = kMostBwd; vec >= 1; vec = vec > 2 ? 2 : vec - 1) {  // any may run, by the pointers' alignment
         const int nb = ceil_div(c.T, (long long)bwd_run(c.T, c.C, vec) * kRuns);
         const size_t n = sizeof(float) * (size_t)nb * (conv->width + 1) * c.C;
         if (n > most) most = n;
@@ -824,16 +915,16 @@ ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
 
+    const int vec = conv_vec(conv, c, kMostBwd, ptrs, 8);
     ConvArgs a = {};
-    fill_args(conv, c, &a);
+    fill_args(conv, c, vec, &a);
+    if (!(a.status = status_word())) return SSD_ERR_CUDA;
     a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
     a.init = initial_state, a.dfinal = d_final_state, a.du = du, a.dinit = d_initial_state;
     for (int i = 0; i < 3; ++i) a.out[i] = const_cast<void*>(douts[i]);
     a.partial = static_cast<float*>(workspace);
-    const int vec = conv_vec(conv, c, kMostBwd, ptrs, 8);
     const long long nvec = c.C / vec;
     a.run = bwd_run(c.T, c.C, vec);
-    a.nchblk = ceil_div(nvec, kLanes);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = d_initial_state ? ceil_div(srows, kRuns) : 0;
     const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);

@@ -36,215 +36,211 @@ struct GatedArgs {
     int nw, teams;
     int nrb;       // blocks of a group
     int wbf16;
-    float eps;
+    int stages;
+    int* status;
+    float eps, inv;  // inv: 1 / n
 };
 
-// The N tensors of one row, thread by thread, on their way: through the ring (S stages) or, in
-// single elements (S = 0), through registers one row ahead.
-template <typename T, int VEC, int NV, int S, int N>
-struct Rows {
-    Pack<T, VEC> next[S ? 1 : NV][N];
-    const T* src[N];         // this thread's first element of row 0
-    long long stride[N];
-    char* ring;
-    int thr, nthr;
-    static constexpr int bytes = VEC * (int)sizeof(T);
-    __device__ __forceinline__ char* at(int stage, int i, int k) const {
-        return ring + ((size_t)(stage * NV + i) * N + k) * nthr * bytes;
-    }
-    __device__ __forceinline__ void load(const GatedArgs& a, const Team& t, long long row, int stage) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (row < a.rows && c < a.n)
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const T* p = src[k] + row * stride[k] + c;
-                    if constexpr (S > 0)
-                        Slot<T, VEC>::copy(at(stage, i, k), thr, nthr, p);
-                    else
-                        next[i][k].load(p);
-                }
-        }
-        if constexpr (S > 0) cp_async_commit();
-    }
-    __device__ __forceinline__ void get(int stage, int i, int k, float* f) const {
-        if constexpr (S > 0)
-            Slot<T, VEC>::read(at(stage, i, k), thr, nthr, f);
-        else
-            next[i][k].get(f);
-    }
-};
-
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) gated_fwd_kernel(const GatedArgs a) {
-    constexpr int S = ring_stages(VEC, NV);
-    __shared__ float buf[2][32];
-    extern __shared__ __align__(16) char ring[];
-    const Team t = team_of(a.nw);
-    const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
-    const int g0 = g * a.n;
-    float w[NV][VEC];
+template <int VEC, int NV>
+__device__ __forceinline__ void weights_of(const GatedArgs& a, const Team& t, int g0,
+                                           typename Lanes<VEC>::V (*v)[Lanes<VEC>::N]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.n) params<VEC>(a.w, g0 + c, a.wbf16, w[i]);
-    }
-    const long long step = (long long)a.nrb * a.teams;
-    long long row = (long long)rb * a.teams + t.id;
-    Rows<T, VEC, NV, S, 2> in;
-    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
-    in.src[0] = static_cast<const T*>(a.y) + g0, in.stride[0] = a.ys;
-    in.src[1] = static_cast<const T*>(a.z) + g0, in.stride[1] = a.zs;
+        const int c = ((t.warp * NV + i) * 32 + t.lane) * VEC;
+        float f[VEC];
 #pragma unroll
-    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
-    int stage = 0, flip = 0;
-    // every team of the block takes the same number of rows (some of them beyond the last)
-    for (long long first = (long long)rb * a.teams; first < a.rows; first += step) {
-        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
-        const bool on = row < a.rows;
-        float v[NV][VEC];
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (on && c < a.n) {
-                float z[VEC];
-                in.get(stage, i, 0, v[i]);
-                in.get(stage, i, 1, z);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[i][e] *= z[e] * sigmoid_of<T>(z[e]);
-                    q = fmaf(v[i][e], v[i][e], q);
-                }
-            }
-        }
-        // this thread's places of the stage are read: the row S rounds on takes them
-        in.load(a, t, row + (S ? S : 1) * step, stage);
-        team_sum<1>(t, &q, buf[flip]);
-        flip ^= 1;
-        const float rstd = 1.f / sqrtf(q / a.n + a.eps);
-        if (on) {
-            if (t.thread == 0 && a.rstd) a.rstd[row * a.G + g] = rstd;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t.thread + i * a.nw * 32) * VEC;
-                if (c >= a.n) continue;
-                float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = v[i][e] * rstd * w[i][e];
-                store_vec<VEC>(static_cast<T*>(a.out) + row * a.os + g0 + c, o);
-            }
-        }
-        row += step;
-        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+        for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+        if (c < a.n) params<VEC>(a.w, g0 + c, a.wbf16, f);
+        to_lanes<VEC>(f, v[i]);
     }
 }
 
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) gated_bwd_kernel(const GatedArgs a) {
-    constexpr int S = ring_stages(VEC, NV);
-    __shared__ float buf[2][32];
-    extern __shared__ __align__(16) char ring[];
+__global__ void __maxnreg__(row_regs(VEC, NV, false)) gated_fwd_kernel(const GatedArgs a) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
+    __shared__ TeamBuf<1> buf;
+    extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
-    float w[NV][VEC], dw[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.n) params<VEC>(a.w, g0 + c, a.wbf16, w[i]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
-    }
     const long long step = (long long)a.nrb * a.teams;
-    long long row = (long long)rb * a.teams + t.id;
-    Rows<T, VEC, NV, S, 3> in;
-    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
-    in.src[0] = static_cast<const T*>(a.dout) + g0, in.stride[0] = a.os;
-    in.src[1] = static_cast<const T*>(a.y) + g0, in.stride[1] = a.ys;
-    in.src[2] = static_cast<const T*>(a.z) + g0, in.stride[2] = a.zs;
+    const long long row = (long long)rb * a.teams + t.id;
+    using In = Rows<T, T, 2, 0, VEC, NV>;
+    In in;
+    __shared__ RowBars bars;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    const int rounds = rows_of((long long)rb * a.teams, step, a.rows);
+    int mine = rows_of(row, step, a.rows);
+    in.begin(t, mine, a.n, a.stages, ring, &bars, a.status);
+    in.template a<0>(t, a.y, row, step, a.ys, g0);
+    in.template a<1>(t, a.z, row, step, a.zs, g0);
+    buf.clear();  // and its barrier
+    in.start();
+    V w[NV][N];
+    weights_of<VEC, NV>(a, t, g0, w);
+    T* out = static_cast<T*>(a.out) + row * a.os + g0 + In::column(t, 0);
+    const long long ostep = step * a.os, sstep = step * a.G;
+    float* stats = a.rstd ? a.rstd + row * a.G + g : nullptr;
+    const float inv = a.inv, eps = a.eps;
+    int flip = 0;
+    for (int round = 0; round < rounds; ++round, --mine) {
+        const bool on = mine > 0;
+        if (on) in.arrived();
+        V v[NV][N];
+        V q = both<V>(0.f);
 #pragma unroll
-    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
-    float next = row < a.rows ? a.rstd_in[row * a.G + g] : 0.f;
-    int stage = 0, flip = 0;
-    // every team of the block takes the same number of rows (some of them beyond the last)
-    for (long long first = (long long)rb * a.teams; first < a.rows; first += step) {
-        const float rstd = next;
-        next = row + step < a.rows ? a.rstd_in[(row + step) * a.G + g] : 0.f;
-        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
-        const bool on = row < a.rows;
-        // d = w dout, gate = silu(z), gy = y silu'(z)
-        float d[NV][VEC], xh[NV][VEC], gate[NV][VEC], gy[NV][VEC];
-        float sum = 0.f;
+        for (int i = 0; i < NV; ++i)
+            if (on && in.in[i]) {
+                V z[N];
+                in.get_a(t, i, 0, v[i]);
+                in.get_a(t, i, 1, z);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (on && c < a.n) {
-                float y[VEC], z[VEC];
-                in.get(stage, i, 0, d[i]);
-                in.get(stage, i, 1, y);
-                in.get(stage, i, 2, z);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float s = sigmoid_of<T>(z[e]);
-                    gate[i][e] = z[e] * s;
-                    gy[i][e] = y[e] * fmaf(gate[i][e], 1.f - s, s);
-                    xh[i][e] = y[e] * gate[i][e] * rstd;
-                    dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
-                    d[i][e] *= w[i][e];
-                    sum = fmaf(d[i][e], xh[i][e], sum);
+                for (int e = 0; e < N; ++e) {
+                    v[i][e] = mul_(v[i][e], mul_(z[e], sigmoid_lanes<T>(z[e])));
+                    q = fma_(v[i][e], v[i][e], q);
                 }
             }
-        }
-        // this thread's places of the stage are read: the row S rounds on takes them
-        in.load(a, t, row + (S ? S : 1) * step, stage);
-        team_sum<1>(t, &sum, buf[flip]);
+        in.done();
+        float sum = lane_sum(q);
+        team_sum<1>(t, &sum, buf, flip);
         flip ^= 1;
-        const float c2 = sum / a.n;
+        in.reuse(t);
+        const float rstd = __frsqrt_rn(fmaf(sum, inv, eps));
         if (on) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t.thread + i * a.nw * 32) * VEC;
-                if (c >= a.n) continue;
-                float oy[VEC], oz[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float dv = (d[i][e] - xh[i][e] * c2) * rstd;
-                    oy[e] = dv * gate[i][e];
-                    oz[e] = dv * gy[i][e];
-                }
-                store_vec<VEC>(static_cast<T*>(a.dy) + row * a.dys + g0 + c, oy);
-                store_vec<VEC>(static_cast<T*>(a.dz) + row * a.dzs + g0 + c, oz);
+            if (stats) {
+                if (t.rank == 0) *stats = rstd;
+                stats += sstep;
             }
+            const V r = both<V>(rstd);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in.in[i]) {
+                    V o[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) o[e] = mul_(mul_(v[i][e], r), w[i][e]);
+                    store_lanes<VEC>(out + i * 32 * VEC, o);
+                }
         }
-        row += step;
-        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+        out += ostep;
+    }
+    in.drain();
+}
+
+template <typename T, int VEC, int NV>
+__global__ void __maxnreg__(row_regs(VEC, NV, true)) gated_bwd_kernel(const GatedArgs a) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
+    __shared__ TeamBuf<1> buf;
+    extern __shared__ __align__(128) char ring[];
+    const Team t = team_of(a.nw);
+    const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
+    const int g0 = g * a.n;
+    const long long step = (long long)a.nrb * a.teams;
+    const long long row = (long long)rb * a.teams + t.id;
+    using In = Rows<T, T, 3, 0, VEC, NV>;
+    In in;
+    __shared__ RowBars bars;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    const int rounds = rows_of((long long)rb * a.teams, step, a.rows);
+    int mine = rows_of(row, step, a.rows);
+    in.begin(t, mine, a.n, a.stages, ring, &bars, a.status);
+    in.template a<0>(t, a.dout, row, step, a.os, g0);
+    in.template a<1>(t, a.y, row, step, a.ys, g0);
+    in.template a<2>(t, a.z, row, step, a.zs, g0);
+    buf.clear();  // and its barrier
+    in.start();
+    V w[NV][N], dw[NV][N];
+    weights_of<VEC, NV>(a, t, g0, w);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[i][e] = both<V>(0.f);
+    T* dy = static_cast<T*>(a.dy) + row * a.dys + g0 + In::column(t, 0);
+    T* dz = static_cast<T*>(a.dz) + row * a.dzs + g0 + In::column(t, 0);
+    const long long ystep = step * a.dys, zstep = step * a.dzs, sstep = step * a.G;
+    const float* stats = a.rstd_in + row * a.G + g;
+    const float inv = a.inv;
+    float next = mine > 0 ? *stats : 0.f;
+    int flip = 0;
+    const V one = both<V>(1.f), minus = both<V>(-1.f);
+    for (int round = 0; round < rounds; ++round, --mine) {
+        const V r = both<V>(next);
+        stats += sstep;
+        if (mine > 1) next = *stats;
+        const bool on = mine > 0;
+        if (on) in.arrived();
+        // d = w dout, gate = silu(z), gy = y silu'(z)
+        V d[NV][N], xh[NV][N], gate[NV][N], gy[NV][N];
+        V s = both<V>(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (on && in.in[i]) {
+                V y[N], z[N];
+                in.get_a(t, i, 0, d[i]);
+                in.get_a(t, i, 1, y);
+                in.get_a(t, i, 2, z);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const V sg = sigmoid_lanes<T>(z[e]);
+                    gate[i][e] = mul_(z[e], sg);
+                    gy[i][e] = mul_(y[e], fma_(gate[i][e], fma_(sg, minus, one), sg));
+                    xh[i][e] = mul_(mul_(y[e], gate[i][e]), r);
+                    dw[i][e] = fma_(d[i][e], xh[i][e], dw[i][e]);
+                    d[i][e] = mul_(d[i][e], w[i][e]);
+                    s = fma_(d[i][e], xh[i][e], s);
+                }
+            }
+        in.done();
+        float sum = lane_sum(s);
+        team_sum<1>(t, &sum, buf, flip);
+        flip ^= 1;
+        in.reuse(t);
+        if (on) {
+            const V c2 = both<V>(-sum * inv);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in.in[i]) {
+                    V oy[N], oz[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const V dv = mul_(fma_(xh[i][e], c2, d[i][e]), r);
+                        oy[e] = mul_(dv, gate[i][e]);
+                        oz[e] = mul_(dv, gy[i][e]);
+                    }
+                    store_lanes<VEC>(dy + i * 32 * VEC, oy);
+                    store_lanes<VEC>(dz + i * 32 * VEC, oz);
+                }
+        }
+        dy += ystep;
+        dz += zstep;
     }
     float* part = a.partial + (long long)rb * a.D + g0;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
-        if constexpr (S > 0) cp_async_wait<0>();
+        in.drain();
         float* acc = reinterpret_cast<float*>(ring);
         __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
             if (t.id == k)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (t.thread + i * a.nw * 32) * VEC;
+                    const int c = In::column(t, i);
                     if (c >= a.n) continue;
+                    float f[VEC];
+                    from_lanes<VEC>(dw[i], f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        acc[c + e] = k == 0 ? dw[i][e] : acc[c + e] + dw[i][e];
+                    for (int e = 0; e < VEC; ++e) acc[c + e] = k == 0 ? f[e] : acc[c + e] + f[e];
                 }
             __syncthreads();
         }
         for (int i = threadIdx.x; i < a.n; i += blockDim.x) part[i] = acc[i];
         return;
     }
+    in.drain();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.n) store_vec<VEC>(part + c, dw[i]);
+        const int c = In::column(t, i);
+        if (c < a.n) store_lanes<VEC>(part + c, dw[i]);
     }
 }
 
@@ -261,7 +257,8 @@ ssd_status_t check_gated(const ssd_gated_norm_t* p) {
     return SSD_OK;
 }
 
-constexpr int kFwdRegs[2] = {32, 4}, kBwdRegs[2] = {40, 7};
+RowCost fwd_cost(const ssd_gated_norm_t* p) { return {false, 2, (int)dtype_size(p->dtype), 0, 0}; }
+RowCost bwd_cost(const ssd_gated_norm_t* p) { return {true, 3, (int)dtype_size(p->dtype), 0, 0}; }
 int most_vec(const ssd_gated_norm_t* p) { return p->dtype == SSD_DTYPE_BF16 ? 8 : 4; }
 
 // Blocks of one group.
@@ -277,41 +274,42 @@ size_t bwd_smem(const RowPlan& p, int n) {
     return p.ring > sums ? p.ring : sums;
 }
 
-template <typename T, int VEC, int NV>
-cudaError_t launch_nv(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
-                      cudaStream_t s) {
-    const size_t smem = bwd ? bwd_smem(p, a.n) : p.ring;
-    const cudaError_t e = bwd ? allow_smem<&gated_bwd_kernel<T, VEC, NV>>(smem)
-                              : allow_smem<&gated_fwd_kernel<T, VEC, NV>>(smem);
-    if (e != cudaSuccess) return e;
-    if (bwd)
-        gated_bwd_kernel<T, VEC, NV><<<grid, p.threads(), smem, s>>>(a);
-    else
-        gated_fwd_kernel<T, VEC, NV><<<grid, p.threads(), smem, s>>>(a);
-    return cudaSuccess;
+template <bool BWD, typename T, int VEC, int NV>
+cudaError_t launch_nv(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
+    constexpr auto kernel = [] {
+        if constexpr (BWD)
+            return &gated_bwd_kernel<T, VEC, NV>;
+        else
+            return &gated_fwd_kernel<T, VEC, NV>;
+    }();
+    const size_t smem = BWD ? bwd_smem(p, a.n) : p.ring;
+    const cudaError_t e = allow_smem<kernel>(smem);
+    if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
+    return e;
 }
-template <typename T, int VEC>
-cudaError_t launch_vec(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
-                       cudaStream_t s) {
-    if (p.nv == 1) return launch_nv<T, VEC, 1>(bwd, p, grid, a, s);
-    if (p.nv == 2) return launch_nv<T, VEC, 2>(bwd, p, grid, a, s);
-    if (p.nv == 4) return launch_nv<T, VEC, 4>(bwd, p, grid, a, s);
-    if constexpr (most_vectors(VEC, sizeof(T)) == 8) return launch_nv<T, VEC, 8>(bwd, p, grid, a, s);
+template <bool BWD, typename T, int VEC>
+cudaError_t launch_vec(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
+    switch (p.nv) {
+        case 1: return launch_nv<BWD, T, VEC, 1>(p, grid, a, s);
+        case 2: return launch_nv<BWD, T, VEC, 2>(p, grid, a, s);
+        case 3: return launch_nv<BWD, T, VEC, 3>(p, grid, a, s);
+        case 4: return launch_nv<BWD, T, VEC, 4>(p, grid, a, s);
+    }
+    if constexpr (most_vectors(VEC) == 8) return launch_nv<BWD, T, VEC, 8>(p, grid, a, s);
     return cudaErrorInvalidValue;
 }
-template <typename T>
-cudaError_t launch_type(bool bwd, const RowPlan& p, unsigned grid, const GatedArgs& a,
-                        cudaStream_t s) {
-    if constexpr (sizeof(T) == 2)
-        if (p.vec == 8) return launch_vec<T, 8>(bwd, p, grid, a, s);
-    if (p.vec == 4) return launch_vec<T, 4>(bwd, p, grid, a, s);
-    if (p.vec == 2) return launch_vec<T, 2>(bwd, p, grid, a, s);
-    return launch_vec<T, 1>(bwd, p, grid, a, s);
+template <bool BWD, typename T>
+cudaError_t launch_type(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
+    constexpr int wide = sizeof(T) == 2 ? 8 : 4;
+    if (p.vec == wide) return launch_vec<BWD, T, wide>(p, grid, a, s);
+    if (p.vec == 2) return launch_vec<BWD, T, 2>(p, grid, a, s);
+    return launch_vec<BWD, T, 1>(p, grid, a, s);
 }
-cudaError_t launch_gated(const ssd_gated_norm_t* n, bool bwd, const RowPlan& p, unsigned grid,
+template <bool BWD>
+cudaError_t launch_gated(const ssd_gated_norm_t* n, const RowPlan& p, unsigned grid,
                          const GatedArgs& a, cudaStream_t s) {
-    return n->dtype == SSD_DTYPE_F32 ? launch_type<float>(bwd, p, grid, a, s)
-                                     : launch_type<__nv_bfloat16>(bwd, p, grid, a, s);
+    return n->dtype == SSD_DTYPE_F32 ? launch_type<BWD, float>(p, grid, a, s)
+                                     : launch_type<BWD, __nv_bfloat16>(p, grid, a, s);
 }
 
 void fill_args(const ssd_gated_norm_t* g, const RowPlan& p, GatedArgs* a) {
@@ -319,9 +317,10 @@ void fill_args(const ssd_gated_norm_t* g, const RowPlan& p, GatedArgs* a) {
     a->ys = g->y_stride, a->zs = g->z_stride, a->os = g->out_stride;
     a->dys = g->dy_stride, a->dzs = g->dz_stride;
     a->D = g->dim, a->G = g->groups, a->n = g->dim / g->groups;
-    a->nw = p.nw, a->teams = p.teams;
+    a->nw = p.nw, a->teams = p.teams, a->stages = p.stages;
+    a->status = status_word();
     a->wbf16 = g->wdtype == SSD_DTYPE_BF16;
-    a->eps = g->eps;
+    a->eps = g->eps, a->inv = (float)(1.0 / a->n);
 }
 
 }  // namespace
@@ -358,16 +357,17 @@ ssd_status_t ssd_gated_norm_forward(const ssd_gated_norm_t* norm, const void* y,
                                   norm->out_stride};
     RowPlan p;
     if (!plan_row(norm->dim / norm->groups, common_vec(most_vec(norm), strides, 4, ptrs, sizes, 3),
-                  most_vec(norm), 2 * (int)e, kFwdRegs, &p))
+                  fwd_cost(norm), &p))
         return SSD_ERR_UNSUPPORTED;
     GatedArgs a = {};
     fill_args(norm, p, &a);
+    if (!a.status) return SSD_ERR_CUDA;
     a.y = y, a.z = z, a.w = weight, a.out = out, a.rstd = rstd;
     a.nrb = gated_blocks(n, norm->groups, p);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("gated_norm_fwd");
-    cudaError_t err = launch_gated(norm, false, p, (unsigned)a.nrb * norm->groups, a, L.stream);
+    cudaError_t err = launch_gated<false>(norm, p, (unsigned)a.nrb * norm->groups, a, L.stream);
     const cudaError_t last = L.end();
     if (err == cudaSuccess) err = last;
     set_last_launches(L.count);
@@ -381,10 +381,9 @@ ssd_status_t ssd_gated_norm_workspace_size(const ssd_gated_norm_t* norm, size_t*
     const int n = norm->dim / norm->groups;
     size_t most = 256;
     bool any = false;
-    for (int vec = most_vec(norm); vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
+    for (int vec = most_vec(norm); vec >= 1; vec = vec > 2 ? 2 : vec - 1) {  // any may run, by the pointers' alignment
         RowPlan p;
-        if (n % vec || !plan_row(n, vec, most_vec(norm), 3 * (int)dtype_size(norm->dtype), kBwdRegs, &p))
-            continue;
+        if (n % vec || !plan_row(n, vec, bwd_cost(norm), &p)) continue;
         any = true;
         const size_t b = sizeof(float) * (size_t)gated_blocks(norm->rows, norm->groups, p) * norm->dim;
         if (b > most) most = b;
@@ -437,10 +436,11 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
                                   norm->out_stride, norm->dy_stride, norm->dz_stride};
     RowPlan p;
     if (!plan_row(norm->dim / norm->groups, common_vec(most_vec(norm), strides, 6, ptrs, sizes, 5),
-                  most_vec(norm), 3 * (int)e, kBwdRegs, &p))
+                  bwd_cost(norm), &p))
         return SSD_ERR_UNSUPPORTED;
     GatedArgs a = {};
     fill_args(norm, p, &a);
+    if (!a.status) return SSD_ERR_CUDA;
     a.dout = dout, a.y = y, a.z = z, a.w = weight, a.rstd_in = rstd, a.dy = dy, a.dz = dz;
     a.partial = static_cast<float*>(workspace);
     a.nrb = gated_blocks(n, norm->groups, p);
@@ -450,7 +450,7 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
     cudaError_t err = cudaSuccess;
     if (grid > 0) {
         L.begin("gated_norm_bwd");
-        err = launch_gated(norm, true, p, grid, a, L.stream);
+        err = launch_gated<true>(norm, p, grid, a, L.stream);
         const cudaError_t last = L.end();
         if (err == cudaSuccess) err = last;
     }

@@ -45,277 +45,231 @@ struct NormArgs {
     int layer;     // 0: rms
     int wbf16;
     int nk;        // partial rows: d_weight (and d_bias)
-    float eps;
+    int stages;
+    int* status;
+    float eps, inv;  // inv: 1 / D
 };
 
-// The inputs of one row, thread by thread, on their way: through the ring (S stages) or, in
-// single elements (S = 0), through registers one row ahead.
-template <typename T, typename TR, int VEC, int NV, int S>
-struct FwdRow {
-    Pack<T, VEC> nx[S ? 1 : NV];
-    Pack<TR, VEC> nr[S ? 1 : NV];
-    char* ring;
-    int thr, nthr;
-    static constexpr int xb = VEC * (int)sizeof(T), rb = VEC * (int)sizeof(TR);
-    __device__ __forceinline__ char* at(int stage, int i) const {
-        return ring + (size_t)(stage * NV + i) * nthr * (xb + rb);
-    }
-    __device__ __forceinline__ void load(const NormArgs& a, const Team& t, long long row, int stage) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (row < a.rows && c < a.D) {
-                const T* x = static_cast<const T*>(a.x) + row * a.xs + c;
-                const TR* r = static_cast<const TR*>(a.res) + row * a.rs + c;
-                if constexpr (S > 0) {
-                    char* p = at(stage, i);
-                    Slot<T, VEC>::copy(p, thr, nthr, x);
-                    if (a.res) Slot<TR, VEC>::copy(p + nthr * xb, thr, nthr, r);
-                } else {
-                    nx[i].load(x);
-                    if (a.res) nr[i].load(r);
-                }
-            }
-        }
-        if constexpr (S > 0) cp_async_commit();
-    }
-    // vector i of x and (res) of the residual
-    __device__ __forceinline__ void get(int stage, int i, bool res, float* x, float* r) const {
-        if constexpr (S > 0) {
-            const char* p = at(stage, i);
-            Slot<T, VEC>::read(p, thr, nthr, x);
-            if (res) Slot<TR, VEC>::read(p + nthr * xb, thr, nthr, r);
-        } else {
-            nx[i].get(x);
-            if (res) nr[i].get(r);
-        }
-    }
-};
-
-template <typename T, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) norm_fwd_kernel(const NormArgs a) {
-    constexpr int S = ring_stages(VEC, NV);
-    __shared__ float buf[2][32];
-    extern __shared__ __align__(16) char ring[];
-    const Team t = team_of(a.nw);
-    float w[NV][VEC], b[NV][VEC];
+// This thread's parameters of its columns (zero beyond the row).
+template <int VEC, int NV>
+__device__ __forceinline__ void columns_of(const void* p, const Team& t, int cols, int bf16,
+                                           typename Lanes<VEC>::V (*v)[Lanes<VEC>::N]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.D) {
-            params<VEC>(a.w, c, a.wbf16, w[i]);
-            if (a.b) params<VEC>(a.b, c, a.wbf16, b[i]);
-        }
-        if (c >= a.D || !a.b)
+        const int c = ((t.warp * NV + i) * 32 + t.lane) * VEC;
+        float f[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) b[i][e] = 0.f;
-    }
-    const long long step = (long long)gridDim.x * a.teams;
-    long long row = (long long)blockIdx.x * a.teams + t.id;
-    FwdRow<T, TR, VEC, NV, S> in;
-    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
-#pragma unroll
-    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
-    int stage = 0, flip = 0;
-    // every team of the block takes the same number of rows (some of them beyond the last)
-    for (long long first = (long long)blockIdx.x * a.teams; first < a.rows; first += step) {
-        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
-        const bool on = row < a.rows;
-        float v[NV][VEC];
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (on && c < a.D) {
-                float r[VEC];
-                in.get(stage, i, a.res != nullptr, v[i], r);
-                if (a.res) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
-                    store_vec<VEC>(static_cast<TR*>(a.h) + row * a.hs + c, v[i]);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s += v[i][e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-            }
-        }
-        // this thread's places of the stage are read: the row S rounds on takes them
-        in.load(a, t, row + (S ? S : 1) * step, stage);
-        float mean = 0.f;
-        if (a.layer) {
-            team_sum<1>(t, &s, buf[0]);
-            mean = s / a.D;
-        }
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (c < a.D)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = v[i][e] - mean;
-                    q = fmaf(d, d, q);
-                }
-        }
-        // rms rows take the two buffers in turn
-        team_sum<1>(t, &q, buf[a.layer ? 1 : flip]);
-        const float rstd = 1.f / sqrtf(q / a.D + a.eps);
-        if (on) {
-            if (t.thread == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t.thread + i * a.nw * 32) * VEC;
-                if (c >= a.D) continue;
-                float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o[e] = fmaf((v[i][e] - mean) * rstd, w[i][e], b[i][e]);
-                store_vec<VEC>(static_cast<T*>(a.y) + row * a.ys + c, o);
-            }
-        }
-        flip ^= 1;
-        row += step;
-        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+        for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+        if (p && c < cols) params<VEC>(p, c, bf16, f);
+        to_lanes<VEC>(f, v[i]);
     }
 }
 
-// The same for the backward: dy, h and (dh) the residual stream's gradient.
-template <typename T, typename TR, int VEC, int NV, int S>
-struct BwdRow {
-    Pack<T, VEC> ndy[S ? 1 : NV];
-    Pack<TR, VEC> nh[S ? 1 : NV], ndh[S ? 1 : NV];
-    char* ring;
-    int thr, nthr;
-    static constexpr int db = VEC * (int)sizeof(T), hb = VEC * (int)sizeof(TR);
-    __device__ __forceinline__ char* at(int stage, int i) const {
-        return ring + (size_t)(stage * NV + i) * nthr * (db + 2 * hb);
-    }
-    __device__ __forceinline__ void load(const NormArgs& a, const Team& t, long long row, int stage) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (row < a.rows && c < a.D) {
-                const T* dy = static_cast<const T*>(a.dy) + row * a.ys + c;
-                const TR* h = static_cast<const TR*>(a.hin) + row * a.hs + c;
-                const TR* dh = static_cast<const TR*>(a.dh) + row * a.rs + c;
-                if constexpr (S > 0) {
-                    char* p = at(stage, i);
-                    Slot<T, VEC>::copy(p, thr, nthr, dy);
-                    Slot<TR, VEC>::copy(p + nthr * db, thr, nthr, h);
-                    if (a.dh) Slot<TR, VEC>::copy(p + nthr * (db + hb), thr, nthr, dh);
-                } else {
-                    ndy[i].load(dy);
-                    nh[i].load(h);
-                    if (a.dh) ndh[i].load(dh);
-                }
-            }
-        }
-        if constexpr (S > 0) cp_async_commit();
-    }
-    __device__ __forceinline__ void get(int stage, int i, float* dy, float* h) const {
-        if constexpr (S > 0) {
-            Slot<T, VEC>::read(at(stage, i), thr, nthr, dy);
-            Slot<TR, VEC>::read(at(stage, i) + nthr * db, thr, nthr, h);
-        } else {
-            ndy[i].get(dy);
-            nh[i].get(h);
-        }
-    }
-    __device__ __forceinline__ void get_dh(int stage, int i, float* dh) const {
-        if constexpr (S > 0)
-            Slot<TR, VEC>::read(at(stage, i) + nthr * (db + hb), thr, nthr, dh);
-        else
-            ndh[i].get(dh);
-    }
-};
-
-template <typename T, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(team_threads(VEC)) norm_bwd_kernel(const NormArgs a) {
-    constexpr int S = ring_stages(VEC, NV);
-    __shared__ float buf[2][64];
-    extern __shared__ __align__(16) char ring[];
+// RES: with a residual.
+template <typename T, typename TR, bool RES, int VEC, int NV>
+__global__ void __maxnreg__(row_regs(VEC, NV, false)) norm_fwd_kernel(const NormArgs a) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
+    __shared__ TeamBuf<1> buf;
+    extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw);
-    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
-        if (c < a.D) params<VEC>(a.w, c, a.wbf16, w[i]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
-    }
     const long long step = (long long)gridDim.x * a.teams;
     long long row = (long long)blockIdx.x * a.teams + t.id;
-    BwdRow<T, TR, VEC, NV, S> in;
-    in.ring = ring, in.thr = threadIdx.x, in.nthr = blockDim.x;
-#pragma unroll
-    for (int s = 0; s < (S ? S : 1); ++s) in.load(a, t, row + s * step, s);
-    float2 next = row < a.rows ? a.stats_in[row] : make_float2(0.f, 0.f);
-    int stage = 0, flip = 0;
-    // every team of the block takes the same number of rows (some of them beyond the last)
-    for (long long first = (long long)blockIdx.x * a.teams; first < a.rows; first += step) {
-        const float2 st = next;
-        next = row + step < a.rows ? a.stats_in[row + step] : make_float2(0.f, 0.f);
-        if constexpr (S > 0) cp_async_wait<(S ? S - 1 : 0)>();
-        const bool on = row < a.rows;
-        float xh[NV][VEC], d[NV][VEC], g[NV][VEC];
-        float sum[2] = {0.f, 0.f};
+    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV>;
+    In in;
+    __shared__ RowBars bars;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    const int rounds = rows_of((long long)blockIdx.x * a.teams, step, a.rows);
+    int mine = rows_of(row, step, a.rows);
+    in.begin(t, mine, a.D, a.stages, ring, &bars, a.status);
+    in.template a<0>(t, a.x, row, step, a.xs, 0);
+    if constexpr (RES) in.template b<0>(t, a.res, row, step, a.rs);
+    buf.clear();  // and its barrier
+    in.start();
+    V w[NV][N], b[NV][N];
+    columns_of<VEC, NV>(a.w, t, a.D, a.wbf16, w);
+    columns_of<VEC, NV>(a.b, t, a.D, a.wbf16, b);
+    T* y = static_cast<T*>(a.y) + row * a.ys + In::column(t, 0);
+    TR* h = static_cast<TR*>(a.h) + row * a.hs + In::column(t, 0);
+    const long long ystep = step * a.ys, hstep = step * a.hs;
+    float2* stats = a.stats ? a.stats + row : nullptr;
+    const bool layer = a.layer;
+    const float inv = a.inv, eps = a.eps;
+    int flip = 0;
+    for (int round = 0; round < rounds; ++round, --mine) {
+        const bool on = mine > 0;
+        if (on) in.arrived();
+        V v[NV][N];
+        V s = both<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t.thread + i * a.nw * 32) * VEC;
-            if (on && c < a.D) {
-                in.get(stage, i, d[i], xh[i]);
-                if (a.dh) in.get_dh(stage, i, g[i]);
+            if (on && in.in[i]) {
+                in.get_a(t, i, 0, v[i]);
+                if constexpr (RES) {
+                    V r[N];
+                    in.get_b(t, i, 0, r);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    xh[i][e] = (xh[i][e] - st.x) * st.y;
-                    dw[i][e] = fmaf(d[i][e], xh[i][e], dw[i][e]);
-                    db[i][e] += d[i][e];
-                    d[i][e] *= w[i][e];
-                    sum[0] += d[i][e];
-                    sum[1] = fmaf(d[i][e], xh[i][e], sum[1]);
+                    for (int e = 0; e < N; ++e) v[i][e] = add_(v[i][e], r[e]);
+                    store_lanes<VEC>(h + i * 32 * VEC, v[i]);
                 }
+#pragma unroll
+                for (int e = 0; e < N; ++e) s = add_(s, v[i][e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[i][e] = both<V>(0.f);
             }
         }
-        // this thread's places of the stage are read: the row S rounds on takes them
-        in.load(a, t, row + (S ? S : 1) * step, stage);
-        team_sum<2>(t, sum, buf[flip]);
+        in.done();
+        float mean = 0.f;
+        if (layer) {
+            float m = lane_sum(s);
+            team_sum<1>(t, &m, buf, flip);
+            flip ^= 1;
+            in.reuse(t);
+            mean = m * inv;
+        }
+        const V minus = both<V>(-mean);
+        V q = both<V>(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in.in[i])
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    v[i][e] = add_(v[i][e], minus);
+                    q = fma_(v[i][e], v[i][e], q);
+                }
+        float var = lane_sum(q);
+        team_sum<1>(t, &var, buf, flip);
         flip ^= 1;
-        const float c1 = a.layer ? sum[0] / a.D : 0.f, c2 = sum[1] / a.D;
+        if (!layer) in.reuse(t);
+        const float rstd = __frsqrt_rn(fmaf(var, inv, eps));
         if (on) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t.thread + i * a.nw * 32) * VEC;
-                if (c >= a.D) continue;
-                float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    o[e] = (d[i][e] - c1 - xh[i][e] * c2) * st.y;
-                    if (a.dh) o[e] += g[i][e];
-                }
-                store_vec<VEC>(static_cast<T*>(a.dx) + row * a.xs + c, o);
-                if (a.dres) store_vec<VEC>(static_cast<TR*>(a.dres) + row * a.D + c, o);
+            if (stats) {
+                if (t.rank == 0) *stats = make_float2(mean, rstd);
+                stats += step;
             }
+            const V r = both<V>(rstd);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in.in[i]) {
+                    V o[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) o[e] = fma_(mul_(v[i][e], r), w[i][e], b[i][e]);
+                    store_lanes<VEC>(y + i * 32 * VEC, o);
+                }
         }
-        row += step;
-        if (S > 1) stage = stage + 1 == S ? 0 : stage + 1;
+        y += ystep;
+        h += hstep;
+    }
+    in.drain();
+}
+
+// DH: with the residual stream's gradient.
+template <typename T, typename TR, bool DH, int VEC, int NV>
+__global__ void __maxnreg__(row_regs(VEC, NV, true)) norm_bwd_kernel(const NormArgs a) {
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
+    constexpr bool SAME = sizeof(T) == sizeof(TR);
+    __shared__ TeamBuf<2> buf;
+    extern __shared__ __align__(128) char ring[];
+    const Team t = team_of(a.nw);
+    const long long step = (long long)gridDim.x * a.teams;
+    const long long row = (long long)blockIdx.x * a.teams + t.id;
+    using In = Rows<T, TR, 1, DH ? 2 : 1, VEC, NV>;
+    In in;
+    __shared__ RowBars bars;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    const int rounds = rows_of((long long)blockIdx.x * a.teams, step, a.rows);
+    int mine = rows_of(row, step, a.rows);
+    in.begin(t, mine, a.D, a.stages, ring, &bars, a.status);
+    in.template a<0>(t, a.dy, row, step, a.ys, 0);
+    in.template b<0>(t, a.hin, row, step, a.hs);
+    if constexpr (DH) in.template b<1>(t, a.dh, row, step, a.rs);
+    buf.clear();  // and its barrier
+    in.start();
+    V w[NV][N], dw[NV][N], db[NV][N];
+    columns_of<VEC, NV>(a.w, t, a.D, a.wbf16, w);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = both<V>(0.f);
+    T* dx = static_cast<T*>(a.dx) + row * a.xs + In::column(t, 0);
+    TR* dres = static_cast<TR*>(a.dres) + row * a.D + In::column(t, 0);
+    const long long xstep = step * a.xs, rstep = step * a.D;
+    const float2* stats = a.stats_in + row;
+    const bool both_out = !SAME || a.dres;
+    const float inv = a.inv, inv1 = a.layer ? a.inv : 0.f;
+    float2 next = mine > 0 ? *stats : make_float2(0.f, 0.f);
+    int flip = 0;
+    for (int round = 0; round < rounds; ++round, --mine) {
+        const float2 st = next;
+        stats += step;
+        if (mine > 1) next = *stats;
+        const bool on = mine > 0;
+        if (on) in.arrived();
+        V xh[NV][N], d[NV][N], g[NV][N];
+        V s0 = both<V>(0.f), s1 = both<V>(0.f);
+        const V minus = both<V>(-st.x), r = both<V>(st.y);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (on && in.in[i]) {
+                in.get_a(t, i, 0, d[i]);
+                in.get_b(t, i, 0, xh[i]);
+                if constexpr (DH) in.get_b(t, i, 1, g[i]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    xh[i][e] = mul_(add_(xh[i][e], minus), r);
+                    dw[i][e] = fma_(d[i][e], xh[i][e], dw[i][e]);
+                    db[i][e] = add_(db[i][e], d[i][e]);
+                    d[i][e] = mul_(d[i][e], w[i][e]);
+                    s0 = add_(s0, d[i][e]);
+                    s1 = fma_(d[i][e], xh[i][e], s1);
+                }
+            }
+        in.done();
+        float sum[2] = {lane_sum(s0), lane_sum(s1)};
+        team_sum<2>(t, sum, buf, flip);
+        flip ^= 1;
+        in.reuse(t);
+        if (on) {
+            const V c1 = both<V>(-sum[0] * inv1), c2 = both<V>(-sum[1] * inv);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in.in[i]) {
+                    V o[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const V k = fma_(xh[i][e], c2, add_(d[i][e], c1));
+                        if constexpr (DH)
+                            o[e] = fma_(k, r, g[i][e]);
+                        else
+                            o[e] = mul_(k, r);
+                    }
+                    store_lanes<VEC>(dx + i * 32 * VEC, o);
+                    if (both_out) store_lanes<VEC>(dres + i * 32 * VEC, o);
+                }
+        }
+        dx += xstep;
+        dres += rstep;
     }
     float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
-        if constexpr (S > 0) cp_async_wait<0>();
+        in.drain();
         float* acc = reinterpret_cast<float*>(ring);
         __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
             if (t.id == k)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (t.thread + i * a.nw * 32) * VEC;
+                    const int c = In::column(t, i);
                     if (c >= a.D) continue;
+                    float f[VEC], g[VEC];
+                    from_lanes<VEC>(dw[i], f);
+                    from_lanes<VEC>(db[i], g);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        acc[c + e] = k == 0 ? dw[i][e] : acc[c + e] + dw[i][e];
-                        acc[a.D + c + e] = k == 0 ? db[i][e] : acc[a.D + c + e] + db[i][e];
+                        acc[c + e] = k == 0 ? f[e] : acc[c + e] + f[e];
+                        acc[a.D + c + e] = k == 0 ? g[e] : acc[a.D + c + e] + g[e];
                     }
                 }
             __syncthreads();
@@ -323,12 +277,13 @@ __global__ void __launch_bounds__(team_threads(VEC)) norm_bwd_kernel(const NormA
         for (int i = threadIdx.x; i < a.nk * a.D; i += blockDim.x) part[i] = acc[i];
         return;
     }
+    in.drain();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t.thread + i * a.nw * 32) * VEC;
+        const int c = In::column(t, i);
         if (c >= a.D) continue;
-        store_vec<VEC>(part + c, dw[i]);
-        if (a.nk > 1) store_vec<VEC>(part + a.D + c, db[i]);
+        store_lanes<VEC>(part + c, dw[i]);
+        if (a.nk > 1) store_lanes<VEC>(part + a.D + c, db[i]);
     }
 }
 
@@ -349,69 +304,69 @@ ssd_status_t check_norm(const ssd_norm_t* p) {
     return SSD_OK;
 }
 
-// Bytes of a column that a forward (x, residual) and a backward (dy, h, dh) read.
-int fwd_col(const ssd_norm_t* p) { return (int)(dtype_size(p->dtype) + dtype_size(p->rdtype)); }
-int bwd_col(const ssd_norm_t* p) { return (int)(dtype_size(p->dtype) + 2 * dtype_size(p->rdtype)); }
-constexpr int kFwdRegs[2] = {28, 4}, kBwdRegs[2] = {40, 6};
-int most_vec(const ssd_norm_t* p) { return p->dtype == SSD_DTYPE_BF16 ? 8 : 4; }
-
-int row_vec(const ssd_norm_t* p, const void* const* ptrs, const size_t* sizes, int np) {
-    const long long strides[5] = {p->dim, p->x_stride, p->r_stride, p->h_stride, p->y_stride};
-    return common_vec(most_vec(p), strides, 5, ptrs, sizes, np);
+// Elements of a vector at most: 16 bytes of the widest tensor.  (bf16 rows beside a float32
+// residual in vectors of eight would touch every 32-byte sector of the float32 rows twice, in
+// halves: 298 us instead of 216 for the backward at 32768 x 2560.)
+int most_vec(const ssd_norm_t* p, bool residual) {
+    return p->dtype == SSD_DTYPE_F32 || (residual && p->rdtype == SSD_DTYPE_F32) ? 4 : 8;
 }
-
-// Shared memory of a block: the ring, or the sums of several teams at the end.
-size_t fwd_smem(const RowPlan& p) { return p.ring; }
+RowCost fwd_cost(const ssd_norm_t* p, bool residual) {
+    return {false, 1, (int)dtype_size(p->dtype), residual ? 1 : 0, (int)dtype_size(p->rdtype)};
+}
+RowCost bwd_cost(const ssd_norm_t* p, bool dh) {
+    return {true, 1, (int)dtype_size(p->dtype), dh ? 2 : 1, (int)dtype_size(p->rdtype)};
+}
+// Shared memory of a backward's block: the ring, or the sums of several teams at the end.
 size_t bwd_smem(const RowPlan& p, int dim) {
     const size_t sums = p.teams > 1 ? sizeof(float) * 2 * dim : 0;
     return p.ring > sums ? p.ring : sums;
 }
 
-template <typename T, typename TR, int VEC, int NV>
-cudaError_t launch_fwd_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
-    const cudaError_t e = allow_smem<&norm_fwd_kernel<T, TR, VEC, NV>>(fwd_smem(p));
-    if (e == cudaSuccess)
-        norm_fwd_kernel<T, TR, VEC, NV><<<grid, p.threads(), fwd_smem(p), s>>>(a);
+template <bool BWD, typename T, typename TR, bool OPT, int VEC, int NV>
+cudaError_t launch_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    constexpr auto kernel = [] {
+        if constexpr (BWD)
+            return &norm_bwd_kernel<T, TR, OPT, VEC, NV>;
+        else
+            return &norm_fwd_kernel<T, TR, OPT, VEC, NV>;
+    }();
+    const size_t smem = BWD ? bwd_smem(p, a.D) : p.ring;
+    const cudaError_t e = allow_smem<kernel>(smem);
+    if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
     return e;
 }
-template <typename T, typename TR, int VEC, int NV>
-cudaError_t launch_bwd_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
-    const cudaError_t e = allow_smem<&norm_bwd_kernel<T, TR, VEC, NV>>(bwd_smem(p, a.D));
-    if (e == cudaSuccess)
-        norm_bwd_kernel<T, TR, VEC, NV><<<grid, p.threads(), bwd_smem(p, a.D), s>>>(a);
-    return e;
-}
-template <typename T, typename TR, int VEC>
-cudaError_t launch_vec(bool bwd, const RowPlan& p, unsigned grid, const NormArgs& a,
-                       cudaStream_t s) {
-    if (p.nv == 1)
-        return bwd ? launch_bwd_nv<T, TR, VEC, 1>(p, grid, a, s)
-                   : launch_fwd_nv<T, TR, VEC, 1>(p, grid, a, s);
-    if (p.nv == 2)
-        return bwd ? launch_bwd_nv<T, TR, VEC, 2>(p, grid, a, s)
-                   : launch_fwd_nv<T, TR, VEC, 2>(p, grid, a, s);
-    if (p.nv == 4)
-        return bwd ? launch_bwd_nv<T, TR, VEC, 4>(p, grid, a, s)
-                   : launch_fwd_nv<T, TR, VEC, 4>(p, grid, a, s);
-    if constexpr (most_vectors(VEC, sizeof(T)) == 8)
-        return bwd ? launch_bwd_nv<T, TR, VEC, 8>(p, grid, a, s)
-                   : launch_fwd_nv<T, TR, VEC, 8>(p, grid, a, s);
+template <bool BWD, typename T, typename TR, bool OPT, int VEC>
+cudaError_t launch_vec(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    switch (p.nv) {
+        case 1: return launch_nv<BWD, T, TR, OPT, VEC, 1>(p, grid, a, s);
+        case 2: return launch_nv<BWD, T, TR, OPT, VEC, 2>(p, grid, a, s);
+        case 3: return launch_nv<BWD, T, TR, OPT, VEC, 3>(p, grid, a, s);
+        case 4: return launch_nv<BWD, T, TR, OPT, VEC, 4>(p, grid, a, s);
+    }
+    if constexpr (most_vectors(VEC) == 8) return launch_nv<BWD, T, TR, OPT, VEC, 8>(p, grid, a, s);
     return cudaErrorInvalidValue;
 }
-template <typename T, typename TR>
-cudaError_t launch_types(bool bwd, const RowPlan& p, unsigned grid, const NormArgs& a,
-                         cudaStream_t s) {
-    if constexpr (sizeof(T) == 2)
-        if (p.vec == 8) return launch_vec<T, TR, 8>(bwd, p, grid, a, s);
-    if (p.vec == 4) return launch_vec<T, TR, 4>(bwd, p, grid, a, s);
-    if (p.vec == 2) return launch_vec<T, TR, 2>(bwd, p, grid, a, s);
-    return launch_vec<T, TR, 1>(bwd, p, grid, a, s);
+template <bool BWD, typename T, typename TR, bool OPT>
+cudaError_t launch_types(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    constexpr int wide = sizeof(T) == 2 && sizeof(TR) == 2 ? 8 : 4;
+    if (p.vec == wide) return launch_vec<BWD, T, TR, OPT, wide>(p, grid, a, s);
+    if (p.vec == 2) return launch_vec<BWD, T, TR, OPT, 2>(p, grid, a, s);
+    return launch_vec<BWD, T, TR, OPT, 1>(p, grid, a, s);
 }
-cudaError_t launch_norm(const ssd_norm_t* n, bool bwd, const RowPlan& p, unsigned grid,
+// `opt`: with a residual (forward) or with its gradient (backward).
+template <bool BWD>
+cudaError_t launch_norm(const ssd_norm_t* n, bool opt, const RowPlan& p, unsigned grid,
                         const NormArgs& a, cudaStream_t s) {
-    if (n->dtype == SSD_DTYPE_F32) return launch_types<float, float>(bwd, p, grid, a, s);
-    if (n->rdtype == SSD_DTYPE_F32) return launch_types<__nv_bfloat16, float>(bwd, p, grid, a, s);
-    return launch_types<__nv_bfloat16, __nv_bfloat16>(bwd, p, grid, a, s);
+    using B16 = __nv_bfloat16;
+    const bool mixed = n->dtype == SSD_DTYPE_BF16 && n->rdtype == SSD_DTYPE_F32;
+    if (mixed && opt) return launch_types<BWD, B16, float, true>(p, grid, a, s);
+    if constexpr (BWD)
+        if (mixed) return launch_types<BWD, B16, float, false>(p, grid, a, s);
+    if (n->dtype == SSD_DTYPE_BF16)
+        return opt ? launch_types<BWD, B16, B16, true>(p, grid, a, s)
+                   : launch_types<BWD, B16, B16, false>(p, grid, a, s);
+    return opt ? launch_types<BWD, float, float, true>(p, grid, a, s)
+               : launch_types<BWD, float, float, false>(p, grid, a, s);
 }
 
 }  // namespace
@@ -450,20 +405,24 @@ ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void*
     const void* ptrs[4] = {x, y, residual, h};
     const size_t sizes[4] = {e, e, re, re};
     RowPlan p;
-    if (!plan_row(D, row_vec(norm, ptrs, sizes, 4), most_vec(norm), fwd_col(norm), kFwdRegs, &p))
+    const long long strides[5] = {D, norm->x_stride, norm->r_stride, norm->h_stride, norm->y_stride};
+    const bool opt = residual != nullptr;
+    if (!plan_row(D, common_vec(most_vec(norm, opt), strides, 5, ptrs, sizes, 4), fwd_cost(norm, opt), &p))
         return SSD_ERR_UNSUPPORTED;
     NormArgs a = {};
     a.x = x, a.res = residual, a.w = weight, a.b = bias, a.y = y, a.h = h;
     a.stats = reinterpret_cast<float2*>(stats);
     a.rows = n, a.xs = norm->x_stride, a.rs = norm->r_stride, a.hs = norm->h_stride,
     a.ys = norm->y_stride;
-    a.D = D, a.nw = p.nw, a.teams = p.teams;
+    a.D = D, a.nw = p.nw, a.teams = p.teams, a.stages = p.stages;
+    a.status = status_word();
+    if (!a.status) return SSD_ERR_CUDA;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;
-    a.eps = norm->eps;
+    a.eps = norm->eps, a.inv = (float)(1.0 / D);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("norm_fwd");
-    cudaError_t err = launch_norm(norm, false, p, (unsigned)team_blocks(n, p), a, L.stream);
+    cudaError_t err = launch_norm<false>(norm, opt, p, (unsigned)team_blocks(n, p), a, L.stream);
     const cudaError_t last = L.end();
     if (err == cudaSuccess) err = last;
     set_last_launches(L.count);
@@ -476,9 +435,10 @@ ssd_status_t ssd_norm_workspace_size(const ssd_norm_t* norm, size_t* bytes) {
     if (st != SSD_OK) return st;
     size_t most = 256;
     bool any = false;
-    for (int vec = most_vec(norm); vec >= 1; vec >>= 1) {  // any may run, by the pointers' alignment
+    for (int i = 0; i < 6; ++i) {  // any may run, by the pointers' alignment and with dh or without
+        const int vec = i < 2 ? most_vec(norm, true) : i < 4 ? 2 : 1;
         RowPlan p;
-        if (norm->dim % vec || !plan_row(norm->dim, vec, most_vec(norm), bwd_col(norm), kBwdRegs, &p)) continue;
+        if (norm->dim % vec || !plan_row(norm->dim, vec, bwd_cost(norm, i & 1), &p)) continue;
         any = true;
         const size_t n = sizeof(float) * (size_t)team_blocks(norm->rows, p) * 2 * norm->dim;
         if (n > most) most = n;
@@ -523,7 +483,8 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     const void* ptrs[5] = {dy, dx, h, dh, d_residual};
     const size_t sizes[5] = {e, e, re, re, re};
     RowPlan p;
-    if (!plan_row(D, row_vec(norm, ptrs, sizes, 5), most_vec(norm), bwd_col(norm), kBwdRegs, &p))
+    const long long strides[5] = {D, norm->x_stride, norm->r_stride, norm->h_stride, norm->y_stride};
+    if (!plan_row(D, common_vec(most_vec(norm, true), strides, 5, ptrs, sizes, 5), bwd_cost(norm, dh), &p))
         return SSD_ERR_UNSUPPORTED;
     NormArgs a = {};
     a.dy = dy, a.hin = h, a.dh = dh, a.w = weight, a.dx = dx, a.dres = d_residual;
@@ -531,16 +492,19 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     a.partial = static_cast<float*>(workspace);
     a.rows = n, a.xs = norm->x_stride, a.rs = norm->r_stride, a.hs = norm->h_stride,
     a.ys = norm->y_stride;
-    a.D = D, a.nw = p.nw, a.teams = p.teams;
+    a.D = D, a.nw = p.nw, a.teams = p.teams, a.stages = p.stages;
+    a.status = status_word();
+    if (!a.status) return SSD_ERR_CUDA;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;
     a.nk = d_bias ? 2 : 1;
+    a.inv = (float)(1.0 / D);
     const int blocks = team_blocks(n, p);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
     if (blocks > 0) {
         L.begin("norm_bwd");
-        err = launch_norm(norm, true, p, (unsigned)blocks, a, L.stream);
+        err = launch_norm<true>(norm, dh != nullptr, p, (unsigned)blocks, a, L.stream);
         const cudaError_t last = L.end();
         if (err == cudaSuccess) err = last;
     }
