@@ -122,17 +122,16 @@ struct Pack<__nv_bfloat16, 2> {
 // Waits for phase `parity` of a copy's barrier.  The wait is bounded (2 s); one that runs out
 // records SSD_ERR_TIMEOUT and lets every later wait of the thread pass at once, so that a lost
 // copy ends in a status and wrong values, not in a hang.
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* status) {
+    if (tc::mbar_wait(bar, parity)) return false;
+    atomicCAS(status, 0, (int)SSD_ERR_TIMEOUT);
+    return true;
+}
 struct Waiter {
     int* status;
     bool gone = false;
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (tc::mbar_try_wait(bar, parity)) return;
-        slow(bar, parity);
-    }
-    __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) {
-        if (gone || tc::mbar_wait(bar, parity)) return;
-        gone = true;
-        atomicCAS(status, 0, (int)SSD_ERR_TIMEOUT);
+        if (!tc::mbar_try_wait(bar, parity) && !gone) gone = wait_long(bar, parity, status);
     }
 };
 

@@ -115,7 +115,7 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     p->vec = vec;
     const int nvec = (dim + vec - 1) / vec;
     // elements a thread holds at most, as long as a block then has threads enough for the row
-    const int hold = vec == 1 ? 4 : cost.bwd ? 8 : 16;
+    const int hold = vec == 1 ? 4 : cost.bwd ? 8 : 32;
     // A warp spends about as long on a row's sums and addresses as on ten elements a lane, so
     // the cheapest plan has few warps with many elements each, none of them idle.
     long long best = -1;
