@@ -220,6 +220,12 @@ __device__ __forceinline__ F2 add_(F2 a, F2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
+__device__ __forceinline__ F2 sub_(F2 a, F2 b) {
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float sub_(float a, float b) { return a - b; }
 __device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
 __device__ __forceinline__ float mul_(float a, float b) { return a * b; }
 __device__ __forceinline__ float add_(float a, float b) { return a + b; }
@@ -248,18 +254,8 @@ __device__ __forceinline__ void from_lanes(const typename Lanes<VEC>::V* v, floa
 template <typename T>
 __device__ __forceinline__ F2 sigmoid_lanes(F2 v) {
     float f[2];
-    if constexpr (sizeof(T) == 4) {
-        split(v, f);
-        return join(sigmoid_of<T>(f[0]), sigmoid_of<T>(f[1]));
-    } else {  // sigmoid_of<T> on both, the multiply and the add paired
-        split(mul_(v, both<F2>(-1.44269504f)), f);
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f[0]));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f[1]));
-        split(add_(join(f[0], f[1]), both<F2>(1.f)), f);
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f[0]));
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f[1]));
-        return join(f[0], f[1]);
-    }
+    split(v, f);
+    return join(sigmoid_of<T>(f[0]), sigmoid_of<T>(f[1]));
 }
 template <typename T>
 __device__ __forceinline__ float sigmoid_lanes(float v) {

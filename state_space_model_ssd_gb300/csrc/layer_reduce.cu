@@ -3,10 +3,11 @@
 // float32 partial sum per weight, and this kernel adds them in a fixed order, so the
 // gradients are bit-identical from run to run (no atomics).
 //
-// A block owns 32 columns; its warps take the partials in turn, eight loads in flight each,
-// then the warp sums are added.  Bound by the latency of the loads; the bytes (nb * nk * C *
-// 4) come from L2, where the kernel before left them.  The launch itself overlaps the end of
-// that kernel; griddepcontrol.wait holds the loads back until it has finished.
+// A block owns 32 vectors of columns (four columns, or one where a row of partials does not
+// start on 16 bytes); its warps take the partials in turn, eight loads in flight each, then
+// the warp sums are added.  Bound by the latency of the loads; the bytes (nb * nk * C * 4) come
+// from L2, where the kernel before left them.  The launch itself overlaps the end of that
+// kernel; griddepcontrol.wait holds the loads back until it has finished.
 #include <atomic>
 
 #include "layer_device.cuh"
@@ -17,38 +18,55 @@ namespace layer {
 
 namespace {
 
-template <int W>
+template <int W, int VEC>
 __global__ void __launch_bounds__(32 * W)
     partial_sum_kernel(const float* partial, int nb, int nk, long long C, ReduceDst d, int bf16) {
-    __shared__ float part[W][32];
+    __shared__ float part[W][VEC][32];
     const long long M = C * nk;
-    const long long m = (long long)blockIdx.x * 32 + threadIdx.x;
+    const long long m = ((long long)blockIdx.x * 32 + threadIdx.x) * VEC;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float s = 0.f;
+    float s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] = 0.f;
     if (m < M) {
-        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int y = threadIdx.y; y < nb; y += 8 * W)
+        const float* p = partial + m;
+        for (int y = threadIdx.y; y < nb; y += 8 * W) {
+            Pack<float, VEC> v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (y + i * W < nb) t[i] += partial[(y + i * W) * M + m];
-        s = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-    }
-    part[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y != 0 || m >= M) return;
+                if (y + i * W < nb)
+                    v[i].load(p + (long long)(y + i * W) * M);
+                else
+                    v[i].zero();
 #pragma unroll
-    for (int i = 1; i < W; ++i) s += part[i][threadIdx.x];
+            for (int i = 0; i < 8; ++i) {
+                float f[VEC];
+                v[i].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s[e] += f[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[threadIdx.y][e][threadIdx.x] = s[e];
+    __syncthreads();
+    // warp e adds column e of the vectors
+    const int e = threadIdx.y;
+    if (e >= VEC || m >= M) return;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) sum += part[i][e][threadIdx.x];
     int k = 0;
-    long long c = m;
+    long long c = m + e;
     while (c >= C) c -= C, ++k;
-    if (d.dst[k]) set_param(d.dst[k], c * d.step[k], s, bf16);
+    if (d.dst[k]) set_param(d.dst[k], c * d.step[k], sum, bf16);
 }
 
-template <int W>
+template <int W, int VEC>
 cudaError_t launch(const float* partial, int nb, int nk, long long C, const ReduceDst& d, int bf16,
                    cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((C * nk + 31) / 32));
+    cfg.gridDim = dim3((unsigned)((C * nk + 32 * VEC - 1) / (32 * VEC)));
     cfg.blockDim = dim3(32, W);
     cfg.stream = stream;
     cudaLaunchAttribute at = {};
@@ -56,7 +74,7 @@ cudaError_t launch(const float* partial, int nb, int nk, long long C, const Redu
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, partial_sum_kernel<W>, partial, nb, nk, C, d, bf16);
+    return cudaLaunchKernelEx(&cfg, partial_sum_kernel<W, VEC>, partial, nb, nk, C, d, bf16);
 }
 
 __device__ int g_status;
@@ -81,10 +99,16 @@ cudaError_t launch_partial_sum(const float* partial, int nb, int nk, long long C
                                const ReduceDst& d, int wdtype, Launch& L) {
     const int bf16 = wdtype == SSD_DTYPE_BF16;
     L.begin("partial_sum");
-    // few partials take few warps, so that a thread has its eight loads to make
-    cudaError_t e = nb <= 64    ? launch<8>(partial, nb, nk, C, d, bf16, L.stream)
-                    : nb <= 256 ? launch<16>(partial, nb, nk, C, d, bf16, L.stream)
-                                : launch<32>(partial, nb, nk, C, d, bf16, L.stream);
+    // few partials take few warps, so that a thread has its eight loads to make; vectors of four
+    // once there are columns enough to fill the GPU with them
+    const bool wide = C * nk % 4 == 0 && C * nk >= 8192;
+    cudaError_t e;
+    if (nb <= 64)
+        e = wide ? launch<8, 4>(partial, nb, nk, C, d, bf16, L.stream)
+                 : launch<8, 1>(partial, nb, nk, C, d, bf16, L.stream);
+    else
+        e = wide ? launch<16, 4>(partial, nb, nk, C, d, bf16, L.stream)
+                 : launch<32, 1>(partial, nb, nk, C, d, bf16, L.stream);
     const cudaError_t last = L.end();
     return e != cudaSuccess ? e : last;
 }

@@ -24,6 +24,7 @@
 #include "layer_device.cuh"
 #include "layer_host.cuh"
 #include "layer_team.cuh"
+#include "tc_common.cuh"
 
 namespace ssd {
 namespace layer {
@@ -58,6 +59,11 @@ struct ConvArgs {
     int nchblk;           // blocks along the channels
     int wbf16;
     int* status;
+};
+
+// Tiles of the tensors that a kernel reads: u, and in the backward the pieces of dout.
+struct ConvMaps {
+    CUtensorMap u, dout[3];
 };
 
 struct Seq {
@@ -111,6 +117,9 @@ __device__ __forceinline__ Seq seq_at(const ConvArgs& a, int s) {
     return q;
 }
 
+// An offset from a run's first token, where it lies in reach of the run.
+__device__ __forceinline__ int near(long long v) { return (int)clampll(v, -(1 << 29), 1 << 29); }
+
 template <int K>
 __device__ __forceinline__ int state_row(long long p) {
     const int r = (int)(p % K);
@@ -146,11 +155,11 @@ __device__ __forceinline__ void stage_weights(const ConvArgs& a, long long c0, i
     __syncthreads();
 }
 
-// The tokens of a warp's run on their way to it, in groups of kGroup: by bulk copies into a
-// ring of kGroups groups in shared memory, a lane a token, or, in vectors of less than 16 bytes,
-// through registers one group ahead.  N tensors, of the block's channels.
-constexpr int kGroup = 4;
-constexpr int kGroups = 3;
+// The tokens of a warp's run on their way to it, in groups of kGroup: as tiles of the block's
+// channels that one lane has copied (TMA) into a ring of kGroups groups in shared memory, or, in
+// vectors of less than 16 bytes, through registers one group ahead.  N tensors.
+constexpr int kGroup = 8;
+constexpr int kGroups = 2;
 struct RunBars {
     uint64_t full[kRuns][kGroups];
 };
@@ -158,24 +167,27 @@ template <typename T, int VEC, int N>
 struct Run {
     static constexpr bool BULK = VEC >= 4;
     static constexpr int line = kLanes * VEC * (int)sizeof(T);  // a token of a tensor in the ring
+    static constexpr int tile = kGroup * line;
     Pack<T, VEC> next[BULK ? 1 : kGroup][N];
-    const T* src[N];  // the next token to load: this lane's of the group, or its channels
+    const T* src[N];  // the next token to load, this lane's channels
     long long stride[N];
+    const CUtensorMap* map[N];
+    int col[N];       // the block's first channel in each map
+    int token;        // the next to load
     int left;         // tokens still to load
-    uint32_t bytes;   // of a token
     char* ring;       // this warp's
     uint64_t* full;
     int fill, stage;
     uint32_t parity;
     Waiter waiter;
 
-    // `tokens` (perhaps none) from t0 on, `channels` of them; every lane of the warp calls it.
-    __device__ __forceinline__ void begin(int tokens, int channels, char* all, RunBars* bars,
+    // `tokens` (perhaps none) from t0 on; every lane of the warp calls it.
+    __device__ __forceinline__ void begin(long long t0, int tokens, char* all, RunBars* bars,
                                           int* status) {
         left = tokens;
         if constexpr (BULK) {
-            bytes = channels * (int)sizeof(T);
-            ring = all + threadIdx.y * (kGroups * kGroup * N * line);
+            token = (int)t0;
+            ring = all + threadIdx.y * (kGroups * N * tile);
             full = bars->full[threadIdx.y];
             fill = stage = 0;
             parity = 0;
@@ -187,11 +199,16 @@ struct Run {
             __syncwarp();
         }
     }
-    // tensor k: its token t0, the block's first channel
+    // tensor k: its map and the block's first channel there, or token t0 at that channel
     template <int K>
-    __device__ __forceinline__ void tensor(const T* p, long long by) {
-        src[K] = p + (BULK ? threadIdx.x * by : threadIdx.x * VEC);
-        stride[K] = by;
+    __device__ __forceinline__ void tensor(const CUtensorMap* m, int c, const T* p, long long by) {
+        if constexpr (BULK) {
+            map[K] = m;
+            col[K] = c;
+        } else {
+            src[K] = p + threadIdx.x * VEC;
+            stride[K] = by;
+        }
     }
     __device__ __forceinline__ void start() {
         if constexpr (BULK) {
@@ -201,22 +218,18 @@ struct Run {
             fetch();
         }
     }
+    // Tiles are whole: tokens beyond the last are zeros, or a neighbour's that is not looked at.
     __device__ __forceinline__ void issue() {
-        if (left > 0) {
-            const int n = left < kGroup ? left : kGroup;
-            uint64_t* bar = &full[fill];
-            if (threadIdx.x == 0) tc::mbar_expect_tx(bar, n * N * bytes);
-            __syncwarp();
-            if ((int)threadIdx.x < n) {
-                char* at = ring + (fill * kGroup + threadIdx.x) * (N * line);
+        if (left <= 0) return;
+        if (threadIdx.x == 0) {
+            tc::mbar_expect_tx(&full[fill], N * tile);
 #pragma unroll
-                for (int k = 0; k < N; ++k) tc::bulk_load(at + k * line, src[k], bytes, bar);
-            }
-#pragma unroll
-            for (int k = 0; k < N; ++k) src[k] += kGroup * stride[k];
-            left -= kGroup;
-            fill = fill + 1 == kGroups ? 0 : fill + 1;
+            for (int k = 0; k < N; ++k)
+                tc::tma_load_2d(ring + (fill * N + k) * tile, map[k], &full[fill], col[k], token);
         }
+        token += kGroup;
+        left -= kGroup;
+        fill = fill + 1 == kGroups ? 0 : fill + 1;
     }
     __device__ __forceinline__ void fetch() {
 #pragma unroll
@@ -250,7 +263,7 @@ struct Run {
         float f[VEC];
         if constexpr (BULK) {
             Pack<T, VEC> p;
-            p.load(reinterpret_cast<const T*>(ring + ((stage * kGroup + i) * N + k) * line) +
+            p.load(reinterpret_cast<const T*>(ring + (stage * N + k) * tile + i * line) +
                    threadIdx.x * VEC);
             p.get(f);
         } else {
@@ -265,6 +278,7 @@ struct Channels {
     long long c0;   // first
     int n;          // how many
     int piece;
+    int off;        // first channel within the piece
     long long c;    // this lane's first, or the block's where the lane has none
     bool on;        // this lane has channels
 };
@@ -274,7 +288,7 @@ __device__ __forceinline__ Channels channels_of(const ConvArgs& a, int cb) {
     r.piece = cb >= a.blk2 ? 2 : cb >= a.blk1 ? 1 : 0;
     const int first = r.piece == 2 ? a.blk2 : r.piece == 1 ? a.blk1 : 0;
     const int width = r.piece == 2 ? a.width[2] : r.piece == 1 ? a.width[1] : a.width[0];
-    const int off = (cb - first) * (kLanes * VEC);
+    const int off = r.off = (cb - first) * (kLanes * VEC);
     r.c0 = (r.piece == 2 ? a.off2 : r.piece == 1 ? a.off1 : 0) + off;
     r.n = width - off < kLanes * VEC ? width - off : kLanes * VEC;
     r.on = (int)threadIdx.x * VEC < r.n;
@@ -299,8 +313,8 @@ __device__ __forceinline__ void token_lanes(const ConvArgs& a, const Seq& q, lon
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvArgs a, bool silu) {
+template <typename T, int VEC, int K, bool SILU>
+__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvArgs a, const __grid_constant__ ConvMaps maps) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     using In = Run<T, VEC, 1>;
@@ -328,9 +342,9 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
     const long long t0 = ((long long)rb * kRuns + threadIdx.y) * a.run;
     const long long t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
     In in;
-    in.begin(t0 < t1 ? (int)(t1 - t0) : 0, ch.n, ring, &bars, a.status);
+    in.begin(t0, t0 < t1 ? (int)(t1 - t0) : 0, ring, &bars, a.status);
     if (t0 < t1 && (In::BULK || ch.on)) {  // on their way before the weights are looked at
-        in.template tensor<0>(static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
+        in.template tensor<0>(&maps.u, (int)ch.c0, static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
         in.start();
     }
     stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
@@ -347,52 +361,55 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, t0 - q.start - 1 - j, c, win[j]);
 
-    for (long long t = t0; t < t1; t += kGroup, out += kGroup * ostride) {
+    const int total = (int)(t1 - t0);
+    int end = near(q.end - t0);  // the sequence's end, from t0
+    for (int n = 0; n < total; n += kGroup, out += kGroup * ostride) {
         in.arrived();
         V cur[kGroup][N];
-        auto work = [&](int i) {
+        auto work = [&](int i, bool live) {
             V o[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 V v = fma_(w[K - 1][e], cur[i][e], b[e]);
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) v = fma_(w[K - 2 - j][e], win[j][e], v);
-                o[e] = silu ? mul_(v, sigmoid_lanes<T>(v)) : v;
+                o[e] = SILU ? mul_(v, sigmoid_lanes<T>(v)) : v;
 #pragma unroll
                 for (int j = K - 2; j > 0; --j) win[j][e] = win[j - 1][e];
                 win[0][e] = cur[i][e];
             }
             float f[VEC];
             from_lanes<VEC>(o, f);
-            if (!q.live)
+            if (!live)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) f[e] = 0.f;
             if (ch.on) store_vec<VEC>(out + i * ostride, f);
         };
-        const bool whole = t + kGroup <= t1 && t + kGroup <= q.end;  // the same for the warp
+        const bool whole = n + kGroup <= total && n + kGroup <= end && q.live;  // the same for the warp
         if constexpr (!In::BULK) {  // the registers are read: the next group takes them
 #pragma unroll
             for (int i = 0; i < kGroup; ++i)
-                if (whole || t + i < t1) in.get(i, 0, cur[i]);
+                if (whole || n + i < total) in.get(i, 0, cur[i]);
             in.fetch();
         }
         if (whole) {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
                 if constexpr (In::BULK) in.get(i, 0, cur[i]);
-                work(i);
+                work(i, true);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-                if (t + i >= t1) break;
-                if (t + i == q.end) {
-                    q = seq_of(a, t + i);
+                if (n + i >= total) break;
+                if (n + i == end) {
+                    q = seq_of(a, t0 + n + i);
+                    end = near(q.end - t0);
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
                 }
                 if constexpr (In::BULK) in.get(i, 0, cur[i]);
-                work(i);
+                work(i, q.live);
             }
         }
         in.reuse();
@@ -402,18 +419,17 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
 
 // ------------------------------------------------------------------ backward
 // g at one token: pre from the current token and its window.
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, bool SILU>
 __device__ __forceinline__ void grad_pre(const typename Lanes<VEC>::V (*w)[Lanes<VEC>::N],
                                          const typename Lanes<VEC>::V* b,
                                          const typename Lanes<VEC>::V* cur,
                                          const typename Lanes<VEC>::V (*win)[Lanes<VEC>::N],
-                                         const typename Lanes<VEC>::V* dy, bool silu,
+                                         const typename Lanes<VEC>::V* dy,
                                          typename Lanes<VEC>::V* g) {
     using V = typename Lanes<VEC>::V;
-    const V one = both<V>(1.f), minus = both<V>(-1.f);
 #pragma unroll
     for (int e = 0; e < Lanes<VEC>::N; ++e) {
-        if (!silu) {
+        if constexpr (!SILU) {
             g[e] = dy[e];
             continue;
         }
@@ -421,16 +437,16 @@ __device__ __forceinline__ void grad_pre(const typename Lanes<VEC>::V (*w)[Lanes
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) v = fma_(w[K - 2 - j][e], win[j][e], v);
         const V s = sigmoid_lanes<T>(v);
-        g[e] = mul_(mul_(dy[e], s), fma_(v, fma_(s, minus, one), one));
+        const V p = mul_(v, s);  // silu' = s + p (1 - s), in a form without constants to hold
+        g[e] = mul_(dy[e], sub_(add_(s, p), mul_(p, s)));
     }
 }
 
 // The carried state's gradient, row r of sequence q: from the first tokens that read the
 // row's position p0 - m, and passed through where the row is still in the final state.
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, bool SILU>
 __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, long long c,
-                                        const Channels& ch, const float (*ws)[kLanes * VEC],
-                                        bool silu) {
+                                        const Channels& ch, const float (*ws)[kLanes * VEC]) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     V w[K][N], b[N];
@@ -465,7 +481,7 @@ __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, 
         v.load(dout + (q.start + i) * dstride);
         v.get(f);
         to_lanes<VEC>(f, dy);
-        grad_pre<T, VEC, K>(w, b, cur, win, dy, silu, g);
+        grad_pre<T, VEC, K, SILU>(w, b, cur, win, dy, g);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (k == K - 1 - (i + m))
@@ -476,8 +492,8 @@ __device__ __noinline__ void state_grad(const ConvArgs& a, const Seq& q, int r, 
     store_vec<VEC>(static_cast<T*>(a.dinit) + at, f);
 }
 
-template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvArgs a, bool silu) {
+template <typename T, int VEC, int K, bool SILU>
+__global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvArgs a, const __grid_constant__ ConvMaps maps) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     using In = Run<T, VEC, 2>;
@@ -492,7 +508,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
         stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
         const long long item = (long long)(rb - a.nrunblk) * kRuns + threadIdx.y;
         if (ch.on && item < (long long)a.nseq * K)
-            state_grad<T, VEC, K>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, ch, ws, silu);
+            state_grad<T, VEC, K, SILU>(a, seq_at(a, (int)(item / K)), (int)(item % K), c, ch, ws);
         return;
     }
 
@@ -502,12 +518,12 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
     const long long t2 = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;
     const bool on = t0 < t1 && (In::BULK || ch.on);
     In in;
-    in.begin(t0 < t1 ? (int)(t2 - t0) : 0, ch.n, ring, &bars, a.status);
+    in.begin(t0, t0 < t1 ? (int)(t2 - t0) : 0, ring, &bars, a.status);
     if (on) {
         int dstride;
         const T* dout = piece_at<T>(a, ch, ch.c0, &dstride);
-        in.template tensor<0>(static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
-        in.template tensor<1>(dout + t0 * dstride, dstride);
+        in.template tensor<0>(&maps.u, (int)ch.c0, static_cast<const T*>(a.u) + t0 * a.us + ch.c0, a.us);
+        in.template tensor<1>(&maps.dout[ch.piece], ch.off, dout + t0 * dstride, dstride);
         in.start();
     }
     stage_weights<VEC, K>(a, ch.c0, ch.n, ws);
@@ -522,7 +538,8 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
         to_lanes<VEC>(&ws[K][threadIdx.x * VEC], b);
 #pragma unroll
         for (int k = 0; k < K; ++k) to_lanes<VEC>(&ws[k][threadIdx.x * VEC], w[k]);
-        T* du = static_cast<T*>(a.du) + c;
+        T* du = static_cast<T*>(a.du) + t0 * a.dus + c;  // token t of the loop below
+        const long long dus = a.dus;
         Seq q = seq_of(a, t0);
         V win[K - 1][N];  // win[j]: token t - 1 - j
         V acc[K][N];      // acc[j]: du of token t - j so far
@@ -533,7 +550,9 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[j][e] = both<V>(0.f);
 
-        for (long long t = t0; t < t2; t += kGroup) {
+        const int mine = (int)(t1 - t0), total = (int)(t2 - t0);
+        int begin = near(q.start - t0), end = near(q.end - t0);  // the sequence, from t0
+        for (int n = 0; n < total; n += kGroup, du += kGroup * dus) {
             in.arrived();
             V cur[kGroup][N], dy[kGroup][N], g[N];
             auto sums = [&](int i) {
@@ -554,15 +573,14 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
                     win[0][e] = cur[i][e];
                 }
             };
-            auto emit = [&](long long tok, const V* v) {
+            auto emit = [&](int i, const V* v) {  // token t0 + n + i
                 float f[VEC];
                 from_lanes<VEC>(v, f);
-                if (ch.on) store_vec<VEC>(du + tok * a.dus, f);
+                if (ch.on) store_vec<VEC>(du + i * dus, f);
             };
-            // a whole group inside the run, and no end or beginning of a sequence in reach;
-            // the same for the warp
-            const bool whole = t >= t0 + K - 1 && t + kGroup <= t1 && q.live &&
-                               t >= q.start + K - 1 && t + kGroup + K <= q.end;
+            // a whole group inside the run, and no end or beginning of a sequence in reach; the
+            // same for the warp
+            const bool whole = n + kGroup <= mine && n + kGroup + K <= end && n >= begin + K - 1 && q.live;
             auto read = [&](int i) {
                 in.get(i, 0, cur[i]);
                 in.get(i, 1, dy[i]);
@@ -570,14 +588,14 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
             if constexpr (!In::BULK) {  // the registers are read: the next group takes them
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i)
-                    if (whole || t + i < t2) read(i);
+                    if (whole || n + i < total) read(i);
                 in.fetch();
             }
             if (whole) {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
                     if constexpr (In::BULK) read(i);
-                    grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
+                    grad_pre<T, VEC, K, SILU>(w, b, cur[i], win, dy[i], g);
                     sums(i);
 #pragma unroll
                     for (int e = 0; e < N; ++e) {
@@ -586,33 +604,34 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
                             acc[j][e] = fma_(w[K - 1 - j][e], g[e], acc[j - 1][e]);
                         acc[0][e] = mul_(w[K - 1][e], g[e]);
                     }
-                    emit(t + i - (K - 1), acc[K - 1]);
+                    if (i >= K - 1 || n > 0) emit(i - (K - 1), acc[K - 1]);
                     shift(i);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    const long long tt = t + i;
-                    if (tt >= t2) break;
-                    if (tt == q.end) {
-                        q = seq_of(a, tt);
+                    const int at = n + i;
+                    if (at >= total) break;
+                    if (at == end) {
+                        q = seq_of(a, t0 + at);
+                        begin = near(q.start - t0), end = near(q.end - t0);
 #pragma unroll
                         for (int j = 0; j < K - 1; ++j)
                             token_lanes<T, VEC, K>(a, q, -1 - j, c, win[j]);
                     }
                     if constexpr (In::BULK) read(i);
-                    grad_pre<T, VEC, K>(w, b, cur[i], win, dy[i], silu, g);
+                    grad_pre<T, VEC, K, SILU>(w, b, cur[i], win, dy[i], g);
                     if (!q.live)
 #pragma unroll
                         for (int e = 0; e < N; ++e) g[e] = both<V>(0.f);
-                    if (tt < t1 && q.live) sums(i);
-                    // acc[j] becomes token tt - j; token tt starts from the final state's
+                    if (at < mine && q.live) sums(i);
+                    // acc[j] becomes token at - j; token at starts from the final state's
                     // gradient where it is still in the window there
                     float f[VEC];
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) f[e] = 0.f;
-                    if (a.dfinal && q.live && q.end - tt <= K) {
-                        const long long p = (a.pos ? a.pos[q.s] : 0) + (tt - q.start);
+                    if (a.dfinal && q.live && end - at <= K) {
+                        const long long p = (a.pos ? a.pos[q.s] : 0) + (t0 + at - q.start);
                         Pack<T, VEC> v;
                         v.load(static_cast<const T*>(a.dfinal) +
                                ((long long)q.s * K + state_row<K>(p)) * a.C + c);
@@ -625,11 +644,11 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
                     to_lanes<VEC>(f, acc[0]);
 #pragma unroll
                     for (int j = 0; j < K; ++j)
-                        if (tt - j >= q.start)  // a token of an earlier sequence gets nothing
+                        if (at - j >= begin)  // a token of an earlier sequence gets nothing
 #pragma unroll
                             for (int e = 0; e < N; ++e)
                                 acc[j][e] = fma_(w[K - 1 - j][e], g[e], acc[j][e]);
-                    if (tt - (K - 1) >= t0) emit(tt - (K - 1), acc[K - 1]);
+                    if (at >= K - 1) emit(i - (K - 1), acc[K - 1]);
                     shift(i);
                 }
             }
@@ -642,7 +661,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
             if (ch.on && tok >= t0 && tok < t1) {
                 float f[VEC];
                 from_lanes<VEC>(acc[j], f);
-                store_vec<VEC>(du + tok * a.dus, f);
+                store_vec<VEC>(static_cast<T*>(a.du) + tok * dus + c, f);
             }
         }
     }
@@ -761,32 +780,64 @@ constexpr size_t conv_smem(bool bwd) {
     const size_t sums = bwd ? sizeof(float) * kRuns * (K + 1) * VEC * kLanes : 0;
     return ring > sums ? ring : sums;
 }
-template <bool BWD, typename T, int VEC, int K>
-cudaError_t launch_k(unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
-    constexpr auto kernel = BWD ? &conv_bwd_kernel<T, BWD ? VEC : 1, K> : &conv_fwd_kernel<T, BWD ? 1 : VEC, K>;
+// Map over a [rows][cols] tensor with rows `stride` elements apart: tiles of kGroup rows and
+// the columns of a block.
+template <typename T, int VEC>
+bool make_tile_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long stride) {
+    tcc::EncodeTiledFn enc = tcc::encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(stride * sizeof(T))};
+    const cuuint32_t box[2] = {kLanes * VEC, kGroup};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+               const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <bool BWD, typename T, int VEC, int K, bool SILU>
+cudaError_t launch_k(unsigned grid, const ConvArgs& a, cudaStream_t s) {
+    constexpr auto kernel = [] {
+        if constexpr (BWD)
+            return &conv_bwd_kernel<T, VEC, K, SILU>;
+        else
+            return &conv_fwd_kernel<T, VEC, K, SILU>;
+    }();
     constexpr size_t smem = conv_smem<T, VEC, K>(BWD);
+    ConvMaps maps;
+    if (VEC >= 4 && a.T > 0) {
+        if (!make_tile_map<T, VEC>(&maps.u, a.u, a.T, a.C, a.us)) return cudaErrorUnknown;
+        for (int i = 0; BWD && i < 3; ++i)
+            if (a.width[i] && !make_tile_map<T, VEC>(&maps.dout[i], a.out[i], a.T, a.width[i], a.width[i]))
+                return cudaErrorUnknown;
+    }
     const cudaError_t e = allow_smem<kernel>(smem);
-    if (e == cudaSuccess) kernel<<<grid, dim3(kLanes, kRuns), smem, s>>>(a, silu);
+    if (e == cudaSuccess) kernel<<<grid, dim3(kLanes, kRuns), smem, s>>>(a, maps);
     return e;
 }
-template <bool BWD, typename T, int VEC>
-cudaError_t launch_vec(int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
-    if (K == 2) return launch_k<BWD, T, VEC, 2>(grid, a, silu, s);
-    if (K == 3) return launch_k<BWD, T, VEC, 3>(grid, a, silu, s);
-    return launch_k<BWD, T, VEC, 4>(grid, a, silu, s);
+template <bool BWD, typename T, int VEC, bool SILU>
+cudaError_t launch_vec(int K, unsigned grid, const ConvArgs& a, cudaStream_t s) {
+    if (K == 2) return launch_k<BWD, T, VEC, 2, SILU>(grid, a, s);
+    if (K == 3) return launch_k<BWD, T, VEC, 3, SILU>(grid, a, s);
+    return launch_k<BWD, T, VEC, 4, SILU>(grid, a, s);
 }
-template <bool BWD, typename T>
-cudaError_t launch_type(int vec, int K, unsigned grid, const ConvArgs& a, bool silu, cudaStream_t s) {
+template <bool BWD, typename T, bool SILU>
+cudaError_t launch_type(int vec, int K, unsigned grid, const ConvArgs& a, cudaStream_t s) {
     constexpr int wide = sizeof(T) == 2 && !BWD ? 8 : 4;
-    if (vec == wide) return launch_vec<BWD, T, wide>(K, grid, a, silu, s);
-    if (vec == 2) return launch_vec<BWD, T, 2>(K, grid, a, silu, s);
-    return launch_vec<BWD, T, 1>(K, grid, a, silu, s);
+    if (vec == wide) return launch_vec<BWD, T, wide, SILU>(K, grid, a, s);
+    if (vec == 2) return launch_vec<BWD, T, 2, SILU>(K, grid, a, s);
+    return launch_vec<BWD, T, 1, SILU>(K, grid, a, s);
+}
+template <bool BWD, bool SILU>
+cudaError_t launch_silu(const ssd_conv_t* p, int vec, unsigned grid, const ConvArgs& a, cudaStream_t s) {
+    return p->dtype == SSD_DTYPE_BF16
+               ? launch_type<BWD, __nv_bfloat16, SILU>(vec, p->width, grid, a, s)
+               : launch_type<BWD, float, SILU>(vec, p->width, grid, a, s);
 }
 template <bool BWD>
 cudaError_t launch_conv(const ssd_conv_t* p, int vec, unsigned grid, const ConvArgs& a, cudaStream_t s) {
-    const bool silu = p->activation == 1;
-    return p->dtype == SSD_DTYPE_BF16 ? launch_type<BWD, __nv_bfloat16>(vec, p->width, grid, a, silu, s)
-                                      : launch_type<BWD, float>(vec, p->width, grid, a, silu, s);
+    return p->activation == 1 ? launch_silu<BWD, true>(p, vec, grid, a, s)
+                              : launch_silu<BWD, false>(p, vec, grid, a, s);
 }
 
 }  // namespace
@@ -841,7 +892,7 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
     a.init = initial_state, a.final_state = final_state;
     for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
     const long long nvec = c.C / vec;
-    a.run = choose_run(c.T, nvec, 32, 1024);
+    a.run = choose_run(c.T, nvec, 64, 1024);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = final_state ? ceil_div(srows, kRuns) : 0;
     const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);

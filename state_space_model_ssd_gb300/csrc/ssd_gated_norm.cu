@@ -163,7 +163,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true)) gated_bwd_kernel(const Gate
     const float inv = a.inv;
     float next = mine > 0 ? *stats : 0.f;
     int flip = 0;
-    const V one = both<V>(1.f), minus = both<V>(-1.f);
     for (int round = 0; round < rounds; ++round, --mine) {
         const V r = both<V>(next);
         stats += sstep;
@@ -184,7 +183,8 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true)) gated_bwd_kernel(const Gate
                 for (int e = 0; e < N; ++e) {
                     const V sg = sigmoid_lanes<T>(z[e]);
                     gate[i][e] = mul_(z[e], sg);
-                    gy[i][e] = mul_(y[e], fma_(gate[i][e], fma_(sg, minus, one), sg));
+                    // silu'(z) = s + gate (1 - s), in a form without constants to hold
+                    gy[i][e] = mul_(y[e], sub_(add_(sg, gate[i][e]), mul_(gate[i][e], sg)));
                     xh[i][e] = mul_(mul_(y[e], gate[i][e]), r);
                     dw[i][e] = fma_(d[i][e], xh[i][e], dw[i][e]);
                     d[i][e] = mul_(d[i][e], w[i][e]);
