@@ -1,7 +1,7 @@
 // Rows of a norm are worked on by teams: `nw` warps that hold one row in registers.  A warp
 // owns NV * 32 * VEC neighbouring columns, a lane VEC of them NV times over, 32 * VEC apart, so
 // that all of a thread's places in a row are offsets known when compiling.  A block holds one
-// team, or several one-warp teams.
+// team, or several teams of a warp or less (8 or 16 lanes, for rows of so few vectors).
 #pragma once
 
 #include <atomic>
@@ -14,18 +14,20 @@ namespace layer {
 
 struct Team {
     int nw;      // warps in the team
+    int width;   // lanes of a warp in the team
     int warp;    // this warp in its team
-    int lane;
+    int lane;    // this lane of them
     int rank;    // this thread in its team
     int id;      // the team in its block
 };
-__device__ __forceinline__ Team team_of(int nw) {
+__device__ __forceinline__ Team team_of(int nw, int width) {
     Team t;
     const int w = threadIdx.x >> 5;
     t.nw = nw;
-    t.id = w / nw;
-    t.warp = w - t.id * nw;
-    t.lane = threadIdx.x & 31;
+    t.width = width;
+    t.lane = threadIdx.x & (width - 1);
+    t.id = width == 32 ? w / nw : threadIdx.x / width;
+    t.warp = width == 32 ? w - t.id * nw : 0;
     t.rank = t.warp * 32 + t.lane;
     return t;
 }
@@ -49,8 +51,9 @@ template <int N>
 __device__ __forceinline__ void team_sum(const Team& t, float* x, TeamBuf<N>& buf, int flip) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
+        if (o < t.width)  // the same for the block
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+            for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
     if (t.nw == 1) return;
     if (t.lane == 0)
 #pragma unroll
@@ -85,59 +88,73 @@ inline int common_vec(int most, const long long* strides, int ns, const void* co
 // How a row of `dim` columns is laid over threads.
 struct RowPlan {
     int vec;     // elements of a vector
-    int nv;      // vectors a thread holds: 1, 2, 3, 4 or 8
+    int nv;      // vectors a thread holds: 1, 2, 3, 4, 6, 8 or 16
     int nw;      // warps in a team
+    int width;   // lanes of a warp in a team
     int teams;   // teams in a block
     int per_sm;  // blocks an SM holds at once
-    int stages;  // rows in flight by bulk copies (0: through registers)
+    bool bulk;   // rows arrive by bulk copies (or through registers)
+    int stages;  // rows in flight then
     size_t ring; // bytes of shared memory they take
-    int threads() const { return nw * teams * 32; }
+    int threads() const { return nw * teams * width; }
 };
 // Longest rows.
 constexpr int most_columns(int vec) { return vec >= 4 ? 16384 : 8192; }
-constexpr int most_vectors(int vec) { return vec == 8 ? 4 : 8; }
+constexpr int most_vectors(int vec) { return vec == 8 ? 4 : vec == 1 ? 16 : 8; }
 // Registers of a thread that holds e elements of a row: what the kernels need without spilling
-// (beyond 16 elements a backward spills, on rows of more than 8192 columns), and no more, since
+// (a backward spills beyond 24 elements, on rows of more than 9216 columns), and no more, since
 // they decide how many rows an SM works on.
-constexpr int row_regs(int vec, int nv, bool bwd) {
+constexpr int row_regs(int vec, int nv, bool bwd, bool bulk) {
     const int e = vec * nv;
-    const int r = bwd ? (e <= 2 ? 56 : e <= 4 ? 64 : e <= 8 ? 96 : 128)
-                      : (e <= 2 ? 40 : e <= 4 ? 48 : e <= 8 ? 64 : e <= 16 ? 96 : 128);
-    return vec == 1 && r > 64 ? 64 : r;
+    if (bwd) return e <= 2 ? 56 : e <= 4 ? (bulk ? 64 : 80) : e <= 8 ? (bulk ? 96 : 112) : 128;
+    return e <= 2 ? 40 : e <= 4 ? 56 : e <= 8 ? (bulk ? 64 : 80) : e <= 16 ? (bulk ? 96 : 128) : 128;
 }
 // What a row's plan goes by: the tensors read, na of `ab` bytes an element and nb of `bb`.
 struct RowCost {
     bool bwd;
     int na, ab, nb, bb;
 };
+// Warps of so many registers a thread that an SM holds: each quarter has 16384 registers.
+inline int resident_warps(int regs) { return 4 * (16384 / (32 * regs)); }
 inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     if (dim > most_columns(vec)) return false;
     p->vec = vec;
     const int nvec = (dim + vec - 1) / vec;
-    // elements a thread holds at most, as long as a block then has threads enough for the row
-    const int hold = vec == 1 ? 4 : cost.bwd ? 8 : 32;
-    // A warp spends about as long on a row's sums and addresses as on ten elements a lane, so
-    // the cheapest plan has few warps with many elements each, none of them idle.
-    long long best = -1;
-    const int sizes[5] = {1, 2, 3, 4, 8};
+    // Elements a thread holds without spilling, where more threads do as well.  At 32768 x 2560
+    // (us): a forward through registers with 8 / 16 / 32 elements 171 / 158 / 202, a backward
+    // with 8 / 16 and the residual's gradient 222 / 267, without it 134 / 109.
+    const int hold = cost.bwd ? (vec == 1 ? 4 : vec == 2 || cost.nb > 1 ? 8 : 16)
+                              : (vec == 1 ? 8 : cost.nb > 0 || cost.na == 1 ? 16 : 32);
+    // A warp spends about as long on a row's sums and addresses as on fourteen elements a lane,
+    // and up to sixteen warps on an SM each add their share of its rate: the plan with the least
+    // of that time per row wins.
+    double best = -1;
+    const int sizes[7] = {1, 2, 3, 4, 6, 8, 16};
     for (int nv : sizes) {
-        if (nv > most_vectors(vec)) break;
-        const int nw = ((nvec + nv - 1) / nv + 31) / 32;
-        if (nw > 32 || nw * 32 * row_regs(vec, nv, cost.bwd) > 65536) continue;
-        if (nv * vec > hold && best >= 0) break;
-        const long long c = (long long)nw * (10 + nv * vec);
+        if (nv > most_vectors(vec) || (nv * vec > hold && best >= 0)) break;
+        const int nw = ((nvec + nv - 1) / nv + 31) / 32, teams = nw == 1 ? 4 : 1;
+        // A backward's rows come by bulk copies from a full warp on: at 32768 x 5120 312 us
+        // against 529 through registers, which its sums need.  A forward has registers to spare
+        // (158 against 175 us at 32768 x 2560).
+        const bool bulk = cost.bwd && vec >= 4 && nvec > 32;
+        int warps = resident_warps(row_regs(vec, nv, cost.bwd, bulk)) / (nw * teams) * (nw * teams);
+        if (nw > 32 || warps == 0) continue;
+        if (warps > 16) warps = 16;
+        const double c = nw * (14.0 + nv * vec) / warps;
         if (best >= 0 && c >= best) continue;
         best = c;
         p->nv = nv;
         p->nw = nw;
+        p->bulk = bulk;
     }
     if (best < 0) return false;
-    p->teams = p->nw == 1 ? 4 : 1;
-    p->per_sm = 65536 / row_regs(vec, p->nv, cost.bwd) / p->threads();
+    p->width = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
+    p->teams = p->nw == 1 ? 128 / p->width : 1;
+    p->per_sm = resident_warps(row_regs(vec, p->nv, cost.bwd, p->bulk)) / (p->threads() / 32);
     if (p->per_sm > 16) p->per_sm = 16;
     p->stages = 0;
     p->ring = 0;
-    if (vec >= 4) {
+    if (p->bulk) {
         // two to eight rows in flight a team, within what the blocks of an SM can share
         const size_t row = (size_t)dim * (cost.na * cost.ab + cost.nb * cost.bb) * p->teams;
         const size_t all = 210 << 10;
@@ -156,9 +173,8 @@ constexpr int kMostStages = 8;
 struct RowBars {
     uint64_t full[4][kMostStages];  // by team of the block
 };
-template <typename A, typename B, int NA, int NB, int VEC, int NV>
+template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK>
 struct Rows {
-    static constexpr bool BULK = VEC >= 4;
     Pack<A, VEC> ra[BULK ? 1 : NV][NA];
     Pack<B, VEC> rb[BULK ? 1 : NV][NB ? NB : 1];
     const A* pa[NA];           // the next row to load: its start, or this thread's part of it

@@ -158,14 +158,17 @@ __device__ __forceinline__ void stage_weights(const ConvArgs& a, long long c0, i
 // The tokens of a warp's run on their way to it, in groups of kGroup: as tiles of the block's
 // channels that one lane has copied (TMA) into a ring of kGroups groups in shared memory, or, in
 // vectors of less than 16 bytes, through registers one group ahead.  N tensors.
-constexpr int kGroup = 8;
-constexpr int kGroups = 2;
+// Two groups of eight tokens; four tokens and three groups where a token of both tensors takes
+// 1 KB (float32 backward), for two blocks an SM.
+constexpr int group_of(int vec, int esize, int n) { return vec * esize * n > 16 ? 4 : 8; }
+constexpr int groups_of(int vec, int esize, int n) { return vec * esize * n > 16 ? 3 : 2; }
 struct RunBars {
-    uint64_t full[kRuns][kGroups];
+    uint64_t full[kRuns][3];
 };
 template <typename T, int VEC, int N>
 struct Run {
     static constexpr bool BULK = VEC >= 4;
+    static constexpr int kGroup = group_of(VEC, sizeof(T), N), kGroups = groups_of(VEC, sizeof(T), N);
     static constexpr int line = kLanes * VEC * (int)sizeof(T);  // a token of a tensor in the ring
     static constexpr int tile = kGroup * line;
     Pack<T, VEC> next[BULK ? 1 : kGroup][N];
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_fwd_kernel(const ConvAr
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     using In = Run<T, VEC, 1>;
+    constexpr int kGroup = In::kGroup;
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
     __shared__ RunBars bars;
     extern __shared__ __align__(128) char ring[];
@@ -497,6 +501,7 @@ __global__ void __launch_bounds__(kLanes* kRuns, 2) conv_bwd_kernel(const ConvAr
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     using In = Run<T, VEC, 2>;
+    constexpr int kGroup = In::kGroup;
     __shared__ __align__(16) float ws[K + 1][kLanes * VEC];
     __shared__ RunBars bars;
     extern __shared__ __align__(128) char ring[];
@@ -776,19 +781,22 @@ void fill_args(const ssd_conv_t* p, const Conv& c, int vec, ConvArgs* a) {
 // Shared memory of a block: the ring, or in the backward the runs' sums at the end.
 template <typename T, int VEC, int K>
 constexpr size_t conv_smem(bool bwd) {
-    const size_t ring = VEC >= 4 ? (size_t)kRuns * kGroups * kGroup * (bwd ? 2 : 1) * kLanes * VEC * sizeof(T) : 0;
+    const size_t n = bwd ? 2 : 1;
+    const size_t ring = VEC >= 4 ? kRuns * n * kLanes * VEC * sizeof(T) * group_of(VEC, sizeof(T), n) *
+                                       groups_of(VEC, sizeof(T), n)
+                                 : 0;
     const size_t sums = bwd ? sizeof(float) * kRuns * (K + 1) * VEC * kLanes : 0;
     return ring > sums ? ring : sums;
 }
-// Map over a [rows][cols] tensor with rows `stride` elements apart: tiles of kGroup rows and
-// the columns of a block.
-template <typename T, int VEC>
+// Map over a [rows][cols] tensor with rows `stride` elements apart: tiles of a group of
+// rows and the columns of a block.
+template <typename T, int VEC, int N>
 bool make_tile_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long stride) {
     tcc::EncodeTiledFn enc = tcc::encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(stride * sizeof(T))};
-    const cuuint32_t box[2] = {kLanes * VEC, kGroup};
+    const cuuint32_t box[2] = {kLanes * VEC, (cuuint32_t)group_of(VEC, sizeof(T), N)};
     const cuuint32_t es[2] = {1, 1};
     return enc(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -806,9 +814,9 @@ cudaError_t launch_k(unsigned grid, const ConvArgs& a, cudaStream_t s) {
     constexpr size_t smem = conv_smem<T, VEC, K>(BWD);
     ConvMaps maps;
     if (VEC >= 4 && a.T > 0) {
-        if (!make_tile_map<T, VEC>(&maps.u, a.u, a.T, a.C, a.us)) return cudaErrorUnknown;
+        if (!make_tile_map<T, VEC, BWD ? 2 : 1>(&maps.u, a.u, a.T, a.C, a.us)) return cudaErrorUnknown;
         for (int i = 0; BWD && i < 3; ++i)
-            if (a.width[i] && !make_tile_map<T, VEC>(&maps.dout[i], a.out[i], a.T, a.width[i], a.width[i]))
+            if (a.width[i] && !make_tile_map<T, VEC, BWD ? 2 : 1>(&maps.dout[i], a.out[i], a.T, a.width[i], a.width[i]))
                 return cudaErrorUnknown;
     }
     const cudaError_t e = allow_smem<kernel>(smem);

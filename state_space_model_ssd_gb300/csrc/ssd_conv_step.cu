@@ -10,11 +10,11 @@
 // pos-1 .. pos-K+1 and the new token; one of them writes row pos mod K, which none reads, so
 // the blocks need not wait for one another.
 //
-// Bound by the state's bytes (2 P N 4 per row and head).  One CTA takes PR rows of one
-// head's state; it has its first pieces of the state in flight while it works out the
-// PR + 2 N channels it needs (B and C again in every CTA of a group: 2 N K elements out of
-// L2 against 8 PR N bytes of state).  With few rows in the batch a head's state is split
-// over several CTAs, so that the whole GPU's loads are in flight.
+// Bound by the state's bytes (2 P N 4 per row and head).  With a large batch a CTA takes several
+// heads of one group, one after the other: the B and C channels (2 N of them, against P of x a
+// head) are then worked out once for all.  With few rows in the batch a head's state is split
+// over several CTAs, so that the whole GPU's loads are in flight.  A CTA has its first pieces
+// of the state on their way while it works out its channels.
 #include <limits.h>
 #include <math.h>
 
@@ -40,9 +40,12 @@ struct StepArgs {
     const int* slots;
     void* y;
     long long us, C;
-    int H, P, N, G, nslots, split, wbf16;
+    int H, P, N, G, nslots, wbf16;
+    int split, heads;  // CTAs a head, heads a CTA (one of the two is 1)
+    int log_n4;        // log2 of the float4 pieces in a row of the state
     float delta_init;
 };
+constexpr int kMostHeads = 8;
 
 // The taps of channel c.
 template <int K>
@@ -59,21 +62,101 @@ __device__ __forceinline__ void taps(const StepArgs& a, long long c, float* w) {
     for (int k = 0; k < K; ++k) w[k] = param(a.w, c * K + k, a.wbf16);
 }
 
+// The sums over the 2^LOG lanes of a row of kPieces values a lane, in LOG steps that halve the
+// values as long as there are several: lane bits from the top choose which value a lane goes on
+// with.  Returns this lane's sum, of the value `*which`; the lanes whose low bits (below those
+// used for the choice) are zero between them have one each.
+template <int LOG>
+__device__ __forceinline__ float halving_sum(float (&v)[kPieces], int lane, int* which) {
+    int n = kPieces, id = 0;
+#pragma unroll
+    for (int step = 0; step < LOG; ++step) {
+        const int o = 1 << (LOG - 1 - step);
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & o;
+            id = id * 2 + up;
+#pragma unroll
+            for (int i = 0; i < kPieces / 2; ++i)
+                if (i < n) {
+                    const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+    *which = id;
+    return v[0];
+}
+
+// One head's rows p0 .. p0 + PR of the state: H <- decay H + xs B^T in place, y = H C.
+// LOG: log2 of the pieces in a row, 3 or more (0: fewer, known at run time).
+template <typename T, int LOG>
+__device__ __forceinline__ void step_rows(float4* s4, float4 (&piece)[kPieces], int total, int log_n4,
+                                          float decay, const float* xs, const float* bs,
+                                          const float* cs, T* y) {
+    const int ln4 = LOG ? LOG : log_n4, n4 = 1 << ln4;
+    for (int base = 0; base < total; base += kPieces * kStepThreads) {
+        if (base > 0)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int e = base + i * kStepThreads + threadIdx.x;
+                if (e < total) piece[i] = s4[e];
+            }
+        // a thread's pieces lie in the same columns (n4 divides the block's threads)
+        const int n = (threadIdx.x & (n4 - 1)) * 4;
+        const float4 bv = *reinterpret_cast<const float4*>(bs + n);
+        const float4 cv = *reinterpret_cast<const float4*>(cs + n);
+        float sum[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int e = base + i * kStepThreads + threadIdx.x;
+            sum[i] = 0.f;
+            if (e < total) {
+                const float xv = xs[e >> ln4];
+                float4 s;
+                s.x = fmaf(decay, piece[i].x, xv * bv.x);
+                s.y = fmaf(decay, piece[i].y, xv * bv.y);
+                s.z = fmaf(decay, piece[i].z, xv * bv.z);
+                s.w = fmaf(decay, piece[i].w, xv * bv.w);
+                s4[e] = s;
+                sum[i] = (s.x * cv.x + s.y * cv.y) + (s.z * cv.z + s.w * cv.w);
+            }
+        }
+        if constexpr (LOG >= 3) {
+            int which;
+            const float t = halving_sum<LOG>(sum, threadIdx.x & (n4 - 1), &which);
+            const int e = base + which * kStepThreads + threadIdx.x;
+            if ((threadIdx.x & ((n4 >> 3) - 1)) == 0 && e < total) st_out(y, e >> ln4, t);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                for (int o = n4 >> 1; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o, n4);
+                const int e = base + i * kStepThreads + threadIdx.x;
+                if (n == 0 && e < total) st_out(y, e >> ln4, sum[i]);
+            }
+        }
+    }
+}
+
 template <typename T, int K>
 __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepArgs a) {
-    __shared__ float xs[128], bs[128], cs[128];
+    __shared__ __align__(16) float xs[kMostHeads][128], bs[128], cs[128];
+    __shared__ float decays[kMostHeads];
     const int row = blockIdx.y;
-    const int h = blockIdx.x / a.split, part = blockIdx.x - h * a.split;
+    const int unit = blockIdx.x / a.split, part = blockIdx.x - unit * a.split;
+    const int h0 = unit * a.heads;
     const int PR = a.P / a.split, p0 = part * PR;
     const int slot = a.slots ? a.slots[row] : row;
-    T* y = static_cast<T*>(a.y) + ((long long)row * a.H + h) * a.P + p0;
+    T* y = static_cast<T*>(a.y) + ((long long)row * a.H + h0) * a.P + p0;
     if (slot < 0 || slot >= a.nslots) {  // a padding row of the batch
-        for (int i = threadIdx.x; i < PR; i += kStepThreads) st_out(y, i, 0.f);
+        for (int i = threadIdx.x; i < PR * a.heads; i += kStepThreads) st_out(y, i, 0.f);
         return;
     }
-    const int n4 = a.N >> 2, total = PR * n4;  // float4 pieces of this CTA
-    float4* s4 = reinterpret_cast<float4*>(
-        a.state + (((long long)slot * a.H + h) * a.P + p0) * a.N);
+    const int total = PR << a.log_n4;  // float4 pieces of a head here
+    float4* s4 =
+        reinterpret_cast<float4*>(a.state + (((long long)slot * a.H + h0) * a.P + p0) * a.N);
     float4 piece[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -81,10 +164,13 @@ __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepAr
         if (e < total) piece[i] = s4[e];
     }
 
-    const int Hg = a.H / a.G, g = h / Hg;
+    const int g = h0 / (a.H / a.G);
     const int pos = a.pos[row];
-    const float delta = softplus_f(a.raw[(long long)row * a.H + h] + a.delta_init);
-    const float decay = expf(-delta);
+    if (threadIdx.x >= kStepThreads - a.heads) {  // the threads with the fewest channels
+        const int h = kStepThreads - 1 - threadIdx.x;
+        const float delta = softplus_f(a.raw[(long long)row * a.H + h0 + h] + a.delta_init);
+        decays[h] = delta;  // the decay follows below
+    }
     int at[K];  // at[j]: the window's row of position pos - j
 #pragma unroll
     for (int j = 0; j < K; ++j) {
@@ -93,12 +179,13 @@ __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepAr
     }
     T* win = static_cast<T*>(a.window) + (long long)slot * K * a.C;
     const T* u = static_cast<const T*>(a.u) + row * a.us;
-    const bool owns_bc = part == 0 && h == g * Hg;
-    for (int i = threadIdx.x; i < PR + 2 * a.N; i += kStepThreads) {
-        const int j = i - PR;  // B and C channels follow the x channels
-        const long long c = j < 0        ? (long long)h * a.P + p0 + i
-                            : j < a.N    ? (long long)a.H * a.P + g * a.N + j
-                                         : (long long)a.H * a.P + (a.G + g) * a.N + (j - a.N);
+    const bool owns_bc = part == 0 && h0 == g * (a.H / a.G);
+    const int nx = PR * a.heads;  // x channels (several heads: whole ones, next to one another)
+    for (int i = threadIdx.x; i < nx + 2 * a.N; i += kStepThreads) {
+        const int j = i - nx;  // B and C channels follow the x channels
+        const long long c = j < 0     ? (long long)h0 * a.P + p0 + i
+                            : j < a.N ? (long long)a.H * a.P + g * a.N + j
+                                      : (long long)a.H * a.P + (a.G + g) * a.N + (j - a.N);
         const T tok = u[c];
         float w[K];
         taps<K>(a, c, w);
@@ -108,44 +195,48 @@ __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepAr
         for (int k = 1; k < K; ++k)
             v = fmaf(w[K - 1 - k], static_cast<float>(win[at[k] * a.C + c]), v);
         if (j < 0 || owns_bc) win[at[0] * a.C + c] = tok;
-        v *= sigmoid_of<float>(v);
+        v *= sigmoid_of<T>(v);
         if (j < 0)
-            xs[i] = delta * v;
+            xs[0][i] = v;  // heads of PR channels one after the other
         else if (j < a.N)
             bs[j] = v;
         else
             cs[j - a.N] = v;
     }
     __syncthreads();
+    // delta into x, then the decays in its place
+    float scaled[(kMostHeads * 128) / kStepThreads];
+#pragma unroll
+    for (int k = 0; k < (kMostHeads * 128) / kStepThreads; ++k) {
+        const int i = k * kStepThreads + threadIdx.x;
+        if (i < nx) scaled[k] = xs[0][i] * decays[i / PR];
+    }
+    const float decay0 = threadIdx.x < a.heads ? expf(-decays[threadIdx.x]) : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < (kMostHeads * 128) / kStepThreads; ++k) {
+        const int i = k * kStepThreads + threadIdx.x;
+        if (i < nx) xs[0][i] = scaled[k];
+    }
+    if (threadIdx.x < a.heads) decays[threadIdx.x] = decay0;
+    __syncthreads();
 
-    for (int base = 0; base < total; base += kPieces * kStepThreads) {
-        if (base > 0)
+    for (int h = 0; h < a.heads; ++h) {
+        if (h > 0)
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int e = base + i * kStepThreads + threadIdx.x;
+                const int e = i * kStepThreads + threadIdx.x;
                 if (e < total) piece[i] = s4[e];
             }
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int e = base + i * kStepThreads + threadIdx.x;
-            if (base + i * kStepThreads >= total) break;  // the same for the whole block
-            const bool in = e < total;
-            const int p = e / n4, n = (e - p * n4) * 4;
-            float sum = 0.f;
-            if (in) {
-                const float xv = xs[p];
-                float4 s;
-                s.x = fmaf(decay, piece[i].x, xv * bs[n]);
-                s.y = fmaf(decay, piece[i].y, xv * bs[n + 1]);
-                s.z = fmaf(decay, piece[i].z, xv * bs[n + 2]);
-                s.w = fmaf(decay, piece[i].w, xv * bs[n + 3]);
-                s4[e] = s;
-                sum = s.x * cs[n] + s.y * cs[n + 1] + s.z * cs[n + 2] + s.w * cs[n + 3];
-            }
-            // the n4 consecutive lanes of one row (n4 divides 32)
-            for (int o = n4 >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, n4);
-            if (in && n == 0) st_out(y, p, sum);
-        }
+        const float* x = &xs[0][0] + h * PR;
+        if (a.log_n4 == 5)
+            step_rows<T, 5>(s4, piece, total, 5, decays[h], x, bs, cs, y);
+        else if (a.log_n4 == 4)
+            step_rows<T, 4>(s4, piece, total, 4, decays[h], x, bs, cs, y);
+        else
+            step_rows<T, 0>(s4, piece, total, a.log_n4, decays[h], x, bs, cs, y);
+        s4 += (long long)a.P << a.log_n4;
+        y += a.P;
     }
 }
 
@@ -205,7 +296,14 @@ ssd_status_t ssd_conv_decode_step(const ssd_problem_t* prob, int32_t width, int3
     const long long units = p.batch * p.nheads, want = 2LL * sm_count();
     while (units * a.split < want && p.headdim / (2 * a.split) * (p.dstate / 4) >= kStepThreads)
         a.split *= 2;
-    const dim3 grid((unsigned)(p.nheads * a.split), (unsigned)p.batch);
+    // Heads a CTA: while that leaves two rounds of the four CTAs an SM holds.
+    a.heads = 1;
+    const int per_group = p.nheads / p.ngroups;
+    while (a.split == 1 && a.heads < kMostHeads && per_group % (2 * a.heads) == 0 &&
+           units / (2 * a.heads) >= 8LL * sm_count())
+        a.heads *= 2;
+    for (int n = p.dstate / 4; n > 1; n >>= 1) ++a.log_n4;
+    const dim3 grid((unsigned)(p.nheads / a.heads * a.split), (unsigned)p.batch);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     L.begin("conv_decode_step");

@@ -33,7 +33,7 @@ struct GatedArgs {
     float* partial;
     long long rows, ys, zs, os, dys, dzs;
     int D, G, n;   // columns, groups, columns of a group
-    int nw, teams;
+    int nw, width, teams;
     int nrb;       // blocks of a group
     int wbf16;
     int stages;
@@ -55,18 +55,18 @@ __device__ __forceinline__ void weights_of(const GatedArgs& a, const Team& t, in
     }
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __maxnreg__(row_regs(VEC, NV, false)) gated_fwd_kernel(const GatedArgs a) {
+template <typename T, int VEC, int NV, bool BULK>
+__global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(const GatedArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
     extern __shared__ __align__(128) char ring[];
-    const Team t = team_of(a.nw);
+    const Team t = team_of(a.nw, a.width);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
     const long long step = (long long)a.nrb * a.teams;
     const long long row = (long long)rb * a.teams + t.id;
-    using In = Rows<T, T, 2, 0, VEC, NV>;
+    using In = Rows<T, T, 2, 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
     // every team of the block takes the rounds of its first team, the last perhaps without a row
@@ -127,18 +127,18 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false)) gated_fwd_kernel(const Gat
     in.drain();
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __maxnreg__(row_regs(VEC, NV, true)) gated_bwd_kernel(const GatedArgs a) {
+template <typename T, int VEC, int NV, bool BULK>
+__global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) gated_bwd_kernel(const GatedArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
     extern __shared__ __align__(128) char ring[];
-    const Team t = team_of(a.nw);
+    const Team t = team_of(a.nw, a.width);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
     const long long step = (long long)a.nrb * a.teams;
     const long long row = (long long)rb * a.teams + t.id;
-    using In = Rows<T, T, 3, 0, VEC, NV>;
+    using In = Rows<T, T, 3, 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
     // every team of the block takes the rounds of its first team, the last perhaps without a row
@@ -274,18 +274,29 @@ size_t bwd_smem(const RowPlan& p, int n) {
     return p.ring > sums ? p.ring : sums;
 }
 
-template <bool BWD, typename T, int VEC, int NV>
-cudaError_t launch_nv(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
+template <bool BWD, typename T, int VEC, int NV, bool BULK>
+cudaError_t launch_mode(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
     constexpr auto kernel = [] {
         if constexpr (BWD)
-            return &gated_bwd_kernel<T, VEC, NV>;
+            return &gated_bwd_kernel<T, VEC, NV, BULK>;
         else
-            return &gated_fwd_kernel<T, VEC, NV>;
+            return &gated_fwd_kernel<T, VEC, NV, BULK>;
     }();
     const size_t smem = BWD ? bwd_smem(p, a.n) : p.ring;
     const cudaError_t e = allow_smem<kernel>(smem);
     if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
     return e;
+}
+// The backward's wide rows come by bulk copies unless a warp has lanes to spare.
+template <bool BWD, typename T, int VEC, int NV>
+cudaError_t launch_nv(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
+    if constexpr (BWD && VEC >= 4) {
+        if (p.bulk) return launch_mode<BWD, T, VEC, NV, true>(p, grid, a, s);
+        if constexpr (NV == 1) return launch_mode<BWD, T, VEC, NV, false>(p, grid, a, s);
+        return cudaErrorInvalidValue;
+    } else {
+        return launch_mode<BWD, T, VEC, NV, false>(p, grid, a, s);
+    }
 }
 template <bool BWD, typename T, int VEC>
 cudaError_t launch_vec(const RowPlan& p, unsigned grid, const GatedArgs& a, cudaStream_t s) {
@@ -294,8 +305,16 @@ cudaError_t launch_vec(const RowPlan& p, unsigned grid, const GatedArgs& a, cuda
         case 2: return launch_nv<BWD, T, VEC, 2>(p, grid, a, s);
         case 3: return launch_nv<BWD, T, VEC, 3>(p, grid, a, s);
         case 4: return launch_nv<BWD, T, VEC, 4>(p, grid, a, s);
+        case 6:
+            if constexpr (most_vectors(VEC) >= 8) return launch_nv<BWD, T, VEC, 6>(p, grid, a, s);
+            break;
+        case 8:
+            if constexpr (most_vectors(VEC) >= 8) return launch_nv<BWD, T, VEC, 8>(p, grid, a, s);
+            break;
+        case 16:
+            if constexpr (most_vectors(VEC) >= 16) return launch_nv<BWD, T, VEC, 16>(p, grid, a, s);
+            break;
     }
-    if constexpr (most_vectors(VEC) == 8) return launch_nv<BWD, T, VEC, 8>(p, grid, a, s);
     return cudaErrorInvalidValue;
 }
 template <bool BWD, typename T>
@@ -317,7 +336,7 @@ void fill_args(const ssd_gated_norm_t* g, const RowPlan& p, GatedArgs* a) {
     a->ys = g->y_stride, a->zs = g->z_stride, a->os = g->out_stride;
     a->dys = g->dy_stride, a->dzs = g->dz_stride;
     a->D = g->dim, a->G = g->groups, a->n = g->dim / g->groups;
-    a->nw = p.nw, a->teams = p.teams, a->stages = p.stages;
+    a->nw = p.nw, a->width = p.width, a->teams = p.teams, a->stages = p.stages;
     a->status = status_word();
     a->wbf16 = g->wdtype == SSD_DTYPE_BF16;
     a->eps = g->eps, a->inv = (float)(1.0 / a->n);

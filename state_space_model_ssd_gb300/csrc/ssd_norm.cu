@@ -41,7 +41,7 @@ struct NormArgs {
     void* dres;
     float* partial;
     long long rows, xs, rs, hs, ys;
-    int D, nw, teams;
+    int D, nw, width, teams;
     int layer;     // 0: rms
     int wbf16;
     int nk;        // partial rows: d_weight (and d_bias)
@@ -66,16 +66,16 @@ __device__ __forceinline__ void columns_of(const void* p, const Team& t, int col
 }
 
 // RES: with a residual.
-template <typename T, typename TR, bool RES, int VEC, int NV>
-__global__ void __maxnreg__(row_regs(VEC, NV, false)) norm_fwd_kernel(const NormArgs a) {
+template <typename T, typename TR, bool RES, int VEC, int NV, bool BULK>
+__global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(const NormArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
     extern __shared__ __align__(128) char ring[];
-    const Team t = team_of(a.nw);
+    const Team t = team_of(a.nw, a.width);
     const long long step = (long long)gridDim.x * a.teams;
     long long row = (long long)blockIdx.x * a.teams + t.id;
-    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV>;
+    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
     // every team of the block takes the rounds of its first team, the last perhaps without a row
@@ -165,17 +165,17 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false)) norm_fwd_kernel(const Norm
 }
 
 // DH: with the residual stream's gradient.
-template <typename T, typename TR, bool DH, int VEC, int NV>
-__global__ void __maxnreg__(row_regs(VEC, NV, true)) norm_bwd_kernel(const NormArgs a) {
+template <typename T, typename TR, bool DH, int VEC, int NV, bool BULK>
+__global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) norm_bwd_kernel(const NormArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     constexpr bool SAME = sizeof(T) == sizeof(TR);
     __shared__ TeamBuf<2> buf;
     extern __shared__ __align__(128) char ring[];
-    const Team t = team_of(a.nw);
+    const Team t = team_of(a.nw, a.width);
     const long long step = (long long)gridDim.x * a.teams;
     const long long row = (long long)blockIdx.x * a.teams + t.id;
-    using In = Rows<T, TR, 1, DH ? 2 : 1, VEC, NV>;
+    using In = Rows<T, TR, 1, DH ? 2 : 1, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
     // every team of the block takes the rounds of its first team, the last perhaps without a row
@@ -322,18 +322,29 @@ size_t bwd_smem(const RowPlan& p, int dim) {
     return p.ring > sums ? p.ring : sums;
 }
 
-template <bool BWD, typename T, typename TR, bool OPT, int VEC, int NV>
-cudaError_t launch_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+template <bool BWD, typename T, typename TR, bool OPT, int VEC, int NV, bool BULK>
+cudaError_t launch_mode(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
     constexpr auto kernel = [] {
         if constexpr (BWD)
-            return &norm_bwd_kernel<T, TR, OPT, VEC, NV>;
+            return &norm_bwd_kernel<T, TR, OPT, VEC, NV, BULK>;
         else
-            return &norm_fwd_kernel<T, TR, OPT, VEC, NV>;
+            return &norm_fwd_kernel<T, TR, OPT, VEC, NV, BULK>;
     }();
     const size_t smem = BWD ? bwd_smem(p, a.D) : p.ring;
     const cudaError_t e = allow_smem<kernel>(smem);
     if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
     return e;
+}
+// The backward's wide rows come by bulk copies unless a warp has lanes to spare.
+template <bool BWD, typename T, typename TR, bool OPT, int VEC, int NV>
+cudaError_t launch_nv(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
+    if constexpr (BWD && VEC >= 4) {
+        if (p.bulk) return launch_mode<BWD, T, TR, OPT, VEC, NV, true>(p, grid, a, s);
+        if constexpr (NV == 1) return launch_mode<BWD, T, TR, OPT, VEC, NV, false>(p, grid, a, s);
+        return cudaErrorInvalidValue;
+    } else {
+        return launch_mode<BWD, T, TR, OPT, VEC, NV, false>(p, grid, a, s);
+    }
 }
 template <bool BWD, typename T, typename TR, bool OPT, int VEC>
 cudaError_t launch_vec(const RowPlan& p, unsigned grid, const NormArgs& a, cudaStream_t s) {
@@ -342,8 +353,16 @@ cudaError_t launch_vec(const RowPlan& p, unsigned grid, const NormArgs& a, cudaS
         case 2: return launch_nv<BWD, T, TR, OPT, VEC, 2>(p, grid, a, s);
         case 3: return launch_nv<BWD, T, TR, OPT, VEC, 3>(p, grid, a, s);
         case 4: return launch_nv<BWD, T, TR, OPT, VEC, 4>(p, grid, a, s);
+        case 6:
+            if constexpr (most_vectors(VEC) >= 8) return launch_nv<BWD, T, TR, OPT, VEC, 6>(p, grid, a, s);
+            break;
+        case 8:
+            if constexpr (most_vectors(VEC) >= 8) return launch_nv<BWD, T, TR, OPT, VEC, 8>(p, grid, a, s);
+            break;
+        case 16:
+            if constexpr (most_vectors(VEC) >= 16) return launch_nv<BWD, T, TR, OPT, VEC, 16>(p, grid, a, s);
+            break;
     }
-    if constexpr (most_vectors(VEC) == 8) return launch_nv<BWD, T, TR, OPT, VEC, 8>(p, grid, a, s);
     return cudaErrorInvalidValue;
 }
 template <bool BWD, typename T, typename TR, bool OPT>
@@ -414,7 +433,7 @@ ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void*
     a.stats = reinterpret_cast<float2*>(stats);
     a.rows = n, a.xs = norm->x_stride, a.rs = norm->r_stride, a.hs = norm->h_stride,
     a.ys = norm->y_stride;
-    a.D = D, a.nw = p.nw, a.teams = p.teams, a.stages = p.stages;
+    a.D = D, a.nw = p.nw, a.width = p.width, a.teams = p.teams, a.stages = p.stages;
     a.status = status_word();
     if (!a.status) return SSD_ERR_CUDA;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;
@@ -492,7 +511,7 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     a.partial = static_cast<float*>(workspace);
     a.rows = n, a.xs = norm->x_stride, a.rs = norm->r_stride, a.hs = norm->h_stride,
     a.ys = norm->y_stride;
-    a.D = D, a.nw = p.nw, a.teams = p.teams, a.stages = p.stages;
+    a.D = D, a.nw = p.nw, a.width = p.width, a.teams = p.teams, a.stages = p.stages;
     a.status = status_word();
     if (!a.status) return SSD_ERR_CUDA;
     a.layer = norm->kind == SSD_NORM_LAYER, a.wbf16 = norm->wdtype == SSD_DTYPE_BF16;

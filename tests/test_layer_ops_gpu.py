@@ -229,7 +229,10 @@ def test_conv_malformed_lengths_stay_in_range(ssd):
 @pytest.mark.parametrize("dt,B,H,P,N,G,K,slots,strided", [
     ("bf16", 1, 80, 64, 128, 1, 4, None, False), ("bf16", 5, 6, 64, 64, 2, 4, [3, -1, 0, 9, 5], True),
     ("f32", 3, 2, 128, 128, 1, 3, [2, 0, 1], False), ("f32", 1, 1, 8, 8, 1, 2, [1], False),
-    ("bf16", 40, 4, 16, 32, 4, 4, None, True)])
+    ("bf16", 40, 4, 16, 32, 4, 4, None, True),
+    # many rows: several heads of a group to a block
+    ("bf16", 40, 64, 16, 32, 2, 4, None, False), ("f32", 170, 32, 8, 64, 1, 3, None, True),
+    ("bf16", 90, 56, 32, 128, 1, 4, None, False)])
 def test_step(ssd, dt, B, H, P, N, G, K, slots, strided):
     import torch
     rng = np.random.default_rng(B + H)
@@ -279,6 +282,11 @@ NORM = [
     (33, 4100, "f32", "f32", "f32", True, "layer", False), (9, 16384, "bf16", "f32", "f32", True, "layer", False),
     (7, 8191, "bf16", "bf16", "f32", True, "layer", False), (11, 12000, "f32", None, "f32", True, "rms", False),
     (2500, 1536, "bf16", "f32", "f32", True, "layer", False),
+    # fewer vectors than a warp has lanes; two elements a vector; no multiple of anything
+    (333, 24, "bf16", "f32", "f32", True, "layer", True), (70, 128, "bf16", "bf16", "f32", True, "rms", False),
+    (41, 34, "f32", None, "f32", True, "layer", False), (19, 1030, "bf16", "f32", "f32", True, "layer", False),
+    (1000, 13, "bf16", None, "f32", True, "rms", False), (6, 6000, "bf16", None, "f32", True, "layer", True),
+    (5, 10000, "bf16", "bf16", "f32", True, "layer", False), (5, 8190, "f32", "f32", "f32", True, "layer", False),
 ]
 
 
@@ -299,7 +307,7 @@ def _norm_case(case, seed):
         t["res"] = t["dh"] = a["res"] = a["dh"] = None
     if strided:
         for k in ("x", "res", "dy", "dh"):
-            t[k] = _strided(t[k], 16, 8)
+            t[k] = None if t[k] is None else _strided(t[k], 16, 8)
     return t, a
 
 
@@ -399,6 +407,8 @@ def test_norm_of_a_large_offset_keeps_its_variance(ssd):
 # rows, D, groups, dtype, parameter type, strided
 GATED = [(1, 1, 1, "f32", "f32", False), (3, 64, 1, "bf16", "f32", True), (5, 5120, 8, "bf16", "f32", True),
          (40, 1536, 1, "bf16", "bf16", False), (33, 105, 3, "bf16", "f32", True), (600, 96, 2, "f32", "f32", True),
+         (333, 80, 10, "bf16", "f32", True), (65, 128, 8, "bf16", "f32", False), (50, 96, 6, "f32", "f32", True),
+         (1300, 640, 1, "bf16", "f32", False), (21, 4098, 1, "bf16", "f32", True), (30, 9000, 3, "f32", "f32", False),
          (9, 16384, 1, "bf16", "f32", False), (17, 999, 1, "f32", "f32", False), (2100, 1024, 4, "bf16", "f32", False)]
 
 
