@@ -49,11 +49,16 @@ struct TeamBuf {
 // the first.
 template <int N>
 __device__ __forceinline__ void team_sum(const Team& t, float* x, TeamBuf<N>& buf, int flip) {
+    if (t.width == 32) {  // the same for the block
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (o < t.width)  // the same for the block
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+    } else {
+        for (int o = t.width >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+    }
     if (t.nw == 1) return;
     if (t.lane == 0)
 #pragma unroll
@@ -173,30 +178,45 @@ constexpr int kMostStages = 8;
 struct RowBars {
     uint64_t full[4][kMostStages];  // by team of the block
 };
+// The rows of a team: first, first + by, ... below `rows` (all below 2^31).
+struct RowRange {
+    int first, by, rows;
+    __device__ __forceinline__ RowRange(long long f, long long b, long long n)
+        : first((int)(f < n ? f : n)), by((int)b), rows((int)n) {}
+    __device__ __forceinline__ int count() const {
+        return first < rows ? (int)(((unsigned)(rows - first) - 1) / (unsigned)by) + 1 : 0;
+    }
+};
+// Where a kernel's rows come from: pointers and strides in the kernel's parameters, so that an
+// address costs no register between its uses.
+template <typename T>
+__device__ __forceinline__ const T* row_at(const void* p, int row, long long stride) {
+    return static_cast<const T*>(p) + row * stride;
+}
+// From(): k -> the start of a row of tensor k.
 template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK>
 struct Rows {
     Pack<A, VEC> ra[BULK ? 1 : NV][NA];
     Pack<B, VEC> rb[BULK ? 1 : NV][NB ? NB : 1];
-    const A* pa[NA];           // the next row to load: its start, or this thread's part of it
-    const B* pb[NB ? NB : 1];
-    long long sa[NA], sb[NB ? NB : 1];  // elements from a row to the team's next
+    int next, by;              // the next row to load
     int left;                  // rows still to load
     bool in[NV];               // whether vector i lies in the row
     char* ring;                // this team's
     uint64_t* full;
     int cols, stages, fill, stage;
     uint32_t parity;
-    bool issues;               // this thread issues the copies
     Waiter waiter;
 
     static __device__ __forceinline__ int column(const Team& t, int i) {
         return ((t.warp * NV + i) * 32 + t.lane) * VEC;
     }
-    // `count` rows for this team, of `n` columns.  A barrier of the block has to come between
-    // this and start().
-    __device__ __forceinline__ void begin(const Team& t, int count, int n, int nstages, char* all,
+    // The rows of `r`, of `n` columns.  A barrier of the block has to come between this and
+    // start().
+    __device__ __forceinline__ void begin(const Team& t, const RowRange& r, int n, int nstages, char* all,
                                           RowBars* bars, int* status) {
-        left = count;
+        next = r.first;
+        by = r.by;
+        left = BULK && t.rank != 0 ? 0 : r.count();  // one thread issues the copies
         cols = n;
 #pragma unroll
         for (int i = 0; i < NV; ++i) in[i] = column(t, i) < n;
@@ -204,11 +224,10 @@ struct Rows {
             stages = nstages;
             fill = stage = 0;
             parity = 0;
-            issues = t.rank == 0;
             waiter.status = status;
             full = bars->full[t.id];
-            ring = all + (size_t)t.id * stages * row_bytes();
-            if (issues) {
+            ring = all + t.id * stages * row_bytes();
+            if (t.rank == 0) {
                 for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
                 tc::fence_mbar_init();
             }
@@ -217,74 +236,68 @@ struct Rows {
     __device__ __forceinline__ uint32_t row_bytes() const {
         return (uint32_t)cols * (NA * (int)sizeof(A) + NB * (int)sizeof(B));
     }
-    template <int K>
-    __device__ __forceinline__ void a(const Team& t, const void* p, long long row, long long by,
-                                      long long stride, int col) {
-        pa[K] = static_cast<const A*>(p) + row * stride + col + (BULK ? 0 : column(t, 0));
-        sa[K] = by * stride;
-    }
-    template <int K>
-    __device__ __forceinline__ void b(const Team& t, const void* p, long long row, long long by,
-                                      long long stride) {
-        pb[K] = static_cast<const B*>(p) + row * stride + (BULK ? 0 : column(t, 0));
-        sb[K] = by * stride;
-    }
-    __device__ __forceinline__ void start() {
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void start(const Team& t, const FA& from_a, const FB& from_b) {
         if constexpr (BULK) {
-            for (int s = 0; s < stages; ++s) issue();
+            for (int s = 0; s < stages; ++s) issue(from_a, from_b);
         } else {
-            fetch();
+            fetch(t, from_a, from_b);
         }
     }
-    __device__ __forceinline__ void advance() {
-#pragma unroll
-        for (int k = 0; k < NA; ++k) pa[k] += sa[k];
-#pragma unroll
-        for (int k = 0; k < NB; ++k) pb[k] += sb[k];
-        --left;
-    }
-    __device__ __forceinline__ void issue() {
-        if (issues && left > 0) {
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void issue(const FA& from_a, const FB& from_b) {
+        if (left > 0) {
             uint64_t* bar = &full[fill];
             char* at = ring + fill * row_bytes();
             tc::mbar_expect_tx(bar, row_bytes());
 #pragma unroll
             for (int k = 0; k < NA; ++k)
-                tc::bulk_load(at + k * cols * (int)sizeof(A), pa[k], cols * (int)sizeof(A), bar);
+                tc::bulk_load(at + k * cols * (int)sizeof(A), from_a(k, next), cols * (int)sizeof(A), bar);
             at += NA * cols * (int)sizeof(A);
 #pragma unroll
             for (int k = 0; k < NB; ++k)
-                tc::bulk_load(at + k * cols * (int)sizeof(B), pb[k], cols * (int)sizeof(B), bar);
-            advance();
+                tc::bulk_load(at + k * cols * (int)sizeof(B), from_b(k, next), cols * (int)sizeof(B), bar);
+            next += by;
+            --left;
             fill = fill + 1 == stages ? 0 : fill + 1;
         }
     }
-    __device__ __forceinline__ void fetch() {
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void fetch(const Team& t, const FA& from_a, const FB& from_b) {
         if (left <= 0) return;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
+        for (int k = 0; k < NA; ++k) {
+            const A* p = from_a(k, next) + column(t, 0);
 #pragma unroll
-                for (int k = 0; k < NA; ++k) ra[i][k].load(pa[k] + i * 32 * VEC);
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) ra[i][k].load(p + i * 32 * VEC);
+        }
 #pragma unroll
-                for (int k = 0; k < NB; ++k) rb[i][k].load(pb[k] + i * 32 * VEC);
-            }
-        advance();
+        for (int k = 0; k < NB; ++k) {
+            const B* p = from_b(k, next) + column(t, 0);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) rb[i][k].load(p + i * 32 * VEC);
+        }
+        next += by;
+        --left;
     }
     // Before the first get of a row that this team has.
     __device__ __forceinline__ void arrived() {
         if constexpr (BULK) waiter.wait(&full[stage], parity);
     }
     // After the last get of a row: registers take the next row.
-    __device__ __forceinline__ void done() {
-        if constexpr (!BULK) fetch();
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void done(const Team& t, const FA& from_a, const FB& from_b) {
+        if constexpr (!BULK) fetch(t, from_a, from_b);
     }
     // Once the whole team has done its gets (a team of one warp waits for itself here): the
     // row's place takes another.
-    __device__ __forceinline__ void reuse(const Team& t) {
+    template <typename FA, typename FB>
+    __device__ __forceinline__ void reuse(const Team& t, const FA& from_a, const FB& from_b) {
         if constexpr (BULK) {
             if (t.nw == 1) __syncwarp();
-            issue();
+            issue(from_a, from_b);
             if (++stage == stages) stage = 0, parity ^= 1;
         }
     }
@@ -292,7 +305,7 @@ struct Rows {
     // more unless a wait ran out; then it is waited for once more.
     __device__ __forceinline__ void drain() {
         if constexpr (BULK)
-            if (waiter.gone && issues)
+            if (waiter.gone)
                 for (int s = 0; s < stages; ++s) tc::mbar_wait(&full[s], parity);
     }
     __device__ __forceinline__ void get_a(const Team& t, int i, int k, typename Lanes<VEC>::V* v) const {
@@ -319,10 +332,6 @@ struct Rows {
         to_lanes<VEC>(f, v);
     }
 };
-// Rows first, first + by, ... below `rows`.
-__device__ __forceinline__ int rows_of(long long first, long long by, long long rows) {
-    return first < rows ? (int)((rows - first + by - 1) / by) : 0;
-}
 __device__ __forceinline__ float lane_sum(F2 v) {
     float f[2];
     split(v, f);

@@ -64,28 +64,25 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
     const Team t = team_of(a.nw, a.width);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
-    const long long step = (long long)a.nrb * a.teams;
-    const long long row = (long long)rb * a.teams + t.id;
+    const RowRange rows((long long)rb * a.teams + t.id, (long long)a.nrb * a.teams, a.rows);
     using In = Rows<T, T, 2, 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
-    // every team of the block takes the rounds of its first team, the last perhaps without a row
-    const int rounds = rows_of((long long)rb * a.teams, step, a.rows);
-    int mine = rows_of(row, step, a.rows);
-    in.begin(t, mine, a.n, a.stages, ring, &bars, a.status);
-    in.template a<0>(t, a.y, row, step, a.ys, g0);
-    in.template a<1>(t, a.z, row, step, a.zs, g0);
+    auto from_a = [&](int k, int row) {
+        return (k == 0 ? row_at<T>(a.y, row, a.ys) : row_at<T>(a.z, row, a.zs)) + g0;
+    };
+    auto from_b = [&](int, int) { return static_cast<const T*>(nullptr); };
+    in.begin(t, rows, a.n, a.stages, ring, &bars, a.status);
     buf.clear();  // and its barrier
-    in.start();
+    in.start(t, from_a, from_b);
     V w[NV][N];
     weights_of<VEC, NV>(a, t, g0, w);
-    T* out = static_cast<T*>(a.out) + row * a.os + g0 + In::column(t, 0);
-    const long long ostep = step * a.os, sstep = step * a.G;
-    float* stats = a.rstd ? a.rstd + row * a.G + g : nullptr;
     const float inv = a.inv, eps = a.eps;
     int flip = 0;
-    for (int round = 0; round < rounds; ++round, --mine) {
-        const bool on = mine > 0;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    int row = rows.first;
+    for (int first = rb * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
+        const bool on = row < rows.rows;
         if (on) in.arrived();
         V v[NV][N];
         V q = both<V>(0.f);
@@ -101,17 +98,15 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
                     q = fma_(v[i][e], v[i][e], q);
                 }
             }
-        in.done();
+        in.done(t, from_a, from_b);
         float sum = lane_sum(q);
         team_sum<1>(t, &sum, buf, flip);
         flip ^= 1;
-        in.reuse(t);
+        in.reuse(t, from_a, from_b);
         const float rstd = __frsqrt_rn(fmaf(sum, inv, eps));
         if (on) {
-            if (stats) {
-                if (t.rank == 0) *stats = rstd;
-                stats += sstep;
-            }
+            if (t.rank == 0 && a.rstd) a.rstd[(long long)row * a.G + g] = rstd;
+            T* out = static_cast<T*>(a.out) + row * a.os + g0 + In::column(t, 0);
             const V r = both<V>(rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -122,7 +117,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
                     store_lanes<VEC>(out + i * 32 * VEC, o);
                 }
         }
-        out += ostep;
     }
     in.drain();
 }
@@ -136,38 +130,35 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) gated_bwd_kernel(cons
     const Team t = team_of(a.nw, a.width);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
-    const long long step = (long long)a.nrb * a.teams;
-    const long long row = (long long)rb * a.teams + t.id;
+    const RowRange rows((long long)rb * a.teams + t.id, (long long)a.nrb * a.teams, a.rows);
     using In = Rows<T, T, 3, 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
-    // every team of the block takes the rounds of its first team, the last perhaps without a row
-    const int rounds = rows_of((long long)rb * a.teams, step, a.rows);
-    int mine = rows_of(row, step, a.rows);
-    in.begin(t, mine, a.n, a.stages, ring, &bars, a.status);
-    in.template a<0>(t, a.dout, row, step, a.os, g0);
-    in.template a<1>(t, a.y, row, step, a.ys, g0);
-    in.template a<2>(t, a.z, row, step, a.zs, g0);
+    auto from_a = [&](int k, int row) {
+        return (k == 0   ? row_at<T>(a.dout, row, a.os)
+                : k == 1 ? row_at<T>(a.y, row, a.ys)
+                         : row_at<T>(a.z, row, a.zs)) +
+               g0;
+    };
+    auto from_b = [&](int, int) { return static_cast<const T*>(nullptr); };
+    in.begin(t, rows, a.n, a.stages, ring, &bars, a.status);
     buf.clear();  // and its barrier
-    in.start();
+    in.start(t, from_a, from_b);
     V w[NV][N], dw[NV][N];
     weights_of<VEC, NV>(a, t, g0, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[i][e] = both<V>(0.f);
-    T* dy = static_cast<T*>(a.dy) + row * a.dys + g0 + In::column(t, 0);
-    T* dz = static_cast<T*>(a.dz) + row * a.dzs + g0 + In::column(t, 0);
-    const long long ystep = step * a.dys, zstep = step * a.dzs, sstep = step * a.G;
-    const float* stats = a.rstd_in + row * a.G + g;
     const float inv = a.inv;
-    float next = mine > 0 ? *stats : 0.f;
+    float next = rows.first < rows.rows ? a.rstd_in[(long long)rows.first * a.G + g] : 0.f;
     int flip = 0;
-    for (int round = 0; round < rounds; ++round, --mine) {
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    int row = rows.first;
+    for (int first = rb * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
         const V r = both<V>(next);
-        stats += sstep;
-        if (mine > 1) next = *stats;
-        const bool on = mine > 0;
+        if (row + rows.by < rows.rows) next = a.rstd_in[(long long)(row + rows.by) * a.G + g];
+        const bool on = row < rows.rows;
         if (on) in.arrived();
         // d = w dout, gate = silu(z), gy = y silu'(z)
         V d[NV][N], xh[NV][N], gate[NV][N], gy[NV][N];
@@ -191,13 +182,15 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) gated_bwd_kernel(cons
                     s = fma_(d[i][e], xh[i][e], s);
                 }
             }
-        in.done();
+        in.done(t, from_a, from_b);
         float sum = lane_sum(s);
         team_sum<1>(t, &sum, buf, flip);
         flip ^= 1;
-        in.reuse(t);
+        in.reuse(t, from_a, from_b);
         if (on) {
             const V c2 = both<V>(-sum * inv);
+            T* dy = static_cast<T*>(a.dy) + row * a.dys + g0 + In::column(t, 0);
+            T* dz = static_cast<T*>(a.dz) + row * a.dzs + g0 + In::column(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in.in[i]) {
@@ -212,8 +205,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) gated_bwd_kernel(cons
                     store_lanes<VEC>(dz + i * 32 * VEC, oz);
                 }
         }
-        dy += ystep;
-        dz += zstep;
     }
     float* part = a.partial + (long long)rb * a.D + g0;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
@@ -253,7 +244,7 @@ ssd_status_t check_gated(const ssd_gated_norm_t* p) {
     if (p->y_stride < p->dim || p->z_stride < p->dim || p->out_stride < p->dim ||
         p->dy_stride < p->dim || p->dz_stride < p->dim)
         return SSD_ERR_INVALID_ARG;
-    if (p->rows > INT_MAX || p->rows * p->groups > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    if (p->rows > INT_MAX - (1 << 20) || p->rows * p->groups > INT_MAX) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

@@ -73,31 +73,25 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
     __shared__ TeamBuf<1> buf;
     extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw, a.width);
-    const long long step = (long long)gridDim.x * a.teams;
-    long long row = (long long)blockIdx.x * a.teams + t.id;
+    const RowRange rows((long long)blockIdx.x * a.teams + t.id, (long long)gridDim.x * a.teams, a.rows);
     using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
-    // every team of the block takes the rounds of its first team, the last perhaps without a row
-    const int rounds = rows_of((long long)blockIdx.x * a.teams, step, a.rows);
-    int mine = rows_of(row, step, a.rows);
-    in.begin(t, mine, a.D, a.stages, ring, &bars, a.status);
-    in.template a<0>(t, a.x, row, step, a.xs, 0);
-    if constexpr (RES) in.template b<0>(t, a.res, row, step, a.rs);
+    auto from_a = [&](int, int row) { return row_at<T>(a.x, row, a.xs); };
+    auto from_b = [&](int, int row) { return row_at<TR>(a.res, row, a.rs); };
+    in.begin(t, rows, a.D, a.stages, ring, &bars, a.status);
     buf.clear();  // and its barrier
-    in.start();
+    in.start(t, from_a, from_b);
     V w[NV][N], b[NV][N];
     columns_of<VEC, NV>(a.w, t, a.D, a.wbf16, w);
     columns_of<VEC, NV>(a.b, t, a.D, a.wbf16, b);
-    T* y = static_cast<T*>(a.y) + row * a.ys + In::column(t, 0);
-    TR* h = static_cast<TR*>(a.h) + row * a.hs + In::column(t, 0);
-    const long long ystep = step * a.ys, hstep = step * a.hs;
-    float2* stats = a.stats ? a.stats + row : nullptr;
     const bool layer = a.layer;
     const float inv = a.inv, eps = a.eps;
     int flip = 0;
-    for (int round = 0; round < rounds; ++round, --mine) {
-        const bool on = mine > 0;
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    int row = rows.first;
+    for (int first = blockIdx.x * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
+        const bool on = row < rows.rows;
         if (on) in.arrived();
         V v[NV][N];
         V s = both<V>(0.f);
@@ -110,7 +104,7 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
                     in.get_b(t, i, 0, r);
 #pragma unroll
                     for (int e = 0; e < N; ++e) v[i][e] = add_(v[i][e], r[e]);
-                    store_lanes<VEC>(h + i * 32 * VEC, v[i]);
+                    store_lanes<VEC>(static_cast<TR*>(a.h) + row * a.hs + In::column(t, i), v[i]);
                 }
 #pragma unroll
                 for (int e = 0; e < N; ++e) s = add_(s, v[i][e]);
@@ -119,13 +113,13 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
                 for (int e = 0; e < N; ++e) v[i][e] = both<V>(0.f);
             }
         }
-        in.done();
+        in.done(t, from_a, from_b);
         float mean = 0.f;
         if (layer) {
             float m = lane_sum(s);
             team_sum<1>(t, &m, buf, flip);
             flip ^= 1;
-            in.reuse(t);
+            in.reuse(t, from_a, from_b);
             mean = m * inv;
         }
         const V minus = both<V>(-mean);
@@ -141,13 +135,11 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
         float var = lane_sum(q);
         team_sum<1>(t, &var, buf, flip);
         flip ^= 1;
-        if (!layer) in.reuse(t);
+        if (!layer) in.reuse(t, from_a, from_b);
         const float rstd = __frsqrt_rn(fmaf(var, inv, eps));
         if (on) {
-            if (stats) {
-                if (t.rank == 0) *stats = make_float2(mean, rstd);
-                stats += step;
-            }
+            if (t.rank == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
+            T* y = static_cast<T*>(a.y) + row * a.ys + In::column(t, 0);
             const V r = both<V>(rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -158,8 +150,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
                     store_lanes<VEC>(y + i * 32 * VEC, o);
                 }
         }
-        y += ystep;
-        h += hstep;
     }
     in.drain();
 }
@@ -173,39 +163,33 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) norm_bwd_kernel(const
     __shared__ TeamBuf<2> buf;
     extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw, a.width);
-    const long long step = (long long)gridDim.x * a.teams;
-    const long long row = (long long)blockIdx.x * a.teams + t.id;
+    const RowRange rows((long long)blockIdx.x * a.teams + t.id, (long long)gridDim.x * a.teams, a.rows);
     using In = Rows<T, TR, 1, DH ? 2 : 1, VEC, NV, BULK>;
     In in;
     __shared__ RowBars bars;
-    // every team of the block takes the rounds of its first team, the last perhaps without a row
-    const int rounds = rows_of((long long)blockIdx.x * a.teams, step, a.rows);
-    int mine = rows_of(row, step, a.rows);
-    in.begin(t, mine, a.D, a.stages, ring, &bars, a.status);
-    in.template a<0>(t, a.dy, row, step, a.ys, 0);
-    in.template b<0>(t, a.hin, row, step, a.hs);
-    if constexpr (DH) in.template b<1>(t, a.dh, row, step, a.rs);
+    auto from_a = [&](int, int row) { return row_at<T>(a.dy, row, a.ys); };
+    auto from_b = [&](int k, int row) {
+        return DH && k == 1 ? row_at<TR>(a.dh, row, a.rs) : row_at<TR>(a.hin, row, a.hs);
+    };
+    in.begin(t, rows, a.D, a.stages, ring, &bars, a.status);
     buf.clear();  // and its barrier
-    in.start();
+    in.start(t, from_a, from_b);
     V w[NV][N], dw[NV][N], db[NV][N];
     columns_of<VEC, NV>(a.w, t, a.D, a.wbf16, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = both<V>(0.f);
-    T* dx = static_cast<T*>(a.dx) + row * a.xs + In::column(t, 0);
-    TR* dres = static_cast<TR*>(a.dres) + row * a.D + In::column(t, 0);
-    const long long xstep = step * a.xs, rstep = step * a.D;
-    const float2* stats = a.stats_in + row;
     const bool both_out = !SAME || a.dres;
     const float inv = a.inv, inv1 = a.layer ? a.inv : 0.f;
-    float2 next = mine > 0 ? *stats : make_float2(0.f, 0.f);
+    float2 next = rows.first < rows.rows ? a.stats_in[rows.first] : make_float2(0.f, 0.f);
     int flip = 0;
-    for (int round = 0; round < rounds; ++round, --mine) {
+    // every team of the block takes the rounds of its first team, the last perhaps without a row
+    int row = rows.first;
+    for (int first = blockIdx.x * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
         const float2 st = next;
-        stats += step;
-        if (mine > 1) next = *stats;
-        const bool on = mine > 0;
+        if (row + rows.by < rows.rows) next = a.stats_in[row + rows.by];
+        const bool on = row < rows.rows;
         if (on) in.arrived();
         V xh[NV][N], d[NV][N], g[NV][N];
         V s0 = both<V>(0.f), s1 = both<V>(0.f);
@@ -226,13 +210,15 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) norm_bwd_kernel(const
                     s1 = fma_(d[i][e], xh[i][e], s1);
                 }
             }
-        in.done();
+        in.done(t, from_a, from_b);
         float sum[2] = {lane_sum(s0), lane_sum(s1)};
         team_sum<2>(t, sum, buf, flip);
         flip ^= 1;
-        in.reuse(t);
+        in.reuse(t, from_a, from_b);
         if (on) {
             const V c1 = both<V>(-sum[0] * inv1), c2 = both<V>(-sum[1] * inv);
+            T* dx = static_cast<T*>(a.dx) + row * a.xs + In::column(t, 0);
+            TR* dres = static_cast<TR*>(a.dres) + (long long)row * a.D + In::column(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in.in[i]) {
@@ -249,8 +235,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) norm_bwd_kernel(const
                     if (both_out) store_lanes<VEC>(dres + i * 32 * VEC, o);
                 }
         }
-        dx += xstep;
-        dres += rstep;
     }
     float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
@@ -300,7 +284,7 @@ ssd_status_t check_norm(const ssd_norm_t* p) {
         return SSD_ERR_INVALID_ARG;
     // the residual stream is kept in the activations' type or in float32
     if (p->dtype == SSD_DTYPE_F32 && p->rdtype != SSD_DTYPE_F32) return SSD_ERR_UNSUPPORTED;
-    if (p->rows > INT_MAX) return SSD_ERR_UNSUPPORTED;
+    if (p->rows > INT_MAX - (1 << 20)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
