@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ssd.h"
 
 namespace ssd {
@@ -166,10 +168,13 @@ bool tc_supported(int dtype, int P, int N, int Q, int H, int G);
 
 // SMs of the current device (persistent grids size themselves by it).
 inline int sm_count() {
+    static std::atomic<int> known[64];  // by device
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load()) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
         return 1;
+    if (dev >= 0 && dev < 64) known[dev].store(n);
     return n;
 }
 
