@@ -27,9 +27,9 @@ from ._lib import SSDError, check
 __all__ = ["forward", "backward", "bidirectional_forward", "bidirectional_backward", "decode_step", "step_host", "step_host_size", "workspace_size",
            "dispatch_path", "make_problem", "last_launch_count", "profiler", "SSDError",
            "conv_forward", "conv_backward", "conv_decode_step", "norm_forward", "norm_backward",
-           "gated_norm_forward", "gated_norm_backward"]
+           "gated_norm_forward", "gated_norm_backward", "layer_status"]
 
-_LAYER = frozenset(__all__[-7:])
+_LAYER = frozenset(__all__[-8:])
 
 
 def __getattr__(name):

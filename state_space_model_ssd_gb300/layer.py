@@ -7,13 +7,15 @@
     n, h, stats = norm_forward(x, w_norm, b_norm, residual=h)
 
 and their backward passes.  Activations are float32 or bfloat16 CUDA tensors; their rows may
-be strided (a slice of the in-projection's output), with neighbouring channels adjacent.
+be strided (a slice of the in-projection's output) as long as they are evenly spaced over all
+leading dimensions, with neighbouring channels adjacent.
 Weights and biases are float32 or bfloat16.  With ``stream`` the call runs there, and what it
 allocates belongs to that stream.
 """
 
 from __future__ import annotations
 
+import ctypes
 import os
 
 import torch
@@ -21,7 +23,7 @@ import torch
 from . import _lib
 
 __all__ = ["conv_forward", "conv_backward", "conv_decode_step", "norm_forward", "norm_backward",
-           "gated_norm_forward", "gated_norm_backward"]
+           "gated_norm_forward", "gated_norm_backward", "layer_status"]
 
 if not os.path.exists(os.path.join(_lib.PKG, "_layer_ext.so")):
     raise RuntimeError("_layer_ext.so is not built; run state_space_model_ssd_gb300/build.py or "
@@ -142,3 +144,14 @@ def gated_norm_backward(dout, y, z, weight, rstd, groups: int = 1, out=None, wor
     in-projection's gradient)."""
     args = (dout, y, z, weight, rstd, groups, out, workspace)
     return _ext.gated_norm_backward(*args) if stream is None else _on(stream, _ext.gated_norm_backward, *args)
+
+
+def layer_status(stream=None) -> int:
+    """Waits for ``stream`` (default: the current one) and returns what the calls of this module
+    have recorded on the current device since the last query: 0, or the code of SSD_ERR_TIMEOUT
+    if a kernel's bounded wait ran out (its outputs are then not valid)."""
+    v = ctypes.c_int32(0)
+    s = torch.cuda.current_stream() if stream is None else stream
+    _lib.check(_lib.lib().ssd_layer_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(v)),
+               "ssd_layer_status")
+    return int(v.value)

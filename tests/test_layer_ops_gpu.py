@@ -568,3 +568,8 @@ def test_offsets_beyond_32_bits(ssd):
     want, _, _ = ref.norm(u[0, T - 64:].double().cpu().numpy(), w[:, 0].double().cpu().numpy(), None, None,
                           1e-5, False)
     ref.assert_close(x[0, T - 64:], want, "bf16", "norm")
+
+
+def test_no_wait_ran_out(ssd):
+    """The operators' status word after everything above, and after a query."""
+    assert ssd.layer_status() == 0 and ssd.layer_status() == 0
