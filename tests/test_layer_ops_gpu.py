@@ -570,6 +570,74 @@ def test_offsets_beyond_32_bits(ssd):
     ref.assert_close(x[0, T - 64:], want, "bf16", "norm")
 
 
+@pytest.mark.parametrize("D", [24, 100, 256, 1000, 2560])
+def test_rows_do_not_touch_one_another(ssd, D):
+    """A row of NaN and one of infinities leave every other row's result alone."""
+    import torch
+    R = 37
+    t, _ = _norm_case((R, D, "bf16", "f32", "f32", True, "layer", False), 20)
+    y, h, st = ssd.norm_forward(t["x"], t["w"], t["b"], residual=t["res"])
+    g = ssd.norm_backward(t["dy"], h, t["w"], st, dh=t["dh"])
+    gt, _ = _gated_case((R, D, 1, "bf16", "f32", False), 21)
+    o, r = ssd.gated_norm_forward(gt["y"], gt["z"], gt["w"])
+    gg = ssd.gated_norm_backward(gt["dout"], gt["y"], gt["z"], gt["w"], r)
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    for row, v in ((5, float("nan")), (18, float("inf"))):
+        t["x"][row], gt["y"][row], h[row], t["dy"][row] = v, v, v, v
+        keep[row] = False
+    y2, _, _ = ssd.norm_forward(t["x"], t["w"], t["b"], residual=t["res"])
+    g2 = ssd.norm_backward(t["dy"], h, t["w"], st, dh=t["dh"])
+    o2, _ = ssd.gated_norm_forward(gt["y"], gt["z"], gt["w"])
+    gg2 = ssd.gated_norm_backward(gt["dout"], gt["y"], gt["z"], gt["w"], r)
+    for a, b in ((y, y2), (g["dx"], g2["dx"]), (o, o2), (gg["dy"], gg2["dy"]), (gg["dz"], gg2["dz"])):
+        assert bool((a[keep] == b[keep]).all())
+        assert not bool(torch.isfinite(b[5]).any())
+
+
+def test_in_a_cuda_graph(ssd):
+    """A captured step and training pass give, replayed on new inputs, what the calls give."""
+    import torch
+    H, P, N, K = 8, 64, 64, 4
+    C = H * P + 2 * N
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rnd(*s, dt=torch.bfloat16):
+        return torch.randn(*s, generator=gen, device="cuda").to(dt)
+
+    w, b, gw = rnd(C, K, dt=torch.float32), rnd(C, dt=torch.float32), rnd(H * P, dt=torch.float32)
+    u, tok, raw = rnd(1, 500, C), rnd(3, C), rnd(3, H, dt=torch.float32)
+    z = rnd(1, 500, H * P)
+    state, win = rnd(3, H, P, N, dt=torch.float32), rnd(3, K, C)
+    pos = torch.tensor([4, 9, 2], dtype=torch.int32, device="cuda")
+    split = ((H, P), (1, N), (1, N))
+
+    def work():
+        outs, _ = ssd.conv_forward(u, w, b, split=split)
+        o, r = ssd.gated_norm_forward(outs[0], z, gw)
+        gn = ssd.gated_norm_backward(o, outs[0], z, gw, r)
+        g = ssd.conv_backward(u, w, b, (gn["dy"], outs[1], outs[2]))
+        y = ssd.conv_decode_step(state, win, tok, raw, w, b, pos, -4.6)
+        return [o, gn["d_weight"], g["du"], g["d_weight"], g["d_bias"], y, state, win]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = work()
+    for t in (u, tok, z):
+        t.copy_(rnd(*t.shape))
+    s0, w0 = state.clone(), win.clone()
+    graph.replay()
+    got = [t.clone() for t in captured]
+    state.copy_(s0)
+    win.copy_(w0)
+    for x, y in zip(got, work()):
+        assert bool((x == y).all())
+
+
 def test_no_wait_ran_out(ssd):
     """The operators' status word after everything above, and after a query."""
     assert ssd.layer_status() == 0 and ssd.layer_status() == 0
