@@ -141,7 +141,7 @@ __device__ __forceinline__ void step_rows(float4* s4, float4 (&piece)[kPieces], 
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 3) conv_step_kernel(const StepArgs a) {
     __shared__ __align__(16) float xs[kMostHeads][128], bs[128], cs[128];
     __shared__ float decays[kMostHeads];
     const int row = blockIdx.y;
@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepAr
 
     const int g = h0 / (a.H / a.G);
     const int pos = a.pos[row];
+    const float* raw = a.raw + (long long)row * a.H + h0;
     if (threadIdx.x >= kStepThreads - a.heads) {  // the threads with the fewest channels
         const int h = kStepThreads - 1 - threadIdx.x;
-        const float delta = softplus_f(a.raw[(long long)row * a.H + h0 + h] + a.delta_init);
-        decays[h] = delta;  // the decay follows below
+        decays[h] = expf(-softplus_f(raw[h] + a.delta_init));
     }
     int at[K];  // at[j]: the window's row of position pos - j
 #pragma unroll
@@ -197,30 +197,13 @@ __global__ void __launch_bounds__(kStepThreads, 4) conv_step_kernel(const StepAr
         if (j < 0 || owns_bc) win[at[0] * a.C + c] = tok;
         v *= sigmoid_of<T>(v);
         if (j < 0)
-            xs[0][i] = v;  // heads of PR channels one after the other
+            xs[0][i] = v * softplus_f(raw[i / PR] + a.delta_init);  // PR channels a head
         else if (j < a.N)
             bs[j] = v;
         else
             cs[j - a.N] = v;
     }
     __syncthreads();
-    // delta into x, then the decays in its place
-    float scaled[(kMostHeads * 128) / kStepThreads];
-#pragma unroll
-    for (int k = 0; k < (kMostHeads * 128) / kStepThreads; ++k) {
-        const int i = k * kStepThreads + threadIdx.x;
-        if (i < nx) scaled[k] = xs[0][i] * decays[i / PR];
-    }
-    const float decay0 = threadIdx.x < a.heads ? expf(-decays[threadIdx.x]) : 0.f;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < (kMostHeads * 128) / kStepThreads; ++k) {
-        const int i = k * kStepThreads + threadIdx.x;
-        if (i < nx) xs[0][i] = scaled[k];
-    }
-    if (threadIdx.x < a.heads) decays[threadIdx.x] = decay0;
-    __syncthreads();
-
     for (int h = 0; h < a.heads; ++h) {
         if (h > 0)
 #pragma unroll
@@ -296,11 +279,12 @@ ssd_status_t ssd_conv_decode_step(const ssd_problem_t* prob, int32_t width, int3
     const long long units = p.batch * p.nheads, want = 2LL * sm_count();
     while (units * a.split < want && p.headdim / (2 * a.split) * (p.dstate / 4) >= kStepThreads)
         a.split *= 2;
-    // Heads a CTA: while that leaves two rounds of the four CTAs an SM holds.
+    // Heads a CTA: while that leaves five rounds of the three CTAs an SM holds, so that the last,
+    // partly filled one weighs little (128 rows of 80 heads: 4 heads 111 us, 8 122, 1 139).
     a.heads = 1;
     const int per_group = p.nheads / p.ngroups;
     while (a.split == 1 && a.heads < kMostHeads && per_group % (2 * a.heads) == 0 &&
-           units / (2 * a.heads) >= 8LL * sm_count())
+           units / (2 * a.heads) >= 15LL * sm_count())
         a.heads *= 2;
     for (int n = p.dstate / 4; n > 1; n >>= 1) ++a.log_n4;
     const dim3 grid((unsigned)(p.nheads / a.heads * a.split), (unsigned)p.batch);
