@@ -743,22 +743,41 @@ constexpr int kMostBwd = 4;  // 8 bytes of bf16: the sums take the registers of 
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// Tokens a thread walks.  Long runs re-read less (K-1 tokens a run) but leave fewer threads:
-// the longest power of two up to `most` that still gives every SM `want` threads.
-int choose_run(long long T, long long nvec, int most, int want) {
-    const long long need = (long long)sm_count() * want;
-    int run = most;
-    while (run > 1 && (T + run - 1) / run * nvec < need) run >>= 1;
-    return run;
+// Blocks of channels: none straddles two pieces.
+int channel_blocks(const ssd_conv_t* p, int vec) {
+    const int wide = kLanes * vec;
+    return ceil_div(p->split[0], wide) + ceil_div(p->split[1], wide) + ceil_div(p->split[2], wide);
 }
 
-// Blocks along the tokens of the backward: the partial sums' count, and with it the
-// workspace, follows it; at most kMaxRunBlocks.
-constexpr int kMaxRunBlocks = 1024;
-int bwd_run(long long T, long long C, int vec) {
-    int run = choose_run(T, (C + vec - 1) / vec, 64, 1024);
-    while ((T + (long long)run * kRuns - 1) / ((long long)run * kRuns) > kMaxRunBlocks) run <<= 1;
-    return run;
+// Tokens a warp walks: the run with the shortest estimated time, which is the rounds of blocks
+// (two an SM; three in short vectors) times a run and `over` tokens' worth of starting and
+// ending it.  Few tokens get short runs, many the length that fills the last round: 65536
+// tokens of 1792 channels took 90 us in runs of 64 (3.4 rounds).  Whole groups of eight tokens
+// but for the shortest; `most` blocks along the tokens.
+int choose_run(long long T, int nch, int vec, int over, long long most) {
+    const long long at_once = (long long)sm_count() * (vec > 2 ? 2 : 3);
+    long long best = -1;
+    int pick = 1;
+    for (long long run = 1; run <= (1 << 28); run = run < 8 ? run * 2 : run < 128 ? run + 8 : run * 2) {
+        const long long nb = (T + run * kRuns - 1) / (run * kRuns);
+        if (nb > most) continue;
+        const long long cost = (nb * nch + at_once - 1) / at_once * (run + over);
+        if (best >= 0 && cost >= best) {
+            if (run >= 128) break;
+            continue;
+        }
+        best = cost;
+        pick = (int)run;
+    }
+    return pick;
+}
+int fwd_run(const ssd_conv_t* p, long long T, int vec) {
+    return choose_run(T, channel_blocks(p, vec), vec, 8, 1LL << 40);
+}
+// Blocks along the tokens of the backward: the partial sums' count, and with it the workspace,
+// follows it.
+int bwd_run(const ssd_conv_t* p, long long T, int vec) {
+    return choose_run(T, channel_blocks(p, vec), vec, 13, 1024);
 }
 
 void fill_args(const ssd_conv_t* p, const Conv& c, int vec, ConvArgs* a) {
@@ -773,7 +792,7 @@ void fill_args(const ssd_conv_t* p, const Conv& c, int vec, ConvArgs* a) {
     const int wide = kLanes * vec;
     a->blk1 = ceil_div(p->split[0], wide);
     a->blk2 = a->blk1 + ceil_div(p->split[1], wide);
-    a->nchblk = a->blk2 + ceil_div(p->split[2], wide);
+    a->nchblk = channel_blocks(p, vec);
     a->nseq = c.nseq;
     a->wbf16 = p->wdtype == SSD_DTYPE_BF16;
 }
@@ -899,8 +918,7 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
     a.u = u, a.w = weight, a.b = bias, a.cu = cu_seqlens, a.pos = positions;
     a.init = initial_state, a.final_state = final_state;
     for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
-    const long long nvec = c.C / vec;
-    a.run = choose_run(c.T, nvec, 64, 1024);
+    a.run = fwd_run(conv, c.T, vec);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = final_state ? ceil_div(srows, kRuns) : 0;
     const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);
@@ -922,7 +940,7 @@ ssd_status_t ssd_conv_workspace_size(const ssd_conv_t* conv, size_t* bytes) {
     if (st != SSD_OK) return st;
     size_t most = 0;
     for (int vec = kMostBwd; vec >= 1; vec = vec > 2 ? 2 : vec - 1) {  // any may run, by the pointers' alignment
-        const int nb = ceil_div(c.T, (long long)bwd_run(c.T, c.C, vec) * kRuns);
+        const int nb = ceil_div(c.T, (long long)bwd_run(conv, c.T, vec) * kRuns);
         const size_t n = sizeof(float) * (size_t)nb * (conv->width + 1) * c.C;
         if (n > most) most = n;
     }
@@ -982,8 +1000,7 @@ ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void
     a.init = initial_state, a.dfinal = d_final_state, a.du = du, a.dinit = d_initial_state;
     for (int i = 0; i < 3; ++i) a.out[i] = const_cast<void*>(douts[i]);
     a.partial = static_cast<float*>(workspace);
-    const long long nvec = c.C / vec;
-    a.run = bwd_run(c.T, c.C, vec);
+    a.run = bwd_run(conv, c.T, vec);
     a.nrunblk = ceil_div(c.T, (long long)a.run * kRuns);
     const int nstate = d_initial_state ? ceil_div(srows, kRuns) : 0;
     const long long grid = (long long)a.nchblk * (a.nrunblk + nstate);
