@@ -146,7 +146,7 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
         if (nw > 32 || warps == 0) continue;
         if (warps > 16) warps = 16;
         double c = nw * (14.0 + nv * vec) / warps;
-        if (cost.bwd && nv * vec > 8) c *= 1.25;  // as measured: 392 us against 364 in 8 groups of 640
+        if (cost.bwd && nv * vec > 8) c *= 1.25;  // as measured: 392 us against 332 in 8 groups of 640
         if (best >= 0 && c >= best) continue;
         best = c;
         p->nv = nv;
@@ -158,10 +158,10 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     p->teams = p->nw == 1 ? 128 / p->width : 1;
     p->per_sm = resident_warps(row_regs(vec, p->nv, cost.bwd, p->bulk)) / (p->threads() / 32);
     if (p->per_sm > 16) p->per_sm = 16;
-    // With rows on their way in bulk, sixteen warps are enough, and fewer blocks with more rows
-    // each in flight do better: 222 us against 242 at 32768 x 2560 with one block of ten warps
-    // an SM instead of two.
-    if (p->bulk && p->per_sm * p->threads() > 512) p->per_sm = 512 / p->threads() > 1 ? 512 / p->threads() : 1;
+    // Where a row's arithmetic is little, sixteen warps are enough, and fewer blocks with more
+    // rows each on their way do better: 222 us against 242 at 32768 x 2560 with one block of ten
+    // warps an SM instead of two.  Not so the gated rows (332 us against 365 in 8 groups of 640).
+    if (p->bulk && cost.nb > 0 && p->per_sm * p->threads() > 512) p->per_sm = 512 / p->threads() > 1 ? 512 / p->threads() : 1;
     p->stages = 0;
     p->ring = 0;
     if (p->bulk) {

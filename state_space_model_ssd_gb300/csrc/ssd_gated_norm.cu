@@ -9,6 +9,10 @@
 //
 // Bound by HBM (three tensors forward, five backward).  A (row, group) is one row of a team;
 // blocks stay with one group, so that the backward's dw stays in registers.
+//
+// GB300, 32768 x 5120, bf16: forward 156 us (95 % of the measured copy rate); backward 287 us in
+// one group (86 %), 330 in eight (75 %: three warps a row of 640 columns leave a sixth of their
+// lanes idle and share out the sums' fixed cost less well).
 #include <limits.h>
 
 #include "layer_device.cuh"

@@ -13,6 +13,10 @@
 // once, the variance is the two-pass one (sums of squares of v - mu), and in the backward a
 // block keeps its columns' dw and db in registers over all the rows it takes; a second
 // kernel adds the blocks' partial sums in a fixed order.
+//
+// GB300, 32768 x 2560, bf16 with a float32 residual: forward 154 us (97 % of the measured copy
+// rate), backward 228 us (87 %, its partial sums included); without a residual 83 and 109 us
+// (60 and 68 %), where the sums over a row and the two passes over its elements bound them.
 #include <limits.h>
 
 #include "layer_device.cuh"
