@@ -1,6 +1,6 @@
 // Device helpers of the operators around the scan (convolution, norms): vector loads that
-// keep their 16 bytes packed until they are used, the SiLU and its derivative, sums over a
-// team of warps, and the reduction of per-block partial sums.
+// keep their 16 bytes packed until they are used, bounded waits, parameters of either type, the
+// sigmoid, and pairs of channels in one register pair.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -32,13 +32,6 @@ struct Pack<float, 4> {
     __device__ __forceinline__ void get(float* f) const {
         f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
     }
-};
-template <>
-struct Pack<float, 8> {
-    Pack<float, 4> a, b;
-    __device__ __forceinline__ void load(const float* p) { a.load(p), b.load(p + 4); }
-    __device__ __forceinline__ void zero() { a.zero(), b.zero(); }
-    __device__ __forceinline__ void get(float* f) const { a.get(f), b.get(f + 4); }
 };
 __device__ __forceinline__ void unpack2(uint32_t w, float* f) {
     f[0] = __uint_as_float(w << 16);

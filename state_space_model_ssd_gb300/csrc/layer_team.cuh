@@ -97,6 +97,7 @@ struct RowPlan {
     int nw;      // warps in a team
     int width;   // lanes of a warp in a team
     int teams;   // teams in a block
+    int regs;    // registers of a thread
     int per_sm;  // blocks an SM holds at once
     bool bulk;   // rows arrive by bulk copies (or through registers)
     int stages;  // rows in flight then
@@ -107,12 +108,15 @@ struct RowPlan {
 constexpr int most_columns(int vec) { return vec >= 4 ? 16384 : 8192; }
 constexpr int most_vectors(int vec) { return vec == 8 ? 4 : vec == 1 ? 16 : 8; }
 // Registers of a thread that holds e elements of a row: what the kernels need without spilling
-// (a backward spills beyond 24 elements, on rows of more than 9216 columns), and no more, since
-// they decide how many rows an SM works on.
-constexpr int row_regs(int vec, int nv, bool bwd, bool bulk) {
+// (up to 16 elements; more are held only on the longest rows), and no more, since they decide
+// how many rows an SM works on.
+constexpr int fwd_regs(int vec, int nv) {
     const int e = vec * nv;
-    if (bwd) return e <= 2 ? 56 : e <= 4 ? (bulk ? 64 : 80) : e <= 8 ? (bulk ? 96 : 112) : 128;
-    return e <= 2 ? 40 : e <= 4 ? 56 : e <= 8 ? (bulk ? 64 : 80) : e <= 16 ? (bulk ? 96 : 128) : 128;
+    return e <= 2 ? 40 : e <= 4 ? 56 : e <= 8 ? 80 : 128;
+}
+constexpr int bwd_regs(int vec, int nv, bool bulk) {
+    const int e = vec * nv;
+    return e <= 2 ? 56 : e <= 4 ? (bulk ? 64 : 80) : e <= 8 ? (bulk ? 96 : 112) : 128;
 }
 // What a row's plan goes by: the tensors read, na of `ab` bytes an element and nb of `bb`.
 struct RowCost {
@@ -142,7 +146,8 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
         // against 529 through registers, which its sums need.  A forward has registers to spare
         // (158 against 175 us at 32768 x 2560).
         const bool bulk = cost.bwd && vec >= 4 && nvec > 32;
-        int warps = resident_warps(row_regs(vec, nv, cost.bwd, bulk)) / (nw * teams) * (nw * teams);
+        const int regs = cost.bwd ? bwd_regs(vec, nv, bulk) : fwd_regs(vec, nv);
+        int warps = resident_warps(regs) / (nw * teams) * (nw * teams);
         if (nw > 32 || warps == 0) continue;
         if (warps > 16) warps = 16;
         double c = nw * (14.0 + nv * vec) / warps;
@@ -152,11 +157,12 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
         p->nv = nv;
         p->nw = nw;
         p->bulk = bulk;
+        p->regs = regs;
     }
     if (best < 0) return false;
     p->width = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
     p->teams = p->nw == 1 ? 128 / p->width : 1;
-    p->per_sm = resident_warps(row_regs(vec, p->nv, cost.bwd, p->bulk)) / (p->threads() / 32);
+    p->per_sm = resident_warps(p->regs) / (p->threads() / 32);
     if (p->per_sm > 16) p->per_sm = 16;
     // Where a row's arithmetic is little, sixteen warps are enough, and fewer blocks with more
     // rows each on their way do better: 222 us against 242 at 32768 x 2560 with one block of ten
@@ -176,8 +182,8 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     return true;
 }
 // The tensors of a team's rows on their way to its threads: by bulk copies into a ring of
-// `stages` rows in shared memory, which one thread of the team issues, or, in vectors of less
-// than 16 bytes, through registers one row ahead.  The first NA tensors have elements of type A,
+// `stages` rows in shared memory, which one thread of the team issues (backwards of a warp and
+// more in vectors of 16 bytes), or through registers one row ahead.  The first NA tensors have elements of type A,
 // the NB others of type B.
 constexpr int kMostStages = 8;
 struct RowBars {

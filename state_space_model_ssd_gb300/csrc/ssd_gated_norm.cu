@@ -59,24 +59,22 @@ __device__ __forceinline__ void weights_of(const GatedArgs& a, const Team& t, in
     }
 }
 
-template <typename T, int VEC, int NV, bool BULK>
-__global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(const GatedArgs a) {
+template <typename T, int VEC, int NV>
+__global__ void __maxnreg__(fwd_regs(VEC, NV)) gated_fwd_kernel(const GatedArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
-    extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw, a.width);
     const int g = blockIdx.x % a.G, rb = blockIdx.x / a.G;
     const int g0 = g * a.n;
     const RowRange rows((long long)rb * a.teams + t.id, (long long)a.nrb * a.teams, a.rows);
-    using In = Rows<T, T, 2, 0, VEC, NV, BULK>;
+    using In = Rows<T, T, 2, 0, VEC, NV, false>;
     In in;
-    __shared__ RowBars bars;
     auto from_a = [&](int k, int row) {
         return (k == 0 ? row_at<T>(a.y, row, a.ys) : row_at<T>(a.z, row, a.zs)) + g0;
     };
     auto from_b = [&](int, int) { return static_cast<const T*>(nullptr); };
-    in.begin(t, rows, a.n, a.stages, ring, &bars, a.status);
+    in.begin(t, rows, a.n, 0, nullptr, nullptr, nullptr);
     buf.clear();  // and its barrier
     in.start(t, from_a, from_b);
     V w[NV][N];
@@ -87,7 +85,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
     int row = rows.first;
     for (int first = rb * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
         const bool on = row < rows.rows;
-        if (on) in.arrived();
         V v[NV][N];
         V q = both<V>(0.f);
 #pragma unroll
@@ -106,7 +103,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
         float sum = lane_sum(q);
         team_sum<1>(t, &sum, buf, flip);
         flip ^= 1;
-        in.reuse(t, from_a, from_b);
         const float rstd = __frsqrt_rn(fmaf(sum, inv, eps));
         if (on) {
             if (t.rank == 0 && a.rstd) a.rstd[(long long)row * a.G + g] = rstd;
@@ -122,11 +118,10 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) gated_fwd_kernel(con
                 }
         }
     }
-    in.drain();
 }
 
 template <typename T, int VEC, int NV, bool BULK>
-__global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) gated_bwd_kernel(const GatedArgs a) {
+__global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const GatedArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
@@ -275,9 +270,9 @@ cudaError_t launch_mode(const RowPlan& p, unsigned grid, const GatedArgs& a, cud
         if constexpr (BWD)
             return &gated_bwd_kernel<T, VEC, NV, BULK>;
         else
-            return &gated_fwd_kernel<T, VEC, NV, BULK>;
+            return &gated_fwd_kernel<T, VEC, NV>;
     }();
-    const size_t smem = BWD ? bwd_smem(p, a.n) : p.ring;
+    const size_t smem = BWD ? bwd_smem(p, a.n) : 0;
     const cudaError_t e = allow_smem<kernel>(smem);
     if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
     return e;

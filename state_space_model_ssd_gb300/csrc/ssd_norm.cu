@@ -70,20 +70,18 @@ __device__ __forceinline__ void columns_of(const void* p, const Team& t, int col
 }
 
 // RES: with a residual.
-template <typename T, typename TR, bool RES, int VEC, int NV, bool BULK>
-__global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(const NormArgs a) {
+template <typename T, typename TR, bool RES, int VEC, int NV>
+__global__ void __maxnreg__(fwd_regs(VEC, NV)) norm_fwd_kernel(const NormArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     __shared__ TeamBuf<1> buf;
-    extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw, a.width);
     const RowRange rows((long long)blockIdx.x * a.teams + t.id, (long long)gridDim.x * a.teams, a.rows);
-    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, BULK>;
+    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, false>;
     In in;
-    __shared__ RowBars bars;
     auto from_a = [&](int, int row) { return row_at<T>(a.x, row, a.xs); };
     auto from_b = [&](int, int row) { return row_at<TR>(a.res, row, a.rs); };
-    in.begin(t, rows, a.D, a.stages, ring, &bars, a.status);
+    in.begin(t, rows, a.D, 0, nullptr, nullptr, nullptr);
     buf.clear();  // and its barrier
     in.start(t, from_a, from_b);
     V w[NV][N], b[NV][N];
@@ -96,7 +94,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
     int row = rows.first;
     for (int first = blockIdx.x * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
         const bool on = row < rows.rows;
-        if (on) in.arrived();
         V v[NV][N];
         V s = both<V>(0.f);
 #pragma unroll
@@ -123,7 +120,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
             float m = lane_sum(s);
             team_sum<1>(t, &m, buf, flip);
             flip ^= 1;
-            in.reuse(t, from_a, from_b);
             mean = m * inv;
         }
         const V minus = both<V>(-mean);
@@ -139,7 +135,6 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
         float var = lane_sum(q);
         team_sum<1>(t, &var, buf, flip);
         flip ^= 1;
-        if (!layer) in.reuse(t, from_a, from_b);
         const float rstd = __frsqrt_rn(fmaf(var, inv, eps));
         if (on) {
             if (t.rank == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
@@ -155,12 +150,11 @@ __global__ void __maxnreg__(row_regs(VEC, NV, false, BULK)) norm_fwd_kernel(cons
                 }
         }
     }
-    in.drain();
 }
 
 // DH: with the residual stream's gradient.
 template <typename T, typename TR, bool DH, int VEC, int NV, bool BULK>
-__global__ void __maxnreg__(row_regs(VEC, NV, true, BULK)) norm_bwd_kernel(const NormArgs a) {
+__global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
     constexpr bool SAME = sizeof(T) == sizeof(TR);
@@ -316,9 +310,9 @@ cudaError_t launch_mode(const RowPlan& p, unsigned grid, const NormArgs& a, cuda
         if constexpr (BWD)
             return &norm_bwd_kernel<T, TR, OPT, VEC, NV, BULK>;
         else
-            return &norm_fwd_kernel<T, TR, OPT, VEC, NV, BULK>;
+            return &norm_fwd_kernel<T, TR, OPT, VEC, NV>;
     }();
-    const size_t smem = BWD ? bwd_smem(p, a.D) : p.ring;
+    const size_t smem = BWD ? bwd_smem(p, a.D) : 0;
     const cudaError_t e = allow_smem<kernel>(smem);
     if (e == cudaSuccess) kernel<<<grid, p.threads(), smem, s>>>(a);
     return e;
