@@ -42,6 +42,10 @@ struct TeamBuf {
         for (int i = threadIdx.x; i < 2 * N * 32; i += blockDim.x) f[i] = 0.f;
         __syncthreads();
     }
+    __device__ __forceinline__ float sum4(int flip, int i, int k) const {
+        const float4 w = v[flip][i][k];
+        return (w.x + w.y) + (w.z + w.w);
+    }
 };
 // Sums N values over the team, the same bits in every thread.  Every thread of the block
 // calls it (one-warp teams need no barrier).  Two calls in a row take different halves of the
@@ -65,13 +69,14 @@ __device__ __forceinline__ void team_sum(const Team& t, float* x, TeamBuf<N>& bu
         for (int i = 0; i < N; ++i) reinterpret_cast<float*>(buf.v[flip][i])[t.warp] = x[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.f;
-    for (int k = 0; k < t.nw; k += 4)
+    for (int i = 0; i < N; ++i) x[i] = buf.sum4(flip, i, 0) + buf.sum4(flip, i, 1);
+    if (t.nw <= 8) return;  // the same for the block
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float4 w = buf.v[flip][i][k >> 2];
-            x[i] += (w.x + w.y) + (w.z + w.w);
-        }
+    for (int i = 0; i < N; ++i) x[i] += buf.sum4(flip, i, 2) + buf.sum4(flip, i, 3);
+    if (t.nw <= 16) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] += (buf.sum4(flip, i, 4) + buf.sum4(flip, i, 5)) + (buf.sum4(flip, i, 6) + buf.sum4(flip, i, 7));
 }
 
 // A row's vectors: `most` elements (16 bytes of the widest tensor) where every row of every
@@ -129,11 +134,13 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     if (dim > most_columns(vec)) return false;
     p->vec = vec;
     const int nvec = (dim + vec - 1) / vec;
-    // Elements a thread holds without spilling, where more threads do as well.  At 32768 x 2560
-    // (us): a forward through registers with 8 / 16 / 32 elements 171 / 158 / 202, a backward
-    // with 8 / 16 and the residual's gradient 222 / 267, without it 134 / 109.
+    // Elements a thread holds, where more threads do as well.  At 32768 x 2560 (us): a forward
+    // without a residual 72 with 16, 65 with 32 (at 32768 x 5120 221 and 114; single elements
+    // 130 with 8, 107 with 16); with a bf16 residual 113, 107, 133 with 16, 24, 32; with a float32
+    // residual 168, 160, 184 with 12, 16, 24 (single elements 202, 212 with 8, 16); a backward
+    // with the residual's gradient 222, 267 with 8, 16, without it 134, 109.
     const int hold = cost.bwd ? (vec == 1 ? 4 : vec == 2 || cost.nb > 1 ? 8 : 16)
-                              : (vec == 1 ? 8 : cost.nb > 0 || cost.na == 1 ? 16 : 32);
+                              : cost.nb == 0 ? (vec == 1 ? 16 : 32) : vec == 1 ? 8 : vec == 8 ? 24 : 16;
     // A warp spends about as long on a row's sums and addresses as on fourteen elements a lane,
     // and up to sixteen warps on an SM each add their share of its rate: the plan with the least
     // of that time per row wins.
@@ -168,23 +175,28 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     // rows each on their way do better: 222 us against 242 at 32768 x 2560 with one block of ten
     // warps an SM instead of two.  Not so the gated rows (332 us against 365 in 8 groups of 640).
     if (p->bulk && cost.nb > 0 && p->per_sm * p->threads() > 512) p->per_sm = 512 / p->threads() > 1 ? 512 / p->threads() : 1;
+    const size_t bytes = (size_t)dim * (cost.na * cost.ab + cost.nb * cost.bb) * p->teams;
+    // More than 48 KB of rows with their residual on their way to an SM get into each other's
+    // way: 204 us against 220 at 32768 x 2560 in float32 with two blocks an SM instead of three.
+    // Not so the gated rows (182 us against 155 at 32768 x 5120).
+    if (!cost.bwd && cost.nb > 0)
+        while (p->per_sm > 1 && p->per_sm * bytes > 48 << 10) --p->per_sm;
     p->stages = 0;
     p->ring = 0;
     if (p->bulk) {
         // two to eight rows in flight a team, within what the blocks of an SM can share
-        const size_t row = (size_t)dim * (cost.na * cost.ab + cost.nb * cost.bb) * p->teams;
         const size_t all = 210 << 10;
-        while (p->per_sm > 1 && 2 * row + 4096 > all / p->per_sm) --p->per_sm;
-        size_t s = (all / p->per_sm - 4096) / row;
+        while (p->per_sm > 1 && 2 * bytes + 4096 > all / p->per_sm) --p->per_sm;
+        size_t s = (all / p->per_sm - 4096) / bytes;
         p->stages = s > 8 ? 8 : s < 1 ? 1 : (int)s;
-        p->ring = p->stages * row;
+        p->ring = p->stages * bytes;
     }
     return true;
 }
 // The tensors of a team's rows on their way to its threads: by bulk copies into a ring of
 // `stages` rows in shared memory, which one thread of the team issues (backwards of a warp and
-// more in vectors of 16 bytes), or through registers one row ahead.  The first NA tensors have elements of type A,
-// the NB others of type B.
+// more in vectors of 16 bytes), or through registers one row ahead.  DEPTH: rows on their way in
+// registers.  The first NA tensors have elements of type A, the NB others of type B.
 constexpr int kMostStages = 8;
 struct RowBars {
     uint64_t full[4][kMostStages];  // by team of the block
@@ -205,10 +217,10 @@ __device__ __forceinline__ const T* row_at(const void* p, int row, long long str
     return static_cast<const T*>(p) + row * stride;
 }
 // From(): k -> the start of a row of tensor k.
-template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK>
+template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK, int DEPTH = 1>
 struct Rows {
-    Pack<A, VEC> ra[BULK ? 1 : NV][NA];
-    Pack<B, VEC> rb[BULK ? 1 : NV][NB ? NB : 1];
+    Pack<A, VEC> ra[DEPTH][BULK ? 1 : NV][NA];
+    Pack<B, VEC> rb[DEPTH][BULK ? 1 : NV][NB ? NB : 1];
     int next, by;              // the next row to load
     int left;                  // rows still to load
     bool in[NV];               // whether vector i lies in the row
@@ -242,6 +254,16 @@ struct Rows {
                 for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
                 tc::fence_mbar_init();
             }
+        } else {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                    for (int k = 0; k < NA; ++k) ra[d][i][k].zero();
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) rb[d][i][k].zero();
+                }
         }
     }
     __device__ __forceinline__ uint32_t row_bytes() const {
@@ -252,7 +274,8 @@ struct Rows {
         if constexpr (BULK) {
             for (int s = 0; s < stages; ++s) issue(from_a, from_b);
         } else {
-            fetch(t, from_a, from_b);
+            fetch<0>(t, from_a, from_b);
+            if constexpr (DEPTH > 1) fetch<1>(t, from_a, from_b);
         }
     }
     template <typename FA, typename FB>
@@ -273,22 +296,23 @@ struct Rows {
             fill = fill + 1 == stages ? 0 : fill + 1;
         }
     }
-    template <typename FA, typename FB>
+    // S: which of the DEPTH.
+    template <int S, typename FA, typename FB>
     __device__ __forceinline__ void fetch(const Team& t, const FA& from_a, const FB& from_b) {
-        if (left <= 0) return;
+        const bool more = left > 0;
 #pragma unroll
         for (int k = 0; k < NA; ++k) {
             const A* p = from_a(k, next) + column(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (in[i]) ra[i][k].load(p + i * 32 * VEC);
+                if (more && in[i]) ra[S][i][k].load(p + i * 32 * VEC);
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             const B* p = from_b(k, next) + column(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (in[i]) rb[i][k].load(p + i * 32 * VEC);
+                if (more && in[i]) rb[S][i][k].load(p + i * 32 * VEC);
         }
         next += by;
         --left;
@@ -298,9 +322,9 @@ struct Rows {
         if constexpr (BULK) waiter.wait(&full[stage], parity);
     }
     // After the last get of a row: registers take the next row.
-    template <typename FA, typename FB>
+    template <int S = 0, typename FA, typename FB>
     __device__ __forceinline__ void done(const Team& t, const FA& from_a, const FB& from_b) {
-        if constexpr (!BULK) fetch(t, from_a, from_b);
+        if constexpr (!BULK) fetch<S>(t, from_a, from_b);
     }
     // Once the whole team has done its gets (a team of one warp waits for itself here): the
     // row's place takes another.
@@ -319,26 +343,31 @@ struct Rows {
             if (waiter.gone)
                 for (int s = 0; s < stages; ++s) tc::mbar_wait(&full[s], parity);
     }
+    // A vector of this thread; zeros where it lies beyond the row, so that sums need no branch.
+    template <int S = 0>
     __device__ __forceinline__ void get_a(const Team& t, int i, int k, typename Lanes<VEC>::V* v) const {
         float f[VEC];
         if constexpr (BULK) {
             Pack<A, VEC> p;
-            p.load(reinterpret_cast<const A*>(ring + stage * row_bytes()) + k * cols + column(t, i));
+            p.zero();
+            if (in[i]) p.load(reinterpret_cast<const A*>(ring + stage * row_bytes()) + k * cols + column(t, i));
             p.get(f);
         } else {
-            ra[i][k].get(f);
+            ra[S][i][k].get(f);
         }
         to_lanes<VEC>(f, v);
     }
+    template <int S = 0>
     __device__ __forceinline__ void get_b(const Team& t, int i, int k, typename Lanes<VEC>::V* v) const {
         float f[VEC];
         if constexpr (BULK) {
             Pack<B, VEC> p;
-            p.load(reinterpret_cast<const B*>(ring + stage * row_bytes() + NA * cols * (int)sizeof(A)) +
+            p.zero();
+            if (in[i]) p.load(reinterpret_cast<const B*>(ring + stage * row_bytes() + NA * cols * (int)sizeof(A)) +
                    k * cols + column(t, i));
             p.get(f);
         } else {
-            rb[i][k].get(f);
+            rb[S][i][k].get(f);
         }
         to_lanes<VEC>(f, v);
     }

@@ -10,8 +10,8 @@
 // Bound by HBM (three tensors forward, five backward).  A (row, group) is one row of a team;
 // blocks stay with one group, so that the backward's dw stays in registers.
 //
-// GB300, 32768 x 5120, bf16: forward 156 us (95 % of the measured copy rate); backward 287 us in
-// one group (86 %), 330 in eight (75 %: three warps a row of 640 columns leave a sixth of their
+// GB300, 32768 x 5120, bf16: forward 155 us (96 % of the measured copy rate); backward 276 us in
+// one group (90 %), 324 in eight (76 %: three warps a row of 640 columns leave a sixth of their
 // lanes idle and share out the sums' fixed cost less well).
 #include <limits.h>
 
@@ -88,34 +88,30 @@ __global__ void __maxnreg__(fwd_regs(VEC, NV)) gated_fwd_kernel(const GatedArgs 
         V v[NV][N];
         V q = both<V>(0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on && in.in[i]) {
-                V z[N];
-                in.get_a(t, i, 0, v[i]);
-                in.get_a(t, i, 1, z);
+        for (int i = 0; i < NV; ++i) {
+            V z[N];
+            in.get_a(t, i, 0, v[i]);
+            in.get_a(t, i, 1, z);
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    v[i][e] = mul_(v[i][e], mul_(z[e], sigmoid_lanes<T>(z[e])));
-                    q = fma_(v[i][e], v[i][e], q);
-                }
+            for (int e = 0; e < N; ++e) {
+                v[i][e] = mul_(v[i][e], mul_(z[e], sigmoid_lanes<T>(z[e])));
+                q = fma_(v[i][e], v[i][e], q);
             }
+        }
         in.done(t, from_a, from_b);
         float sum = lane_sum(q);
         team_sum<1>(t, &sum, buf, flip);
         flip ^= 1;
         const float rstd = __frsqrt_rn(fmaf(sum, inv, eps));
-        if (on) {
-            if (t.rank == 0 && a.rstd) a.rstd[(long long)row * a.G + g] = rstd;
-            T* out = static_cast<T*>(a.out) + row * a.os + g0 + In::column(t, 0);
-            const V r = both<V>(rstd);
+        if (on && t.rank == 0 && a.rstd) a.rstd[(long long)row * a.G + g] = rstd;
+        T* out = static_cast<T*>(a.out) + row * a.os + g0 + In::column(t, 0);
+        const V r = both<V>(rstd);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in.in[i]) {
-                    V o[N];
+        for (int i = 0; i < NV; ++i) {
+            V o[N];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) o[e] = mul_(mul_(v[i][e], r), w[i][e]);
-                    store_lanes<VEC>(out + i * 32 * VEC, o);
-                }
+            for (int e = 0; e < N; ++e) o[e] = mul_(mul_(v[i][e], r), w[i][e]);
+            if (on && in.in[i]) store_lanes<VEC>(out + i * 32 * VEC, o);
         }
     }
 }
@@ -158,13 +154,13 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
         const V r = both<V>(next);
         if (row + rows.by < rows.rows) next = a.rstd_in[(long long)(row + rows.by) * a.G + g];
         const bool on = row < rows.rows;
-        if (on) in.arrived();
         // d = w dout, gate = silu(z), gy = y silu'(z)
         V d[NV][N], xh[NV][N], gate[NV][N], gy[NV][N];
         V s = both<V>(0.f);
+        if (on) {
+            in.arrived();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on && in.in[i]) {
+            for (int i = 0; i < NV; ++i) {
                 V y[N], z[N];
                 in.get_a(t, i, 0, d[i]);
                 in.get_a(t, i, 1, y);
@@ -181,6 +177,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
                     s = fma_(d[i][e], xh[i][e], s);
                 }
             }
+        }
         in.done(t, from_a, from_b);
         float sum = lane_sum(s);
         team_sum<1>(t, &sum, buf, flip);
@@ -191,18 +188,17 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
             T* dy = static_cast<T*>(a.dy) + row * a.dys + g0 + In::column(t, 0);
             T* dz = static_cast<T*>(a.dz) + row * a.dzs + g0 + In::column(t, 0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in.in[i]) {
-                    V oy[N], oz[N];
+            for (int i = 0; i < NV; ++i) {
+                V oy[N], oz[N];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const V dv = mul_(fma_(xh[i][e], c2, d[i][e]), r);
-                        oy[e] = mul_(dv, gate[i][e]);
-                        oz[e] = mul_(dv, gy[i][e]);
-                    }
-                    store_lanes<VEC>(dy + i * 32 * VEC, oy);
-                    store_lanes<VEC>(dz + i * 32 * VEC, oz);
+                for (int e = 0; e < N; ++e) {
+                    const V dv = mul_(fma_(xh[i][e], c2, d[i][e]), r);
+                    oy[e] = mul_(dv, gate[i][e]);
+                    oz[e] = mul_(dv, gy[i][e]);
                 }
+                if (in.in[i]) store_lanes<VEC>(dy + i * 32 * VEC, oy);
+                if (in.in[i]) store_lanes<VEC>(dz + i * 32 * VEC, oz);
+            }
         }
     }
     float* part = a.partial + (long long)rb * a.D + g0;

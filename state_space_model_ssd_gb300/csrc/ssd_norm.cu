@@ -14,10 +14,16 @@
 // block keeps its columns' dw and db in registers over all the rows it takes; a second
 // kernel adds the blocks' partial sums in a fixed order.
 //
-// GB300, 32768 x 2560, bf16 with a float32 residual: forward 154 us (97 % of the measured copy
-// rate), backward 228 us (87 %, its partial sums included); without a residual 83 and 109 us
-// (60 and 68 %), where the sums over a row and the two passes over its elements bound them.
+// What costs time beside HBM is a row's fixed part: its sums, barriers and addresses.  So a
+// thread's columns beyond the row count as zeros instead of taking branches, and a thread holds as
+// many elements as its registers allow.
+//
+// GB300, 32768 x 2560, bf16 with a float32 residual: forward 160 us (93 % of the measured copy
+// rate), backward 221 us (90 %, its partial sums included); without a residual 65 and 103 us
+// (77 and 72 %); float32 with a residual 203 us forward (97 %).
 #include <limits.h>
+
+#include <type_traits>
 
 #include "layer_device.cuh"
 #include "layer_host.cuh"
@@ -77,7 +83,10 @@ __global__ void __maxnreg__(fwd_regs(VEC, NV)) norm_fwd_kernel(const NormArgs a)
     __shared__ TeamBuf<1> buf;
     const Team t = team_of(a.nw, a.width);
     const RowRange rows((long long)blockIdx.x * a.teams + t.id, (long long)gridDim.x * a.teams, a.rows);
-    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, false>;
+    // Short rows without a residual: two on their way, 52 us instead of 55 at 131072 x 512 and 58
+    // instead of 62 at 262144 x 256; wider ones have no registers for it or gain nothing.
+    constexpr int DEPTH = !RES && VEC * NV <= 16 ? 2 : 1;
+    using In = Rows<T, TR, 1, RES ? 1 : 0, VEC, NV, false, DEPTH>;
     In in;
     auto from_a = [&](int, int row) { return row_at<T>(a.x, row, a.xs); };
     auto from_b = [&](int, int row) { return row_at<TR>(a.res, row, a.rs); };
@@ -91,30 +100,27 @@ __global__ void __maxnreg__(fwd_regs(VEC, NV)) norm_fwd_kernel(const NormArgs a)
     const float inv = a.inv, eps = a.eps;
     int flip = 0;
     // every team of the block takes the rounds of its first team, the last perhaps without a row
-    int row = rows.first;
-    for (int first = blockIdx.x * a.teams; first < rows.rows; first += rows.by, row += rows.by) {
+    int row = rows.first, first = blockIdx.x * a.teams;
+    auto one = [&](auto slot) {
+        constexpr int S = decltype(slot)::value;
         const bool on = row < rows.rows;
         V v[NV][N];
         V s = both<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (on && in.in[i]) {
-                in.get_a(t, i, 0, v[i]);
-                if constexpr (RES) {
-                    V r[N];
-                    in.get_b(t, i, 0, r);
+            in.template get_a<S>(t, i, 0, v[i]);
+            if constexpr (RES) {
+                V r[N];
+                in.template get_b<S>(t, i, 0, r);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) v[i][e] = add_(v[i][e], r[e]);
+                for (int e = 0; e < N; ++e) v[i][e] = add_(v[i][e], r[e]);
+                if (on && in.in[i])
                     store_lanes<VEC>(static_cast<TR*>(a.h) + row * a.hs + In::column(t, i), v[i]);
-                }
-#pragma unroll
-                for (int e = 0; e < N; ++e) s = add_(s, v[i][e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[i][e] = both<V>(0.f);
             }
+#pragma unroll
+            for (int e = 0; e < N; ++e) s = add_(s, v[i][e]);
         }
-        in.done(t, from_a, from_b);
+        in.template done<S>(t, from_a, from_b);
         float mean = 0.f;
         if (layer) {
             float m = lane_sum(s);
@@ -122,33 +128,36 @@ __global__ void __maxnreg__(fwd_regs(VEC, NV)) norm_fwd_kernel(const NormArgs a)
             flip ^= 1;
             mean = m * inv;
         }
-        const V minus = both<V>(-mean);
         V q = both<V>(0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in.in[i])
+        for (int i = 0; i < NV; ++i) {
+            const V minus = both<V>(in.in[i] ? -mean : 0.f);  // nothing beyond the row
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    v[i][e] = add_(v[i][e], minus);
-                    q = fma_(v[i][e], v[i][e], q);
-                }
+            for (int e = 0; e < N; ++e) {
+                v[i][e] = add_(v[i][e], minus);
+                q = fma_(v[i][e], v[i][e], q);
+            }
+        }
         float var = lane_sum(q);
         team_sum<1>(t, &var, buf, flip);
         flip ^= 1;
         const float rstd = __frsqrt_rn(fmaf(var, inv, eps));
-        if (on) {
-            if (t.rank == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
-            T* y = static_cast<T*>(a.y) + row * a.ys + In::column(t, 0);
-            const V r = both<V>(rstd);
+        if (on && t.rank == 0 && a.stats) a.stats[row] = make_float2(mean, rstd);
+        T* y = static_cast<T*>(a.y) + row * a.ys + In::column(t, 0);
+        const V r = both<V>(rstd);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in.in[i]) {
-                    V o[N];
+        for (int i = 0; i < NV; ++i) {
+            V o[N];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) o[e] = fma_(mul_(v[i][e], r), w[i][e], b[i][e]);
-                    store_lanes<VEC>(y + i * 32 * VEC, o);
-                }
+            for (int e = 0; e < N; ++e) o[e] = fma_(mul_(v[i][e], r), w[i][e], b[i][e]);
+            if (on && in.in[i]) store_lanes<VEC>(y + i * 32 * VEC, o);
         }
+        first += rows.by, row += rows.by;
+    };
+    while (first < rows.rows) {
+        one(std::integral_constant<int, 0>());
+        if constexpr (DEPTH > 1)
+            if (first < rows.rows) one(std::integral_constant<int, 1>());
     }
 }
 
@@ -188,13 +197,14 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
         const float2 st = next;
         if (row + rows.by < rows.rows) next = a.stats_in[row + rows.by];
         const bool on = row < rows.rows;
-        if (on) in.arrived();
         V xh[NV][N], d[NV][N], g[NV][N];
         V s0 = both<V>(0.f), s1 = both<V>(0.f);
-        const V minus = both<V>(-st.x), r = both<V>(st.y);
+        const V r = both<V>(st.y);
+        if (on) {
+            in.arrived();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on && in.in[i]) {
+            for (int i = 0; i < NV; ++i) {
+                const V minus = both<V>(in.in[i] ? -st.x : 0.f);  // nothing beyond the row
                 in.get_a(t, i, 0, d[i]);
                 in.get_b(t, i, 0, xh[i]);
                 if constexpr (DH) in.get_b(t, i, 1, g[i]);
@@ -208,6 +218,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
                     s1 = fma_(d[i][e], xh[i][e], s1);
                 }
             }
+        }
         in.done(t, from_a, from_b);
         float sum[2] = {lane_sum(s0), lane_sum(s1)};
         team_sum<2>(t, sum, buf, flip);
@@ -218,20 +229,19 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
             T* dx = static_cast<T*>(a.dx) + row * a.xs + In::column(t, 0);
             TR* dres = static_cast<TR*>(a.dres) + (long long)row * a.D + In::column(t, 0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in.in[i]) {
-                    V o[N];
+            for (int i = 0; i < NV; ++i) {
+                V o[N];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const V k = fma_(xh[i][e], c2, add_(d[i][e], c1));
-                        if constexpr (DH)
-                            o[e] = fma_(k, r, g[i][e]);
-                        else
-                            o[e] = mul_(k, r);
-                    }
-                    store_lanes<VEC>(dx + i * 32 * VEC, o);
-                    if (both_out) store_lanes<VEC>(dres + i * 32 * VEC, o);
+                for (int e = 0; e < N; ++e) {
+                    const V k = fma_(xh[i][e], c2, add_(d[i][e], c1));
+                    if constexpr (DH)
+                        o[e] = fma_(k, r, g[i][e]);
+                    else
+                        o[e] = mul_(k, r);
                 }
+                if (in.in[i]) store_lanes<VEC>(dx + i * 32 * VEC, o);
+                if (both_out && in.in[i]) store_lanes<VEC>(dres + i * 32 * VEC, o);
+            }
         }
     }
     float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
