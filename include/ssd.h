@@ -421,8 +421,8 @@ ssd_status_t ssd_device_status(const void* workspace, void* stream, int32_t* dev
  * unsupported problem.  Pure host function. */
 const char* ssd_dispatch_path(const ssd_problem_t* prob, int for_backward);
 
-/* Number of kernels the last ssd_forward / ssd_backward call on this host
- * thread launched (memsets not counted). */
+/* Number of kernels the last ssd_forward / ssd_backward call, or the last call of an
+ * operator around the scan, on this host thread launched (memsets not counted). */
 int ssd_last_launch_count(void);
 
 /* Per-kernel timing.  While enabled, every kernel launch is bracketed by CUDA

@@ -138,8 +138,9 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     // without a residual 72 with 16, 65 with 32 (at 32768 x 5120 221 and 114; single elements
     // 130 with 8, 107 with 16); with a bf16 residual 113, 107, 133 with 16, 24, 32; with a float32
     // residual 168, 160, 184 with 12, 16, 24 (single elements 202, 212 with 8, 16); a backward
-    // with the residual's gradient 222, 267 with 8, 16, without it 134, 109.
-    const int hold = cost.bwd ? (vec == 1 ? 4 : vec == 2 || cost.nb > 1 ? 8 : 16)
+    // with the residual's gradient 222, 267 with 8, 16 (single elements 309, 273 with 4, 8),
+    // without it 134, 109.
+    const int hold = cost.bwd ? (vec <= 2 || cost.nb > 1 ? 8 : 16)
                               : cost.nb == 0 ? (vec == 1 ? 16 : 32) : vec == 1 ? 8 : vec == 8 ? 24 : 16;
     // A warp spends about as long on a row's sums and addresses as on fourteen elements a lane,
     // and up to sixteen warps on an SM each add their share of its rate: the plan with the least
