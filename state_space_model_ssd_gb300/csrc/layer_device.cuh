@@ -13,7 +13,8 @@
 namespace ssd {
 namespace layer {
 
-// VEC consecutive elements as loaded: 16 bytes or less per load instruction.
+// VEC consecutive elements as loaded: 16 bytes or less per load instruction.  stream(): from
+// global memory that will not be read again.
 template <typename T, int VEC>
 struct Pack;
 
@@ -21,6 +22,7 @@ template <>
 struct Pack<float, 1> {
     float v;
     __device__ __forceinline__ void load(const float* p) { v = *p; }
+    __device__ __forceinline__ void stream(const float* p) { v = __ldcs(p); }
     __device__ __forceinline__ void zero() { v = 0.f; }
     __device__ __forceinline__ void get(float* f) const { f[0] = v; }
 };
@@ -28,6 +30,9 @@ template <>
 struct Pack<float, 4> {
     float4 v;
     __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void stream(const float* p) {
+        v = __ldcs(reinterpret_cast<const float4*>(p));
+    }
     __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float* f) const {
         f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
@@ -99,6 +104,9 @@ template <>
 struct Pack<float, 2> {
     float2 v;
     __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void stream(const float* p) {
+        v = __ldcs(reinterpret_cast<const float2*>(p));
+    }
     __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
     __device__ __forceinline__ void get(float* f) const { f[0] = v.x, f[1] = v.y; }
 };

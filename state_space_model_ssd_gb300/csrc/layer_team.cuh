@@ -196,8 +196,8 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
 }
 // The tensors of a team's rows on their way to its threads: by bulk copies into a ring of
 // `stages` rows in shared memory, which one thread of the team issues (backwards of a warp and
-// more in vectors of 16 bytes), or through registers one row ahead.  DEPTH: rows on their way in
-// registers.  The first NA tensors have elements of type A, the NB others of type B.
+// more in vectors of 16 bytes), or through registers, DEPTH rows ahead.  The first NA tensors
+// have elements of type A, the NB others of type B, read as a stream with STREAM.
 constexpr int kMostStages = 8;
 struct RowBars {
     uint64_t full[4][kMostStages];  // by team of the block
@@ -218,7 +218,8 @@ __device__ __forceinline__ const T* row_at(const void* p, int row, long long str
     return static_cast<const T*>(p) + row * stride;
 }
 // From(): k -> the start of a row of tensor k.
-template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK, int DEPTH = 1>
+template <typename A, typename B, int NA, int NB, int VEC, int NV, bool BULK, int DEPTH = 1,
+          bool STREAM = false>
 struct Rows {
     Pack<A, VEC> ra[DEPTH][BULK ? 1 : NV][NA];
     Pack<B, VEC> rb[DEPTH][BULK ? 1 : NV][NB ? NB : 1];
@@ -313,7 +314,12 @@ struct Rows {
             const B* p = from_b(k, next) + column(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (more && in[i]) rb[S][i][k].load(p + i * 32 * VEC);
+                if (more && in[i]) {
+                    if constexpr (STREAM)
+                        rb[S][i][k].stream(p + i * 32 * VEC);
+                    else
+                        rb[S][i][k].load(p + i * 32 * VEC);
+                }
         }
         next += by;
         --left;
