@@ -170,7 +170,6 @@ template <typename T, typename TR, bool DH, int VEC, int NV, bool BULK>
 __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormArgs a) {
     using V = typename Lanes<VEC>::V;
     constexpr int N = Lanes<VEC>::N;
-    constexpr bool SAME = sizeof(T) == sizeof(TR);
     __shared__ TeamBuf<2> buf;
     extern __shared__ __align__(128) char ring[];
     const Team t = team_of(a.nw, a.width);
@@ -191,7 +190,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = both<V>(0.f);
-    const bool both_out = !SAME || a.dres;
+    const bool both_out = a.dres != nullptr;
     const float inv = a.inv, inv1 = a.layer ? a.inv : 0.f;
     float2 next = rows.first < rows.rows ? a.stats_in[rows.first] : make_float2(0.f, 0.f);
     int flip = 0;
