@@ -419,20 +419,19 @@ PyObject* conv_backward(PyObject* const* a) {
         check(dw, "d_weight", dev, w.scalar_type(), w.sizes());
     else
         dw = empty(w.sizes(), w.scalar_type(), dev);
-    if (b) {
-        db = brought(a[10], "d_bias");
-        if (db.defined())
-            check(db, "d_bias", dev, w.scalar_type(), {C});
-        else
-            db = empty({C}, w.scalar_type(), dev);
+    // what `out` brings is written (or refused), asked for by its argument or not
+    db = brought(a[10], "d_bias");
+    if (db.defined()) {
+        if (!b) value_error("out brings d_bias, but there is no bias");
+        check(db, "d_bias", dev, w.scalar_type(), {C});
+    } else if (b) {
+        db = empty({C}, w.scalar_type(), dev);
     }
-    if (truth(a[9])) {
-        d0 = brought(a[10], "d_initial_state");
-        if (d0.defined())
-            check(d0, "d_initial_state", dev, type, {c.n, c.width, C});
-        else
-            d0 = empty({c.n, c.width, C}, type, dev);
-    }
+    d0 = brought(a[10], "d_initial_state");
+    if (d0.defined())
+        check(d0, "d_initial_state", dev, type, {c.n, c.width, C});
+    else if (truth(a[9]))
+        d0 = empty({c.n, c.width, C}, type, dev);
     size_t need = 0;
     ok(ssd_conv_workspace_size(&c.p, &need), "ssd_conv_workspace_size");
     const Scratch ws(a[11], need, dev);
@@ -598,24 +597,27 @@ PyObject* norm_backward(PyObject* const* a) {
         p.x_stride = rows(dx, "dx", dev, type, dy.sizes());
     else
         dx = empty(dy.sizes(), type, dev), p.x_stride = D;
-    if (rtype != type) {
-        dres = brought(a[7], "d_residual");
-        if (dres.defined())
-            check(dres, "d_residual", dev, rtype, dy.sizes());
-        else
-            dres = empty(dy.sizes(), rtype, dev);
-    }
+    // d_residual is dx itself where the types agree, unless `out` brings another tensor for it
+    // (an earlier call's dict brings dx again)
+    dres = brought(a[7], "d_residual");
+    const bool again = dres.defined() && dres.scalar_type() == type && rtype == type &&
+                       dres.data_ptr() == dx.data_ptr() && dres.sizes() == dx.sizes() &&
+                       dres.strides() == dx.strides();
+    if (again)
+        dres = Tensor();
+    else if (dres.defined())
+        check(dres, "d_residual", dev, rtype, dy.sizes());
+    else if (rtype != type)
+        dres = empty(dy.sizes(), rtype, dev);
     if (dw.defined())
         check(dw, "d_weight", dev, w.scalar_type(), {D});
     else
         dw = empty({D}, w.scalar_type(), dev);
-    if (truth(a[6])) {
-        db = brought(a[7], "d_bias");
-        if (db.defined())
-            check(db, "d_bias", dev, w.scalar_type(), {D});
-        else
-            db = empty({D}, w.scalar_type(), dev);
-    }
+    db = brought(a[7], "d_bias");  // what `out` brings is written, asked for or not
+    if (db.defined())
+        check(db, "d_bias", dev, w.scalar_type(), {D});
+    else if (truth(a[6]))
+        db = empty({D}, w.scalar_type(), dev);
     size_t need = 0;
     ok(ssd_norm_workspace_size(&p, &need), "ssd_norm_workspace_size");
     const Scratch ws(a[8], need, dev);
@@ -627,7 +629,7 @@ PyObject* norm_backward(PyObject* const* a) {
     g.set("dx", dx);
     if (dres.defined()) {
         g.set("d_residual", dres);
-    } else if (dh) {
+    } else if (dh && !again) {
         PyObject* same = PyDict_GetItemString(g.d, "dx");
         if (PyDict_SetItemString(g.d, "d_residual", same) < 0) throw Raised();
     }

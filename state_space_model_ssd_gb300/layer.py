@@ -84,8 +84,9 @@ def conv_backward(u, weight, bias, dy, activation="silu", cu_seqlens=None, posit
                   workspace=None, stream=None):
     """Backward of ``conv_forward``.  ``dy``: the gradient of the output, or a tuple of those of
     its pieces (contiguous, ``[batch, L, ...]``).  Returns a dict ``du, d_weight``, with a bias
-    ``d_bias`` and with ``d_initial_state`` that too; ``out`` may bring any of them (``du`` may
-    be strided, e.g. a slice of the in-projection's gradient)."""
+    ``d_bias`` and with ``d_initial_state`` that too; ``out`` may bring any of them, and what it
+    brings is written (``du`` may be strided, e.g. a slice of the in-projection's gradient;
+    ``d_bias`` without a bias is refused)."""
     args = (u, weight, bias, dy, _silu(activation), cu_seqlens, positions, initial_state,
             d_final_state, d_initial_state, out, workspace)
     return _ext.conv_backward(*args) if stream is None else _on(stream, _ext.conv_backward, *args)
@@ -123,7 +124,8 @@ def norm_backward(dy, h, weight, stats, dh=None, kind: str = "layer", bias: bool
     """Backward of ``norm_forward``: ``dy`` the gradient of y, ``dh`` (optional) that of h, which
     arrives by the residual stream; ``h`` and ``stats`` as the forward returned them.  Returns a
     dict ``dx`` (in the type of dy), ``d_weight``, with ``bias`` ``d_bias``, and with ``dh`` or
-    an h of another type ``d_residual`` (in the type of h; dx itself where the types agree)."""
+    an h of another type ``d_residual`` (in the type of h; dx itself where the types agree).
+    ``out`` may bring any of them, and what it brings is written (``dx`` may be strided)."""
     args = (dy, h, weight, stats, dh, _norm_kind(kind), bias, out, workspace)
     return _ext.norm_backward(*args) if stream is None else _on(stream, _ext.norm_backward, *args)
 

@@ -58,3 +58,64 @@ def test_norm_backward_without_d_residual(ssd, R, D, with_dh, kind):  # noqa: F8
     # the binding's form of it
     g = ssd.norm_backward(dy, h, w, stats, dh=dh, kind=kind)
     assert bool((g["dx"] == full[0]).all()) and bool((g["d_residual"] == dres).all())
+
+
+# dy, h: their types
+@pytest.mark.parametrize("dt,ht", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("R,D", [(40, 768), (21, 34), (50, 97)])
+@pytest.mark.parametrize("with_dh", [False, True])
+def test_norm_backward_writes_what_out_brings(ssd, dt, ht, R, D, with_dh):  # noqa: F811
+    """Every buffer in ``out`` gets the call's result, also d_residual in the type of dx and d_bias
+    without ``bias``; the dict of an earlier call serves again."""
+    import torch
+    rng = np.random.default_rng(R * D)
+    dy, dy64 = _dev(rng.standard_normal((R, D)), dt)
+    h, h64 = _dev(rng.standard_normal((R, D)), ht)
+    dh, dh64 = _dev(rng.standard_normal((R, D)), ht) if with_dh else (None, None)
+    w, w64 = _dev(1 + 0.2 * rng.standard_normal(D), "f32")
+    _, _, st = ref.norm(h64, w64, None, None, 1e-5, True)
+    stats = torch.from_numpy(st.astype(np.float32)).cuda()
+    dv, dw, db = ref.norm_bwd(dy64, h64, w64, stats.double().cpu().numpy(), dh64, True)
+    out = {"dx": torch.full_like(dy, float("nan")), "d_residual": torch.full_like(h, float("nan")),
+           "d_weight": torch.full_like(w, float("nan")), "d_bias": torch.full_like(w, float("nan"))}
+    mine = dict(out)
+    g = ssd.norm_backward(dy, h, w, stats, dh=dh, bias=False, out=out)
+    assert set(g) == set(mine) and all(g[k] is mine[k] for k in mine)
+    ref.assert_close(g["dx"], dv, dt, "dx")
+    ref.assert_close(g["d_residual"], dv, ht, "d_residual")
+    ref.assert_close(g["d_weight"], dw, "f32", "d_weight")
+    ref.assert_close(g["d_bias"], db, "f32", "d_bias")
+    # without buffers: the same bits, and only what was asked for
+    f = ssd.norm_backward(dy, h, w, stats, dh=dh, bias=False)
+    assert "d_bias" not in f and ("d_residual" in f) == (with_dh or dt != ht)
+    assert all(bool((f[k] == g[k]).all()) for k in f)
+    # the dict of an earlier call
+    for t in f.values():
+        t.fill_(float("nan"))
+    before = dict(f)
+    f2 = ssd.norm_backward(dy, h, w, stats, dh=dh, bias=False, out=f)
+    assert all(f2[k] is before[k] and bool((f2[k] == g[k]).all()) for k in before)
+    if dt == ht:  # one buffer for both, under two tensors
+        one = torch.full_like(dy, float("nan"))
+        f3 = ssd.norm_backward(dy, h, w, stats, dh=dh, out={"dx": one, "d_residual": one[:]})
+        assert bool((one == g["dx"]).all()) and bool((f3["d_residual"] == g["dx"]).all())
+    with pytest.raises(ValueError):
+        ssd.norm_backward(dy, h, w, stats, dh=dh, out={"d_residual": torch.empty(R, D + 1, dtype=h.dtype,
+                                                                               device="cuda")})
+
+
+def test_conv_backward_writes_what_out_brings(ssd):  # noqa: F811
+    """d_initial_state in ``out`` is written without being asked for; d_bias without a bias, which
+    has no meaning, is refused."""
+    import torch
+    rng = np.random.default_rng(4)
+    u, _ = _dev(rng.standard_normal((2, 30, 24)), "bf16")
+    w, _ = _dev(rng.standard_normal((24, 4)), "f32")
+    init, _ = _dev(rng.standard_normal((2, 4, 24)), "bf16")
+    want = ssd.conv_backward(u, w, None, u, initial_state=init, d_initial_state=True)
+    buf = torch.full_like(init, float("nan"))
+    g = ssd.conv_backward(u, w, None, u, initial_state=init, out={"d_initial_state": buf})
+    assert g["d_initial_state"] is buf
+    assert set(g) == set(want) and all(bool((g[k] == want[k]).all()) for k in want)
+    with pytest.raises(ValueError):
+        ssd.conv_backward(u, w, None, u, out={"d_bias": torch.empty(24, device="cuda")})
