@@ -262,6 +262,13 @@ template <typename T>
 __device__ __forceinline__ float sigmoid_lanes(float v) {
     return sigmoid_of<T>(v);
 }
+// The derivative of v s, s = sigmoid(v), from s and p = v s: s + p (1 - s).  1 - s is exact from
+// s = 1/2 on and 0 where s = 1, so that nothing cancels at large v, where s + p or p - p s would
+// lose s beside p.
+template <typename V>
+__device__ __forceinline__ V silu_slope(V s, V p) {
+    return fma_(p, sub_(both<V>(1.f), s), s);
+}
 
 }  // namespace layer
 }  // namespace ssd

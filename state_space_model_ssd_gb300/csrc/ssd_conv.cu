@@ -451,8 +451,7 @@ __device__ __forceinline__ void grad_pre(const typename Lanes<VEC>::V (*w)[Lanes
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) v = fma_(w[K - 2 - j][e], win[j][e], v);
         const V s = sigmoid_lanes<T>(v);
-        const V p = mul_(v, s);  // silu' = s + p (1 - s), in a form without constants to hold
-        g[e] = mul_(dy[e], sub_(add_(s, p), mul_(p, s)));
+        g[e] = mul_(dy[e], silu_slope(s, mul_(v, s)));
     }
 }
 

@@ -169,8 +169,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
                 for (int e = 0; e < N; ++e) {
                     const V sg = sigmoid_lanes<T>(z[e]);
                     gate[i][e] = mul_(z[e], sg);
-                    // silu'(z) = s + gate (1 - s), in a form without constants to hold
-                    gy[i][e] = mul_(y[e], sub_(add_(sg, gate[i][e]), mul_(gate[i][e], sg)));
+                    gy[i][e] = mul_(y[e], silu_slope(sg, gate[i][e]));
                     xh[i][e] = mul_(mul_(y[e], gate[i][e]), r);
                     dw[i][e] = fma_(d[i][e], xh[i][e], dw[i][e]);
                     d[i][e] = mul_(d[i][e], w[i][e]);

@@ -119,3 +119,52 @@ def test_conv_backward_writes_what_out_brings(ssd):  # noqa: F811
     assert set(g) == set(want) and all(bool((g[k] == want[k]).all()) for k in want)
     with pytest.raises(ValueError):
         ssd.conv_backward(u, w, None, u, out={"d_bias": torch.empty(24, device="cuda")})
+
+
+# silu'(v) = s + v s (1 - s) where s is 1 to the last bit: 1, however large v is.  Each row or
+# sequence has gates of one size, so that a tolerance of its own largest value judges it.
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gated_backward_at_large_gates(ssd, dt):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(31)
+    scales = np.array([1e-3, 1.0, 9.0, 14.0, 30.0, 1e4, 2.0 ** 24, 3e7, 1e9, 1e12])
+    R, D = len(scales), 64
+    z, z64 = _dev(scales[:, None] * rng.uniform(0.5, 1.5, (R, D)), dt)
+    y, y64 = _dev(rng.standard_normal((R, D)), dt)
+    dout, dout64 = _dev(rng.standard_normal((R, D)), dt)
+    w, w64 = _dev(1 + 0.2 * rng.standard_normal(D), "f32")
+    _, rstd = ssd.gated_norm_forward(y, z, w)
+    _, wr = ref.gated(y64, z64, w64, 1e-5, 1)
+    assert np.abs(rstd.double().cpu().numpy() / wr - 1).max() <= ref.CHAIN
+    # a gradient that survives the norm's own factor 1 / (y z): that of a unit rstd
+    one = torch.ones_like(rstd)
+    for r in (rstd, one):
+        g = ssd.gated_norm_backward(dout, y, z, w, r)
+        # a - xh mean(a xh) of the formula, with xh = y z rstd: finite for either rstd
+        dy, dz, _ = ref.gated_bwd(dout64, y64, z64, w64, r.double().cpu().numpy(), 1)
+        for i in range(R):
+            ref.assert_close(g["dy"][i], dy[i], dt, "dy at gates of %g" % scales[i])
+            ref.assert_close(g["dz"][i], dz[i], dt, "dz at gates of %g" % scales[i])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_conv_backward_at_large_inputs(ssd, dt):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(32)
+    L, C, K = 48, 16, 4
+    w, w64 = _dev(rng.uniform(0.5, 1.0, (C, K)), "f32")
+    b, b64 = _dev(rng.standard_normal(C), "f32")
+    # runs of one sign: a sum that crosses zero between them takes a large step over it
+    sign = np.repeat([1.0, -1.0, 1.0], L // 3)
+    for scale in (9.0, 30.0, 1e4, 2.0 ** 24, 3e7, 1e12):
+        u, u64 = _dev(sign[None, :, None] * scale * rng.uniform(0.5, 1.5, (1, L, C)), dt)
+        init, init64 = _dev(scale * rng.uniform(0.5, 1.5, (1, K, C)), dt)
+        dy, dy64 = _dev(rng.standard_normal((1, L, C)), dt)
+        pos = torch.tensor([6], dtype=torch.int32, device="cuda")
+        g = ssd.conv_backward(u, w, b, dy, initial_state=init, positions=pos, d_initial_state=True)
+        with np.errstate(over="ignore"):
+            du, dw, db, d0 = ref.conv_bwd(u64[0], w64, b64, dy64[0], 6, init64[0])
+        ref.assert_close(g["du"], du[None], dt, "du at %g" % scale)
+        ref.assert_close(g["d_weight"], dw, "f32", "d_weight at %g" % scale)
+        ref.assert_close(g["d_bias"], db, "f32", "d_bias at %g" % scale)
+        ref.assert_close(g["d_initial_state"], d0[None], dt, "d_initial_state at %g" % scale)
