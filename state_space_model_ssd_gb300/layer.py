@@ -150,10 +150,11 @@ def gated_norm_backward(dout, y, z, weight, rstd, groups: int = 1, out=None, wor
 
 def layer_status(stream=None) -> int:
     """Waits for ``stream`` (default: the current one) and returns what the calls of this module
-    have recorded on the current device since the last query: 0, or the code of SSD_ERR_TIMEOUT
-    if a kernel's bounded wait ran out (its outputs are then not valid)."""
+    have recorded on its device since the last query: 0, or the code of SSD_ERR_TIMEOUT if a
+    kernel's bounded wait ran out (its outputs are then not valid)."""
     v = ctypes.c_int32(0)
     s = torch.cuda.current_stream() if stream is None else stream
-    _lib.check(_lib.lib().ssd_layer_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(v)),
-               "ssd_layer_status")
+    with torch.cuda.device(s.device):  # the word is the current device's
+        _lib.check(_lib.lib().ssd_layer_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(v)),
+                   "ssd_layer_status")
     return int(v.value)

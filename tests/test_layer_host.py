@@ -1,0 +1,50 @@
+"""Host code of the operators around the scan that needs no GPU."""
+
+import contextlib
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from state_space_model_ssd_gb300 import build
+    build.build()
+    from state_space_model_ssd_gb300 import layer as m
+    return m
+
+
+def test_status_is_read_on_the_device_of_the_stream(layer, monkeypatch):
+    """ssd_layer_status reads and clears the current device's word: that of the stream given."""
+    import torch
+    from state_space_model_ssd_gb300 import _lib
+    words, current, reads = {0: 0, 1: 5}, [0], []
+
+    class Lib:
+        def ssd_layer_status(self, stream, out):
+            reads.append((stream.value, current[0]))
+            out._obj.value = words[current[0]]
+            words[current[0]] = 0
+            return 0
+
+    @contextlib.contextmanager
+    def device(d):
+        before = current[0]
+        current[0] = torch.device(d).index
+        try:
+            yield
+        finally:
+            current[0] = before
+
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+            self.cuda_stream = 100 + index
+
+    monkeypatch.setattr(_lib, "lib", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(current[0]))
+    assert layer.layer_status() == 0
+    assert words[1] == 5                              # the other device's word still stands
+    assert layer.layer_status(stream=Stream(1)) == 5  # and is that of its own streams
+    assert layer.layer_status(stream=Stream(1)) == 0
+    assert reads == [(100, 0), (101, 1), (101, 1)] and current == [0]
