@@ -282,7 +282,8 @@ ssd_status_t ssd_forward_noalloc_status(void* stream, int32_t* device_status);
  * are counted in elements, from one token or row to the next.  Weights, biases and their
  * gradients are float32 or bf16 (wdtype), whatever the activations are.  An output must not
  * overlap another output or, unless the call's comment says so, an input
- * (SSD_ERR_INVALID_ARG); a tensor counts as everything from its first to its last element. */
+ * (SSD_ERR_INVALID_ARG); a tensor counts as everything from its first to its last element, and
+ * a workspace as an output. */
 
 /* Synchronises `stream` and returns in *device_status what the calls of this section have
  * recorded on the current device since the last query: SSD_OK, or SSD_ERR_TIMEOUT if a

@@ -736,6 +736,11 @@ ssd_status_t check_conv(const ssd_conv_t* p, Conv* c) {
     return SSD_OK;
 }
 
+// Piece i of the outputs or of their gradients.
+Span piece_span(const ssd_conv_t* p, const Conv& c, int i, const void* t) {
+    return Span(t, c.T, p->split[i], p->split[i], c.e);
+}
+
 // Channels of a vector: `most` where every row of every tensor and every piece starts on 16
 // bytes (and tokens move in bulk copies), else two or one.
 int conv_vec(const ssd_conv_t* p, const Conv& c, int most, const void* const* ptrs, int np) {
@@ -909,15 +914,14 @@ ssd_status_t ssd_conv_forward(const ssd_conv_t* conv, const void* u, const void*
         !aligned_to(positions, 4))
         return SSD_ERR_ALIGNMENT;
     // a run reads tokens and states that other blocks may already have written over
-    const Span in(u, c.T, conv->u_stride, c.C, c.e);
     const long long srows = (long long)c.nseq * conv->width;
-    const Span si(initial_state, srows, c.C, c.C, c.e), so(final_state, srows, c.C, c.C, c.e);
-    if (so.overlaps(si) || so.overlaps(in)) return SSD_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i) {
-        const Span o(outs[i], c.T, conv->split[i], conv->split[i], c.e);
-        if (conv->split[i] && (o.overlaps(in) || o.overlaps(si) || o.overlaps(so)))
-            return SSD_ERR_INVALID_ARG;
-    }
+    if (clash({piece_span(conv, c, 0, out0), piece_span(conv, c, 1, out1), piece_span(conv, c, 2, out2),
+               Span(final_state, srows * c.C, c.e)},
+              {Span(u, c.T, conv->u_stride, c.C, c.e), Span(initial_state, srows * c.C, c.e),
+               Span(weight, c.C * conv->width, dtype_size(conv->wdtype)),
+               Span(bias, c.C, dtype_size(conv->wdtype)), Span(cu_seqlens, c.nseq + 1LL, 4),
+               Span(positions, c.nseq, 4)}))
+        return SSD_ERR_INVALID_ARG;
     if (c.T == 0 && !final_state) return SSD_OK;
 
     const int vec = conv_vec(conv, c, most_fwd(c), ptrs, 6);
@@ -985,19 +989,17 @@ ssd_status_t ssd_conv_backward(const ssd_conv_t* conv, const void* u, const void
         !aligned_to(d_bias, we) || !aligned_to(cu_seqlens, 4) || !aligned_to(positions, 4))
         return SSD_ERR_ALIGNMENT;
     const long long srows = (long long)c.nseq * conv->width;
-    const Span in(u, c.T, conv->u_stride, c.C, c.e), o(du, c.T, conv->du_stride, c.C, c.e);
-    const Span si(initial_state, srows, c.C, c.C, c.e), df(d_final_state, srows, c.C, c.C, c.e);
-    const Span di(d_initial_state, srows, c.C, c.C, c.e);
-    if (o.overlaps(in) || o.overlaps(si) || o.overlaps(df) || o.overlaps(di) || di.overlaps(si) ||
-        di.overlaps(in) || di.overlaps(df))
-        return SSD_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i) {
-        const Span d(douts[i], c.T, conv->split[i], conv->split[i], c.e);
-        if (conv->split[i] && (o.overlaps(d) || di.overlaps(d))) return SSD_ERR_INVALID_ARG;
-    }
     size_t need = 0;
     st = ssd_conv_workspace_size(conv, &need);
     if (st != SSD_OK) return st;
+    if (clash({Span(du, c.T, conv->du_stride, c.C, c.e), Span(d_weight, c.C * conv->width, we),
+               Span(d_bias, c.C, we), Span(d_initial_state, srows * c.C, c.e), Span(workspace, need, 1)},
+              {Span(u, c.T, conv->u_stride, c.C, c.e), piece_span(conv, c, 0, dout0),
+               piece_span(conv, c, 1, dout1), piece_span(conv, c, 2, dout2),
+               Span(initial_state, srows * c.C, c.e), Span(d_final_state, srows * c.C, c.e),
+               Span(weight, c.C * conv->width, we), Span(bias, c.C, we),
+               Span(cu_seqlens, c.nseq + 1LL, 4), Span(positions, c.nseq, 4)}))
+        return SSD_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
 

@@ -263,13 +263,12 @@ ssd_status_t ssd_conv_decode_step(const ssd_problem_t* prob, int32_t width, int3
         !aligned_to(y, e) || !aligned_to(raw_dt, 4) || !aligned_to(weight, we) ||
         !aligned_to(bias, we) || !aligned_to(positions, 4) || !aligned_to(slots, 4))
         return SSD_ERR_ALIGNMENT;
-    const Span ss(state, nslots, (long long)p.nheads * p.headdim * p.dstate,
-                  (long long)p.nheads * p.headdim * p.dstate, 4);
-    const Span sw(conv_state, nslots, width * C, width * C, e);
-    const Span su(u, p.batch, u_stride, C, e);
-    const Span sy(y, p.batch, p.nheads * p.headdim, p.nheads * p.headdim, e);
-    if (ss.overlaps(sw) || ss.overlaps(su) || ss.overlaps(sy) || sw.overlaps(su) ||
-        sw.overlaps(sy) || sy.overlaps(su))
+    const long long hp = (long long)p.nheads * p.headdim;
+    if (clash({Span(state, nslots * hp * p.dstate, 4), Span(conv_state, nslots * width * C, e),
+               Span(y, p.batch * hp, e)},
+              {Span(u, p.batch, u_stride, C, e), Span(raw_dt, p.batch * (long long)p.nheads, 4),
+               Span(weight, C * width, we), Span(bias, C, we), Span(positions, p.batch, 4),
+               Span(slots, p.batch, 4)}))
         return SSD_ERR_INVALID_ARG;
     StepArgs a = {};
     a.state = state, a.window = conv_state, a.u = u, a.raw = raw_dt, a.w = weight, a.b = bias;

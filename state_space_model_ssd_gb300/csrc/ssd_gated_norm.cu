@@ -352,8 +352,11 @@ ssd_status_t ssd_gated_norm_forward(const ssd_gated_norm_t* norm, const void* y,
     // out may replace y or z, element by element
     const Span sy(y, n, norm->y_stride, norm->dim, e), sz(z, n, norm->z_stride, norm->dim, e);
     const Span so(out, n, norm->out_stride, norm->dim, e);
-    if ((so.overlaps(sy) && !(out == y && norm->out_stride == norm->y_stride)) ||
-        (so.overlaps(sz) && !(out == z && norm->out_stride == norm->z_stride)))
+    const bool out_y = out == y && norm->out_stride == norm->y_stride;
+    const bool out_z = out == z && norm->out_stride == norm->z_stride;
+    if (clash({so, Span(rstd, n * norm->groups, 4)},
+              {out_y ? Span() : sy, out_z ? Span() : sz,
+               Span(weight, norm->dim, dtype_size(norm->wdtype))}))
         return SSD_ERR_INVALID_ARG;
     const void* ptrs[3] = {y, z, out};
     const size_t sizes[3] = {e, e, e};
@@ -413,25 +416,20 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
         !aligned_to(dz, e) || !aligned_to(rstd, 4) || !aligned_to(weight, we) ||
         !aligned_to(d_weight, we))
         return SSD_ERR_ALIGNMENT;
-    // outputs may replace inputs element by element; any other overlap is refused
-    struct Side {
-        const void* p;
-        long long stride;
-    };
-    const Side ins[3] = {{dout, norm->out_stride}, {y, norm->y_stride}, {z, norm->z_stride}};
-    const Side os[2] = {{dy, norm->dy_stride}, {dz, norm->dz_stride}};
-    for (const Side& o : os) {
-        const Span so(o.p, n, o.stride, norm->dim, e);
-        for (const Side& i : ins)
-            if (so.overlaps(Span(i.p, n, i.stride, norm->dim, e)) &&
-                !(o.p == i.p && o.stride == i.stride))
-                return SSD_ERR_INVALID_ARG;
-    }
-    if (Span(dy, n, norm->dy_stride, norm->dim, e).overlaps(Span(dz, n, norm->dz_stride, norm->dim, e)))
-        return SSD_ERR_INVALID_ARG;
     size_t need = 0;
     st = ssd_gated_norm_workspace_size(norm, &need);
     if (st != SSD_OK) return st;
+    // outputs may replace inputs element by element; any other overlap is refused
+    const int D = norm->dim;
+    auto in = [&](const void* p, long long stride) {
+        const bool replaced = (p == dy && stride == norm->dy_stride) || (p == dz && stride == norm->dz_stride);
+        return replaced ? Span() : Span(p, n, stride, D, e);
+    };
+    if (clash({Span(dy, n, norm->dy_stride, D, e), Span(dz, n, norm->dz_stride, D, e),
+               Span(d_weight, D, we), Span(workspace, need, 1)},
+              {in(dout, norm->out_stride), in(y, norm->y_stride), in(z, norm->z_stride),
+               Span(weight, D, we), Span(rstd, n * norm->groups, 4)}))
+        return SSD_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
     const void* ptrs[5] = {dout, y, z, dy, dz};

@@ -413,8 +413,8 @@ ssd_status_t ssd_norm_forward(const ssd_norm_t* norm, const void* x, const void*
     const Span sy(y, n, norm->y_stride, D, e), sh(h, n, norm->h_stride, D, re);
     const bool same_y = x == y && norm->x_stride == norm->y_stride;
     const bool same_h = residual == h && norm->r_stride == norm->h_stride;
-    if ((sy.overlaps(sx) && !same_y) || (sh.overlaps(sr) && !same_h) || sy.overlaps(sr) ||
-        sh.overlaps(sx) || sy.overlaps(sh))
+    if (clash({sy, sh, Span(stats, 2 * n, 4)},
+              {same_y ? Span() : sx, same_h ? Span() : sr, Span(weight, D, we), Span(bias, D, we)}))
         return SSD_ERR_INVALID_ARG;
     const void* ptrs[4] = {x, y, residual, h};
     const size_t sizes[4] = {e, e, re, re};
@@ -486,12 +486,13 @@ ssd_status_t ssd_norm_backward(const ssd_norm_t* norm, const void* dy, const voi
     const bool dx_dy = dx == dy && norm->x_stride == norm->y_stride;
     const bool dx_dh = dx == dh && norm->x_stride == norm->r_stride && e == re;
     const bool dr_dh = d_residual == dh && norm->r_stride == D;
-    if ((sdx.overlaps(sdy) && !dx_dy) || (sdx.overlaps(sdh) && !dx_dh) || sdx.overlaps(sh) ||
-        sdx.overlaps(sdr) || sdr.overlaps(sdy) || sdr.overlaps(sh) || (sdr.overlaps(sdh) && !dr_dh))
-        return SSD_ERR_INVALID_ARG;
     size_t need = 0;
     st = ssd_norm_workspace_size(norm, &need);
     if (st != SSD_OK) return st;
+    if (clash({sdx, sdr, Span(d_weight, D, we), Span(d_bias, D, we), Span(workspace, need, 1)},
+              {dx_dy ? Span() : sdy, dx_dh || dr_dh ? Span() : sdh, sh, Span(weight, D, we),
+               Span(stats, 2 * n, 4)}))
+        return SSD_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
     const void* ptrs[5] = {dy, dx, h, dh, d_residual};

@@ -190,3 +190,125 @@ def test_binding_refuses(lib):
         ssd.norm_forward(torch.zeros(2, 8), torch.ones(8))
     with pytest.raises(ValueError):
         ssd.gated_norm_forward(torch.zeros(2, 8), torch.zeros(2, 8), torch.ones(8))
+
+
+# ------------------------------------------------------------------ outputs over other buffers
+# Every output over every other output and every input of a call is refused, but for the places
+# that an output may take.  Addresses a MB apart; an overlap starts 32 bytes before the end of the
+# other buffer, so that its whole extent counts.  Nothing is launched: a call that is not refused
+# would be, so that without a GPU it ends in another status.
+
+def _inside(mb, nbytes):
+    return ctypes.c_void_p((mb << 20) + nbytes - 32)
+
+
+def _refused(call, outs, ins, allowed=()):
+    """``call(**addresses)``; outs and ins: name -> (MB, bytes of the buffer)."""
+    every = dict(outs, **ins)
+    for o in outs:
+        for other, (mb, n) in every.items():
+            if o != other:
+                assert call(**{o: _inside(mb, n)}) == 1, (o, other)
+                if (o, other) not in allowed:
+                    assert call(**{o: at(mb)}) == 1, (o, other)
+
+
+def test_conv_outputs_over_anything(lib):
+    p = _conv(nseq=2)
+    T, K, srows = 10, 4, 2 * 4
+
+    def fwd(u=at(1), w=at(2), b=at(3), cu=at(4), pos=at(5), init=at(6), o0=at(7), o1=at(8), o2=at(9), final=at(10)):
+        return lib.ssd_conv_forward(ctypes.byref(p), u, w, b, cu, pos, init, o0, o1, o2, final, None)
+
+    ins = {"u": (1, T * 32 * 2), "w": (2, 32 * K * 4), "b": (3, 32 * 4), "cu": (4, 32), "pos": (5, 32),
+           "init": (6, srows * 32 * 2)}
+    # the shortest buffers (12 and 8 bytes) are hit by their first byte alone
+    outs = {"o0": (7, T * 16 * 2), "o1": (8, T * 8 * 2), "o2": (9, T * 8 * 2), "final": (10, srows * 32 * 2)}
+    _refused(fwd, outs, ins)
+
+    n = ctypes.c_size_t()
+    assert lib.ssd_conv_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+
+    def bwd(u=at(1), w=at(2), b=at(3), cu=at(4), pos=at(5), init=at(6), d0=at(7), d1=at(8), d2=at(9), df=at(10),
+            du=at(11), dw=at(12), db=at(13), di=at(14), ws=at(15)):
+        return lib.ssd_conv_backward(ctypes.byref(p), u, w, b, cu, pos, init, d0, d1, d2, df, du, dw, db, di, ws,
+                                     n.value, None)
+
+    ins.update(d0=(7, T * 16 * 2), d1=(8, T * 8 * 2), d2=(9, T * 8 * 2), df=(10, srows * 32 * 2))
+    outs = {"du": (11, T * 32 * 2), "dw": (12, 32 * K * 4), "db": (13, 32 * 4), "di": (14, srows * 32 * 2)}
+    _refused(bwd, outs, dict(ins, ws=(15, n.value)))
+
+
+def test_step_outputs_over_anything(lib):
+    prob, C, K, n = _step(), 4 * 16 + 2 * 16, 4, 3
+
+    def step(state=at(1), win=at(2), u=at(3), raw=at(4), w=at(5), b=at(6), pos=at(7), slots=at(8), y=at(9)):
+        return lib.ssd_conv_decode_step(ctypes.byref(prob), K, 0, n, C, state, win, u, raw, w, b, pos, slots, y,
+                                        None)
+
+    _refused(step, {"state": (1, n * 4 * 16 * 16 * 4), "win": (2, n * K * C * 2), "y": (9, n * 64 * 2)},
+             {"u": (3, n * C * 2), "raw": (4, n * 4 * 4), "w": (5, C * K * 4), "b": (6, C * 4), "pos": (7, 32),
+              "slots": (8, 32)})
+
+
+def test_norm_outputs_over_anything(lib):
+    p, R, D = _norm(), 4, 64
+
+    def fwd(x=at(1), r=at(2), w=at(3), b=at(4), y=at(5), h=at(6), st=at(7)):
+        return lib.ssd_norm_forward(ctypes.byref(p), x, r, w, b, y, h, st, None)
+
+    _refused(fwd, {"y": (5, R * D * 2), "h": (6, R * D * 4), "st": (7, R * 8)},
+             {"x": (1, R * D * 2), "r": (2, R * D * 4), "w": (3, D * 4), "b": (4, D * 4)},
+             allowed=[("y", "x"), ("h", "r")])
+    # taken places do not hide what lies over them
+    assert fwd(y=at(1), st=at(1)) == 1 and fwd(h=at(2), st=at(2)) == 1 and fwd(y=at(1), h=at(1)) == 1
+    n = ctypes.c_size_t()
+    assert lib.ssd_norm_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+
+    def bwd(dy=at(1), h=at(2), dh=at(3), w=at(4), st=at(5), dx=at(6), dr=at(7), dw=at(8), db=at(9), ws=at(10)):
+        return lib.ssd_norm_backward(ctypes.byref(p), dy, h, dh, w, st, dx, dr, dw, db, ws, n.value, None)
+
+    _refused(bwd, {"dx": (6, R * D * 2), "dr": (7, R * D * 4), "dw": (8, D * 4), "db": (9, D * 4)},
+             {"dy": (1, R * D * 2), "h": (2, R * D * 4), "dh": (3, R * D * 4), "w": (4, D * 4), "st": (5, R * 8),
+              "ws": (10, n.value)}, allowed=[("dx", "dy"), ("dr", "dh")])
+    assert bwd(dx=at(1), dr=at(1)) == 1 and bwd(dx=at(1), dw=at(1)) == 1 and bwd(dr=at(3), dx=at(3)) == 1
+    same = _norm(rdtype=1)
+    p = same
+    assert bwd(dx=at(3), dr=at(3)) == 1 and bwd(dx=at(3), db=at(3)) == 1
+
+
+def test_gated_norm_outputs_over_anything(lib):
+    p, R, D, G = _gated(), 4, 64, 2
+
+    def fwd(y=at(1), z=at(2), w=at(3), out=at(4), rstd=at(5)):
+        return lib.ssd_gated_norm_forward(ctypes.byref(p), y, z, w, out, rstd, None)
+
+    _refused(fwd, {"out": (4, R * D * 2), "rstd": (5, R * G * 4)},
+             {"y": (1, R * D * 2), "z": (2, R * D * 2), "w": (3, D * 4)}, allowed=[("out", "y"), ("out", "z")])
+    assert fwd(out=at(1), rstd=at(1)) == 1
+    n = ctypes.c_size_t()
+    assert lib.ssd_gated_norm_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+
+    def bwd(do=at(1), y=at(2), z=at(3), w=at(4), rstd=at(5), dy=at(6), dz=at(7), dw=at(8), ws=at(9)):
+        return lib.ssd_gated_norm_backward(ctypes.byref(p), do, y, z, w, rstd, dy, dz, dw, ws, n.value, None)
+
+    _refused(bwd, {"dy": (6, R * D * 2), "dz": (7, R * D * 2), "dw": (8, D * 4)},
+             {"do": (1, R * D * 2), "y": (2, R * D * 2), "z": (3, R * D * 2), "w": (4, D * 4), "rstd": (5, R * G * 4),
+              "ws": (9, n.value)}, allowed=[(o, i) for o in ("dy", "dz") for i in ("do", "y", "z")])
+    assert bwd(dy=at(1), dz=at(1)) == 1 and bwd(dy=at(2), dw=at(2)) == 1
+    # the workspace over an input or an output
+    assert bwd(ws=at(6)) == 1 and bwd(ws=at(1)) == 1
+
+
+def test_an_empty_buffer_lies_over_nothing(lib):
+    """No token at all: u and du of no bytes inside another buffer are no overlap (without a GPU
+    the call then ends for want of a device)."""
+    p = _conv(seqlen=0)
+    n = ctypes.c_size_t()
+    assert lib.ssd_conv_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+    inside = _inside(6, 4 * 32 * 2)
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("would be launched")
+    assert lib.ssd_conv_backward(ctypes.byref(p), inside, at(2), None, None, None, at(6), inside, inside, inside,
+                                 None, inside, at(12), None, at(14), at(15), n.value, None) == 5
