@@ -555,6 +555,8 @@ PyObject* norm_forward(PyObject* const* a) {
             h = tensor(a[7], "residual_out");
             p.h_stride = rows(h, "residual_out", dev, rtype, x.sizes());
         }
+    } else if (a[7] != Py_None) {
+        value_error("residual_out without a residual: h is x itself");
     }
     if (truth(a[8])) stats = empty({p.rows, 2}, at::kFloat, dev);
     ok(ssd_norm_forward(&p, x.data_ptr(), ptr(res), w.data_ptr(), ptr(b), y.data_ptr(),

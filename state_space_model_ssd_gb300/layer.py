@@ -114,7 +114,8 @@ def norm_forward(x, weight, bias=None, residual=None, eps: float = 1e-5, kind: s
     "rms" does not.  ``residual`` has the shape of x and its type or float32.  Returns
     ``(y, h, stats)``: y in the type of x; h = x + residual in the residual's type (x itself
     without one); stats float32 ``[rows, 2]``, each row's mean and 1 / deviation, for the
-    backward (None with ``stats=False``).  ``out=x`` and ``residual_out=residual`` work in place."""
+    backward (None with ``stats=False``).  ``out=x`` and ``residual_out=residual`` work in place;
+    ``residual_out`` without a residual is refused."""
     args = (x, weight, bias, residual, eps, _norm_kind(kind), out, residual_out, stats)
     return _ext.norm_forward(*args) if stream is None else _on(stream, _ext.norm_forward, *args)
 

@@ -168,3 +168,11 @@ def test_conv_backward_at_large_inputs(ssd, dt):  # noqa: F811
         ref.assert_close(g["d_weight"], dw, "f32", "d_weight at %g" % scale)
         ref.assert_close(g["d_bias"], db, "f32", "d_bias at %g" % scale)
         ref.assert_close(g["d_initial_state"], d0[None], dt, "d_initial_state at %g" % scale)
+
+
+def test_norm_forward_refuses_a_residual_out_without_a_residual(ssd):  # noqa: F811
+    """h is x itself then: a buffer for it would be left unwritten."""
+    import torch
+    x, w = torch.randn(3, 16, device="cuda"), torch.ones(16, device="cuda")
+    with pytest.raises(ValueError):
+        ssd.norm_forward(x, w, residual_out=torch.empty_like(x))
