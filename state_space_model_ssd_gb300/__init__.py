@@ -33,7 +33,7 @@ _LAYER = frozenset(__all__[-8:])
 
 
 def __getattr__(name):
-    # the operators around the scan live in .layer, which imports torch: loaded on first use
+    # the operators around the scan live in .layer: imported on first use
     if name in _LAYER:
         from . import layer
         globals()[name] = f = getattr(layer, name)

@@ -18,25 +18,40 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 from . import _lib
 
 __all__ = ["conv_forward", "conv_backward", "conv_decode_step", "norm_forward", "norm_backward",
            "gated_norm_forward", "gated_norm_backward", "layer_status"]
 
-if not os.path.exists(os.path.join(_lib.PKG, "_layer_ext.so")):
-    raise RuntimeError("_layer_ext.so is not built; run state_space_model_ssd_gb300/build.py or "
-                       "__graft_entry__.build()")
-from . import _layer_ext as _ext  # noqa: E402  (checks, allocation and the call into libssd.so)
 
-_ext.set_error(_lib.SSDError)
+def _load():
+    """The binding: checks, allocation and the call into libssd.so."""
+    global _ext
+    if not os.path.exists(os.path.join(_lib.PKG, "_layer_ext.so")):
+        raise RuntimeError("_layer_ext.so is not built; run state_space_model_ssd_gb300/build.py or "
+                           "__graft_entry__.build()")
+    import torch  # noqa: F401  (the binding is linked against its libraries)
+    from . import _layer_ext
+    _layer_ext.set_error(_lib.SSDError)
+    _ext = _layer_ext
+    return _ext
+
+
+class _Unloaded:
+    """In the binding's place until the first call."""
+
+    def __getattr__(self, name):
+        return getattr(_load(), name)
+
+
+_ext = _Unloaded()
 _KIND = {"layer": 0, "rms": 1}
 _SILU = {"silu": True, None: False}
 
 
 def _on(stream, f, *args):
     """``f`` with ``stream`` current: it launches there, and what it allocates belongs to it."""
+    import torch
     for t in args:
         if isinstance(t, torch.Tensor):
             if stream.device != t.device:
@@ -153,6 +168,7 @@ def layer_status(stream=None) -> int:
     """Waits for ``stream`` (default: the current one) and returns what the calls of this module
     have recorded on its device since the last query: 0, or the code of SSD_ERR_TIMEOUT if a
     kernel's bounded wait ran out (its outputs are then not valid)."""
+    import torch
     v = ctypes.c_int32(0)
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(s.device):  # the word is the current device's

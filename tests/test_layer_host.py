@@ -48,3 +48,41 @@ def test_status_is_read_on_the_device_of_the_stream(layer, monkeypatch):
     assert layer.layer_status(stream=Stream(1)) == 5  # and is that of its own streams
     assert layer.layer_status(stream=Stream(1)) == 0
     assert reads == [(100, 0), (101, 1), (101, 1)] and current == [0]
+
+
+def _python(code):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    return subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+
+
+def test_package_names_need_neither_torch_nor_the_binding(layer):
+    """``from state_space_model_ssd_gb300 import *`` needs what a call of the scan's C library needs;
+    torch and the binding are looked for by the first call that takes tensors."""
+    r = _python("""
+import sys
+sys.modules["torch"] = None
+from state_space_model_ssd_gb300 import *
+import state_space_model_ssd_gb300 as ssd
+assert all(callable(globals()[n]) for n in ssd.__all__)
+try:
+    norm_forward(None, None)
+except ImportError:
+    print("torch is missing")
+""")
+    assert r.returncode == 0 and r.stdout == "torch is missing\n", r.stderr
+    r = _python("""
+import os
+exists = os.path.exists
+os.path.exists = lambda p: exists(p) and not str(p).endswith("_layer_ext.so")
+from state_space_model_ssd_gb300 import *
+for call in (lambda: norm_forward(None, None), lambda: conv_decode_step(*[None] * 8)):
+    try:
+        call()
+    except RuntimeError as e:
+        assert "not built" in str(e)
+        print("not built")
+""")
+    assert r.returncode == 0 and r.stdout == "not built\n" * 2, r.stderr
