@@ -3,12 +3,14 @@ of the operators around the scan to torch tensors.
 
 Each .cu file is compiled by nvcc in parallel, then linked into
 ``state_space_model_ssd_gb300/libssd.so``; ``csrc/layer_ext.cpp`` is compiled beside them and
-linked against it and torch's libraries into ``_layer_ext.so``.  No CMake.
+linked against it and torch's libraries into ``_layer_ext.so`` (left out where torch is not
+installed).  No CMake.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -83,27 +85,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + hdrs):
             jobs.append(common + ["-c", src, "-o", obj])
-    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    ext_compile, ext_obj, ext_link = _ext_commands(cuda_home)
-    if force or _stale(ext_obj, [EXT_SRC] + hdrs):
-        jobs.insert(0, ext_compile)
-    if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(jobs))) as ex:
-            futs = [ex.submit(subprocess.run, j, capture_output=True, text=True) for j in jobs]
-            for j, f in zip(jobs, futs):
-                r = f.result()
-                if verbose or r.returncode != 0:
-                    sys.stderr.write(r.stdout + r.stderr)
-                if r.returncode != 0:
-                    raise RuntimeError("%s failed on %s" % (os.path.basename(j[0]), j[-3]))
-    if force or any(j is not ext_compile for j in jobs) or _stale(LIB, objs):
+    # the binding alone needs torch: without it the C library is built all the same
+    ext = None
+    if importlib.util.find_spec("torch") is None:
+        sys.stderr.write("torch is not installed: _layer_ext.so, the binding of the operators around the "
+                         "scan, is not built\n")
+    else:
+        ext = _ext_commands(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))))
+    ext_jobs = [ext[0]] if ext and (force or _stale(ext[1], [EXT_SRC] + hdrs)) else []
+
+    def failed(job, done):
+        if verbose or done.returncode != 0:
+            sys.stderr.write(done.stdout + done.stderr)
+        if done.returncode == 0:
+            return None
+        return RuntimeError("%s failed on %s" % (os.path.basename(job[0]), job[job.index("-o") - 1]))
+
+    errors, ext_errors = [], []
+    if ext_jobs or jobs:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(ext_jobs + jobs))) as ex:
+            futs = [ex.submit(subprocess.run, j, capture_output=True, text=True) for j in ext_jobs + jobs]
+            for j, f in zip(ext_jobs + jobs, futs):
+                (ext_errors if j in ext_jobs else errors).append(failed(j, f.result()))
+    for e in filter(None, errors):
+        raise e
+    if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".%d.tmp" % os.getpid()
         subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        check=True)
         os.replace(tmp, LIB)
-    if force or _stale(EXT, [ext_obj]):
+    for e in filter(None, ext_errors):
+        raise e
+    if ext and (force or _stale(EXT, [ext[1]])):
         tmp = EXT + ".%d.tmp" % os.getpid()
-        subprocess.run(ext_link + ["-o", tmp], check=True)
+        subprocess.run(ext[2] + ["-o", tmp], check=True)
         os.replace(tmp, EXT)
     return LIB
 
