@@ -25,6 +25,7 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
 EXT = os.path.join(PKG, "_layer_ext.so")
 EXT_SRC = os.path.join(CSRC, "layer_ext.cpp")
+LINKED = "layer_ext.linked"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -61,6 +62,15 @@ def _ext_commands(cuda_home):
     link = [cxx, "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
             "-ltorch", "-ltorch_python", "-L", PKG, "-l:libssd.so", "-Wl,-rpath,$ORIGIN"]
     return compile_, obj, link
+
+
+def _linked() -> str:
+    """The object that _layer_ext.so was linked from."""
+    try:
+        with open(os.path.join(OBJDIR, LINKED)) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def _stale(target, deps) -> bool:
@@ -116,10 +126,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, LIB)
     for e in filter(None, ext_errors):
         raise e
-    if ext and (force or _stale(EXT, [ext[1]])):
+    # another torch's object may be older than the module linked since: the object linked is on record
+    if ext and (force or _stale(EXT, [ext[1]]) or _linked() != os.path.basename(ext[1])):
         tmp = EXT + ".%d.tmp" % os.getpid()
         subprocess.run(ext[2] + ["-o", tmp], check=True)
         os.replace(tmp, EXT)
+        with open(os.path.join(OBJDIR, LINKED), "w") as f:
+            f.write(os.path.basename(ext[1]))
     return LIB
 
 

@@ -64,3 +64,16 @@ def test_a_kernel_that_does_not_compile_fails_the_build(fake):
     with pytest.raises(RuntimeError, match="ssd_norm"):
         fake.build()
     assert not os.path.exists(fake.LIB)
+
+
+def test_binding_follows_the_torch_that_is_installed(fake, monkeypatch):
+    """Back to an earlier torch, whose object is older than the module that was linked since."""
+    import torch
+    linked = lambda: open(fake.EXT).read()  # noqa: E731
+    for version in ("2.9.1", "2.11.0", "2.9.1", "2.9.1", "2.11.0"):
+        monkeypatch.setattr(torch, "__version__", version)
+        n = len(fake.ran)
+        same = os.path.exists(fake.EXT) and "torch" + version in linked()
+        fake.build()
+        assert "torch" + version in linked()
+        assert not same or len(fake.ran) == n
