@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "layer_ring.cuh"
 #include "ssd_device.cuh"
 #include "tc_ptx.cuh"
 
@@ -122,19 +123,27 @@ struct Pack<__nv_bfloat16, 2> {
 
 // Waits for phase `parity` of a copy's barrier.  The wait is bounded (2 s); one that runs out
 // records SSD_ERR_TIMEOUT and lets every later wait of the thread pass at once, so that a lost
-// copy ends in a status and wrong values, not in a hang.
+// copy ends in a status and wrong values, not in a hang.  The thread that issues the copies then
+// issues no more, and before it leaves waits once more, bounded again, for those on their way:
+// they may be late, and must not land in shared memory that by then is another block's.
 static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* status) {
     if (tc::mbar_wait(bar, parity)) return false;
     atomicCAS(status, 0, (int)SSD_ERR_TIMEOUT);
     return true;
 }
-struct Waiter {
-    int* status;
-    bool gone = false;
-    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!tc::mbar_try_wait(bar, parity) && !gone) gone = wait_long(bar, parity, status);
-    }
-};
+// `left`: the copies that the thread has still to issue, 0 or more; where a wait has run out, minus
+// one and those (so that the one register says both).
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity, int* status, int& left) {
+    if (!tc::mbar_try_wait(bar, parity) && left >= 0 && wait_long(bar, parity, status)) left = ~left;
+}
+// After the last use of a ring, in the thread that issues its copies: nothing is on its way any more
+// unless a wait ran out.  idle: places gone over without a copy for them, at the end.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int places, int stage, uint32_t parity,
+                                           int left, int idle = 0) {
+    if (left < 0)
+        for (int s = 0; s < places; ++s)
+            tc::mbar_wait(&full[s], landed_parity(s, places, stage, parity, ~left + idle));
+}
 
 // Parameters (weight, bias) are float32 or bfloat16, whatever the activations' type.
 __device__ __forceinline__ float param(const void* p, long long i, int bf16) {

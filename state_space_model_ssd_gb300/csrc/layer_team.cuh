@@ -224,13 +224,13 @@ struct Rows {
     Pack<A, VEC> ra[DEPTH][BULK ? 1 : NV][NA];
     Pack<B, VEC> rb[DEPTH][BULK ? 1 : NV][NB ? NB : 1];
     int next, by;              // the next row to load
-    int left;                  // rows still to load
+    int left;                  // rows still to load (as wait_copy has it)
     bool in[NV];               // whether vector i lies in the row
     char* ring;                // this team's
     uint64_t* full;
     int cols, stages, fill, stage;
     uint32_t parity;
-    Waiter waiter;
+    int* status;
 
     static __device__ __forceinline__ int column(const Team& t, int i) {
         return ((t.warp * NV + i) * 32 + t.lane) * VEC;
@@ -238,7 +238,7 @@ struct Rows {
     // The rows of `r`, of `n` columns.  A barrier of the block has to come between this and
     // start().
     __device__ __forceinline__ void begin(const Team& t, const RowRange& r, int n, int nstages, char* all,
-                                          RowBars* bars, int* status) {
+                                          RowBars* bars, int* status_word) {
         next = r.first;
         by = r.by;
         left = BULK && t.rank != 0 ? 0 : r.count();  // one thread issues the copies
@@ -249,7 +249,7 @@ struct Rows {
             stages = nstages;
             fill = stage = 0;
             parity = 0;
-            waiter.status = status;
+            status = status_word;
             full = bars->full[t.id];
             ring = all + t.id * stages * row_bytes();
             if (t.rank == 0) {
@@ -326,7 +326,7 @@ struct Rows {
     }
     // Before the first get of a row that this team has.
     __device__ __forceinline__ void arrived() {
-        if constexpr (BULK) waiter.wait(&full[stage], parity);
+        if constexpr (BULK) wait_copy(&full[stage], parity, status, left);
     }
     // After the last get of a row: registers take the next row.
     template <int S = 0, typename FA, typename FB>
@@ -343,12 +343,11 @@ struct Rows {
             if (++stage == stages) stage = 0, parity ^= 1;
         }
     }
-    // Before the block ends or its ring is used for something else: nothing is on its way any
-    // more unless a wait ran out; then it is waited for once more.
-    __device__ __forceinline__ void drain() {
+    // After the last row, before the block ends or its ring is used for something else.  idle: the
+    // team went through the last round without a row (and over a place more than its rows took).
+    __device__ __forceinline__ void drain(const Team& t, bool idle) const {
         if constexpr (BULK)
-            if (waiter.gone)
-                for (int s = 0; s < stages; ++s) tc::mbar_wait(&full[s], parity);
+            if (t.rank == 0) drain_ring(full, stages, stage, parity, left, idle);
     }
     // A vector of this thread; zeros where it lies beyond the row, so that sums need no branch.
     template <int S = 0>

@@ -187,24 +187,24 @@ struct Run {
     const CUtensorMap* map[N];
     int col[N];       // the block's first channel in each map
     int token;        // the next to load
-    int left;         // tokens still to load
+    int left;         // groups (single loads: tokens) still to load (groups as wait_copy has it)
     char* ring;       // this warp's
     uint64_t* full;
     int fill, stage;
     uint32_t parity;
-    Waiter waiter;
+    int* status;
 
     // `tokens` (perhaps none) from t0 on; every lane of the warp calls it.
     __device__ __forceinline__ void begin(long long t0, int tokens, char* all, RunBars* bars,
-                                          int* status) {
-        left = tokens;
+                                          int* status_word) {
+        left = BULK ? (tokens + kGroup - 1) / kGroup : tokens;
         if constexpr (BULK) {
             token = (int)t0;
             ring = all + threadIdx.y * (kGroups * N * tile);
             full = bars->full[threadIdx.y];
             fill = stage = 0;
             parity = 0;
-            waiter.status = status;
+            status = status_word;
             if (threadIdx.x == 0) {
                 for (int s = 0; s < kGroups; ++s) tc::mbar_init(&full[s], 1);
                 tc::fence_mbar_init();
@@ -241,7 +241,7 @@ struct Run {
                 tc::tma_load_2d(ring + (fill * N + k) * tile, map[k], &full[fill], col[k], token);
         }
         token += kGroup;
-        left -= kGroup;
+        --left;
         fill = fill + 1 == kGroups ? 0 : fill + 1;
     }
     __device__ __forceinline__ void fetch() {
@@ -255,7 +255,7 @@ struct Run {
         for (int k = 0; k < N; ++k) src[k] += kGroup * stride[k];
     }
     __device__ __forceinline__ void arrived() {
-        if constexpr (BULK) waiter.wait(&full[stage], parity);
+        if constexpr (BULK) wait_copy(&full[stage], parity, status, left);
     }
     // After the last get of a group: its place takes another.
     __device__ __forceinline__ void reuse() {
@@ -265,12 +265,10 @@ struct Run {
             if (++stage == kGroups) stage = 0, parity ^= 1;
         }
     }
-    // Before the block ends or its ring is used for something else: nothing is on its way any
-    // more unless a wait ran out; then it is waited for once more.
-    __device__ __forceinline__ void drain() {
+    // After the last group, before the block ends or its ring is used for something else.
+    __device__ __forceinline__ void drain() const {
         if constexpr (BULK)
-            if (waiter.gone)
-                for (int s = 0; s < kGroups; ++s) tc::mbar_wait(&full[s], parity);
+            if (threadIdx.x == 0) drain_ring(full, kGroups, stage, parity, left);
     }
     __device__ __forceinline__ void get(int i, int k, typename Lanes<VEC>::V* v) const {
         float f[VEC];

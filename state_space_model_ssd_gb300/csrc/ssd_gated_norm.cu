@@ -202,7 +202,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
     }
     float* part = a.partial + (long long)rb * a.D + g0;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
-        in.drain();
+        in.drain(t, row - rows.by >= rows.rows);
         float* acc = reinterpret_cast<float*>(ring);
         __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
@@ -221,7 +221,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) gated_bwd_kernel(const Gate
         for (int i = threadIdx.x; i < a.n; i += blockDim.x) part[i] = acc[i];
         return;
     }
-    in.drain();
+    in.drain(t, row - rows.by >= rows.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = In::column(t, i);

@@ -249,7 +249,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
     }
     float* part = a.partial + (long long)blockIdx.x * a.nk * a.D;
     if (a.teams > 1) {  // the teams' sums are joined in order, in the ring's place
-        in.drain();
+        in.drain(t, row - rows.by >= rows.rows);
         float* acc = reinterpret_cast<float*>(ring);
         __syncthreads();
         for (int k = 0; k < a.teams; ++k) {
@@ -272,7 +272,7 @@ __global__ void __maxnreg__(bwd_regs(VEC, NV, BULK)) norm_bwd_kernel(const NormA
         for (int i = threadIdx.x; i < a.nk * a.D; i += blockDim.x) part[i] = acc[i];
         return;
     }
-    in.drain();
+    in.drain(t, row - rows.by >= rows.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = In::column(t, i);

@@ -86,3 +86,39 @@ for call in (lambda: norm_forward(None, None), lambda: conv_decode_step(*[None] 
         print("not built")
 """)
     assert r.returncode == 0 and r.stdout == "not built\n" * 2, r.stderr
+
+
+@pytest.fixture(scope="module")
+def ring(tmp_path_factory):
+    """csrc/layer_ring.cuh, compiled for the host."""
+    import ctypes
+    import subprocess
+    from state_space_model_ssd_gb300 import build
+    d = tmp_path_factory.mktemp("ring")
+    src, so = str(d / "ring.cpp"), str(d / "ring.so")
+    with open(src, "w") as f:
+        f.write('#include "layer_ring.cuh"\n'
+                'extern "C" unsigned landed_parity(int p, int n, int s, unsigned q, int u) {\n'
+                '    return ssd::layer::landed_parity(p, n, s, q, u);\n}\n')
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", build.CSRC, src, "-o", so], check=True)
+    return ctypes.CDLL(so)
+
+
+def test_a_thread_that_gave_up_waits_for_every_copy_on_its_way(ring):
+    """A ring of barriers whose phase with parity q counts as complete once the barrier has left it.
+    At every row whose wait can run out, the thread issues no more, walks on to its last row, and
+    then waits: at each place, for the phase that is incomplete until its copy lands; at places
+    without a copy on its way, for one that is complete."""
+    for places in range(1, 9):
+        for rows in range(1, 4 * places + 2):
+            for row in range(rows):  # the wait for it runs out; the copies before it have landed
+                sent = min(places + row, rows)
+                issued = [len(range(p, sent, places)) for p in range(places)]
+                landed = [len(range(p, row, places)) for p in range(places)]
+                stage, parity = rows % places, rows // places & 1  # after the last row
+                for p in range(places):
+                    q = ring.landed_parity(p, places, stage, parity, rows - sent)
+                    late = issued[p] - landed[p]
+                    assert late in (0, 1)
+                    assert ((landed[p] & 1) == q) == (late == 1), (places, rows, row, p)
+                    assert issued[p] & 1 != q         # passes once every copy has landed
