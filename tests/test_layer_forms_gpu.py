@@ -176,3 +176,184 @@ def test_norm_forward_refuses_a_residual_out_without_a_residual(ssd):  # noqa: F
     x, w = torch.randn(3, 16, device="cuda"), torch.ones(16, device="cuda")
     with pytest.raises(ValueError):
         ssd.norm_forward(x, w, residual_out=torch.empty_like(x))
+
+
+# Rows of one column.  rms: dx = rstd a (1 - xh^2) with xh^2 = 1 - eps rstd^2, layer: xh = 0 and
+# dx = rstd (a - a): the terms cancel, so that the bound is the chain's roundings of the terms
+# before they do, rstd max|a| with a = w dy (and of dh, which does not cancel).
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dt,ht,with_dh", [("f32", "f32", False), ("f32", "f32", True), ("bf16", "f32", True),
+                                           ("bf16", "bf16", False), ("bf16", "bf16", True)])
+@pytest.mark.parametrize("R", [1, 300])
+def test_norm_backward_of_one_column(ssd, R, kind, dt, ht, with_dh):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(41)
+    dy, dy64 = _dev(rng.standard_normal((R, 1)), dt)
+    h, h64 = _dev(2 + rng.random((R, 1)), ht)
+    dh, dh64 = _dev(rng.standard_normal((R, 1)), ht) if with_dh else (None, None)
+    w, w64 = _dev([1.3], "f32")
+    _, _, st = ref.norm(h64, w64, None, None, 1e-5, kind == "layer")
+    stats = torch.from_numpy(st.astype(np.float32)).cuda()
+    st = stats.double().cpu().numpy()
+    g = ssd.norm_backward(dy, h, w, stats, dh=dh, kind=kind)
+    dv, dw, db = ref.norm_bwd(dy64, h64, w64, st, dh64, kind == "layer")
+    terms = np.abs(st[:, 1:] * w64 * dy64).max() + (np.abs(dh64).max() if with_dh else 0.0)
+    for key, d in [("dx", dt)] + ([("d_residual", ht)] if "d_residual" in g else []):
+        off = np.abs(g[key].double().cpu().numpy() - dv)
+        assert (off <= ref.ROUND[d] * np.abs(dv) + ref.CHAIN * terms).all(), key
+    # xh is 0 (layer) or 1 (rms), to a rounding or two
+    ref.assert_close(g["d_weight"], dw, "f32", "d_weight")
+    ref.assert_close(g["d_bias"], db, "f32", "d_bias")
+
+
+@pytest.mark.parametrize("dt,wdt,has_b", [("bf16", "bf16", True), ("bf16", "bf16", False), ("f32", "bf16", False),
+                                          ("bf16", "f32", False), ("f32", "f32", False)])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_step_parameters(ssd, dt, wdt, has_b, K):  # noqa: F811
+    """The step's weights and bias in either type, and no bias: what the prompt's convolution and
+    the formulas of the scan give."""
+    import torch
+    B, H, P, N, G = 5, 6, 16, 32, 2
+    C = H * P + 2 * G * N
+    rng = np.random.default_rng(42)
+    st, st64 = _dev(rng.standard_normal((B, H, P, N)), "f32")
+    win, win64 = _dev(rng.standard_normal((B, K, C)), dt)
+    u, u64 = _dev(rng.standard_normal((B, C)), dt)
+    w, w64 = _dev(rng.uniform(-1, 1, (C, K)), wdt)
+    b, b64 = _dev(rng.uniform(-1, 1, C), wdt) if has_b else (None, np.zeros(C))
+    raw = rng.standard_normal((B, H)).astype(np.float32)
+    pos = rng.integers(0, 50, B)
+    y = ssd.conv_decode_step(st, win, u, torch.from_numpy(raw).cuda(), w, b,
+                             torch.from_numpy(pos.astype(np.int32)).cuda(), -4.6, ngroups=G)
+    want = np.zeros((B, H, P))
+    for i in range(B):
+        o, s, _ = ref.conv(u64[i:i + 1], w64, b64, int(pos[i]), win64[i])
+        win64[i, int(pos[i]) % K] = s[int(pos[i]) % K]
+        x = o[0, :H * P].reshape(H, P)
+        Bm, Cm = (np.repeat(o[0, H * P + k * G * N:H * P + (k + 1) * G * N].reshape(G, N), H // G, 0)
+                  for k in (0, 1))
+        delta = np.log1p(np.exp(raw[i].astype(np.float64) - 4.6))
+        st64[i] = np.exp(-delta)[:, None, None] * st64[i] + (delta[:, None] * x)[..., None] * Bm[:, None]
+        want[i] = np.einsum("hpn,hn->hp", st64[i], Cm)
+    ref.assert_close(y, want, dt, "y")
+    ref.assert_close(st, st64, "f32", "state")
+    assert np.array_equal(win.double().cpu().numpy(), win64)
+
+
+def test_every_operator_on_a_stream_of_its_own(ssd):  # noqa: F811
+    """``stream=``: a chain of calls there, ordered behind a long copy by that stream alone, gives what
+    the current stream gives."""
+    import torch
+    H, P, N, K, T = 8, 64, 64, 4, 3000
+    C, D = H * P + 2 * N, H * P
+    gen = torch.Generator(device="cuda").manual_seed(6)
+
+    def rnd(*s, dt=torch.bfloat16):
+        return torch.randn(*s, generator=gen, device="cuda").to(dt)
+
+    src = rnd(1, T, C)
+    w, b, gw = rnd(C, K, dt=torch.float32), rnd(C, dt=torch.float32), rnd(D, dt=torch.float32)
+    z, tok, raw = rnd(1, T, D), rnd(3, C), rnd(3, H, dt=torch.float32)
+    state, win = rnd(3, H, P, N, dt=torch.float32), rnd(3, K, C)
+    pos = torch.tensor([4, 9, 2], dtype=torch.int32, device="cuda")
+    big = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    s = torch.cuda.Stream()
+
+    def chain(u, s_, w_, stream):
+        kw = {} if stream is None else {"stream": stream}
+        o, f = ssd.conv_forward(u, w, b, split=((H, P), (1, N), (1, N)), final_state=True, **kw)
+        y, r = ssd.gated_norm_forward(o[0], z, gw, **kw)
+        gn = ssd.gated_norm_backward(y, o[0], z, gw, r, **kw)
+        gc = ssd.conv_backward(u, w, b, (gn["dy"], o[1], o[2]), **kw)
+        n, _, st = ssd.norm_forward(y, gw, **kw)
+        nb = ssd.norm_backward(n, y, gw, st, **kw)
+        t = ssd.conv_decode_step(s_, w_, tok, raw, w, b, pos, -4.6, **kw)
+        return [*o, f, y, r, *gn.values(), *gc.values(), n, st, *nb.values(), t, s_, w_]
+
+    want = chain(src, state.clone(), win.clone(), None)
+    u = torch.zeros_like(src)
+    s2, w2 = state.clone(), win.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):  # what the chain reads arrives late on its stream
+        for _ in range(8):
+            big.fill_(1.0)
+        u.copy_(src)
+    got = chain(u, s2, w2, s)
+    s.synchronize()
+    for x, y in zip(got, want):
+        assert bool((x == y).all())
+
+
+def test_norm_offsets_beyond_32_bits(ssd):  # noqa: F811
+    """2,100,000 rows of 1152 columns, 2.4e9 elements a tensor: the last rows' gradients, and the sums
+    over all rows, of which only the first and the last are not zero."""
+    import torch
+    R, D, G, n = 2_100_000, 1152, 2, 32
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    rng = np.random.default_rng(43)
+    at = np.r_[0:n, R - n:R]
+    rows = torch.from_numpy(at).cuda()
+
+    def tensor(dt):
+        t = torch.zeros(R, D, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device="cuda")
+        v, v64 = _dev(rng.standard_normal((2 * n, D)), dt)
+        t[rows] = v
+        return t, v64
+
+    w, w64 = _dev(1 + 0.2 * rng.standard_normal(D), "f32")
+    (y, y64), (z, z64), (do, do64) = tensor("bf16"), tensor("bf16"), tensor("bf16")
+    out, rstd = ssd.gated_norm_forward(y, z, w, groups=G)
+    wo, wr = ref.gated(y64, z64, w64, 1e-5, G)
+    ref.assert_close(out[rows], wo, "bf16", "out")
+    ref.assert_close(rstd[rows], wr, "f32", "rstd")
+    del out
+    g = ssd.gated_norm_backward(do, y, z, w, rstd, groups=G)
+    dy, dz, dw = ref.gated_bwd(do64, y64, z64, w64, rstd[rows].double().cpu().numpy(), G)
+    ref.assert_close(g["dy"][rows], dy, "bf16", "dy")
+    ref.assert_close(g["dz"][rows], dz, "bf16", "dz")
+    ref.assert_close(g["d_weight"], dw, "f32", "d_weight")
+    del g, y, z, rstd
+    h, h64 = tensor("f32")
+    dh, dh64 = tensor("f32")
+    _, _, st = ref.norm(h64, w64, None, None, 1e-5, True)
+    stats = torch.zeros(R, 2, device="cuda")
+    stats[rows] = torch.from_numpy(st.astype(np.float32)).cuda()
+    g = ssd.norm_backward(do, h, w, stats, dh=dh)
+    dv, dw, db = ref.norm_bwd(do64, h64, w64, stats[rows].double().cpu().numpy(), dh64, True)
+    ref.assert_close(g["dx"][rows], dv, "bf16", "dx")
+    ref.assert_close(g["d_residual"][rows], dv, "f32", "d_residual")
+    ref.assert_close(g["d_weight"], dw, "f32", "d_weight")
+    ref.assert_close(g["d_bias"], db, "f32", "d_bias")
+
+
+# More rows than the GPU holds at once, so that every block goes round its ring.
+@pytest.mark.parametrize("dt,rdt,D", [("f32", "f32", 12288), ("bf16", "f32", 16384), ("bf16", "bf16", 9000),
+                                      ("f32", None, 16384), ("bf16", None, 12000)])
+def test_long_rows(ssd, dt, rdt, D):  # noqa: F811
+    import torch
+    R = 700
+    rng = np.random.default_rng(D)
+    x, x64 = _dev(rng.standard_normal((R, D)), dt)
+    res, res64 = _dev(rng.standard_normal((R, D)), rdt) if rdt else (None, None)
+    dy, dy64 = _dev(rng.standard_normal((R, D)), dt)
+    w, w64 = _dev(1 + 0.2 * rng.standard_normal(D), "f32")
+    y, h, stats = ssd.norm_forward(x, w, residual=res)
+    wy, wh, _ = ref.norm(x64, w64, None, res64, 1e-5, True)
+    ref.assert_close(y, wy, dt, "y")
+    h64 = h.double().cpu().numpy()
+    ref.assert_close(h, wh, rdt or dt, "h")
+    g = ssd.norm_backward(dy, h, w, stats, dh=res)
+    dv, dw, db = ref.norm_bwd(dy64, h64, w64, stats.double().cpu().numpy(), res64, True)
+    ref.assert_close(g["dx"], dv, dt, "dx")
+    ref.assert_close(g["d_weight"], dw, "f32", "d_weight")
+    ref.assert_close(g["d_bias"], db, "f32", "d_bias")
+    z, z64 = _dev(rng.standard_normal((R, D)), dt)
+    out, rstd = ssd.gated_norm_forward(x, z, w)
+    wo, _ = ref.gated(x64, z64, w64, 1e-5, 1)
+    ref.assert_close(out, wo, dt, "out")
+    gg = ssd.gated_norm_backward(dy, x, z, w, rstd)
+    ey, ez, ew = ref.gated_bwd(dy64, x64, z64, w64, rstd.double().cpu().numpy(), 1)
+    ref.assert_close(gg["dy"], ey, dt, "dy")
+    ref.assert_close(gg["dz"], ez, dt, "dz")
+    ref.assert_close(gg["d_weight"], ew, "f32", "gated d_weight")
