@@ -21,7 +21,8 @@
  *    buffers).  The caller owns every buffer; the library allocates nothing on
  *    the device and keeps no pointer after a call returns.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
- *    default stream).  No call synchronises except ssd_device_status().
+ *    default stream).  No call synchronises except the queries of a status
+ *    (ssd_device_status(), ssd_forward_noalloc_status(), ssd_layer_status()).
  *  - Host-side argument checks run before any launch; on failure nothing is
  *    launched and a nonzero ssd_status_t is returned.  Errors that only the
  *    device can see (a malformed cu_seqlens array) are recorded in a status

@@ -112,9 +112,12 @@ struct RowPlan {
 // Longest rows.
 constexpr int most_columns(int vec) { return vec >= 4 ? 16384 : 8192; }
 constexpr int most_vectors(int vec) { return vec == 8 ? 4 : vec == 1 ? 16 : 8; }
-// Registers of a thread that holds e elements of a row: what the kernels need without spilling
-// (up to 16 elements; more are held only on the longest rows), and no more, since they decide
-// how many rows an SM works on.
+// Registers of a thread that holds e elements of a row: few, since they decide how many rows an SM
+// works on.  They do not hold everything.  A thread stores to local memory (-Xptxas -v) 4 to 64
+// bytes in some backwards of up to 16 elements in wide vectors; 48 to 240 in the forwards without a
+// residual and the float32 gated one at 32 elements, which rows of 832 columns on may take; 16 to 384
+// in backwards of 12 and 16 elements in pairs or single elements (more than 4096 columns); and beyond
+// 8192 columns 300 to 1360 in the backwards, 108 to 768 in forwards with a residual.
 constexpr int fwd_regs(int vec, int nv) {
     const int e = vec * nv;
     return e <= 2 ? 40 : e <= 4 ? 56 : e <= 8 ? 80 : 128;
@@ -134,14 +137,18 @@ inline bool plan_row(int dim, int vec, const RowCost& cost, RowPlan* p) {
     if (dim > most_columns(vec)) return false;
     p->vec = vec;
     const int nvec = (dim + vec - 1) / vec;
-    // Elements a thread holds, where more threads do as well.  At 32768 x 2560 (us): a forward
+    // Elements a thread holds, where more threads do as well, in bf16 rows but for the residuals and
+    // gradients named.  At 32768 x 2560 (us): a forward
     // without a residual 72 with 16, 65 with 32 (at 32768 x 5120 221 and 114; single elements
     // 130 with 8, 107 with 16); with a bf16 residual 113, 107, 133 with 16, 24, 32; with a float32
     // residual 168, 160, 184 with 12, 16, 24 (single elements 202, 212 with 8, 16); a backward
     // with the residual's gradient 222, 267 with 8, 16 (single elements 309, 273 with 4, 8),
-    // without it 134, 109.
+    // without it 134, 109.  Float32 rows take the same counts: a forward without a residual 133
+    // (74 % of the copy rate), its row ahead alone 32 registers; fewer were not tried there.
     const int hold = cost.bwd ? (vec <= 2 || cost.nb > 1 ? 8 : 16)
                               : cost.nb == 0 ? (vec == 1 ? 16 : 32) : vec == 1 ? 8 : vec == 8 ? 24 : 16;
+    // The constants here and below come from the widths that their figures name; between those they
+    // are steps (512 threads leave ten warps an SM at 2560 columns, sixteen at 2048 and 4096).
     // A warp spends about as long on a row's sums and addresses as on fourteen elements a lane,
     // and up to sixteen warps on an SM each add their share of its rate: the plan with the least
     // of that time per row wins.

@@ -25,10 +25,13 @@
 //
 // GB300, bf16, K = 4, SiLU: forward of 32768 x 5376 119 us (88 % of the measured copy rate on 2
 // bytes in and 2 out an element), of 65536 packed tokens x 1792 91 us (76 %: the B and C pieces
-// fill half of their blocks' lanes); backward of 32768 x 5376 222 us (70 % on 6 bytes an
-// element, its partial sums included), where the instructions of 16 warps an SM bound it: four
-// channels a lane take 128 registers, two 342 us for their overhead, eight 295 us for want of
-// warps.
+// fill half of their blocks' lanes); backward of 32768 x 5376 219 us (71 % on 6 bytes an
+// element, its partial sums included), of 65536 packed tokens x 1792 157 us (66 %).  The backward
+// fills neither memory nor the issue slots (at half the size DRAM 58 %, SM 48 % busy): sixteen warps
+// an SM, of 128 registers a thread, wait for the chain of a token's taps, sigmoid, slope and sums
+// (25 instructions an element).  Four channels a lane measured best: two 342 us for their overhead,
+// eight 295 us for want of warps.  Float32, 32768 x 5376: forward 244, backward 368 us (85 % both).
+// Rows off 16 bytes (pairs or single elements): forward 43 to 68 %, backward 20 to 53 %.
 #include <limits.h>
 
 #include "layer_device.cuh"

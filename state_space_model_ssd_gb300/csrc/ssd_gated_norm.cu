@@ -10,9 +10,11 @@
 // Bound by HBM (three tensors forward, five backward).  A (row, group) is one row of a team;
 // blocks stay with one group, so that the backward's dw stays in registers.
 //
-// GB300, 32768 x 5120, bf16: forward 155 us (96 % of the measured copy rate); backward 276 us in
-// one group (90 %), 324 in eight (76 %: three warps a row of 640 columns leave a sixth of their
-// lanes idle and share out the sums' fixed cost less well).
+// GB300, 32768 x 5120, bf16: forward 155 us (95 % of the measured copy rate); backward 276 us in
+// one group (90 %), 327 in eight (76 %: three warps a row of 640 columns leave a sixth of their
+// lanes idle and share out the sums' fixed cost less well).  Float32, 16384 x 5120: forward 216 us
+// (69 %: its 32 elements a thread spill), backward 305 us (81 %).  bf16, 8192 x 16384: forward
+// 126 us (94 %), backward 483 us (41 %: spills).
 #include <limits.h>
 
 #include "layer_device.cuh"
