@@ -414,6 +414,111 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
                                      void* dy, void* dz, void* d_weight, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------- linear attention and beam search
+ *
+ * The rules of the section above hold here too (alignment of the element type, strides,
+ * overlaps, ssd_layer_status); workspaces are 256-byte aligned.
+ *
+ * Linear attention with a decay for each head: with a = exp(log_decay[h]), every token t
+ *     S_t = a S_{t-1} + v_t k_t^T            (S is P x N, float32)
+ *     o_t = scale S_t q_t
+ * with S = initial_state (or zero) before the first token of every sequence.  log_decay is
+ * float32 device memory, zero or negative (-inf: nothing is remembered), and takes no
+ * gradient.  Query heads h read key and value head h / (H / G); each has a state of its own, in
+ * the layout of the scan's.  q [T][H][N], k [T][G][N], v [T][G][P], o [T][H][P]: the heads of a
+ * token lie next to one another, tokens `stride` elements apart; tensors of the same stride may
+ * lie between one another's tokens (slices of one projection's rows).  A malformed cu_seqlens is
+ * clamped as in the convolution; outputs of tokens behind the last sequence are zero.  bf16
+ * calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
+ * blocks of 128 tokens: there a NaN or an infinity in a token reaches the outputs of all tokens
+ * of its sequence in its block.  Others run the same walk on the plain cores. */
+typedef struct {
+    int64_t batch;       /* rows of a dense batch; 1 with cu_seqlens */
+    int64_t seqlen;      /* tokens per row; with cu_seqlens: all tokens T (<= 2^31 - 1) */
+    int64_t q_stride, k_stride, v_stride;
+    int64_t o_stride;    /* o; its gradient in the backward */
+    int64_t dq_stride, dk_stride, dv_stride; /* backward (0 in a forward) */
+    int32_t nheads;      /* H */
+    int32_t ngroups;     /* G, divides H */
+    int32_t headdim;     /* P, 1 to 128 */
+    int32_t dstate;      /* N, 1 to 128 */
+    int32_t nseq;        /* 0: dense batch; > 0: number of packed sequences */
+    int32_t dtype;       /* ssd_dtype_t of q, k, v, o and their gradients */
+    float scale;
+} ssd_linattn_t;
+
+/* Bytes of workspace of ssd_linear_attention_forward (for_backward = 0, may be 0) or
+ * _backward; they follow the current device's SM count. */
+ssd_status_t ssd_linear_attention_workspace_size(const ssd_linattn_t* prob, int for_backward,
+                                                 size_t* bytes);
+
+/* initial_state, final_state: [nseq or batch][H][P][N] float32, or NULL.  The final state of an
+ * empty sequence is its initial one. */
+ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void* q, const void* k,
+                                          const void* v, const float* log_decay,
+                                          const int32_t* cu_seqlens, const float* initial_state,
+                                          void* o, float* final_state, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Gradients of q, k and v (k's and v's summed over the heads that share them) and, when
+ * d_initial_state is not NULL, of the initial states, from those of o and (d_final_state, or
+ * NULL: zero) of the final states.  The same inputs give the same bits in every call. */
+ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void* q, const void* k,
+                                           const void* v, const float* log_decay,
+                                           const int32_t* cu_seqlens, const float* initial_state,
+                                           const void* dout, const float* d_final_state, void* dq,
+                                           void* dk, void* dv, float* d_initial_state,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of prob->batch rows (prob->seqlen = 1, nseq = 0).  Row i uses cache slot
+ * slots[i] (NULL: i) of state [nslots][H][P][N] float32, updated in place; a slot outside
+ * 0 .. nslots - 1 marks a padding row, whose o is zero and which touches no state.  The live
+ * rows' slots must differ. */
+ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int32_t nslots, float* state,
+                                       const void* q, const void* k, const void* v,
+                                       const float* log_decay, const int32_t* slots, void* o,
+                                       void* stream);
+
+/* Beam search: of the candidates (beam i, token t) of each batch row, with the score
+ *     scores[i] + logits[i][t] - log sum_u exp(logits[i][u]),
+ * the `keep` best, best first.  Candidates of one beam are ordered by their logits, those of
+ * different beams by their scores before rounding to float32; equal ones by beam, then token.
+ * finished (one byte a beam, not 0: ended; NULL: none has): such a beam has the one candidate
+ * pad_token, at its score.  What is left out, tokens with a logit of -inf and every token of a
+ * beam whose score is not finite or whose logits hold a NaN or +inf or nothing but -inf, has the
+ * score -inf. */
+typedef struct {
+    int64_t batch;
+    int64_t stride;      /* elements from one beam's logits to the next (>= vocab) */
+    int32_t beams;       /* 1 to 64 */
+    int32_t vocab;       /* <= 2^24 */
+    int32_t keep;        /* 1 to 64, <= beams * vocab */
+    int32_t pad_token;
+    int32_t dtype;       /* ssd_dtype_t of the logits */
+} ssd_beam_t;
+
+ssd_status_t ssd_beam_select_workspace_size(const ssd_beam_t* beam, size_t* bytes);
+
+/* logits [batch][beams][vocab], scores [batch][beams] float32; out_scores float32, parents
+ * (the beam) and tokens int32, all [batch][keep]. */
+ssd_status_t ssd_beam_select(const ssd_beam_t* beam, const void* logits, const float* scores,
+                             const uint8_t* finished, float* out_scores, int32_t* parents,
+                             int32_t* tokens, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Beam search over cached states: beam j of each batch row goes on from the state of beam
+ * parents[j] (parents, slots, new_slots: int32 [batch][beams], beams 1 to 64).  The first beam
+ * with a parent takes its parent's slot; each other one takes the next slot, in the order of
+ * the beams, of a beam that nobody goes on from, and the parent's state is copied there in each
+ * of `ncaches` caches: cache i holds nslots slots of slot_bytes[i] bytes, slot_strides[i] bytes
+ * apart (host arrays).  So only the states of beams that are doubled move, in place.  A beam
+ * whose parent lies outside 0 .. beams - 1 gets slot -1; a slot outside 0 .. nslots - 1 is
+ * passed on and its states are left alone.  The slots of live beams must differ. */
+ssd_status_t ssd_beam_reorder(int64_t batch, int32_t beams, const int32_t* slots,
+                              const int32_t* parents, int32_t* new_slots, int32_t ncaches,
+                              void* const* caches, const int64_t* slot_bytes,
+                              const int64_t* slot_strides, int32_t nslots, void* stream);
+
 /* Synchronises `stream` and returns in *device_status the status word that
  * the last call using `workspace` left (SSD_OK, SSD_ERR_DEVICE, SSD_ERR_TIMEOUT).
  * Returns SSD_ERR_CUDA if the synchronisation itself failed. */

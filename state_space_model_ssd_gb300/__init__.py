@@ -13,7 +13,9 @@ B, C ``[batch, L, G, N]``; with ``cu_seqlens`` (int32, ``[nseq + 1]``) the batch
 is 1 and the tokens are packed sequences.
 
 The operators that stand around the scan in a layer (``conv_forward``, ``conv_decode_step``,
-``norm_forward``, ``gated_norm_forward`` and their backward passes) are in ``layer``.
+``norm_forward``, ``gated_norm_forward`` and their backward passes) are in ``layer``, linear
+attention with a decay for each head (``linear_attention_forward``, ``_backward``, ``_step``) in
+``attention``, beam search over cached states (``beam_select``, ``beam_reorder``) in ``beam``.
 """
 
 from __future__ import annotations
@@ -27,16 +29,24 @@ from ._lib import SSDError, check
 __all__ = ["forward", "backward", "bidirectional_forward", "bidirectional_backward", "decode_step", "step_host", "step_host_size", "workspace_size",
            "dispatch_path", "make_problem", "last_launch_count", "profiler", "SSDError",
            "conv_forward", "conv_backward", "conv_decode_step", "norm_forward", "norm_backward",
-           "gated_norm_forward", "gated_norm_backward", "layer_status"]
+           "gated_norm_forward", "gated_norm_backward", "layer_status",
+           "linear_attention_forward", "linear_attention_backward", "linear_attention_step",
+           "beam_select", "beam_reorder"]
 
-_LAYER = frozenset(__all__[-8:])
+# the modules that are imported when one of their functions is first used
+_LATER = {name: "layer" for name in ("conv_forward", "conv_backward", "conv_decode_step", "norm_forward",
+                                     "norm_backward", "gated_norm_forward", "gated_norm_backward",
+                                     "layer_status")}
+_LATER.update({name: "attention" for name in ("linear_attention_forward", "linear_attention_backward",
+                                              "linear_attention_step")})
+_LATER.update({name: "beam" for name in ("beam_select", "beam_reorder")})
 
 
 def __getattr__(name):
-    # the operators around the scan live in .layer: imported on first use
-    if name in _LAYER:
-        from . import layer
-        globals()[name] = f = getattr(layer, name)
+    if name in _LATER:
+        import importlib
+        f = getattr(importlib.import_module("." + _LATER[name], __name__), name)
+        globals()[name] = f
         return f
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 

@@ -86,6 +86,41 @@ class GatedNormProblem(ctypes.Structure):
     ]
 
 
+class LinAttnProblem(ctypes.Structure):
+    """Mirror of ssd_linattn_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("o_stride", ctypes.c_int64),
+        ("dq_stride", ctypes.c_int64),
+        ("dk_stride", ctypes.c_int64),
+        ("dv_stride", ctypes.c_int64),
+        ("nheads", ctypes.c_int32),
+        ("ngroups", ctypes.c_int32),
+        ("headdim", ctypes.c_int32),
+        ("dstate", ctypes.c_int32),
+        ("nseq", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class BeamProblem(ctypes.Structure):
+    """Mirror of ssd_beam_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("stride", ctypes.c_int64),
+        ("beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("keep", ctypes.c_int32),
+        ("pad_token", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 class SSDError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -99,6 +134,8 @@ _PP = ctypes.POINTER(Problem)
 _PC = ctypes.POINTER(ConvProblem)
 _PN = ctypes.POINTER(NormProblem)
 _PG = ctypes.POINTER(GatedNormProblem)
+_PL = ctypes.POINTER(LinAttnProblem)
+_PB = ctypes.POINTER(BeamProblem)
 _SZ = ctypes.c_size_t
 _I32 = ctypes.c_int32
 _SIGS = {
@@ -134,6 +171,14 @@ _SIGS = {
     "ssd_gated_norm_forward": (ctypes.c_int, [_PG] + [_VP] * 6),
     "ssd_gated_norm_workspace_size": (ctypes.c_int, [_PG, ctypes.POINTER(_SZ)]),
     "ssd_gated_norm_backward": (ctypes.c_int, [_PG] + [_VP] * 9 + [_SZ, _VP]),
+    "ssd_linear_attention_workspace_size": (ctypes.c_int, [_PL, ctypes.c_int, ctypes.POINTER(_SZ)]),
+    "ssd_linear_attention_forward": (ctypes.c_int, [_PL] + [_VP] * 9 + [_SZ, _VP]),
+    "ssd_linear_attention_backward": (ctypes.c_int, [_PL] + [_VP] * 13 + [_SZ, _VP]),
+    "ssd_linear_attention_step": (ctypes.c_int, [_PL, _I32] + [_VP] * 8),
+    "ssd_beam_select_workspace_size": (ctypes.c_int, [_PB, ctypes.POINTER(_SZ)]),
+    "ssd_beam_select": (ctypes.c_int, [_PB] + [_VP] * 7 + [_SZ, _VP]),
+    "ssd_beam_reorder": (ctypes.c_int, [ctypes.c_int64, _I32] + [_VP] * 3 + [_I32] + [_VP] * 3 +
+                         [_I32, _VP]),
     "ssd_device_status": (ctypes.c_int, [_VP, _VP, ctypes.POINTER(ctypes.c_int32)]),
     "ssd_dispatch_path": (ctypes.c_char_p, [_PP, ctypes.c_int]),
     "ssd_last_launch_count": (ctypes.c_int, []),

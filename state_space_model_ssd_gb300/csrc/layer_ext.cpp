@@ -1,10 +1,11 @@
-// The operators around the scan as functions on torch tensors: checks of the arguments,
+// The operators around the scan, linear attention and beam search as functions on torch tensors: checks of the arguments,
 // allocation of what the caller did not bring, and the call into libssd.so on the current
 // stream.  A CPython module rather than a ctypes binding because the smallest calls (a
 // handful of rows, one token) spend longer in the host code than on the GPU: a call costs
 // about a third of what the same steps take in Python.
 //
-// Positional arguments only; the Python module `layer` has the signatures and documents them.
+// Positional arguments only; the Python modules `layer`, `attention` and `beam` have the signatures
+// and document them.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -12,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "ssd.h"
@@ -734,6 +736,291 @@ PyObject* gated_norm_backward(PyObject* const* a) {
     return g.release();
 }
 
+// ------------------------------------------------------------------ linear attention
+// The stride between the tokens of t [..., heads, channels], whose heads lie next to one another.
+int64_t tokens(const Tensor& t, const char* name) {
+    const int64_t d = t.dim(), H = t.size(d - 2), D = t.size(d - 1);
+    if (t.is_contiguous()) return H * D;
+    if ((D > 1 && t.stride(d - 1) != 1) || (H > 1 && t.stride(d - 2) != D))
+        value_error(std::string(name) + ": the heads of a token must lie next to one another");
+    int64_t step = -1, span = 1;
+    for (int64_t i = d - 3; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (step < 0)
+            step = t.stride(i);
+        else if (t.stride(i) != span * step)
+            value_error(std::string(name) + ": tokens must be evenly spaced");
+        span *= t.size(i);
+    }
+    if (step < 0) return H * D;
+    if (step < H * D) value_error(std::string(name) + ": tokens overlap");
+    return step;
+}
+int64_t tokens(const Tensor& t, const char* name, at::Device dev, at::ScalarType type,
+               at::IntArrayRef shape) {
+    on_device(t, name, dev);
+    of_type(t, name, type);
+    of_shape(t, name, shape);
+    return tokens(t, name);
+}
+
+struct AttnCall {
+    ssd_linattn_t p;
+    int64_t n;
+};
+void attn_problem(AttnCall* c, const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& ld,
+                  PyObject* scale, const Tensor* cu, const Tensor* init) {
+    on_gpu(q, "q");
+    if (q.dim() != 4 || k.dim() != 4 || v.dim() != 4)
+        value_error("q must be [batch, L, H, N], k [batch, L, G, N], v [batch, L, G, P]");
+    const auto dev = q.device();
+    const auto type = q.scalar_type();
+    const int64_t B = q.size(0), L = q.size(1), H = q.size(2), N = q.size(3), G = k.size(2), P = v.size(3);
+    if (H > INT32_MAX || N > INT32_MAX || P > INT32_MAX || G < 1 || H % G != 0)
+        value_error("q has " + std::to_string(H) + " heads, k " + std::to_string(G));
+    c->p = {};
+    c->p.dtype = code(q, "q");
+    c->p.q_stride = tokens(q, "q");
+    c->p.k_stride = tokens(k, "k", dev, type, {B, L, G, N});
+    c->p.v_stride = tokens(v, "v", dev, type, {B, L, G, P});
+    check(ld, "log_decay", dev, at::kFloat, {H});
+    int64_t nseq = 0;
+    if (cu) {
+        on_device(*cu, "cu_seqlens", dev);
+        of_type(*cu, "cu_seqlens", at::kInt);
+        contiguous(*cu, "cu_seqlens");
+        if (B != 1) value_error("packed sequences need batch == 1");
+        nseq = cu->numel() - 1;
+        if (cu->dim() != 1 || nseq < 1) value_error("cu_seqlens must be [nseq + 1]");
+        if (nseq > INT32_MAX) throw Status{SSD_ERR_UNSUPPORTED, "ssd_linear_attention"};
+    }
+    c->n = nseq ? nseq : B;
+    if (init) check(*init, "initial_state", dev, at::kFloat, {c->n, H, P, N});
+    c->p.batch = B, c->p.seqlen = L, c->p.nseq = (int32_t)nseq;
+    c->p.nheads = (int32_t)H, c->p.ngroups = (int32_t)G, c->p.headdim = (int32_t)P, c->p.dstate = (int32_t)N;
+    c->p.o_stride = H * P;
+    c->p.scale = scale == Py_None ? (float)(1.0 / std::sqrt((double)N)) : (float)number(scale);
+}
+float* floats(const Tensor* t) { return static_cast<float*>(ptr(t)); }
+float* floats(const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
+int32_t* ints(const Tensor* t) { return static_cast<int32_t*>(ptr(t)); }
+
+// q, k, v, log_decay, scale, cu_seqlens, initial_state, final_state, out, final_state_out, workspace
+PyObject* linear_attention_forward(PyObject* const* a) {
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Tensor& ld = tensor(a[3], "log_decay");
+    const Tensor *cu = maybe(a[5], "cu_seqlens"), *init = maybe(a[6], "initial_state");
+    AttnCall c;
+    attn_problem(&c, q, k, v, ld, a[4], cu, init);
+    const auto dev = q.device();
+    const int64_t B = q.size(0), L = q.size(1), H = q.size(2), N = q.size(3), P = v.size(3);
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor o, final;
+    if (a[8] == Py_None) {
+        o = empty({B, L, H, P}, q.scalar_type(), dev);
+    } else {
+        o = tensor(a[8], "out");
+        c.p.o_stride = tokens(o, "out", dev, q.scalar_type(), {B, L, H, P});
+    }
+    if (a[9] != Py_None) {
+        final = tensor(a[9], "final_state_out");
+        check(final, "final_state_out", dev, at::kFloat, {c.n, H, P, N});
+    } else if (truth(a[7])) {
+        final = empty({c.n, H, P, N}, at::kFloat, dev);
+    }
+    size_t need = 0;
+    ok(ssd_linear_attention_workspace_size(&c.p, 0, &need), "ssd_linear_attention_workspace_size");
+    const Scratch ws(a[10], need, dev);
+    ok(ssd_linear_attention_forward(&c.p, q.data_ptr(), k.data_ptr(), v.data_ptr(), floats(&ld), ints(cu),
+                                    floats(init), o.data_ptr(), floats(final), ws.p, ws.n, stream_of(dev)),
+       "ssd_linear_attention_forward");
+    return tuple({wrap(o), wrap(final)});
+}
+
+// q, k, v, log_decay, do, scale, cu_seqlens, initial_state, d_final_state, d_initial_state, out,
+// workspace
+PyObject* linear_attention_backward(PyObject* const* a) {
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Tensor &ld = tensor(a[3], "log_decay"), &dout = tensor(a[4], "do");
+    const Tensor *cu = maybe(a[6], "cu_seqlens"), *init = maybe(a[7], "initial_state");
+    const Tensor* dfinal = maybe(a[8], "d_final_state");
+    AttnCall c;
+    attn_problem(&c, q, k, v, ld, a[5], cu, init);
+    const auto dev = q.device();
+    const auto type = q.scalar_type();
+    const int64_t B = q.size(0), L = q.size(1), H = q.size(2), N = q.size(3), P = v.size(3);
+    c.p.o_stride = tokens(dout, "do", dev, type, {B, L, H, P});
+    if (dfinal) check(*dfinal, "d_final_state", dev, at::kFloat, {c.n, H, P, N});
+    const c10::cuda::CUDAGuard guard(dev);
+    Dict g(a[10]);
+    struct Grad {
+        const char* name;
+        const Tensor& of;
+        int64_t* stride;
+        Tensor t;
+    } grads[3] = {{"dq", q, &c.p.dq_stride, {}}, {"dk", k, &c.p.dk_stride, {}}, {"dv", v, &c.p.dv_stride, {}}};
+    for (Grad& d : grads) {
+        d.t = brought(a[10], d.name);
+        if (d.t.defined())
+            *d.stride = tokens(d.t, d.name, dev, type, d.of.sizes());
+        else
+            d.t = empty(d.of.sizes(), type, dev), *d.stride = d.of.size(2) * d.of.size(3);
+    }
+    Tensor d0 = brought(a[10], "d_initial_state");  // what `out` brings is written, asked for or not
+    if (d0.defined())
+        check(d0, "d_initial_state", dev, at::kFloat, {c.n, H, P, N});
+    else if (truth(a[9]))
+        d0 = empty({c.n, H, P, N}, at::kFloat, dev);
+    size_t need = 0;
+    ok(ssd_linear_attention_workspace_size(&c.p, 1, &need), "ssd_linear_attention_workspace_size");
+    const Scratch ws(a[11], need, dev);
+    ok(ssd_linear_attention_backward(&c.p, q.data_ptr(), k.data_ptr(), v.data_ptr(), floats(&ld), ints(cu),
+                                     floats(init), dout.data_ptr(), floats(dfinal), grads[0].t.data_ptr(),
+                                     grads[1].t.data_ptr(), grads[2].t.data_ptr(), floats(d0), ws.p, ws.n,
+                                     stream_of(dev)),
+       "ssd_linear_attention_backward");
+    for (const Grad& d : grads) g.set(d.name, d.t);
+    if (d0.defined()) g.set("d_initial_state", d0);
+    return g.release();
+}
+
+// state, q, k, v, log_decay, scale, slots, out
+PyObject* linear_attention_step(PyObject* const* a) {
+    const Tensor &state = tensor(a[0], "state"), &q = tensor(a[1], "q"), &k = tensor(a[2], "k");
+    const Tensor &v = tensor(a[3], "v"), &ld = tensor(a[4], "log_decay");
+    const Tensor* slots = maybe(a[6], "slots");
+    on_gpu(q, "q");
+    if (q.dim() != 3 || k.dim() != 3 || v.dim() != 3 || state.dim() != 4)
+        value_error("q must be [batch, H, N], k [batch, G, N], v [batch, G, P], state [nslots, H, P, N]");
+    const auto dev = q.device();
+    const auto type = q.scalar_type();
+    const int64_t B = q.size(0), H = q.size(1), N = q.size(2), G = k.size(1), P = v.size(2), n = state.size(0);
+    if (G < 1 || H % G != 0)
+        value_error("q has " + std::to_string(H) + " heads, k " + std::to_string(G));
+    if (n > INT32_MAX || H > INT32_MAX || N > INT32_MAX || P > INT32_MAX)
+        throw Status{SSD_ERR_UNSUPPORTED, "ssd_linear_attention_step"};
+    ssd_linattn_t p = {};
+    p.batch = B, p.seqlen = 1;
+    p.nheads = (int32_t)H, p.ngroups = (int32_t)G, p.headdim = (int32_t)P, p.dstate = (int32_t)N;
+    p.dtype = code(q, "q");
+    p.q_stride = tokens(q, "q");
+    p.k_stride = tokens(k, "k", dev, type, {B, G, N});
+    p.v_stride = tokens(v, "v", dev, type, {B, G, P});
+    p.o_stride = H * P;
+    p.scale = a[5] == Py_None ? (float)(1.0 / std::sqrt((double)N)) : (float)number(a[5]);
+    check(state, "state", dev, at::kFloat, {n, H, P, N});
+    check(ld, "log_decay", dev, at::kFloat, {H});
+    if (slots) check(*slots, "slots", dev, at::kInt, {B});
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor o;
+    if (a[7] == Py_None) {
+        o = empty({B, H, P}, type, dev);
+    } else {
+        o = tensor(a[7], "out");
+        p.o_stride = tokens(o, "out", dev, type, {B, H, P});
+    }
+    ok(ssd_linear_attention_step(&p, (int32_t)n, floats(&state), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                 floats(&ld), ints(slots), o.data_ptr(), stream_of(dev)),
+       "ssd_linear_attention_step");
+    return wrap(o);
+}
+
+// ------------------------------------------------------------------ beam search
+// logits, scores, keep, finished, pad_token, out, workspace
+PyObject* beam_select(PyObject* const* a) {
+    const Tensor &x = tensor(a[0], "logits"), &scores = tensor(a[1], "scores");
+    const Tensor* finished = maybe(a[3], "finished");
+    on_gpu(x, "logits");
+    if (x.dim() != 3) value_error("logits must be [batch, beams, vocab]");
+    const auto dev = x.device();
+    const int64_t B = x.size(0), K = x.size(1), V = x.size(2);
+    if (K > INT32_MAX || V > INT32_MAX) throw Status{SSD_ERR_UNSUPPORTED, "ssd_beam_select"};
+    ssd_beam_t p = {};
+    p.stride = rows(x, "logits");
+    p.dtype = code(x, "logits");
+    p.batch = B, p.beams = (int32_t)K, p.vocab = (int32_t)V;
+    p.keep = a[2] == Py_None ? p.beams : int32(a[2], "keep");
+    p.pad_token = int32(a[4], "pad_token");
+    check(scores, "scores", dev, at::kFloat, {B, K});
+    if (finished) {
+        if (finished->scalar_type() != at::kBool && finished->scalar_type() != at::kByte)
+            type_error("finished must be torch.bool or torch.uint8, got " + text(finished->scalar_type()));
+        check(*finished, "finished", dev, finished->scalar_type(), {B, K});
+    }
+    size_t need = 0;
+    const c10::cuda::CUDAGuard guard(dev);
+    ok(ssd_beam_select_workspace_size(&p, &need), "ssd_beam_select_workspace_size");
+    Tensor out[3];
+    const at::ScalarType types[3] = {at::kFloat, at::kInt, at::kInt};
+    if (a[5] == Py_None) {
+        for (int i = 0; i < 3; ++i) out[i] = empty({B, p.keep}, types[i], dev);
+    } else {
+        if (!PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 3)
+            type_error("out must be a tuple (scores, parents, tokens)");
+        for (int i = 0; i < 3; ++i) {
+            out[i] = tensor(PyTuple_GET_ITEM(a[5], i), "out");
+            check(out[i], "out", dev, types[i], {B, p.keep});
+        }
+    }
+    const Scratch ws(a[6], need, dev);
+    ok(ssd_beam_select(&p, x.data_ptr(), floats(&scores), static_cast<uint8_t*>(ptr(finished)),
+                       floats(out[0]), ints(&out[1]), ints(&out[2]), ws.p, ws.n, stream_of(dev)),
+       "ssd_beam_select");
+    return tuple({wrap(out[0]), wrap(out[1]), wrap(out[2])});
+}
+
+// caches, slots, parents, out
+PyObject* beam_reorder(PyObject* const* a) {
+    const Tensor &slots = tensor(a[1], "slots"), &parents = tensor(a[2], "parents");
+    on_gpu(slots, "slots");
+    if (slots.dim() != 2) value_error("slots must be [batch, beams]");
+    const auto dev = slots.device();
+    const int64_t B = slots.size(0), K = slots.size(1);
+    if (K > INT32_MAX) throw Status{SSD_ERR_UNSUPPORTED, "ssd_beam_reorder"};
+    check(slots, "slots", dev, at::kInt, {B, K});
+    check(parents, "parents", dev, at::kInt, {B, K});
+    if (!PyTuple_Check(a[0]) && !PyList_Check(a[0])) type_error("caches must be a list of tensors");
+    const Py_ssize_t n = PySequence_Size(a[0]);
+    c10::SmallVector<void*, 128> at_;
+    c10::SmallVector<int64_t, 128> bytes, strides;
+    int64_t nslots = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const Tensor& t = tensor(PyList_Check(a[0]) ? PyList_GET_ITEM(a[0], i) : PyTuple_GET_ITEM(a[0], i), "caches");
+        on_device(t, "caches", dev);
+        if (t.dim() < 1) value_error("caches must be [nslots, ...]");
+        if (nslots >= 0 && t.size(0) != nslots)
+            value_error("caches must have the same slots, got " + std::to_string(nslots) + " and " +
+                        std::to_string(t.size(0)));
+        nslots = t.size(0);
+        int64_t span = 1;
+        for (int64_t d = t.dim() - 1; d > 0; --d) {
+            if (t.size(d) != 1 && t.stride(d) != span) value_error("caches: a slot must be contiguous");
+            span *= t.size(d);
+        }
+        if (nslots > 1 && t.stride(0) < span) value_error("caches: slots overlap");
+        if (span == 0) continue;
+        const int64_t e = (int64_t)t.element_size();
+        at_.push_back(t.data_ptr());
+        bytes.push_back(span * e);
+        strides.push_back((nslots > 1 ? t.stride(0) : span) * e);
+    }
+    if (n == 0) nslots = INT32_MAX;
+    if (nslots < 1 || nslots > INT32_MAX || at_.size() > INT32_MAX)
+        throw Status{nslots < 1 ? SSD_ERR_INVALID_ARG : SSD_ERR_UNSUPPORTED, "ssd_beam_reorder"};
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor out;
+    if (a[3] == Py_None) {
+        out = empty({B, K}, at::kInt, dev);
+    } else {
+        out = tensor(a[3], "out");
+        check(out, "out", dev, at::kInt, {B, K});
+    }
+    ok(ssd_beam_reorder(B, (int32_t)K, ints(&slots), ints(&parents), ints(&out), (int32_t)at_.size(),
+                        at_.data(), bytes.data(), strides.data(), (int32_t)nslots, stream_of(dev)),
+       "ssd_beam_reorder");
+    return wrap(out);
+}
+
 // ------------------------------------------------------------------ module
 // No C++ exception leaves a call: ours become Python errors, torch's a RuntimeError.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -785,6 +1072,11 @@ PyMethodDef methods[] = {ENTRY(conv_forward, 11),
                          ENTRY(norm_backward, 9),
                          ENTRY(gated_norm_forward, 6),
                          ENTRY(gated_norm_backward, 8),
+                         ENTRY(linear_attention_forward, 11),
+                         ENTRY(linear_attention_backward, 12),
+                         ENTRY(linear_attention_step, 8),
+                         ENTRY(beam_select, 7),
+                         ENTRY(beam_reorder, 4),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_ext", nullptr, -1, methods,
