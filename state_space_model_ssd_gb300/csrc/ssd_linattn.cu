@@ -450,7 +450,7 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
     f.sn = 1, f.sp = N;
     f.out_f32 = p.dtype == SSD_DTYPE_F32;
     a.npass = 1;
-    const bool tc = p.dtype == SSD_DTYPE_BF16 && tc_fits(f);
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
@@ -520,7 +520,7 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
     d.reverse = 1, d.si = d.su = p.scale, d.sx = 1.f;
     d.s_in = d_final_state, d.s_out = d_initial_state, d.sn = 1, d.sp = N, d.out_f32 = f32;
     a.npass = 3;
-    const bool tc = p.dtype == SSD_DTYPE_BF16 && tc_fits(f) && tc_fits(g) && tc_fits(d);
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f) && tc_fits(g) && tc_fits(d);
     if (r > 1) {  // each head's own part, summed after the walk
         g.out = ws + l.dk_part, g.os = H * N, g.out_f32 = 1;
         d.out = ws + l.dv_part, d.os = H * P, d.out_f32 = 1;

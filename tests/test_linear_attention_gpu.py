@@ -112,11 +112,13 @@ TC = [
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES)
-def test_plain_cores(ssd, shape, dtype):
+def test_any_size(ssd, shape, dtype):
     *sizes, cu, state, strided, offset = shape
     s = _make(*sizes, dtype, cu, state, strided, offset=offset)
-    _forward(ssd, s, False)
-    _backward(ssd, s, False)
+    # the one of 128 x 128 channels takes the tensor cores in bfloat16, and has their roundings
+    tc = dtype == "bf16" and sizes[4] == sizes[5] == 128
+    _forward(ssd, s, tc)
+    _backward(ssd, s, tc)
 
 
 @pytest.mark.parametrize("shape", TC)
