@@ -212,20 +212,20 @@ __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_con
         const long long first = first_segment(a, s), row = (long long)a.H * size;
         float S = p.s_in ? p.s_in[s * row + e] : 0.f;
         const Decay whole(ld, a.Ls);
-        float* at = p.s_sum + first * row + e;
-        if (!p.reverse) {
-            for (int k = 0; k < g.cnt; ++k) {
-                const float add = k + 1 < g.cnt ? at[k * row] : 0.f;
-                at[k * row] = S;
-                S = whole(S) + add;
-            }
-        } else {
-            const Decay last(ld, g.len - (g.cnt - 1) * a.Ls);
-            for (int k = g.cnt - 1; k >= 0; --k) {
-                const float add = k > 0 ? at[k * row] : 0.f;
-                at[k * row] = S;
-                S = (k == g.cnt - 1 ? last(S) : whole(S)) + add;
-            }
+        // from the walk's first segment on, eight loads at a time ahead of the stores
+        const long long step = p.reverse ? -row : row;
+        float* at = p.s_sum + (first + (p.reverse ? g.cnt - 1 : 0)) * row + e;
+        const Decay ahead(ld, p.reverse ? g.len - (g.cnt - 1) * a.Ls : a.Ls);
+        for (int k0 = 0; k0 < g.cnt; k0 += 8) {
+            float add[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add[i] = k0 + i + 1 < g.cnt ? at[(k0 + i) * step] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (k0 + i < g.cnt) {
+                    at[(k0 + i) * step] = S;
+                    S = (k0 + i == 0 ? ahead(S) : whole(S)) + add[i];
+                }
         }
     }
 }

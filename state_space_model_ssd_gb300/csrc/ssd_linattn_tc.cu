@@ -46,7 +46,7 @@ struct Maps {
 struct Geometry {
     int stages, kblocks;    // chunks in shared memory at a time; most blocks of 64 channels of q and k
     int stage_bytes, w_at, s_at, aux_at;
-    long long items;
+    int items;
 };
 
 // Barriers and what else is small, behind the tiles.
@@ -55,13 +55,14 @@ struct Aux {
     uint64_t scores, masked, weights, weights_free, state, outs, outs_free, sums, sums_free;
     uint32_t tmem;
     int stop;
-    float pw[4][32];  // a^0 .. a^31, a copy for each of the scores' warps
+    float pw[4][kQ];  // a^0 .. a^127, a copy for each of the scores' warps
 };
 
 // Waits for a phase, at most kLimitNs: one that runs out records SSD_ERR_TIMEOUT and ends every wait
-// of the block, so that a lost arrival is a status and wrong values, not a hang.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+// of the block, so that a lost arrival is a status and wrong values, not a hang.  What is seldom gone
+// through stays out of line here and below: the tasks' loops have to fit the instruction cache
+// together (with everything inlined, 145 KB of code, a chunk took 1.7 times as long).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
     const uint64_t t0 = globaltimer_ns();
     while (!*stop) {
         if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
@@ -72,7 +73,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     }
     return false;
 }
-// The same for a whole warp, whose lanes go on or stop together.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, stop, status);
+}
+// After a wait that ran out: what is on its way must end before the block does.
+__device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000) && globaltimer_ns() - t0 < kLimitNs) {
+    }
+}
+// wait() for a whole warp, whose lanes go on or stop together.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
     return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
 }
@@ -99,7 +109,7 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 template <int NT>
 __device__ __forceinline__ void split_row(const unsigned char* v, unsigned char* w_out, int row, float w, bool in) {
     const uint32_t base = row * 128, x = row & 7;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         const uint32_t at = base + ((c ^ x) << 4);
         const uint4 raw = *reinterpret_cast<const uint4*>(v + at);
@@ -142,15 +152,17 @@ __device__ __forceinline__ void load_sum16(uint32_t taddr, float* f) {
     }
 }
 
+// Steps of 16 of a product move both operands' descriptors by a constant.
+__device__ __forceinline__ uint64_t moved(uint64_t desc, int bytes) { return desc + (uint64_t)(bytes >> 4); }
+
 // k^T W over the chunk's 128 tokens: `k` and `w` shared-memory addresses.  64 channels of k fill the
 // 128 lanes twice.
 template <int NT>
 __device__ __forceinline__ void mma_sums(uint32_t d, uint32_t k, uint32_t w, int kblocks, uint32_t acc) {
     const uint32_t id = idesc_bf16(128, NT * kV, 1, 1);
+    const uint64_t kd = sw128_desc(k, kblocks == 2 ? kSub : 0, 1024), wd = sw128_desc(w, kSub, 1024);
 #pragma unroll
-    for (int i = 0; i < kQ / 16; ++i)
-        mma_bf16(d, sw128_desc(k + i * 2048, kblocks == 2 ? kSub : 0, 1024), sw128_desc(w + i * 2048, kSub, 1024), id,
-                 acc | (i > 0));
+    for (int i = 0; i < kQ / 16; ++i) mma_bf16(d, moved(kd, i * 2048), moved(wd, i * 2048), id, acc | (i > 0));
 }
 
 struct Item {
@@ -158,22 +170,23 @@ struct Item {
     const Pass* p;
     long long id;
     int pass, h, v0, chunks;
+    float ld;
 };
-__device__ __forceinline__ Item take(const WalkArgs& a, long long item) {
-    Item t;
-    const long long row = (long long)a.H * a.tiles;
-    t.id = item / row;
-    const int rest = (int)(item - t.id * row);
-    t.h = rest / a.tiles;
-    int tile = rest - t.h * a.tiles;
-    t.pass = 0;
-    while (t.pass + 1 < a.npass && tile >= a.pass[t.pass].tiles) tile -= a.pass[t.pass++].tiles;
-    t.p = &a.pass[t.pass];
-    t.v0 = tile * kV;
-    t.g = segment(a, t.id);
-    t.chunks = t.g.there ? (t.g.len + kQ - 1) / kQ : 0;
-    return t;
+__device__ __noinline__ void take(const WalkArgs& a, int item, Item* t) {
+    const int row = a.H * a.tiles;
+    const int id = item / row, rest = item - id * row;
+    t->id = id;
+    t->h = rest / a.tiles;
+    int tile = rest - t->h * a.tiles;
+    t->pass = 0;
+    while (t->pass + 1 < a.npass && tile >= a.pass[t->pass].tiles) tile -= a.pass[t->pass++].tiles;
+    t->p = &a.pass[t->pass];
+    t->v0 = tile * kV;
+    t->g = segment(a, t->id);
+    t->chunks = t->g.there ? (t->g.len + kQ - 1) / kQ : 0;
+    t->ld = a.ld[t->h];
 }
+__device__ __noinline__ Decay decay_of(float ld, int n) { return Decay(ld, n); }
 // First token and tokens of the walk's c-th chunk: chunks lie from the segment's start on, so that a walk
 // from the end begins with the short one.
 __device__ __forceinline__ long long chunk_start(const Item& t, int c, int* n) {
@@ -182,70 +195,94 @@ __device__ __forceinline__ long long chunk_start(const Item& t, int c, int* n) {
     return t.g.start + at;
 }
 
-__device__ __forceinline__ void load_chunk(const Maps& maps, const Item& t, long long t0, unsigned char* st,
-                                           int kbytes, uint64_t* bar, bool with_q) {
-    const Pass& p = *t.p;
-    const int kb = p.kd / 64;
-    mbar_expect_tx(bar, (uint32_t)(((with_q ? 2 : 1) * kb + 1) * kSub));
-    for (int b = 0; b < kb; ++b) {
-        if (with_q) tma_load_3d(st + b * kSub, &maps.m[t.pass][0], bar, b * 64, t.h / p.qr, (int)t0);
-        tma_load_3d(st + (with_q ? kbytes : 0) + b * kSub, &maps.m[t.pass][1], bar, b * 64, t.h / p.kr, (int)t0);
+// One chunk's tiles; a thread that issues copies keeps an item's maps and heads at hand.
+struct Tiles {
+    const CUtensorMap *q, *k, *v;
+    int hq, hk, hv, v0, kb;
+    __device__ __forceinline__ Tiles(const Maps& maps, const Item& t)
+        : q(&maps.m[t.pass][0]), k(&maps.m[t.pass][1]), v(&maps.m[t.pass][2]), hq(t.h / t.p->qr),
+          hk(t.h / t.p->kr), hv(t.h / t.p->vr), v0(t.v0), kb(t.p->kd / 64) {}
+    template <bool WITH_Q>
+    __device__ __forceinline__ void load(int t0, unsigned char* st, int kbytes, uint64_t* bar) const {
+        mbar_expect_tx(bar, (uint32_t)(((WITH_Q ? 2 : 1) * kb + 1) * kSub));
+        tma_load_3d(st + (WITH_Q ? 2 : 1) * kbytes, v, bar, v0, hv, t0);
+#pragma unroll 1
+        for (int b = 0; b < kb; ++b, st += kSub) {
+            tma_load_3d(st + (WITH_Q ? kbytes : 0), k, bar, b * 64, hk, t0);
+            if (WITH_Q) tma_load_3d(st, q, bar, b * 64, hq, t0);
+        }
     }
-    tma_load_3d(st + (with_q ? 2 : 1) * kbytes, &maps.m[t.pass][2], bar, t.v0, t.h / p.vr, (int)t0);
+};
+
+// `words` (32 or 64) of a row in stores of 32 bytes, which fill whole sectors, or of 16.
+__device__ __forceinline__ void store_row(char* row, const uint32_t* w, int words, bool wide) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+        if (i < words) {
+            if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + 4 * i), "r"(w[i]),
+                             "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                             "r"(w[i + 7])
+                             : "memory");
+            } else {
+                reinterpret_cast<uint4*>(row)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                reinterpret_cast<uint4*>(row)[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+            }
+        }
 }
 
 // ---------------------------------------------------------------- the walk
 constexpr uint32_t kColScores = 0, kColMasked = 128, kColO1 = 192, kColO2 = 256, kColU = 320;  // 512 columns
 
-// A warp's columns below (or above) the diagonal, 16 at a time, masked by the powers and packed.
-__device__ __forceinline__ void mask16(const uint32_t* s, const float* f, uint32_t* out) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        out[i] = pack_bf16(__uint_as_float(s[2 * i]) * f[2 * i], __uint_as_float(s[2 * i + 1]) * f[2 * i + 1]);
-}
-
-// The state's task for one item: NP of the tile's 64 columns a thread, of row n of S.
-template <int NT, int NP>
+// The state's task for one item: row n of S, all of the tile's columns, a thread (64 channels leave
+// the upper two warps with nothing but their arrivals).
+template <int NT>
 __device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux* x, unsigned char* s_tile,
-                                           uint32_t lane_base, int tid, int& g, int* status) {
+                                           uint32_t u_cols, int n, int& g, int* status) {
     const Pass& p = *t.p;
-    const int n = NP == 64 ? tid : tid & 63, p0 = NP == 64 ? 0 : (tid >> 6) * 32;
-    const long long seq = ((long long)t.g.seq * a.H + t.h) * p.kd * p.vd;
-    const float* in = p.s_seg ? p.s_seg + (t.id * a.H + t.h) * (long long)p.kd * p.vd : p.s_in ? p.s_in + seq : nullptr;
-    float S[NP];
+    const bool mine = n < p.kd;  // the same for a whole warp
+    const long long size = (long long)p.kd * p.vd, from = (long long)t.v0 * p.sp + n * p.sn;
+    const long long seq = ((long long)t.g.seq * a.H + t.h) * size;
+    float S[kV];
+    {
+        const float* in = p.s_seg ? p.s_seg + (t.id * a.H + t.h) * size : p.s_in ? p.s_in + seq : nullptr;
+        const bool some = in && mine;
+        in += from;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) S[i] = in ? in[n * p.sn + (t.v0 + p0 + i) * p.sp] : 0.f;
-    const float ld = a.ld[t.h];
-    const Decay whole(ld, kQ);
+        for (int i = 0; i < kV; ++i) S[i] = some ? in[i * p.sp] : 0.f;
+    }
+    const Decay whole = decay_of(t.ld, kQ), part = decay_of(t.ld, (t.g.len - 1) % kQ + 1);
+    const int short_one = p.reverse ? 0 : t.chunks - 1;
+#pragma unroll 1
     for (int c = 0; c < t.chunks; ++c, ++g) {
-        int len;
-        chunk_start(t, c, &len);
         // the last chunk's q S has read the tile
         if (g > 0 && !wait_warp(&x->outs, (g - 1) & 1, &x->stop, status)) return false;
+        if (mine)
 #pragma unroll
-        for (int i = 0; i < NP; i += 8)
-            *reinterpret_cast<uint4*>(s_tile + n * 128 + ((((p0 + i) >> 3) ^ (n & 7)) << 4)) =
-                make_uint4(pack_bf16(S[i], S[i + 1]), pack_bf16(S[i + 2], S[i + 3]), pack_bf16(S[i + 4], S[i + 5]),
-                           pack_bf16(S[i + 6], S[i + 7]));
+            for (int i = 0; i < kV; i += 8)
+                *reinterpret_cast<uint4*>(s_tile + n * 128 + (((i >> 3) ^ (n & 7)) << 4)) =
+                    make_uint4(pack_bf16(S[i], S[i + 1]), pack_bf16(S[i + 2], S[i + 3]),
+                               pack_bf16(S[i + 4], S[i + 5]), pack_bf16(S[i + 6], S[i + 7]));
         fence_proxy_async();
         mbar_arrive(&x->state);
-        const Decay decay = len == kQ ? whole : Decay(ld, len);
+        const float m = c == short_one ? part.m : whole.m, keep = c == short_one ? part.keep : whole.keep;
         if (!wait_warp(&x->sums, g & 1, &x->stop, status)) return false;
         tc_fence_after();
+        if (mine)
 #pragma unroll
-        for (int i = 0; i < NP; i += 16) {
-            float u[16];
-            load_sum16<NT>(x->tmem + lane_base + kColU + p0 + i, u);
+            for (int i = 0; i < kV; i += 16) {
+                float u[16];
+                load_sum16<NT>(u_cols + i, u);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) S[i + e] = decay(S[i + e]) + u[e];
-        }
+                for (int e = 0; e < 16; ++e) S[i + e] = fmaf(m, S[i + e], keep * S[i + e]) + u[e];
+            }
         tc_fence_before();
         mbar_arrive(&x->sums_free);
     }
-    if (t.g.there && p.s_out && t.g.k == (p.reverse ? 0 : t.g.cnt - 1)) {
-        float* out = p.s_out + seq;
+    if (mine && p.s_out && t.g.k == (p.reverse ? 0 : t.g.cnt - 1)) {
+        float* out = p.s_out + seq + from;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) out[n * p.sn + (t.v0 + p0 + i) * p.sp] = S[i];
+        for (int i = 0; i < kV; ++i) out[i * p.sp] = S[i];
     }
     return true;
 }
@@ -253,8 +290,7 @@ __device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux
 template <int NT>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_walk_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
-    extern __shared__ unsigned char raw[];
-    unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) unsigned char sm[];
     Aux* x = reinterpret_cast<Aux*>(sm + geo.aux_at);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tid = threadIdx.x & 127;                            // within a task's four warps
@@ -280,8 +316,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         // ------------------------------------------------ scores: the masked operand, and the outputs
         const uint32_t mine = tmem + lane_base;
         const int i = tid, w0 = 32 * warp;
-        for (long long item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            const Item t = take(a, item);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, item, &t);
             const Pass& p = *t.p;
             const bool rev = p.reverse;
             char* out = static_cast<char*>(p.out);
@@ -293,10 +330,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                         *reinterpret_cast<uint4*>(out + (r * p.os + col) * oe + i * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             if (t.chunks == 0) continue;
-            const float ld2 = a.ld[t.h] * 1.44269504f;
+            const float ld2 = t.ld * 1.44269504f;
             float* pw = x->pw[warp];
             __syncwarp();  // the last item's are no longer read
-            pw[lane] = power(ld2, lane);
+            for (int d = lane; d < kQ; d += 32) pw[d] = power(ld2, d);
             __syncwarp();
             float far[16];  // a block's factors by column, beside the row's
 #pragma unroll
@@ -309,34 +346,33 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 if (!wait_warp(&x->scores, g & 1, &x->stop, status)) goto done;
                 tc_fence_after();
                 // the operand's last reader, the product before, has finished: its outputs were read
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < kQ / 16; ++b) {
                     const int j0 = 16 * b;
                     uint32_t o[8];
-                    const bool none = rev ? j0 + 15 < w0 : j0 > w0 + 31;
-                    const bool all = n == kQ && (rev ? j0 >= w0 + 31 : j0 + 15 <= w0);
-                    if (none) {
+                    if (rev ? j0 + 15 < w0 : j0 > w0 + 31) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] = 0u;
                     } else {
                         uint32_t s[16];
                         tmem_ld16(mine + kColScores + j0, s);
                         tmem_wait_ld_regs<16>(s);
-                        float f[16];
-                        if (all) {
-                            const float r = power(ld2, rev ? j0 - i : i - j0 - 15);
+                        if (n == kQ && (rev ? j0 >= w0 + 31 : j0 + 15 <= w0)) {
+                            const float r = pw[rev ? j0 - i : i - j0 - 15];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) f[e] = r * far[e];
-                            mask16(s, f, o);
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = pack_bf16(__uint_as_float(s[2 * e]) * (r * far[2 * e]),
+                                                 __uint_as_float(s[2 * e + 1]) * (r * far[2 * e + 1]));
                         } else {
+                            // what is masked may be an infinity or a NaN, and is left out, not multiplied
+                            float f[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const int d = rev ? j0 + e - i : i - j0 - e;
-                                const bool in = d >= 0 && j0 + e < n;
-                                f[e] = !in ? 0.f : d < 32 ? pw[d] : power(ld2, d);
-                                if (!in) s[e] = 0u;  // an infinity or a NaN there must not count
+                                f[e] = d >= 0 && j0 + e < n ? __uint_as_float(s[e]) * pw[d & (kQ - 1)] : 0.f;
                             }
-                            mask16(s, f, o);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
                         }
                     }
                     tmem_st8(mine + kColMasked + 8 * b, o);
@@ -346,8 +382,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mbar_arrive(&x->masked);
                 if (!wait_warp(&x->outs, g & 1, &x->stop, status)) goto done;
                 tc_fence_after();
-                const float fx = n == kQ || !rev ? fx_whole : power(ld2, max(n - 1 - i, 0)) * p.sx;
+                const float fx = n == kQ || !rev ? fx_whole : pw[max(n - 1 - i, 0)] * p.sx;
                 char* row = out + ((t0 + i) * p.os + col) * oe;
+                // both halves are read before the columns are given back, added and stored after
                 uint32_t o1[kV], o2[kV];
 #pragma unroll
                 for (int e = 0; e < kV; e += 16) {
@@ -363,34 +400,30 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 for (int e = 0; e < kV; ++e)
                     o1[e] = __float_as_uint(fmaf(fx, __uint_as_float(o2[e]), fi * __uint_as_float(o1[e])));
                 if (i < n) {
-                    if (p.out_f32) {
+                    if (!p.out_f32) {
 #pragma unroll
-                        for (int e = 0; e < kV; e += 4)
-                            *reinterpret_cast<uint4*>(row + 4 * e) = make_uint4(o1[e], o1[e + 1], o1[e + 2], o1[e + 3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kV; e += 16) tcc::store_bf16x16(row + 2 * e, o1 + e, 1.f, wide);
+                        for (int e = 0; e < kV / 2; ++e)
+                            o1[e] = pack_bf16(__uint_as_float(o1[2 * e]), __uint_as_float(o1[2 * e + 1]));
                     }
+                    store_row(row, o1, p.out_f32 ? kV : kV / 2, wide);
                 }
             }
         }
     } else if (warp < 8) {
         // ------------------------------------------------ state
-        for (long long item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            const Item t = take(a, item);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, item, &t);
             if (!t.g.there) continue;
-            unsigned char* s_tile = sm + geo.s_at;
-            const bool ok = t.p->kd == 128
-                                ? state_item<NT, 64>(a, t, x, s_tile, lane_base, tid, g, status)
-                                : state_item<NT, 32>(a, t, x, s_tile, lane_base, tid, g, status);
-            if (!ok) goto done;
+            if (!state_item<NT>(a, t, x, sm + geo.s_at, tmem + lane_base + kColU, tid, g, status)) goto done;
         }
     } else if (warp < 12) {
         // ------------------------------------------------ weights
-        for (long long item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            const Item t = take(a, item);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, item, &t);
             const Pass& p = *t.p;
-            const float ld2 = a.ld[t.h] * 1.44269504f;
+            const float ld2 = t.ld * 1.44269504f;
             const float whole = power(ld2, p.reverse ? tid + 1 : kQ - 1 - tid) * p.su;
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 int n;
@@ -414,30 +447,34 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else if (warp == 12) {
         // ------------------------------------------------ copies in
         if (lane == 0) {
-            for (long long item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
-                const Item t = take(a, item);
+            for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
+                Item t;
+                take(a, item, &t);
+                const Tiles tiles(maps, t);
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     int n;
                     const long long t0 = chunk_start(t, c, &n);
                     const int s = g % geo.stages;
                     if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    load_chunk(maps, t, t0, sm + s * geo.stage_bytes, kbytes, &x->full[s], true);
+                    tiles.load<true>((int)t0, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
                 }
             }
             // after a wait that ran out: copies on their way must not land in the next block's memory
             if (*(volatile int*)&x->stop)
                 for (int k = max(0, g - geo.stages); k < g; ++k)
-                    mbar_wait(&x->full[k % geo.stages], (k / geo.stages) & 1);
+                    drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
         }
         __syncwarp();
     } else if (warp == 13) {
         // ------------------------------------------------ products
         if (lane == 0) {
             const uint32_t id_a = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kV, 0, 1);
-            const uint32_t s_tile = smem_u32(sm + geo.s_at), w_tile = smem_u32(sm + geo.w_at);
+            const uint32_t w_tile = smem_u32(sm + geo.w_at);
+            const uint64_t s_desc = sw128_desc(smem_u32(sm + geo.s_at), 16, 1024);
             bool stop = false;
-            for (long long item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                const Item t = take(a, item);
+            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
+                Item t;
+                take(a, item, &t);
                 const int kb = t.p->kd / 64;
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     const int s = g % geo.stages;
@@ -445,11 +482,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     stop = !wait(&x->full[s], (g / geo.stages) & 1, &x->stop, status);
                     if (stop) break;
                     // the scores before were read before their product, which is behind this one
-                    for (int i = 0; i < 4 * kb; ++i) {
-                        const uint32_t at = (i >> 2) * kSub + (i & 3) * 32;
-                        mma_bf16(tmem + kColScores, sw128_desc(q + at, 16, 1024), sw128_desc(k + at, 16, 1024), id_a,
-                                 i > 0);
-                    }
+                    const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(k, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < 4 * kb)
+                            mma_bf16(tmem + kColScores, moved(qd, (i >> 2) * kSub + (i & 3) * 32),
+                                     moved(kd, (i >> 2) * kSub + (i & 3) * 32), id_a, i > 0);
                     mma_commit(&x->scores);
                     stop = !wait(&x->weights, g & 1, &x->stop, status) ||
                            (g > 0 && !wait(&x->sums_free, (g - 1) & 1, &x->stop, status));
@@ -462,16 +500,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                            (g > 0 && !wait(&x->outs_free, (g - 1) & 1, &x->stop, status));
                     if (stop) break;
                     tc_fence_after();
-                    for (int i = 0; i < 4 * kb; ++i)
-                        mma_bf16(tmem + kColO2, sw128_desc(q + (i >> 2) * kSub + (i & 3) * 32, 16, 1024),
-                                 sw128_desc(s_tile + i * 2048, 16, 1024), id_o, i > 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < 4 * kb)
+                            mma_bf16(tmem + kColO2, moved(qd, (i >> 2) * kSub + (i & 3) * 32),
+                                     moved(s_desc, i * 2048), id_o, i > 0);
                     stop = !wait(&x->masked, g & 1, &x->stop, status);
                     if (stop) break;
                     tc_fence_after();
+                    const uint64_t vd = sw128_desc(v, 16, 1024);
 #pragma unroll
                     for (int i = 0; i < kQ / 16; ++i)
-                        mma_bf16_ta(tmem + kColO1, tmem + kColMasked + 8 * i, sw128_desc(v + i * 2048, 16, 1024), id_o,
-                                    i > 0);
+                        mma_bf16_ta(tmem + kColO1, tmem + kColMasked + 8 * i, moved(vd, i * 2048), id_o, i > 0);
                     mma_commit(&x->outs);
                     mma_commit(&x->empty[s]);
                 }
@@ -479,7 +519,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (stop) {  // what was issued must end before the columns are given back
                 uint64_t* bar = &x->weights_free;
                 mma_commit(bar);
-                for (int k = 0; k < 2; ++k) mbar_wait(bar, k, kLimitNs / 4);
+                for (int k = 0; k < 2; ++k) drain(bar, k);
             }
         }
         __syncwarp();
@@ -499,8 +539,7 @@ done:
 template <int NT>
 __global__ void __launch_bounds__(kSumThreads, 1)
     tc_sums_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
-    extern __shared__ unsigned char raw[];
-    unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) unsigned char sm[];
     Aux* x = reinterpret_cast<Aux*>(sm + geo.aux_at);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -523,11 +562,12 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     };
     // two sets of weights: one chunk's are made while the other's are read
     if (warp < 4) {
-        for (long long item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            const Item t = take(a, item);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, item, &t);
             if (!wanted(t)) continue;
             const Pass& p = *t.p;
-            const float ld2 = a.ld[t.h] * 1.44269504f;
+            const float ld2 = t.ld * 1.44269504f;
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 const int s = g % geo.stages, at = c * kQ + tid;
                 unsigned char* st = sm + s * geo.stage_bytes;
@@ -545,14 +585,15 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             }
             if (!wait_warp(&x->sums, m & 1, &x->stop, status)) goto done;
             tc_fence_after();
-            const int n = p.kd == 128 ? tid : tid & 63, p0 = p.kd == 128 ? 0 : (tid >> 6) * 32;
-            const int np = p.kd == 128 ? 64 : 32;
-            float* out = p.s_sum + (t.id * a.H + t.h) * (long long)p.kd * p.vd;
-            for (int i = 0; i < np; i += 16) {
-                float u[16];
-                load_sum16<NT>(tmem + lane_base + p0 + i, u);
+            if (tid < p.kd) {
+                float* out = p.s_sum + (t.id * a.H + t.h) * (long long)p.kd * p.vd + tid * p.sn + t.v0 * p.sp;
+#pragma unroll 1
+                for (int i = 0; i < kV; i += 16) {
+                    float u[16];
+                    load_sum16<NT>(tmem + lane_base + i, u);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) out[n * p.sn + (t.v0 + p0 + i + e) * p.sp] = u[e];
+                    for (int e = 0; e < 16; ++e) out[(i + e) * p.sp] = u[e];
+                }
             }
             tc_fence_before();
             mbar_arrive(&x->sums_free);
@@ -560,25 +601,28 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         }
     } else if (warp == 4) {
         if (lane == 0) {
-            for (long long item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
-                const Item t = take(a, item);
+            for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
+                Item t;
+                take(a, item, &t);
                 if (!wanted(t)) continue;
+                const Tiles tiles(maps, t);
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     const int s = g % geo.stages;
                     if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    load_chunk(maps, t, t.g.start + c * kQ, sm + s * geo.stage_bytes, kbytes, &x->full[s], false);
+                    tiles.load<false>((int)t.g.start + c * kQ, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
                 }
             }
             if (*(volatile int*)&x->stop)
                 for (int k = max(0, g - geo.stages); k < g; ++k)
-                    mbar_wait(&x->full[k % geo.stages], (k / geo.stages) & 1);
+                    drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
         }
         __syncwarp();
     } else {
         if (lane == 0) {
             bool stop = false;
-            for (long long item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                const Item t = take(a, item);
+            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
+                Item t;
+                take(a, item, &t);
                 if (!wanted(t)) continue;
                 if (m > 0 && !wait(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
                 tc_fence_after();
@@ -597,7 +641,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             }
             if (*(volatile int*)&x->stop) {
                 mma_commit(&x->sums);
-                for (int k = 0; k < 2; ++k) mbar_wait(&x->sums, k, kLimitNs / 4);
+                for (int k = 0; k < 2; ++k) drain(&x->sums, k);
             }
         }
         __syncwarp();
@@ -675,14 +719,14 @@ cudaError_t tc_walk(const WalkArgs& a, Launch& L) {
     const bool three = exact_states(a);
     Geometry geo;
     geo.kblocks = kblocks_of(a);
-    geo.items = a.ids * a.H * a.tiles;
+    geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
     geo.stage_bytes = (2 * geo.kblocks + 1) * kSub;
-    const int rest = (three ? 3 : 2) * kSub + geo.kblocks * 64 * 128 + (int)sizeof(Aux) + 1024;
+    const int rest = (three ? 3 : 2) * kSub + geo.kblocks * 64 * 128 + (int)sizeof(Aux);
     geo.stages = std::min(3, (kMostSmem - rest) / geo.stage_bytes);
     geo.w_at = geo.stages * geo.stage_bytes;
     geo.s_at = geo.w_at + (three ? 3 : 2) * kSub;
     geo.aux_at = geo.s_at + geo.kblocks * 64 * 128;
-    const size_t smem = (size_t)geo.aux_at + sizeof(Aux) + 1024;
+    const size_t smem = (size_t)geo.aux_at + sizeof(Aux);
     L.begin("linattn_tc_walk");
     const cudaError_t e = three ? launch(tc_walk_kernel<3>, a, m, geo, kWalkThreads, smem, L.stream)
                                 : launch(tc_walk_kernel<2>, a, m, geo, kWalkThreads, smem, L.stream);
@@ -696,13 +740,13 @@ cudaError_t tc_sums(const WalkArgs& a, Launch& L) {
     const bool three = exact_states(a);
     Geometry geo;
     geo.kblocks = kblocks_of(a);
-    geo.items = a.ids * a.H * a.tiles;
+    geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
     geo.stage_bytes = (geo.kblocks + 1) * kSub;
     const int w = 2 * (three ? 3 : 2) * kSub;
-    geo.stages = std::min(kMostStages, (kMostSmem - w - (int)sizeof(Aux) - 1024) / geo.stage_bytes);
+    geo.stages = std::min(kMostStages, (kMostSmem - w - (int)sizeof(Aux)) / geo.stage_bytes);
     geo.w_at = geo.stages * geo.stage_bytes;
     geo.s_at = geo.aux_at = geo.w_at + w;
-    const size_t smem = (size_t)geo.aux_at + sizeof(Aux) + 1024;
+    const size_t smem = (size_t)geo.aux_at + sizeof(Aux);
     L.begin("linattn_tc_sums");
     const cudaError_t e = three ? launch(tc_sums_kernel<3>, a, m, geo, kSumThreads, smem, L.stream)
                                 : launch(tc_sums_kernel<2>, a, m, geo, kSumThreads, smem, L.stream);
