@@ -311,7 +311,7 @@ Plan make_plan(const ssd_linattn_t& p, bool bwd) {
                                 : (p.headdim + kTcTile - 1) / kTcTile;
     const long long per_cut = (long long)p.nheads * tiles;  // items for each run of tokens
     const long long sms = sm_count();
-    const bool dense_full = !p.nseq && l.n * per_cut >= 4 * sms;
+    const bool dense_full = !p.nseq && l.n * per_cut >= 2 * sms;
     if (p.seqlen > 512 && !dense_full) {
         long long want = (8 * sms + per_cut - 1) / per_cut;  // cuts of all tokens
         long long Ls = (l.T / want + 127) / 128 * 128;

@@ -15,12 +15,16 @@
 // another and are added in float32.  A power a^(i-j) is never split into a^i a^-j over more than 16
 // tokens below the diagonal, so that nothing overflows.
 //
-// One block an SM with warps for each task: scores (A to the masked operand, and the outputs), state
-// (U into S), weights (v to W), one for the copies in (TMA, two or three chunks ahead), one for the
-// products.  Blocks stay and take items in turn; the tiles of all passes of one segment and head are
-// next to one another, so that what they all read comes from L2 after the first.
+// One block an SM, four warps for each of four tasks: mask (A to the masked operand), outputs,
+// state (U into S) and weights (v to W); one warp for the copies in (TMA, two or three chunks ahead);
+// two that issue products, A and O1 in one, U and O2 in the other, so that the chunk's two chains
+// (scores, mask, outputs; weights, sums, state) wait for each other only at the outputs.  Blocks
+// stay and take items in turn, or, where items are long and of unequal cost, there is a block for
+// each item, the dearest first.  The tiles of all passes of one segment and head are next to one
+// another, so that what they all read comes from L2 after the first.
 #include <algorithm>
 
+#include "layer_device.cuh"
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
@@ -35,7 +39,7 @@ using tcc::pack_bf16;
 constexpr int kQ = kTcChunk;                 // 128 tokens
 constexpr int kV = kTcTile;                  // 64 columns
 constexpr int kSub = kQ * 128;               // bytes of a tile of 64 channels: rows of 128 bytes
-constexpr int kWalkThreads = 14 * 32;
+constexpr int kWalkThreads = 19 * 32;
 constexpr int kSumThreads = 6 * 32;
 constexpr int kMostStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;
@@ -46,16 +50,16 @@ struct Maps {
 struct Geometry {
     int stages, kblocks;    // chunks in shared memory at a time; most blocks of 64 channels of q and k
     int stage_bytes, w_at, s_at, aux_at;
-    int items;
+    int items, by_pass;
 };
 
 // Barriers and what else is small, behind the tiles.
 struct Aux {
-    uint64_t full[kMostStages], empty[kMostStages], made[2];
-    uint64_t scores, masked, weights, weights_free, state, outs, outs_free, sums, sums_free;
+    uint64_t full[kMostStages], empty[kMostStages], empty_v[kMostStages], weights[kMostStages], made[2];
+    uint64_t scores[2], masked[2], masked_free, state, state_free, outs, outs_free, sums, sums_free;
     uint32_t tmem;
     int stop;
-    float pw[4][kQ];  // a^0 .. a^127, a copy for each of the scores' warps
+    float diag[4][64];  // a copy for each of the mask's warps: 0 (31 times), a^0 .. a^31
 };
 
 // Waits for a phase, at most kLimitNs: one that runs out records SSD_ERR_TIMEOUT and ends every wait
@@ -101,6 +105,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// 32 lanes x 8 columns: tmem_ld16 of half the width.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void reg_dep8(uint32_t* r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+using layer::F2;
+__device__ __forceinline__ F2 pair(uint32_t a, uint32_t b) { return layer::join(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint32_t pack(F2 v) {
+    float f[2];
+    layer::split(v, f);
+    return pack_bf16(f[0], f[1]);
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -109,19 +131,21 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 template <int NT>
 __device__ __forceinline__ void split_row(const unsigned char* v, unsigned char* w_out, int row, float w, bool in) {
     const uint32_t base = row * 128, x = row & 7;
-#pragma unroll 1
+    const F2 ww = layer::both<F2>(w);
+#pragma unroll 2
     for (int c = 0; c < 8; ++c) {
         const uint32_t at = base + ((c ^ x) << 4);
-        const uint4 raw = *reinterpret_cast<const uint4*>(v + at);
+        uint4 raw = *reinterpret_cast<const uint4*>(v + at);
+        if (!in) raw = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
         uint32_t t[NT][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo = in ? bf_lo(words[i]) * w : 0.f, hi = in ? bf_hi(words[i]) * w : 0.f;
+            F2 f = layer::mul_(layer::join(bf_lo(words[i]), bf_hi(words[i])), ww);
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
-                t[k][i] = pack_bf16(lo, hi);
-                if (k + 1 < NT) lo -= bf_lo(t[k][i]), hi -= bf_hi(t[k][i]);
+                t[k][i] = pack(f);
+                if (k + 1 < NT) f = layer::sub_(f, layer::join(bf_lo(t[k][i]), bf_hi(t[k][i])));
             }
         }
 #pragma unroll
@@ -134,21 +158,20 @@ __device__ __forceinline__ void zero_row(unsigned char* tile, int row) {
     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Adds the NT terms of columns [col, col + 16) of U, kV columns apart, of this thread's lane.
+// Adds the NT terms of columns [col, col + 8) of U, kV columns apart, of this thread's lane.
 template <int NT>
-__device__ __forceinline__ void load_sum16(uint32_t taddr, float* f) {
-    uint32_t r[NT][16];
+__device__ __forceinline__ void load_sum8(uint32_t taddr, F2* f) {
+    uint32_t r[NT][8];
 #pragma unroll
-    for (int k = 0; k < NT; ++k) tmem_ld16(taddr + k * kV, r[k]);
+    for (int k = 0; k < NT; ++k) tmem_ld8(taddr + k * kV, r[k]);
     tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < NT; ++k) reg_dep16(r[k]);
+    for (int k = 0; k < NT; ++k) reg_dep8(r[k]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = __uint_as_float(r[NT - 1][i]);  // the small terms first
+    for (int i = 0; i < 4; ++i) {
+        f[i] = pair(r[NT - 1][2 * i], r[NT - 1][2 * i + 1]);  // the small terms first
 #pragma unroll
-        for (int k = NT - 2; k >= 0; --k) s += __uint_as_float(r[k][i]);
-        f[i] = s;
+        for (int k = NT - 2; k >= 0; --k) f[i] = layer::add_(f[i], pair(r[k][2 * i], r[k][2 * i + 1]));
     }
 }
 
@@ -203,36 +226,95 @@ struct Tiles {
         : q(&maps.m[t.pass][0]), k(&maps.m[t.pass][1]), v(&maps.m[t.pass][2]), hq(t.h / t.p->qr),
           hk(t.h / t.p->kr), hv(t.h / t.p->vr), v0(t.v0), kb(t.p->kd / 64) {}
     template <bool WITH_Q>
-    __device__ __forceinline__ void load(int t0, unsigned char* st, int kbytes, uint64_t* bar) const {
+    __device__ __forceinline__ void load_qk(int t0, unsigned char* st, int kbytes, uint64_t* bar) const {
         mbar_expect_tx(bar, (uint32_t)(((WITH_Q ? 2 : 1) * kb + 1) * kSub));
-        tma_load_3d(st + (WITH_Q ? 2 : 1) * kbytes, v, bar, v0, hv, t0);
 #pragma unroll 1
         for (int b = 0; b < kb; ++b, st += kSub) {
             tma_load_3d(st + (WITH_Q ? kbytes : 0), k, bar, b * 64, hk, t0);
             if (WITH_Q) tma_load_3d(st, q, bar, b * 64, hq, t0);
         }
     }
+    __device__ __forceinline__ void load_v(int t0, unsigned char* at, uint64_t* bar) const {
+        tma_load_3d(at, v, bar, v0, hv, t0);
+    }
 };
 
-// `words` (32 or 64) of a row in stores of 32 bytes, which fill whole sectors, or of 16.
-__device__ __forceinline__ void store_row(char* row, const uint32_t* w, int words, bool wide) {
-#pragma unroll
-    for (int i = 0; i < 64; i += 8)
-        if (i < words) {
-            if (wide) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + 4 * i), "r"(w[i]),
-                             "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
-                             "r"(w[i + 7])
-                             : "memory");
-            } else {
-                reinterpret_cast<uint4*>(row)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                reinterpret_cast<uint4*>(row)[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
-            }
-        }
+// 8 words of a row in a store of 32 bytes, which fills a whole sector, or in two of 16.
+__device__ __forceinline__ void store8(char* at, const uint32_t* w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // ---------------------------------------------------------------- the walk
-constexpr uint32_t kColScores = 0, kColMasked = 128, kColO1 = 192, kColO2 = 256, kColU = 320;  // 512 columns
+// TMEM, 512 columns.  With two terms the scores have two places, and the masked operand goes over the
+// scores it came from; with three the scores have one, and the operand its own.
+template <int NT>
+struct Cols {
+    static constexpr int kPlaces = NT == 2 ? 2 : 1;
+    static constexpr uint32_t scores(int g) { return NT == 2 ? (g & 1) * 128 : 0; }
+    static constexpr uint32_t masked(int g) { return NT == 2 ? (g & 1) * 128 : 128; }
+    static constexpr uint32_t o1 = NT == 2 ? 256 : 192, o2 = o1 + kV, u = o2 + kV;
+    static_assert(u + NT * kV <= 512, "TMEM");
+    // the place and parity of chunk g's scores and masks
+    static constexpr int at(int g) { return kPlaces == 2 ? g & 1 : 0; }
+    static constexpr int parity(int g) { return kPlaces == 2 ? (g >> 1) & 1 : g & 1; }
+};
+
+// The mask's task for one chunk: 32 scores of a row at a time.  Those far from the diagonal take the
+// row's power at the group's nearer end times the column's from there, so that no power is of a
+// negative distance; those at it a table of the powers with zeros beyond it.
+template <int NT>
+__device__ __forceinline__ void mask_chunk(uint32_t lanes, int g, int n, bool rev, int warp, int lane, float ld2,
+                                           const float* diag, const F2* far) {
+    const int i = 32 * warp + lane;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const int j0 = 32 * q;
+        uint32_t o[16];
+        if (rev ? q < warp : q > warp) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+        } else {
+            uint32_t s[32];
+            tmem_ld16(lanes + Cols<NT>::scores(g) + j0, *reinterpret_cast<uint32_t(*)[16]>(s));
+            tmem_ld16(lanes + Cols<NT>::scores(g) + j0 + 16, *reinterpret_cast<uint32_t(*)[16]>(s + 16));
+            tmem_wait_ld_regs<32>(s);
+            if (j0 + 32 > n) {  // tokens of other sequences, an infinity or a NaN maybe
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (j0 + e >= n) s[e] = 0u;
+            }
+            if (q == warp) {
+                const float* f = rev ? diag + 31 - lane : diag + 31 + lane;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const F2 w = rev ? layer::join(f[2 * e], f[2 * e + 1]) : layer::join(f[-2 * e], f[-2 * e - 1]);
+                    o[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), w));
+                }
+            } else {
+                // forwards the power to the half's last column, from the end to its first
+                const int d = rev ? j0 - i : i - j0 - 15, step = rev ? 16 : -16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const F2 r = layer::both<F2>(power(ld2, d + h * step));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[8 * h + e] =
+                            pack(layer::mul_(pair(s[16 * h + 2 * e], s[16 * h + 2 * e + 1]), layer::mul_(r, far[e])));
+                }
+            }
+        }
+        tmem_st8(lanes + Cols<NT>::masked(g) + j0 / 2, o);
+        tmem_st8(lanes + Cols<NT>::masked(g) + j0 / 2 + 8, o + 8);
+    }
+    tmem_wait_st();
+}
 
 // The state's task for one item: row n of S, all of the tile's columns, a thread (64 channels leave
 // the upper two warps with nothing but their arrivals).
@@ -243,38 +325,42 @@ __device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux
     const bool mine = n < p.kd;  // the same for a whole warp
     const long long size = (long long)p.kd * p.vd, from = (long long)t.v0 * p.sp + n * p.sn;
     const long long seq = ((long long)t.g.seq * a.H + t.h) * size;
-    float S[kV];
+    F2 S[kV / 2];
     {
         const float* in = p.s_seg ? p.s_seg + (t.id * a.H + t.h) * size : p.s_in ? p.s_in + seq : nullptr;
         const bool some = in && mine;
         in += from;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) S[i] = some ? in[i * p.sp] : 0.f;
+        for (int i = 0; i < kV / 2; ++i)
+            S[i] = some ? layer::join(in[2 * i * p.sp], in[(2 * i + 1) * p.sp]) : layer::join(0.f, 0.f);
     }
     const Decay whole = decay_of(t.ld, kQ), part = decay_of(t.ld, (t.g.len - 1) % kQ + 1);
     const int short_one = p.reverse ? 0 : t.chunks - 1;
 #pragma unroll 1
     for (int c = 0; c < t.chunks; ++c, ++g) {
         // the last chunk's q S has read the tile
-        if (g > 0 && !wait_warp(&x->outs, (g - 1) & 1, &x->stop, status)) return false;
+        if (g > 0 && !wait_warp(&x->state_free, (g - 1) & 1, &x->stop, status)) return false;
         if (mine)
 #pragma unroll
-            for (int i = 0; i < kV; i += 8)
-                *reinterpret_cast<uint4*>(s_tile + n * 128 + (((i >> 3) ^ (n & 7)) << 4)) =
-                    make_uint4(pack_bf16(S[i], S[i + 1]), pack_bf16(S[i + 2], S[i + 3]),
-                               pack_bf16(S[i + 4], S[i + 5]), pack_bf16(S[i + 6], S[i + 7]));
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(s_tile + n * 128 + ((i ^ (n & 7)) << 4)) =
+                    make_uint4(pack(S[4 * i]), pack(S[4 * i + 1]), pack(S[4 * i + 2]), pack(S[4 * i + 3]));
         fence_proxy_async();
         mbar_arrive(&x->state);
-        const float m = c == short_one ? part.m : whole.m, keep = c == short_one ? part.keep : whole.keep;
+        const Decay d = c == short_one ? part : whole;
+        const F2 m = layer::both<F2>(d.m);
         if (!wait_warp(&x->sums, g & 1, &x->stop, status)) return false;
         tc_fence_after();
         if (mine)
 #pragma unroll
-            for (int i = 0; i < kV; i += 16) {
-                float u[16];
-                load_sum16<NT>(u_cols + i, u);
+            for (int i = 0; i < 8; ++i) {
+                F2 u[4];
+                load_sum8<NT>(u_cols + 8 * i, u);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[i + e] = fmaf(m, S[i + e], keep * S[i + e]) + u[e];
+                for (int e = 0; e < 4; ++e) {
+                    if (d.keep != 0.f) u[e] = layer::add_(u[e], S[4 * i + e]);
+                    S[4 * i + e] = layer::fma_(m, S[4 * i + e], u[e]);
+                }
             }
         tc_fence_before();
         mbar_arrive(&x->sums_free);
@@ -282,14 +368,30 @@ __device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux
     if (mine && p.s_out && t.g.k == (p.reverse ? 0 : t.g.cnt - 1)) {
         float* out = p.s_out + seq + from;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) out[i * p.sp] = S[i];
+        for (int i = 0; i < kV / 2; ++i) {
+            float f[2];
+            layer::split(S[i], f);
+            out[2 * i * p.sp] = f[0], out[(2 * i + 1) * p.sp] = f[1];
+        }
     }
     return true;
+}
+
+// Where item `item` of a launch is in the order of `take`.
+__device__ __forceinline__ int ordered_item(const WalkArgs& a, const Geometry& geo, int item) {
+    if (!geo.by_pass) return item;
+    // pass by pass, the tiles of one next to one another
+    const int pairs = (int)a.ids * a.H;
+    int tile = 0, p = 0;
+    while (p + 1 < a.npass && item >= pairs * a.pass[p].tiles) item -= pairs * a.pass[p].tiles, tile += a.pass[p++].tiles;
+    const int w = a.pass[p].tiles;
+    return item / w * a.tiles + tile + item % w;
 }
 
 template <int NT>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_walk_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
+    using C = Cols<NT>;
     extern __shared__ __align__(1024) unsigned char sm[];
     Aux* x = reinterpret_cast<Aux*>(sm + geo.aux_at);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -298,31 +400,65 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const int kbytes = geo.kblocks * kSub;
     int* status = a.status;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < geo.stages; ++s) mbar_init(&x->full[s], 1), mbar_init(&x->empty[s], 1);
-        mbar_init(&x->scores, 1), mbar_init(&x->outs, 1), mbar_init(&x->sums, 1);
-        mbar_init(&x->weights_free, 1);
-        mbar_init(&x->masked, 128), mbar_init(&x->weights, 128), mbar_init(&x->state, 128);
-        mbar_init(&x->outs_free, 128), mbar_init(&x->sums_free, 128);
+        for (int s = 0; s < geo.stages; ++s) {
+            mbar_init(&x->full[s], 1), mbar_init(&x->weights[s], 128);
+            mbar_init(&x->empty[s], 2), mbar_init(&x->empty_v[s], 2);
+        }
+        for (int s = 0; s < 2; ++s) mbar_init(&x->scores[s], 1), mbar_init(&x->masked[s], 128);
+        mbar_init(&x->masked_free, 1), mbar_init(&x->state_free, 1), mbar_init(&x->sums, 1);
+        mbar_init(&x->outs, 2);
+        mbar_init(&x->state, 128), mbar_init(&x->outs_free, 128);
+        mbar_init(&x->sums_free, 128);
         x->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 13) tmem_alloc(&x->tmem, 512);
+    if (warp == 16) tmem_alloc(&x->tmem, 512);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = x->tmem;
     int g = 0;  // chunks of this block so far
 
     if (warp < 4) {
-        // ------------------------------------------------ scores: the masked operand, and the outputs
-        const uint32_t mine = tmem + lane_base;
-        const int i = tid, w0 = 32 * warp;
+        // ------------------------------------------------ mask
+        float* diag = x->diag[warp];
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, item, &t);
+            take(a, ordered_item(a, geo, item), &t);
+            const bool rev = t.p->reverse;
+            const float ld2 = t.ld * 1.44269504f;
+            __syncwarp();  // the last item's are no longer read
+            diag[lane] = 0.f;
+            __syncwarp();
+            diag[lane + 31] = power(ld2, lane);
+            __syncwarp();
+            F2 far[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                far[e] = rev ? layer::join(diag[31 + 2 * e], diag[32 + 2 * e]) : layer::join(diag[46 - 2 * e], diag[45 - 2 * e]);
+#pragma unroll 1
+            for (int c = 0; c < t.chunks; ++c, ++g) {
+                int n;
+                chunk_start(t, c, &n);
+                if (!wait_warp(&x->scores[C::at(g)], C::parity(g), &x->stop, status)) goto done;
+                // where the operand has one place: its last reader
+                if (C::kPlaces == 1 && g > 0 && !wait_warp(&x->masked_free, (g - 1) & 1, &x->stop, status)) goto done;
+                tc_fence_after();
+                mask_chunk<NT>(tmem + lane_base, g, n, rev, warp, lane, ld2, diag, far);
+                tc_fence_before();
+                mbar_arrive(&x->masked[C::at(g)]);
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------ outputs
+        const uint32_t mine = tmem + lane_base;
+        const int i = tid;
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, ordered_item(a, geo, item), &t);
             const Pass& p = *t.p;
-            const bool rev = p.reverse;
+            const bool rev = p.reverse, f32 = p.out_f32;
             char* out = static_cast<char*>(p.out);
-            const int oe = p.out_f32 ? 4 : 2;
+            const int oe = f32 ? 4 : 2;
             const long long col = (long long)(t.h / p.outr) * p.vd + t.v0;
             if (a.cu) {  // tokens behind the last sequence
                 for (long long r = border(a, a.nseq) + t.id; r < a.T; r += a.ids)
@@ -331,100 +467,72 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
             if (t.chunks == 0) continue;
             const float ld2 = t.ld * 1.44269504f;
-            float* pw = x->pw[warp];
-            __syncwarp();  // the last item's are no longer read
-            for (int d = lane; d < kQ; d += 32) pw[d] = power(ld2, d);
-            __syncwarp();
-            float far[16];  // a block's factors by column, beside the row's
-#pragma unroll
-            for (int e = 0; e < 16; ++e) far[e] = pw[rev ? e : 15 - e];
-            const float fi = p.si, fx_whole = power(ld2, rev ? kQ - 1 - i : i + 1) * p.sx;
+            const F2 fi = layer::both<F2>(p.si);
+            const float fx_whole = power(ld2, rev ? kQ - 1 - i : i + 1) * p.sx;
             const bool wide = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(p.os * oe)) & 31) == 0;
+#pragma unroll 1
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 int n;
                 const long long t0 = chunk_start(t, c, &n);
-                if (!wait_warp(&x->scores, g & 1, &x->stop, status)) goto done;
-                tc_fence_after();
-                // the operand's last reader, the product before, has finished: its outputs were read
-#pragma unroll 1
-                for (int b = 0; b < kQ / 16; ++b) {
-                    const int j0 = 16 * b;
-                    uint32_t o[8];
-                    if (rev ? j0 + 15 < w0 : j0 > w0 + 31) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = 0u;
-                    } else {
-                        uint32_t s[16];
-                        tmem_ld16(mine + kColScores + j0, s);
-                        tmem_wait_ld_regs<16>(s);
-                        if (n == kQ && (rev ? j0 >= w0 + 31 : j0 + 15 <= w0)) {
-                            const float r = pw[rev ? j0 - i : i - j0 - 15];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                o[e] = pack_bf16(__uint_as_float(s[2 * e]) * (r * far[2 * e]),
-                                                 __uint_as_float(s[2 * e + 1]) * (r * far[2 * e + 1]));
-                        } else {
-                            // what is masked may be an infinity or a NaN, and is left out, not multiplied
-                            float f[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int d = rev ? j0 + e - i : i - j0 - e;
-                                f[e] = d >= 0 && j0 + e < n ? __uint_as_float(s[e]) * pw[d & (kQ - 1)] : 0.f;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-                        }
-                    }
-                    tmem_st8(mine + kColMasked + 8 * b, o);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&x->masked);
+                const F2 fx = layer::both<F2>(n == kQ || !rev ? fx_whole : power(ld2, max(n - 1 - i, 0)) * p.sx);
+                char* row = out + ((t0 + i) * p.os + col) * oe;
                 if (!wait_warp(&x->outs, g & 1, &x->stop, status)) goto done;
                 tc_fence_after();
-                const float fx = n == kQ || !rev ? fx_whole : pw[max(n - 1 - i, 0)] * p.sx;
-                char* row = out + ((t0 + i) * p.os + col) * oe;
-                // both halves are read before the columns are given back, added and stored after
-                uint32_t o1[kV], o2[kV];
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h, row += 32 * oe) {
+                    uint32_t o1[32], o2[32];
 #pragma unroll
-                for (int e = 0; e < kV; e += 16) {
-                    tmem_ld16(mine + kColO1 + e, *reinterpret_cast<uint32_t(*)[16]>(o1 + e));
-                    tmem_ld16(mine + kColO2 + e, *reinterpret_cast<uint32_t(*)[16]>(o2 + e));
-                }
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < kV; e += 16) reg_dep16(o1 + e), reg_dep16(o2 + e);
-                tc_fence_before();
-                mbar_arrive(&x->outs_free);
-#pragma unroll
-                for (int e = 0; e < kV; ++e)
-                    o1[e] = __float_as_uint(fmaf(fx, __uint_as_float(o2[e]), fi * __uint_as_float(o1[e])));
-                if (i < n) {
-                    if (!p.out_f32) {
-#pragma unroll
-                        for (int e = 0; e < kV / 2; ++e)
-                            o1[e] = pack_bf16(__uint_as_float(o1[2 * e]), __uint_as_float(o1[2 * e + 1]));
+                    for (int e = 0; e < 32; e += 16) {
+                        tmem_ld16(mine + C::o1 + 32 * h + e, *reinterpret_cast<uint32_t(*)[16]>(o1 + e));
+                        tmem_ld16(mine + C::o2 + 32 * h + e, *reinterpret_cast<uint32_t(*)[16]>(o2 + e));
                     }
-                    store_row(row, o1, p.out_f32 ? kV : kV / 2, wide);
+                    tmem_wait_ld_regs<32>(o1);
+                    tmem_wait_ld_regs<32>(o2);
+                    if (h == 1) {
+                        tc_fence_before();
+                        mbar_arrive(&x->outs_free);
+                    }
+                    F2 v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = layer::fma_(fx, pair(o2[2 * e], o2[2 * e + 1]), layer::mul_(fi, pair(o1[2 * e], o1[2 * e + 1])));
+                    if (i < n) {
+                        if (f32) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float f[2];
+                                layer::split(v[e], f);
+                                o1[2 * e] = __float_as_uint(f[0]), o1[2 * e + 1] = __float_as_uint(f[1]);
+                            }
+                            store8(row + 64, o1 + 16, wide);
+                            store8(row + 96, o1 + 24, wide);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o1[e] = pack(v[e]);
+                        }
+                        store8(row, o1, wide);
+                        store8(row + 32, o1 + 8, wide);
+                    }
                 }
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ------------------------------------------------ state
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, item, &t);
+            take(a, ordered_item(a, geo, item), &t);
             if (!t.g.there) continue;
-            if (!state_item<NT>(a, t, x, sm + geo.s_at, tmem + lane_base + kColU, tid, g, status)) goto done;
+            if (!state_item<NT>(a, t, x, sm + geo.s_at, tmem + lane_base + C::u, tid, g, status)) goto done;
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------ weights
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, item, &t);
+            take(a, ordered_item(a, geo, item), &t);
             const Pass& p = *t.p;
             const float ld2 = t.ld * 1.44269504f;
             const float whole = power(ld2, p.reverse ? tid + 1 : kQ - 1 - tid) * p.su;
+#pragma unroll 1
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 int n;
                 chunk_start(t, c, &n);
@@ -432,31 +540,34 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 unsigned char* st = sm + s * geo.stage_bytes;
                 if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status)) goto done;
                 // the product before has read the last weights
-                if (g > 0 && !wait_warp(&x->weights_free, (g - 1) & 1, &x->stop, status)) goto done;
+                if (g > 0 && !wait_warp(&x->sums, (g - 1) & 1, &x->stop, status)) goto done;
                 const bool in = tid < n;
-                const float w = n == kQ || p.reverse ? whole : in ? power(ld2, n - 1 - tid) * p.su : 0.f;
+                const float w = n == kQ || p.reverse ? whole : power(ld2, max(n - 1 - tid, 0)) * p.su;
                 split_row<NT>(st + 2 * kbytes, sm + geo.w_at, tid, w, in);
                 if (!in) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
                     zero_row(st + 2 * kbytes, tid);
                     for (int b = 0; b < p.kd / 64; ++b) zero_row(st + kbytes + b * kSub, tid);
                 }
                 fence_proxy_async();
-                mbar_arrive(&x->weights);
+                mbar_arrive(&x->weights[s]);
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         // ------------------------------------------------ copies in
         if (lane == 0) {
             for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
                 Item t;
-                take(a, item, &t);
+                take(a, ordered_item(a, geo, item), &t);
                 const Tiles tiles(maps, t);
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     int n;
-                    const long long t0 = chunk_start(t, c, &n);
-                    const int s = g % geo.stages;
-                    if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    tiles.load<true>((int)t0, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
+                    const int t0 = (int)chunk_start(t, c, &n), s = g % geo.stages, ph = (g / geo.stages - 1) & 1;
+                    unsigned char* st = sm + s * geo.stage_bytes;
+                    if (g >= geo.stages && !wait(&x->empty[s], ph, &x->stop, status)) break;
+                    tiles.load_qk<true>(t0, st, kbytes, &x->full[s]);
+                    // the rest of the chunk is issued in any case: its barrier counts on it
+                    if (g >= geo.stages && !wait(&x->empty_v[s], ph, &x->stop, status)) drain(&x->empty_v[s], ph);
+                    tiles.load_v(t0, st + 2 * kbytes, &x->full[s]);
                 }
             }
             // after a wait that ran out: copies on their way must not land in the next block's memory
@@ -465,37 +576,81 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
         }
         __syncwarp();
-    } else if (warp == 13) {
-        // ------------------------------------------------ products
+    } else if (warp == 17) {
+        // ------------------------------------------------ products: scores, and the masked ones with v
         if (lane == 0) {
             const uint32_t id_a = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kV, 0, 1);
-            const uint32_t w_tile = smem_u32(sm + geo.w_at);
-            const uint64_t s_desc = sw128_desc(smem_u32(sm + geo.s_at), 16, 1024);
             bool stop = false;
+            // the masked product of chunk k, which waits for the next chunk's scores
+            const auto masked = [&](int k) {
+                const int s = k % geo.stages;
+                // with the weights v's rows behind the sequence's end are zero
+                if (!wait(&x->masked[C::at(k)], C::parity(k), &x->stop, status) ||
+                    !wait(&x->weights[s], (k / geo.stages) & 1, &x->stop, status) ||
+                    (k > 0 && !wait(&x->outs_free, (k - 1) & 1, &x->stop, status)))
+                    return false;
+                tc_fence_after();
+                const uint64_t vd = sw128_desc(smem_u32(sm + s * geo.stage_bytes) + 2 * kbytes, 16, 1024);
+#pragma unroll
+                for (int i = 0; i < kQ / 16; ++i)
+                    mma_bf16_ta(tmem + C::o1, tmem + C::masked(k) + 8 * i, moved(vd, i * 2048), id_o, i > 0);
+                mma_commit(&x->outs);
+                if (C::kPlaces == 1) mma_commit(&x->masked_free);
+                mma_commit(&x->empty_v[s]);
+                return true;
+            };
             for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
                 Item t;
-                take(a, item, &t);
+                take(a, ordered_item(a, geo, item), &t);
                 const int kb = t.p->kd / 64;
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     const int s = g % geo.stages;
-                    const uint32_t q = smem_u32(sm + s * geo.stage_bytes), k = q + kbytes, v = k + kbytes;
-                    stop = !wait(&x->full[s], (g / geo.stages) & 1, &x->stop, status);
+                    const uint32_t q = smem_u32(sm + s * geo.stage_bytes);
+                    const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(q + kbytes, 16, 1024);
+                    // with one place for the scores, those before have been read
+                    stop = !wait(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
+                           (C::kPlaces == 1 && g > 0 && !wait(&x->masked[0], (g - 1) & 1, &x->stop, status));
                     if (stop) break;
-                    // the scores before were read before their product, which is behind this one
-                    const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(k, 16, 1024);
+                    tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (i < 4 * kb)
-                            mma_bf16(tmem + kColScores, moved(qd, (i >> 2) * kSub + (i & 3) * 32),
+                            mma_bf16(tmem + C::scores(g), moved(qd, (i >> 2) * kSub + (i & 3) * 32),
                                      moved(kd, (i >> 2) * kSub + (i & 3) * 32), id_a, i > 0);
-                    mma_commit(&x->scores);
-                    stop = !wait(&x->weights, g & 1, &x->stop, status) ||
+                    mma_commit(&x->scores[C::at(g)]);
+                    mma_commit(&x->empty[s]);
+                    stop = g > 0 && !masked(g - 1);
+                    if (stop) break;
+                }
+            }
+            if (!stop && g > 0) stop = !masked(g - 1);
+            if (stop) {  // what was issued must end before the columns are given back
+                mma_commit(&x->scores[0]);
+                for (int k = 0; k < 2; ++k) drain(&x->scores[0], k);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ products: the sums, and q with the state
+        if (lane == 0) {
+            const uint32_t id_o = idesc_bf16(128, kV, 0, 1), w_tile = smem_u32(sm + geo.w_at);
+            const uint64_t sd = sw128_desc(smem_u32(sm + geo.s_at), 16, 1024);
+            bool stop = false;
+            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
+                Item t;
+                take(a, ordered_item(a, geo, item), &t);
+                const int kb = t.p->kd / 64;
+                for (int c = 0; c < t.chunks; ++c, ++g) {
+                    const int s = g % geo.stages;
+                    const uint32_t q = smem_u32(sm + s * geo.stage_bytes);
+                    const uint64_t qd = sw128_desc(q, 16, 1024);
+                    // weights are made of a chunk that has landed
+                    stop = !wait(&x->weights[s], (g / geo.stages) & 1, &x->stop, status) ||
                            (g > 0 && !wait(&x->sums_free, (g - 1) & 1, &x->stop, status));
                     if (stop) break;
                     tc_fence_after();
-                    mma_sums<NT>(tmem + kColU, k, w_tile, kb, 0u);
+                    mma_sums<NT>(tmem + C::u, q + kbytes, w_tile, kb, 0u);
                     mma_commit(&x->sums);
-                    mma_commit(&x->weights_free);
                     stop = !wait(&x->state, g & 1, &x->stop, status) ||
                            (g > 0 && !wait(&x->outs_free, (g - 1) & 1, &x->stop, status));
                     if (stop) break;
@@ -503,30 +658,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (i < 4 * kb)
-                            mma_bf16(tmem + kColO2, moved(qd, (i >> 2) * kSub + (i & 3) * 32),
-                                     moved(s_desc, i * 2048), id_o, i > 0);
-                    stop = !wait(&x->masked, g & 1, &x->stop, status);
-                    if (stop) break;
-                    tc_fence_after();
-                    const uint64_t vd = sw128_desc(v, 16, 1024);
-#pragma unroll
-                    for (int i = 0; i < kQ / 16; ++i)
-                        mma_bf16_ta(tmem + kColO1, tmem + kColMasked + 8 * i, moved(vd, i * 2048), id_o, i > 0);
+                            mma_bf16(tmem + C::o2, moved(qd, (i >> 2) * kSub + (i & 3) * 32), moved(sd, i * 2048), id_o,
+                                     i > 0);
+                    mma_commit(&x->state_free);
                     mma_commit(&x->outs);
                     mma_commit(&x->empty[s]);
+                    mma_commit(&x->empty_v[s]);
                 }
             }
-            if (stop) {  // what was issued must end before the columns are given back
-                uint64_t* bar = &x->weights_free;
-                mma_commit(bar);
-                for (int k = 0; k < 2; ++k) drain(bar, k);
+            if (stop) {
+                mma_commit(&x->sums);
+                for (int k = 0; k < 2; ++k) drain(&x->sums, k);
             }
         }
         __syncwarp();
     }
 done:
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 16) {
         tmem_relinquish();
         tmem_dealloc(tmem, 512);
     }
@@ -588,11 +737,15 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             if (tid < p.kd) {
                 float* out = p.s_sum + (t.id * a.H + t.h) * (long long)p.kd * p.vd + tid * p.sn + t.v0 * p.sp;
 #pragma unroll 1
-                for (int i = 0; i < kV; i += 16) {
-                    float u[16];
-                    load_sum16<NT>(tmem + lane_base + i, u);
+                for (int i = 0; i < kV; i += 8) {
+                    F2 u[4];
+                    load_sum8<NT>(tmem + lane_base + i, u);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) out[(i + e) * p.sp] = u[e];
+                    for (int e = 0; e < 4; ++e) {
+                        float f[2];
+                        layer::split(u[e], f);
+                        out[(i + 2 * e) * p.sp] = f[0], out[(i + 2 * e + 1) * p.sp] = f[1];
+                    }
                 }
             }
             tc_fence_before();
@@ -609,7 +762,9 @@ __global__ void __launch_bounds__(kSumThreads, 1)
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     const int s = g % geo.stages;
                     if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    tiles.load<false>((int)t.g.start + c * kQ, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
+                    unsigned char* st = sm + s * geo.stage_bytes;
+                    tiles.load_qk<false>((int)t.g.start + c * kQ, st, kbytes, &x->full[s]);
+                    tiles.load_v((int)t.g.start + c * kQ, st + kbytes, &x->full[s]);
                 }
             }
             if (*(volatile int*)&x->stop)
@@ -686,7 +841,7 @@ cudaError_t launch(K kernel, const WalkArgs& a, const Maps& m, const Geometry& g
                    cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min<long long>(geo.items, sm_count());
+    const unsigned grid = (unsigned)(geo.by_pass ? geo.items : std::min(geo.items, sm_count()));
     kernel<<<grid, threads, smem, stream>>>(a, m, geo);
     return cudaSuccess;
 }
@@ -713,11 +868,17 @@ bool tc_fits(const Pass& p) {
            ok(p.v, p.vs, 2) && ok(p.out, p.os, p.out_f32 ? 4 : 2);
 }
 
-cudaError_t tc_walk(const WalkArgs& a, Launch& L) {
+cudaError_t tc_walk(const WalkArgs& given, Launch& L) {
+    WalkArgs a = given;
+    // whole sequences: a block for each item, those with the larger states first
+    const bool by_pass = !a.Ls && !a.cu && a.rowlen >= 16 * kQ;
+    if (by_pass)
+        std::stable_sort(a.pass, a.pass + a.npass, [](const Pass& x, const Pass& y) { return x.kd > y.kd; });
     Maps m;
     if (!make_maps(a, &m)) return cudaErrorInvalidValue;
     const bool three = exact_states(a);
     Geometry geo;
+    geo.by_pass = by_pass;
     geo.kblocks = kblocks_of(a);
     geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
     geo.stage_bytes = (2 * geo.kblocks + 1) * kSub;
@@ -739,6 +900,7 @@ cudaError_t tc_sums(const WalkArgs& a, Launch& L) {
     if (!make_maps(a, &m)) return cudaErrorInvalidValue;
     const bool three = exact_states(a);
     Geometry geo;
+    geo.by_pass = 0;
     geo.kblocks = kblocks_of(a);
     geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
     geo.stage_bytes = (geo.kblocks + 1) * kSub;
