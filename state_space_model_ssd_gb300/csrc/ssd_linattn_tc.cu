@@ -48,18 +48,20 @@ struct Maps {
     CUtensorMap m[3][3];  // of each pass: q, k, v
 };
 struct Geometry {
-    int stages, kblocks;    // chunks in shared memory at a time; most blocks of 64 channels of q and k
-    int stage_bytes, w_at, s_at, aux_at;
+    int stages, v_stages;   // chunks of q and k, and of v, in shared memory at a time
+    int kblocks;            // most blocks of 64 channels of q and k
+    int stage_bytes, v_at, w_at, s_at, aux_at;
     int items, by_pass;
 };
 
 // Barriers and what else is small, behind the tiles.
 struct Aux {
-    uint64_t full[kMostStages], empty[kMostStages], empty_v[kMostStages], weights[kMostStages], made[2];
+    uint64_t full[kMostStages], empty[kMostStages], full_v[kMostStages], empty_v[kMostStages], weights[kMostStages];
+    uint64_t made[2];
     uint64_t scores[2], masked[2], masked_free, state, state_free, outs, outs_free, sums, sums_free;
     uint32_t tmem;
     int stop;
-    float diag[4][64];  // a copy for each of the mask's warps: 0 (31 times), a^0 .. a^31
+    float diag[4][64];  // for each of the mask's warps: a^0 .. a^31 in the columns' order, zeros before or after
 };
 
 // Waits for a phase, at most kLimitNs: one that runs out records SSD_ERR_TIMEOUT and ends every wait
@@ -89,6 +91,18 @@ __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
 // wait() for a whole warp, whose lanes go on or stop together.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
     return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
+}
+
+// One thread of a warp that is together.  The products' warps go through their loops as warps, on
+// values that are the same in all lanes, so that descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+template <typename T>
+__device__ __forceinline__ T same(T v) {
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // D[tmem] (+)= A[tmem] B[smem]: A's rows in the lanes, two bf16 of a row in each column.
@@ -195,14 +209,25 @@ struct Item {
     int pass, h, v0, chunks;
     float ld;
 };
-__device__ __noinline__ void take(const WalkArgs& a, int item, Item* t) {
-    const int row = a.H * a.tiles;
-    const int id = item / row, rest = item - id * row;
+__device__ __noinline__ void take(const WalkArgs& a, int by_pass, int item, Item* t) {
+    int id, tile, pass = 0;
+    if (by_pass) {  // pass by pass, the tiles of one segment and head next to one another
+        const int pairs = (int)a.ids * a.H;
+        while (pass + 1 < a.npass && item >= pairs * a.pass[pass].tiles) item -= pairs * a.pass[pass++].tiles;
+        const int w = a.pass[pass].tiles, pair = item / w;
+        tile = item - pair * w;
+        id = pair / a.H;
+        t->h = pair - id * a.H;
+    } else {  // the tiles of all passes of one
+        const int row = a.H * a.tiles;
+        id = item / row;
+        const int rest = item - id * row;
+        t->h = rest / a.tiles;
+        tile = rest - t->h * a.tiles;
+        while (pass + 1 < a.npass && tile >= a.pass[pass].tiles) tile -= a.pass[pass++].tiles;
+    }
     t->id = id;
-    t->h = rest / a.tiles;
-    int tile = rest - t->h * a.tiles;
-    t->pass = 0;
-    while (t->pass + 1 < a.npass && tile >= a.pass[t->pass].tiles) tile -= a.pass[t->pass++].tiles;
+    t->pass = pass;
     t->p = &a.pass[t->pass];
     t->v0 = tile * kV;
     t->g = segment(a, t->id);
@@ -227,7 +252,7 @@ struct Tiles {
           hk(t.h / t.p->kr), hv(t.h / t.p->vr), v0(t.v0), kb(t.p->kd / 64) {}
     template <bool WITH_Q>
     __device__ __forceinline__ void load_qk(int t0, unsigned char* st, int kbytes, uint64_t* bar) const {
-        mbar_expect_tx(bar, (uint32_t)(((WITH_Q ? 2 : 1) * kb + 1) * kSub));
+        mbar_expect_tx(bar, (uint32_t)((WITH_Q ? 2 : 1) * kb * kSub));
 #pragma unroll 1
         for (int b = 0; b < kb; ++b, st += kSub) {
             tma_load_3d(st + (WITH_Q ? kbytes : 0), k, bar, b * 64, hk, t0);
@@ -235,6 +260,7 @@ struct Tiles {
         }
     }
     __device__ __forceinline__ void load_v(int t0, unsigned char* at, uint64_t* bar) const {
+        mbar_expect_tx(bar, kSub);
         tma_load_3d(at, v, bar, v0, hv, t0);
     }
 };
@@ -291,12 +317,10 @@ __device__ __forceinline__ void mask_chunk(uint32_t lanes, int g, int n, bool re
                     if (j0 + e >= n) s[e] = 0u;
             }
             if (q == warp) {
-                const float* f = rev ? diag + 31 - lane : diag + 31 + lane;
+                const float* f = diag + 31 - lane;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const F2 w = rev ? layer::join(f[2 * e], f[2 * e + 1]) : layer::join(f[-2 * e], f[-2 * e - 1]);
-                    o[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), w));
-                }
+                for (int e = 0; e < 16; ++e)
+                    o[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(f[2 * e], f[2 * e + 1])));
             } else {
                 // forwards the power to the half's last column, from the end to its first
                 const int d = rev ? j0 - i : i - j0 - 15, step = rev ? 16 : -16;
@@ -377,17 +401,6 @@ __device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux
     return true;
 }
 
-// Where item `item` of a launch is in the order of `take`.
-__device__ __forceinline__ int ordered_item(const WalkArgs& a, const Geometry& geo, int item) {
-    if (!geo.by_pass) return item;
-    // pass by pass, the tiles of one next to one another
-    const int pairs = (int)a.ids * a.H;
-    int tile = 0, p = 0;
-    while (p + 1 < a.npass && item >= pairs * a.pass[p].tiles) item -= pairs * a.pass[p].tiles, tile += a.pass[p++].tiles;
-    const int w = a.pass[p].tiles;
-    return item / w * a.tiles + tile + item % w;
-}
-
 template <int NT>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_walk_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
@@ -401,8 +414,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     int* status = a.status;
     if (threadIdx.x == 0) {
         for (int s = 0; s < geo.stages; ++s) {
-            mbar_init(&x->full[s], 1), mbar_init(&x->weights[s], 128);
-            mbar_init(&x->empty[s], 2), mbar_init(&x->empty_v[s], 2);
+            mbar_init(&x->full[s], 1), mbar_init(&x->empty[s], 2);
+        }
+        for (int s = 0; s < geo.v_stages; ++s) {
+            mbar_init(&x->full_v[s], 1), mbar_init(&x->empty_v[s], 2), mbar_init(&x->weights[s], 128);
         }
         for (int s = 0; s < 2; ++s) mbar_init(&x->scores[s], 1), mbar_init(&x->masked[s], 128);
         mbar_init(&x->masked_free, 1), mbar_init(&x->state_free, 1), mbar_init(&x->sums, 1);
@@ -423,18 +438,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float* diag = x->diag[warp];
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, ordered_item(a, geo, item), &t);
+            take(a, geo.by_pass, item, &t);
             const bool rev = t.p->reverse;
             const float ld2 = t.ld * 1.44269504f;
             __syncwarp();  // the last item's are no longer read
-            diag[lane] = 0.f;
+            // column e of row `lane` is at 31 - lane + e: from the end a^(e - lane), else a^(lane - e)
+            diag[rev ? lane : lane + 31] = 0.f;
             __syncwarp();
-            diag[lane + 31] = power(ld2, lane);
+            diag[rev ? lane + 31 : 31 - lane] = power(ld2, lane);
             __syncwarp();
             F2 far[8];
+            const float* first = rev ? diag + 31 : diag + 16;  // a^0 .. a^15, or a^15 .. a^0
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                far[e] = rev ? layer::join(diag[31 + 2 * e], diag[32 + 2 * e]) : layer::join(diag[46 - 2 * e], diag[45 - 2 * e]);
+            for (int e = 0; e < 8; ++e) far[e] = layer::join(first[2 * e], first[2 * e + 1]);
 #pragma unroll 1
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 int n;
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const int i = tid;
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, ordered_item(a, geo, item), &t);
+            take(a, geo.by_pass, item, &t);
             const Pass& p = *t.p;
             const bool rev = p.reverse, f32 = p.out_f32;
             char* out = static_cast<char*>(p.out);
@@ -520,7 +536,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         // ------------------------------------------------ state
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, ordered_item(a, geo, item), &t);
+            take(a, geo.by_pass, item, &t);
             if (!t.g.there) continue;
             if (!state_item<NT>(a, t, x, sm + geo.s_at, tmem + lane_base + C::u, tid, g, status)) goto done;
         }
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         // ------------------------------------------------ weights
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, ordered_item(a, geo, item), &t);
+            take(a, geo.by_pass, item, &t);
             const Pass& p = *t.p;
             const float ld2 = t.ld * 1.44269504f;
             const float whole = power(ld2, p.reverse ? tid + 1 : kQ - 1 - tid) * p.su;
@@ -536,17 +552,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             for (int c = 0; c < t.chunks; ++c, ++g) {
                 int n;
                 chunk_start(t, c, &n);
-                const int s = g % geo.stages;
-                unsigned char* st = sm + s * geo.stage_bytes;
-                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status)) goto done;
+                const int s = g % geo.v_stages;
+                unsigned char* v = sm + geo.v_at + s * kSub;
+                if (!wait_warp(&x->full_v[s], (g / geo.v_stages) & 1, &x->stop, status)) goto done;
                 // the product before has read the last weights
                 if (g > 0 && !wait_warp(&x->sums, (g - 1) & 1, &x->stop, status)) goto done;
                 const bool in = tid < n;
                 const float w = n == kQ || p.reverse ? whole : power(ld2, max(n - 1 - tid, 0)) * p.su;
-                split_row<NT>(st + 2 * kbytes, sm + geo.w_at, tid, w, in);
-                if (!in) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
-                    zero_row(st + 2 * kbytes, tid);
-                    for (int b = 0; b < p.kd / 64; ++b) zero_row(st + kbytes + b * kSub, tid);
+                split_row<NT>(v, sm + geo.w_at, tid, w, in);
+                if (n < kQ) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
+                    const int k = g % geo.stages;
+                    if (!wait_warp(&x->full[k], (g / geo.stages) & 1, &x->stop, status)) goto done;
+                    if (!in) {
+                        zero_row(v, tid);
+                        for (int b = 0; b < p.kd / 64; ++b)
+                            zero_row(sm + k * geo.stage_bytes + kbytes + b * kSub, tid);
+                    }
                 }
                 fence_proxy_async();
                 mbar_arrive(&x->weights[s]);
@@ -555,123 +576,130 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else if (warp == 16) {
         // ------------------------------------------------ copies in
         if (lane == 0) {
+            int issued = 0;
             for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
                 Item t;
-                take(a, ordered_item(a, geo, item), &t);
+                take(a, geo.by_pass, item, &t);
                 const Tiles tiles(maps, t);
                 for (int c = 0; c < t.chunks; ++c, ++g) {
                     int n;
-                    const int t0 = (int)chunk_start(t, c, &n), s = g % geo.stages, ph = (g / geo.stages - 1) & 1;
-                    unsigned char* st = sm + s * geo.stage_bytes;
-                    if (g >= geo.stages && !wait(&x->empty[s], ph, &x->stop, status)) break;
-                    tiles.load_qk<true>(t0, st, kbytes, &x->full[s]);
-                    // the rest of the chunk is issued in any case: its barrier counts on it
-                    if (g >= geo.stages && !wait(&x->empty_v[s], ph, &x->stop, status)) drain(&x->empty_v[s], ph);
-                    tiles.load_v(t0, st + 2 * kbytes, &x->full[s]);
+                    const int t0 = (int)chunk_start(t, c, &n), s = g % geo.stages, vs = g % geo.v_stages;
+                    if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
+                    tiles.load_qk<true>(t0, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
+                    ++issued;
+                    if (g >= geo.v_stages && !wait(&x->empty_v[vs], (g / geo.v_stages - 1) & 1, &x->stop, status)) break;
+                    tiles.load_v(t0, sm + geo.v_at + vs * kSub, &x->full_v[vs]);
                 }
             }
             // after a wait that ran out: copies on their way must not land in the next block's memory
-            if (*(volatile int*)&x->stop)
-                for (int k = max(0, g - geo.stages); k < g; ++k)
+            if (*(volatile int*)&x->stop) {
+                for (int k = max(0, issued - geo.stages); k < issued; ++k)
                     drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
+                for (int k = max(0, g - geo.v_stages); k < g; ++k)
+                    drain(&x->full_v[k % geo.v_stages], (k / geo.v_stages) & 1);
+            }
         }
         __syncwarp();
     } else if (warp == 17) {
         // ------------------------------------------------ products: scores, and the masked ones with v
-        if (lane == 0) {
-            const uint32_t id_a = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kV, 0, 1);
-            bool stop = false;
-            // the masked product of chunk k, which waits for the next chunk's scores
-            const auto masked = [&](int k) {
-                const int s = k % geo.stages;
-                // with the weights v's rows behind the sequence's end are zero
-                if (!wait(&x->masked[C::at(k)], C::parity(k), &x->stop, status) ||
-                    !wait(&x->weights[s], (k / geo.stages) & 1, &x->stop, status) ||
-                    (k > 0 && !wait(&x->outs_free, (k - 1) & 1, &x->stop, status)))
-                    return false;
-                tc_fence_after();
-                const uint64_t vd = sw128_desc(smem_u32(sm + s * geo.stage_bytes) + 2 * kbytes, 16, 1024);
-#pragma unroll
-                for (int i = 0; i < kQ / 16; ++i)
-                    mma_bf16_ta(tmem + C::o1, tmem + C::masked(k) + 8 * i, moved(vd, i * 2048), id_o, i > 0);
-                mma_commit(&x->outs);
-                if (C::kPlaces == 1) mma_commit(&x->masked_free);
-                mma_commit(&x->empty_v[s]);
-                return true;
-            };
-            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                Item t;
-                take(a, ordered_item(a, geo, item), &t);
-                const int kb = t.p->kd / 64;
-                for (int c = 0; c < t.chunks; ++c, ++g) {
-                    const int s = g % geo.stages;
-                    const uint32_t q = smem_u32(sm + s * geo.stage_bytes);
-                    const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(q + kbytes, 16, 1024);
-                    // with one place for the scores, those before have been read
-                    stop = !wait(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
-                           (C::kPlaces == 1 && g > 0 && !wait(&x->masked[0], (g - 1) & 1, &x->stop, status));
-                    if (stop) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < 4 * kb)
-                            mma_bf16(tmem + C::scores(g), moved(qd, (i >> 2) * kSub + (i & 3) * 32),
-                                     moved(kd, (i >> 2) * kSub + (i & 3) * 32), id_a, i > 0);
-                    mma_commit(&x->scores[C::at(g)]);
-                    mma_commit(&x->empty[s]);
-                    stop = g > 0 && !masked(g - 1);
-                    if (stop) break;
+        const uint32_t id_a = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kV, 0, 1);
+        const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
+        int item = blockIdx.x - gridDim.x, left = 0, kb = 0;
+        for (bool more = true; more; ++g) {
+            while (left == 0 && more) {
+                item += gridDim.x;
+                more = item < geo.items;
+                if (more) {
+                    Item t;
+                    take(a, geo.by_pass, item, &t);
+                    left = same(t.chunks), kb = same(t.p->kd / 64);
                 }
             }
-            if (!stop && g > 0) stop = !masked(g - 1);
-            if (stop) {  // what was issued must end before the columns are given back
-                mma_commit(&x->scores[0]);
-                for (int k = 0; k < 2; ++k) drain(&x->scores[0], k);
-            }
-        }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------ products: the sums, and q with the state
-        if (lane == 0) {
-            const uint32_t id_o = idesc_bf16(128, kV, 0, 1), w_tile = smem_u32(sm + geo.w_at);
-            const uint64_t sd = sw128_desc(smem_u32(sm + geo.s_at), 16, 1024);
-            bool stop = false;
-            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                Item t;
-                take(a, ordered_item(a, geo, item), &t);
-                const int kb = t.p->kd / 64;
-                for (int c = 0; c < t.chunks; ++c, ++g) {
-                    const int s = g % geo.stages;
-                    const uint32_t q = smem_u32(sm + s * geo.stage_bytes);
-                    const uint64_t qd = sw128_desc(q, 16, 1024);
-                    // weights are made of a chunk that has landed
-                    stop = !wait(&x->weights[s], (g / geo.stages) & 1, &x->stop, status) ||
-                           (g > 0 && !wait(&x->sums_free, (g - 1) & 1, &x->stop, status));
-                    if (stop) break;
-                    tc_fence_after();
-                    mma_sums<NT>(tmem + C::u, q + kbytes, w_tile, kb, 0u);
-                    mma_commit(&x->sums);
-                    stop = !wait(&x->state, g & 1, &x->stop, status) ||
-                           (g > 0 && !wait(&x->outs_free, (g - 1) & 1, &x->stop, status));
-                    if (stop) break;
-                    tc_fence_after();
+            if (more) {
+                const int s = g % geo.stages;
+                // with one place for the scores, those before have been read
+                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
+                    (C::kPlaces == 1 && g > 0 && !wait_warp(&x->masked[0], (g - 1) & 1, &x->stop, status)))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    uint64_t qd = sw128_desc(base + s * geo.stage_bytes, 16, 1024), kd = moved(qd, kbytes);
+#pragma unroll 1
+                    for (int b = 0; b < kb; ++b, qd = moved(qd, kSub), kd = moved(kd, kSub))
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < 4 * kb)
-                            mma_bf16(tmem + C::o2, moved(qd, (i >> 2) * kSub + (i & 3) * 32), moved(sd, i * 2048), id_o,
-                                     i > 0);
-                    mma_commit(&x->state_free);
-                    mma_commit(&x->outs);
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16(tm + C::scores(g), moved(qd, i * 32), moved(kd, i * 32), id_a, b + i > 0);
+                    mma_commit(&x->scores[C::at(g)]);
                     mma_commit(&x->empty[s]);
+                }
+                --left;
+            }
+            if (g > 0) {  // the masked product of the chunk before, whose mask this one's scores went ahead of
+                const int k = g - 1, s = k % geo.v_stages;
+                // with the weights v's rows behind the sequence's end are zero
+                if (!wait_warp(&x->masked[C::at(k)], C::parity(k), &x->stop, status) ||
+                    !wait_warp(&x->weights[s], (k / geo.v_stages) & 1, &x->stop, status) ||
+                    (k > 0 && !wait_warp(&x->outs_free, (k - 1) & 1, &x->stop, status)))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t vd = sw128_desc(base + geo.v_at + s * kSub, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < kQ / 16; ++i)
+                        mma_bf16_ta(tm + C::o1, tm + C::masked(k) + 8 * i, moved(vd, i * 2048), id_o, i > 0);
+                    mma_commit(&x->outs);
+                    if (C::kPlaces == 1) mma_commit(&x->masked_free);
                     mma_commit(&x->empty_v[s]);
                 }
             }
-            if (stop) {
-                mma_commit(&x->sums);
-                for (int k = 0; k < 2; ++k) drain(&x->sums, k);
+        }
+        if (*(volatile int*)&x->stop) {  // what was issued must end before the columns are given back
+            if (elect_one()) mma_commit(&x->scores[0]);
+            for (int k = 0; k < 2; ++k) drain(&x->scores[0], k);
+        }
+    } else {
+        // ------------------------------------------------ products: the sums, and q with the state
+        const uint32_t id_o = idesc_bf16(128, kV, 0, 1);
+        const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            Item t;
+            take(a, geo.by_pass, item, &t);
+            const int kb = same(t.p->kd / 64), chunks = same(t.chunks);
+            for (int c = 0; c < chunks; ++c, ++g) {
+                const int s = g % geo.stages, vs = g % geo.v_stages;
+                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
+                    !wait_warp(&x->weights[vs], (g / geo.v_stages) & 1, &x->stop, status) ||
+                    (g > 0 && !wait_warp(&x->sums_free, (g - 1) & 1, &x->stop, status)))
+                    goto stopped;
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_sums<NT>(tm + C::u, base + s * geo.stage_bytes + kbytes, base + geo.w_at, kb, 0u);
+                    mma_commit(&x->sums);
+                    mma_commit(&x->empty_v[vs]);
+                }
+                if (!wait_warp(&x->state, g & 1, &x->stop, status) ||
+                    (g > 0 && !wait_warp(&x->outs_free, (g - 1) & 1, &x->stop, status)))
+                    goto stopped;
+                tc_fence_after();
+                if (elect_one()) {
+                    uint64_t qd = sw128_desc(base + s * geo.stage_bytes, 16, 1024);
+                    uint64_t sd = sw128_desc(base + geo.s_at, 16, 1024);
+#pragma unroll 1
+                    for (int b = 0; b < kb; ++b, qd = moved(qd, kSub), sd = moved(sd, 8192))
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16(tm + C::o2, moved(qd, i * 32), moved(sd, i * 2048), id_o, b + i > 0);
+                    mma_commit(&x->state_free);
+                    mma_commit(&x->outs);
+                    mma_commit(&x->empty[s]);
+                }
             }
         }
-        __syncwarp();
+    stopped:
+        if (*(volatile int*)&x->stop) {
+            if (elect_one()) mma_commit(&x->sums);
+            for (int k = 0; k < 2; ++k) drain(&x->sums, k);
+        }
     }
 done:
     __syncthreads();
@@ -695,7 +723,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     const int kbytes = geo.kblocks * kSub;
     int* status = a.status;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < geo.stages; ++s) mbar_init(&x->full[s], 1), mbar_init(&x->empty[s], 1);
+        // a chunk's copies are announced in two steps
+        for (int s = 0; s < geo.stages; ++s) mbar_init(&x->full[s], 2), mbar_init(&x->empty[s], 1);
         for (int s = 0; s < 2; ++s) mbar_init(&x->made[s], 128);
         mbar_init(&x->sums, 1), mbar_init(&x->sums_free, 128);
         x->stop = 0;
@@ -713,7 +742,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     if (warp < 4) {
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             Item t;
-            take(a, item, &t);
+            take(a, geo.by_pass, item, &t);
             if (!wanted(t)) continue;
             const Pass& p = *t.p;
             const float ld2 = t.ld * 1.44269504f;
@@ -756,7 +785,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         if (lane == 0) {
             for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
                 Item t;
-                take(a, item, &t);
+                take(a, geo.by_pass, item, &t);
                 if (!wanted(t)) continue;
                 const Tiles tiles(maps, t);
                 for (int c = 0; c < t.chunks; ++c, ++g) {
@@ -777,7 +806,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             bool stop = false;
             for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
                 Item t;
-                take(a, item, &t);
+                take(a, geo.by_pass, item, &t);
                 if (!wanted(t)) continue;
                 if (m > 0 && !wait(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
                 tc_fence_after();
@@ -881,12 +910,21 @@ cudaError_t tc_walk(const WalkArgs& given, Launch& L) {
     geo.by_pass = by_pass;
     geo.kblocks = kblocks_of(a);
     geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
-    geo.stage_bytes = (2 * geo.kblocks + 1) * kSub;
-    const int rest = (three ? 3 : 2) * kSub + geo.kblocks * 64 * 128 + (int)sizeof(Aux);
-    geo.stages = std::min(3, (kMostSmem - rest) / geo.stage_bytes);
-    geo.w_at = geo.stages * geo.stage_bytes;
-    geo.s_at = geo.w_at + (three ? 3 : 2) * kSub;
-    geo.aux_at = geo.s_at + geo.kblocks * 64 * 128;
+    geo.stage_bytes = 2 * geo.kblocks * kSub;
+    const int w = (three ? 3 : 2) * kSub, state = geo.kblocks * 64 * 128;
+    const auto total = [&](int stages, int v_stages) {
+        return stages * geo.stage_bytes + v_stages * kSub + w + state + (int)sizeof(Aux);
+    };
+    geo.stages = geo.v_stages = 2;
+    // v is given back last, and gets its place first
+    while (geo.v_stages < kMostStages && total(geo.stages, geo.v_stages + 1) <= kMostSmem) {
+        ++geo.v_stages;
+        if (geo.stages < geo.v_stages && total(geo.stages + 1, geo.v_stages) <= kMostSmem) ++geo.stages;
+    }
+    geo.v_at = geo.stages * geo.stage_bytes;
+    geo.w_at = geo.v_at + geo.v_stages * kSub;
+    geo.s_at = geo.w_at + w;
+    geo.aux_at = geo.s_at + state;
     const size_t smem = (size_t)geo.aux_at + sizeof(Aux);
     L.begin("linattn_tc_walk");
     const cudaError_t e = three ? launch(tc_walk_kernel<3>, a, m, geo, kWalkThreads, smem, L.stream)
