@@ -119,6 +119,7 @@ __device__ __forceinline__ float power(float ld2, int d) { return d == 0 ? 1.f :
 // below 1/2 that sum would cancel, and few factors matter.
 struct Decay {
     float m, keep;  // keep: 1 or 0
+    Decay() = default;
     __device__ __forceinline__ Decay(float ld, int d) {
         const float m1 = d == 0 ? 0.f : expm1f(ld * d);
         keep = m1 > -0.5f ? 1.f : 0.f;

@@ -11,16 +11,19 @@
 // The state goes from chunk to chunk in registers, in float32.  W must not be rounded to bf16: the
 // states are float32 outputs.  So W is split into three bf16 terms, W = W1 + W2 + W3 to 2^-25 (two,
 // to 2^-18, in calls that return no state, whose outputs are all rounded to 2^-9), which stand
-// side by side as one operand of 192 columns: the products k W1, k W2, k W3 come out beside one
-// another and are added in float32.  A power a^(i-j) is never split into a^i a^-j over more than 16
+// side by side as one operand: the products k W1 and k W2 come out beside one another (k W3 is added
+// to the second) and are added in float32.  A power a^(i-j) is never split into a^i a^-j over more than 16
 // tokens below the diagonal, so that nothing overflows.
 //
-// One block an SM, four warps for each of four tasks: mask (A to the masked operand), outputs,
-// state (U into S) and weights (v to W); one warp for the copies in (TMA, two or three chunks ahead);
-// two that issue products, A and O1 in one, U and O2 in the other, so that the chunk's two chains
-// (scores, mask, outputs; weights, sums, state) wait for each other only at the outputs.  Blocks
-// stay and take items in turn, or, where items are long and of unequal cost, there is a block for
-// each item, the dearest first.  The tiles of all passes of one segment and head are next to one
+// One block an SM: sixteen warps that all go through the same steps of a chunk (mask, state, the next
+// chunk's weights, outputs), each on its 32 rows and a quarter of the columns, one warp for the copies
+// in (TMA, two or three chunks ahead), and two that issue products: A and O1 in one, U and O2 in the
+// other.  While the warps are at one step, the products of the steps before run.  Warps with a task
+// each (mask, state, weights, outputs side by side) were 1.3 to 1.5 times slower: four streams of
+// instructions that each go straight through a few hundred of them leave the instruction caches
+// nothing to share (a third of the stalls), while here sixteen warps follow one another.
+// Blocks stay and take items in turn, or, where items are long and of unequal cost, there is a block
+// for each item, the dearest first.  The tiles of all passes of one segment and head are next to one
 // another, so that what they all read comes from L2 after the first.
 #include <algorithm>
 
@@ -41,6 +44,7 @@ constexpr int kV = kTcTile;                  // 64 columns
 constexpr int kSub = kQ * 128;               // bytes of a tile of 64 channels: rows of 128 bytes
 constexpr int kWalkThreads = 19 * 32;
 constexpr int kSumThreads = 6 * 32;
+constexpr int kTeam = 16;                    // warps that work on the numbers
 constexpr int kMostStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
@@ -54,14 +58,69 @@ struct Geometry {
     int items, by_pass;
 };
 
+// What a block works on at a time: one segment, head and tile.  It is kept in shared memory, as nothing
+// that is read often may be on the stack: beside 227 KB of shared memory there is no L1 to hold it (a
+// few spilled registers, at 9 % hits, cost a third of the walk's time).
+struct Item {
+    Seg g;
+    const Pass* p;
+    long long id;
+    int pass, h, v0, chunks, kb, rev, f32, short_one;  // short_one: the chunk that may be short
+    float ld, ld2, si, sx, su;
+    Decay whole, last;  // over a whole chunk, and over the short one
+    char* out;          // the tile's columns of the segment's first token
+    long long os;       // bytes from one token of out to the next
+};
+__device__ __noinline__ void take(const WalkArgs& a, int by_pass, int item, Item* t) {
+    int id, tile, pass = 0;
+    if (by_pass) {  // pass by pass, the tiles of one segment and head next to one another
+        const int pairs = (int)a.ids * a.H;
+        while (pass + 1 < a.npass && item >= pairs * a.pass[pass].tiles) item -= pairs * a.pass[pass++].tiles;
+        const int w = a.pass[pass].tiles, pair = item / w;
+        tile = item - pair * w;
+        id = pair / a.H;
+        t->h = pair - id * a.H;
+    } else {  // the tiles of all passes of one
+        const int row = a.H * a.tiles;
+        id = item / row;
+        const int rest = item - id * row;
+        t->h = rest / a.tiles;
+        tile = rest - t->h * a.tiles;
+        while (pass + 1 < a.npass && tile >= a.pass[pass].tiles) tile -= a.pass[pass++].tiles;
+    }
+    t->id = id;
+    t->pass = pass;
+    t->p = &a.pass[t->pass];
+    t->v0 = tile * kV;
+    t->g = segment(a, t->id);
+    t->chunks = t->g.there ? (t->g.len + kQ - 1) / kQ : 0;
+    const Pass& p = *t->p;
+    const float ld = a.ld[t->h];
+    t->ld = ld, t->ld2 = ld * 1.44269504f;
+    t->kb = p.kd / 64, t->rev = p.reverse, t->f32 = p.out_f32, t->si = p.si, t->sx = p.sx, t->su = p.su;
+    t->short_one = p.reverse ? 0 : t->chunks - 1;
+    t->whole = Decay(ld, kQ), t->last = Decay(ld, (t->g.len - 1) % kQ + 1);
+    t->os = p.os * (p.out_f32 ? 4 : 2);
+    t->out = static_cast<char*>(p.out) + t->g.start * t->os +
+             ((long long)(t->h / p.outr) * p.vd + t->v0) * (p.out_f32 ? 4 : 2);
+}
 // Barriers and what else is small, behind the tiles.
+constexpr int kBelow = 31;  // zeros before a^0
 struct Aux {
     uint64_t full[kMostStages], empty[kMostStages], full_v[kMostStages], empty_v[kMostStages], weights[kMostStages];
-    uint64_t made[2];
-    uint64_t scores[2], masked[2], masked_free, state, state_free, outs, outs_free, sums, sums_free;
+    uint64_t scores, masked, state, state_free, outs, outs_free, sums, item_full[2], item_empty[2];
     uint32_t tmem;
     int stop;
-    float diag[4][64];  // for each of the mask's warps: a^0 .. a^31 in the columns' order, zeros before or after
+    // the item the block works on and the next, and the powers of their heads: 0 for -kBelow .. -1,
+    // a^0 .. a^127; made by the warp that copies in
+    Item items[2];
+    float powers[2][kBelow + kQ];
+};
+struct SumsAux {
+    uint64_t full[kMostStages], empty[kMostStages], made[2], sums, sums_free;
+    uint32_t tmem;
+    int stop;
+    Item items[kSumThreads / 32];  // of each warp
 };
 
 // Waits for a phase, at most kLimitNs: one that runs out records SSD_ERR_TIMEOUT and ends every wait
@@ -140,14 +199,16 @@ __device__ __forceinline__ uint32_t pack(F2 v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Row `row` of a 128 x 64 tile of v times w into NT tiles kSub apart: each term is what the ones before
-// it left, rounded to bf16.  A weight of a token behind the sequence's end is a zero row.
+// Pieces first .. first + pieces of 8 columns of row `row` of a 128 x 64 tile of v, times w, into NT
+// tiles kSub apart: each term is what the ones before it left, rounded to bf16.  A token behind the
+// sequence's end is a zero row.
 template <int NT>
-__device__ __forceinline__ void split_row(const unsigned char* v, unsigned char* w_out, int row, float w, bool in) {
+__device__ __forceinline__ void split_row(const unsigned char* v, unsigned char* w_out, int row, int first, int pieces,
+                                          float w, bool in) {
     const uint32_t base = row * 128, x = row & 7;
     const F2 ww = layer::both<F2>(w);
-#pragma unroll 2
-    for (int c = 0; c < 8; ++c) {
+#pragma unroll 1
+    for (int c = first; c < first + pieces; ++c) {
         const uint32_t at = base + ((c ^ x) << 4);
         uint4 raw = *reinterpret_cast<const uint4*>(v + at);
         if (!in) raw = make_uint4(0u, 0u, 0u, 0u);
@@ -172,76 +233,57 @@ __device__ __forceinline__ void zero_row(unsigned char* tile, int row) {
     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Adds the NT terms of columns [col, col + 8) of U, kV columns apart, of this thread's lane.
-template <int NT>
+// Columns [col, col + 8) of U: the large term and, kV columns on, the small ones, added.
 __device__ __forceinline__ void load_sum8(uint32_t taddr, F2* f) {
-    uint32_t r[NT][8];
-#pragma unroll
-    for (int k = 0; k < NT; ++k) tmem_ld8(taddr + k * kV, r[k]);
+    uint32_t r[2][8];
+    tmem_ld8(taddr, r[0]);
+    tmem_ld8(taddr + kV, r[1]);
     tmem_wait_ld();
+    reg_dep8(r[0]), reg_dep8(r[1]);
 #pragma unroll
-    for (int k = 0; k < NT; ++k) reg_dep8(r[k]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[i] = pair(r[NT - 1][2 * i], r[NT - 1][2 * i + 1]);  // the small terms first
-#pragma unroll
-        for (int k = NT - 2; k >= 0; --k) f[i] = layer::add_(f[i], pair(r[k][2 * i], r[k][2 * i + 1]));
-    }
+    for (int i = 0; i < 4; ++i) f[i] = layer::add_(pair(r[1][2 * i], r[1][2 * i + 1]), pair(r[0][2 * i], r[0][2 * i + 1]));
 }
 
 // Steps of 16 of a product move both operands' descriptors by a constant.
 __device__ __forceinline__ uint64_t moved(uint64_t desc, int bytes) { return desc + (uint64_t)(bytes >> 4); }
 
 // k^T W over the chunk's 128 tokens: `k` and `w` shared-memory addresses.  64 channels of k fill the
-// 128 lanes twice.
+// 128 lanes twice.  The first two terms go side by side, the third onto the second.
 template <int NT>
 __device__ __forceinline__ void mma_sums(uint32_t d, uint32_t k, uint32_t w, int kblocks, uint32_t acc) {
-    const uint32_t id = idesc_bf16(128, NT * kV, 1, 1);
     const uint64_t kd = sw128_desc(k, kblocks == 2 ? kSub : 0, 1024), wd = sw128_desc(w, kSub, 1024);
 #pragma unroll
-    for (int i = 0; i < kQ / 16; ++i) mma_bf16(d, moved(kd, i * 2048), moved(wd, i * 2048), id, acc | (i > 0));
+    for (int i = 0; i < kQ / 16; ++i)
+        mma_bf16(d, moved(kd, i * 2048), moved(wd, i * 2048), idesc_bf16(128, 2 * kV, 1, 1), acc | (i > 0));
+    if constexpr (NT == 3) {
+#pragma unroll
+        for (int i = 0; i < kQ / 16; ++i)
+            mma_bf16(d + kV, moved(kd, i * 2048), moved(wd, 2 * kSub + i * 2048), idesc_bf16(128, kV, 1, 1), 1u);
+    }
 }
 
-struct Item {
-    Seg g;
-    const Pass* p;
-    long long id;
-    int pass, h, v0, chunks;
-    float ld;
+// An item's chunks, from registers (what `take` filled in is in memory, and read again after every
+// barrier).  They lie from the segment's start on, so that a walk from the end begins with the short
+// one.
+struct Chunks {
+    long long start;
+    int len, chunks;
+    bool rev;
+    __device__ __forceinline__ explicit Chunks(const Item& t)
+        : start(t.g.start), len(t.g.len), chunks(t.chunks), rev(t.p->reverse) {}
+    // the walk's c-th chunk: its first token in the segment, how many it has
+    __device__ __forceinline__ int first(int c) const { return (rev ? chunks - 1 - c : c) * kQ; }
+    __device__ __forceinline__ int tokens(int c) const { return min(kQ, len - first(c)); }
 };
-__device__ __noinline__ void take(const WalkArgs& a, int by_pass, int item, Item* t) {
-    int id, tile, pass = 0;
-    if (by_pass) {  // pass by pass, the tiles of one segment and head next to one another
-        const int pairs = (int)a.ids * a.H;
-        while (pass + 1 < a.npass && item >= pairs * a.pass[pass].tiles) item -= pairs * a.pass[pass++].tiles;
-        const int w = a.pass[pass].tiles, pair = item / w;
-        tile = item - pair * w;
-        id = pair / a.H;
-        t->h = pair - id * a.H;
-    } else {  // the tiles of all passes of one
-        const int row = a.H * a.tiles;
-        id = item / row;
-        const int rest = item - id * row;
-        t->h = rest / a.tiles;
-        tile = rest - t->h * a.tiles;
-        while (pass + 1 < a.npass && tile >= a.pass[pass].tiles) tile -= a.pass[pass++].tiles;
+
+// A place in a ring of barriers and the parity of its phase.
+struct Place {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int places) {
+        if (++s == places) s = 0, phase ^= 1u;
     }
-    t->id = id;
-    t->pass = pass;
-    t->p = &a.pass[t->pass];
-    t->v0 = tile * kV;
-    t->g = segment(a, t->id);
-    t->chunks = t->g.there ? (t->g.len + kQ - 1) / kQ : 0;
-    t->ld = a.ld[t->h];
-}
-__device__ __noinline__ Decay decay_of(float ld, int n) { return Decay(ld, n); }
-// First token and tokens of the walk's c-th chunk: chunks lie from the segment's start on, so that a walk
-// from the end begins with the short one.
-__device__ __forceinline__ long long chunk_start(const Item& t, int c, int* n) {
-    const int at = (t.p->reverse ? t.chunks - 1 - c : c) * kQ;
-    *n = min(kQ, t.g.len - at);
-    return t.g.start + at;
-}
+};
 
 // One chunk's tiles; a thread that issues copies keeps an item's maps and heads at hand.
 struct Tiles {
@@ -278,133 +320,15 @@ __device__ __forceinline__ void store8(char* at, const uint32_t* w, bool wide) {
 }
 
 // ---------------------------------------------------------------- the walk
-// TMEM, 512 columns.  With two terms the scores have two places, and the masked operand goes over the
-// scores it came from; with three the scores have one, and the operand its own.
-template <int NT>
-struct Cols {
-    static constexpr int kPlaces = NT == 2 ? 2 : 1;
-    static constexpr uint32_t scores(int g) { return NT == 2 ? (g & 1) * 128 : 0; }
-    static constexpr uint32_t masked(int g) { return NT == 2 ? (g & 1) * 128 : 128; }
-    static constexpr uint32_t o1 = NT == 2 ? 256 : 192, o2 = o1 + kV, u = o2 + kV;
-    static_assert(u + NT * kV <= 512, "TMEM");
-    // the place and parity of chunk g's scores and masks
-    static constexpr int at(int g) { return kPlaces == 2 ? g & 1 : 0; }
-    static constexpr int parity(int g) { return kPlaces == 2 ? (g >> 1) & 1 : g & 1; }
+// Columns of TMEM: the scores, the masked operand, the two parts of the outputs, the state, the sums.
+struct C {
+    static constexpr uint32_t scores = 0, masked = 128, o1 = 192, o2 = o1 + kV, state = o2 + kV, u = state + kV;
+    static_assert(u + 2 * kV <= 512, "TMEM");
 };
-
-// The mask's task for one chunk: 32 scores of a row at a time.  Those far from the diagonal take the
-// row's power at the group's nearer end times the column's from there, so that no power is of a
-// negative distance; those at it a table of the powers with zeros beyond it.
-template <int NT>
-__device__ __forceinline__ void mask_chunk(uint32_t lanes, int g, int n, bool rev, int warp, int lane, float ld2,
-                                           const float* diag, const F2* far) {
-    const int i = 32 * warp + lane;
-#pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-        const int j0 = 32 * q;
-        uint32_t o[16];
-        if (rev ? q < warp : q > warp) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-        } else {
-            uint32_t s[32];
-            tmem_ld16(lanes + Cols<NT>::scores(g) + j0, *reinterpret_cast<uint32_t(*)[16]>(s));
-            tmem_ld16(lanes + Cols<NT>::scores(g) + j0 + 16, *reinterpret_cast<uint32_t(*)[16]>(s + 16));
-            tmem_wait_ld_regs<32>(s);
-            if (j0 + 32 > n) {  // tokens of other sequences, an infinity or a NaN maybe
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (j0 + e >= n) s[e] = 0u;
-            }
-            if (q == warp) {
-                const float* f = diag + 31 - lane;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    o[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(f[2 * e], f[2 * e + 1])));
-            } else {
-                // forwards the power to the half's last column, from the end to its first
-                const int d = rev ? j0 - i : i - j0 - 15, step = rev ? 16 : -16;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const F2 r = layer::both<F2>(power(ld2, d + h * step));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[8 * h + e] =
-                            pack(layer::mul_(pair(s[16 * h + 2 * e], s[16 * h + 2 * e + 1]), layer::mul_(r, far[e])));
-                }
-            }
-        }
-        tmem_st8(lanes + Cols<NT>::masked(g) + j0 / 2, o);
-        tmem_st8(lanes + Cols<NT>::masked(g) + j0 / 2 + 8, o + 8);
-    }
-    tmem_wait_st();
-}
-
-// The state's task for one item: row n of S, all of the tile's columns, a thread (64 channels leave
-// the upper two warps with nothing but their arrivals).
-template <int NT>
-__device__ __forceinline__ bool state_item(const WalkArgs& a, const Item& t, Aux* x, unsigned char* s_tile,
-                                           uint32_t u_cols, int n, int& g, int* status) {
-    const Pass& p = *t.p;
-    const bool mine = n < p.kd;  // the same for a whole warp
-    const long long size = (long long)p.kd * p.vd, from = (long long)t.v0 * p.sp + n * p.sn;
-    const long long seq = ((long long)t.g.seq * a.H + t.h) * size;
-    F2 S[kV / 2];
-    {
-        const float* in = p.s_seg ? p.s_seg + (t.id * a.H + t.h) * size : p.s_in ? p.s_in + seq : nullptr;
-        const bool some = in && mine;
-        in += from;
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i)
-            S[i] = some ? layer::join(in[2 * i * p.sp], in[(2 * i + 1) * p.sp]) : layer::join(0.f, 0.f);
-    }
-    const Decay whole = decay_of(t.ld, kQ), part = decay_of(t.ld, (t.g.len - 1) % kQ + 1);
-    const int short_one = p.reverse ? 0 : t.chunks - 1;
-#pragma unroll 1
-    for (int c = 0; c < t.chunks; ++c, ++g) {
-        // the last chunk's q S has read the tile
-        if (g > 0 && !wait_warp(&x->state_free, (g - 1) & 1, &x->stop, status)) return false;
-        if (mine)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(s_tile + n * 128 + ((i ^ (n & 7)) << 4)) =
-                    make_uint4(pack(S[4 * i]), pack(S[4 * i + 1]), pack(S[4 * i + 2]), pack(S[4 * i + 3]));
-        fence_proxy_async();
-        mbar_arrive(&x->state);
-        const Decay d = c == short_one ? part : whole;
-        const F2 m = layer::both<F2>(d.m);
-        if (!wait_warp(&x->sums, g & 1, &x->stop, status)) return false;
-        tc_fence_after();
-        if (mine)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                F2 u[4];
-                load_sum8<NT>(u_cols + 8 * i, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (d.keep != 0.f) u[e] = layer::add_(u[e], S[4 * i + e]);
-                    S[4 * i + e] = layer::fma_(m, S[4 * i + e], u[e]);
-                }
-            }
-        tc_fence_before();
-        mbar_arrive(&x->sums_free);
-    }
-    if (mine && p.s_out && t.g.k == (p.reverse ? 0 : t.g.cnt - 1)) {
-        float* out = p.s_out + seq + from;
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i) {
-            float f[2];
-            layer::split(S[i], f);
-            out[2 * i * p.sp] = f[0], out[(2 * i + 1) * p.sp] = f[1];
-        }
-    }
-    return true;
-}
 
 template <int NT>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_walk_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
-    using C = Cols<NT>;
     extern __shared__ __align__(1024) unsigned char sm[];
     Aux* x = reinterpret_cast<Aux*>(sm + geo.aux_at);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -417,13 +341,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             mbar_init(&x->full[s], 1), mbar_init(&x->empty[s], 2);
         }
         for (int s = 0; s < geo.v_stages; ++s) {
-            mbar_init(&x->full_v[s], 1), mbar_init(&x->empty_v[s], 2), mbar_init(&x->weights[s], 128);
+            mbar_init(&x->full_v[s], 1), mbar_init(&x->empty_v[s], 2), mbar_init(&x->weights[s], kTeam);
         }
-        for (int s = 0; s < 2; ++s) mbar_init(&x->scores[s], 1), mbar_init(&x->masked[s], 128);
-        mbar_init(&x->masked_free, 1), mbar_init(&x->state_free, 1), mbar_init(&x->sums, 1);
-        mbar_init(&x->outs, 2);
-        mbar_init(&x->state, 128), mbar_init(&x->outs_free, 128);
-        mbar_init(&x->sums_free, 128);
+        mbar_init(&x->scores, 1), mbar_init(&x->state_free, 1), mbar_init(&x->sums, 1), mbar_init(&x->outs, 2);
+        for (int s = 0; s < 2; ++s) mbar_init(&x->item_full[s], 1), mbar_init(&x->item_empty[s], kTeam + 2);
+        mbar_init(&x->masked, kTeam), mbar_init(&x->state, kTeam), mbar_init(&x->outs_free, kTeam);
         x->stop = 0;
         fence_mbar_init();
     }
@@ -431,245 +353,297 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = x->tmem;
-    int g = 0;  // chunks of this block so far
+    int g = 0;         // chunks of this block so far
+    Place qk, vv, it;  // where the chunk's q and k, its v, and the item are
+    const auto give_back = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x->item_empty[it.s]);
+        it.next(2);
+    };
 
-    if (warp < 4) {
-        // ------------------------------------------------ mask
-        float* diag = x->diag[warp];
-        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
-            const bool rev = t.p->reverse;
-            const float ld2 = t.ld * 1.44269504f;
-            __syncwarp();  // the last item's are no longer read
-            // column e of row `lane` is at 31 - lane + e: from the end a^(e - lane), else a^(lane - e)
-            diag[rev ? lane : lane + 31] = 0.f;
-            __syncwarp();
-            diag[rev ? lane + 31 : 31 - lane] = power(ld2, lane);
-            __syncwarp();
-            F2 far[8];
-            const float* first = rev ? diag + 31 : diag + 16;  // a^0 .. a^15, or a^15 .. a^0
-#pragma unroll
-            for (int e = 0; e < 8; ++e) far[e] = layer::join(first[2 * e], first[2 * e + 1]);
-#pragma unroll 1
-            for (int c = 0; c < t.chunks; ++c, ++g) {
-                int n;
-                chunk_start(t, c, &n);
-                if (!wait_warp(&x->scores[C::at(g)], C::parity(g), &x->stop, status)) goto done;
-                // where the operand has one place: its last reader
-                if (C::kPlaces == 1 && g > 0 && !wait_warp(&x->masked_free, (g - 1) & 1, &x->stop, status)) goto done;
-                tc_fence_after();
-                mask_chunk<NT>(tmem + lane_base, g, n, rev, warp, lane, ld2, diag, far);
-                tc_fence_before();
-                mbar_arrive(&x->masked[C::at(g)]);
-            }
-        }
-    } else if (warp < 8) {
-        // ------------------------------------------------ outputs
+    if (warp < kTeam) {
+        // ------------------------------------------------ the team: row i, a quarter of the columns
         const uint32_t mine = tmem + lane_base;
-        const int i = tid;
-        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
-            const Pass& p = *t.p;
-            const bool rev = p.reverse, f32 = p.out_f32;
-            char* out = static_cast<char*>(p.out);
-            const int oe = f32 ? 4 : 2;
-            const long long col = (long long)(t.h / p.outr) * p.vd + t.v0;
+        const int i = tid, quad = warp & 3, part = warp >> 2;
+        const uint32_t cols = mine + 16 * part;   // a quarter of 64 columns
+        unsigned char* w_tile = sm + geo.w_at;
+        unsigned char* s_tile = sm + geo.s_at;
+        // the scores' groups of 16 columns that are this warp's: one from either end, so that none has
+        // two below the diagonal while another has none
+        const int j0 = 16 * part, j1 = 16 * (7 - part);
+        const auto arrive = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x, give_back()) {
+            if (!wait_warp(&x->item_full[it.s], it.phase, &x->stop, status)) break;
+            const Item& t = x->items[it.s];
             if (a.cu) {  // tokens behind the last sequence
+                const int oe = t.f32 ? 4 : 2;
                 for (long long r = border(a, a.nseq) + t.id; r < a.T; r += a.ids)
-                    if (i < kV * oe / 16)
-                        *reinterpret_cast<uint4*>(out + (r * p.os + col) * oe + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < oe)
+                        *reinterpret_cast<uint4*>(t.out + (r - t.g.start) * t.os + 16 * part * oe + i * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
             }
-            if (t.chunks == 0) continue;
-            const float ld2 = t.ld * 1.44269504f;
-            const F2 fi = layer::both<F2>(p.si);
-            const float fx_whole = power(ld2, rev ? kQ - 1 - i : i + 1) * p.sx;
-            const bool wide = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(p.os * oe)) & 31) == 0;
-#pragma unroll 1
-            for (int c = 0; c < t.chunks; ++c, ++g) {
-                int n;
-                const long long t0 = chunk_start(t, c, &n);
-                const F2 fx = layer::both<F2>(n == kQ || !rev ? fx_whole : power(ld2, max(n - 1 - i, 0)) * p.sx);
-                char* row = out + ((t0 + i) * p.os + col) * oe;
-                if (!wait_warp(&x->outs, g & 1, &x->stop, status)) goto done;
-                tc_fence_after();
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h, row += 32 * oe) {
-                    uint32_t o1[32], o2[32];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        tmem_ld16(mine + C::o1 + 32 * h + e, *reinterpret_cast<uint32_t(*)[16]>(o1 + e));
-                        tmem_ld16(mine + C::o2 + 32 * h + e, *reinterpret_cast<uint32_t(*)[16]>(o2 + e));
-                    }
-                    tmem_wait_ld_regs<32>(o1);
-                    tmem_wait_ld_regs<32>(o2);
-                    if (h == 1) {
-                        tc_fence_before();
-                        mbar_arrive(&x->outs_free);
-                    }
-                    F2 v[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e] = layer::fma_(fx, pair(o2[2 * e], o2[2 * e + 1]), layer::mul_(fi, pair(o1[2 * e], o1[2 * e + 1])));
-                    if (i < n) {
-                        if (f32) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float f[2];
-                                layer::split(v[e], f);
-                                o1[2 * e] = __float_as_uint(f[0]), o1[2 * e + 1] = __float_as_uint(f[1]);
-                            }
-                            store8(row + 64, o1 + 16, wide);
-                            store8(row + 96, o1 + 24, wide);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o1[e] = pack(v[e]);
-                        }
-                        store8(row, o1, wide);
-                        store8(row + 32, o1 + 8, wide);
-                    }
-                }
-            }
-        }
-    } else if (warp < 12) {
-        // ------------------------------------------------ state
-        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
             if (!t.g.there) continue;
-            if (!state_item<NT>(a, t, x, sm + geo.s_at, tmem + lane_base + C::u, tid, g, status)) goto done;
-        }
-    } else if (warp < 16) {
-        // ------------------------------------------------ weights
-        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
-            const Pass& p = *t.p;
-            const float ld2 = t.ld * 1.44269504f;
-            const float whole = power(ld2, p.reverse ? tid + 1 : kQ - 1 - tid) * p.su;
-#pragma unroll 1
-            for (int c = 0; c < t.chunks; ++c, ++g) {
-                int n;
-                chunk_start(t, c, &n);
-                const int s = g % geo.v_stages;
-                unsigned char* v = sm + geo.v_at + s * kSub;
-                if (!wait_warp(&x->full_v[s], (g / geo.v_stages) & 1, &x->stop, status)) goto done;
-                // the product before has read the last weights
-                if (g > 0 && !wait_warp(&x->sums, (g - 1) & 1, &x->stop, status)) goto done;
-                const bool in = tid < n;
-                const float w = n == kQ || p.reverse ? whole : power(ld2, max(n - 1 - tid, 0)) * p.su;
-                split_row<NT>(v, sm + geo.w_at, tid, w, in);
-                if (n < kQ) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
-                    const int k = g % geo.stages;
-                    if (!wait_warp(&x->full[k], (g / geo.stages) & 1, &x->stop, status)) goto done;
-                    if (!in) {
-                        zero_row(v, tid);
-                        for (int b = 0; b < p.kd / 64; ++b)
-                            zero_row(sm + k * geo.stage_bytes + kbytes + b * kSub, tid);
-                    }
+            const bool state_row = i < t.p->kd;  // 64 channels leave half of the lanes out; whole warps
+            // this thread's part of the state of sequence or segment `row`, columns t.p->sp apart
+            const auto state_at = [&](long long row) {
+                return ((row * a.H + t.h) * t.p->kd) * t.p->vd + (t.v0 + 16 * part) * t.p->sp + i * t.p->sn;
+            };
+            {
+                const float* in = t.p->s_seg  ? t.p->s_seg + state_at(t.id)
+                                  : t.p->s_in ? t.p->s_in + state_at(t.g.seq)
+                                              : nullptr;
+                const long long sp = t.p->sp;
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = in && state_row ? __float_as_uint(in[e * sp]) : 0u;
+                tmem_st16(cols + C::state, w);
+                tmem_wait_st();
+            }
+            const int rev = t.rev, chunks = t.chunks;
+            const bool some0 = rev ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31;
+            const bool some1 = rev ? j1 + 15 >= 32 * quad : j1 <= 32 * quad + 31;
+            const float fx_whole = power(t.ld2, rev ? kQ - 1 - i : i + 1) * t.sx;
+            const float w_whole = power(t.ld2, rev ? i + 1 : kQ - 1 - i) * t.su;
+
+            // S as bf16 for q S of chunk k, once the one before has read the tile
+            const auto give_state = [&](int k) {
+                if (k > 0 && !wait_warp(&x->state_free, (k - 1) & 1, &x->stop, status)) return false;
+                uint32_t w[16];
+                tmem_ld16(cols + C::state, w);
+                tmem_wait_ld_regs<16>(w);
+                if (state_row) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = pack(pair(w[2 * e], w[2 * e + 1]));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint4*>(s_tile + i * 128 + (((2 * part + e) ^ (i & 7)) << 4)) =
+                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                 }
                 fence_proxy_async();
-                mbar_arrive(&x->weights[s]);
+                arrive(&x->state);
+                return true;
+            };
+#pragma unroll 1
+            for (int c = -1; c < chunks; ++c) {
+                const int k = g + c;  // of all the block's chunks
+                const int n = c == t.short_one ? t.g.len - (chunks - 1) * kQ : kQ;
+                if (c >= 0) {
+                    // ---- mask
+                    if (!wait_warp(&x->scores, k & 1, &x->stop, status)) goto done;
+                    tc_fence_after();
+                    // times a^distance, or 0 on the other side of the diagonal
+                    const float* f = x->powers[it.s] + kBelow + (rev ? -i : i);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = u ? j1 : j0;
+                        const float* at = f + (rev ? j : -j);
+                        uint32_t s[16];
+                        if (u ? some1 : some0) {
+                            tmem_ld16(mine + C::scores + j, s);
+                            tmem_wait_ld_regs<16>(s);
+                            if (n < kQ) {  // tokens of other sequences, an infinity or a NaN maybe
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (j + e >= n) s[e] = 0u;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const F2 p = rev ? layer::join(at[2 * e], at[2 * e + 1]) : layer::join(at[-2 * e], at[-2 * e - 1]);
+                                s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), p));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) s[e] = 0u;
+                        }
+                        tmem_st8(mine + C::masked + j / 2, s);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(&x->masked);
+                    // ---- state
+                    if (!wait_warp(&x->sums, k & 1, &x->stop, status)) goto done;
+                    tc_fence_after();
+                    {
+                        const Decay& d = c == t.short_one ? t.last : t.whole;
+                        const F2 m = layer::both<F2>(d.m), keep = layer::both<F2>(d.keep);
+#pragma unroll
+                        for (int h = 0; h < 16; h += 8) {
+                            uint32_t w[8];
+                            F2 add[4];
+                            tmem_ld8(cols + C::state + h, w);
+                            load_sum8(cols + C::u + h, add);
+                            reg_dep8(w);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const F2 old = pair(w[2 * e], w[2 * e + 1]);
+                                float f[2];
+                                layer::split(layer::fma_(m, old, layer::fma_(keep, old, add[e])), f);
+                                w[2 * e] = __float_as_uint(f[0]), w[2 * e + 1] = __float_as_uint(f[1]);
+                            }
+                            tmem_st8(cols + C::state + h, w);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                }
+                if (c + 1 < chunks) {
+                    // ---- the next chunk's weights: the sums' product before has read the last ones
+                    const int m = c + 1 == t.short_one ? t.g.len - (chunks - 1) * kQ : kQ;
+                    unsigned char* v = sm + geo.v_at + vv.s * kSub;
+                    if (!wait_warp(&x->full_v[vv.s], vv.phase, &x->stop, status)) goto done;
+                    const bool in = i < m;
+                    const float w = m == kQ || rev ? w_whole : power(t.ld2, max(m - 1 - i, 0)) * t.su;
+                    split_row<NT>(v, w_tile, i, 2 * part, 2, w, in);
+                    if (m < kQ) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
+                        if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status)) goto done;
+                        if (!in && part <= t.kb) zero_row(part ? sm + qk.s * geo.stage_bytes + kbytes + (part - 1) * kSub : v, i);
+                    }
+                    fence_proxy_async();
+                    arrive(&x->weights[vv.s]);
+                    qk.next(geo.stages), vv.next(geo.v_stages);
+                    if (!give_state(k + 1)) goto done;
+                }
+                if (c >= 0) {
+                    // ---- outputs
+                    const F2 fx = layer::both<F2>(n == kQ || !rev ? fx_whole : power(t.ld2, max(n - 1 - i, 0)) * t.sx);
+                    if (!wait_warp(&x->outs, k & 1, &x->stop, status)) goto done;
+                    tc_fence_after();
+                    uint32_t o1[16], o2[16];
+                    tmem_ld16(cols + C::o1, o1);
+                    tmem_ld16(cols + C::o2, o2);
+                    tmem_wait_ld_regs<16>(o1);
+                    reg_dep16(o2);
+                    tc_fence_before();
+                    arrive(&x->outs_free);
+                    if (i < n) {
+                        const int oe = t.f32 ? 4 : 2;
+                        char* row = t.out + (long long)((rev ? chunks - 1 - c : c) * kQ + i) * t.os + 16 * part * oe;
+                        const bool wide = ((reinterpret_cast<uintptr_t>(t.out) | (uintptr_t)t.os) & 31) == 0;
+                        const F2 fi = layer::both<F2>(t.si);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const F2 v = layer::fma_(fx, pair(o2[2 * e], o2[2 * e + 1]),
+                                                     layer::mul_(fi, pair(o1[2 * e], o1[2 * e + 1])));
+                            float f[2];
+                            layer::split(v, f);
+                            o1[2 * e] = __float_as_uint(f[0]), o1[2 * e + 1] = __float_as_uint(f[1]);
+                            o2[e] = pack(v);
+                        }
+                        if (t.f32) {
+                            store8(row, o1, wide);
+                            store8(row + 32, o1 + 8, wide);
+                        } else {
+                            store8(row, o2, wide);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            g += chunks;
+            if (t.p->s_out && t.g.k == (rev ? 0 : t.g.cnt - 1) && state_row) {
+                float* final = t.p->s_out + state_at(t.g.seq);
+                const long long sp = t.p->sp;
+                uint32_t w[16];
+                tmem_ld16(cols + C::state, w);
+                tmem_wait_ld_regs<16>(w);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) final[e * sp] = __uint_as_float(w[e]);
             }
         }
     } else if (warp == 16) {
-        // ------------------------------------------------ copies in
-        if (lane == 0) {
-            int issued = 0;
-            for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
-                Item t;
-                take(a, geo.by_pass, item, &t);
+        // ------------------------------------------------ items, their powers, and copies in
+        int issued = 0;
+        for (int item = blockIdx.x, m = 0; item < geo.items; item += gridDim.x, ++m, it.next(2)) {
+            if (m >= 2 && !wait_warp(&x->item_empty[it.s], it.phase ^ 1u, &x->stop, status)) break;
+            Item& t = x->items[it.s];
+            if (lane == 0) take(a, geo.by_pass, item, &t);
+            __syncwarp();
+            for (int d = lane - kBelow - 1; d < kQ; d += 32)
+                if (d >= -kBelow) x->powers[it.s][d + kBelow] = d < 0 ? 0.f : power(t.ld2, d);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&x->item_full[it.s]);
                 const Tiles tiles(maps, t);
-                for (int c = 0; c < t.chunks; ++c, ++g) {
-                    int n;
-                    const int t0 = (int)chunk_start(t, c, &n), s = g % geo.stages, vs = g % geo.v_stages;
-                    if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    tiles.load_qk<true>(t0, sm + s * geo.stage_bytes, kbytes, &x->full[s]);
+                const Chunks ch(t);
+                for (int c = 0; c < ch.chunks; ++c, ++g, qk.next(geo.stages), vv.next(geo.v_stages)) {
+                    const int t0 = (int)ch.start + ch.first(c);
+                    // a place's phase of being given back is one behind that of being filled
+                    if (g >= geo.stages && !wait(&x->empty[qk.s], qk.phase ^ 1u, &x->stop, status)) break;
+                    tiles.load_qk<true>(t0, sm + qk.s * geo.stage_bytes, kbytes, &x->full[qk.s]);
                     ++issued;
-                    if (g >= geo.v_stages && !wait(&x->empty_v[vs], (g / geo.v_stages - 1) & 1, &x->stop, status)) break;
-                    tiles.load_v(t0, sm + geo.v_at + vs * kSub, &x->full_v[vs]);
+                    if (g >= geo.v_stages && !wait(&x->empty_v[vv.s], vv.phase ^ 1u, &x->stop, status)) break;
+                    tiles.load_v(t0, sm + geo.v_at + vv.s * kSub, &x->full_v[vv.s]);
                 }
             }
-            // after a wait that ran out: copies on their way must not land in the next block's memory
-            if (*(volatile int*)&x->stop) {
-                for (int k = max(0, issued - geo.stages); k < issued; ++k)
-                    drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
-                for (int k = max(0, g - geo.v_stages); k < g; ++k)
-                    drain(&x->full_v[k % geo.v_stages], (k / geo.v_stages) & 1);
-            }
+            if (__any_sync(0xffffffffu, *(volatile int*)&x->stop)) break;
+        }
+        // after a wait that ran out: copies on their way must not land in the next block's memory
+        if (lane == 0 && *(volatile int*)&x->stop) {
+            for (int k = max(0, issued - geo.stages); k < issued; ++k)
+                drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
+            for (int k = max(0, g - geo.v_stages); k < g; ++k)
+                drain(&x->full_v[k % geo.v_stages], (k / geo.v_stages) & 1);
         }
         __syncwarp();
     } else if (warp == 17) {
         // ------------------------------------------------ products: scores, and the masked ones with v
         const uint32_t id_a = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kV, 0, 1);
         const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
-        int item = blockIdx.x - gridDim.x, left = 0, kb = 0;
-        for (bool more = true; more; ++g) {
-            while (left == 0 && more) {
-                item += gridDim.x;
-                more = item < geo.items;
-                if (more) {
-                    Item t;
-                    take(a, geo.by_pass, item, &t);
-                    left = same(t.chunks), kb = same(t.p->kd / 64);
-                }
-            }
-            if (more) {
-                const int s = g % geo.stages;
-                // with one place for the scores, those before have been read
-                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
-                    (C::kPlaces == 1 && g > 0 && !wait_warp(&x->masked[0], (g - 1) & 1, &x->stop, status)))
-                    break;
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x, give_back()) {
+            if (!wait_warp(&x->item_full[it.s], it.phase, &x->stop, status)) break;
+            const Item& t = x->items[it.s];
+            const int kb = same(t.kb), chunks = same(t.chunks);
+            for (int c = 0; c < chunks; ++c, ++g, qk.next(geo.stages), vv.next(geo.v_stages)) {
+                // the scores before have been read: their mask was waited for
+                if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status)) goto stopped_a;
                 tc_fence_after();
                 if (elect_one()) {
-                    uint64_t qd = sw128_desc(base + s * geo.stage_bytes, 16, 1024), kd = moved(qd, kbytes);
+                    uint64_t qd = sw128_desc(base + qk.s * geo.stage_bytes, 16, 1024), kd = moved(qd, kbytes);
 #pragma unroll 1
                     for (int b = 0; b < kb; ++b, qd = moved(qd, kSub), kd = moved(kd, kSub))
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16(tm + C::scores(g), moved(qd, i * 32), moved(kd, i * 32), id_a, b + i > 0);
-                    mma_commit(&x->scores[C::at(g)]);
-                    mma_commit(&x->empty[s]);
+                            mma_bf16(tm + C::scores, moved(qd, i * 32), moved(kd, i * 32), id_a, b + i > 0);
+                    mma_commit(&x->scores);
+                    mma_commit(&x->empty[qk.s]);
                 }
-                --left;
-            }
-            if (g > 0) {  // the masked product of the chunk before, whose mask this one's scores went ahead of
-                const int k = g - 1, s = k % geo.v_stages;
                 // with the weights v's rows behind the sequence's end are zero
-                if (!wait_warp(&x->masked[C::at(k)], C::parity(k), &x->stop, status) ||
-                    !wait_warp(&x->weights[s], (k / geo.v_stages) & 1, &x->stop, status) ||
-                    (k > 0 && !wait_warp(&x->outs_free, (k - 1) & 1, &x->stop, status)))
-                    break;
+                if (!wait_warp(&x->masked, g & 1, &x->stop, status) ||
+                    !wait_warp(&x->weights[vv.s], vv.phase, &x->stop, status) ||
+                    (g > 0 && !wait_warp(&x->outs_free, (g - 1) & 1, &x->stop, status)))
+                    goto stopped_a;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t vd = sw128_desc(base + geo.v_at + s * kSub, 16, 1024);
+                    const uint64_t vd = sw128_desc(base + geo.v_at + vv.s * kSub, 16, 1024);
 #pragma unroll
                     for (int i = 0; i < kQ / 16; ++i)
-                        mma_bf16_ta(tm + C::o1, tm + C::masked(k) + 8 * i, moved(vd, i * 2048), id_o, i > 0);
+                        mma_bf16_ta(tm + C::o1, tm + C::masked + 8 * i, moved(vd, i * 2048), id_o, i > 0);
                     mma_commit(&x->outs);
-                    if (C::kPlaces == 1) mma_commit(&x->masked_free);
-                    mma_commit(&x->empty_v[s]);
+                    mma_commit(&x->empty_v[vv.s]);
                 }
             }
         }
+    stopped_a:
         if (*(volatile int*)&x->stop) {  // what was issued must end before the columns are given back
-            if (elect_one()) mma_commit(&x->scores[0]);
-            for (int k = 0; k < 2; ++k) drain(&x->scores[0], k);
+            if (elect_one()) mma_commit(&x->scores);
+            for (int k = 0; k < 2; ++k) drain(&x->scores, k);
         }
     } else {
         // ------------------------------------------------ products: the sums, and q with the state
         const uint32_t id_o = idesc_bf16(128, kV, 0, 1);
         const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
-        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
-            const int kb = same(t.p->kd / 64), chunks = same(t.chunks);
-            for (int c = 0; c < chunks; ++c, ++g) {
-                const int s = g % geo.stages, vs = g % geo.v_stages;
-                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status) ||
-                    !wait_warp(&x->weights[vs], (g / geo.v_stages) & 1, &x->stop, status) ||
-                    (g > 0 && !wait_warp(&x->sums_free, (g - 1) & 1, &x->stop, status)))
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x, give_back()) {
+            if (!wait_warp(&x->item_full[it.s], it.phase, &x->stop, status)) break;
+            const Item& t = x->items[it.s];
+            const int kb = same(t.kb), chunks = same(t.chunks);
+            for (int c = 0; c < chunks; ++c, ++g, qk.next(geo.stages), vv.next(geo.v_stages)) {
+                const int s = qk.s, vs = vv.s;
+                // weights come after the last sums have been read
+                if (!wait_warp(&x->full[s], qk.phase, &x->stop, status) ||
+                    !wait_warp(&x->weights[vs], vv.phase, &x->stop, status))
                     goto stopped;
                 tc_fence_after();
                 if (elect_one()) {
@@ -717,7 +691,7 @@ template <int NT>
 __global__ void __launch_bounds__(kSumThreads, 1)
     tc_sums_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
     extern __shared__ __align__(1024) unsigned char sm[];
-    Aux* x = reinterpret_cast<Aux*>(sm + geo.aux_at);
+    SumsAux* x = reinterpret_cast<SumsAux*>(sm + geo.aux_at);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const int kbytes = geo.kblocks * kSub;
@@ -730,19 +704,21 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         x->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(&x->tmem, 256);
+    if (warp == 5) tmem_alloc(&x->tmem, 128);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = x->tmem;
+    Item& t = x->items[warp];
     int g = 0, m = 0;  // chunks and items of this block so far
-    const auto wanted = [&](const Item& t) {  // nothing comes after a walk's last segment
+    const auto wanted = [](const Item& t) {  // nothing comes after a walk's last segment
         return t.g.there && t.g.k != (t.p->reverse ? 0 : t.g.cnt - 1);
     };
     // two sets of weights: one chunk's are made while the other's are read
     if (warp < 4) {
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            Item t;
-            take(a, geo.by_pass, item, &t);
+            __syncwarp();
+            if (lane == 0) take(a, geo.by_pass, item, &t);
+            __syncwarp();
             if (!wanted(t)) continue;
             const Pass& p = *t.p;
             const float ld2 = t.ld * 1.44269504f;
@@ -755,7 +731,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
                     goto done;
                 const bool in = at < t.g.len;
                 const float w = in ? power(ld2, p.reverse ? at + 1 : t.g.len - 1 - at) * p.su : 0.f;
-                split_row<NT>(st + kbytes, sm + geo.w_at + (g & 1) * NT * kSub, tid, w, in);
+                split_row<NT>(st + kbytes, sm + geo.w_at + (g & 1) * NT * kSub, tid, 0, 8, w, in);
                 if (!in)
                     for (int b = 0; b < p.kd / 64; ++b) zero_row(st + b * kSub, tid);
                 fence_proxy_async();
@@ -768,7 +744,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 #pragma unroll 1
                 for (int i = 0; i < kV; i += 8) {
                     F2 u[4];
-                    load_sum8<NT>(tmem + lane_base + i, u);
+                    load_sum8(tmem + lane_base + i, u);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float f[2];
@@ -784,7 +760,6 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     } else if (warp == 4) {
         if (lane == 0) {
             for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
-                Item t;
                 take(a, geo.by_pass, item, &t);
                 if (!wanted(t)) continue;
                 const Tiles tiles(maps, t);
@@ -805,7 +780,6 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         if (lane == 0) {
             bool stop = false;
             for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                Item t;
                 take(a, geo.by_pass, item, &t);
                 if (!wanted(t)) continue;
                 if (m > 0 && !wait(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
@@ -834,7 +808,7 @@ done:
     __syncthreads();
     if (warp == 5) {
         tmem_relinquish();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 128);
     }
 }
 
@@ -943,10 +917,10 @@ cudaError_t tc_sums(const WalkArgs& a, Launch& L) {
     geo.items = (int)(a.ids * a.H * a.tiles);  // the caller has seen to it that these fit
     geo.stage_bytes = (geo.kblocks + 1) * kSub;
     const int w = 2 * (three ? 3 : 2) * kSub;
-    geo.stages = std::min(kMostStages, (kMostSmem - w - (int)sizeof(Aux)) / geo.stage_bytes);
+    geo.stages = std::min(kMostStages, (kMostSmem - w - (int)sizeof(SumsAux)) / geo.stage_bytes);
     geo.w_at = geo.stages * geo.stage_bytes;
     geo.s_at = geo.aux_at = geo.w_at + w;
-    const size_t smem = (size_t)geo.aux_at + sizeof(Aux);
+    const size_t smem = (size_t)geo.aux_at + sizeof(SumsAux);
     L.begin("linattn_tc_sums");
     const cudaError_t e = three ? launch(tc_sums_kernel<3>, a, m, geo, kSumThreads, smem, L.stream)
                                 : launch(tc_sums_kernel<2>, a, m, geo, kSumThreads, smem, L.stream);
