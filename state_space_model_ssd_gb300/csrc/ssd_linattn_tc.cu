@@ -16,9 +16,9 @@
 // tokens below the diagonal, so that nothing overflows.
 //
 // One block an SM: sixteen warps that all go through the same steps of a chunk (mask, state, the next
-// chunk's weights, outputs), each on its 32 rows and a quarter of the columns, one warp for the copies
-// in (TMA, two or three chunks ahead), and two that issue products: A and O1 in one, U and O2 in the
-// other.  While the warps are at one step, the products of the steps before run.  Warps with a task
+// chunk's weights, outputs), each on its 32 rows and a quarter of the columns, a warp for the copies
+// in (TMA, two or three chunks ahead), and one for those out, and two that issue products: A and O1 in one, U and O2 in
+// the other.  While the warps are at one step, the products of the steps before run.  Warps with a task
 // each (mask, state, weights, outputs side by side) were 1.3 to 1.5 times slower: four streams of
 // instructions that each go straight through a few hundred of them leave the instruction caches
 // nothing to share (a third of the stalls), while here sixteen warps follow one another.
@@ -42,14 +42,14 @@ using tcc::pack_bf16;
 constexpr int kQ = kTcChunk;                 // 128 tokens
 constexpr int kV = kTcTile;                  // 64 columns
 constexpr int kSub = kQ * 128;               // bytes of a tile of 64 channels: rows of 128 bytes
-constexpr int kWalkThreads = 19 * 32;
+constexpr int kWalkThreads = 20 * 32;
 constexpr int kSumThreads = 6 * 32;
 constexpr int kTeam = 16;                    // warps that work on the numbers
 constexpr int kMostStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 struct Maps {
-    CUtensorMap m[3][3];  // of each pass: q, k, v
+    CUtensorMap m[3][4];  // of each pass: q, k, v, and out where it is bf16
 };
 struct Geometry {
     int stages, v_stages;   // chunks of q and k, and of v, in shared memory at a time
@@ -107,11 +107,13 @@ __device__ __noinline__ void take(const WalkArgs& a, int by_pass, int item, Item
 // Barriers and what else is small, behind the tiles.
 constexpr int kBelow = 31;  // zeros before a^0
 struct Aux {
-    uint64_t full[kMostStages], empty[kMostStages], full_v[kMostStages], empty_v[kMostStages], weights[kMostStages];
-    uint64_t scores, masked, state, state_free, outs, outs_free, sums, item_full[2], item_empty[2];
+    uint64_t full[kMostStages], empty[kMostStages], full_v[kMostStages], empty_v[kMostStages], weights[kMostStages],
+        outputs[kMostStages];
+    uint64_t scores, masked, outs, outs_free, sums, item_full[2], item_empty[2];
     uint32_t tmem;
     int stop;
-    // the item the block works on and the next, and the powers of their heads: 0 for -kBelow .. -1,
+    // the item the block works on and the next, and the powers of their heads by column minus row, in
+    // the order of the columns: a^127 .. a^0 and kBelow zeros, or, in a walk from the end, the zeros and
     // a^0 .. a^127; made by the warp that copies in
     Item items[2];
     float powers[2][kBelow + kQ];
@@ -150,6 +152,22 @@ __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
 // wait() for a whole warp, whose lanes go on or stop together.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
     return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
+}
+
+// A look at a barrier ahead of its wait: the answer comes while other work goes on.
+__device__ __forceinline__ bool peek(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_peeked(bool seen, uint64_t* bar, uint32_t parity, volatile int* stop, int* status) {
+    return __all_sync(0xffffffffu, seen) || __all_sync(0xffffffffu, wait_long(bar, parity, stop, status));
 }
 
 // One thread of a warp that is together.  The products' warps go through their loops as warps, on
@@ -207,7 +225,7 @@ __device__ __forceinline__ void split_row(const unsigned char* v, unsigned char*
                                           float w, bool in) {
     const uint32_t base = row * 128, x = row & 7;
     const F2 ww = layer::both<F2>(w);
-#pragma unroll 1
+#pragma unroll 2
     for (int c = first; c < first + pieces; ++c) {
         const uint32_t at = base + ((c ^ x) << 4);
         uint4 raw = *reinterpret_cast<const uint4*>(v + at);
@@ -271,9 +289,8 @@ struct Chunks {
     bool rev;
     __device__ __forceinline__ explicit Chunks(const Item& t)
         : start(t.g.start), len(t.g.len), chunks(t.chunks), rev(t.p->reverse) {}
-    // the walk's c-th chunk: its first token in the segment, how many it has
+    // the first token of the walk's c-th chunk, in the segment
     __device__ __forceinline__ int first(int c) const { return (rev ? chunks - 1 - c : c) * kQ; }
-    __device__ __forceinline__ int tokens(int c) const { return min(kQ, len - first(c)); }
 };
 
 // A place in a ring of barriers and the parity of its phase.
@@ -320,10 +337,11 @@ __device__ __forceinline__ void store8(char* at, const uint32_t* w, bool wide) {
 }
 
 // ---------------------------------------------------------------- the walk
-// Columns of TMEM: the scores, the masked operand, the two parts of the outputs, the state, the sums.
+// Columns of TMEM: the scores, the masked operand, the two parts of the outputs (that from the state
+// in two places, so that chunk k's need not wait for the last outputs to be read), the sums.
 struct C {
-    static constexpr uint32_t scores = 0, masked = 128, o1 = 192, o2 = o1 + kV, state = o2 + kV, u = state + kV;
-    static_assert(u + 2 * kV <= 512, "TMEM");
+    static constexpr uint32_t scores = 0, masked = 128, o1 = 192, u = 384;
+    static constexpr uint32_t o2(int k) { return 256 + (k & 1) * kV; }
 };
 
 template <int NT>
@@ -341,11 +359,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             mbar_init(&x->full[s], 1), mbar_init(&x->empty[s], 2);
         }
         for (int s = 0; s < geo.v_stages; ++s) {
-            mbar_init(&x->full_v[s], 1), mbar_init(&x->empty_v[s], 2), mbar_init(&x->weights[s], kTeam);
+            mbar_init(&x->full_v[s], 1), mbar_init(&x->empty_v[s], 1);
+            mbar_init(&x->weights[s], kTeam), mbar_init(&x->outputs[s], kTeam);
         }
-        mbar_init(&x->scores, 1), mbar_init(&x->state_free, 1), mbar_init(&x->sums, 1), mbar_init(&x->outs, 2);
-        for (int s = 0; s < 2; ++s) mbar_init(&x->item_full[s], 1), mbar_init(&x->item_empty[s], kTeam + 2);
-        mbar_init(&x->masked, kTeam), mbar_init(&x->state, kTeam), mbar_init(&x->outs_free, kTeam);
+        mbar_init(&x->scores, 1), mbar_init(&x->sums, 1), mbar_init(&x->outs, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&x->item_full[s], 1), mbar_init(&x->item_empty[s], kTeam + 3);
+        mbar_init(&x->masked, kTeam), mbar_init(&x->outs_free, kTeam);
         x->stop = 0;
         fence_mbar_init();
     }
@@ -355,6 +374,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const uint32_t tmem = x->tmem;
     int g = 0;         // chunks of this block so far
     Place qk, vv, it;  // where the chunk's q and k, its v, and the item are
+    Place done_v;      // where the v of the chunk is whose outputs are next
     const auto give_back = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(&x->item_empty[it.s]);
@@ -391,16 +411,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const auto state_at = [&](long long row) {
                 return ((row * a.H + t.h) * t.p->kd) * t.p->vd + (t.v0 + 16 * part) * t.p->sp + i * t.p->sn;
             };
+            F2 S[8];
             {
                 const float* in = t.p->s_seg  ? t.p->s_seg + state_at(t.id)
                                   : t.p->s_in ? t.p->s_in + state_at(t.g.seq)
                                               : nullptr;
                 const long long sp = t.p->sp;
-                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = in && state_row ? __float_as_uint(in[e * sp]) : 0u;
-                tmem_st16(cols + C::state, w);
-                tmem_wait_st();
+                for (int e = 0; e < 8; ++e)
+                    S[e] = in && state_row ? layer::join(in[2 * e * sp], in[(2 * e + 1) * sp]) : layer::join(0.f, 0.f);
             }
             const int rev = t.rev, chunks = t.chunks;
             const bool some0 = rev ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31;
@@ -408,38 +427,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const float fx_whole = power(t.ld2, rev ? kQ - 1 - i : i + 1) * t.sx;
             const float w_whole = power(t.ld2, rev ? i + 1 : kQ - 1 - i) * t.su;
 
-            // S as bf16 for q S of chunk k, once the one before has read the tile
-            const auto give_state = [&](int k) {
-                if (k > 0 && !wait_warp(&x->state_free, (k - 1) & 1, &x->stop, status)) return false;
-                uint32_t w[16];
-                tmem_ld16(cols + C::state, w);
-                tmem_wait_ld_regs<16>(w);
-                if (state_row) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = pack(pair(w[2 * e], w[2 * e + 1]));
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<uint4*>(s_tile + i * 128 + (((2 * part + e) ^ (i & 7)) << 4)) =
-                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                }
-                fence_proxy_async();
-                arrive(&x->state);
-                return true;
-            };
+            const int short_one = t.short_one, short_n = t.g.len - (chunks - 1) * kQ;
+            bool seen = false;  // what the last look at the barrier of the next wait said
 #pragma unroll 1
             for (int c = -1; c < chunks; ++c) {
                 const int k = g + c;  // of all the block's chunks
-                const int n = c == t.short_one ? t.g.len - (chunks - 1) * kQ : kQ;
+                const int n = c == short_one ? short_n : kQ;
                 if (c >= 0) {
                     // ---- mask
-                    if (!wait_warp(&x->scores, k & 1, &x->stop, status)) goto done;
+                    if (!wait_peeked(seen, &x->scores, k & 1, &x->stop, status)) goto done;
                     tc_fence_after();
                     // times a^distance, or 0 on the other side of the diagonal
-                    const float* f = x->powers[it.s] + kBelow + (rev ? -i : i);
+                    const float* f = x->powers[it.s] + (rev ? kBelow : kQ - 1) - i;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = u ? j1 : j0;
-                        const float* at = f + (rev ? j : -j);
+                        const float* at = f + j;
                         uint32_t s[16];
                         if (u ? some1 : some0) {
                             tmem_ld16(mine + C::scores + j, s);
@@ -450,53 +453,52 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                     if (j + e >= n) s[e] = 0u;
                             }
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const F2 p = rev ? layer::join(at[2 * e], at[2 * e + 1]) : layer::join(at[-2 * e], at[-2 * e - 1]);
-                                s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), p));
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(at[2 * e], at[2 * e + 1])));
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) s[e] = 0u;
                         }
                         tmem_st8(mine + C::masked + j / 2, s);
                     }
+                    seen = peek(&x->sums, k & 1);
                     tmem_wait_st();
                     tc_fence_before();
                     arrive(&x->masked);
                     // ---- state
-                    if (!wait_warp(&x->sums, k & 1, &x->stop, status)) goto done;
+                    if (!wait_peeked(seen, &x->sums, k & 1, &x->stop, status)) goto done;
                     tc_fence_after();
+                    seen = peek(&x->full_v[vv.s], vv.phase);
                     {
-                        const Decay& d = c == t.short_one ? t.last : t.whole;
+                        const Decay& d = c == short_one ? t.last : t.whole;
                         const F2 m = layer::both<F2>(d.m), keep = layer::both<F2>(d.keep);
 #pragma unroll
-                        for (int h = 0; h < 16; h += 8) {
-                            uint32_t w[8];
+                        for (int h = 0; h < 2; ++h) {
                             F2 add[4];
-                            tmem_ld8(cols + C::state + h, w);
-                            load_sum8(cols + C::u + h, add);
-                            reg_dep8(w);
+                            load_sum8(cols + C::u + 8 * h, add);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const F2 old = pair(w[2 * e], w[2 * e + 1]);
-                                float f[2];
-                                layer::split(layer::fma_(m, old, layer::fma_(keep, old, add[e])), f);
-                                w[2 * e] = __float_as_uint(f[0]), w[2 * e + 1] = __float_as_uint(f[1]);
-                            }
-                            tmem_st8(cols + C::state + h, w);
+                            for (int e = 0; e < 4; ++e)
+                                S[4 * h + e] = layer::fma_(m, S[4 * h + e], layer::fma_(keep, S[4 * h + e], add[e]));
                         }
-                        tmem_wait_st();
                     }
                     tc_fence_before();
                 }
                 if (c + 1 < chunks) {
-                    // ---- the next chunk's weights: the sums' product before has read the last ones
-                    const int m = c + 1 == t.short_one ? t.g.len - (chunks - 1) * kQ : kQ;
+                    // ---- for the next chunk: S as bf16 and the weights; q S and the sums before, which came
+                    // with one another, have read the last ones
+                    if (state_row) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint4*>(s_tile + i * 128 + (((2 * part + e) ^ (i & 7)) << 4)) =
+                                make_uint4(pack(S[4 * e]), pack(S[4 * e + 1]), pack(S[4 * e + 2]), pack(S[4 * e + 3]));
+                    }
+                    const int m = c + 1 == short_one ? short_n : kQ;
                     unsigned char* v = sm + geo.v_at + vv.s * kSub;
-                    if (!wait_warp(&x->full_v[vv.s], vv.phase, &x->stop, status)) goto done;
+                    if (!wait_peeked(c >= 0 && seen, &x->full_v[vv.s], vv.phase, &x->stop, status)) goto done;
                     const bool in = i < m;
                     const float w = m == kQ || rev ? w_whole : power(t.ld2, max(m - 1 - i, 0)) * t.su;
                     split_row<NT>(v, w_tile, i, 2 * part, 2, w, in);
+                    seen = c >= 0 && peek(&x->outs, k & 1);
                     if (m < kQ) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
                         if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status)) goto done;
                         if (!in && part <= t.kb) zero_row(part ? sm + qk.s * geo.stage_bytes + kbytes + (part - 1) * kSub : v, i);
@@ -504,34 +506,41 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     fence_proxy_async();
                     arrive(&x->weights[vv.s]);
                     qk.next(geo.stages), vv.next(geo.v_stages);
-                    if (!give_state(k + 1)) goto done;
                 }
                 if (c >= 0) {
                     // ---- outputs
                     const F2 fx = layer::both<F2>(n == kQ || !rev ? fx_whole : power(t.ld2, max(n - 1 - i, 0)) * t.sx);
-                    if (!wait_warp(&x->outs, k & 1, &x->stop, status)) goto done;
+                    if (!wait_peeked(c + 1 < chunks && seen, &x->outs, k & 1, &x->stop, status)) goto done;
                     tc_fence_after();
                     uint32_t o1[16], o2[16];
                     tmem_ld16(cols + C::o1, o1);
-                    tmem_ld16(cols + C::o2, o2);
+                    tmem_ld16(cols + C::o2(k), o2);
                     tmem_wait_ld_regs<16>(o1);
                     reg_dep16(o2);
                     tc_fence_before();
                     arrive(&x->outs_free);
-                    if (i < n) {
+                    seen = peek(&x->scores, (k + 1) & 1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const F2 v = layer::fma_(fx, pair(o2[2 * e], o2[2 * e + 1]),
+                                                 layer::mul_(layer::both<F2>(t.si), pair(o1[2 * e], o1[2 * e + 1])));
+                        float f[2];
+                        layer::split(v, f);
+                        o1[2 * e] = __float_as_uint(f[0]), o1[2 * e + 1] = __float_as_uint(f[1]);
+                        o2[e] = pack(v);
+                    }
+                    if (n == kQ && !t.f32) {
+                        // over the chunk's v, which all its products have read
+                        unsigned char* tile = sm + geo.v_at + done_v.s * kSub + i * 128;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint4*>(tile + (((2 * part + e) ^ (i & 7)) << 4)) =
+                                make_uint4(o2[4 * e], o2[4 * e + 1], o2[4 * e + 2], o2[4 * e + 3]);
+                        fence_proxy_async();
+                    } else if (i < n) {
                         const int oe = t.f32 ? 4 : 2;
                         char* row = t.out + (long long)((rev ? chunks - 1 - c : c) * kQ + i) * t.os + 16 * part * oe;
                         const bool wide = ((reinterpret_cast<uintptr_t>(t.out) | (uintptr_t)t.os) & 31) == 0;
-                        const F2 fi = layer::both<F2>(t.si);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const F2 v = layer::fma_(fx, pair(o2[2 * e], o2[2 * e + 1]),
-                                                     layer::mul_(fi, pair(o1[2 * e], o1[2 * e + 1])));
-                            float f[2];
-                            layer::split(v, f);
-                            o1[2 * e] = __float_as_uint(f[0]), o1[2 * e + 1] = __float_as_uint(f[1]);
-                            o2[e] = pack(v);
-                        }
                         if (t.f32) {
                             store8(row, o1, wide);
                             store8(row + 32, o1 + 8, wide);
@@ -539,18 +548,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                             store8(row, o2, wide);
                         }
                     }
-                    __syncwarp();
+                    arrive(&x->outputs[done_v.s]);
+                    done_v.next(geo.v_stages);
                 }
             }
             g += chunks;
             if (t.p->s_out && t.g.k == (rev ? 0 : t.g.cnt - 1) && state_row) {
                 float* final = t.p->s_out + state_at(t.g.seq);
                 const long long sp = t.p->sp;
-                uint32_t w[16];
-                tmem_ld16(cols + C::state, w);
-                tmem_wait_ld_regs<16>(w);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) final[e * sp] = __uint_as_float(w[e]);
+                for (int e = 0; e < 8; ++e) {
+                    float f[2];
+                    layer::split(S[e], f);
+                    final[2 * e * sp] = f[0], final[(2 * e + 1) * sp] = f[1];
+                }
             }
         }
     } else if (warp == 16) {
@@ -561,8 +572,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             Item& t = x->items[it.s];
             if (lane == 0) take(a, geo.by_pass, item, &t);
             __syncwarp();
-            for (int d = lane - kBelow - 1; d < kQ; d += 32)
-                if (d >= -kBelow) x->powers[it.s][d + kBelow] = d < 0 ? 0.f : power(t.ld2, d);
+            for (int e = lane; e < kBelow + kQ; e += 32) {
+                const int d = t.rev ? e - kBelow : kQ - 1 - e;
+                x->powers[it.s][e] = d < 0 ? 0.f : power(t.ld2, d);
+            }
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&x->item_full[it.s]);
@@ -622,7 +635,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     for (int i = 0; i < kQ / 16; ++i)
                         mma_bf16_ta(tm + C::o1, tm + C::masked + 8 * i, moved(vd, i * 2048), id_o, i > 0);
                     mma_commit(&x->outs);
-                    mma_commit(&x->empty_v[vv.s]);
                 }
             }
         }
@@ -631,7 +643,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (elect_one()) mma_commit(&x->scores);
             for (int k = 0; k < 2; ++k) drain(&x->scores, k);
         }
-    } else {
+    } else if (warp == 18) {
         // ------------------------------------------------ products: the sums, and q with the state
         const uint32_t id_o = idesc_bf16(128, kV, 0, 1);
         const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
@@ -641,18 +653,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const int kb = same(t.kb), chunks = same(t.chunks);
             for (int c = 0; c < chunks; ++c, ++g, qk.next(geo.stages), vv.next(geo.v_stages)) {
                 const int s = qk.s, vs = vv.s;
-                // weights come after the last sums have been read
+                // weights come with the state, after the last sums have been read
                 if (!wait_warp(&x->full[s], qk.phase, &x->stop, status) ||
                     !wait_warp(&x->weights[vs], vv.phase, &x->stop, status))
-                    goto stopped;
-                tc_fence_after();
-                if (elect_one()) {
-                    mma_sums<NT>(tm + C::u, base + s * geo.stage_bytes + kbytes, base + geo.w_at, kb, 0u);
-                    mma_commit(&x->sums);
-                    mma_commit(&x->empty_v[vs]);
-                }
-                if (!wait_warp(&x->state, g & 1, &x->stop, status) ||
-                    (g > 0 && !wait_warp(&x->outs_free, (g - 1) & 1, &x->stop, status)))
                     goto stopped;
                 tc_fence_after();
                 if (elect_one()) {
@@ -662,9 +665,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     for (int b = 0; b < kb; ++b, qd = moved(qd, kSub), sd = moved(sd, 8192))
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16(tm + C::o2, moved(qd, i * 32), moved(sd, i * 2048), id_o, b + i > 0);
-                    mma_commit(&x->state_free);
-                    mma_commit(&x->outs);
+                            mma_bf16(tm + C::o2(g), moved(qd, i * 32), moved(sd, i * 2048), id_o, b + i > 0);
+                    mma_sums<NT>(tm + C::u, base + s * geo.stage_bytes + kbytes, base + geo.w_at, kb, 0u);
+                    mma_commit(&x->sums);
                     mma_commit(&x->empty[s]);
                 }
             }
@@ -674,6 +677,30 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (elect_one()) mma_commit(&x->sums);
             for (int k = 0; k < 2; ++k) drain(&x->sums, k);
         }
+    } else {
+        // ------------------------------------------------ copies out, and v given back
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x, give_back()) {
+            if (!wait_warp(&x->item_full[it.s], it.phase, &x->stop, status)) break;
+            const Item& t = x->items[it.s];
+            const Chunks ch(t);
+            const CUtensorMap* map = &maps.m[t.pass][3];
+            const int head = t.h / t.p->outr, v0 = t.v0, short_one = t.g.len == kQ * ch.chunks ? -1 : t.short_one;
+            const bool bulk = !t.f32;
+            for (int c = 0; c < ch.chunks; ++c, vv.next(geo.v_stages)) {
+                if (!wait_warp(&x->outputs[vv.s], vv.phase, &x->stop, status)) goto done;
+                if (lane == 0) {
+                    if (bulk && c != short_one) {
+                        tma_store_3d(map, sm + geo.v_at + vv.s * kSub, v0, head, (int)ch.start + ch.first(c));
+                        tma_store_commit();
+                        tma_store_wait_read<0>();
+                    }
+                    mbar_arrive(&x->empty_v[vv.s]);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) tma_store_wait_all<0>();
+        __syncwarp();
     }
 done:
     __syncthreads();
@@ -831,7 +858,8 @@ bool make_maps(const WalkArgs& a, Maps* m) {
         const Pass& p = a.pass[i];
         if (!make_map(&m->m[i][0], p.q, a.T, a.H / p.qr, p.kd, p.qs) ||
             !make_map(&m->m[i][1], p.k, a.T, a.H / p.kr, p.kd, p.ks) ||
-            !make_map(&m->m[i][2], p.v, a.T, a.H / p.vr, p.vd, p.vs))
+            !make_map(&m->m[i][2], p.v, a.T, a.H / p.vr, p.vd, p.vs) ||
+            (!p.out_f32 && !make_map(&m->m[i][3], p.out, a.T, a.H / p.outr, p.vd, p.os)))
             return false;
     }
     return true;
