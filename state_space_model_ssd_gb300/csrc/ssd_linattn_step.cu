@@ -7,6 +7,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "layer_device.cuh"
 #include "layer_host.cuh"
 
@@ -15,7 +17,7 @@ namespace layer {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPieces = 8;  // of a thread in flight
 
 struct StepArgs {
@@ -33,7 +35,7 @@ struct StepArgs {
 
 // VEC: elements of a piece; N is a multiple of it.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) attn_step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) attn_step_kernel(const StepArgs a) {
     const int row = blockIdx.z, h = blockIdx.y;
     const int slot = a.slots ? a.slots[row] : row;
     const int p0 = blockIdx.x * a.rows, np = min(a.rows, a.P - p0);
@@ -137,9 +139,9 @@ extern "C" ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int
     const int vec = N % 4 == 0 ? 4 : 1;
     a.lanes = 1;
     while (a.lanes < 32 && a.lanes * vec < N) a.lanes *= 2;
-    // rows of the state a block takes: all, halved while the batch leaves SMs with fewer than two
-    // blocks and each thread keeps a piece
-    a.rows = (int)P;
+    // rows of the state a block takes: as many as its threads have in flight at once, halved while the
+    // batch leaves SMs with fewer than two blocks and each thread keeps a piece
+    a.rows = std::min((int)P, std::max(1, kPieces * kThreads / a.lanes));
     while (B * H * ((P + a.rows - 1) / a.rows) < 2LL * sm_count() && a.rows * a.lanes >= 2 * kThreads)
         a.rows = (a.rows + 1) / 2;
     const dim3 grid((unsigned)((P + a.rows - 1) / a.rows), (unsigned)H, (unsigned)B);
