@@ -4,13 +4,13 @@
 // Selection.  A candidate's score is scores_i + x_t - log sum exp x.  Two launches, the second of which
 // starts while the first ends:
 //  * A block takes a slice of one beam's logits, which its threads hold in registers: read once,
-//    bound by those bytes.  It leaves the slice's maximum, the sum of exp(x - maximum), and its
-//    `keep` best logits.  To find them each of the eight warps takes the r-th best of its threads' own
+//    bound by those bytes.  It leaves the slice's maximum rounded up, the sum of exp(x - that), and
+//    its `keep` best logits.  To find them each of the eight warps takes the r-th best of its threads' own
 //    maxima, r = keep / 8 rounded up: at least `keep` elements of the slice reach the lowest of the
 //    eight, and few more do (about 60 of 8192 for 16).  Those are gathered and ranked.
-//  * A block for each batch row adds up the slices' sums in float64, turns the slices' best into
-//    scores in float64, and takes the best in the same way.  Between beams, whose scores differ by
-//    their logarithms' rounding, float64 decides; within a beam the logits do.
+//  * A block for each batch row adds up the slices' sums and turns the slices' best into
+//    scores, both as pairs of floats, and takes the best in the same way.  Between beams, whose scores differ
+//    by their logarithms' rounding, the pairs decide; within a beam the logits do.
 // Ranks are counted (how many others come before), so that nothing depends on an order of arrival.
 // GB300: 64 x 8 x 50277 float32 logits, 16 kept: MEASURE_A us; 1 x 4 x 50277 bf16, 8 kept: MEASURE_B us.
 //
@@ -38,9 +38,60 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ unsigned long long ordered(double x) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+// A number as the sum of two floats, the second at most half a step of the first: 48 bits without the
+// float64 units, of which this GPU has few.  The sums are Knuth's and Dekker's.
+struct Pair {
+    float hi, lo;
+    __device__ __forceinline__ Pair plus(float x) const {
+        const float s = hi + x, b = s - hi;
+        const float rest = (hi - (s - b)) + (x - b) + lo;  // exact but for the last sum
+        const float t = s + rest;
+        return Pair{t, (s - t) + rest};
+    }
+    __device__ __forceinline__ Pair plus(Pair x) const {
+        const Pair r = plus(x.hi);
+        const float t = r.hi + (r.lo + x.lo);
+        return Pair{t, (r.hi - t) + (r.lo + x.lo)};
+    }
+    __device__ __forceinline__ Pair times(Pair x) const {
+        const float p = hi * x.hi, rest = fmaf(hi, x.hi, -p) + (hi * x.lo + lo * x.hi);
+        const float t = p + rest;
+        return Pair{t, (p - t) + rest};
+    }
+    __device__ __forceinline__ unsigned long long key() const {
+        return (unsigned long long)ordered(hi) << 32 | ordered(lo);
+    }
+};
+// e^-n for a whole n >= 0, by the powers of two in n.
+__device__ __forceinline__ Pair exp_minus(float n) {
+    const Pair e[7] = {{0.3678794503211975f, -9.149755619830557e-09f}, {0.1353352814912796f, 1.7453331002670325e-09f}, {0.018315639346837997f, -4.581038048900865e-10f}, {0.000335462624207139f, 3.695373000656144e-12f}, {1.1253517584464134e-07f, -1.1253822674030483e-15f}, {1.2664165777252073e-14f, -2.2815788510487642e-22f}, {1.6038109389511792e-28f, -4.840254038107756e-36f}};
+    if (n > 103.f) return Pair{0.f, 0.f};
+    Pair r{1.f, 0.f};
+    const int k = (int)n;
+#pragma unroll
+    for (int b = 0; b < 7; ++b)
+        if (k >> b & 1) r = r.times(e[b]);
+    return r;
+}
+// log x for x > 0: with x = 2^e f, f within sqrt(2) of 1, and s = (f - 1) / (f + 1),
+// log f = 2 s + 2 s^3 / 3 + 2 s^5 / 5 + ..., the first term as a pair.  Off by a few 1e-10.
+__device__ __forceinline__ Pair log_of(Pair x) {
+    int e = (int)(__float_as_uint(x.hi) >> 23) - 127;
+    float f = __uint_as_float((__float_as_uint(x.hi) & 0x7fffffu) | 0x3f800000u);
+    if (f > 1.41421356f) f *= 0.5f, ++e;
+    const float lo = ldexpf(x.lo, -e);
+    const Pair n = Pair{f - 1.f, 0.f}.plus(lo), d = Pair{f, lo}.plus(1.f);
+    const float s = n.hi / d.hi;
+    const float rest = (fmaf(-s, d.hi, n.hi) + (n.lo - s * d.lo)) / d.hi;
+    const float z = s * s;
+    float p = 2.f / 13.f;
+    p = fmaf(p, z, 2.f / 11.f), p = fmaf(p, z, 2.f / 9.f), p = fmaf(p, z, 2.f / 7.f);
+    p = fmaf(p, z, 2.f / 5.f), p = fmaf(p, z, 2.f / 3.f);
+    // log 2 in a part whose multiples are exact, and the rest
+    return Pair{e * 0.693145751953125f, 0.f}.plus(Pair{2.f * s, 2.f * rest + s * (z * p)}).plus(e * 1.428606765330187e-06f);
 }
 
 struct SelectArgs {
@@ -52,7 +103,7 @@ struct SelectArgs {
     // of slice s of beam row r: best[(r slices + s) keep + i], the logit and its token (-1: none)
     float* best;
     int* best_token;
-    float2* sums;  // the slice's maximum, the sum of exp(x - maximum)
+    float2* sums;  // the slice's maximum rounded up, the sum of exp(x - that)
     long long stride;
     int beams, vocab, keep, slices, pad;
 };
@@ -72,14 +123,9 @@ __device__ __forceinline__ void rank_all(const Key* key, const int* idx, int m, 
 }
 // The largest key of a warp.
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-__device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
-    const uint32_t hi = (uint32_t)(x >> 32), top = warp_max(hi);
-    return (unsigned long long)top << 32 | warp_max(hi == top ? (uint32_t)x : 0u);
-}
 // The r-th largest of a warp's keys (0 where there are fewer).
-template <typename Key>
-__device__ __forceinline__ Key warp_nth(Key x, int r, int lane) {
-    Key best = warp_max(x);
+__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int r, int lane) {
+    uint32_t best = warp_max(x);
     for (int k = 1; k < r; ++k) {  // the first lane that has it gives it up
         const unsigned mine = __ballot_sync(0xffffffffu, x == best);
         if (lane == __ffs(mine) - 1) x = 0;
@@ -89,7 +135,7 @@ __device__ __forceinline__ Key warp_nth(Key x, int r, int lane) {
 }
 
 template <typename T, int E>
-__global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArgs a) {
     constexpr int kList = 2048;  // more candidates than this (equal ones) take the long way
     __shared__ uint32_t lkey[kList];
     __shared__ int lidx[kList];
@@ -102,10 +148,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const SelectArg
     const T* x = static_cast<const T*>(a.logits) + (long long)row * a.stride;
     const int base = slice * kThreads * E, n = min(kThreads * E, a.vocab - base);
     float f[E];
+    x += base + tid;
+    if (n == kThreads * E) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kThreads + tid;
-        f[e] = i < n ? static_cast<float>(x[base + i]) : -INFINITY;
+        for (int e = 0; e < E; ++e) f[e] = static_cast<float>(x[e * kThreads]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = e * kThreads + tid < n ? static_cast<float>(x[e * kThreads]) : -INFINITY;
     }
     float top = f[0];
 #pragma unroll
@@ -115,23 +164,34 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const SelectArg
     if (tid == 0) count = 0;
     if (lane == 0) top_key[warp] = best, nth_key[warp] = nth;
     __syncthreads();
-    uint32_t mk = top_key[0], bound = nth_key[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) mk = max(mk, top_key[w]), bound = min(bound, nth_key[w]);
+    const uint32_t mk = warp_max(lane < kWarps ? top_key[lane] : 0u);
+    const uint32_t bound = ~warp_max(lane < kWarps ? ~nth_key[lane] : 0u);
     // a warp without that many threads with elements bounds nothing
-    const float low = bound ? __uint_as_float(bound & 0x80000000u ? bound ^ 0x80000000u : ~bound) : -INFINITY;
-    const float m = __uint_as_float(mk & 0x80000000u ? mk ^ 0x80000000u : ~mk);
-    const float shift = m == -INFINITY ? 0.f : m;  // nothing but -inf: a sum of 0, or of a NaN
-    float sum = 0.f;
+    const float low = bound ? unordered(bound) : -INFINITY;
+    const float m = unordered(mk);
+    // a whole number, so that sums of other slices come to it by whole powers of e; nothing but -inf: a
+    // sum of 0, or of a NaN
+    const float shift = m == -INFINITY ? 0.f : ceilf(m);
+    F2 sums = both<F2>(0.f);
+    unsigned reach = 0u;  // the elements that reach the bound, a bit each
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum += __expf(f[e] - shift);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kThreads + tid;
-        if (f[e] >= low && i < n) {  // no NaN is: its beam has no candidates
-            const int to = atomicAdd(&count, 1);
-            if (to < kList) lkey[to] = ordered(f[e]), lidx[to] = i;
-        }
+    for (int e = 0; e < E; e += 2) {
+        float d[2];
+        split(mul_(add_(join(f[e], f[e + 1]), both<F2>(-shift)), both<F2>(1.44269504f)), d);
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(d[0]));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(d[1]));
+        sums = add_(sums, join(d[0], d[1]));
+        // no NaN reaches it: its beam has no candidates
+        reach |= (f[e] >= low ? 1u << e : 0u) | (f[e + 1] >= low ? 2u << e : 0u);
+    }
+    float halves[2];
+    split(sums, halves);
+    float sum = halves[0] + halves[1];
+    for (; reach; reach &= reach - 1) {
+        const int i = (__ffs(reach) - 1) * kThreads + tid;
+        if (i >= n) break;
+        const int to = atomicAdd(&count, 1);
+        if (to < kList) lkey[to] = ordered(static_cast<float>(x[i - tid])), lidx[to] = i;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -141,14 +201,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const SelectArg
         float s = part[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) s += part[w];
-        a.sums[(long long)row * a.slices + slice] = make_float2(m, s);
+        a.sums[(long long)row * a.slices + slice] = make_float2(m == -INFINITY ? m : shift, s);
     }
     const long long out = ((long long)row * a.slices + slice) * a.keep;
     int found = count;
     if (found <= kList) {
         rank_all(lkey, lidx, found, a.keep, [&](int rank, int i) {
             const uint32_t u = lkey[i];
-            a.best[out + rank] = __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+            a.best[out + rank] = unordered(u);
             a.best_token[out + rank] = base + lidx[i];
         });
     } else {
@@ -175,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const SelectArg
                 if (top_key[w] > last || (top_key[w] == last && (int)nth_key[w] < last_i))
                     last = top_key[w], last_i = (int)nth_key[w];
             if (tid == 0) {
-                a.best[out + r] = __uint_as_float(last & 0x80000000u ? last ^ 0x80000000u : ~last);
+                a.best[out + r] = unordered(last);
                 a.best_token[out + r] = base + last_i;
             }
         }
@@ -189,8 +249,9 @@ constexpr int kRound = 4;
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a) {
     constexpr int kList = kMostKeep + kRound * kThreads;
-    __shared__ double base[kMostBeams];  // scores_i - log sum exp, NaN: nothing to choose from
-    __shared__ unsigned long long lkey[kList], nth_key[kWarps];
+    __shared__ Pair base[kMostBeams];  // scores_i - log sum exp, NaN: nothing to choose from
+    __shared__ bool over[kMostBeams];
+    __shared__ unsigned long long lkey[kList];
     __shared__ int lidx[kList], count;
     // the best so far, in order
     __shared__ unsigned long long rkey[kMostKeep];
@@ -201,76 +262,98 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
     for (int i = warp; i < a.beams; i += kWarps) {
         const long long row = b * a.beams + i;
         const float score = a.scores[row];
-        double v = isfinite(score) ? (double)score : (double)NAN;
+        Pair v{isfinite(score) ? score : NAN, 0.f};
         if (!(a.finished && a.finished[row])) {
             float m = -INFINITY;
             const float2* s = a.sums + row * a.slices;
             for (int k = lane; k < a.slices; k += 32) m = fmaxf(m, s[k].x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            double t = 0.0;  // a slice of nothing but -inf has a sum of 0 or NaN
-            for (int k = lane; k < a.slices; k += 32)
-                t += s[k].x == -INFINITY ? (double)s[k].y : (double)s[k].y * exp((double)s[k].x - (double)m);
+            Pair t{0.f, 0.f};
+            for (int k = lane; k < a.slices; k += 32) {
+                const float2 at = s[k];
+                // a slice of nothing but -inf has a sum of 0 or NaN
+                t = t.plus(at.x == -INFINITY ? Pair{at.y, 0.f} : exp_minus(m - at.x).times(Pair{at.y, 0.f}));
+            }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            v = isfinite(m) ? v - ((double)m + log(t)) : (double)NAN;
+            for (int o = 16; o > 0; o >>= 1)
+                t = t.plus(Pair{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+            const Pair l = log_of(t).plus(m);
+            v = isfinite(m) && isfinite(t.hi) ? Pair{-l.hi, -l.lo}.plus(v.hi) : Pair{NAN, 0.f};
         }
-        if (lane == 0) base[i] = v;
+        if (lane == 0) {
+            base[i] = v;
+            over[i] = a.finished && a.finished[row];
+        }
     }
     int have = 0;  // of the best so far
-    const int per = a.slices * a.keep;
-    const long long all = (long long)a.beams * per;
+    const int per = a.slices * a.keep, all = a.beams * per;
+    const int* tokens = a.best_token + b * all;
+    const float* logits = a.best + b * all;
+    const unsigned long long lowest = Pair{-INFINITY, 0.f}.key();
     __syncthreads();
-    for (long long c0 = 0; c0 < all; c0 += kRound * kThreads) {
+    for (int c0 = 0; c0 < all; c0 += kRound * kThreads) {
         unsigned long long ck[kRound], best = 0;
         int ci[kRound];
+        float x[kRound];
+#pragma unroll
+        for (int u = 0; u < kRound; ++u) {
+            const int c = c0 + u * kThreads + tid;
+            ci[u] = c < all ? tokens[c] : -1;
+            x[u] = c < all ? logits[c] : 0.f;
+        }
         // what a full list's last entry comes before is out
         const unsigned long long floor_key = have == a.keep ? rkey[a.keep - 1] : 0ull;
         const int floor_idx = have == a.keep ? ridx[a.keep - 1] : INT_MAX;
         bool any = false;
 #pragma unroll
         for (int u = 0; u < kRound; ++u) {
-            const long long c = c0 + u * kThreads + tid;
-            ck[u] = 0ull, ci[u] = INT_MAX;
+            const int c = c0 + u * kThreads + tid;
+            ck[u] = 0ull;
             if (c < all) {
-                const int i = (int)(c / per), k = (int)(c - (long long)i * per);
-                const long long row = b * a.beams + i;
-                const bool ended = a.finished && a.finished[row];
-                const double from = base[i];
-                double v = -(double)INFINITY;
-                int t = -1;
-                if (ended || !isfinite(from)) {
+                const int i = c / per, k = c - i * per;
+                const Pair from = base[i];
+                const bool choice = isfinite(from.hi);
+                unsigned long long key = lowest;
+                int t = ci[u];
+                if (over[i] || !choice) {
                     // the first tokens, at -inf; an ended beam's padding token at its score
-                    if (k < a.keep && k < a.vocab) t = k;
-                    if (ended && isfinite(from)) {
+                    t = k < a.keep && k < a.vocab ? k : -1;
+                    if (over[i] && choice) {
                         if (k == a.keep - 1 && a.pad >= a.keep) t = a.pad;
-                        if (t == a.pad) v = from;
+                        if (t == a.pad) key = from.key();
                     }
-                } else {
-                    t = a.best_token[row * per + k];
-                    if (t >= 0) v = from + (double)a.best[row * per + k];
+                } else if (x[u] != -INFINITY) {
+                    key = from.plus(x[u]).key();
                 }
+                ci[u] = INT_MAX;
                 if (t >= 0) {
-                    const unsigned long long key = ordered(v);
                     const int at = i * a.vocab + t;
                     if (key > floor_key || (key == floor_key && at < floor_idx)) {
                         ck[u] = key, ci[u] = at, any = true;
                         best = max(best, key);
                     }
                 }
+            } else {
+                ci[u] = INT_MAX;
             }
         }
-        const unsigned long long nth = warp_nth(best, (a.keep + kWarps - 1) / kWarps, lane);
-        if (lane == 0) nth_key[warp] = nth;
         if (tid == 0) count = have;
         if (tid < have) lkey[tid] = rkey[tid], lidx[tid] = ridx[tid];
         if (!__syncthreads_or(any)) continue;
-        unsigned long long bound = nth_key[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) bound = min(bound, nth_key[w]);
+        // the keep-th best of the threads' own best, to its first 32 bits, bit by bit: at least `keep`
+        // candidates reach it (beams differ too much for a bound by warps)
+        const uint32_t top = (uint32_t)(best >> 32);
+        uint32_t bound = 0u;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t t = bound | 1u << bit;
+            const int n = __syncthreads_count(top >= t);
+            if (n >= a.keep) bound = t;
+            if (n == a.keep) break;
+        }
 #pragma unroll
         for (int u = 0; u < kRound; ++u)
-            if (ci[u] != INT_MAX && ck[u] >= bound) {
+            if (ci[u] != INT_MAX && (uint32_t)(ck[u] >> 32) >= bound) {
                 const int to = atomicAdd(&count, 1);
                 lkey[to] = ck[u], lidx[to] = ci[u];
             }
@@ -282,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
     if (tid < have) {
         const unsigned long long u = rkey[tid];
         const long long out = b * a.keep + tid;
-        a.out_scores[out] = (float)__longlong_as_double((long long)(u >> 63 ? u ^ 0x8000000000000000ull : ~u));
+        a.out_scores[out] = unordered((uint32_t)(u >> 32));  // the pair rounded to float32
         a.parents[out] = ridx[tid] / a.vocab;
         a.tokens[out] = ridx[tid] % a.vocab;
     }
@@ -404,13 +487,13 @@ ssd_status_t check_beam(const ssd_beam_t* p) {
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
-constexpr int kWide = 32, kNarrow = 8;  // elements a thread
+constexpr int kWide = 16, kNarrow = 8;  // elements a thread
 struct SelectPlan {
     int e, slices;
     size_t best, token, sums, total;
 };
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
-// Eight elements a thread while slices of 32 leave fewer than two blocks for each SM: then a slice's
+// Eight elements a thread while slices of 16 leave fewer than two blocks for each SM: then a slice's
 // latency is all there is.
 SelectPlan select_plan(const ssd_beam_t& p) {
     SelectPlan l;
