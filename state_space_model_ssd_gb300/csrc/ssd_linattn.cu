@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "layer_device.cuh"
 #include "linattn.cuh"
 
 namespace ssd {
@@ -198,33 +199,43 @@ cudaError_t simt_launch(const WalkArgs& a, cudaStream_t stream) {
 }
 
 // The states that enter each segment, in the walk's direction, over what each segment adds:
-// S <- a^len S + sum.  One thread an element of a head's state and sequence; its loads do not
-// depend on one another.  Bound by the states' bytes, read and written once.
+// S <- a^len S + sum.  A thread goes through one sequence with VEC elements of a head's state; eight
+// segments' loads are on their way ahead of their stores.  Bound by the states' bytes, read and
+// written once.
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_constant__ WalkArgs a) {
     const Pass& p = a.pass[blockIdx.z];
-    const int size = p.kd * p.vd;
-    const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (e >= (long long)a.H * size) return;
-    const int h = (int)(e / size);
-    const float ld = a.ld[h];
+    const int size = p.kd * p.vd, row = a.H * size;  // less than 2^31: check_sizes
+    const int e = ((int)blockIdx.x * kThreads + threadIdx.x) * VEC;
+    if (e >= row) return;
+    const float ld = a.ld[e / size];
+    const Decay whole(ld, a.Ls);
     for (int s = blockIdx.y; s < a.nseq; s += gridDim.y) {
         const Seg g = sequence(a, s);
-        const long long first = first_segment(a, s), row = (long long)a.H * size;
-        float S = p.s_in ? p.s_in[s * row + e] : 0.f;
-        const Decay whole(ld, a.Ls);
-        // from the walk's first segment on, eight loads at a time ahead of the stores
-        const long long step = p.reverse ? -row : row;
-        float* at = p.s_sum + (first + (p.reverse ? g.cnt - 1 : 0)) * row + e;
+        Pack<float, VEC> v;
+        float S[VEC];
+        v.zero();
+        if (p.s_in) v.load(p.s_in + (long long)s * row + e);
+        v.get(S);
+        // from the walk's first segment on
+        const long long step = p.reverse ? -(long long)row : row;
+        float* at = p.s_sum + (first_segment(a, s) + (p.reverse ? g.cnt - 1 : 0)) * row + e;
         const Decay ahead(ld, p.reverse ? g.len - (g.cnt - 1) * a.Ls : a.Ls);
         for (int k0 = 0; k0 < g.cnt; k0 += 8) {
-            float add[8];
+            Pack<float, VEC> add[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) add[i] = k0 + i + 1 < g.cnt ? at[(k0 + i) * step] : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                add[i].zero();
+                if (k0 + i + 1 < g.cnt) add[i].load(at + (k0 + i) * step);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (k0 + i < g.cnt) {
-                    at[(k0 + i) * step] = S;
-                    S = (k0 + i == 0 ? ahead(S) : whole(S)) + add[i];
+                    store_vec<VEC>(at + (k0 + i) * step, S);
+                    float f[VEC];
+                    add[i].get(f);
+#pragma unroll
+                    for (int u = 0; u < VEC; ++u) S[u] = (k0 + i == 0 ? ahead(S[u]) : whole(S[u])) + f[u];
                 }
         }
     }
@@ -264,6 +275,7 @@ ssd_status_t check_sizes(const ssd_linattn_t* p, bool bwd) {
         !isfinite(p->scale) || (p->nseq > 0 && p->batch != 1))
         return SSD_ERR_INVALID_ARG;
     const long long H = p->nheads, G = p->ngroups, P = p->headdim, N = p->dstate;
+    // a head's state has up to 2^14 elements, all heads' together fewer than 2^31
     if (p->headdim > 128 || p->dstate > 128 || p->nheads > 65535 || p->batch > INT_MAX ||
         p->seqlen > INT_MAX || p->batch * p->seqlen > INT_MAX)
         return SSD_ERR_UNSUPPORTED;
@@ -369,11 +381,16 @@ cudaError_t launch_walk(WalkArgs a, bool tc, bool sums, int dtype, Launch& L) {
 }
 
 cudaError_t launch_scan(const WalkArgs& a, Launch& L) {
-    const long long size = (long long)a.H * a.pass[0].kd * a.pass[0].vd;
+    const int state = a.pass[0].kd * a.pass[0].vd;
+    bool four = state % 4 == 0;
+    for (int i = 0; i < a.npass; ++i) four = four && aligned_to(a.pass[i].s_in, 16);
+    const long long n = (long long)a.H * state / (four ? 4 : 1);
+    const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), (unsigned)std::min(a.nseq, 65535), (unsigned)a.npass);
     L.begin("linattn_scan");
-    segment_scan_kernel<<<dim3((unsigned)((size + kThreads - 1) / kThreads),
-                               (unsigned)std::min(a.nseq, 65535), (unsigned)a.npass),
-                          kThreads, 0, L.stream>>>(a);
+    if (four)
+        segment_scan_kernel<4><<<grid, kThreads, 0, L.stream>>>(a);
+    else
+        segment_scan_kernel<1><<<grid, kThreads, 0, L.stream>>>(a);
     return L.end();
 }
 

@@ -43,7 +43,7 @@ constexpr int kQ = kTcChunk;                 // 128 tokens
 constexpr int kV = kTcTile;                  // 64 columns
 constexpr int kSub = kQ * 128;               // bytes of a tile of 64 channels: rows of 128 bytes
 constexpr int kWalkThreads = 20 * 32;
-constexpr int kSumThreads = 6 * 32;
+constexpr int kSumThreads = 18 * 32;
 constexpr int kTeam = 16;                    // warps that work on the numbers
 constexpr int kMostStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;
@@ -119,7 +119,7 @@ struct Aux {
     float powers[2][kBelow + kQ];
 };
 struct SumsAux {
-    uint64_t full[kMostStages], empty[kMostStages], made[2], sums, sums_free;
+    uint64_t full[kMostStages], empty[kMostStages], made[2], used[2], sums, sums_free;
     uint32_t tmem;
     int stop;
     Item items[kSumThreads / 32];  // of each warp
@@ -719,121 +719,126 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     tc_sums_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
     extern __shared__ __align__(1024) unsigned char sm[];
     SumsAux* x = reinterpret_cast<SumsAux*>(sm + geo.aux_at);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = threadIdx.x & 127, part = warp >> 2;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const int kbytes = geo.kblocks * kSub;
     int* status = a.status;
     if (threadIdx.x == 0) {
         // a chunk's copies are announced in two steps
         for (int s = 0; s < geo.stages; ++s) mbar_init(&x->full[s], 2), mbar_init(&x->empty[s], 1);
-        for (int s = 0; s < 2; ++s) mbar_init(&x->made[s], 128);
-        mbar_init(&x->sums, 1), mbar_init(&x->sums_free, 128);
+        for (int s = 0; s < 2; ++s) mbar_init(&x->made[s], kTeam), mbar_init(&x->used[s], 1);
+        mbar_init(&x->sums, 1), mbar_init(&x->sums_free, kTeam);
         x->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(&x->tmem, 128);
+    if (warp == 17) tmem_alloc(&x->tmem, 128);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = x->tmem;
     Item& t = x->items[warp];
     int g = 0, m = 0;  // chunks and items of this block so far
+    Place st, w_set;   // of two sets of weights one chunk's are made while the other's are read
     const auto wanted = [](const Item& t) {  // nothing comes after a walk's last segment
-        return t.g.there && t.g.k != (t.p->reverse ? 0 : t.g.cnt - 1);
+        return t.g.there && t.g.k != (t.rev ? 0 : t.g.cnt - 1);
     };
-    // two sets of weights: one chunk's are made while the other's are read
-    if (warp < 4) {
+    const auto next_item = [&](int item) {
+        __syncwarp();
+        if (lane == 0) take(a, geo.by_pass, item, &t);
+        __syncwarp();
+        return wanted(t);
+    };
+    const auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    if (warp < kTeam) {
+        // ------------------------------------------------ weights: a row, a quarter of the columns a thread
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
-            __syncwarp();
-            if (lane == 0) take(a, geo.by_pass, item, &t);
-            __syncwarp();
-            if (!wanted(t)) continue;
-            const Pass& p = *t.p;
-            const float ld2 = t.ld * 1.44269504f;
-            for (int c = 0; c < t.chunks; ++c, ++g) {
-                const int s = g % geo.stages, at = c * kQ + tid;
-                unsigned char* st = sm + s * geo.stage_bytes;
-                if (!wait_warp(&x->full[s], (g / geo.stages) & 1, &x->stop, status)) goto done;
-                // the set's last reader has finished: its stage was given back before
-                if (g >= 2 && !wait_warp(&x->empty[(g - 2) % geo.stages], ((g - 2) / geo.stages) & 1, &x->stop, status))
-                    goto done;
-                const bool in = at < t.g.len;
-                const float w = in ? power(ld2, p.reverse ? at + 1 : t.g.len - 1 - at) * p.su : 0.f;
-                split_row<NT>(st + kbytes, sm + geo.w_at + (g & 1) * NT * kSub, tid, 0, 8, w, in);
-                if (!in)
-                    for (int b = 0; b < p.kd / 64; ++b) zero_row(st + b * kSub, tid);
+            if (!next_item(item)) continue;
+            const int chunks = t.chunks, len = t.g.len, rev = t.rev, kb = t.kb;
+            const float ld2 = t.ld2, su = t.su;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, ++g, st.next(geo.stages), w_set.next(2)) {
+                const int at = c * kQ + i;
+                unsigned char* v = sm + st.s * geo.stage_bytes + kbytes;
+                const bool in = at < len;
+                const float w = in ? power(ld2, rev ? at + 1 : len - 1 - at) * su : 0.f;
+                if (!wait_warp(&x->full[st.s], st.phase, &x->stop, status)) goto done;
+                if (g >= 2 && !wait_warp(&x->used[w_set.s], w_set.phase ^ 1u, &x->stop, status)) goto done;
+                split_row<NT>(v, sm + geo.w_at + w_set.s * NT * kSub, i, 2 * part, 2, w, in);
+                if (!in && part < kb) zero_row(v - kbytes + part * kSub, i);
                 fence_proxy_async();
-                mbar_arrive(&x->made[g & 1]);
+                arrive(&x->made[w_set.s]);
             }
             if (!wait_warp(&x->sums, m & 1, &x->stop, status)) goto done;
             tc_fence_after();
-            if (tid < p.kd) {
-                float* out = p.s_sum + (t.id * a.H + t.h) * (long long)p.kd * p.vd + tid * p.sn + t.v0 * p.sp;
-#pragma unroll 1
-                for (int i = 0; i < kV; i += 8) {
-                    F2 u[4];
-                    load_sum8(tmem + lane_base + i, u);
+            F2 u[8];
+            load_sum8(tmem + lane_base + 16 * part, u);
+            load_sum8(tmem + lane_base + 16 * part + 8, u + 4);
+            tc_fence_before();
+            arrive(&x->sums_free);
+            if (i < t.p->kd) {
+                const long long sp = t.p->sp;
+                float* out = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
+                             (t.v0 + 16 * part) * sp;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float f[2];
-                        layer::split(u[e], f);
-                        out[(i + 2 * e) * p.sp] = f[0], out[(i + 2 * e + 1) * p.sp] = f[1];
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    float f[2];
+                    layer::split(u[e], f);
+                    out[2 * e * sp] = f[0], out[(2 * e + 1) * sp] = f[1];
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&x->sums_free);
+            __syncwarp();
             ++m;
         }
-    } else if (warp == 4) {
-        if (lane == 0) {
-            for (int item = blockIdx.x; item < geo.items && !x->stop; item += gridDim.x) {
-                take(a, geo.by_pass, item, &t);
-                if (!wanted(t)) continue;
+    } else if (warp == 16) {
+        // ------------------------------------------------ copies in
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            if (!next_item(item)) continue;
+            if (lane == 0) {
                 const Tiles tiles(maps, t);
-                for (int c = 0; c < t.chunks; ++c, ++g) {
-                    const int s = g % geo.stages;
-                    if (g >= geo.stages && !wait(&x->empty[s], (g / geo.stages - 1) & 1, &x->stop, status)) break;
-                    unsigned char* st = sm + s * geo.stage_bytes;
-                    tiles.load_qk<false>((int)t.g.start + c * kQ, st, kbytes, &x->full[s]);
-                    tiles.load_v((int)t.g.start + c * kQ, st + kbytes, &x->full[s]);
+                const int chunks = t.chunks, t0 = (int)t.g.start;
+                for (int c = 0; c < chunks; ++c, ++g, st.next(geo.stages)) {
+                    if (g >= geo.stages && !wait(&x->empty[st.s], st.phase ^ 1u, &x->stop, status)) break;
+                    unsigned char* to = sm + st.s * geo.stage_bytes;
+                    tiles.load_qk<false>(t0 + c * kQ, to, kbytes, &x->full[st.s]);
+                    tiles.load_v(t0 + c * kQ, to + kbytes, &x->full[st.s]);
                 }
             }
-            if (*(volatile int*)&x->stop)
-                for (int k = max(0, g - geo.stages); k < g; ++k)
-                    drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
+            if (__any_sync(0xffffffffu, *(volatile int*)&x->stop)) break;
         }
+        if (lane == 0 && *(volatile int*)&x->stop)
+            for (int k = max(0, g - geo.stages); k < g; ++k)
+                drain(&x->full[k % geo.stages], (k / geo.stages) & 1);
         __syncwarp();
     } else {
-        if (lane == 0) {
-            bool stop = false;
-            for (int item = blockIdx.x; item < geo.items && !stop; item += gridDim.x) {
-                take(a, geo.by_pass, item, &t);
-                if (!wanted(t)) continue;
-                if (m > 0 && !wait(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
+        // ------------------------------------------------ products
+        const uint32_t base = same(smem_u32(sm)), tm = same(tmem);
+        for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
+            if (!next_item(item)) continue;
+            const int kb = same(t.kb), chunks = same(t.chunks);
+            if (m > 0 && !wait_warp(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
+            for (int c = 0; c < chunks; ++c, st.next(geo.stages), w_set.next(2)) {
+                if (!wait_warp(&x->made[w_set.s], w_set.phase, &x->stop, status)) goto stopped;
                 tc_fence_after();
-                for (int c = 0; c < t.chunks; ++c, ++g) {
-                    const int s = g % geo.stages;
-                    stop = !wait(&x->made[g & 1], (g >> 1) & 1, &x->stop, status);
-                    if (stop) break;
-                    tc_fence_after();
-                    mma_sums<NT>(tmem, smem_u32(sm + s * geo.stage_bytes),
-                                 smem_u32(sm + geo.w_at + (g & 1) * NT * kSub), t.p->kd / 64, c > 0);
-                    mma_commit(&x->empty[s]);
+                if (elect_one()) {
+                    mma_sums<NT>(tm, base + st.s * geo.stage_bytes, base + geo.w_at + w_set.s * NT * kSub, kb, c > 0);
+                    mma_commit(&x->empty[st.s]);
+                    mma_commit(&x->used[w_set.s]);
+                    if (c + 1 == chunks) mma_commit(&x->sums);
                 }
-                if (stop) break;
-                mma_commit(&x->sums);
-                ++m;
             }
-            if (*(volatile int*)&x->stop) {
-                mma_commit(&x->sums);
-                for (int k = 0; k < 2; ++k) drain(&x->sums, k);
-            }
+            ++m;
         }
-        __syncwarp();
+    stopped:
+        if (*(volatile int*)&x->stop) {
+            if (elect_one()) mma_commit(&x->sums);
+            for (int k = 0; k < 2; ++k) drain(&x->sums, k);
+        }
     }
 done:
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 17) {
         tmem_relinquish();
         tmem_dealloc(tmem, 128);
     }
