@@ -135,6 +135,11 @@ __device__ __forceinline__ const Pass& pass_of(const WalkArgs& a, int& t) {
     return a.pass[p];
 }
 
+// A forward of at most so many tokens a sequence is stepped through them (ssd_linattn_step.cu).
+constexpr int kFewTokens = 16;
+bool few_fits(const WalkArgs& a);
+cudaError_t few_tokens(const WalkArgs& a, int dtype, Launch& L);
+
 constexpr int kSimtTile = 32;  // columns of v a block of the plain walk takes
 
 // The tensor-core walk (ssd_linattn_tc.cu): whether it takes these tensors, and the launches.

@@ -81,12 +81,14 @@ __global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_consta
     for (int c0 = 0; c0 < g.len; c0 += kQ) {
         const int n = min(kQ, g.len - c0);
         __syncthreads();
+#pragma unroll 4
         for (int e = tid; e < kQ * kd; e += kThreads) {
             const int r = e / kd, c = e - r * kd;
             const long long t = g.start + (p.reverse ? g.len - 1 - (c0 + r) : c0 + r);
             if (OUT) qs[r * ks1 + c] = r < n ? static_cast<float>(q[t * p.qs + c]) : 0.f;
             ks[r * ks1 + c] = r < n ? static_cast<float>(k[t * p.ks + c]) : 0.f;
         }
+#pragma unroll
         for (int e = tid; e < kQ * kVT; e += kThreads) {
             const int r = e / kVT, c = e - r * kVT;
             const long long t = g.start + (p.reverse ? g.len - 1 - (c0 + r) : c0 + r);
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_consta
         if (OUT) {
             if (j0 <= i0 + 1 && i0 < n) {
                 float d[2][2] = {};
+#pragma unroll 8
                 for (int c = 0; c < kd; ++c) {
                     const float q0 = qs[i0 * ks1 + c], q1 = qs[(i0 + 1) * ks1 + c];
                     const float k0 = ks[j0 * ks1 + c], k1 = ks[(j0 + 1) * ks1 + c];
@@ -112,12 +115,14 @@ __global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_consta
             __syncthreads();
             if (i0 < n) {
                 float o[2][2] = {}, w[2][2] = {};
+#pragma unroll 4
                 for (int j = 0; j <= i0 + 1; ++j) {  // the entry above the diagonal is not read
                     const float a0 = j <= i0 ? sc[i0 * kVS + j] : 0.f, a1 = sc[(i0 + 1) * kVS + j];
                     const float b0 = vs[j * kVS + j0], b1 = vs[j * kVS + j0 + 1];
                     if (j <= i0) o[0][0] = fmaf(a0, b0, o[0][0]), o[0][1] = fmaf(a0, b1, o[0][1]);
                     o[1][0] = fmaf(a1, b0, o[1][0]), o[1][1] = fmaf(a1, b1, o[1][1]);
                 }
+#pragma unroll 8
                 for (int c = 0; c < kd; ++c) {
                     const float a0 = qs[i0 * ks1 + c], a1 = qs[(i0 + 1) * ks1 + c];
                     const float b0 = S[c * kVS + j0], b1 = S[c * kVS + j0 + 1];
@@ -154,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_consta
         for (int u = tid; u < (kd + 3) / 4 * (kVT / 4); u += kThreads) {
             const int n0 = u / (kVT / 4) * 4, p0 = u % (kVT / 4) * 4;
             float d[4][4] = {};
+#pragma unroll 4
             for (int r = 0; r < n; ++r) {
                 float kk[4], vv[4];
 #pragma unroll
@@ -241,22 +247,35 @@ __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_con
     }
 }
 
-// The gradients of shared heads: out[t][g][c] = sum of part[t][g r + i][c], i < r, in order.
-template <typename T>
+// The gradients of shared heads: out[t][g][c] = sum of part[t][g r + i][c], i < r, in order; VEC
+// columns a thread.  Bound by the parts' bytes.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) shared_sum_kernel(const float* part, T* out, long long T_,
                                                               int G, int r, int D, long long stride) {
-    const long long n = T_ * G * D;
-    for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < n;
-         e += (long long)gridDim.x * kThreads) {
-        const int c = (int)(e % D);
-        const long long tg = e / D;
-        const int g = (int)(tg % G);
-        const long long t = tg / G;
-        const float* src = part + (tg * r) * D + c;
-        float s = 0.f;
-        for (int i = 0; i < r; ++i) s += src[(long long)i * D];
-        st_out(out, t * stride + (long long)g * D + c, s);
-    }
+    const int row = G * D / VEC;  // vectors of a token
+    for (long long t = blockIdx.y; t < T_; t += gridDim.y)
+        for (int e = blockIdx.x * kThreads + threadIdx.x; e < row; e += gridDim.x * kThreads) {
+            const int g = e * VEC / D, c = e * VEC - g * D;
+            const float* src = part + ((t * G + g) * r) * D + c;
+            float s[VEC] = {};
+            for (int i0 = 0; i0 < r; i0 += 4) {
+                Pack<float, VEC> v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i].zero();
+                    if (i0 + i < r) v[i].load(src + (long long)(i0 + i) * D);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[VEC];
+                    v[i].get(f);
+                    if (i0 + i < r)
+#pragma unroll
+                        for (int u = 0; u < VEC; ++u) s[u] += f[u];
+                }
+            }
+            store_vec<VEC>(out + t * stride + (long long)g * D + c, s);
+        }
 }
 
 // ---------------------------------------------------------------- host
@@ -397,16 +416,25 @@ cudaError_t launch_scan(const WalkArgs& a, Launch& L) {
 cudaError_t launch_shared_sum(const float* part, void* out, const ssd_linattn_t& p, long long T, int D,
                               long long stride, Launch& L) {
     const int r = p.nheads / p.ngroups;
-    const long long n = T * p.ngroups * D;
-    if (n == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 16LL * sm_count());
+    if (T == 0) return cudaSuccess;
+    // four columns where they and out's rows allow it
+    const bool four = D % 4 == 0 && stride % 4 == 0 && aligned_to(out, p.dtype == SSD_DTYPE_BF16 ? 8 : 16);
+    const int row = p.ngroups * D / (four ? 4 : 1);
+    const dim3 grid((unsigned)((row + kThreads - 1) / kThreads), (unsigned)std::min<long long>(T, 65535));
     L.begin("linattn_shared_sum");
-    if (p.dtype == SSD_DTYPE_BF16)
-        shared_sum_kernel<<<grid, kThreads, 0, L.stream>>>(part, static_cast<__nv_bfloat16*>(out), T,
-                                                           p.ngroups, r, D, stride);
-    else
-        shared_sum_kernel<<<grid, kThreads, 0, L.stream>>>(part, static_cast<float*>(out), T, p.ngroups,
-                                                           r, D, stride);
+    if (p.dtype == SSD_DTYPE_BF16) {
+        auto* o = static_cast<__nv_bfloat16*>(out);
+        if (four)
+            shared_sum_kernel<__nv_bfloat16, 4><<<grid, kThreads, 0, L.stream>>>(part, o, T, p.ngroups, r, D, stride);
+        else
+            shared_sum_kernel<__nv_bfloat16, 1><<<grid, kThreads, 0, L.stream>>>(part, o, T, p.ngroups, r, D, stride);
+    } else {
+        auto* o = static_cast<float*>(out);
+        if (four)
+            shared_sum_kernel<float, 4><<<grid, kThreads, 0, L.stream>>>(part, o, T, p.ngroups, r, D, stride);
+        else
+            shared_sum_kernel<float, 1><<<grid, kThreads, 0, L.stream>>>(part, o, T, p.ngroups, r, D, stride);
+    }
     return L.end();
 }
 
@@ -471,6 +499,11 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
+    if (few_fits(a)) {
+        err = few_tokens(a, p.dtype, L);
+        set_last_launches(L.count);
+        return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    }
     if (l.Ls) {
         f.s_sum = reinterpret_cast<float*>(ws + l.s_seg);
         err = launch_walk(a, tc, true, p.dtype, L);

@@ -10,7 +10,7 @@
 #include <algorithm>
 
 #include "layer_device.cuh"
-#include "layer_host.cuh"
+#include "linattn.cuh"
 
 namespace ssd {
 namespace layer {
@@ -100,8 +100,157 @@ __global__ void __launch_bounds__(kThreads, 6) attn_step_kernel(const StepArgs a
     }
 }
 
+// `width` elements of each of `n` tokens, `stride` apart, as rows of 128 floats: a warp takes every
+// fourth token, and has its elements on their way before the first is put down.
+template <typename T>
+struct Rows4 {
+    T x[linattn::kFewTokens / (kThreads / 32)][4];
+    __device__ __forceinline__ void load(const T* from, long long stride, int width, int n) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int u = 0; u < linattn::kFewTokens / (kThreads / 32); ++u) {
+            const int t = (threadIdx.x >> 5) + u * (kThreads / 32);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (t < n && lane + 32 * c < width) x[u][c] = from[t * stride + lane + 32 * c];
+        }
+    }
+    __device__ __forceinline__ void store(float* to, int width, int n) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int u = 0; u < linattn::kFewTokens / (kThreads / 32); ++u) {
+            const int t = (threadIdx.x >> 5) + u * (kThreads / 32);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (t < n && lane + 32 * c < width) to[t * 128 + lane + 32 * c] = static_cast<float>(x[u][c]);
+        }
+    }
+};
+
+// A few tokens of every sequence in the same way: the state stays in registers over them, their q, k
+// and v in shared memory.  A chunked walk's fixed steps take longer than sixteen tokens here: seven
+// tokens of 80 heads of 64 x 128, MEASURE_FEW.
+template <typename T, int PIECES>
+__global__ void __launch_bounds__(kThreads, 4) attn_few_kernel(const __grid_constant__ linattn::WalkArgs a, int lanes, int rows) {
+    constexpr int kTokens = linattn::kFewTokens;
+    __shared__ __align__(16) float qs[kTokens][128], ks[kTokens][128];
+    __shared__ float vs[kTokens][128];
+    const linattn::Pass& p = a.pass[0];
+    const int h = blockIdx.y, N = p.kd, p0 = blockIdx.x * rows, np = min(rows, p.vd - p0);
+    T* out = static_cast<T*>(p.out) + (long long)h * p.vd + p0;
+    if (a.cu && blockIdx.z == 0)  // tokens behind the last sequence
+        for (long long t = linattn::border(a, a.nseq); t < a.T; ++t)
+            for (int i = threadIdx.x; i < np; i += kThreads) st_out(out, t * p.os + i, 0.f);
+    for (int s = blockIdx.z; s < a.nseq; s += gridDim.z) {
+        const linattn::Seg g = linattn::sequence(a, s);
+        const int lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes, step = kThreads / lanes;
+        const bool in = 4 * lane < N;
+        const long long at = (((long long)s * a.H + h) * p.vd + p0) * N + 4 * lane;
+        float4 S[PIECES];
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int r = i * step + first;
+            S[i] = p.s_in && in && r < np ? *reinterpret_cast<const float4*>(p.s_in + at + (long long)r * N)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncthreads();
+        const T* q = static_cast<const T*>(p.q) + g.start * p.qs + (long long)h * N;
+        const T* k = static_cast<const T*>(p.k) + g.start * p.ks + (long long)(h / p.kr) * N;
+        const T* v = static_cast<const T*>(p.v) + g.start * p.vs + (long long)(h / p.vr) * p.vd + p0;
+        {
+            Rows4<T> qr, kr, vr;
+            qr.load(q, p.qs, N, g.len);
+            kr.load(k, p.ks, N, g.len);
+            vr.load(v, p.vs, np, g.len);
+            qr.store(&qs[0][0], N, g.len);
+            kr.store(&ks[0][0], N, g.len);
+            vr.store(&vs[0][0], np, g.len);
+        }
+        __syncthreads();
+        const float decay = expf(a.ld[h]);
+        for (int t = 0; t < g.len; ++t) {
+            float4 qq = make_float4(0.f, 0.f, 0.f, 0.f), kk = qq;
+            if (in) qq = *reinterpret_cast<const float4*>(&qs[t][4 * lane]), kk = *reinterpret_cast<const float4*>(&ks[t][4 * lane]);
+            float sum[PIECES];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int r = i * step + first;
+                const float vv = r < np ? vs[t][r] : 0.f;
+                float4& w = S[i];
+                w.x = fmaf(decay, w.x, vv * kk.x);
+                w.y = fmaf(decay, w.y, vv * kk.y);
+                w.z = fmaf(decay, w.z, vv * kk.z);
+                w.w = fmaf(decay, w.w, vv * kk.w);
+                sum[i] = (w.x * qq.x + w.y * qq.y) + (w.z * qq.z + w.w * qq.w);
+            }
+            for (int m = lanes >> 1; m > 0; m >>= 1)
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], m);
+            if (lane == 0)
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) {
+                    const int r = i * step + first;
+                    if (r < np) st_out(out, (g.start + t) * p.os + r, sum[i] * p.sx);
+                }
+        }
+        if (p.s_out && in)
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int r = i * step + first;
+                if (r < np) *reinterpret_cast<float4*>(p.s_out + at + (long long)r * N) = S[i];
+            }
+    }
+}
+
+// Lanes of a row of N elements in pieces of `vec`, and the rows of P that a block takes: as many as
+// its threads have in flight at once, halved while there are fewer than two blocks for each SM and
+// each thread keeps a piece.
+void step_shape(int P, int N, int vec, long long heads, int* lanes, int* rows) {
+    *lanes = 1;
+    while (*lanes < 32 && *lanes * vec < N) *lanes *= 2;
+    *rows = std::min(P, std::max(1, kPieces * kThreads / *lanes));
+    while (heads * ((P + *rows - 1) / *rows) < 2LL * sm_count() && *rows * *lanes >= 2 * kThreads)
+        *rows = (*rows + 1) / 2;
+}
+
 }  // namespace
 }  // namespace layer
+
+bool linattn::few_fits(const WalkArgs& a) {
+    const Pass& p = a.pass[0];
+    return (a.cu ? a.T : a.rowlen) <= kFewTokens && p.kd % 4 == 0 && layer::aligned_to(p.s_in, 16) &&
+           layer::aligned_to(p.s_out, 16);
+}
+
+cudaError_t linattn::few_tokens(const WalkArgs& a, int dtype, Launch& L) {
+    const Pass& p = a.pass[0];
+    int lanes = 1;
+    while (lanes < 32 && lanes * 4 < p.kd) lanes *= 2;
+    // as few pieces of the state a thread as leave the blocks one round of the four an SM holds: the
+    // tokens' steps wait for one another, so that only blocks side by side hide them
+    const auto rows_of = [&](int pieces) { return std::min(p.vd, pieces * layer::kThreads / lanes); };
+    int pieces = 2;
+    while (pieces < 8 && (long long)a.nseq * a.H * ((p.vd + rows_of(pieces) - 1) / rows_of(pieces)) > 4LL * sm_count())
+        pieces *= 2;
+    const int rows = rows_of(pieces);
+    const dim3 grid((unsigned)((p.vd + rows - 1) / rows), (unsigned)a.H, (unsigned)std::min(a.nseq, 65535));
+    const auto run = [&](auto t) {
+        using T = decltype(t);
+        if (pieces == 2)
+            layer::attn_few_kernel<T, 2><<<grid, layer::kThreads, 0, L.stream>>>(a, lanes, rows);
+        else if (pieces == 4)
+            layer::attn_few_kernel<T, 4><<<grid, layer::kThreads, 0, L.stream>>>(a, lanes, rows);
+        else
+            layer::attn_few_kernel<T, 8><<<grid, layer::kThreads, 0, L.stream>>>(a, lanes, rows);
+    };
+    L.begin("linattn_few");
+    if (dtype == SSD_DTYPE_BF16)
+        run(__nv_bfloat16());
+    else
+        run(float());
+    return L.end();
+}
+
 }  // namespace ssd
 
 using namespace ssd;
@@ -137,13 +286,7 @@ extern "C" ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int
     a.H = p.nheads, a.r = (int)(H / G), a.P = p.headdim, a.N = p.dstate, a.nslots = nslots;
     a.scale = p.scale;
     const int vec = N % 4 == 0 ? 4 : 1;
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes * vec < N) a.lanes *= 2;
-    // rows of the state a block takes: as many as its threads have in flight at once, halved while the
-    // batch leaves SMs with fewer than two blocks and each thread keeps a piece
-    a.rows = std::min((int)P, std::max(1, kPieces * kThreads / a.lanes));
-    while (B * H * ((P + a.rows - 1) / a.rows) < 2LL * sm_count() && a.rows * a.lanes >= 2 * kThreads)
-        a.rows = (a.rows + 1) / 2;
+    step_shape(p.headdim, p.dstate, vec, B * H, &a.lanes, &a.rows);
     const dim3 grid((unsigned)((P + a.rows - 1) / a.rows), (unsigned)H, (unsigned)B);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
