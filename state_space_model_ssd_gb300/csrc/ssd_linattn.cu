@@ -331,22 +331,28 @@ bool rows_clash(std::initializer_list<Rows> outs, std::initializer_list<Rows> in
 
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// How the sequences are cut.  Not at all while the longest one may be short, or a dense batch has
-// items for all SMs; otherwise into segments that leave several items for each SM, of 512 to
-// 4096 tokens: shorter ones would move more of states (P N float32 four times each) than of tokens.
+// How the sequences are cut, by sizes alone.  Not at all while the longest one may be short, or a dense
+// batch has items for twice the SMs; otherwise into segments that leave several items for each SM, up to
+// 4096 tokens.  On the tensor cores a segment has at least 512 tokens: shorter ones would move more of
+// states (P N float32 four times each) than of tokens.  The plain walk takes 5 us for 32 tokens, one
+// after the other, so that 64 are worth the two launches more (2 x 333 tokens of 5 heads in float32,
+// backward: MEASURE_SIMT).
 Plan make_plan(const ssd_linattn_t& p, bool bwd) {
     Plan l = {};
     l.T = p.batch * p.seqlen;
     l.n = p.nseq ? p.nseq : (int)p.batch;
-    const long long tiles = bwd ? (2 * p.dstate + p.headdim + kTcTile - 1) / kTcTile
-                                : (p.headdim + kTcTile - 1) / kTcTile;
-    const long long per_cut = (long long)p.nheads * tiles;  // items for each run of tokens
+    const auto tensor = [](int n) { return n == 64 || n == 128; };
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && tensor(p.headdim) && tensor(p.dstate);
+    const int tile = tc ? kTcTile : kSimtTile, least = tc ? 512 : 64, step = tc ? kTcChunk : kQ;
+    const auto tiles = [&](int n) { return (n + tile - 1) / tile; };
+    // items for each run of tokens
+    const long long per_cut = (long long)p.nheads * ((bwd ? 2 * tiles(p.dstate) : 0) + tiles(p.headdim));
     const long long sms = sm_count();
     const bool dense_full = !p.nseq && l.n * per_cut >= 2 * sms;
-    if (p.seqlen > 512 && !dense_full) {
-        long long want = (8 * sms + per_cut - 1) / per_cut;  // cuts of all tokens
-        long long Ls = (l.T / want + 127) / 128 * 128;
-        Ls = std::min<long long>(std::max<long long>(Ls, 512), 4096);
+    if (p.seqlen > least && !dense_full) {
+        const long long want = (8 * sms + per_cut - 1) / per_cut;  // cuts of all tokens
+        long long Ls = (l.T / want + step - 1) / step * step;
+        Ls = std::min<long long>(std::max<long long>(Ls, least), 4096);
         if (Ls < p.seqlen) l.Ls = (int)Ls;
     }
     l.per = l.Ls ? (int)((p.seqlen + l.Ls - 1) / l.Ls) : 1;
