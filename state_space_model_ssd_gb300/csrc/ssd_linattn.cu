@@ -226,13 +226,15 @@ __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_con
         // from the walk's first segment on
         const long long step = p.reverse ? -(long long)row : row;
         float* at = p.s_sum + (first_segment(a, s) + (p.reverse ? g.cnt - 1 : 0)) * row + e;
-        const Decay ahead(ld, p.reverse ? g.len - (g.cnt - 1) * a.Ls : a.Ls);
+        // the short segment is the sequence's last: from the end the first
+        const Decay last(ld, g.len - (g.cnt - 1) * a.Ls);
+        const int short_one = p.reverse ? 0 : g.cnt - 1, summed = p.s_out ? g.cnt : g.cnt - 1;
         for (int k0 = 0; k0 < g.cnt; k0 += 8) {
             Pack<float, VEC> add[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 add[i].zero();
-                if (k0 + i + 1 < g.cnt) add[i].load(at + (k0 + i) * step);
+                if (k0 + i < summed) add[i].load(at + (k0 + i) * step);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -241,9 +243,23 @@ __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_con
                     float f[VEC];
                     add[i].get(f);
 #pragma unroll
-                    for (int u = 0; u < VEC; ++u) S[u] = (k0 + i == 0 ? ahead(S[u]) : whole(S[u])) + f[u];
+                    for (int u = 0; u < VEC; ++u) S[u] = (k0 + i == short_one ? last(S[u]) : whole(S[u])) + f[u];
                 }
         }
+        if (p.s_out) store_vec<VEC>(p.s_out + (long long)s * row + e, S);
+    }
+}
+
+// Final states of sequences that are not cut: what the sums left there, and the decayed initial ones.
+__global__ void __launch_bounds__(kThreads) final_state_kernel(const __grid_constant__ WalkArgs a) {
+    const Pass& p = a.pass[0];
+    const int size = p.kd * p.vd, row = a.H * size;
+    const int e = (int)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= row) return;
+    const float ld = a.ld[e / size];
+    for (int s = blockIdx.y; s < a.nseq; s += gridDim.y) {
+        const long long at = (long long)s * row + e;
+        p.s_out[at] += Decay(ld, sequence(a, s).len)(p.s_in[at]);
     }
 }
 
@@ -408,7 +424,7 @@ cudaError_t launch_walk(WalkArgs a, bool tc, bool sums, int dtype, Launch& L) {
 cudaError_t launch_scan(const WalkArgs& a, Launch& L) {
     const int state = a.pass[0].kd * a.pass[0].vd;
     bool four = state % 4 == 0;
-    for (int i = 0; i < a.npass; ++i) four = four && aligned_to(a.pass[i].s_in, 16);
+    for (int i = 0; i < a.npass; ++i) four = four && aligned_to(a.pass[i].s_in, 16) && aligned_to(a.pass[i].s_out, 16);
     const long long n = (long long)a.H * state / (four ? 4 : 1);
     const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), (unsigned)std::min(a.nseq, 65535), (unsigned)a.npass);
     L.begin("linattn_scan");
@@ -416,6 +432,26 @@ cudaError_t launch_scan(const WalkArgs& a, Launch& L) {
         segment_scan_kernel<4><<<grid, kThreads, 0, L.stream>>>(a);
     else
         segment_scan_kernel<1><<<grid, kThreads, 0, L.stream>>>(a);
+    return L.end();
+}
+
+// On the tensor cores the final states of a pass come from the sums (linattn_tc_sums), so that the walk
+// does without exact ones: of sequences that are cut by the scan over them, of long ones with states of 128
+// channels by a pass of their own, into the final states themselves.
+bool sums_pay(const WalkArgs& a, const Pass& p) {
+    return p.s_out && (a.Ls || ((p.kd == 128 || p.vd == 128) && !a.cu && a.rowlen >= 1024));
+}
+cudaError_t final_states(const WalkArgs& a, const Pass& p, int dtype, Launch& L) {
+    WalkArgs f = a;
+    f.pass[0] = p;
+    f.npass = 1;
+    f.pass[0].s_sum = p.s_out;
+    cudaError_t e = launch_walk(f, true, true, dtype, L);
+    if (e != cudaSuccess || !p.s_in) return e;
+    const long long n = (long long)a.H * p.kd * p.vd;
+    L.begin("linattn_final");
+    final_state_kernel<<<dim3((unsigned)((n + kThreads - 1) / kThreads), (unsigned)std::min(a.nseq, 65535)),
+                         kThreads, 0, L.stream>>>(f);
     return L.end();
 }
 
@@ -510,12 +546,17 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
         set_last_launches(L.count);
         return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
     }
+    const bool by_sums = tc && sums_pay(a, f);
     if (l.Ls) {
+        if (!by_sums) f.s_out = nullptr;  // the walk's
         f.s_sum = reinterpret_cast<float*>(ws + l.s_seg);
         err = launch_walk(a, tc, true, p.dtype, L);
         if (err == cudaSuccess) err = launch_scan(a, L);
         f.s_seg = f.s_sum;
+    } else if (by_sums) {
+        err = final_states(a, f, p.dtype, L);
     }
+    f.s_out = by_sums ? nullptr : final_state;
     if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
     set_last_launches(L.count);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
@@ -584,6 +625,7 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
+    const bool by_sums = tc && sums_pay(a, d);
     if (l.Ls) {
         // the states by segments from k and v, their adjoints from q and do
         WalkArgs s = a;
@@ -591,11 +633,15 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
         s.pass[0].s_sum = reinterpret_cast<float*>(ws + l.s_seg);
         s.pass[1] = d;
         s.pass[1].s_sum = reinterpret_cast<float*>(ws + l.r_seg);
+        if (!by_sums) s.pass[1].s_out = nullptr;
         err = launch_walk(s, tc, true, p.dtype, L);
         if (err == cudaSuccess) err = launch_scan(s, L);
         f.s_seg = s.pass[0].s_sum;
         g.s_seg = d.s_seg = s.pass[1].s_sum;
+    } else if (by_sums) {
+        err = final_states(a, d, p.dtype, L);
     }
+    if (by_sums) d.s_out = nullptr;
     if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
     if (r > 1 && err == cudaSuccess)
         err = launch_shared_sum(static_cast<const float*>(g.out), dk, p, T, (int)N, p.dk_stride, L);

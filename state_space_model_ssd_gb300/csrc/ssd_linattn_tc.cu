@@ -713,7 +713,9 @@ done:
 // ---------------------------------------------------------------- sums over segments
 // U = k^T W over a whole segment, each token weighted by its power to the segment's end (or, in a
 // walk from the end, its start), in one accumulation: the state after the segment from none before.
-// Bound by the bytes of k and v.
+// Bound by the bytes of k and v.  Where the final states are wanted it takes the last segments too, with
+// three terms, and the walk does with two: in shared memory the third leaves a walk over 128 channels
+// two places for v, where three keep it going (32768 tokens of 80 heads, 64 x 128: 509 against 338 us).
 template <int NT>
 __global__ void __launch_bounds__(kSumThreads, 1)
     tc_sums_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
@@ -738,8 +740,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     Item& t = x->items[warp];
     int g = 0, m = 0;  // chunks and items of this block so far
     Place st, w_set;   // of two sets of weights one chunk's are made while the other's are read
-    const auto wanted = [](const Item& t) {  // nothing comes after a walk's last segment
-        return t.g.there && t.g.k != (t.rev ? 0 : t.g.cnt - 1);
+    const auto wanted = [](const Item& t) {  // nothing but the final state comes after a walk's last segment
+        return t.g.there && (t.p->s_out || t.g.k != (t.rev ? 0 : t.g.cnt - 1));
     };
     const auto next_item = [&](int item) {
         __syncwarp();
@@ -757,6 +759,15 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             if (!next_item(item)) continue;
             const int chunks = t.chunks, len = t.g.len, rev = t.rev, kb = t.kb;
             const float ld2 = t.ld2, su = t.su;
+            const long long sp = t.p->sp;
+            float* out = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
+                         (t.v0 + 16 * part) * sp;
+            if (chunks == 0) {  // an empty sequence; the products' warp passes it over
+                if (i < t.p->kd)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) out[e * sp] = 0.f;
+                continue;
+            }
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, ++g, st.next(geo.stages), w_set.next(2)) {
                 const int at = c * kQ + i;
@@ -778,9 +789,6 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             tc_fence_before();
             arrive(&x->sums_free);
             if (i < t.p->kd) {
-                const long long sp = t.p->sp;
-                float* out = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
-                             (t.v0 + 16 * part) * sp;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float f[2];
@@ -817,6 +825,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             if (!next_item(item)) continue;
             const int kb = same(t.kb), chunks = same(t.chunks);
+            if (chunks == 0) continue;
             if (m > 0 && !wait_warp(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
             for (int c = 0; c < chunks; ++c, st.next(geo.stages), w_set.next(2)) {
                 if (!wait_warp(&x->made[w_set.s], w_set.phase, &x->stop, status)) goto stopped;
