@@ -301,6 +301,7 @@ struct Plan {
     int Ls, per;
     long long ids;
     size_t s_seg, r_seg, dk_part, dv_part, total;
+    bool fits;                   // its items are fewer than 2^31
 };
 
 ssd_status_t check_sizes(const ssd_linattn_t* p, bool bwd) {
@@ -373,6 +374,7 @@ Plan make_plan(const ssd_linattn_t& p, bool bwd) {
     }
     l.per = l.Ls ? (int)((p.seqlen + l.Ls - 1) / l.Ls) : 1;
     l.ids = !l.Ls ? l.n : p.nseq ? l.T / l.Ls + l.n : (long long)l.n * l.per;
+    l.fits = 2 * l.ids * per_cut <= INT_MAX;  // twice: rows off 16 bytes take the plain walk, in tiles of 32
     const size_t state = (size_t)p.headdim * p.dstate * sizeof(float);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -409,7 +411,6 @@ void set_tiles(WalkArgs& a, int tile) {
 
 cudaError_t launch_walk(WalkArgs a, bool tc, bool sums, int dtype, Launch& L) {
     set_tiles(a, tc ? kTcTile : kSimtTile);
-    if (a.ids * a.H * a.tiles > INT_MAX) return cudaErrorInvalidConfiguration;
     if (tc) return sums ? tc_sums(a, L) : tc_walk(a, L);
     L.begin(sums ? "linattn_sums" : "linattn_walk");
     const bool b = dtype == SSD_DTYPE_BF16;
@@ -495,7 +496,9 @@ ssd_status_t ssd_linear_attention_workspace_size(const ssd_linattn_t* prob, int 
     if (!bytes) return SSD_ERR_INVALID_ARG;
     const ssd_status_t st = check_sizes(prob, for_backward != 0);
     if (st != SSD_OK) return st;
-    *bytes = make_plan(*prob, for_backward != 0).total;
+    const Plan l = make_plan(*prob, for_backward != 0);
+    if (!l.fits) return SSD_ERR_UNSUPPORTED;
+    *bytes = l.total;
     return SSD_OK;
 }
 
@@ -517,6 +520,7 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
         !aligned_to(final_state, 4) || !aligned_to(workspace, 256))
         return SSD_ERR_ALIGNMENT;
     const Plan l = make_plan(p, false);
+    if (!l.fits) return SSD_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSD_ERR_WORKSPACE;
     const long long states = (long long)l.n * H * P * N;
     if (rows_clash({Rows(o, T, p.o_stride, H * P, e), Rows(final_state, states, 4), Rows(workspace, l.total, 1)},
@@ -582,6 +586,7 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
         !aligned_to(d_initial_state, 4) || !aligned_to(workspace, 256))
         return SSD_ERR_ALIGNMENT;
     const Plan l = make_plan(p, true);
+    if (!l.fits) return SSD_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSD_ERR_WORKSPACE;
     const long long states = (long long)l.n * H * P * N;
     if (rows_clash({Rows(dq, T, p.dq_stride, H * N, e), Rows(dk, T, p.dk_stride, G * N, e),

@@ -26,6 +26,7 @@
 // for each item, the dearest first.  The tiles of all passes of one segment and head are next to one
 // another, so that what they all read comes from L2 after the first.
 #include <algorithm>
+#include <utility>
 
 #include "layer_device.cuh"
 #include "linattn.cuh"
@@ -105,7 +106,7 @@ __device__ __noinline__ void take(const WalkArgs& a, int by_pass, int item, Item
              ((long long)(t->h / p.outr) * p.vd + t->v0) * (p.out_f32 ? 4 : 2);
 }
 // Barriers and what else is small, behind the tiles.
-constexpr int kBelow = 31;  // zeros before a^0
+constexpr int kBelow = 32;  // zeros before a^0
 struct Aux {
     uint64_t full[kMostStages], empty[kMostStages], full_v[kMostStages], empty_v[kMostStages], weights[kMostStages],
         outputs[kMostStages];
@@ -116,7 +117,7 @@ struct Aux {
     // the order of the columns: a^127 .. a^0 and kBelow zeros, or, in a walk from the end, the zeros and
     // a^0 .. a^127; made by the warp that copies in
     Item items[2];
-    float powers[2][kBelow + kQ];
+    alignas(16) float powers[2][kBelow + kQ];
 };
 struct SumsAux {
     uint64_t full[kMostStages], empty[kMostStages], made[2], used[2], sums, sums_free;
@@ -424,6 +425,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const int rev = t.rev, chunks = t.chunks;
             const bool some0 = rev ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31;
             const bool some1 = rev ? j1 + 15 >= 32 * quad : j1 <= 32 * quad + 31;
+            // of a group off the diagonal: the row's power to its nearer column
+            const float r0 = power(t.ld2, max(rev ? j0 - i : i - j0 - 15, 0));
+            const float r1 = power(t.ld2, max(rev ? j1 - i : i - j1 - 15, 0));
             const float fx_whole = power(t.ld2, rev ? kQ - 1 - i : i + 1) * t.sx;
             const float w_whole = power(t.ld2, rev ? i + 1 : kQ - 1 - i) * t.su;
 
@@ -438,11 +442,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     if (!wait_peeked(seen, &x->scores, k & 1, &x->stop, status)) goto done;
                     tc_fence_after();
                     // times a^distance, or 0 on the other side of the diagonal
-                    const float* f = x->powers[it.s] + (rev ? kBelow : kQ - 1) - i;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = u ? j1 : j0;
-                        const float* at = f + j;
                         uint32_t s[16];
                         if (u ? some1 : some0) {
                             tmem_ld16(mine + C::scores + j, s);
@@ -452,9 +454,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                 for (int e = 0; e < 16; ++e)
                                     if (j + e >= n) s[e] = 0u;
                             }
+                            if (j >> 5 == quad) {  // at the diagonal: the table from the row's place on
+                                const float* at = x->powers[it.s] + (rev ? kBelow : kQ - 1) - i + j;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(at[2 * e], at[2 * e + 1])));
+                                for (int e = 0; e < 8; ++e)
+                                    s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(at[2 * e], at[2 * e + 1])));
+                            } else {  // a^15 .. a^0, or from the end a^0 .. a^15, the same for all rows
+                                const float4* at = reinterpret_cast<const float4*>(x->powers[it.s] + (rev ? kBelow : kQ - 16));
+                                const F2 r = layer::both<F2>(u ? r1 : r0);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float4 f = at[e];
+                                    s[2 * e] = pack(layer::mul_(pair(s[4 * e], s[4 * e + 1]), layer::mul_(r, layer::join(f.x, f.y))));
+                                    s[2 * e + 1] = pack(layer::mul_(pair(s[4 * e + 2], s[4 * e + 3]), layer::mul_(r, layer::join(f.z, f.w))));
+                                }
+                            }
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) s[e] = 0u;
@@ -917,8 +931,8 @@ cudaError_t tc_walk(const WalkArgs& given, Launch& L) {
     WalkArgs a = given;
     // whole sequences: a block for each item, those with the larger states first
     const bool by_pass = !a.Ls && !a.cu && a.rowlen >= 16 * kQ;
-    if (by_pass)
-        std::stable_sort(a.pass, a.pass + a.npass, [](const Pass& x, const Pass& y) { return x.kd > y.kd; });
+    for (int i = 1; by_pass && i < a.npass; ++i)
+        for (int j = i; j > 0 && a.pass[j].kd > a.pass[j - 1].kd; --j) std::swap(a.pass[j], a.pass[j - 1]);
     Maps m;
     if (!make_maps(a, &m)) return cudaErrorInvalidValue;
     const bool three = exact_states(a);

@@ -56,6 +56,23 @@ def test_select_ties(ssd):
     _same(ssd.beam_select(x, s, 64), ref.beam_select(x, s, 64))
 
 
+@pytest.mark.parametrize("V", [4095, 4096, 4097, 8192, 12289])
+def test_select_slices(ssd, V):
+    """Borders of slices, with enough rows for the wide ones; slices of equal logits, which outnumber
+    the list of candidates, take the long way."""
+    import torch
+    x, s = _make(40, 4, V, torch.float32, seed=V)
+    x[3] = torch.round(x[3])
+    x[4] = 0.0
+    x[5, :, ::2] = -torch.inf
+    x[6] = -torch.inf
+    x[6, :, 17] = 1.0
+    x[7] = x[7, :1]
+    s[7] = -1.0
+    for keep in (1, 9, 64):
+        _same(ssd.beam_select(x, s, keep), ref.beam_select(x, s, keep))
+
+
 def test_select_order_of_the_vocabulary(ssd):
     """Rising and falling logits, and the best in one thread's reach."""
     import torch
@@ -121,6 +138,22 @@ def test_reorder(ssd, B, K, kind):
             b[to] = b[frm]
         assert torch.equal(c, b)
     assert torch.equal(wide[:, :5], rest[:, :5]) and torch.equal(wide[:, 2500:], rest[:, 2500:])
+
+
+def test_select_on_another_stream_into_given_outputs(ssd):
+    import torch
+    x, s = _make(3, 4, 3000, torch.bfloat16, seed=8)
+    want = ssd.beam_select(x, s, 6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = tuple(torch.empty_like(t) for t in want)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    got = ssd.beam_select(x, s, 6, out=out, workspace=ws, stream=side)
+    new = ssd.beam_reorder([], want[1][:, :4].contiguous(), want[1][:, :4].contiguous(), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b, c in zip(want, got, out):
+        assert torch.equal(a, b) and b.data_ptr() == c.data_ptr()
+    assert new.shape == (3, 4)
 
 
 def test_reorder_leaves_slots_outside_the_cache(ssd):

@@ -129,6 +129,60 @@ def test_tensor_cores(ssd, shape):
     _backward(ssd, s, True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,cu", [(1, None), (2, None), (16, None), (17, None), (16, [0, 0, 5, 5, 12]), (9, [0, 9])])
+@pytest.mark.parametrize("B,H,G,P,N", [(1, 4, 2, 64, 128), (3, 2, 1, 100, 12), (2, 3, 3, 5, 7), (1, 80, 80, 64, 64)])
+def test_a_few_tokens(ssd, B, H, G, P, N, L, cu, dtype):
+    """Up to sixteen tokens a sequence are stepped through, in float32; one more is a walk."""
+    if cu is not None and B > 1:
+        B = 1
+    s = _make(B, L, H, G, P, N, dtype, cu, True, L % 2 == 1)
+    walk = L > 16 and dtype == "bf16" and P % 64 == 0 and N % 64 == 0
+    o, _ = _forward(ssd, s, walk)
+    if cu is not None:
+        assert not o[:, cu[-1]:].any()
+
+
+# the forms of the launch: whole sequences by the pass, states of 128 channels by sums of their own, cut
+# sequences with their final states from the scan, one long sequence of many segments
+@pytest.mark.parametrize("B,L,H,G,P,N,state,strided", [(4, 2100, 26, 26, 64, 64, True, False),
+                                                       (4, 2100, 26, 13, 64, 64, False, True),
+                                                       (8, 1100, 20, 20, 128, 128, True, False),
+                                                       (6, 1024, 30, 10, 64, 128, True, True),
+                                                       (2, 5000, 3, 1, 64, 128, True, False)])
+def test_forms_of_the_launch(ssd, B, L, H, G, P, N, state, strided):
+    s = _make(B, L, H, G, P, N, "bf16", None, state, strided, seed=11)
+    _forward(ssd, s, True)
+    _backward(ssd, s, True)
+
+
+def test_offsets_beyond_32_bits(ssd):
+    """Tokens whose elements lie beyond 2^31: the end of a long sequence is that of a short one that goes
+    on from its state."""
+    import torch
+    T, H, N, P = 290000, 60, 128, 64
+    assert T * H * N > 2 ** 31
+    q = torch.randn(1, T, H, N, device="cuda", dtype=torch.bfloat16)
+    k = torch.randn(1, T, H, N, device="cuda", dtype=torch.bfloat16)
+    v = torch.randn(1, T, H, P, device="cuda", dtype=torch.bfloat16)
+    ld = -torch.exp2(-2.0 - 6.0 * torch.arange(H, device="cuda") / H).float()
+    o, final = ssd.linear_attention_forward(q, k, v, ld, final_state=True)
+    cut = T - 1000
+    _, state = ssd.linear_attention_forward(q[:, cut - 20000:cut], k[:, cut - 20000:cut], v[:, cut - 20000:cut], ld,
+                                            final_state=True)   # e^(-20000 / 256) of what was before is gone
+    o1, final1 = ssd.linear_attention_forward(q[:, cut:], k[:, cut:], v[:, cut:], ld, initial_state=state,
+                                              final_state=True)
+    # two float32 sums of thousands of terms in other orders; outputs rounded to bfloat16 thrice
+    assert (final - final1).norm() <= 1e-5 * final.norm()
+    d = (o[:, cut:].float() - o1.float()).norm()
+    assert d <= 3 * ref.EPS16 * o1.float().norm()
+    g = ssd.linear_attention_backward(q, k, v, ld, o)
+    g1 = ssd.linear_attention_backward(q[:, cut:], k[:, cut:], v[:, cut:], ld, o[:, cut:], initial_state=state)
+    for n in ("dq", "dk", "dv"):
+        a, b = g[n][:, cut:].float(), g1[n].float()
+        assert (a - b).norm() <= 3 * ref.EPS16 * b.norm(), n
+
+
 @pytest.mark.parametrize("P,N", [(64, 64), (128, 128), (24, 40)])
 @pytest.mark.parametrize("ld", [0.0, -1e-6, -30.0, -1e9, float("-inf")])
 def test_decays(ssd, ld, P, N):
