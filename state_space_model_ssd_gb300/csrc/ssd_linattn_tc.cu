@@ -16,15 +16,21 @@
 // tokens below the diagonal, so that nothing overflows.
 //
 // One block an SM: sixteen warps that all go through the same steps of a chunk (mask, state, the next
-// chunk's weights, outputs), each on its 32 rows and a quarter of the columns, a warp for the copies
-// in (TMA, two or three chunks ahead), and one for those out, and two that issue products: A and O1 in one, U and O2 in
-// the other.  While the warps are at one step, the products of the steps before run.  Warps with a task
-// each (mask, state, weights, outputs side by side) were 1.3 to 1.5 times slower: four streams of
-// instructions that each go straight through a few hundred of them leave the instruction caches
-// nothing to share (a third of the stalls), while here sixteen warps follow one another.
+// chunk's weights, outputs), each on its 32 rows and a quarter of the columns; a warp for the items and the
+// copies in (TMA, two to four chunks ahead), one for the copies out, and two that issue products: A and
+// O1 in one, O2 and U in the other.  While the sixteen are at one step, the products of the steps before
+// run.  Two things decide the pace.  Instructions: with a task for each four warps (mask, outputs, state,
+// weights side by side) every stream goes straight through some hundred instructions a chunk and the
+// caches hold 79 % of them, against 95 % where sixteen warps follow one another (32768 tokens of 80
+// heads forward 400 us, so 345).  And the stack: beside the tiles nothing is left of L1 for it, see Item.
 // Blocks stay and take items in turn, or, where items are long and of unequal cost, there is a block
 // for each item, the dearest first.  The tiles of all passes of one segment and head are next to one
 // another, so that what they all read comes from L2 after the first.
+//
+// GB300, 32768 tokens of 80 heads, 64 x 128 states: forward 338 us for the walk (88 % of the copy rate on its
+// bytes), 170 for the sums, 22 for the scan; backward, five tiles for each head's chunk, 1337 us:
+// 3700 cycles for a tile's chunk with 55 % of the issue slots and a third of the tensor pipe in use, no
+// step of it more than 9 % by itself.
 #include <algorithm>
 #include <utility>
 
@@ -120,7 +126,7 @@ struct Aux {
     alignas(16) float powers[2][kBelow + kQ];
 };
 struct SumsAux {
-    uint64_t full[kMostStages], empty[kMostStages], made[2], used[2], sums, sums_free;
+    uint64_t full[kMostStages], empty[kMostStages], made[2], used[2], sums[2], sums_free[2];
     uint32_t tmem;
     int stop;
     Item items[kSumThreads / 32];  // of each warp
@@ -498,20 +504,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     tc_fence_before();
                 }
                 if (c + 1 < chunks) {
-                    // ---- for the next chunk: S as bf16 and the weights; q S and the sums before, which came
-                    // with one another, have read the last ones
-                    if (state_row) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<uint4*>(s_tile + i * 128 + (((2 * part + e) ^ (i & 7)) << 4)) =
-                                make_uint4(pack(S[4 * e]), pack(S[4 * e + 1]), pack(S[4 * e + 2]), pack(S[4 * e + 3]));
-                    }
+                    // ---- for the next chunk: the weights and S as bf16 (at an item's start its loads arrive
+                    // meanwhile); q S and the sums before, which came with one another, have read the last ones
                     const int m = c + 1 == short_one ? short_n : kQ;
                     unsigned char* v = sm + geo.v_at + vv.s * kSub;
                     if (!wait_peeked(c >= 0 && seen, &x->full_v[vv.s], vv.phase, &x->stop, status)) goto done;
                     const bool in = i < m;
                     const float w = m == kQ || rev ? w_whole : power(t.ld2, max(m - 1 - i, 0)) * t.su;
                     split_row<NT>(v, w_tile, i, 2 * part, 2, w, in);
+                    if (state_row) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint4*>(s_tile + i * 128 + (((2 * part + e) ^ (i & 7)) << 4)) =
+                                make_uint4(pack(S[4 * e]), pack(S[4 * e + 1]), pack(S[4 * e + 2]), pack(S[4 * e + 3]));
+                    }
                     seen = c >= 0 && peek(&x->outs, k & 1);
                     if (m < kQ) {  // rows of other sequences meet zeros, which an infinity or a NaN would outlive
                         if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status)) goto done;
@@ -725,8 +731,12 @@ done:
 }
 
 // ---------------------------------------------------------------- sums over segments
+constexpr int kRun = 4;
+
 // U = k^T W over a whole segment, each token weighted by its power to the segment's end (or, in a
-// walk from the end, its start), in one accumulation: the state after the segment from none before.
+// walk from the end, its start): the state after the segment from none before.  The tensor cores
+// accumulate kRun chunks, whose sums are added up in registers: over 4096 tokens in one accumulation,
+// which does not round to nearest, a slowly decaying state was off by 3e-6.
 // Bound by the bytes of k and v.  Where the final states are wanted it takes the last segments too, with
 // three terms, and the walk does with two: in shared memory the third leaves a walk over 128 channels
 // two places for v, where three keep it going (32768 tokens of 80 heads, 64 x 128: 509 against 338 us).
@@ -743,16 +753,16 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         // a chunk's copies are announced in two steps
         for (int s = 0; s < geo.stages; ++s) mbar_init(&x->full[s], 2), mbar_init(&x->empty[s], 1);
         for (int s = 0; s < 2; ++s) mbar_init(&x->made[s], kTeam), mbar_init(&x->used[s], 1);
-        mbar_init(&x->sums, 1), mbar_init(&x->sums_free, kTeam);
+        for (int s = 0; s < 2; ++s) mbar_init(&x->sums[s], 1), mbar_init(&x->sums_free[s], kTeam);
         x->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 17) tmem_alloc(&x->tmem, 128);
+    if (warp == 17) tmem_alloc(&x->tmem, 256);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = x->tmem;
     Item& t = x->items[warp];
-    int g = 0, m = 0;  // chunks and items of this block so far
+    int g = 0, m = 0;  // chunks and runs of this block so far
     Place st, w_set;   // of two sets of weights one chunk's are made while the other's are read
     const auto wanted = [](const Item& t) {  // nothing but the final state comes after a walk's last segment
         return t.g.there && (t.p->s_out || t.g.k != (t.rev ? 0 : t.g.cnt - 1));
@@ -769,50 +779,73 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     };
     if (warp < kTeam) {
         // ------------------------------------------------ weights: a row, a quarter of the columns a thread
+        // what the run before has left is read one run later, when its products are done; the item that its
+        // last run ends has `out` for the whole
+        F2 acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = layer::both<F2>(0.f);
+        float* out = nullptr;
+        int sp = 0;
+        bool ends = false, row = false;
+        const auto read_run = [&] {
+            if (!wait_warp(&x->sums[(m - 1) & 1], ((m - 1) >> 1) & 1, &x->stop, status)) return false;
+            tc_fence_after();
+            const uint32_t from = tmem + lane_base + ((m - 1) & 1) * 2 * kV + 16 * part;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                F2 u[4];
+                load_sum8(from + 8 * h, u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[4 * h + e] = layer::add_(acc[4 * h + e], u[e]);
+            }
+            tc_fence_before();
+            arrive(&x->sums_free[(m - 1) & 1]);
+            if (ends) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float f[2];
+                    layer::split(acc[e], f);
+                    if (row) out[2 * e * sp] = f[0], out[(2 * e + 1) * sp] = f[1];
+                    acc[e] = layer::both<F2>(0.f);
+                }
+                __syncwarp();
+            }
+            return true;
+        };
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             if (!next_item(item)) continue;
-            const int chunks = t.chunks, len = t.g.len, rev = t.rev, kb = t.kb;
-            const float ld2 = t.ld2, su = t.su;
-            const long long sp = t.p->sp;
-            float* out = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
-                         (t.v0 + 16 * part) * sp;
+            const int chunks = t.chunks;
             if (chunks == 0) {  // an empty sequence; the products' warp passes it over
+                float* zero = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
+                              (t.v0 + 16 * part) * t.p->sp;
                 if (i < t.p->kd)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) out[e * sp] = 0.f;
+                    for (int e = 0; e < 16; ++e) zero[e * t.p->sp] = 0.f;
                 continue;
             }
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, ++g, st.next(geo.stages), w_set.next(2)) {
                 const int at = c * kQ + i;
                 unsigned char* v = sm + st.s * geo.stage_bytes + kbytes;
-                const bool in = at < len;
-                const float w = in ? power(ld2, rev ? at + 1 : len - 1 - at) * su : 0.f;
+                const bool in = at < t.g.len;
+                const float w = in ? power(t.ld2, t.rev ? at + 1 : t.g.len - 1 - at) * t.su : 0.f;
                 if (!wait_warp(&x->full[st.s], st.phase, &x->stop, status)) goto done;
                 if (g >= 2 && !wait_warp(&x->used[w_set.s], w_set.phase ^ 1u, &x->stop, status)) goto done;
                 split_row<NT>(v, sm + geo.w_at + w_set.s * NT * kSub, i, 2 * part, 2, w, in);
-                if (!in && part < kb) zero_row(v - kbytes + part * kSub, i);
+                if (!in && part < t.kb) zero_row(v - kbytes + part * kSub, i);
                 fence_proxy_async();
                 arrive(&x->made[w_set.s]);
-            }
-            if (!wait_warp(&x->sums, m & 1, &x->stop, status)) goto done;
-            tc_fence_after();
-            F2 u[8];
-            load_sum8(tmem + lane_base + 16 * part, u);
-            load_sum8(tmem + lane_base + 16 * part + 8, u + 4);
-            tc_fence_before();
-            arrive(&x->sums_free);
-            if (i < t.p->kd) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float f[2];
-                    layer::split(u[e], f);
-                    out[2 * e * sp] = f[0], out[(2 * e + 1) * sp] = f[1];
+                if (c % kRun == 0) {
+                    if (m > 0 && !read_run()) goto done;
+                    ++m;
+                    ends = c + kRun >= chunks;
+                    sp = (int)t.p->sp, row = i < t.p->kd;
+                    out = t.p->s_sum + (t.id * a.H + t.h) * (long long)t.p->kd * t.p->vd + i * t.p->sn +
+                          (t.v0 + 16 * part) * t.p->sp;
                 }
             }
-            __syncwarp();
-            ++m;
         }
+        if (m > 0 && !read_run()) goto done;
     } else if (warp == 16) {
         // ------------------------------------------------ copies in
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
@@ -839,31 +872,32 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x) {
             if (!next_item(item)) continue;
             const int kb = same(t.kb), chunks = same(t.chunks);
-            if (chunks == 0) continue;
-            if (m > 0 && !wait_warp(&x->sums_free, (m - 1) & 1, &x->stop, status)) break;
             for (int c = 0; c < chunks; ++c, st.next(geo.stages), w_set.next(2)) {
+                if (c % kRun == 0 && m > 1 && !wait_warp(&x->sums_free[m & 1], ((m >> 1) - 1) & 1, &x->stop, status))
+                    goto stopped;
                 if (!wait_warp(&x->made[w_set.s], w_set.phase, &x->stop, status)) goto stopped;
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_sums<NT>(tm, base + st.s * geo.stage_bytes, base + geo.w_at + w_set.s * NT * kSub, kb, c > 0);
+                    mma_sums<NT>(tm + (m & 1) * 2 * kV, base + st.s * geo.stage_bytes,
+                                 base + geo.w_at + w_set.s * NT * kSub, kb, c % kRun > 0);
                     mma_commit(&x->empty[st.s]);
                     mma_commit(&x->used[w_set.s]);
-                    if (c + 1 == chunks) mma_commit(&x->sums);
+                    if (c % kRun == kRun - 1 || c + 1 == chunks) mma_commit(&x->sums[m & 1]);
                 }
+                m += c % kRun == kRun - 1 || c + 1 == chunks;
             }
-            ++m;
         }
     stopped:
         if (*(volatile int*)&x->stop) {
-            if (elect_one()) mma_commit(&x->sums);
-            for (int k = 0; k < 2; ++k) drain(&x->sums, k);
+            if (elect_one()) mma_commit(&x->sums[0]);
+            for (int k = 0; k < 2; ++k) drain(&x->sums[0], k);
         }
     }
 done:
     __syncthreads();
     if (warp == 17) {
         tmem_relinquish();
-        tmem_dealloc(tmem, 128);
+        tmem_dealloc(tmem, 256);
     }
 }
 

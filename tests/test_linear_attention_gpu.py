@@ -156,6 +156,41 @@ def test_forms_of_the_launch(ssd, B, L, H, G, P, N, state, strided):
     _backward(ssd, s, True)
 
 
+@pytest.mark.parametrize("B,L,H,P,N", [(8, 4096, 20, 128, 128), (2, 4096, 32, 128, 64), (1, 16384, 8, 64, 64),
+                                       (4, 4096, 40, 64, 64)])
+def test_states_of_slow_decays_keep_their_bits(ssd, B, L, H, P, N):
+    """States that thousands of tokens are summed into: off by 2^-19 of their size at most, in each
+    direction.  The weighted values are split to 2^-25.  The tensor cores' sums may cut off instead of
+    rounding: 512 tokens are 96 additions of 16, each of which loses half of 2^-23 of a sum in the mean
+    that is itself half its size in the mean: 96 * 2^-25 = 2^-18.4 of that run's part, and a run is at
+    most half of what a state of 4096 tokens and these decays holds."""
+    import torch
+    s = _make(B, L, H, H, P, N, "bf16", state=True, seed=13)
+    ld = -torch.exp2(-6 - 6 * torch.arange(H, device="cuda") / (H - 1)).float()
+    _, final = ssd.linear_attention_forward(s["q"], s["k"], s["v"], ld, initial_state=s["init"], final_state=True,
+                                            scale=s["scale"])
+    back = ssd.linear_attention_backward(s["q"], s["k"], s["v"], ld, s["do"], scale=s["scale"],
+                                         initial_state=s["init"], d_final_state=s["dfinal"], d_initial_state=True)
+    a = ld.double()
+
+    def walk(S, rows, cols, blocks, weight):
+        for lo in blocks:
+            hi = min(lo + 64, L)
+            t = torch.arange(hi - lo, device="cuda", dtype=torch.float64)
+            w = torch.exp(a[:, None] * weight(t, hi - lo))
+            S = S * torch.exp(a * (hi - lo))[:, None, None] + torch.einsum(
+                "bthp,ht,bthn->bhpn", rows[:, lo:hi].double(), w, cols[:, lo:hi].double())
+        return S
+
+    ends = {"final": (final, walk(s["init"].double(), s["v"], s["k"], range(0, L, 64), lambda t, m: m - 1 - t)),
+            "d_initial": (back["d_initial_state"],
+                          walk(s["dfinal"].double(), s["do"].double() * s["scale"], s["q"],
+                               reversed(range(0, L, 64)), lambda t, m: t + 1))}
+    for name, (got, exact) in ends.items():
+        off = (got.double() - exact).norm(dim=(2, 3)) / exact.norm(dim=(2, 3))
+        assert off.max().item() <= 2.0 ** -19, (name, off.max().item())
+
+
 def test_offsets_beyond_32_bits(ssd):
     """Tokens whose elements lie beyond 2^31: the end of a long sequence is that of a short one that goes
     on from its state."""
