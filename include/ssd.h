@@ -431,7 +431,9 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
  * clamped as in the convolution; outputs of tokens behind the last sequence are zero.  bf16
  * calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
  * blocks of 128 tokens: there a NaN or an infinity in a token reaches the outputs of all tokens
- * of its sequence in its block.  Others run the same walk on the plain cores. */
+ * of its sequence in its block.  Forwards of up to 16 tokens a sequence (a batch row, or all packed
+ * ones) are stepped through token by token, and all other calls run the walk on the plain cores, in
+ * float32. */
 typedef struct {
     int64_t batch;       /* rows of a dense batch; 1 with cu_seqlens */
     int64_t seqlen;      /* tokens per row; with cu_seqlens: all tokens T (<= 2^31 - 1) */
