@@ -18,45 +18,81 @@ using namespace layer;
 
 constexpr int kThreads = 256;
 constexpr int kQ = 32;           // tokens of a chunk
-constexpr int kVT = kSimtTile;
-constexpr int kVS = kVT + 1;     // rows of shared memory one word apart from a multiple of 32
+constexpr int kRows = kQ / 8;    // of them, what a warp loads
 
-__host__ __device__ constexpr size_t simt_smem(int kd) {
-    return sizeof(float) * (2 * (size_t)kQ * (kd + 1) + 2 * (size_t)kQ * kVS + (size_t)kd * kVS + kQ + 2);
+// Rows of q and k in shared memory are an odd number of 16 bytes long: eight threads read four channels
+// of eight rows in one go (20720 tokens of 7 heads, 90 x 90, at an even one: 840 us, so 524).
+__host__ __device__ constexpr int whole4(int kd) { return (kd + 3) / 4 * 4; }
+__host__ __device__ constexpr int row_words(int kd) { return (whole4(kd) / 4 | 1) * 4; }
+__host__ __device__ constexpr size_t simt_smem(int kd, int vt) {
+    return sizeof(float) * (2 * (size_t)kQ * row_words(kd) + 2 * (size_t)kQ * vt + (size_t)kQ * (kQ + 1) +
+                            (size_t)whole4(kd) * (vt + 4) + kQ + 2);
 }
 
-// One segment, head and tile of v's columns: 32 tokens at a time, everything in float32 in
-// shared memory, each thread a 2 x 2 piece of the 32 x 32 products and up to 4 x 4 of the state.
-// Bound by shared memory: the four products read two words for two multiply-adds.  It serves
-// float32 and the sizes that the tensor cores do not take.  OUT: false where only the state after
-// the segment is wanted.
-template <typename T, bool OUT>
-__global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_constant__ WalkArgs a) {
-    extern __shared__ float sm[];
+__device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+}
+// o += a b for VPT neighbouring columns
+template <int VPT>
+__device__ __forceinline__ void add_row(float* o, float a, const float* b) {
+    if constexpr (VPT == 4) {
+        const float4 f = four(b);
+        o[0] = fmaf(a, f.x, o[0]), o[1] = fmaf(a, f.y, o[1]), o[2] = fmaf(a, f.z, o[2]), o[3] = fmaf(a, f.w, o[3]);
+    } else {
+        const float2 f = *reinterpret_cast<const float2*>(b);
+        o[0] = fmaf(a, f.x, o[0]), o[1] = fmaf(a, f.y, o[1]);
+    }
+}
+template <int VPT, typename O>
+__device__ __forceinline__ void put_row(O* p, const float* f, int n, bool vec) {
+    if (vec && n >= VPT) {
+        store_vec<VPT>(p, f);
+        return;
+    }
+#pragma unroll
+    for (int y = 0; y < VPT; ++y)
+        if (y < n) st_out(p, y, f[y]);
+}
+
+// One segment, head and tile of VT columns of v: 32 tokens at a time, everything in float32 in
+// shared memory.  A thread has the rows i and i + 16 of the products, one or two columns of the scores
+// and VT / 16 of the outputs, and pieces of 4 x 4 of the state; the next chunk's rows come into registers
+// meanwhile.  Operands are read four at a time, so that multiply-adds and shared memory take about as
+// long.  Bound by the issue of instructions, 65 % of which are multiply-adds at 128 channels (32768 tokens of
+// 16 heads in float32, 64 x 128: 947 us for the walk, 367 for the sums; with 2 x 2 pieces read word by word
+// 1516 and 654).  It serves float32 and the sizes that the tensor cores do not take.  OUT: false where only the
+// state after the segment is wanted.
+template <typename T, bool OUT, int VT>
+__global__ void __launch_bounds__(kThreads, 2) simt_walk_kernel(const __grid_constant__ WalkArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int VPT = VT / 16, kS = VT + 4;
     const long long item = blockIdx.x;
     const long long id = item / ((long long)a.tiles * a.H);
     const int rest = (int)(item - id * a.tiles * a.H);
     const int h = rest / a.tiles;
     int tile = rest - h * a.tiles;
     const Pass& p = pass_of(a, tile);
-    const int v0 = tile * kVT, vw = min(kVT, p.vd - v0);
-    const int tid = threadIdx.x, kd = p.kd, ks1 = kd + 1;
+    const int v0 = tile * VT, vw = min(VT, p.vd - v0);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int kd = p.kd, kd4 = whole4(kd), ks1 = row_words(kd);
     float* qs = sm;
     float* ks = qs + kQ * ks1;
-    float* vs = ks + kQ * ks1;
-    float* sc = vs + kQ * kVS;
-    float* S = sc + kQ * kVS;
-    float* pw = S + kd * kVS;  // a^0 .. a^(kQ + 1)
+    float* vs = ks + kQ * ks1;   // v, and v with the weights of the state
+    float* ws = vs + kQ * VT;
+    float* S = ws + kQ * VT;
+    float* sc = S + kd4 * kS;    // rows of kQ + 1
+    float* pw = sc + kQ * (kQ + 1);  // a^0 .. a^(kQ + 1)
 
     const T* v = static_cast<const T*>(p.v) + (long long)(h / p.vr) * p.vd + v0;
+    const long long o_at = (long long)(h / p.outr) * p.vd + v0;
     if (OUT && a.cu) {  // tokens behind the last sequence
         for (long long t = border(a, a.nseq) + id; t < a.T; t += a.ids)
             for (int c = tid; c < vw; c += kThreads) {
-                const long long o = t * p.os + (long long)(h / p.outr) * p.vd + v0 + c;
                 if (p.out_f32)
-                    st_out(static_cast<float*>(p.out), o, 0.f);
+                    st_out(static_cast<float*>(p.out), t * p.os + o_at + c, 0.f);
                 else
-                    st_out(static_cast<T*>(p.out), o, 0.f);
+                    st_out(static_cast<T*>(p.out), t * p.os + o_at + c, 0.f);
             }
     }
     const Seg g = segment(a, id);
@@ -66,142 +102,187 @@ __global__ void __launch_bounds__(kThreads) simt_walk_kernel(const __grid_consta
 
     const float ld = a.ld[h], ld2 = ld * 1.44269504f;
     for (int d = tid; d < kQ + 2; d += kThreads) pw[d] = power(ld2, d);
-    const long long seq_state = ((long long)g.seq * a.H + h) * p.kd * p.vd;
-    const long long seg_state = (id * a.H + h) * p.kd * p.vd;
+    const long long seq_state = ((long long)g.seq * a.H + h) * kd * p.vd;
+    const long long seg_state = (id * a.H + h) * kd * p.vd;
     const float* in = !OUT ? nullptr : p.s_seg ? p.s_seg + seg_state : p.s_in ? p.s_in + seq_state : nullptr;
-    for (int e = tid; e < kd * kVT; e += kThreads) {
-        // neighbouring threads take neighbouring elements of the state in memory
-        const int n = p.sn == 1 ? e % kd : e / kVT, c = p.sn == 1 ? e / kd : e % kVT;
-        S[n * kVS + c] = in && c < vw ? in[n * p.sn + (v0 + c) * p.sp] : 0.f;
+    // a warp takes neighbouring elements of the state in memory, 8 x 4 of them where they follow one
+    // another along n: rows of shared memory are 16 bytes apart in the banks
+    const int nb = (kd4 + 7) / 8, elems = nb * 8 * VT;
+    const auto place = [&](int e, int& n, int& c) {
+        const int w = e >> 5;
+        if (p.sn == 1)
+            n = (e & 7) + 8 * (w % nb), c = (e >> 3 & 3) + 4 * (w / nb);
+        else
+            n = e / VT, c = e % VT;
+    };
+#pragma unroll 1
+    for (int e = tid; e < elems; e += kThreads) {
+        int n, c;
+        place(e, n, c);
+        if (n < kd4) S[n * kS + c] = in && n < kd && c < vw ? in[n * p.sn + (v0 + c) * p.sp] : 0.f;
     }
     const T* q = static_cast<const T*>(p.q) + (long long)(h / p.qr) * kd;
     const T* k = static_cast<const T*>(p.k) + (long long)(h / p.kr) * kd;
-    const int i0 = (tid / 16) * 2, j0 = (tid % 16) * 2;
+    const int i = tid / 16, j = tid % 16, j0 = j * VPT;
+    const int bytes = p.out_f32 ? 4 : (int)sizeof(T);
+    const bool vec = OUT && ((p.os | o_at) & (VPT - 1)) == 0 &&
+                     (reinterpret_cast<uintptr_t>(p.out) & (VPT * bytes - 1)) == 0;
 
-    for (int c0 = 0; c0 < g.len; c0 += kQ) {
+    float rq[kRows][4], rk[kRows][4], rv[kRows][VT / 32];  // the rows warp + 8 x of the next chunk
+    const auto fetch = [&](int c0) {
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+            const int r = c0 + warp + 8 * x;
+            const bool in_seg = r < g.len;
+            const long long t = g.start + (p.reverse ? g.len - 1 - r : r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int c = lane + 32 * y;
+                const bool there = in_seg && c < kd;
+                if (OUT) rq[x][y] = there ? static_cast<float>(q[t * p.qs + c]) : 0.f;
+                rk[x][y] = there ? static_cast<float>(k[t * p.ks + c]) : 0.f;
+            }
+#pragma unroll
+            for (int y = 0; y < VT / 32; ++y) {
+                const int c = lane + 32 * y;
+                rv[x][y] = in_seg && c < vw ? static_cast<float>(v[t * p.vs + c]) : 0.f;
+            }
+        }
+    };
+#pragma unroll 1
+    for (int c0 = -kQ; c0 < g.len; c0 += kQ) {
         const int n = min(kQ, g.len - c0);
         __syncthreads();
-#pragma unroll 4
-        for (int e = tid; e < kQ * kd; e += kThreads) {
-            const int r = e / kd, c = e - r * kd;
-            const long long t = g.start + (p.reverse ? g.len - 1 - (c0 + r) : c0 + r);
-            if (OUT) qs[r * ks1 + c] = r < n ? static_cast<float>(q[t * p.qs + c]) : 0.f;
-            ks[r * ks1 + c] = r < n ? static_cast<float>(k[t * p.ks + c]) : 0.f;
-        }
 #pragma unroll
-        for (int e = tid; e < kQ * kVT; e += kThreads) {
-            const int r = e / kVT, c = e - r * kVT;
-            const long long t = g.start + (p.reverse ? g.len - 1 - (c0 + r) : c0 + r);
-            vs[r * kVS + c] = r < n && c < vw ? static_cast<float>(v[t * p.vs + c]) : 0.f;
+        for (int x = 0; x < kRows; ++x) {
+            if (c0 < 0) break;
+            const int r = warp + 8 * x;
+            const float w = r < n ? pw[n - 1 - r + p.reverse] * p.su : 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int c = lane + 32 * y;
+                if (c < kd4) {
+                    if (OUT) qs[r * ks1 + c] = rq[x][y];
+                    ks[r * ks1 + c] = rk[x][y];
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < VT / 32; ++y) {
+                const int c = lane + 32 * y;
+                if (OUT) vs[r * VT + c] = rv[x][y];
+                ws[r * VT + c] = rv[x][y] * w;
+            }
         }
         __syncthreads();
+        if (c0 + kQ < g.len) fetch(c0 + kQ);
+        if (c0 < 0) continue;
         if (OUT) {
-            if (j0 <= i0 + 1 && i0 < n) {
-                float d[2][2] = {};
-#pragma unroll 8
-                for (int c = 0; c < kd; ++c) {
-                    const float q0 = qs[i0 * ks1 + c], q1 = qs[(i0 + 1) * ks1 + c];
-                    const float k0 = ks[j0 * ks1 + c], k1 = ks[(j0 + 1) * ks1 + c];
-                    d[0][0] = fmaf(q0, k0, d[0][0]), d[0][1] = fmaf(q0, k1, d[0][1]);
-                    d[1][0] = fmaf(q1, k0, d[1][0]), d[1][1] = fmaf(q1, k1, d[1][1]);
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        if (j0 + y <= i0 + x)
-                            sc[(i0 + x) * kVS + j0 + y] = d[x][y] * pw[i0 + x - j0 - y] * p.si;
-            }
-            __syncthreads();
-            if (i0 < n) {
-                float o[2][2] = {}, w[2][2] = {};
+            if (i < n) {  // the scores (i, j), (i + 16, j), (i + 16, j + 16)
+                float d00 = 0.f, d10 = 0.f, d11 = 0.f;
+                const float* q0 = qs + i * ks1;
+                const float* k0 = ks + j * ks1;
 #pragma unroll 4
-                for (int j = 0; j <= i0 + 1; ++j) {  // the entry above the diagonal is not read
-                    const float a0 = j <= i0 ? sc[i0 * kVS + j] : 0.f, a1 = sc[(i0 + 1) * kVS + j];
-                    const float b0 = vs[j * kVS + j0], b1 = vs[j * kVS + j0 + 1];
-                    if (j <= i0) o[0][0] = fmaf(a0, b0, o[0][0]), o[0][1] = fmaf(a0, b1, o[0][1]);
-                    o[1][0] = fmaf(a1, b0, o[1][0]), o[1][1] = fmaf(a1, b1, o[1][1]);
+                for (int c = 0; c < kd4; c += 4) {
+                    const float4 ka = four(k0 + c), qb = four(q0 + 16 * ks1 + c);
+                    d00 = dot4(four(q0 + c), ka, d00);
+                    d10 = dot4(qb, ka, d10);
+                    d11 = dot4(qb, four(k0 + 16 * ks1 + c), d11);
                 }
-#pragma unroll 8
-                for (int c = 0; c < kd; ++c) {
-                    const float a0 = qs[i0 * ks1 + c], a1 = qs[(i0 + 1) * ks1 + c];
-                    const float b0 = S[c * kVS + j0], b1 = S[c * kVS + j0 + 1];
-                    w[0][0] = fmaf(a0, b0, w[0][0]), w[0][1] = fmaf(a0, b1, w[0][1]);
-                    w[1][0] = fmaf(a1, b0, w[1][0]), w[1][1] = fmaf(a1, b1, w[1][1]);
+                float* s0 = sc + i * (kQ + 1) + j;
+                float* s1 = s0 + 16 * (kQ + 1);
+                if (j <= i) s0[0] = d00 * pw[i - j] * p.si, s1[16] = d11 * pw[i - j] * p.si;
+                s1[0] = d10 * pw[i + 16 - j] * p.si;
+            }
+            __syncthreads();
+            if (i < n) {
+                float o[2][VPT] = {}, w[2][VPT] = {};
+                const float* s0 = sc + i * (kQ + 1);
+                const float* s1 = s0 + 16 * (kQ + 1);
+#pragma unroll 4
+                for (int c = 0; c <= i; ++c) {  // entries above the diagonal are not read
+                    add_row<VPT>(o[0], s0[c], vs + c * VT + j0);
+                    add_row<VPT>(o[1], s1[c], vs + c * VT + j0);
+                }
+                if (i + 16 < n)
+#pragma unroll 4
+                    for (int c = i + 1; c <= i + 16; ++c) add_row<VPT>(o[1], s1[c], vs + c * VT + j0);
+                const float* q0 = qs + i * ks1;
+                const float* q1 = q0 + 16 * ks1;
+#pragma unroll 2
+                for (int c = 0; c < kd4; c += 4) {
+                    const float4 a0 = four(q0 + c), a1 = four(q1 + c);
+                    const float* b = S + c * kS + j0;
+                    add_row<VPT>(w[0], a0.x, b), add_row<VPT>(w[1], a1.x, b);
+                    add_row<VPT>(w[0], a0.y, b + kS), add_row<VPT>(w[1], a1.y, b + kS);
+                    add_row<VPT>(w[0], a0.z, b + 2 * kS), add_row<VPT>(w[1], a1.z, b + 2 * kS);
+                    add_row<VPT>(w[0], a0.w, b + 3 * kS), add_row<VPT>(w[1], a1.w, b + 3 * kS);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (i0 + x < n) {
-                        const int r = c0 + i0 + x;
-                        const long long t = g.start + (p.reverse ? g.len - 1 - r : r);
-                        const float f = pw[i0 + x + 1 - p.reverse] * p.sx;
+                for (int x = 0; x < 2; ++x) {
+                    const int r = i + 16 * x;
+                    if (r >= n || j0 >= vw) continue;
+                    const long long t = g.start + (p.reverse ? g.len - 1 - c0 - r : c0 + r);
+                    const float f = pw[r + 1 - p.reverse] * p.sx;
+                    float val[VPT];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            if (j0 + y < vw) {
-                                const float val = fmaf(f, w[x][y], o[x][y]);
-                                const long long at = t * p.os + (long long)(h / p.outr) * p.vd + v0 + j0 + y;
-                                if (p.out_f32)
-                                    st_out(static_cast<float*>(p.out), at, val);
-                                else
-                                    st_out(static_cast<T*>(p.out), at, val);
-                            }
-                    }
+                    for (int y = 0; y < VPT; ++y) val[y] = fmaf(f, w[x][y], o[x][y]);
+                    const long long at = t * p.os + o_at + j0;
+                    if (p.out_f32)
+                        put_row<VPT>(static_cast<float*>(p.out) + at, val, vw - j0, vec);
+                    else
+                        put_row<VPT>(static_cast<T*>(p.out) + at, val, vw - j0, vec);
+                }
             }
             __syncthreads();
         }
-        // the state: v's rows take their weights first
-        for (int e = tid; e < kQ * kVT; e += kThreads) {
-            const int r = e / kVT, c = e - r * kVT;
-            if (r < n) vs[r * kVS + c] *= pw[n - 1 - r + p.reverse] * p.su;
-        }
-        __syncthreads();
         const Decay decay(ld, n);
-        for (int u = tid; u < (kd + 3) / 4 * (kVT / 4); u += kThreads) {
-            const int n0 = u / (kVT / 4) * 4, p0 = u % (kVT / 4) * 4;
+#pragma unroll 1
+        for (int u = tid; u < kd4 / 4 * (VT / 4); u += kThreads) {
+            const int n0 = u / (VT / 4) * 4, p0 = u % (VT / 4) * 4;
             float d[4][4] = {};
 #pragma unroll 4
             for (int r = 0; r < n; ++r) {
-                float kk[4], vv[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    kk[x] = n0 + x < kd ? ks[r * ks1 + n0 + x] : 0.f;
-                    vv[x] = vs[r * kVS + p0 + x];
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) d[x][y] = fmaf(kk[x], vv[y], d[x][y]);
+                const float4 kk = four(ks + r * ks1 + n0);
+                const float* b = ws + r * VT + p0;
+                add_row<4>(d[0], kk.x, b), add_row<4>(d[1], kk.y, b);
+                add_row<4>(d[2], kk.z, b), add_row<4>(d[3], kk.w, b);
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (n0 + x < kd) {
-                        float* s = &S[(n0 + x) * kVS + p0 + y];
-                        *s = decay(*s) + d[x][y];
-                    }
+            for (int x = 0; x < 4; ++x) {
+                if (n0 + x >= kd) break;  // stays 0 for any v
+                float4* s = reinterpret_cast<float4*>(S + (n0 + x) * kS + p0);
+                const float4 f = *s;
+                *s = make_float4(decay(f.x) + d[x][0], decay(f.y) + d[x][1], decay(f.z) + d[x][2],
+                                 decay(f.w) + d[x][3]);
+            }
         }
     }
     __syncthreads();
     float* out = !OUT ? p.s_sum + seg_state
                  : p.s_out && g.k == (p.reverse ? 0 : g.cnt - 1) ? p.s_out + seq_state : nullptr;
     if (!out) return;
-    for (int e = tid; e < kd * kVT; e += kThreads) {
-        const int n = p.sn == 1 ? e % kd : e / kVT, c = p.sn == 1 ? e / kd : e % kVT;
-        if (c < vw) out[n * p.sn + (v0 + c) * p.sp] = S[n * kVS + c];
+#pragma unroll 1
+    for (int e = tid; e < elems; e += kThreads) {
+        int n, c;
+        place(e, n, c);
+        if (n < kd && c < vw) out[n * p.sn + (v0 + c) * p.sp] = S[n * kS + c];
     }
 }
 
-template <typename T, bool OUT>
+template <typename T, bool OUT, int VT>
 cudaError_t simt_launch(const WalkArgs& a, cudaStream_t stream) {
     int kd = 0;
     for (int i = 0; i < a.npass; ++i) kd = std::max(kd, a.pass[i].kd);
-    const size_t smem = simt_smem(kd);
-    cudaError_t e = cudaFuncSetAttribute(simt_walk_kernel<T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)simt_smem(128));
+    cudaError_t e = cudaFuncSetAttribute(simt_walk_kernel<T, OUT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)simt_smem(128, VT));
     if (e != cudaSuccess) return e;
-    simt_walk_kernel<T, OUT><<<(unsigned)(a.ids * a.H * a.tiles), kThreads, smem, stream>>>(a);
+    simt_walk_kernel<T, OUT, VT><<<(unsigned)(a.ids * a.H * a.tiles), kThreads, simt_smem(kd, VT), stream>>>(a);
     return cudaSuccess;
+}
+template <typename T>
+cudaError_t simt_launch(const WalkArgs& a, bool sums, int tile, cudaStream_t stream) {
+    if (tile == 32) return sums ? simt_launch<T, false, 32>(a, stream) : simt_launch<T, true, 32>(a, stream);
+    return sums ? simt_launch<T, false, 64>(a, stream) : simt_launch<T, true, 64>(a, stream);
 }
 
 // The states that enter each segment, in the walk's direction, over what each segment adds:
@@ -360,7 +441,8 @@ Plan make_plan(const ssd_linattn_t& p, bool bwd) {
     l.n = p.nseq ? p.nseq : (int)p.batch;
     const auto tensor = [](int n) { return n == 64 || n == 128; };
     const bool tc = p.dtype == SSD_DTYPE_BF16 && tensor(p.headdim) && tensor(p.dstate);
-    const int tile = tc ? kTcTile : kSimtTile, least = tc ? 512 : 64, step = tc ? kTcChunk : kQ;
+    const int tile = tc ? kTcTile : simt_tile(bwd ? std::max(p.headdim, p.dstate) : p.headdim);
+    const int least = tc ? 512 : 64, step = tc ? kTcChunk : kQ;
     const auto tiles = [&](int n) { return (n + tile - 1) / tile; };
     // items for each run of tokens
     const long long per_cut = (long long)p.nheads * ((bwd ? 2 * tiles(p.dstate) : 0) + tiles(p.headdim));
@@ -374,7 +456,7 @@ Plan make_plan(const ssd_linattn_t& p, bool bwd) {
     }
     l.per = l.Ls ? (int)((p.seqlen + l.Ls - 1) / l.Ls) : 1;
     l.ids = !l.Ls ? l.n : p.nseq ? l.T / l.Ls + l.n : (long long)l.n * l.per;
-    l.fits = 2 * l.ids * per_cut <= INT_MAX;  // twice: rows off 16 bytes take the plain walk, in tiles of 32
+    l.fits = 2 * l.ids * per_cut <= INT_MAX;  // twice: a pass of few columns may go by itself in tiles of 32
     const size_t state = (size_t)p.headdim * p.dstate * sizeof(float);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -410,14 +492,14 @@ void set_tiles(WalkArgs& a, int tile) {
 }
 
 cudaError_t launch_walk(WalkArgs a, bool tc, bool sums, int dtype, Launch& L) {
-    set_tiles(a, tc ? kTcTile : kSimtTile);
+    int vd = 0;
+    for (int i = 0; i < a.npass; ++i) vd = std::max(vd, a.pass[i].vd);
+    const int tile = tc ? kTcTile : simt_tile(vd);
+    set_tiles(a, tile);
     if (tc) return sums ? tc_sums(a, L) : tc_walk(a, L);
     L.begin(sums ? "linattn_sums" : "linattn_walk");
-    const bool b = dtype == SSD_DTYPE_BF16;
-    cudaError_t e = sums ? (b ? simt_launch<__nv_bfloat16, false>(a, L.stream)
-                              : simt_launch<float, false>(a, L.stream))
-                         : (b ? simt_launch<__nv_bfloat16, true>(a, L.stream)
-                              : simt_launch<float, true>(a, L.stream));
+    const cudaError_t e = dtype == SSD_DTYPE_BF16 ? simt_launch<__nv_bfloat16>(a, sums, tile, L.stream)
+                                                  : simt_launch<float>(a, sums, tile, L.stream);
     const cudaError_t last = L.end();
     return e != cudaSuccess ? e : last;
 }
