@@ -431,7 +431,9 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
  * clamped as in the convolution; outputs of tokens behind the last sequence are zero.  bf16
  * calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
  * blocks of 128 tokens: there a NaN or an infinity in a token reaches the outputs of all tokens
- * of its sequence in its block.  Forwards of up to 16 tokens a sequence (a batch row, or all packed
+ * of its sequence in its block.  So do bf16 calls of other N and P with 16384 rows (of a head and
+ * token) or more and N + P at least a quarter of what they come to rounded up to 64 or 128, by
+ * copies in the workspace.  Forwards of up to 16 tokens a sequence (a batch row, or all packed
  * ones) are stepped through token by token, and all other calls run the walk on the plain cores, in
  * float32. */
 typedef struct {

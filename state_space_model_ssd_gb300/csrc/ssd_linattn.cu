@@ -375,7 +375,74 @@ __global__ void __launch_bounds__(kThreads) shared_sum_kernel(const float* part,
         }
 }
 
+// Tensors laid out anew: element (t, h, c) of to is that of from, or 0 outside of from's h and c.
+struct Copy {
+    const void* from;
+    void* to;
+    long long n, fs, ts;  // t < n, and elements from one to the next
+    int h, c, fh, fc;     // of to, and of from
+    int fw, tw;           // elements from one h to the next
+    int f32;
+};
+struct Copies {
+    Copy c[6];
+    int n;
+};
+// A lane has four elements of a row and 16 or all lanes a row (c up to 64, or 128); four rows are on
+// their way at a time.  Bound by the bytes where rows start on four elements, else by single loads and
+// stores.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const Copy& j) {
+    const int lane = threadIdx.x & 31, lanes = j.c <= 64 ? 16 : 32, at_once = 32 / lanes;
+    const int c = lane % lanes * 4, sub = lane / lanes;
+    const unsigned groups = (unsigned)(j.h + 4 * at_once - 1) / (4 * at_once);
+    const long long items = j.n * groups;
+    const T* from = static_cast<const T*>(j.from) + c;
+    T* to = static_cast<T*>(j.to) + c;
+    const auto fours = [](const void* p, long long a, int b) {
+        return ((a | b) & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0;
+    };
+    const int in = j.fc - c, out = j.c - c;  // elements from c on
+    const bool load4 = in >= 4 && fours(j.from, j.fs, j.fw), store4 = out >= 4 && fours(j.to, j.ts, j.tw);
+    for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items;
+         i += (long long)gridDim.x * (kThreads / 32)) {
+        const long long t = items <= UINT_MAX ? (unsigned)i / groups : i / groups;
+        const int h0 = (int)(i - t * groups) * 4 * at_once + sub;
+        float v[4][4] = {};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int h = h0 + x * at_once;
+            const T* p = from + t * j.fs + (long long)h * j.fw;
+            if (h >= j.fh) continue;
+            if (load4) {
+                Pack<T, 4> q;
+                q.load(p);
+                q.get(v[x]);
+            } else {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (y < in) v[x][y] = static_cast<float>(p[y]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int h = h0 + x * at_once;
+            if (h < j.h) put_row<4>(to + t * j.ts + (long long)h * j.tw, v[x], out, store4);
+        }
+    }
+}
+__global__ void __launch_bounds__(kThreads) copies_kernel(const __grid_constant__ Copies a) {
+    const Copy& j = a.c[blockIdx.y];
+    if (j.f32)
+        copy_rows<float>(j);
+    else
+        copy_rows<__nv_bfloat16>(j);
+}
+
 // ---------------------------------------------------------------- host
+// Rows of one head and token from which the tensors are laid out anew: see pads.
+constexpr long long kPadRows = 16384;
+
 struct Plan {
     long long T;
     int n;                       // sequences
@@ -383,6 +450,11 @@ struct Plan {
     long long ids;
     size_t s_seg, r_seg, dk_part, dv_part, total;
     bool fits;                   // its items are fewer than 2^31
+    // bf16 of other channels than 64 and 128, laid out in the workspace for the tensor cores: the problem
+    // as it is there (pads) and its tensors: q, k, v, o or do, the gradients, the states
+    bool pads;
+    ssd_linattn_t p;
+    size_t q, k, v, o, dq, dk, dv, s_in, s_out, r_in;
 };
 
 ssd_status_t check_sizes(const ssd_linattn_t* p, bool bwd) {
@@ -435,11 +507,29 @@ size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 // states (P N float32 four times each) than of tokens.  The plain walk takes 5 us for 32 tokens, one
 // after the other, so that 64 are worth the two launches more (2 x 333 tokens of 5 heads in float32,
 // backward: 57 us uncut, 31).
-Plan make_plan(const ssd_linattn_t& p, bool bwd) {
+bool tensor(int n) { return n == 64 || n == 128; }
+// Whether rows are worth laying out anew, with zeros up to 64 or 128 channels: two passes over the
+// tensors, which are at most four times as wide, and two launches, so that few tokens are not.  32768
+// tokens of 24 heads, 80 x 96: forward 776 us of which 405 are the copies, backward 1487 (669), on the
+// plain cores 4085 and 9442; 16384 rows of 33 x 33 channels 56 and 63, for 52 and 103.
+bool pads(const ssd_linattn_t& p) {
+    const int P = p.headdim <= 64 ? 64 : 128, N = p.dstate <= 64 ? 64 : 128;
+    return p.dtype == SSD_DTYPE_BF16 && !(tensor(p.headdim) && tensor(p.dstate)) && p.seqlen > kFewTokens &&
+           p.batch * p.seqlen * p.nheads >= kPadRows && P + N <= 4 * (p.headdim + p.dstate);
+}
+Plan make_plan(const ssd_linattn_t& given, bool bwd) {
     Plan l = {};
+    ssd_linattn_t& p = l.p;
+    p = given;
+    l.pads = pads(p);
+    if (l.pads) {
+        p.headdim = p.headdim <= 64 ? 64 : 128, p.dstate = p.dstate <= 64 ? 64 : 128;
+        const int64_t H = p.nheads, G = p.ngroups;
+        p.q_stride = p.dq_stride = H * p.dstate, p.k_stride = p.dk_stride = G * p.dstate;
+        p.o_stride = H * p.headdim, p.v_stride = p.dv_stride = G * p.headdim;
+    }
     l.T = p.batch * p.seqlen;
     l.n = p.nseq ? p.nseq : (int)p.batch;
-    const auto tensor = [](int n) { return n == 64 || n == 128; };
     const bool tc = p.dtype == SSD_DTYPE_BF16 && tensor(p.headdim) && tensor(p.dstate);
     const int tile = tc ? kTcTile : simt_tile(bwd ? std::max(p.headdim, p.dstate) : p.headdim);
     const int least = tc ? 512 : 64, step = tc ? kTcChunk : kQ;
@@ -471,6 +561,13 @@ Plan make_plan(const ssd_linattn_t& p, bool bwd) {
     if (bwd && p.nheads != p.ngroups) {
         l.dk_part = take((size_t)l.T * p.nheads * p.dstate * sizeof(float));
         l.dv_part = take((size_t)l.T * p.nheads * p.headdim * sizeof(float));
+    }
+    if (l.pads) {
+        const size_t states = (size_t)l.n * p.nheads * state, T = 2 * (size_t)l.T;
+        const size_t q = T * p.q_stride, k = T * p.k_stride, v = T * p.v_stride;
+        l.q = take(q), l.k = take(k), l.v = take(v), l.o = take(T * p.o_stride);
+        l.s_in = take(states), l.s_out = take(states);
+        if (bwd) l.dq = take(q), l.dk = take(k), l.dv = take(v), l.r_in = take(states);
     }
     l.total = at;
     return l;
@@ -563,6 +660,142 @@ cudaError_t launch_shared_sum(const float* part, void* out, const ssd_linattn_t&
     return L.end();
 }
 
+// The launches of a problem whose arguments have been checked.
+cudaError_t run_forward(const ssd_linattn_t& p, const Plan& l, const void* q, const void* k, const void* v,
+                        const float* ld, const int32_t* cu, const float* initial_state, void* o,
+                        float* final_state, char* ws, Launch& L) {
+    const long long T = l.T, H = p.nheads, G = p.ngroups, N = p.dstate;
+    WalkArgs a = common(p, l, ld, cu);
+    if (!(a.status = status_word())) return cudaErrorUnknown;
+    const int r = (int)(H / G);
+    Pass& f = a.pass[0];
+    f.q = q, f.k = k, f.v = v, f.out = o;
+    f.qs = p.q_stride, f.ks = p.k_stride, f.vs = p.v_stride, f.os = p.o_stride;
+    f.kd = p.dstate, f.vd = p.headdim, f.qr = 1, f.kr = r, f.vr = r, f.outr = 1;
+    f.si = f.sx = p.scale, f.su = 1.f;
+    f.s_in = initial_state, f.s_out = final_state;
+    f.sn = 1, f.sp = N;
+    f.out_f32 = p.dtype == SSD_DTYPE_F32;
+    a.npass = 1;
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f);
+    cudaError_t err = cudaSuccess;
+    if (few_fits(a)) {
+        return few_tokens(a, p.dtype, L);
+    }
+    const bool by_sums = tc && sums_pay(a, f);
+    if (l.Ls) {
+        if (!by_sums) f.s_out = nullptr;  // the walk's
+        f.s_sum = reinterpret_cast<float*>(ws + l.s_seg);
+        err = launch_walk(a, tc, true, p.dtype, L);
+        if (err == cudaSuccess) err = launch_scan(a, L);
+        f.s_seg = f.s_sum;
+    } else if (by_sums) {
+        err = final_states(a, f, p.dtype, L);
+    }
+    f.s_out = by_sums ? nullptr : final_state;
+    if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
+    return err;
+}
+cudaError_t run_backward(const ssd_linattn_t& p, const Plan& l, const void* q, const void* k, const void* v,
+                     const float* ld, const int32_t* cu, const float* initial_state, const void* dout,
+                     const float* d_final_state, void* dq, void* dk, void* dv, float* d_initial_state, char* ws,
+                     Launch& L) {
+    const long long T = l.T, H = p.nheads, G = p.ngroups, P = p.headdim, N = p.dstate;
+    WalkArgs a = common(p, l, ld, cu);
+    if (!(a.status = status_word())) return cudaErrorUnknown;
+    const int r = (int)(H / G);
+    const int f32 = p.dtype == SSD_DTYPE_F32;
+    // dq from (do, v, k); dk from (v, do, q); dv from (k, q, do): linattn.cuh
+    Pass& f = a.pass[0];
+    f.q = dout, f.k = v, f.v = k, f.out = dq;
+    f.qs = p.o_stride, f.ks = p.v_stride, f.vs = p.k_stride, f.os = p.dq_stride;
+    f.kd = p.headdim, f.vd = p.dstate, f.qr = 1, f.kr = r, f.vr = r, f.outr = 1;
+    f.si = f.sx = p.scale, f.su = 1.f;
+    f.s_in = initial_state, f.sn = N, f.sp = 1, f.out_f32 = f32;
+    Pass& g = a.pass[1];
+    g.q = v, g.k = dout, g.v = q, g.out = dk;
+    g.qs = p.v_stride, g.ks = p.o_stride, g.vs = p.q_stride, g.os = p.dk_stride;
+    g.kd = p.headdim, g.vd = p.dstate, g.qr = r, g.kr = 1, g.vr = 1, g.outr = 1;
+    g.reverse = 1, g.si = g.su = p.scale, g.sx = 1.f;
+    g.s_in = d_final_state, g.sn = N, g.sp = 1, g.out_f32 = f32;
+    Pass& d = a.pass[2];
+    d.q = k, d.k = q, d.v = dout, d.out = dv;
+    d.qs = p.k_stride, d.ks = p.q_stride, d.vs = p.o_stride, d.os = p.dv_stride;
+    d.kd = p.dstate, d.vd = p.headdim, d.qr = r, d.kr = 1, d.vr = 1, d.outr = 1;
+    d.reverse = 1, d.si = d.su = p.scale, d.sx = 1.f;
+    d.s_in = d_final_state, d.s_out = d_initial_state, d.sn = 1, d.sp = N, d.out_f32 = f32;
+    a.npass = 3;
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f) && tc_fits(g) && tc_fits(d);
+    if (r > 1) {  // each head's own part, summed after the walk
+        g.out = ws + l.dk_part, g.os = H * N, g.out_f32 = 1;
+        d.out = ws + l.dv_part, d.os = H * P, d.out_f32 = 1;
+    }
+    cudaError_t err = cudaSuccess;
+    const bool by_sums = tc && sums_pay(a, d);
+    if (l.Ls) {
+        // the states by segments from k and v, their adjoints from q and do
+        WalkArgs s = a;
+        s.npass = 2;
+        s.pass[0].s_sum = reinterpret_cast<float*>(ws + l.s_seg);
+        s.pass[1] = d;
+        s.pass[1].s_sum = reinterpret_cast<float*>(ws + l.r_seg);
+        if (!by_sums) s.pass[1].s_out = nullptr;
+        err = launch_walk(s, tc, true, p.dtype, L);
+        if (err == cudaSuccess) err = launch_scan(s, L);
+        f.s_seg = s.pass[0].s_sum;
+        g.s_seg = d.s_seg = s.pass[1].s_sum;
+    } else if (by_sums) {
+        err = final_states(a, d, p.dtype, L);
+    }
+    if (by_sums) d.s_out = nullptr;
+    if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
+    if (r > 1 && err == cudaSuccess)
+        err = launch_shared_sum(static_cast<const float*>(g.out), dk, p, T, (int)N, p.dk_stride, L);
+    if (r > 1 && err == cudaSuccess)
+        err = launch_shared_sum(static_cast<const float*>(d.out), dv, p, T, (int)P, p.dv_stride, L);
+    return err;
+}
+
+// The copies between a call's tensors and those in the workspace.
+struct Padding {
+    const ssd_linattn_t &u, &p;  // as the user has it, and as it is in the workspace
+    const Plan& l;
+    char* ws;
+    Copies a = {};
+    void add(const void* from, void* to, long long n, long long fs, long long ts, int h, int c, int fh, int fc,
+             int fw, int tw, int f32) {
+        a.c[a.n++] = {from, to, n, fs, ts, h, c, fh, fc, fw, tw, f32};
+    }
+    void* in(const void* x, size_t at, long long stride, int heads, int width, int wide) {
+        add(x, ws + at, l.T, stride, (long long)heads * wide, heads, wide, heads, width, width, wide, 0);
+        return ws + at;
+    }
+    void out(size_t at, void* x, long long stride, int heads, int width, int wide) {
+        add(ws + at, x, l.T, (long long)heads * wide, stride, heads, width, heads, width, wide, width, 0);
+    }
+    // states [n, H, P, N]; NULL where the call has none
+    float* state_in(const float* x, size_t at) {
+        if (!x) return nullptr;
+        add(x, ws + at, (long long)l.n * u.nheads, (long long)u.headdim * u.dstate, (long long)p.headdim * p.dstate,
+            p.headdim, p.dstate, u.headdim, u.dstate, u.dstate, p.dstate, 1);
+        return reinterpret_cast<float*>(ws + at);
+    }
+    void state_out(size_t at, float* x) {
+        if (x)
+            add(ws + at, x, (long long)l.n * u.nheads, (long long)p.headdim * p.dstate,
+                (long long)u.headdim * u.dstate, u.headdim, u.dstate, u.headdim, u.dstate, p.dstate, u.dstate, 1);
+    }
+    cudaError_t launch(const char* name, Launch& L) {
+        long long items = 0;  // at most: four rows each
+        for (int i = 0; i < a.n; ++i) items = std::max(items, a.c[i].n * ((a.c[i].h + 3) / 4));
+        const long long blocks = std::min<long long>((items + kThreads / 32 - 1) / (kThreads / 32), 8ll * sm_count());
+        L.begin(name);
+        copies_kernel<<<dim3((unsigned)blocks, (unsigned)a.n), kThreads, 0, L.stream>>>(a);
+        a.n = 0;
+        return L.end();
+    }
+};
+
 }  // namespace
 }  // namespace linattn
 }  // namespace ssd
@@ -610,40 +843,27 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
                Rows(v, T, p.v_stride, G * P, e), Rows(log_decay, H, 4),
                Rows(cu_seqlens, p.nseq ? p.nseq + 1 : 0, 4), Rows(initial_state, states, 4)}))
         return SSD_ERR_INVALID_ARG;
-    WalkArgs a = common(p, l, log_decay, cu_seqlens);
-    if (!(a.status = status_word())) return SSD_ERR_CUDA;
     char* ws = static_cast<char*>(workspace);
-    const int r = (int)(H / G);
-    Pass& f = a.pass[0];
-    f.q = q, f.k = k, f.v = v, f.out = o;
-    f.qs = p.q_stride, f.ks = p.k_stride, f.vs = p.v_stride, f.os = p.o_stride;
-    f.kd = p.dstate, f.vd = p.headdim, f.qr = 1, f.kr = r, f.vr = r, f.outr = 1;
-    f.si = f.sx = p.scale, f.su = 1.f;
-    f.s_in = initial_state, f.s_out = final_state;
-    f.sn = 1, f.sp = N;
-    f.out_f32 = p.dtype == SSD_DTYPE_F32;
-    a.npass = 1;
-    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f);
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
-    cudaError_t err = cudaSuccess;
-    if (few_fits(a)) {
-        err = few_tokens(a, p.dtype, L);
-        set_last_launches(L.count);
-        return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    cudaError_t err;
+    if (l.pads) {
+        const ssd_linattn_t& w = l.p;
+        Padding c{p, w, l, ws};
+        const void* wq = c.in(q, l.q, p.q_stride, p.nheads, p.dstate, w.dstate);
+        const void* wk = c.in(k, l.k, p.k_stride, p.ngroups, p.dstate, w.dstate);
+        const void* wv = c.in(v, l.v, p.v_stride, p.ngroups, p.headdim, w.headdim);
+        const float* in = c.state_in(initial_state, l.s_in);
+        err = c.launch("linattn_pad", L);
+        if (err == cudaSuccess)
+            err = run_forward(w, l, wq, wk, wv, log_decay, cu_seqlens, in, ws + l.o,
+                          final_state ? reinterpret_cast<float*>(ws + l.s_out) : nullptr, ws, L);
+        c.out(l.o, o, p.o_stride, p.nheads, p.headdim, w.headdim);
+        c.state_out(l.s_out, final_state);
+        if (err == cudaSuccess) err = c.launch("linattn_unpad", L);
+    } else {
+        err = run_forward(p, l, q, k, v, log_decay, cu_seqlens, initial_state, o, final_state, ws, L);
     }
-    const bool by_sums = tc && sums_pay(a, f);
-    if (l.Ls) {
-        if (!by_sums) f.s_out = nullptr;  // the walk's
-        f.s_sum = reinterpret_cast<float*>(ws + l.s_seg);
-        err = launch_walk(a, tc, true, p.dtype, L);
-        if (err == cudaSuccess) err = launch_scan(a, L);
-        f.s_seg = f.s_sum;
-    } else if (by_sums) {
-        err = final_states(a, f, p.dtype, L);
-    }
-    f.s_out = by_sums ? nullptr : final_state;
-    if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
     set_last_launches(L.count);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -679,61 +899,32 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
                Rows(log_decay, H, 4), Rows(cu_seqlens, p.nseq ? p.nseq + 1 : 0, 4),
                Rows(initial_state, states, 4), Rows(d_final_state, states, 4)}))
         return SSD_ERR_INVALID_ARG;
-    WalkArgs a = common(p, l, log_decay, cu_seqlens);
-    if (!(a.status = status_word())) return SSD_ERR_CUDA;
     char* ws = static_cast<char*>(workspace);
-    const int r = (int)(H / G);
-    const int f32 = p.dtype == SSD_DTYPE_F32;
-    // dq from (do, v, k); dk from (v, do, q); dv from (k, q, do): linattn.cuh
-    Pass& f = a.pass[0];
-    f.q = dout, f.k = v, f.v = k, f.out = dq;
-    f.qs = p.o_stride, f.ks = p.v_stride, f.vs = p.k_stride, f.os = p.dq_stride;
-    f.kd = p.headdim, f.vd = p.dstate, f.qr = 1, f.kr = r, f.vr = r, f.outr = 1;
-    f.si = f.sx = p.scale, f.su = 1.f;
-    f.s_in = initial_state, f.sn = N, f.sp = 1, f.out_f32 = f32;
-    Pass& g = a.pass[1];
-    g.q = v, g.k = dout, g.v = q, g.out = dk;
-    g.qs = p.v_stride, g.ks = p.o_stride, g.vs = p.q_stride, g.os = p.dk_stride;
-    g.kd = p.headdim, g.vd = p.dstate, g.qr = r, g.kr = 1, g.vr = 1, g.outr = 1;
-    g.reverse = 1, g.si = g.su = p.scale, g.sx = 1.f;
-    g.s_in = d_final_state, g.sn = N, g.sp = 1, g.out_f32 = f32;
-    Pass& d = a.pass[2];
-    d.q = k, d.k = q, d.v = dout, d.out = dv;
-    d.qs = p.k_stride, d.ks = p.q_stride, d.vs = p.o_stride, d.os = p.dv_stride;
-    d.kd = p.dstate, d.vd = p.headdim, d.qr = r, d.kr = 1, d.vr = 1, d.outr = 1;
-    d.reverse = 1, d.si = d.su = p.scale, d.sx = 1.f;
-    d.s_in = d_final_state, d.s_out = d_initial_state, d.sn = 1, d.sp = N, d.out_f32 = f32;
-    a.npass = 3;
-    const bool tc = p.dtype == SSD_DTYPE_BF16 && T > 0 && tc_fits(f) && tc_fits(g) && tc_fits(d);
-    if (r > 1) {  // each head's own part, summed after the walk
-        g.out = ws + l.dk_part, g.os = H * N, g.out_f32 = 1;
-        d.out = ws + l.dv_part, d.os = H * P, d.out_f32 = 1;
-    }
     Launch L;
     L.stream = static_cast<cudaStream_t>(stream);
-    cudaError_t err = cudaSuccess;
-    const bool by_sums = tc && sums_pay(a, d);
-    if (l.Ls) {
-        // the states by segments from k and v, their adjoints from q and do
-        WalkArgs s = a;
-        s.npass = 2;
-        s.pass[0].s_sum = reinterpret_cast<float*>(ws + l.s_seg);
-        s.pass[1] = d;
-        s.pass[1].s_sum = reinterpret_cast<float*>(ws + l.r_seg);
-        if (!by_sums) s.pass[1].s_out = nullptr;
-        err = launch_walk(s, tc, true, p.dtype, L);
-        if (err == cudaSuccess) err = launch_scan(s, L);
-        f.s_seg = s.pass[0].s_sum;
-        g.s_seg = d.s_seg = s.pass[1].s_sum;
-    } else if (by_sums) {
-        err = final_states(a, d, p.dtype, L);
+    cudaError_t err;
+    if (l.pads) {
+        const ssd_linattn_t& w = l.p;
+        Padding c{p, w, l, ws};
+        const void* wq = c.in(q, l.q, p.q_stride, p.nheads, p.dstate, w.dstate);
+        const void* wk = c.in(k, l.k, p.k_stride, p.ngroups, p.dstate, w.dstate);
+        const void* wv = c.in(v, l.v, p.v_stride, p.ngroups, p.headdim, w.headdim);
+        const void* wo = c.in(dout, l.o, p.o_stride, p.nheads, p.headdim, w.headdim);
+        const float* in = c.state_in(initial_state, l.s_in);
+        const float* rin = c.state_in(d_final_state, l.r_in);
+        err = c.launch("linattn_pad", L);
+        if (err == cudaSuccess)
+            err = run_backward(w, l, wq, wk, wv, log_decay, cu_seqlens, in, wo, rin, ws + l.dq, ws + l.dk, ws + l.dv,
+                           d_initial_state ? reinterpret_cast<float*>(ws + l.s_out) : nullptr, ws, L);
+        c.out(l.dq, dq, p.dq_stride, p.nheads, p.dstate, w.dstate);
+        c.out(l.dk, dk, p.dk_stride, p.ngroups, p.dstate, w.dstate);
+        c.out(l.dv, dv, p.dv_stride, p.ngroups, p.headdim, w.headdim);
+        c.state_out(l.s_out, d_initial_state);
+        if (err == cudaSuccess) err = c.launch("linattn_unpad", L);
+    } else {
+        err = run_backward(p, l, q, k, v, log_decay, cu_seqlens, initial_state, dout, d_final_state, dq, dk, dv,
+                       d_initial_state, ws, L);
     }
-    if (by_sums) d.s_out = nullptr;
-    if (err == cudaSuccess) err = launch_walk(a, tc, false, p.dtype, L);
-    if (r > 1 && err == cudaSuccess)
-        err = launch_shared_sum(static_cast<const float*>(g.out), dk, p, T, (int)N, p.dk_stride, L);
-    if (r > 1 && err == cudaSuccess)
-        err = launch_shared_sum(static_cast<const float*>(d.out), dv, p, T, (int)P, p.dv_stride, L);
     set_last_launches(L.count);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }

@@ -156,6 +156,40 @@ def test_forms_of_the_launch(ssd, B, L, H, G, P, N, state, strided):
     _backward(ssd, s, True)
 
 
+# enough tokens of other channels for their rows to be laid out anew for the tensor cores; the last two
+# just too few, and too narrow, for that
+@pytest.mark.parametrize("B,L,H,G,P,N,cu,state,strided,offset,tc", [
+    (2, 1030, 8, 8, 90, 15, None, True, False, 0, True),
+    (1, 2100, 8, 2, 33, 65, None, True, True, 3, True),
+    (1, 2100, 8, 4, 80, 96, [0, 1290, 1290, 1300, 1428], True, True, 0, True),
+    (9, 130, 15, 5, 127, 64, None, False, True, 1, True),
+    (950, 18, 1, 1, 31, 17, None, True, False, 0, True),
+    (1, 2047, 8, 2, 33, 65, None, True, False, 0, False),
+    (1, 2100, 8, 8, 12, 10, None, True, True, 0, False)])
+def test_rows_laid_out_anew(ssd, B, L, H, G, P, N, cu, state, strided, offset, tc):
+    import torch
+    s = _make(B, L, H, G, P, N, "bf16", cu, state, strided, seed=17, offset=offset)
+    o, final = _forward(ssd, s, tc)
+    g = _backward(ssd, s, tc)
+    # into slices of wider rows, what lies beside them left as it is
+    rows = torch.full((B, L, H * N + G * (N + P) + 5), 7.0, device="cuda", dtype=torch.bfloat16)
+    views = {"dq": rows[..., 1:1 + H * N].unflatten(2, (H, N)),
+             "dk": rows[..., 2 + H * N:2 + (H + G) * N].unflatten(2, (G, N)),
+             "dv": rows[..., 4 + (H + G) * N:4 + (H + G) * N + G * P].unflatten(2, (G, P))}
+    ssd.linear_attention_backward(s["q"], s["k"], s["v"], s["ld"], s["do"], scale=s["scale"], cu_seqlens=s["cu"],
+                                  initial_state=s["init"], d_final_state=s["dfinal"], d_initial_state=state,
+                                  out=dict(views))
+    for name, view in views.items():
+        assert torch.equal(view, g[name]), name
+    beside = [0, 1 + H * N, 2 + (H + G) * N, 3 + (H + G) * N, rows.shape[2] - 1]
+    assert (rows[..., beside] == 7).all()
+    if cu is not None:
+        assert not o[:, cu[-1]:].any() and not views["dq"][:, cu[-1]:].any()
+    o2, none = ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], scale=s["scale"], cu_seqlens=s["cu"],
+                                            initial_state=s["init"])
+    assert none is None and torch.isfinite(o2).all()
+
+
 @pytest.mark.parametrize("B,L,H,P,N", [(8, 4096, 20, 128, 128), (2, 4096, 32, 128, 64), (1, 16384, 8, 64, 64),
                                        (4, 4096, 40, 64, 64)])
 def test_states_of_slow_decays_keep_their_bits(ssd, B, L, H, P, N):
