@@ -66,7 +66,7 @@ __device__ __forceinline__ long long border(const WalkArgs& a, int s) {
 // of which may be holes: ceil(len / Ls) is at most floor((cu + len) / Ls) - floor(cu / Ls) + 1.
 __device__ __forceinline__ long long first_segment(const WalkArgs& a, int s) {
     if (!a.Ls) return s;
-    return a.cu ? border(a, s) / a.Ls + s : (long long)s * a.per;
+    return a.cu ? (long long)((unsigned)border(a, s) / (unsigned)a.Ls) + s : (long long)s * a.per;
 }
 __device__ __forceinline__ Seg sequence(const WalkArgs& a, int s) {
     Seg g;

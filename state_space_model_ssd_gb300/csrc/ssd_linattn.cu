@@ -290,7 +290,7 @@ cudaError_t simt_launch(const WalkArgs& a, bool sums, int tile, cudaStream_t str
 // segments' loads are on their way ahead of their stores.  Bound by the states' bytes, read and
 // written once.
 template <int VEC>
-__global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_constant__ WalkArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) segment_scan_kernel(const __grid_constant__ WalkArgs a) {
     const Pass& p = a.pass[blockIdx.z];
     const int size = p.kd * p.vd, row = a.H * size;  // less than 2^31: check_sizes
     const int e = ((int)blockIdx.x * kThreads + threadIdx.x) * VEC;
@@ -314,18 +314,19 @@ __global__ void __launch_bounds__(kThreads) segment_scan_kernel(const __grid_con
             Pack<float, VEC> add[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                if (k0 + i >= g.cnt) break;
                 add[i].zero();
                 if (k0 + i < summed) add[i].load(at + (k0 + i) * step);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k0 + i < g.cnt) {
-                    store_vec<VEC>(at + (k0 + i) * step, S);
-                    float f[VEC];
-                    add[i].get(f);
+            for (int i = 0; i < 8; ++i) {
+                if (k0 + i >= g.cnt) break;
+                store_vec<VEC>(at + (k0 + i) * step, S);
+                float f[VEC];
+                add[i].get(f);
 #pragma unroll
-                    for (int u = 0; u < VEC; ++u) S[u] = (k0 + i == short_one ? last(S[u]) : whole(S[u])) + f[u];
-                }
+                for (int u = 0; u < VEC; ++u) S[u] = (k0 + i == short_one ? last(S[u]) : whole(S[u])) + f[u];
+            }
         }
         if (p.s_out) store_vec<VEC>(p.s_out + (long long)s * row + e, S);
     }
