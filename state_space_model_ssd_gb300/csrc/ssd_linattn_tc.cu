@@ -28,7 +28,7 @@
 // another, so that what they all read comes from L2 after the first.
 //
 // GB300, 32768 tokens of 80 heads, 64 x 128 states: forward 338 us for the walk (88 % of the copy rate on its
-// bytes), 170 for the sums, 22 for the scan; backward, five tiles for each head's chunk, 1337 us:
+// bytes), 167 for the sums, 17 for the scan; backward, five tiles for each head's chunk, 1337 us:
 // 3700 cycles for a tile's chunk with 55 % of the issue slots and a third of the tensor pipe in use, no
 // step of it more than 9 % by itself.
 #include <algorithm>

@@ -185,9 +185,17 @@ def test_rows_laid_out_anew(ssd, B, L, H, G, P, N, cu, state, strided, offset, t
     assert (rows[..., beside] == 7).all()
     if cu is not None:
         assert not o[:, cu[-1]:].any() and not views["dq"][:, cu[-1]:].any()
-    o2, none = ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], scale=s["scale"], cu_seqlens=s["cu"],
-                                            initial_state=s["init"])
+    # captured on a stream of its own, without the states
+    call = lambda: ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], scale=s["scale"],  # noqa: E731
+                                                cu_seqlens=s["cu"], initial_state=s["init"])
+    o2, none = call()
     assert none is None and torch.isfinite(o2).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, _ = call()
+    o3.fill_(7.0)
+    graph.replay()
+    assert torch.equal(o2, o3)
 
 
 @pytest.mark.parametrize("B,L,H,P,N", [(8, 4096, 20, 128, 128), (2, 4096, 32, 128, 64), (1, 16384, 8, 64, 64),
