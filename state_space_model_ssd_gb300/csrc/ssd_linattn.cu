@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(kThreads, 4) segment_scan_kernel(const __grid_
     const float ld = a.ld[e / size];
     const Decay whole(ld, a.Ls);
     for (int s = blockIdx.y; s < a.nseq; s += gridDim.y) {
-        const Seg g = sequence(a, s);
-        Pack<float, VEC> v;
-        float S[VEC];
+        Pack<float, VEC> v;  // on its way before the sequence is looked up
         v.zero();
         if (p.s_in) v.load(p.s_in + (long long)s * row + e);
+        const Seg g = sequence(a, s);
+        float S[VEC];
         v.get(S);
         // from the walk's first segment on
         const long long step = p.reverse ? -(long long)row : row;
