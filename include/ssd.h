@@ -427,9 +427,10 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
  * gradient.  Query heads h read key and value head h / (H / G); each has a state of its own, in
  * the layout of the scan's.  q [T][H][N], k [T][G][N], v [T][G][P], o [T][H][P]: the heads of a
  * token lie next to one another, tokens `stride` elements apart; tensors of the same stride may
- * lie between one another's tokens (slices of one projection's rows).  A malformed cu_seqlens is
- * clamped as in the convolution; outputs of tokens behind the last sequence are zero.  bf16
- * calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
+ * lie between one another's tokens (slices of one projection's rows).  cu_seqlens is read with
+ * every entry clamped to 0 .. T; borders that fall give wrong values, no access out of range.
+ * Outputs and gradients of tokens before the first border or from the last one on are zero.
+ * bf16 calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
  * blocks of 128 tokens: there a NaN or an infinity in a token reaches the outputs of all tokens
  * of its sequence in its block.  So do bf16 calls of other N and P with 16384 rows (of a head and
  * token) or more and N + P at least a quarter of what they come to rounded up to 64 or 128, by

@@ -27,8 +27,8 @@ __all__ = ["linear_attention_forward", "linear_attention_backward", "linear_atte
 def linear_attention_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, initial_state=None,
                              final_state: bool = False, out=None, final_state_out=None, workspace=None,
                              stream=None):
-    """``cu_seqlens`` (int32 ``[nseq + 1]``, batch 1) packs sequences; outputs of tokens behind the
-    last one are zero.  ``initial_state`` float32 ``[nseq or batch, H, P, N]`` is what each sequence
+    """``cu_seqlens`` (int32 ``[nseq + 1]``, batch 1) packs sequences; outputs (and gradients) of
+    tokens before the first one or behind the last one are zero.  ``initial_state`` float32 ``[nseq or batch, H, P, N]`` is what each sequence
     goes on from.  Returns ``(o, final_state or None)``: o ``[batch, L, H, P]`` in the type of q, the
     final states as the initial ones.
 

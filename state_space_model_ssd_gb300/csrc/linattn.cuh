@@ -62,6 +62,13 @@ __device__ __forceinline__ long long border(const WalkArgs& a, int s) {
     const long long v = a.cu[s];
     return v < 0 ? 0 : v > a.T ? a.T : v;
 }
+// The tokens of no sequence, before the first border and from the last one on: their outputs are zero.
+struct Outside {
+    long long first, last, n;
+    __device__ __forceinline__ explicit Outside(const WalkArgs& a)
+        : first(border(a, 0)), last(border(a, a.nseq)), n(first + a.T - last) {}
+    __device__ __forceinline__ long long token(long long i) const { return i < first ? i : last + (i - first); }
+};
 // The first segment of sequence s; packed sequences have cu[s] / Ls + s of them before it, some
 // of which may be holes: ceil(len / Ls) is at most floor((cu + len) / Ls) - floor(cu / Ls) + 1.
 __device__ __forceinline__ long long first_segment(const WalkArgs& a, int s) {

@@ -86,14 +86,17 @@ __global__ void __launch_bounds__(kThreads, 2) simt_walk_kernel(const __grid_con
 
     const T* v = static_cast<const T*>(p.v) + (long long)(h / p.vr) * p.vd + v0;
     const long long o_at = (long long)(h / p.outr) * p.vd + v0;
-    if (OUT && a.cu) {  // tokens behind the last sequence
-        for (long long t = border(a, a.nseq) + id; t < a.T; t += a.ids)
+    if (OUT && a.cu) {
+        const Outside none(a);
+        for (long long r = id; r < none.n; r += a.ids) {
+            const long long t = none.token(r);
             for (int c = tid; c < vw; c += kThreads) {
                 if (p.out_f32)
                     st_out(static_cast<float*>(p.out), t * p.os + o_at + c, 0.f);
                 else
                     st_out(static_cast<T*>(p.out), t * p.os + o_at + c, 0.f);
             }
+        }
     }
     const Seg g = segment(a, id);
     if (!g.there) return;

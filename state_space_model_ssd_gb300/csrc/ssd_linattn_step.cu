@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(kThreads, 4) attn_few_kernel(const __grid_cons
     const linattn::Pass& p = a.pass[0];
     const int h = blockIdx.y, N = p.kd, p0 = blockIdx.x * rows, np = min(rows, p.vd - p0);
     T* out = static_cast<T*>(p.out) + (long long)h * p.vd + p0;
-    if (a.cu && blockIdx.z == 0)  // tokens behind the last sequence
-        for (long long t = linattn::border(a, a.nseq); t < a.T; ++t)
-            for (int i = threadIdx.x; i < np; i += kThreads) st_out(out, t * p.os + i, 0.f);
+    if (a.cu && blockIdx.z == 0) {
+        const linattn::Outside none(a);
+        for (long long t = 0; t < none.n; ++t)
+            for (int i = threadIdx.x; i < np; i += kThreads) st_out(out, none.token(t) * p.os + i, 0.f);
+    }
     for (int s = blockIdx.z; s < a.nseq; s += gridDim.z) {
         const linattn::Seg g = linattn::sequence(a, s);
         const int lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes, step = kThreads / lanes;

@@ -405,11 +405,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         for (int item = blockIdx.x; item < geo.items; item += gridDim.x, give_back()) {
             if (!wait_warp(&x->item_full[it.s], it.phase, &x->stop, status)) break;
             const Item& t = x->items[it.s];
-            if (a.cu) {  // tokens behind the last sequence
+            if (a.cu) {
                 const int oe = t.f32 ? 4 : 2;
-                for (long long r = border(a, a.nseq) + t.id; r < a.T; r += a.ids)
+                const Outside none(a);
+                for (long long r = t.id; r < none.n; r += a.ids)
                     if (i < oe)
-                        *reinterpret_cast<uint4*>(t.out + (r - t.g.start) * t.os + 16 * part * oe + i * 16) =
+                        *reinterpret_cast<uint4*>(t.out + (none.token(r) - t.g.start) * t.os + 16 * part * oe + i * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
             }
             if (!t.g.there) continue;
