@@ -487,7 +487,8 @@ ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int32_t nslots
 /* Beam search: of the candidates (beam i, token t) of each batch row, with the score
  *     scores[i] + logits[i][t] - log sum_u exp(logits[i][u]),
  * the `keep` best, best first.  Candidates of one beam are ordered by their logits, those of
- * different beams by their scores before rounding to float32; equal ones by beam, then token.
+ * different beams by their scores in float64, before they are rounded (or overflow) to float32; equal
+ * ones by beam, then token.
  * finished (one byte a beam, not 0: ended; NULL: none has): such a beam has the one candidate
  * pad_token, at its score.  What is left out, tokens with a logit of -inf and every token of a
  * beam whose score is not finite or whose logits hold a NaN or +inf or nothing but -inf, has the

@@ -8,9 +8,9 @@
 //    its `keep` best logits.  To find them each of the eight warps takes the r-th best of its threads' own
 //    maxima, r = keep / 8 rounded up: at least `keep` elements of the slice reach the lowest of the
 //    eight, and few more do (about 60 of 8192 for 16).  Those are gathered and ranked.
-//  * A block for each batch row adds up the slices' sums and turns the slices' best into
-//    scores, both as pairs of floats, and takes the best in the same way.  Between beams, whose scores differ
-//    by their logarithms' rounding, the pairs decide; within a beam the logits do.
+//  * A block for each batch row adds up the slices' sums as pairs of floats, turns the slices' best into
+//    scores in float64, and takes the best in the same way.  Equal scores of one beam are ordered by
+//    their logits.
 // Ranks are counted (how many others come before), so that nothing depends on an order of arrival.
 // GB300: 64 x 8 x 50277 float32 logits, 16 kept: 50 us, of which the slices 34 (45 % of the copy rate:
 // 400 instructions a warp for sixteen elements a thread keep the SMs busier than memory) and the
@@ -21,6 +21,7 @@
 // copies and caches.  Bound by the bytes of the states that move: 16 x 4 beams, half of them doubled,
 // 24 layers of states of 24 heads x 64 x 128 and windows: 196 us (92 % of the copy rate; each cache
 // shared out by itself 221).
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -46,6 +47,13 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
+__device__ __forceinline__ unsigned long long ordered(double x) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+    return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double unordered(unsigned long long u) {
+    return __longlong_as_double((long long)(u >> 63 ? u ^ 1ull << 63 : ~u));
+}
 // A number as the sum of two floats, the second at most half a step of the first: 48 bits without the
 // float64 units, of which this GPU has few.  The sums are Knuth's and Dekker's.
 struct Pair {
@@ -65,9 +73,6 @@ struct Pair {
         const float p = hi * x.hi, rest = fmaf(hi, x.hi, -p) + (hi * x.lo + lo * x.hi);
         const float t = p + rest;
         return Pair{t, (p - t) + rest};
-    }
-    __device__ __forceinline__ unsigned long long key() const {
-        return (unsigned long long)ordered(hi) << 32 | ordered(lo);
     }
 };
 // e^-n for a whole n >= 0, by the powers of two in n.
@@ -115,11 +120,11 @@ struct SelectArgs {
 
 // The first `keep` of `m` pairs (key, index), largest key first, equal keys by index, to ranks
 // 0 .. min(m, keep) - 1: sink(rank, i) for the i-th pair.
-template <typename Key, typename Sink>
-__device__ __forceinline__ void rank_all(const Key* key, const int* idx, int m, int keep, Sink sink) {
+template <typename Key, typename Index, typename Sink>
+__device__ __forceinline__ void rank_all(const Key* key, const Index* idx, int m, int keep, Sink sink) {
     for (int i = threadIdx.x; i < m; i += kThreads) {
         const Key x = key[i];
-        const int at = idx[i];
+        const Index at = idx[i];
         int before = 0;
 #pragma unroll 4
         for (int j = 0; j < m; ++j) before += key[j] > x || (key[j] == x && idx[j] < at);
@@ -252,22 +257,29 @@ __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArg
 // Candidates of a thread and round of the merge.
 constexpr int kRound = 4;
 
+// Where candidates of equal scores come: by beam, logit (largest first) and token.  A beam's scores
+// are one float64 sum each, which never falls where the logit rises, so that its candidates come in the
+// order of their logits however coarse the sums are.
+__device__ __forceinline__ unsigned long long place(int beam, uint32_t logit, int token) {
+    return (unsigned long long)beam << 56 | (unsigned long long)~logit << 24 | (unsigned)token;
+}
+
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a) {
     constexpr int kList = kMostKeep + kRound * kThreads;
-    __shared__ Pair base[kMostBeams];  // scores_i - log sum exp, NaN: nothing to choose from
+    __shared__ double base[kMostBeams];  // scores_i - log sum exp, NaN: nothing to choose from
+    __shared__ float near[kMostBeams];   // the same rounded
     __shared__ bool over[kMostBeams];
-    __shared__ unsigned long long lkey[kList];
-    __shared__ int lidx[kList], count;
+    __shared__ unsigned long long lkey[kList], lat[kList];
+    __shared__ int count;
     // the best so far, in order
-    __shared__ unsigned long long rkey[kMostKeep];
-    __shared__ int ridx[kMostKeep];
+    __shared__ unsigned long long rkey[kMostKeep], rat[kMostKeep];
     const long long b = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = warp; i < a.beams; i += kWarps) {
         const long long row = b * a.beams + i;
         const float score = a.scores[row];
-        Pair v{isfinite(score) ? score : NAN, 0.f};
+        double v = isfinite(score) ? score : NAN;
         if (!(a.finished && a.finished[row])) {
             float m = -INFINITY;
             const float2* s = a.sums + row * a.slices;
@@ -284,10 +296,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
             for (int o = 16; o > 0; o >>= 1)
                 t = t.plus(Pair{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
             const Pair l = log_of(t).plus(m);
-            v = isfinite(m) && isfinite(t.hi) ? Pair{-l.hi, -l.lo}.plus(v.hi) : Pair{NAN, 0.f};
+            v = isfinite(m) && isfinite(t.hi) ? v - ((double)l.hi + l.lo) : NAN;
         }
         if (lane == 0) {
             base[i] = v;
+            near[i] = (float)v;
             over[i] = a.finished && a.finished[row];
         }
     }
@@ -295,84 +308,83 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
     const int per = a.slices * a.keep, all = a.beams * per;
     const int* tokens = a.best_token + b * all;
     const float* logits = a.best + b * all;
-    const unsigned long long lowest = Pair{-INFINITY, 0.f}.key();
     __syncthreads();
+    // the largest of the beams' sums
+    float most = 0.f;
+    for (int i = lane; i < a.beams; i += 32) most = fmaxf(most, fabsf(near[i]));
+    most = __uint_as_float(warp_max(__float_as_uint(most)));
+    // what a candidate's float32 score must reach so that its score proper can reach one whose float32 score
+    // is `bound`: both are off by 2^-24 of themselves and of the beam's sum at most (FLT_MAX stands for +inf)
+    const auto reach = [&](float bound) {
+        const float t = fminf(bound, FLT_MAX);
+        return t - (fabsf(t) * 0x1p-22f + most * 0x1p-22f + FLT_MIN);
+    };
     for (int c0 = 0; c0 < all; c0 += kRound * kThreads) {
-        unsigned long long ck[kRound], best = 0;
-        int ci[kRound];
-        float x[kRound];
+        int ct[kRound];
+        float x[kRound], score[kRound];
 #pragma unroll
         for (int u = 0; u < kRound; ++u) {
             const int c = c0 + u * kThreads + tid;
-            ci[u] = c < all ? tokens[c] : -1;
+            ct[u] = c < all ? tokens[c] : -1;
             x[u] = c < all ? logits[c] : 0.f;
         }
-        // what a full list's last entry comes before is out
-        const unsigned long long floor_key = have == a.keep ? rkey[a.keep - 1] : 0ull;
-        const int floor_idx = have == a.keep ? ridx[a.keep - 1] : INT_MAX;
-        bool any = false;
+        // with a full list, what cannot come before its last entry is out, and so is all at -inf: it comes
+        // in the order of its places
+        const float floor = have == a.keep ? reach((float)unordered(rkey[a.keep - 1])) : -INFINITY;
+        uint32_t best = 0u;
 #pragma unroll
         for (int u = 0; u < kRound; ++u) {
             const int c = c0 + u * kThreads + tid;
-            ck[u] = 0ull;
+            score[u] = -INFINITY;
             if (c < all) {
                 const int i = c / per, k = c - i * per;
-                const Pair from = base[i];
-                const bool choice = isfinite(from.hi);
-                unsigned long long key = lowest;
-                int t = ci[u];
+                const float from = near[i];
+                const bool choice = from == from;
                 if (over[i] || !choice) {
                     // the first tokens, at -inf; an ended beam's padding token at its score
-                    t = k < a.keep && k < a.vocab ? k : -1;
+                    ct[u] = k < a.keep && k < a.vocab ? k : -1;
+                    x[u] = -INFINITY;
                     if (over[i] && choice) {
-                        if (k == a.keep - 1 && a.pad >= a.keep) t = a.pad;
-                        if (t == a.pad) key = from.key();
-                    }
-                } else if (x[u] != -INFINITY) {
-                    key = from.plus(x[u]).key();
-                }
-                ci[u] = INT_MAX;
-                if (t >= 0) {
-                    const int at = i * a.vocab + t;
-                    if (key > floor_key || (key == floor_key && at < floor_idx)) {
-                        ck[u] = key, ci[u] = at, any = true;
-                        best = max(best, key);
+                        if (k == a.keep - 1 && a.pad >= a.keep) ct[u] = a.pad;
+                        if (ct[u] == a.pad) x[u] = 0.f;
                     }
                 }
-            } else {
-                ci[u] = INT_MAX;
+                if (x[u] != -INFINITY) score[u] = from + x[u];
+                if (have == a.keep && (x[u] == -INFINITY || score[u] < floor)) ct[u] = -1;
+                if (ct[u] >= 0) best = max(best, ordered(score[u]));
             }
         }
         if (tid == 0) count = have;
-        if (tid < have) lkey[tid] = rkey[tid], lidx[tid] = ridx[tid];
-        if (!__syncthreads_or(any)) continue;
-        // the keep-th best of the threads' own best, to its first 32 bits, bit by bit: at least `keep`
-        // candidates reach it (beams differ too much for a bound by warps)
-        const uint32_t top = (uint32_t)(best >> 32);
+        if (tid < have) lkey[tid] = rkey[tid], lat[tid] = rat[tid];
+        if (!__syncthreads_or(best != 0u)) continue;
+        // the keep-th best of the threads' own best, bit by bit: at least `keep` candidates reach it (beams
+        // differ too much for a bound by warps)
         uint32_t bound = 0u;
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t t = bound | 1u << bit;
-            const int n = __syncthreads_count(top >= t);
+            const int n = __syncthreads_count(best >= t);
             if (n >= a.keep) bound = t;
             if (n == a.keep) break;
         }
+        const float low = bound ? reach(unordered(bound)) : -INFINITY;
 #pragma unroll
         for (int u = 0; u < kRound; ++u)
-            if (ci[u] != INT_MAX && (uint32_t)(ck[u] >> 32) >= bound) {
-                const int to = atomicAdd(&count, 1);
-                lkey[to] = ck[u], lidx[to] = ci[u];
+            if (ct[u] >= 0 && score[u] >= low) {
+                const int i = (c0 + u * kThreads + tid) / per, to = atomicAdd(&count, 1);
+                lkey[to] = ordered(x[u] == -INFINITY ? (double)x[u] : base[i] + x[u]);
+                lat[to] = place(i, ordered(x[u]), ct[u]);
             }
         __syncthreads();
-        rank_all(lkey, lidx, count, a.keep, [&](int rank, int i) { rkey[rank] = lkey[i], ridx[rank] = lidx[i]; });
+        rank_all(lkey, lat, count, a.keep, [&](int rank, int i) { rkey[rank] = lkey[i], rat[rank] = lat[i]; });
         have = min(count, a.keep);
         __syncthreads();
     }
     if (tid < have) {
-        const unsigned long long u = rkey[tid];
+        const unsigned long long at = rat[tid];
         const long long out = b * a.keep + tid;
-        a.out_scores[out] = unordered((uint32_t)(u >> 32));  // the pair rounded to float32
-        a.parents[out] = ridx[tid] / a.vocab;
-        a.tokens[out] = ridx[tid] % a.vocab;
+        a.out_scores[out] = (float)unordered(rkey[tid]);
+        a.parents[out] = (int)(at >> 56);
+        a.tokens[out] = (int)(at & 0xffffffu);
     }
 }
 
