@@ -7,12 +7,14 @@
 //    bound by those bytes.  It leaves the slice's maximum rounded up, the sum of exp(x - that), and
 //    its `keep` best logits.  To find them each of the eight warps takes the r-th best of its threads' own
 //    maxima, r = keep / 8 rounded up: at least `keep` elements of the slice reach the lowest of the
-//    eight, and few more do (about 60 of 8192 for 16).  Those are gathered and ranked.
+//    eight, and few more do (about 35 of 4096 for 16).  Those are gathered and ranked.  Elements at -inf are
+//    neither: a masked vocabulary costs no more than an open one (one token in a hundred open 51 us, where
+//    ranking the others took 524).
 //  * A block for each batch row adds up the slices' sums as pairs of floats, turns the slices' best into
 //    scores in float64, and takes the best in the same way.  Equal scores of one beam are ordered by
 //    their logits.
 // Ranks are counted (how many others come before), so that nothing depends on an order of arrival.
-// GB300: 64 x 8 x 50277 float32 logits, 16 kept: 50 us, of which the slices 34 (45 % of the copy rate:
+// GB300: 64 x 8 x 50277 float32 logits, 16 kept: 53 us, of which the slices 36 (42 % of the copy rate:
 // 400 instructions a warp for sixteen elements a thread keep the SMs busier than memory) and the
 // merge, a chain of latencies, 16.  1 x 4 x 50277 bf16, 8 kept: 13 us a call, 9.9 in a replayed graph.
 //
@@ -146,7 +148,9 @@ __device__ __forceinline__ uint32_t warp_nth(uint32_t x, int r, int lane) {
 
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArgs a) {
-    constexpr int kList = 2048;  // more candidates than this (equal ones) take the long way
+    // more candidates than are ranked: with less shared memory for a block the merge's do not fit in beside
+    // them before the SM is empty (64 x 8 x 50277 float32: 54.5 us, so 53.0)
+    constexpr int kList = 2048;
     __shared__ uint32_t lkey[kList];
     __shared__ int lidx[kList];
     __shared__ uint32_t top_key[kWarps], nth_key[kWarps];
@@ -169,16 +173,28 @@ __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArg
     float top = f[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(f[e], top);  // the other one of a NaN and a number
-    const uint32_t mine = tid < n ? ordered(top) : 0u;
+    const uint32_t mine = top > -INFINITY ? ordered(top) : 0u;  // 0: nothing to choose from
     const uint32_t best = warp_max(mine), nth = warp_nth(mine, (a.keep + kWarps - 1) / kWarps, lane);
     if (tid == 0) count = 0;
     if (lane == 0) top_key[warp] = best, nth_key[warp] = nth;
     __syncthreads();
     const uint32_t mk = warp_max(lane < kWarps ? top_key[lane] : 0u);
     const uint32_t bound = ~warp_max(lane < kWarps ? ~nth_key[lane] : 0u);
-    // a warp without that many threads with elements bounds nothing
-    const float low = bound ? unordered(bound) : -INFINITY;
-    const float m = unordered(mk);
+    float low = -FLT_MAX;
+    if (bound) {
+        low = unordered(bound);
+    } else if (__syncthreads_count(mine != 0u) >= a.keep) {
+        // masks leave a warp without that many threads with elements above -inf, which bounds nothing: the
+        // keep-th best of all threads' own maxima, bit by bit
+        uint32_t t = 0u;
+        for (int bit = 31; bit >= 0; --bit) {
+            const int reached = __syncthreads_count(mine >= (t | 1u << bit));
+            if (reached >= a.keep) t |= 1u << bit;
+            if (reached == a.keep) break;
+        }
+        low = unordered(t);
+    }
+    const float m = mk ? unordered(mk) : -INFINITY;
     // a whole number, so that sums of other slices come to it by whole powers of e; nothing but -inf: a
     // sum of 0, or of a NaN
     const float shift = m == -INFINITY ? 0.f : ceilf(m);
@@ -215,7 +231,11 @@ __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArg
     }
     const long long out = ((long long)row * a.slices + slice) * a.keep;
     int found = count;
-    if (found <= kList) {
+    // Ranks take a step for each pair, of which a thread has that many; the long way takes some hundred
+    // instructions and two barriers for each candidate kept.  Ties decide which is less: logits of one value,
+    // 64 x 8 x 50277 float32, 16 kept, 247 us, ranked 769.  A limit of 22 sends open vocabularies the long way
+    // (1 kept: 41.0 us, so 39.1), one of 200 leaves ties to the ranks (32 kept, one value: 513 and 909).
+    if (found <= kList && found * ((found + kThreads - 1) / kThreads) <= 64 * a.keep) {
         rank_all(lkey, lidx, found, a.keep, [&](int rank, int i) {
             const uint32_t u = lkey[i];
             a.best[out + rank] = unordered(u);
@@ -223,16 +243,17 @@ __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArg
         });
     } else {
         // one after the other: the best that comes behind the last one taken
-        uint32_t last = 0xffffffffu;
-        int last_i = -1;
+        uint32_t last = 0xffffffffu, key = 0u;
+        int last_i = INT_MAX, at = INT_MAX;
         for (int r = 0; r < a.keep; ++r) {
-            uint32_t key = 0u;
-            int at = INT_MAX;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = e * kThreads + tid;
-                const uint32_t k = ordered(f[e]);
-                if (i < n && f[e] == f[e] && (k < last || (k == last && i > last_i)) && k > key) key = k, at = i;
+            if (at == last_i) {  // at first, and where the last one was this thread's
+                key = 0u, at = INT_MAX;
+#pragma unroll 4
+                for (int i = tid; i < n; i += kThreads) {
+                    const float logit = static_cast<float>(x[i - tid]);
+                    const uint32_t k = ordered(logit);
+                    if (logit >= low && (k < last || (k == last && i > last_i)) && k > key) key = k, at = i;
+                }
             }
             const uint32_t wk = warp_max(key);
             const int wi = (int)__reduce_min_sync(0xffffffffu, (unsigned)(key == wk ? at : INT_MAX));
@@ -250,6 +271,23 @@ __global__ void __launch_bounds__(kThreads, 6) beam_slice_kernel(const SelectArg
             }
         }
         found = a.keep;
+    }
+    // where fewer are above -inf, the slice's first tokens at -inf
+#pragma unroll 1
+    for (int e = 0; e < n && found < a.keep; e += kThreads) {
+        const int i = e + tid;
+        const bool masked = i < n && static_cast<float>(x[e]) == -INFINITY;
+        const unsigned those = __ballot_sync(0xffffffffu, masked);
+        __syncthreads();
+        if (lane == 0) top_key[warp] = __popc(those);
+        __syncthreads();
+        int to = found + __popc(those & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            to += w < warp ? top_key[w] : 0;
+            found += top_key[w];
+        }
+        if (masked && to < a.keep) a.best[out + to] = -INFINITY, a.best_token[out + to] = base + i;
     }
     for (int i = found + tid; i < a.keep; i += kThreads) a.best_token[out + i] = -1;
 }
@@ -270,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
     __shared__ float near[kMostBeams];   // the same rounded
     __shared__ bool over[kMostBeams];
     __shared__ unsigned long long lkey[kList], lat[kList];
-    __shared__ int count;
+    __shared__ int count, masked[kRound][kWarps];
     // the best so far, in order
     __shared__ unsigned long long rkey[kMostKeep], rat[kMostKeep];
     const long long b = blockIdx.x;
@@ -331,7 +369,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
         // with a full list, what cannot come before its last entry is out, and so is all at -inf: it comes
         // in the order of its places
         const float floor = have == a.keep ? reach((float)unordered(rkey[a.keep - 1])) : -INFINITY;
-        uint32_t best = 0u;
+        uint32_t best = 0u;  // of what is above -inf
+        bool any = false;
 #pragma unroll
         for (int u = 0; u < kRound; ++u) {
             const int c = c0 + u * kThreads + tid;
@@ -351,12 +390,13 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
                 }
                 if (x[u] != -INFINITY) score[u] = from + x[u];
                 if (have == a.keep && (x[u] == -INFINITY || score[u] < floor)) ct[u] = -1;
-                if (ct[u] >= 0) best = max(best, ordered(score[u]));
+                if (ct[u] >= 0) any = true;
+                if (ct[u] >= 0 && x[u] != -INFINITY) best = max(best, ordered(score[u]));
             }
         }
         if (tid == 0) count = have;
         if (tid < have) lkey[tid] = rkey[tid], lat[tid] = rat[tid];
-        if (!__syncthreads_or(best != 0u)) continue;
+        if (!__syncthreads_or(any)) continue;
         // the keep-th best of the threads' own best, bit by bit: at least `keep` candidates reach it (beams
         // differ too much for a bound by warps)
         uint32_t bound = 0u;
@@ -369,11 +409,34 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const SelectArgs a
         const float low = bound ? reach(unordered(bound)) : -INFINITY;
 #pragma unroll
         for (int u = 0; u < kRound; ++u)
-            if (ct[u] >= 0 && score[u] >= low) {
+            if (ct[u] >= 0 && x[u] != -INFINITY && score[u] >= low) {
                 const int i = (c0 + u * kThreads + tid) / per, to = atomicAdd(&count, 1);
-                lkey[to] = ordered(x[u] == -INFINITY ? (double)x[u] : base[i] + x[u]);
+                lkey[to] = ordered(base[i] + x[u]);
                 lat[to] = place(i, ordered(x[u]), ct[u]);
             }
+        if (!bound && have < a.keep) {  // maybe fewer than are kept: the first at -inf too
+            unsigned those[kRound];
+#pragma unroll
+            for (int u = 0; u < kRound; ++u) {
+                those[u] = __ballot_sync(0xffffffffu, ct[u] >= 0 && x[u] == -INFINITY);
+                if (lane == 0) masked[u][warp] = __popc(those[u]);
+            }
+            __syncthreads();
+            int before = 0;
+#pragma unroll
+            for (int u = 0; u < kRound; ++u) {
+                int r = before + __popc(those[u] & ((1u << lane) - 1));
+                for (int w = 0; w < kWarps; ++w) {
+                    r += w < warp ? masked[u][w] : 0;
+                    before += masked[u][w];
+                }
+                if (those[u] >> lane & 1 && r < a.keep) {
+                    const int to = atomicAdd(&count, 1);
+                    lkey[to] = ordered((double)-INFINITY);
+                    lat[to] = place((c0 + u * kThreads + tid) / per, 0u, ct[u]);
+                }
+            }
+        }
         __syncthreads();
         rank_all(lkey, lat, count, a.keep, [&](int rank, int i) { rkey[rank] = lkey[i], rat[rank] = lat[i]; });
         have = min(count, a.keep);

@@ -50,3 +50,79 @@ def test_scores_at_the_end_of_the_range(ssd):  # noqa: F811
     scores, parents, tokens = ssd.beam_select(x, s, 64)
     assert torch.equal(parents.long(), want[1]) and torch.equal(tokens.long(), want[2])
     assert torch.equal(scores, want[0].float())
+
+
+def _masked(x, kind):
+    import torch
+    V = x.shape[-1]
+    t = torch.arange(V, device="cuda")
+    if isinstance(kind, float):
+        open_ = torch.rand(V, generator=torch.Generator(device="cuda").manual_seed(9), device="cuda") < kind
+    else:
+        open_ = {"runs": t % 256 < 128, "few": (t >= V // 3) & (t < V // 3 + 20), "last": t == V - 1,
+                 "threads": t % 256 < 40, "one warp": t % 256 >= 32}[kind]
+    return x.masked_fill(~open_, -torch.inf)
+
+
+# the smaller batch takes slices of 2048 elements, the larger one of 4096
+@pytest.mark.parametrize("B,K,V,dtype", [(1, 4, 9001, "float32"), (90, 4, 12289, "float32"), (40, 8, 8190, "bfloat16")])
+@pytest.mark.parametrize("kind", [0.5, 0.1, 0.01, 0.001, "runs", "few", "last", "threads", "one warp"])
+def test_masked_vocabularies(ssd, kind, B, K, V, dtype):  # noqa: F811
+    """Constrained decoding: most tokens at -inf, at random and in patterns that leave some threads and
+    warps without any; some beams ended or without a choice."""
+    import torch
+    x, s = _make(B, K, V, getattr(torch, dtype), seed=3)
+    x = _masked(x, kind)
+    x[0, 1] = -torch.inf
+    f = torch.zeros(B, K, dtype=torch.bool, device="cuda")
+    f[0, 2] = f[-1, 0] = True
+    for keep in (1, 16, 64):
+        _same(ssd.beam_select(x, s, keep, finished=f, pad_token=3), ref.beam_select(x, s, keep, f, 3))
+
+
+@pytest.mark.parametrize("V", [4095, 4096, 8191, 8192, 12289])
+def test_wide_slices(ssd, V):  # noqa: F811
+    """Borders of the slices of 4096 elements; equal and rounded logits, of which more reach the bound
+    than are ranked."""
+    import torch
+    x, s = _make(80, 4, V, torch.float32, seed=V)
+    x[1] = 0.0
+    x[2] = torch.round(x[2])
+    x[3] = x[3, :1]
+    s[3] = -1.0
+    x[4] = torch.round(x[4] / 4)
+    x[5, :, :100] = 3.0
+    for keep in (1, 9, 64):
+        _same(ssd.beam_select(x, s, keep), ref.beam_select(x, s, keep))
+
+
+def _time(f):
+    """Microseconds of a call in a replayed graph: the least of five runs of twenty."""
+    import torch
+    f()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f()
+    graph.replay()
+    best = float("inf")
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(20):
+            graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 50)
+    return best
+
+
+@pytest.mark.parametrize("B,K,keep", [(1, 4, 8), (64, 8, 16)])
+def test_masks_cost_little(ssd, B, K, keep):  # noqa: F811
+    """A masked vocabulary takes no more than twice the time of an open one (ranking what is at -inf
+    took ten to sixty times as long)."""
+    import torch
+    x, s = _make(B, K, 50277, torch.float32, seed=6)
+    whole = _time(lambda: ssd.beam_select(x, s, keep))
+    for kind in (0.5, 0.01, 0.001, "runs", "few", "threads"):
+        y = _masked(x, kind)
+        assert _time(lambda: ssd.beam_select(y, s, keep)) <= 2 * whole, kind
