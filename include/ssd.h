@@ -432,9 +432,9 @@ ssd_status_t ssd_gated_norm_backward(const ssd_gated_norm_t* norm, const void* d
  * Outputs and gradients of tokens before the first border or from the last one on are zero.
  * bf16 calls with N and P 64 or 128, whose rows all start on 16 bytes, run on the tensor cores in
  * blocks of 128 tokens: there a NaN or an infinity in a token reaches the outputs of all tokens
- * of its sequence in its block.  So do bf16 calls of other N and P with 16384 rows (of a head and
- * token) or more and N + P at least a quarter of what they come to rounded up to 64 or 128, by
- * copies in the workspace.  Forwards of up to 16 tokens a sequence (a batch row, or all packed
+ * of its sequence in its block.  So do bf16 calls of other N and P, or with rows off 16 bytes, with
+ * 16384 rows (of a head and token) or more and N + P at least a quarter of what they come to
+ * rounded up to 64 or 128, by copies in the workspace.  Forwards of up to 16 tokens a sequence (a batch row, or all packed
  * ones) are stepped through token by token, and all other calls run the walk on the plain cores, in
  * float32. */
 typedef struct {
@@ -453,7 +453,10 @@ typedef struct {
 } ssd_linattn_t;
 
 /* Bytes of workspace of ssd_linear_attention_forward (for_backward = 0, may be 0) or
- * _backward; they follow the current device's SM count. */
+ * _backward; they follow the current device's SM count.  They do for any tensors of these
+ * strides.  Where the strides are multiples of 8 elements but a tensor does not start on 16
+ * bytes, a larger workspace, of the size for a q_stride that is no such multiple, lets the call go
+ * by copies too; otherwise it runs on the plain cores. */
 ssd_status_t ssd_linear_attention_workspace_size(const ssd_linattn_t* prob, int for_backward,
                                                  size_t* bytes);
 

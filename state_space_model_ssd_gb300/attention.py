@@ -35,9 +35,10 @@ def linear_attention_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, in
     bfloat16 calls with N and P 64 or 128, every row on 16 bytes, run on the tensor cores in
     blocks of 128 tokens (the masked products and the state that meets q are rounded to bfloat16
     there, the states themselves are float32): a NaN or an infinity in a token then reaches the
-    outputs of all tokens of its sequence in its block.  bfloat16 calls of other sizes take that way too,
-    by copies in the workspace, from 16384 rows (of a head and token) on, unless they are so narrow
-    that the copies were over four times as wide.  Forwards of up to 16 tokens a sequence are stepped
+    outputs of all tokens of its sequence in its block.  bfloat16 calls of other sizes, or with rows off
+    16 bytes, take that way too, by copies in the workspace, from 16384 rows (of a head and token)
+    on, unless they are so narrow that the copies were over four times as wide (or tensors do not
+    start on 16 bytes and ``workspace`` is too small for copies).  Forwards of up to 16 tokens a sequence are stepped
     through, and all other calls run on the plain cores, in float32."""
     args = (q, k, v, log_decay, scale, cu_seqlens, initial_state, final_state, out, final_state_out, workspace)
     return (layer._ext.linear_attention_forward(*args) if stream is None

@@ -801,6 +801,19 @@ void attn_problem(AttnCall* c, const Tensor& q, const Tensor& k, const Tensor& v
     c->p.o_stride = H * P;
     c->p.scale = scale == Py_None ? (float)(1.0 / std::sqrt((double)N)) : (float)number(scale);
 }
+// Bytes of workspace; where the call brings none, also for the copies by which tensors that do not start
+// on 16 bytes reach the tensor cores.
+size_t attn_workspace(const ssd_linattn_t& p, int bwd, PyObject* given, std::initializer_list<const Tensor*> tensors) {
+    size_t need = 0, more = 0;
+    ok(ssd_linear_attention_workspace_size(&p, bwd, &need), "ssd_linear_attention_workspace_size");
+    uintptr_t at = 0;
+    for (const Tensor* t : tensors) at |= (uintptr_t)t->data_ptr();
+    if (given != Py_None || at % 16 == 0) return need;
+    ssd_linattn_t odd = p;
+    odd.q_stride |= 1;
+    ok(ssd_linear_attention_workspace_size(&odd, bwd, &more), "ssd_linear_attention_workspace_size");
+    return need > more ? need : more;
+}
 float* floats(const Tensor* t) { return static_cast<float*>(ptr(t)); }
 float* floats(const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
 int32_t* ints(const Tensor* t) { return static_cast<int32_t*>(ptr(t)); }
@@ -828,9 +841,7 @@ PyObject* linear_attention_forward(PyObject* const* a) {
     } else if (truth(a[7])) {
         final = empty({c.n, H, P, N}, at::kFloat, dev);
     }
-    size_t need = 0;
-    ok(ssd_linear_attention_workspace_size(&c.p, 0, &need), "ssd_linear_attention_workspace_size");
-    const Scratch ws(a[10], need, dev);
+    const Scratch ws(a[10], attn_workspace(c.p, 0, a[10], {&q, &k, &v, &o}), dev);
     ok(ssd_linear_attention_forward(&c.p, q.data_ptr(), k.data_ptr(), v.data_ptr(), floats(&ld), ints(cu),
                                     floats(init), o.data_ptr(), floats(final), ws.p, ws.n, stream_of(dev)),
        "ssd_linear_attention_forward");
@@ -871,9 +882,8 @@ PyObject* linear_attention_backward(PyObject* const* a) {
         check(d0, "d_initial_state", dev, at::kFloat, {c.n, H, P, N});
     else if (truth(a[9]))
         d0 = empty({c.n, H, P, N}, at::kFloat, dev);
-    size_t need = 0;
-    ok(ssd_linear_attention_workspace_size(&c.p, 1, &need), "ssd_linear_attention_workspace_size");
-    const Scratch ws(a[11], need, dev);
+    const Scratch ws(a[11], attn_workspace(c.p, 1, a[11], {&q, &k, &v, &dout, &grads[0].t, &grads[1].t, &grads[2].t}),
+                     dev);
     ok(ssd_linear_attention_backward(&c.p, q.data_ptr(), k.data_ptr(), v.data_ptr(), floats(&ld), ints(cu),
                                      floats(init), dout.data_ptr(), floats(dfinal), grads[0].t.data_ptr(),
                                      grads[1].t.data_ptr(), grads[2].t.data_ptr(), floats(d0), ws.p, ws.n,

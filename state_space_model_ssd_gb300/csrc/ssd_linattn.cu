@@ -454,8 +454,10 @@ struct Plan {
     long long ids;
     size_t s_seg, r_seg, dk_part, dv_part, total;
     bool fits;                   // its items are fewer than 2^31
-    // bf16 of other channels than 64 and 128, laid out in the workspace for the tensor cores: the problem
-    // as it is there (pads) and its tensors: q, k, v, o or do, the gradients, the states
+    bool tc;                     // it runs on the tensor cores
+    // bf16 of other channels than 64 and 128 or with rows off 16 bytes, laid out in the workspace for the
+    // tensor cores: the problem as it is there (pads) and its tensors: q, k, v, o or do, the gradients, the
+    // states
     bool pads;
     ssd_linattn_t p;
     size_t q, k, v, o, dq, dk, dv, s_in, s_out, r_in;
@@ -515,17 +517,27 @@ bool tensor(int n) { return n == 64 || n == 128; }
 // Whether rows are worth laying out anew, with zeros up to 64 or 128 channels: two passes over the
 // tensors, which are at most four times as wide, and two launches, so that few tokens are not.  32768
 // tokens of 24 heads, 80 x 96: forward 776 us of which 405 are the copies, backward 1487 (669), on the
-// plain cores 4085 and 9442; 16384 rows of 33 x 33 channels 56 and 63, for 52 and 103.
-bool pads(const ssd_linattn_t& p) {
+// plain cores 4085 and 9442; 64 x 128 with three more elements a token 527 and 1054, on the plain cores 2740
+// and 7724; 16384 rows of 33 x 33 channels 56 and 63, for 52 and 103.
+bool pads(const ssd_linattn_t& p, bool rows16) {
     const int P = p.headdim <= 64 ? 64 : 128, N = p.dstate <= 64 ? 64 : 128;
-    return p.dtype == SSD_DTYPE_BF16 && !(tensor(p.headdim) && tensor(p.dstate)) && p.seqlen > kFewTokens &&
+    return p.dtype == SSD_DTYPE_BF16 && !(rows16 && tensor(p.headdim) && tensor(p.dstate)) && p.seqlen > kFewTokens &&
            p.batch * p.seqlen * p.nheads >= kPadRows && P + N <= 4 * (p.headdim + p.dstate);
 }
-Plan make_plan(const ssd_linattn_t& given, bool bwd) {
+// Whether tokens of bf16 tensors that start on 16 bytes do so too.  Gradients of shared heads are
+// written by a kernel of their own.
+bool tokens16(const ssd_linattn_t& p, bool bwd) {
+    int64_t s = p.q_stride | p.k_stride | p.v_stride | p.o_stride;
+    if (bwd) s |= p.dq_stride;
+    if (bwd && p.nheads == p.ngroups) s |= p.dk_stride | p.dv_stride;
+    return s % 8 == 0;
+}
+// rows16: every token starts on 16 bytes.
+Plan make_plan(const ssd_linattn_t& given, bool bwd, bool rows16, bool copies = true) {
     Plan l = {};
     ssd_linattn_t& p = l.p;
     p = given;
-    l.pads = pads(p);
+    l.pads = copies && pads(p, rows16);
     if (l.pads) {
         p.headdim = p.headdim <= 64 ? 64 : 128, p.dstate = p.dstate <= 64 ? 64 : 128;
         const int64_t H = p.nheads, G = p.ngroups;
@@ -534,7 +546,8 @@ Plan make_plan(const ssd_linattn_t& given, bool bwd) {
     }
     l.T = p.batch * p.seqlen;
     l.n = p.nseq ? p.nseq : (int)p.batch;
-    const bool tc = p.dtype == SSD_DTYPE_BF16 && tensor(p.headdim) && tensor(p.dstate);
+    const bool tc = p.dtype == SSD_DTYPE_BF16 && tensor(p.headdim) && tensor(p.dstate) && (rows16 || l.pads);
+    l.tc = tc;
     const int tile = tc ? kTcTile : simt_tile(bwd ? std::max(p.headdim, p.dstate) : p.headdim);
     const int least = tc ? 512 : 64, step = tc ? kTcChunk : kQ;
     const auto tiles = [&](int n) { return (n + tile - 1) / tile; };
@@ -575,6 +588,16 @@ Plan make_plan(const ssd_linattn_t& given, bool bwd) {
     }
     l.total = at;
     return l;
+}
+// The plan of a call whose tensors start on 16 bytes, or do not: then the strides, by which the workspace
+// was asked for, say nothing, and there are copies if it holds them.
+Plan call_plan(const ssd_linattn_t& p, bool bwd, std::initializer_list<const void*> tensors, size_t workspace_bytes) {
+    const Plan l = make_plan(p, bwd, tokens16(p, bwd));
+    uintptr_t at = 0;
+    for (const void* t : tensors) at |= (uintptr_t)t;
+    if (!l.tc || l.pads || at % 16 == 0) return l;
+    const Plan c = make_plan(p, bwd, false);
+    return c.pads && workspace_bytes >= c.total ? c : make_plan(p, bwd, false, false);
 }
 
 WalkArgs common(const ssd_linattn_t& p, const Plan& l, const float* ld, const int32_t* cu) {
@@ -815,9 +838,11 @@ ssd_status_t ssd_linear_attention_workspace_size(const ssd_linattn_t* prob, int 
     if (!bytes) return SSD_ERR_INVALID_ARG;
     const ssd_status_t st = check_sizes(prob, for_backward != 0);
     if (st != SSD_OK) return st;
-    const Plan l = make_plan(*prob, for_backward != 0);
+    const bool bwd = for_backward != 0;
+    const Plan l = make_plan(*prob, bwd, tokens16(*prob, bwd));
     if (!l.fits) return SSD_ERR_UNSUPPORTED;
-    *bytes = l.total;
+    // enough for the plain cores too, where a call's tensors may not start on 16 bytes
+    *bytes = l.tc && !l.pads ? std::max(l.total, make_plan(*prob, bwd, false, false).total) : l.total;
     return SSD_OK;
 }
 
@@ -838,7 +863,7 @@ ssd_status_t ssd_linear_attention_forward(const ssd_linattn_t* prob, const void*
         !aligned_to(log_decay, 4) || !aligned_to(cu_seqlens, 4) || !aligned_to(initial_state, 4) ||
         !aligned_to(final_state, 4) || !aligned_to(workspace, 256))
         return SSD_ERR_ALIGNMENT;
-    const Plan l = make_plan(p, false);
+    const Plan l = call_plan(p, false, {q, k, v, o}, workspace_bytes);
     if (!l.fits) return SSD_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSD_ERR_WORKSPACE;
     const long long states = (long long)l.n * H * P * N;
@@ -891,7 +916,8 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
         !aligned_to(cu_seqlens, 4) || !aligned_to(initial_state, 4) || !aligned_to(d_final_state, 4) ||
         !aligned_to(d_initial_state, 4) || !aligned_to(workspace, 256))
         return SSD_ERR_ALIGNMENT;
-    const Plan l = make_plan(p, true);
+    const bool own = p.nheads == p.ngroups;
+    const Plan l = call_plan(p, true, {q, k, v, dout, dq, own ? dk : nullptr, own ? dv : nullptr}, workspace_bytes);
     if (!l.fits) return SSD_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSD_ERR_WORKSPACE;
     const long long states = (long long)l.n * H * P * N;

@@ -1,11 +1,38 @@
 """Linear attention: borders that are not what they should be, rows of no sequence, and which of the
 kernels takes a call."""
 
+import contextlib
+import ctypes
+
 import pytest
 
 from test_linear_attention_gpu import _backward, _forward, _make, ssd  # noqa: F401  (ssd is the built package)
 
 pytestmark = pytest.mark.gpu
+
+
+@contextlib.contextmanager
+def _launches(ssd, names):  # noqa: F811
+    """The names of the kernels launched meanwhile, into the list ``names``."""
+    ssd.profiler.reset()
+    ssd.profiler.enable(True)
+    try:
+        yield
+        names += ssd.profiler.read()
+    finally:
+        ssd.profiler.enable(False)
+        ssd.profiler.reset()
+
+
+def _workspace_size(s, bwd):
+    from state_space_model_ssd_gb300 import _lib
+    q, k, v = s["q"], s["k"], s["v"]
+    (B, L, H, N), G, P = q.shape, k.shape[2], v.shape[3]
+    p = _lib.LinAttnProblem(B, L, q.stride(1), k.stride(1), v.stride(1), H * P, *((H * N, G * N, G * P) if bwd else (0, 0, 0)),
+                            H, G, P, N, 0 if s["cu"] is None else s["n"], 1 if q.dtype.itemsize == 2 else 0, s["scale"])
+    n = ctypes.c_size_t()
+    assert _lib.lib().ssd_linear_attention_workspace_size(ctypes.byref(p), bwd, ctypes.byref(n)) == 0
+    return n.value
 
 
 # few tokens, plain cores, tensor cores uncut and cut, rows laid out anew; heads of their own and shared
@@ -26,3 +53,54 @@ def test_tokens_before_the_first_sequence(ssd, L, H, G, P, N, cu):  # noqa: F811
     _backward(ssd, s, tc, out=outs, workspace=ws)
     for t in (o, *(outs[n] for n in ("dq", "dk", "dv"))):
         assert not t[:, :cu[0]].any() and not t[:, cu[-1]:].any()
+
+
+# an odd number of elements beside q, k and v; whole rows on 16 bytes, but q, k and v off them
+@pytest.mark.parametrize("L,H,G,P,N,cu", [(2100, 8, 8, 64, 128, None), (2100, 8, 2, 128, 64, [0, 1290, 1290, 1300, 1428]),
+                                          (4200, 4, 4, 64, 64, None)])
+@pytest.mark.parametrize("offset", [3, 4])
+def test_rows_off_16_bytes(ssd, L, H, G, P, N, cu, offset):  # noqa: F811
+    """Many rows of 64 and 128 channels reach the tensor cores by copies, as those of other channels do."""
+    import torch
+    s = _make(1, L, H, G, P, N, "bf16", cu, True, True, seed=29, offset=offset)
+    assert (s["q"].stride(1) % 8 == 0) == (offset == 4) and s["q"].data_ptr() % 16
+    names = []
+    with _launches(ssd, names):
+        _forward(ssd, s, True)
+        _backward(ssd, s, True)
+    assert {"linattn_pad", "linattn_tc_walk", "linattn_unpad"} <= set(names) and "linattn_walk" not in names
+    # a workspace of the size asked for by the strides does
+    names = []
+    with _launches(ssd, names):
+        _forward(ssd, s, True, workspace=torch.empty(_workspace_size(s, 0), dtype=torch.uint8, device="cuda"))
+        _backward(ssd, s, True, workspace=torch.empty(_workspace_size(s, 1), dtype=torch.uint8, device="cuda"))
+    assert ("linattn_pad" in names) == (offset == 3) and ("linattn_walk" in names) == (offset == 4)
+
+
+@pytest.mark.parametrize("offset", [3, 4])
+def test_few_rows_off_16_bytes(ssd, offset):  # noqa: F811
+    """Too few rows for copies: cut for the plain cores, which go through 32 tokens at a time, not for the
+    tensor cores."""
+    s = _make(1, 400, 2, 2, 64, 64, "bf16", None, True, True, offset=offset)
+    names = []
+    with _launches(ssd, names):
+        _forward(ssd, s, False)
+        _backward(ssd, s, False)
+    assert set(names) == {"linattn_sums", "linattn_scan", "linattn_walk"}
+
+
+# the tests of the tensor cores take them, directly or by copies
+@pytest.mark.parametrize("L,H,G,P,N,cu,names", [
+    (1500, 3, 3, 64, 64, None, {"linattn_tc_sums", "linattn_scan", "linattn_tc_walk"}),
+    (130, 2, 1, 128, 64, None, {"linattn_tc_walk", "linattn_shared_sum"}),
+    (257, 4, 2, 128, 128, [0, 0, 1, 64, 191, 257], {"linattn_tc_walk", "linattn_shared_sum"}),
+    (2100, 8, 8, 80, 96, None, {"linattn_pad", "linattn_tc_sums", "linattn_scan", "linattn_tc_walk", "linattn_unpad"}),
+    (2047, 8, 8, 33, 65, None, {"linattn_sums", "linattn_scan", "linattn_walk"}),
+    (2100, 8, 8, 12, 10, None, {"linattn_sums", "linattn_scan", "linattn_walk"})])
+def test_which_kernels_run(ssd, L, H, G, P, N, cu, names):  # noqa: F811
+    s = _make(1, L, H, G, P, N, "bf16", cu, True, seed=5)
+    got = []
+    with _launches(ssd, got):
+        ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], cu_seqlens=s["cu"], final_state=True)
+        ssd.linear_attention_backward(s["q"], s["k"], s["v"], s["ld"], s["do"], cu_seqlens=s["cu"])
+    assert set(got) == names
