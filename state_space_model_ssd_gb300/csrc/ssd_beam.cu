@@ -551,6 +551,8 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
             copy_piece<uint4>(to_, from_, bytes);
         else if ((off & 3) == 0)
             copy_piece<uint32_t>(to_, from_, bytes);
+        else if ((off & 1) == 0)
+            copy_piece<uint16_t>(to_, from_, bytes);
         else
             copy_piece<char>(to_, from_, bytes);
     }

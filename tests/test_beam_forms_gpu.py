@@ -126,3 +126,38 @@ def test_masks_cost_little(ssd, B, K, keep):  # noqa: F811
     for kind in (0.5, 0.01, 0.001, "runs", "few", "threads"):
         y = _masked(x, kind)
         assert _time(lambda: ssd.beam_select(y, s, keep)) <= 2 * whole, kind
+
+
+@pytest.mark.parametrize("shape", [(1,), (3,), (4, 1791), (8193,), (20001,)])
+def test_reorder_slots_of_odd_elements(ssd, shape):  # noqa: F811
+    """Slots of two-byte elements that are off four bytes, contiguous and in wider rows."""
+    import torch
+    n = 12
+    row = 1
+    for d in shape:
+        row *= d
+    wide = torch.randn(n, row + 1, device="cuda").half()
+    caches = [torch.randn(n, *shape, device="cuda").bfloat16(), wide[:, 1:], wide.clone()[:, :row]]
+    slots = torch.arange(n, dtype=torch.int32, device="cuda").view(3, 4)
+    parents = torch.tensor([[1, 1, 2, 3], [0, 0, 0, 0], [3, 2, 2, 3]], dtype=torch.int32, device="cuda")
+    want, copies = ref.beam_reorder(slots, parents)
+    after = [c.clone() for c in caches]
+    for c in after:
+        for frm, to in copies:
+            c[to] = c[frm]
+    edge = wide[:, :1].clone()
+    assert ssd.beam_reorder(caches, slots, parents).tolist() == want
+    for c, a in zip(caches, after):
+        assert torch.equal(c, a)
+    assert torch.equal(wide[:, :1], edge)
+
+
+def test_reorder_moves_two_bytes_at_a_time(ssd):  # noqa: F811
+    """Odd numbers of two-byte elements go faster than as many single bytes."""
+    import torch
+    n, row = 64, 400001
+    slots = torch.arange(n, dtype=torch.int32, device="cuda").view(16, 4)
+    parents = torch.tensor([[0, 0, 1, 1]] * 16, dtype=torch.int32, device="cuda")
+    two = [torch.zeros(n, row, device="cuda", dtype=torch.bfloat16)]
+    one = [torch.zeros(n, 2 * row + 1, device="cuda", dtype=torch.uint8)]
+    assert _time(lambda: ssd.beam_reorder(two, slots, parents)) <= 0.9 * _time(lambda: ssd.beam_reorder(one, slots, parents))
