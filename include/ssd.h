@@ -481,7 +481,7 @@ ssd_status_t ssd_linear_attention_backward(const ssd_linattn_t* prob, const void
 /* One token for each of prob->batch rows (prob->seqlen = 1, nseq = 0).  Row i uses cache slot
  * slots[i] (NULL: i) of state [nslots][H][P][N] float32, updated in place; a slot outside
  * 0 .. nslots - 1 marks a padding row, whose o is zero and which touches no state.  The live
- * rows' slots must differ. */
+ * rows' slots must differ.  Where N is a multiple of 4, state is 16-byte aligned. */
 ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int32_t nslots, float* state,
                                        const void* q, const void* k, const void* v,
                                        const float* log_decay, const int32_t* slots, void* o,

@@ -61,7 +61,8 @@ def linear_attention_backward(q, k, v, log_decay, do, scale=None, cu_seqlens=Non
 
 def linear_attention_step(state, q, k, v, log_decay, scale=None, slots=None, out=None, stream=None):
     """One token for each row of a batch: q ``[batch, H, N]``, k ``[batch, G, N]``, v
-    ``[batch, G, P]``.  ``state`` float32 ``[nslots, H, P, N]`` is updated in place.  ``slots``
+    ``[batch, G, P]``.  ``state`` float32 ``[nslots, H, P, N]`` (on 16 bytes where N is a multiple of
+    4) is updated in place.  ``slots``
     int32 ``[batch]``: each row's cache slot (default: its index; the live rows' must differ); a
     row whose slot is negative or beyond the cache is padding, its output zero.  Returns o
     ``[batch, H, P]``."""

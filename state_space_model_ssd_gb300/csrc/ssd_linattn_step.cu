@@ -280,7 +280,8 @@ extern "C" ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int
         return SSD_ERR_INVALID_ARG;
     if (!state || !q || !k || !v || !log_decay || !o) return SSD_ERR_INVALID_ARG;
     const size_t e = dtype_size(p.dtype);
-    if (!aligned_to(state, 16) || !aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) ||
+    const int vec = N % 4 == 0 ? 4 : 1;  // elements of the state in a piece
+    if (!aligned_to(state, 4 * vec) || !aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) ||
         !aligned_to(o, e) || !aligned_to(log_decay, 4) || !aligned_to(slots, 4))
         return SSD_ERR_ALIGNMENT;
     if (clash({Span(state, nslots * H * P * N, 4), Span(o, B, p.o_stride, H * P, e)},
@@ -292,7 +293,6 @@ extern "C" ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int
     a.qs = p.q_stride, a.ks = p.k_stride, a.vs = p.v_stride, a.os = p.o_stride;
     a.H = p.nheads, a.r = (int)(H / G), a.P = p.headdim, a.N = p.dstate, a.nslots = nslots;
     a.scale = p.scale;
-    const int vec = N % 4 == 0 ? 4 : 1;
     step_shape(p.headdim, p.dstate, vec, B * H, &a.lanes, &a.rows);
     const dim3 grid((unsigned)((P + a.rows - 1) / a.rows), (unsigned)H, (unsigned)B);
     Launch L;

@@ -104,3 +104,18 @@ def test_which_kernels_run(ssd, L, H, G, P, N, cu, names):  # noqa: F811
         ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], cu_seqlens=s["cu"], final_state=True)
         ssd.linear_attention_backward(s["q"], s["k"], s["v"], s["ld"], s["do"], cu_seqlens=s["cu"])
     assert set(got) == names
+
+
+def test_step_on_states_off_16_bytes(ssd):  # noqa: F811
+    """One layer's part of a cache for all layers, with rows that no 16 bytes divide: as by itself."""
+    import torch
+    s = _make(3, 1, 3, 3, 5, 21, "bf16", seed=37)
+    cache = torch.randn(4, 5, 3, 5, 21, device="cuda")
+    before = cache.clone()
+    assert cache[1].data_ptr() % 16
+    args = s["q"][:, 0], s["k"][:, 0], s["v"][:, 0], s["ld"]
+    alone = cache[1].clone()
+    want = ssd.linear_attention_step(alone, *args)
+    assert torch.equal(ssd.linear_attention_step(cache[1], *args), want)
+    before[1] = alone
+    assert torch.equal(cache, before)
