@@ -119,3 +119,88 @@ def test_step_on_states_off_16_bytes(ssd):  # noqa: F811
     assert torch.equal(ssd.linear_attention_step(cache[1], *args), want)
     before[1] = alone
     assert torch.equal(cache, before)
+
+
+def _guarded(n, dtype, shape):
+    """A tensor in the middle of a buffer of 7, 256-byte aligned, and a check that what is around it is left."""
+    import torch
+    size = torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((n + 2 * 4096 // size,), 7, dtype=dtype, device="cuda")
+    lo = 4096 // size
+
+    def left():
+        return bool((buf[:lo] == 7).all()) and bool((buf[lo + n:] == 7).all())
+
+    return buf[lo:lo + n].view(shape), left
+
+
+# plain cores, tensor cores cut and uncut, rows laid out anew, shared heads, a few tokens
+@pytest.mark.parametrize("L,H,G,P,N,dtype", [(14, 2, 2, 20, 20, "bf16"), (300, 2, 2, 20, 20, "f32"),
+                                             (2000, 2, 2, 64, 64, "bf16"), (2000, 4, 2, 64, 128, "bf16"),
+                                             (300, 4, 4, 128, 64, "bf16"), (2100, 8, 4, 80, 96, "bf16")])
+@pytest.mark.parametrize("kind", ["falls", "far", "backwards", "saw"])
+def test_borders_that_fall_write_nothing_outside(ssd, L, H, G, P, N, dtype, kind):  # noqa: F811
+    """Both directions, with states, in workspaces and outputs of exactly their sizes, in the middle of
+    others' memory; afterwards a sound call gives what it should."""
+    import torch
+    m = L - 1
+    cu = {"falls": [0, m, m // 4, m // 2], "far": [-5, m // 3, 9 * L, m], "backwards": [m, m // 2, m // 3, 0],
+          "saw": [0, m, 1, L, 2, m // 2, m // 3, L]}[kind]
+    s = _make(1, L, H, G, P, N, dtype, cu, True, seed=41)
+    n, dt = len(cu) - 1, s["q"].dtype
+    checks = []
+
+    def out(dtype, *shape):
+        size = 1
+        for d in shape:
+            size *= d
+        t, left = _guarded(size, dtype, shape)
+        checks.append(left)
+        return t
+
+    o, final = out(dt, 1, L, H, P), out(torch.float32, n, H, P, N)
+    ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], scale=s["scale"], cu_seqlens=s["cu"],
+                                 initial_state=s["init"], out=o, final_state_out=final,
+                                 workspace=out(torch.uint8, _workspace_size(s, 0)))
+    grads = {"dq": out(dt, 1, L, H, N), "dk": out(dt, 1, L, G, N), "dv": out(dt, 1, L, G, P),
+             "d_initial_state": out(torch.float32, n, H, P, N)}
+    ssd.linear_attention_backward(s["q"], s["k"], s["v"], s["ld"], s["do"], scale=s["scale"], cu_seqlens=s["cu"],
+                                  initial_state=s["init"], d_final_state=s["dfinal"], out=grads,
+                                  workspace=out(torch.uint8, _workspace_size(s, 1)))
+    torch.cuda.synchronize()
+    assert all(left() for left in checks)
+    assert ssd.layer_status() == 0
+    s = _make(1, L, H, G, P, N, dtype, [0, m // 2, m], True, seed=43)
+    _forward(ssd, s, dtype == "bf16")
+    _backward(ssd, s, dtype == "bf16")
+
+
+@pytest.mark.parametrize("L,H,G,P,N", [(2100, 8, 8, 80, 96), (2100, 8, 2, 33, 65), (2100, 8, 8, 64, 64)])
+def test_a_sequence_of_nan_stays_alone_in_copies(ssd, L, H, G, P, N):  # noqa: F811
+    """NaN and infinities of one sequence, its states among them, stay out of the others' outputs and
+    gradients where rows are laid out anew."""
+    import torch
+    a, b = 700, 1413
+    s = _make(1, L, H, G, P, N, "bf16", [0, a, b, L], True, P == 64, seed=47, offset=3)
+
+    def run():
+        names = []
+        with _launches(ssd, names):
+            o, f = ssd.linear_attention_forward(s["q"], s["k"], s["v"], s["ld"], cu_seqlens=s["cu"],
+                                                initial_state=s["init"], final_state=True)
+            g = ssd.linear_attention_backward(s["q"], s["k"], s["v"], s["ld"], s["do"], cu_seqlens=s["cu"],
+                                              initial_state=s["init"], d_final_state=s["dfinal"], d_initial_state=True)
+        assert "linattn_pad" in names
+        return (o, g["dq"], g["dk"], g["dv"]), (f, g["d_initial_state"])
+
+    rows0, states0 = run()
+    for x in "qv":
+        s[x][:, a:b] = float("nan")
+    s["k"][:, a:b] = float("inf")
+    s["do"][:, a:b] = float("-inf")
+    s["init"][1] = s["dfinal"][1] = float("nan")
+    rows1, states1 = run()
+    for x, y in zip(rows0, rows1):
+        assert torch.isfinite(x).all() and torch.equal(x[:, :a], y[:, :a]) and torch.equal(x[:, b:], y[:, b:])
+    for x, y in zip(states0, states1):
+        assert torch.equal(x[[0, 2]], y[[0, 2]])
