@@ -33,8 +33,9 @@ def linear_attention_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, in
     final states as the initial ones.
 
     bfloat16 calls with N and P 64 or 128, every row on 16 bytes, run on the tensor cores in
-    blocks of 128 tokens (the masked products and the state that meets q are rounded to bfloat16
-    there, the states themselves are float32): a NaN or an infinity in a token then reaches the
+    blocks of 128 tokens (the state that meets q is rounded to bfloat16 there, and so are the masked
+    products, except of sequences within a block or in calls too small to fill the GPU, where two
+    bfloat16 terms hold them; the states themselves are float32): a NaN or an infinity in a token then reaches the
     outputs of all tokens of its sequence in its block.  bfloat16 calls of other sizes, or with rows off
     16 bytes, take that way too, by copies in the workspace, from 16384 rows (of a head and token)
     on, unless they are so narrow that the copies were over four times as wide (or tensors do not

@@ -3,8 +3,8 @@
 //
 // A chunk takes four products, all with float32 accumulators in TMEM:
 //     A   = q k^T                     128 x 128, over the kd channels
-//     O1  = (A masked by a^(i-j)) v   128 x 64: the mask's product is rounded to bf16 and is the
-//                                     operand that stays in TMEM
+//     O1  = (A masked by a^(i-j)) v   128 x 64: the mask's product is rounded to bf16, or split into
+//                                     two bf16 terms, and is the operand that stays in TMEM
 //     O2  = q S                       128 x 64, S rounded to bf16 in shared memory
 //     U   = k^T W                     kd x 64, W the rows of v times a^(n-1-j)
 //     out = si O1 + sx a^(i+1) O2,    S <- a^n S + U
@@ -345,13 +345,15 @@ __device__ __forceinline__ void store8(char* at, const uint32_t* w, bool wide) {
 
 // ---------------------------------------------------------------- the walk
 // Columns of TMEM: the scores, the masked operand, the two parts of the outputs (that from the state
-// in two places, so that chunk k's need not wait for the last outputs to be read), the sums.
+// in two places, so that chunk k's need not wait for the last outputs to be read), the sums.  A masked
+// operand of two terms lies over the scores: in place of 16 of them eight columns of each.
 struct C {
     static constexpr uint32_t scores = 0, masked = 128, o1 = 192, u = 384;
     static constexpr uint32_t o2(int k) { return 256 + (k & 1) * kV; }
 };
 
-template <int NT>
+// NT, MT: terms of the weighted rows of v and of the masked scores.
+template <int NT, int MT>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_walk_kernel(const __grid_constant__ WalkArgs a, const __grid_constant__ Maps maps, const Geometry geo) {
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -452,7 +454,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = u ? j1 : j0;
-                        uint32_t s[16];
+                        uint32_t s[16], low[8];
+                        const auto put = [&](int e, F2 f) {
+                            s[e] = pack(f);
+                            if constexpr (MT == 2) low[e] = pack(layer::sub_(f, layer::join(bf_lo(s[e]), bf_hi(s[e]))));
+                        };
                         if (u ? some1 : some0) {
                             tmem_ld16(mine + C::scores + j, s);
                             tmem_wait_ld_regs<16>(s);
@@ -465,22 +471,28 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                 const float* at = x->powers[it.s] + (rev ? kBelow : kQ - 1) - i + j;
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    s[e] = pack(layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(at[2 * e], at[2 * e + 1])));
+                                    put(e, layer::mul_(pair(s[2 * e], s[2 * e + 1]), layer::join(at[2 * e], at[2 * e + 1])));
                             } else {  // a^15 .. a^0, or from the end a^0 .. a^15, the same for all rows
                                 const float4* at = reinterpret_cast<const float4*>(x->powers[it.s] + (rev ? kBelow : kQ - 16));
                                 const F2 r = layer::both<F2>(u ? r1 : r0);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const float4 f = at[e];
-                                    s[2 * e] = pack(layer::mul_(pair(s[4 * e], s[4 * e + 1]), layer::mul_(r, layer::join(f.x, f.y))));
-                                    s[2 * e + 1] = pack(layer::mul_(pair(s[4 * e + 2], s[4 * e + 3]), layer::mul_(r, layer::join(f.z, f.w))));
+                                    put(2 * e, layer::mul_(pair(s[4 * e], s[4 * e + 1]), layer::mul_(r, layer::join(f.x, f.y))));
+                                    put(2 * e + 1, layer::mul_(pair(s[4 * e + 2], s[4 * e + 3]), layer::mul_(r, layer::join(f.z, f.w))));
                                 }
                             }
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) s[e] = 0u;
+                            for (int e = 0; e < 8; ++e) s[e] = low[e] = 0u;
                         }
-                        tmem_st8(mine + C::masked + j / 2, s);
+                        if constexpr (MT == 2) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) s[8 + e] = low[e];
+                            tmem_st16(mine + C::scores + j, s);
+                        } else {
+                            tmem_st8(mine + C::masked + j / 2, s);
+                        }
                     }
                     seen = peek(&x->sums, k & 1);
                     tmem_wait_st();
@@ -631,8 +643,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const Item& t = x->items[it.s];
             const int kb = same(t.kb), chunks = same(t.chunks);
             for (int c = 0; c < chunks; ++c, ++g, qk.next(geo.stages), vv.next(geo.v_stages)) {
-                // the scores before have been read: their mask was waited for
-                if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status)) goto stopped_a;
+                // the scores before have been read: their mask was waited for.  So has the operand over them
+                // when its product is done
+                if (!wait_warp(&x->full[qk.s], qk.phase, &x->stop, status) ||
+                    (MT == 2 && g > 0 && !wait_warp(&x->outs, (g - 1) & 1, &x->stop, status)))
+                    goto stopped_a;
                 tc_fence_after();
                 if (elect_one()) {
                     uint64_t qd = sw128_desc(base + qk.s * geo.stage_bytes, 16, 1024), kd = moved(qd, kbytes);
@@ -653,8 +668,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 if (elect_one()) {
                     const uint64_t vd = sw128_desc(base + geo.v_at + vv.s * kSub, 16, 1024);
 #pragma unroll
-                    for (int i = 0; i < kQ / 16; ++i)
-                        mma_bf16_ta(tm + C::o1, tm + C::masked + 8 * i, moved(vd, i * 2048), id_o, i > 0);
+                    for (int i = 0; i < kQ / 16 * MT; ++i)  // 16 tokens, of two terms the larger ones first
+                        mma_bf16_ta(tm + C::o1, tm + (MT == 2 ? C::scores : C::masked) + 8 * i,
+                                    moved(vd, i / MT * 2048), id_o, i > 0);
                     mma_commit(&x->outs);
                 }
             }
@@ -992,8 +1008,16 @@ cudaError_t tc_walk(const WalkArgs& given, Launch& L) {
     geo.aux_at = geo.s_at + state;
     const size_t smem = (size_t)geo.aux_at + sizeof(Aux);
     L.begin("linattn_tc_walk");
-    const cudaError_t e = three ? launch(tc_walk_kernel<3>, a, m, geo, kWalkThreads, smem, L.stream)
-                                : launch(tc_walk_kernel<2>, a, m, geo, kWalkThreads, smem, L.stream);
+    // Scores of one term are off by a rounding of bf16, which adds to that of the output: 1.4 times its error, as
+    // does a state that meets q.  Where no state has come in, or tokens are so few that roundings do not
+    // average (14 tokens of 2 heads: 1.5 times), they are two terms: sequences within a chunk, and launches of
+    // one block an SM at most, whose time is latencies.  64 x 128 tokens of 32 heads, 64 x 64 states, forward
+    // 57.8 us, so 65.8; one of 16 heads the same to 0.3 us.  Everywhere it would cost 32768 tokens of 80 heads 542
+    // us for 518 forward and 1635 for 1343 backward, and leave 1.4 times, for the states.
+    const bool two = (a.cu ? a.T : a.rowlen) <= kQ || geo.items <= sm_count();
+    const auto kernel = three ? two ? tc_walk_kernel<3, 2> : tc_walk_kernel<3, 1>
+                              : two ? tc_walk_kernel<2, 2> : tc_walk_kernel<2, 1>;
+    const cudaError_t e = launch(kernel, a, m, geo, kWalkThreads, smem, L.stream);
     const cudaError_t last = L.end();
     return e != cudaSuccess ? e : last;
 }
