@@ -491,7 +491,8 @@ ssd_status_t ssd_linear_attention_step(const ssd_linattn_t* prob, int32_t nslots
  *     scores[i] + logits[i][t] - log sum_u exp(logits[i][u]),
  * the `keep` best, best first.  Candidates of one beam are ordered by their logits, those of
  * different beams by their scores in float64, before they are rounded (or overflow) to float32; equal
- * ones by beam, then token.
+ * ones by beam, then token.  The sums under the logarithms are float32's: beams may be off against one
+ * another by some 10^-8, and where few logits make up a sum by a few 10^-7.
  * finished (one byte a beam, not 0: ended; NULL: none has): such a beam has the one candidate
  * pad_token, at its score.  What is left out, tokens with a logit of -inf and every token of a
  * beam whose score is not finite or whose logits hold a NaN or +inf or nothing but -inf, has the

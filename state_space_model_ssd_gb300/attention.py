@@ -28,19 +28,21 @@ def linear_attention_forward(q, k, v, log_decay, scale=None, cu_seqlens=None, in
                              final_state: bool = False, out=None, final_state_out=None, workspace=None,
                              stream=None):
     """``cu_seqlens`` (int32 ``[nseq + 1]``, batch 1) packs sequences; outputs (and gradients) of
-    tokens before the first one or behind the last one are zero.  ``initial_state`` float32 ``[nseq or batch, H, P, N]`` is what each sequence
-    goes on from.  Returns ``(o, final_state or None)``: o ``[batch, L, H, P]`` in the type of q, the
-    final states as the initial ones.
+    tokens before the first one or behind the last one are zero.  ``initial_state`` float32
+    ``[nseq or batch, H, P, N]`` is what each sequence goes on from.  Returns
+    ``(o, final_state or None)``: o ``[batch, L, H, P]`` in the type of q, the final states as the
+    initial ones.
 
-    bfloat16 calls with N and P 64 or 128, every row on 16 bytes, run on the tensor cores in
-    blocks of 128 tokens (the state that meets q is rounded to bfloat16 there, and so are the masked
-    products, except of sequences within a block or in calls too small to fill the GPU, where two
-    bfloat16 terms hold them; the states themselves are float32): a NaN or an infinity in a token then reaches the
-    outputs of all tokens of its sequence in its block.  bfloat16 calls of other sizes, or with rows off
-    16 bytes, take that way too, by copies in the workspace, from 16384 rows (of a head and token)
-    on, unless they are so narrow that the copies were over four times as wide (or tensors do not
-    start on 16 bytes and ``workspace`` is too small for copies).  Forwards of up to 16 tokens a sequence are stepped
-    through, and all other calls run on the plain cores, in float32."""
+    bfloat16 calls with N and P 64 or 128, every row on 16 bytes, run on the tensor cores in blocks
+    of 128 tokens: a NaN or an infinity in a token then reaches the outputs of all tokens of its
+    sequence in its block.  The states are float32; where one meets q it is rounded to bfloat16, and
+    so are the masked products of q and k, except of sequences within a block or in calls too small
+    to fill the GPU, where two bfloat16 terms hold them.  bfloat16 calls of other sizes, or with rows
+    off 16 bytes, take that way too, by copies in the workspace, from 16384 rows (of a head and
+    token) on, unless they are so narrow that the copies were over four times as wide (or tensors do
+    not start on 16 bytes and ``workspace`` is too small for copies).  Forwards of up to 16 tokens a
+    sequence (a batch row, or all packed ones) are stepped through, and all other calls run on the
+    plain cores, in float32."""
     args = (q, k, v, log_decay, scale, cu_seqlens, initial_state, final_state, out, final_state_out, workspace)
     return (layer._ext.linear_attention_forward(*args) if stream is None
             else _on(stream, layer._ext.linear_attention_forward, *args))

@@ -1012,8 +1012,8 @@ cudaError_t tc_walk(const WalkArgs& given, Launch& L) {
     // does a state that meets q.  Where no state has come in, or tokens are so few that roundings do not
     // average (14 tokens of 2 heads: 1.5 times), they are two terms: sequences within a chunk, and launches of
     // one block an SM at most, whose time is latencies.  64 x 128 tokens of 32 heads, 64 x 64 states, forward
-    // 57.8 us, so 65.8; one of 16 heads the same to 0.3 us.  Everywhere it would cost 32768 tokens of 80 heads 542
-    // us for 518 forward and 1635 for 1343 backward, and leave 1.4 times, for the states.
+    // 57.8 us, so 65.8; 2048 tokens of 16 heads 27.2, so 28.9.  Everywhere it would cost 32768 tokens of 80 heads
+    // 542 us for 518 forward and 1635 for 1343 backward, and leave 1.4 times, for the states.
     const bool two = (a.cu ? a.T : a.rowlen) <= kQ || geo.items <= sm_count();
     const auto kernel = three ? two ? tc_walk_kernel<3, 2> : tc_walk_kernel<3, 1>
                               : two ? tc_walk_kernel<2, 2> : tc_walk_kernel<2, 1>;
